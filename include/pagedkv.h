@@ -82,6 +82,8 @@ typedef enum { KV_DTYPE_BF16 = 0, KV_DTYPE_INT8 = 1, KV_DTYPE_FP8_E4M3 = 2 } kv_
 #define PAGEDKV_FLAG_BAD_BLOCK 0x2u    /* block id outside [0, num_blocks)    */
 #define PAGEDKV_FLAG_BAD_SEQ_LEN 0x4u  /* seq_len <= 0 or beyond table/hint   */
 #define PAGEDKV_FLAG_WAIT_TIMEOUT 0x8u /* a bounded in-kernel wait gave up    */
+#define PAGEDKV_FLAG_BAD_INDEX 0x10u   /* a keep list that does not ascend in
+                                          [0, seq_len)                        */
 
 /* ------------------------------------------------------------------------ */
 /* Block pool (host bookkeeping)                                            */
@@ -162,6 +164,35 @@ kv_status kv_pool_stats(const kv_pool *pool, int *used, int *free_blocks);
 kv_status kv_pool_prepare_append(kv_pool *pool, int32_t *block_tables,
                                  int max_blocks_per_seq, const int32_t *seq_lens,
                                  int batch, int32_t *copy_pairs, int *num_copies);
+
+/* Destination blocks of an eviction (pagedkv_evict_tokens) that leaves
+ * keep_lens[b] of sequence b's seq_lens[b] tokens per KV head, packed into its
+ * first ceil(keep_lens[b] / block_size) blocks (host arrays):
+ *   - keep_lens[b] == seq_lens[b]: nothing moves, dst_tables[b] lists the same
+ *     blocks;
+ *   - otherwise each of those first blocks stays the sequence's own when it
+ *     holds the only reference (its prefix-cache entry is dropped: the rows
+ *     will be others), and is replaced by a block of the free list when it is
+ *     shared (the other holders keep reading the old one; the sequence's
+ *     reference on it is dropped), and the blocks after them lose the
+ *     sequence's reference.
+ * All new blocks are taken before any reference is dropped, so no destination
+ * is a block that another sequence of the call is still read from.  The caller
+ * uploads dst_tables, runs the eviction with block_tables as the source, and
+ * then uses dst_tables as the sequences' tables; work that later reuses the
+ * freed blocks has to be ordered behind it (the same stream).
+ *   block_tables  host int32 [batch, max_blocks_per_seq] (read only)
+ *   seq_lens, keep_lens  host int32 [batch], 0 <= keep_lens[b] <= seq_lens[b]
+ *   dst_tables    host int32 [batch, max_blocks_per_seq] (output; -1 past the
+ *                 kept blocks; must not be block_tables)
+ * All or nothing: KV_ERR_OUT_OF_BLOCKS when the free list is too short for
+ * the shared blocks, KV_ERR_INVALID_ARG for lengths out of range or a table
+ * entry that is not allocated (or is listed more often than it is
+ * referenced); either leaves the pool as it was. */
+kv_status kv_pool_prepare_evict(kv_pool *pool, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int32_t *seq_lens,
+                                const int32_t *keep_lens, int batch,
+                                int32_t *dst_tables);
 
 /* Prefix cache (“让 Agent 跑得快”, §七 前缀缓存: each full block is hashed from
  * its parent block's hash, its tokens and optional extra keys such as a LoRA
@@ -291,6 +322,46 @@ kv_status reshape_and_cache(const void *k, const void *v, void *k_cache,
                             int num_tokens, int num_blocks, int block_size,
                             int num_kv_heads, int head_dim, kv_dtype dtype,
                             void *stream);
+
+/* Append into an 8-bit pool whose scales follow the data (§四 FP8 量化; notes
+ * §3.2): reshape_and_cache codes a row under the scale it finds, this call
+ * sets the scales too, and finds each row's slot from the block table as
+ * pagedkv_multi_step does.  Sequence b's n_b = query_start[b + 1] -
+ * query_start[b] new tokens are its last n_b ones (seq_lens counts them), rows
+ * query_start[b] .. of new_k and new_v.  For every (block, KV head) that they
+ * touch, K and V apart, with Q = 127 (int8) or 448 (E4M3) and amax the largest
+ * finite magnitude of the block's new rows, in fp32:
+ *   made  = amax / Q
+ *   scale = made               when the block's row 0 is a new row (the tokens
+ *                              open the block; its old contents do not count)
+ *         = max(scale, made)   otherwise;
+ * the new rows get the codes reshape_and_cache gives under that scale, and
+ * when the scale has grown the block's earlier rows are coded again: the code
+ * of the fp32 product (old code * old scale).  A block of zeros has scale 0;
+ * an infinity saturates and never sets a scale, NaN is coded as in
+ * reshape_and_cache.  Rows after the sequence's last are left as they are.
+ *   new_k, new_v  device bf16 [num_tokens, num_kv_heads, head_dim]
+ *   k_cache, v_cache  device pools (int8 or E4M3), k_scale, v_scale device
+ *                 fp32 [num_blocks, num_kv_heads]; all written
+ *   block_tables, max_blocks_per_seq, seq_lens, batch  as for
+ *                 pagedkv_multi_step
+ *   query_start   device int32 [batch + 1], or NULL: one new token per
+ *                 sequence (num_tokens == batch, row b is sequence b's)
+ *   max_query_len host bound on every n_b (ignored without query_start)
+ * No two sequences of the call may append to the same block, and the block a
+ * token joins must not be shared (kv_pool_prepare_append sees to both).
+ * n_b == 0 appends nothing.  Offsets, lengths and table entries out of range
+ * skip the sequence or the block and set PAGEDKV_FLAG_BAD_SEQ_LEN or
+ * PAGEDKV_FLAG_BAD_BLOCK.  One launch, asynchronous on `stream`. */
+kv_status pagedkv_append_scaled(const void *new_k, const void *new_v,
+                                void *k_cache, void *v_cache, float *k_scale,
+                                float *v_scale, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int32_t *seq_lens,
+                                const int32_t *query_start, int batch,
+                                int num_tokens, int max_query_len,
+                                int num_blocks, int block_size,
+                                int num_kv_heads, int head_dim, kv_dtype dtype,
+                                void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Attention                                                                */
@@ -536,6 +607,167 @@ kv_status pagedkv_multi_step(void *out, const void *q, const void *new_k,
                              int num_blocks, int block_size, int max_seq_len,
                              float scale, kv_dtype dtype, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Differential attention                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* Workspace bytes paged_diff_attention_decode may need (0 when every sequence
+ * fits one partition). */
+size_t pagedkv_diff_workspace_bytes(int batch, int num_heads, int head_dim,
+                                    int max_seq_len, int block_size);
+
+/* Differential attention for one query token per sequence: the difference of
+ * two softmax maps over one value, with learned weights.  Head h (of KV head
+ * j = h / (num_heads / num_kv_heads)) has the query rows 2h and 2h + 1; KV
+ * head j has the keys of pool heads 2j and 2j + 1 and, as its value of
+ * 2 * head_dim elements, the values of pool heads 2j and 2j + 1 side by side:
+ *   a_i = softmax_t(scale * q[b, 2h + i] . K[2j + i]_t) . (V[2j] | V[2j+1])_t
+ *   y   = a_0 - lambda[h] * a_1
+ *   out[b, h] = y / sqrt(mean(y^2) + eps) * norm_weight,  or y without one.
+ * A pool for it is one of 2 * num_kv_heads heads, filled, copied and freed by
+ * the calls above.  A factor on the normalised row (1 - lambda_init) belongs
+ * in norm_weight.
+ *   out           device bf16 [batch, num_heads, 2 * head_dim] (output)
+ *   q             device bf16 [batch, 2 * num_heads, head_dim]
+ *   k_cache, v_cache  device pools [num_blocks, block_size, 2 * num_kv_heads,
+ *                 head_dim]; k_scale, v_scale fp32 [num_blocks,
+ *                 2 * num_kv_heads] for 8-bit pools, NULL for bf16
+ *   lambda        device fp32 [num_heads]
+ *   norm_weight   device fp32 [2 * head_dim], or NULL (eps is ignored then)
+ *   other arguments, errors and the treatment of bad lengths and blocks (zero
+ *   rows and a status bit) as for paged_attention_decode.  num_heads may be
+ *   any multiple of num_kv_heads (four heads of a KV head share one read of
+ *   its cache). */
+kv_status paged_diff_attention_decode(
+    void *out, const void *q, const void *k_cache, const void *v_cache,
+    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+    int max_blocks_per_seq, const int32_t *seq_lens, int batch, int num_heads,
+    int num_kv_heads, int head_dim, int num_blocks, int block_size,
+    int max_seq_len, float scale, const float *lambda,
+    const float *norm_weight, float eps, kv_dtype dtype, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Eviction by accumulated attention weight                                 */
+/* ------------------------------------------------------------------------ */
+
+/* The weight of a cached token is the softmax weight that queries gave it,
+ * summed over the query heads of a KV head and over the steps so far.  The
+ * weights of a batch are device fp32 [batch, num_kv_heads, weights_stride],
+ * weights_stride >= every sequence length; row b belongs to the sequence of
+ * row b of the block tables and moves with it.  A cache is kept within a
+ * budget by: attention that adds up the weights (the two calls below), every
+ * so often pagedkv_select_tokens, kv_pool_prepare_evict and
+ * pagedkv_evict_tokens, after which keep_len is the sequences' length. */
+
+/* Workspace bytes paged_attention_decode_weights may need. */
+size_t pagedkv_weights_workspace_bytes(int batch, int num_q_heads, int head_dim,
+                                       int max_seq_len, int block_size);
+
+/* paged_attention_decode that also adds the step's attention weights: with
+ * p[h, t] the softmax weight of query head h on token t of sequence b,
+ *   w[hk, t] = sum of p[h, t] over the query heads h of KV head hk
+ *   weights[b, hk, t] = w[hk, t]                       for t = seq_lens[b] - 1
+ *                     = weights[b, hk, t] + w[hk, t]   for earlier tokens
+ * (the step's own token has no earlier weight, so its entry need not be
+ * cleared).  Entries from seq_lens[b] on are left as they are, and so are all
+ * entries of a sequence with a bad length or block, whose output rows are
+ * zero.  The workspace (16-byte aligned, pagedkv_weights_workspace_bytes) is
+ * always needed: it holds the step's scores.  Other arguments, errors and
+ * limits as for paged_attention_decode; weights_stride >= max_seq_len. */
+kv_status paged_attention_decode_weights(
+    void *out, float *weights, int weights_stride, const void *q,
+    const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int num_blocks, int block_size, int max_seq_len, float scale,
+    kv_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes pagedkv_attention_weights may need. */
+size_t pagedkv_attention_weights_workspace_bytes(int num_tokens,
+                                                 int num_q_heads,
+                                                 int max_seq_len);
+
+/* The weights that several causal query tokens per sequence give (a prompt, a
+ * chunk of one, draft tokens, or the last queries of a prompt alone), beside
+ * paged_attention_multi, whose q, query_start, tables and lengths it takes:
+ * query token i of n_b sits at position seq_lens[b] - n_b + i and attends the
+ * positions up to its own;
+ *   w[hk, t] = sum over those tokens and the query heads of hk of p[i, h, t]
+ *   weights[b, hk, t] = w[hk, t]                       for t >= seq_lens[b] - n_b
+ *                     = weights[b, hk, t] + w[hk, t]   for earlier tokens
+ * With accumulate == 0 earlier tokens are stored too, not added to (the
+ * weights of these queries alone).  n_b == 0 leaves the sequence's entries as
+ * they are, and so do bad offsets, lengths and blocks (flagged as in
+ * paged_attention_multi).  V is not read.  Any group of query heads per KV
+ * head.  Other arguments as for paged_attention_multi; the workspace is
+ * 16-byte aligned, pagedkv_attention_weights_workspace_bytes(...).  Two
+ * launches, asynchronous on `stream`; no atomics, so equal inputs give equal
+ * bits. */
+kv_status pagedkv_attention_weights(
+    float *weights, int weights_stride, const void *q, const void *k_cache,
+    const float *k_scale, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *seq_lens, const int32_t *query_start, int batch,
+    int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+    int head_dim, int num_blocks, int block_size, int max_seq_len, float scale,
+    int accumulate, kv_dtype dtype, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/* The tokens every (sequence, KV head) keeps: all when seq_lens[b] <= budget,
+ * else the last `recent` and, of the others, the budget - recent of largest
+ * weight; of equal weights the lower positions (-0 equals +0, NaN counts as
+ * -infinity).
+ *   keep_idx   device int32 [batch, num_kv_heads, budget] (output): the kept
+ *              positions in ascending order, -1 after the last
+ *   keep_len   device int32 [batch] (output): min(seq_lens[b], budget)
+ *   weights    device fp32 [batch, num_kv_heads, weights_stride]
+ *   max_seq_len  host bound on every seq_lens[b], <= weights_stride
+ *   budget >= 1, 0 <= recent <= budget
+ * A length <= 0 or past max_seq_len gives keep_len 0, a list of -1 and
+ * PAGEDKV_FLAG_BAD_SEQ_LEN.  One launch, asynchronous on `stream`. */
+kv_status pagedkv_select_tokens(int32_t *keep_idx, int32_t *keep_len,
+                                const float *weights, int weights_stride,
+                                const int32_t *seq_lens, int batch,
+                                int num_kv_heads, int max_seq_len, int budget,
+                                int recent, void *stream);
+
+/* Packs the kept tokens of every (sequence, KV head): row keep_idx[b][h][j] of
+ * the sequence (through block_tables) becomes row j (through
+ * dst_block_tables) of K and V for head h, and entry j of its weights, for
+ * j < keep_len[b].  The heads of a sequence keep the same number of tokens but
+ * each its own.  Afterwards keep_len[b] is the sequence's length; rows past it
+ * and blocks that no destination lists are left as they were.
+ *   k_cache, v_cache, k_scale, v_scale  device pools as for copy_blocks (written)
+ *   block_tables  device int32 [batch, max_blocks_per_seq], the source
+ *   dst_block_tables  device int32 [batch, dst_max_blocks]: may be
+ *                 block_tables (packing in place).  Entry j of a row is either
+ *                 entry j of the source row or a block that no source row of
+ *                 the call lists, and no block is the destination of two
+ *                 sequences (kv_pool_prepare_evict makes such tables)
+ *   keep_idx, keep_len, budget  as pagedkv_select_tokens gives them: each list
+ *                 strictly ascending within [0, seq_lens[b])
+ *   weights       device fp32 [batch, num_kv_heads, weights_stride] or NULL
+ * bf16 rows are copied bit for bit.  8-bit rows are coded again under a scale
+ * of their new block's own: max |code * scale| over its finite rows / Q (127
+ * or 448), with fp32 products and quotients as in pagedkv_append_scaled.  A
+ * destination block that is its own source and whose kept rows do not move
+ * keeps its codes and scale.
+ * A list that does not ascend in range leaves that (sequence, head) as it was
+ * and sets PAGEDKV_FLAG_BAD_INDEX; bad lengths skip the sequence
+ * (PAGEDKV_FLAG_BAD_SEQ_LEN), a table entry outside the pool skips the
+ * destination block (PAGEDKV_FLAG_BAD_BLOCK).  One launch, asynchronous on
+ * `stream`. */
+kv_status pagedkv_evict_tokens(void *k_cache, void *v_cache, float *k_scale,
+                               float *v_scale, const int32_t *block_tables,
+                               int max_blocks_per_seq,
+                               const int32_t *dst_block_tables,
+                               int dst_max_blocks, const int32_t *seq_lens,
+                               const int32_t *keep_idx, const int32_t *keep_len,
+                               int budget, float *weights, int weights_stride,
+                               int batch, int num_blocks, int block_size,
+                               int num_kv_heads, int head_dim, kv_dtype dtype,
+                               void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status                                                                   */

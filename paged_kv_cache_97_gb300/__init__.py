@@ -24,6 +24,7 @@ KV_OK, KV_ERR_INVALID_ARG, KV_ERR_OUT_OF_BLOCKS, KV_ERR_CUDA, KV_ERR_DEVICE_INDE
     KV_ERR_NOT_IMPLEMENTED = range(6)
 DTYPE_BF16, DTYPE_INT8, DTYPE_FP8_E4M3 = 0, 1, 2
 FLAG_BAD_SLOT, FLAG_BAD_BLOCK, FLAG_BAD_SEQ_LEN, FLAG_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+FLAG_BAD_INDEX = 0x10
 
 # Every symbol include/pagedkv.h declares, with its ctypes signature.
 _P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
@@ -37,6 +38,7 @@ SIGNATURES = {
     "kv_pool_fork": (_I, [_P, _P, _I]),
     "kv_pool_refcount": (_I, [_P, ctypes.c_int32]),
     "kv_pool_prepare_append": (_I, [_P, _P, _I, _P, _I, _P, _P]),
+    "kv_pool_prepare_evict": (_I, [_P, _P, _I, _P, _P, _I, _P]),
     "pagedkv_copy_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "pagedkv_check_block_pairs": (_I, [_P, _I, _I]),
     "pagedkv_multi_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
@@ -67,6 +69,20 @@ SIGNATURES = {
     "pagedkv_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "pagedkv_decode_step": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I,
                                  _I, _I, _F, _I, _P, _SZ, _P]),
+    "pagedkv_append_scaled": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
+                                   _I, _I, _P]),
+    "pagedkv_diff_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "paged_diff_attention_decode": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                                         _I, _F, _P, _P, _F, _I, _P, _SZ, _P]),
+    "pagedkv_weights_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "paged_attention_decode_weights": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I,
+                                            _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
+    "pagedkv_attention_weights_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "pagedkv_attention_weights": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
+                                       _I, _I, _I, _F, _I, _I, _P, _SZ, _P]),
+    "pagedkv_select_tokens": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
+    "pagedkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I,
+                                  _I, _I, _I, _I, _P]),
 }
 
 _lib = None
@@ -246,6 +262,24 @@ class KVPool:
         _check(self._lib.kv_pool_prepare_append(self._h, bt.ctypes.data, bt.shape[1], sl.ctypes.data,
                                                 bt.shape[0], pairs.ctypes.data, ctypes.byref(n)))
         return pairs[:n.value].copy()
+
+    def prepare_evict(self, block_tables, seq_lens, keep_lens):
+        """Destination tables (a host int32 array like block_tables) of an
+        eviction that leaves keep_lens[b] of seq_lens[b] tokens: blocks the
+        sequence shares are replaced, those it no longer needs released.
+        block_tables stays the source table of evict_tokens."""
+        import numpy as np
+        bt = block_tables
+        if bt.dtype != np.int32 or not bt.flags.c_contiguous or bt.ndim != 2:
+            raise TypeError("block_tables must be a C-contiguous int32 [batch, max_blocks] array")
+        sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
+        kl = np.ascontiguousarray(keep_lens, dtype=np.int32)
+        if sl.shape != (bt.shape[0],) or kl.shape != sl.shape:
+            raise ValueError("seq_lens and keep_lens must have one entry per table row")
+        dst = np.empty_like(bt)
+        _check(self._lib.kv_pool_prepare_evict(self._h, bt.ctypes.data, bt.shape[1], sl.ctypes.data,
+                                               kl.ctypes.data, bt.shape[0], dst.ctypes.data))
+        return dst
 
 
 def block_hash(parent_hash: int, tokens, extra_key: int = 0) -> int:
@@ -615,6 +649,252 @@ def paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_l
                                                  nb, bs, int(max_seq_len), float(scale), dt,
                                                  _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------
+# Self-scaling append, differential attention, eviction
+# --------------------------------------------------------------------------
+
+def _here(*tensors):
+    """Every given tensor lives on the current device (the kernels run there)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _need_scales(k_cache, k_scale, v_scale, with_v=True):
+    """Scales for 8-bit pools (fp32 [num_blocks, pool heads]), none for bf16."""
+    import torch
+    q8 = _pool_dtype(k_cache) != DTYPE_BF16
+    shape = (k_cache.shape[0], k_cache.shape[2])
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale))[:2 if with_v else 1]:
+        if (t is not None) != q8:
+            raise ValueError("8-bit pools need k_scale and v_scale; bf16 pools take none")
+        if t is not None:
+            _need(t, torch.float32, name, 2)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
+
+
+def _need_pools(k_cache, v_cache):
+    _pool_dtype(k_cache)
+    _need(k_cache, k_cache.dtype, "k_cache", 4)
+    _need(v_cache, k_cache.dtype, "v_cache", 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+
+
+def _need_tables(block_tables, seq_lens):
+    import torch
+    _need(block_tables, torch.int32, "block_tables", 2)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    if block_tables.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+
+
+def _need_weights(weights, batch, num_kv_heads):
+    import torch
+    _need(weights, torch.float32, "weights", 3)
+    if weights.shape[0] != batch or weights.shape[1] != num_kv_heads:
+        raise ValueError("weights must be [batch, num_kv_heads, tokens]")
+
+
+def _space(workspace):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def append_scaled(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                  query_start=None, max_query_len=1, stream=None):
+    """Append each sequence's last tokens into 8-bit pools, setting the scale of
+    every (block, KV head) they touch from the data: k, v bf16 [T, Hkv, d], row
+    query_start[b] + i at position seq_lens[b] - n_b + i (one token per
+    sequence without query_start).  Rows already in a block are coded again
+    when its scale grows."""
+    import torch
+    _need(k, torch.bfloat16, "k", 3)
+    _need(v, torch.bfloat16, "v", 3)
+    _need_pools(k_cache, v_cache)
+    dt = _pool_dtype(k_cache)
+    if dt == DTYPE_BF16:
+        raise TypeError("append_scaled writes 8-bit pools (torch.int8 or torch.float8_e4m3fn)")
+    _need_scales(k_cache, k_scale, v_scale)
+    _need_tables(block_tables, seq_lens)
+    nb, bs, hkv, d = k_cache.shape
+    T, B = k.shape[0], seq_lens.shape[0]
+    if k.shape != (T, hkv, d) or v.shape != k.shape:
+        raise ValueError("k, v must be [tokens, num_kv_heads, head_dim]")
+    if query_start is not None:
+        _need(query_start, torch.int32, "query_start", 1)
+        if query_start.shape[0] != B + 1:
+            raise ValueError("query_start must have batch + 1 entries")
+    elif T != B:
+        raise ValueError("without query_start there is one token per sequence")
+    _here(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, query_start)
+    _check(load().pagedkv_append_scaled(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                        _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                                        _ptr(seq_lens), _ptr(query_start), B, T, int(max_query_len),
+                                        nb, bs, hkv, d, dt, _stream(stream)))
+
+
+def diff_workspace_bytes(batch, num_heads, head_dim, max_seq_len, block_size) -> int:
+    return load().pagedkv_diff_workspace_bytes(batch, num_heads, head_dim, max_seq_len, block_size)
+
+
+def paged_diff_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, scale,
+                                lam, norm_weight=None, eps=1e-5, workspace=None, k_scale=None,
+                                v_scale=None, stream=None):
+    """Differential attention for one query token per sequence: out bf16
+    [B, H, 2 d] = norm(softmax(q_1 K_1) V - lam[h] softmax(q_2 K_2) V), with q
+    bf16 [B, 2 H, d] (rows 2h, 2h + 1 of head h), pools of 2 Hkv heads (KV head
+    j: pool heads 2j, 2j + 1), lam fp32 [H] and, for the row's RMS
+    normalisation, norm_weight fp32 [2 d] (None: the plain difference)."""
+    import torch
+    _need(out, torch.bfloat16, "out", 3)
+    _need(q, torch.bfloat16, "q", 3)
+    _need_pools(k_cache, v_cache)
+    _need_scales(k_cache, k_scale, v_scale)
+    _need_tables(block_tables, seq_lens)
+    _need(lam, torch.float32, "lam", 1)
+    nb, bs, pool_heads, d = k_cache.shape
+    B, rows, dq = q.shape
+    H = rows // 2
+    if rows % 2 or pool_heads % 2 or dq != d or out.shape != (B, H, 2 * d) or lam.shape[0] != H:
+        raise ValueError("q must be [batch, 2 heads, head_dim], out [batch, heads, 2 head_dim], lam "
+                         "[heads] and the pools hold 2 KV heads per differential one")
+    if seq_lens.shape[0] != B:
+        raise ValueError("block_tables / seq_lens must have one row per sequence")
+    if norm_weight is not None:
+        _need(norm_weight, torch.float32, "norm_weight", 1)
+        if norm_weight.shape[0] != 2 * d:
+            raise ValueError("norm_weight must have 2 head_dim entries")
+    _here(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, lam, norm_weight, workspace)
+    ws, ws_n = _space(workspace)
+    _check(load().paged_diff_attention_decode(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, H, pool_heads // 2, d, nb, bs,
+        int(max_seq_len), float(scale), _ptr(lam), _ptr(norm_weight), float(eps), _pool_dtype(k_cache),
+        ws, ws_n, _stream(stream)))
+    return out
+
+
+def weights_workspace_bytes(batch, num_q_heads, head_dim, max_seq_len, block_size) -> int:
+    return load().pagedkv_weights_workspace_bytes(batch, num_q_heads, head_dim, max_seq_len, block_size)
+
+
+def paged_attention_decode_weights(out, weights, q, k_cache, v_cache, block_tables, seq_lens,
+                                   max_seq_len, scale, workspace, k_scale=None, v_scale=None,
+                                   stream=None):
+    """paged_attention_decode that also adds each token's attention weight,
+    summed over the query heads of a KV head, to ``weights`` (fp32 [B, Hkv,
+    tokens]; the step's own token's entry is stored)."""
+    import torch
+    _need(out, torch.bfloat16, "out", 3)
+    _need(q, torch.bfloat16, "q", 3)
+    _need_pools(k_cache, v_cache)
+    _need_scales(k_cache, k_scale, v_scale)
+    _need_tables(block_tables, seq_lens)
+    nb, bs, hkv, d = k_cache.shape
+    B, hq, dq = q.shape
+    if out.shape != q.shape or dq != d or seq_lens.shape[0] != B:
+        raise ValueError("q, out, the pools and the tables disagree")
+    _need_weights(weights, B, hkv)
+    _here(out, weights, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace)
+    ws, ws_n = _space(workspace)
+    _check(load().paged_attention_decode_weights(
+        _ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, hq,
+        hkv, d, nb, bs, int(max_seq_len), float(scale), _pool_dtype(k_cache), ws, ws_n,
+        _stream(stream)))
+    return out
+
+
+def attention_weights_workspace_bytes(num_tokens, num_q_heads, max_seq_len) -> int:
+    return load().pagedkv_attention_weights_workspace_bytes(num_tokens, num_q_heads, max_seq_len)
+
+
+def attention_weights(weights, q, k_cache, block_tables, seq_lens, query_start, max_seq_len,
+                      max_query_len, scale, workspace, accumulate=True, k_scale=None, stream=None):
+    """The attention weights that several causal query tokens per sequence (q
+    bf16 [T, Hq, d], as for paged_attention_multi) give the cached tokens:
+    added to ``weights`` (fp32 [B, Hkv, tokens]) for earlier tokens, stored for
+    the queries' own positions (for all of them with accumulate False)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(k_cache, k_cache.dtype, "k_cache", 4)
+    _need_scales(k_cache, k_scale, None, with_v=False)
+    _need_tables(block_tables, seq_lens)
+    _need(query_start, torch.int32, "query_start", 1)
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, dq = q.shape
+    B = seq_lens.shape[0]
+    if dq != d or query_start.shape[0] != B + 1:
+        raise ValueError("q, the pool and query_start disagree")
+    _need_weights(weights, B, hkv)
+    _here(weights, q, k_cache, k_scale, block_tables, seq_lens, query_start, workspace)
+    ws, ws_n = _space(workspace)
+    _check(load().pagedkv_attention_weights(
+        _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), _ptr(query_start), B, T, int(max_query_len), hq, hkv, d,
+        nb, bs, int(max_seq_len), float(scale), 1 if accumulate else 0, _pool_dtype(k_cache), ws, ws_n,
+        _stream(stream)))
+    return weights
+
+
+def select_tokens(keep_idx, keep_len, weights, seq_lens, max_seq_len, recent, stream=None):
+    """The positions each (sequence, KV head) keeps into ``keep_idx`` (int32
+    [B, Hkv, budget], ascending, -1 after the last) and their number into
+    ``keep_len`` (int32 [B]): the last ``recent`` tokens and the heaviest of
+    the others, all when the sequence fits the budget."""
+    import torch
+    _need(keep_idx, torch.int32, "keep_idx", 3)
+    _need(keep_len, torch.int32, "keep_len", 1)
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    B, hkv, budget = keep_idx.shape
+    if keep_len.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("keep_idx, keep_len and seq_lens disagree on the batch size")
+    _need_weights(weights, B, hkv)
+    _here(keep_idx, keep_len, weights, seq_lens)
+    _check(load().pagedkv_select_tokens(_ptr(keep_idx), _ptr(keep_len), _ptr(weights),
+                                        weights.shape[2], _ptr(seq_lens), B, hkv, int(max_seq_len),
+                                        budget, int(recent), _stream(stream)))
+    return keep_idx, keep_len
+
+
+def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
+                 dst_block_tables=None, weights=None, k_scale=None, v_scale=None, stream=None):
+    """Pack the kept rows keep_idx[b, h, :keep_len[b]] (strictly ascending) of
+    every (sequence, KV head) into rows 0 .. of the blocks of
+    ``dst_block_tables`` (None: in place), K, V and ``weights`` alike; 8-bit
+    blocks get scales of their own.  ``keep_len`` is the new length."""
+    import torch
+    _need_pools(k_cache, v_cache)
+    _need_scales(k_cache, k_scale, v_scale)
+    _need_tables(block_tables, seq_lens)
+    _need(keep_idx, torch.int32, "keep_idx", 3)
+    _need(keep_len, torch.int32, "keep_len", 1)
+    nb, bs, hkv, d = k_cache.shape
+    B = seq_lens.shape[0]
+    if keep_idx.shape[:2] != (B, hkv) or keep_len.shape[0] != B:
+        raise ValueError("keep_idx must be [batch, num_kv_heads, budget] and keep_len [batch]")
+    dst = block_tables if dst_block_tables is None else dst_block_tables
+    _need(dst, torch.int32, "dst_block_tables", 2)
+    if dst.shape[0] != B:
+        raise ValueError("dst_block_tables must have one row per sequence")
+    if weights is not None:
+        _need_weights(weights, B, hkv)
+    _here(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len, dst, weights, k_scale, v_scale)
+    _check(load().pagedkv_evict_tokens(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        block_tables.shape[1], _ptr(dst), dst.shape[1], _ptr(seq_lens), _ptr(keep_idx), _ptr(keep_len),
+        keep_idx.shape[2], _ptr(weights), 0 if weights is None else weights.shape[2], B, nb, bs, hkv, d,
+        _pool_dtype(k_cache), _stream(stream)))
 
 
 def get_status(stream=None):

@@ -59,6 +59,8 @@ struct DecodeArgs {
   const int32_t* prefix_blocks; // [num_prefix_blocks] shared first blocks of every sequence, or null
   float* ws_ml;                // [B, Hq, slots, 2]   (m, l) per partial
   float* ws_acc;               // [B, Hq, slots, D]   unnormalised acc
+  float* ws_scores;            // [B, Hq, score_stride] scores kept for the weights, or null
+  int64_t score_stride;
   unsigned int* flags;
   int max_blocks_per_seq, batch, num_q_heads, num_kv_heads, head_dim;
   int num_blocks, block_size, max_seq_len;

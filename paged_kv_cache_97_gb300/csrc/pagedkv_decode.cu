@@ -70,12 +70,17 @@ constexpr int kSpec = (kMaxBlocks + kThreads - 1) / kThreads;  // table entries 
 
 // kQ8: the pools hold 8-bit codes under per-(block, KV head) scales, int8
 // or (kFp8) E4M3; otherwise bf16.
+// kScores: every score (base 2, scaled) also goes to the workspace, row by
+// row ([B, Hq, score_stride] fp32), and every row's (m, l) is written even
+// when it has one partial: the attention-weight kernel behind this one needs
+// both (pagedkv_weights.cu).  A score costs 4 bytes against the 2 d bytes of
+// a bf16 K row that a second product would read again.
 // 8-bit and multi-token instances may be held to 128 registers (4 CTAs of
 // 4 warps per SM, the residency their shared memory allows).
 #ifndef PAGEDKV_Q8_MIN_BLOCKS
 #define PAGEDKV_Q8_MIN_BLOCKS 4
 #endif
-template <int D, int BS, bool kQ8, bool kFp8, bool kMulti>
+template <int D, int BS, bool kQ8, bool kFp8, bool kMulti, bool kScores>
 __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLOCKS : 1)
     decode_kernel(const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const DecodeArgs a) {
@@ -266,6 +271,10 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
   // int8 V enters P . V as c + 1152 (no subtraction per code pair); vb holds
   // sum_t p_t per column (an all-ones A fragment times P^T, one MMA per tile)
   // and O loses 1152 vsum before the warps combine.
+  // (With kScores the bias is subtracted per code pair instead, for K and V:
+  // the scores are an output then, and the biased sums' cancellation would be
+  // their largest error.)
+  constexpr bool kBiased = kQ8 && !kFp8 && !kScores;
   float vsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
   if (!bad && warp == kConsumers) {
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
     // holds for head g (exact products; the cancellation costs about 2^-24
     // of the biased sum, some 1e-6 of a score).
     float kb0 = 0.0f, kb1 = 0.0f;
-    if constexpr (kQ8 && !kFp8) {
+    if constexpr (kBiased) {
       float sq = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < G::kKSteps; ++ks) {
@@ -460,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
 #pragma unroll
             for (int ks = 0; ks < G::kKSteps; ++ks) {
               const uint32_t w0 = kw[0][ks / 4][ks % 4], w1 = kw[1][ks / 4][ks % 4];
-              const uint32_t fa[4] = {codes_to_f16x2<kFp8, true>(w0, 0x4140u), codes_to_f16x2<kFp8, true>(w1, 0x4140u),
-                                      codes_to_f16x2<kFp8, true>(w0, 0x4342u), codes_to_f16x2<kFp8, true>(w1, 0x4342u)};
+              const uint32_t fa[4] = {codes_to_f16x2<kFp8, !kScores>(w0, 0x4140u), codes_to_f16x2<kFp8, !kScores>(w1, 0x4140u),
+                                      codes_to_f16x2<kFp8, !kScores>(w0, 0x4342u), codes_to_f16x2<kFp8, !kScores>(w1, 0x4342u)};
               if (ks & 1) mma16816<true>(c1, fa, qf[ks][0], qf[ks][1]);
               else        mma16816<true>(c0, fa, qf[ks][0], qf[ks][1]);
             }
@@ -480,6 +489,23 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
             sc[tile][1] = tok_lo < valid ? (c0[1] + c1[1] + kb1) * kfac : -INFINITY;
             sc[tile][2] = tok_hi < valid ? (c0[2] + c1[2] + kb0) * kfac : -INFINITY;
             sc[tile][3] = tok_hi < valid ? (c0[3] + c1[3] + kb1) * kfac : -INFINITY;
+          }
+        }
+
+        if constexpr (kScores) {
+          // 8 lanes of one column write 8 consecutive tokens (32 bytes)
+          float* col = a.ws_scores + (head0 + 2 * t) * a.score_stride + (first_blk + j) * BS;
+#pragma unroll
+          for (int tile = 0; tile < G::kTiles; ++tile) {
+            const int lo = tile * 16 + g, hi = lo + 8;
+            if (2 * t < GQ) {
+              if (lo < valid) col[lo] = sc[tile][0];
+              if (hi < valid) col[hi] = sc[tile][2];
+            }
+            if (2 * t + 1 < GQ) {
+              if (lo < valid) col[a.score_stride + lo] = sc[tile][1];
+              if (hi < valid) col[a.score_stride + hi] = sc[tile][3];
+            }
           }
         }
 
@@ -512,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
           o[i][2] *= al0;
           o[i][3] *= al1;
         }
-        if constexpr (kQ8 && !kFp8) {
+        if constexpr (kBiased) {
           vsum[0] *= al0;
           vsum[1] *= al1;
           vsum[2] *= al0;
@@ -583,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
                 vw[rr][1] = v.y ^ kCodeBias<kFp8>;
               }
             }
-            if constexpr (!kFp8) {
+            if constexpr (kBiased) {
               const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
               mma16816<true>(vsum, ones, pb0, pb1);
             }
@@ -592,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
               const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;  // bytes 2,3 or 0,1
               const uint32_t ulo = prmt(vw[0][i / 2], vw[1][i / 2], sel);  // tokens 2t, 2t+1
               const uint32_t uhi = prmt(vw[2][i / 2], vw[3][i / 2], sel);  // tokens 2t+8, 2t+9
-              uint32_t fa[4] = {codes_to_f16x2<kFp8, true>(ulo, 0x4140u), codes_to_f16x2<kFp8, true>(ulo, 0x4342u),
-                                codes_to_f16x2<kFp8, true>(uhi, 0x4140u), codes_to_f16x2<kFp8, true>(uhi, 0x4342u)};
+              uint32_t fa[4] = {codes_to_f16x2<kFp8, !kScores>(ulo, 0x4140u), codes_to_f16x2<kFp8, !kScores>(ulo, 0x4342u),
+                                codes_to_f16x2<kFp8, !kScores>(uhi, 0x4140u), codes_to_f16x2<kFp8, !kScores>(uhi, 0x4342u)};
               if constexpr (kFp8) {
                 fa[0] &= mlo;
                 fa[1] &= mlo;
@@ -630,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
       red_l[warp * 8 + 2 * t] = l_run[0];
       red_l[warp * 8 + 2 * t + 1] = l_run[1];
     }
-    if constexpr (kQ8 && !kFp8) {
+    if constexpr (kBiased) {
 #pragma unroll
       for (int i = 0; i < G::kMTiles; ++i)
 #pragma unroll
@@ -662,11 +688,10 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
       const int hh = i / D, e = i % D;
       const int64_t row = col_row(hh);
       if (row < 0) continue;
-      if (direct) {
-        out[row * D + e] = __float2bfloat16_rn(0.0f);
-      } else {
+      if (direct) out[row * D + e] = __float2bfloat16_rn(0.0f);
+      if (!direct || kScores) {
         const int64_t r = row * a.slots + part;
-        a.ws_acc[r * D + e] = 0.0f;
+        if (!direct) a.ws_acc[r * D + e] = 0.0f;
         if (e == 0) {
           a.ws_ml[2 * r] = 0.0f;
           a.ws_ml[2 * r + 1] = -1.0f;  // marks the row bad for the merge
@@ -693,11 +718,10 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
       den = fmaf(c, red_l[w * 8 + hh], den);
     }
     num *= out_scale;
-    if (direct) {
-      out[row * D + e] = __float2bfloat16_rn(num / den);
-    } else {
+    if (direct) out[row * D + e] = __float2bfloat16_rn(num / den);
+    if (!direct || kScores) {
       const int64_t r = row * a.slots + part;
-      a.ws_acc[r * D + e] = num;
+      if (!direct) a.ws_acc[r * D + e] = num;
       if (e == 0) {
         a.ws_ml[2 * r] = M;
         a.ws_ml[2 * r + 1] = den;
@@ -752,7 +776,7 @@ kv_status make_map(CUtensorMap* map, const void* pool, const DecodeArgs& a) {
   return KV_OK;
 }
 
-template <int D, int BS, bool kQ8, bool kFp8, bool kMulti>
+template <int D, int BS, bool kQ8, bool kFp8, bool kMulti, bool kScores = false>
 kv_status launch_t(const DecodeArgs& a, cudaStream_t s) {
   using G = Geo<D, BS, kQ8>;
   static std::mutex mu;
@@ -763,7 +787,7 @@ kv_status launch_t(const DecodeArgs& a, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(decode_kernel<D, BS, kQ8, kFp8, kMulti>,
+      st = cuda_check(cudaFuncSetAttribute(decode_kernel<D, BS, kQ8, kFp8, kMulti, kScores>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            G::kSmemBytes),
                       "cudaFuncSetAttribute(decode_kernel)");
@@ -775,7 +799,7 @@ kv_status launch_t(const DecodeArgs& a, cudaStream_t s) {
   if ((st = make_kv_maps(a, &km, &vm)) != KV_OK) return st;
   const dim3 grid(a.num_kv_heads, kMulti ? a.batch * a.vgroups : a.batch, a.max_parts);
   if (a.prefix_chunks == 0) {
-    decode_kernel<D, BS, kQ8, kFp8, kMulti><<<grid, kThreads, G::kSmemBytes, s>>>(km, vm, a);
+    decode_kernel<D, BS, kQ8, kFp8, kMulti, kScores><<<grid, kThreads, G::kSmemBytes, s>>>(km, vm, a);
     return cuda_check(cudaGetLastError(), "decode_kernel launch");
   }
   // Behind the prefix kernel: launched as its programmatic dependent so the
@@ -791,12 +815,15 @@ kv_status launch_t(const DecodeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, decode_kernel<D, BS, kQ8, kFp8, kMulti>, km, vm, a),
+  return cuda_check(cudaLaunchKernelEx(&cfg, decode_kernel<D, BS, kQ8, kFp8, kMulti, kScores>, km, vm, a),
                     "decode_kernel launch");
 }
 
 template <int D, bool kQ8, bool kFp8>
 kv_status launch_bs(const DecodeArgs& a, cudaStream_t s) {
+  if (a.ws_scores != nullptr)
+    return a.block_size == 32 ? launch_t<D, 32, kQ8, kFp8, false, true>(a, s)
+                              : launch_t<D, 16, kQ8, kFp8, false, true>(a, s);
   if (a.query_start != nullptr)
     return a.block_size == 32 ? launch_t<D, 32, kQ8, kFp8, true>(a, s) : launch_t<D, 16, kQ8, kFp8, true>(a, s);
   return a.block_size == 32 ? launch_t<D, 32, kQ8, kFp8, false>(a, s) : launch_t<D, 16, kQ8, kFp8, false>(a, s);

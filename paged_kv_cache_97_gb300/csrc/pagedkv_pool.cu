@@ -319,6 +319,62 @@ kv_status kv_pool_prepare_append(kv_pool* p, int32_t* block_tables, int max_bloc
   return pagedkv_check_block_pairs(copy_pairs, n, p->num_blocks);
 }
 
+kv_status kv_pool_prepare_evict(kv_pool* p, const int32_t* block_tables, int max_blocks_per_seq,
+                                const int32_t* seq_lens, const int32_t* keep_lens, int batch,
+                                int32_t* dst_tables) {
+  if (!p || batch < 0 || max_blocks_per_seq <= 0 ||
+      (batch > 0 && (!block_tables || !seq_lens || !keep_lens || !dst_tables)) ||
+      (batch > 0 && dst_tables == block_tables))
+    return fail(KV_ERR_INVALID_ARG, "kv_pool_prepare_evict: bad arguments");
+  const int bs = p->block_size;
+  // Pass 1: every sequence's blocks are allocated, each with a reference per
+  // listing; count the shared blocks that need a replacement (by the counts at
+  // the call's start: a block that two sequences of the call share is read for
+  // both, so neither may pack into it).
+  std::vector<int32_t> listed(p->num_blocks, 0);
+  size_t need = 0;
+  for (int b = 0; b < batch; ++b) {
+    const int L = seq_lens[b], m = keep_lens[b];
+    if (L < 0 || m < 0 || m > L || (L > 0 && (L - 1) / bs >= max_blocks_per_seq))
+      return fail(KV_ERR_INVALID_ARG,
+                  "kv_pool_prepare_evict: sequence %d: keeps %d of %d tokens (a table row holds %d)", b,
+                  m, L, max_blocks_per_seq * bs);
+    for (int j = 0; (int64_t)j * bs < L; ++j) {
+      const int32_t id = block_tables[(int64_t)b * max_blocks_per_seq + j];
+      if (id < 0 || id >= p->num_blocks || ++listed[id] > p->refs[id])
+        return fail(KV_ERR_INVALID_ARG,
+                    "kv_pool_prepare_evict: sequence %d lists block %d, which is not allocated (or "
+                    "listed more often than it is held)", b, id);
+      if (m < L && (int64_t)j * bs < m && p->refs[id] > 1) ++need;
+    }
+  }
+  if (need > p->free_list.size())
+    return fail(KV_ERR_OUT_OF_BLOCKS, "kv_pool_prepare_evict: %zu blocks needed, %zu free", need,
+                p->free_list.size());
+  // Pass 2: all destinations; pass 3: the references dropped (in table order).
+  for (int b = 0; b < batch; ++b) {
+    const int L = seq_lens[b], m = keep_lens[b];
+    for (int j = 0; j < max_blocks_per_seq; ++j) {
+      int32_t& to = dst_tables[(int64_t)b * max_blocks_per_seq + j];
+      to = -1;
+      if ((int64_t)j * bs >= m) continue;
+      to = block_tables[(int64_t)b * max_blocks_per_seq + j];
+      if (m == L) continue;
+      if (p->refs[to] > 1) to = take_block(p);
+      else evict(p, to);                               // its rows become others
+    }
+  }
+  for (int b = 0; b < batch; ++b) {
+    const int L = seq_lens[b], m = keep_lens[b];
+    if (m == L) continue;
+    for (int j = 0; (int64_t)j * bs < L; ++j) {
+      const int64_t at = (int64_t)b * max_blocks_per_seq + j;
+      if (dst_tables[at] != block_tables[at]) drop_ref(p, block_tables[at]);
+    }
+  }
+  return KV_OK;
+}
+
 kv_status pagedkv_check_block_pairs(const int32_t* block_pairs, int num_pairs, int num_blocks) {
   if (num_pairs < 0 || num_blocks <= 0 || (num_pairs > 0 && !block_pairs))
     return fail(KV_ERR_INVALID_ARG, "pagedkv_check_block_pairs: bad arguments");
