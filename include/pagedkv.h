@@ -722,7 +722,8 @@ kv_status pagedkv_attention_weights(
  *              positions in ascending order, -1 after the last
  *   keep_len   device int32 [batch] (output): min(seq_lens[b], budget)
  *   weights    device fp32 [batch, num_kv_heads, weights_stride]
- *   max_seq_len  host bound on every seq_lens[b], <= weights_stride
+ *   max_seq_len  host bound on every seq_lens[b], <= weights_stride and
+ *              <= 2097152
  *   budget >= 1, 0 <= recent <= budget
  * A length <= 0 or past max_seq_len gives keep_len 0, a list of -1 and
  * PAGEDKV_FLAG_BAD_SEQ_LEN.  One launch, asynchronous on `stream`. */

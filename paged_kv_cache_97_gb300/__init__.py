@@ -655,50 +655,56 @@ def paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_l
 # Self-scaling append, differential attention, eviction
 # --------------------------------------------------------------------------
 
-def _here(*tensors):
-    """Every given tensor lives on the current device (the kernels run there)."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+_dt = None                  # torch's dtypes by the names used below, resolved once
 
 
-def _need_scales(k_cache, k_scale, v_scale, with_v=True):
-    """Scales for 8-bit pools (fp32 [num_blocks, pool heads]), none for bf16."""
+def _dtypes():
+    global _dt
+    if _dt is None:
+        import torch
+        _dt = (torch.bfloat16, torch.int32, torch.float32,
+               {torch.bfloat16: DTYPE_BF16, torch.int8: DTYPE_INT8, torch.float8_e4m3fn: DTYPE_FP8_E4M3})
+    return _dt
+
+
+def _need_all(*specs):
+    """Every (tensor, dtype, name, dimensions) is a contiguous tensor of that
+    type on the current device (the kernels run there)."""
     import torch
-    q8 = _pool_dtype(k_cache) != DTYPE_BF16
-    shape = (k_cache.shape[0], k_cache.shape[2])
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale))[:2 if with_v else 1]:
-        if (t is not None) != q8:
-            raise ValueError("8-bit pools need k_scale and v_scale; bf16 pools take none")
-        if t is not None:
-            _need(t, torch.float32, name, 2)
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t, dtype, name, ndim in specs:
+        try:
+            if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _need(t, dtype, name, ndim)
+        raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _pools(k_cache, v_cache, k_scale, v_scale, specs):
+    """The pools' dtype code; their checks (with their scales': fp32
+    [num_blocks, pool heads] for 8-bit pools, none for bf16) go to specs.
+    v_cache None: a call that reads K alone."""
+    kinds = _dtypes()[3]
+    dt = kinds.get(getattr(k_cache, "dtype", None))
+    if dt is None:
+        _pool_dtype(k_cache)
+    specs.append((k_cache, k_cache.dtype, "k_cache", 4))
+    if v_cache is not None:
+        specs.append((v_cache, k_cache.dtype, "v_cache", 4))
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must have the same shape")
+    q8 = dt != DTYPE_BF16
+    if (k_scale is not None) != q8 or (v_cache is not None and (v_scale is not None) != q8):
+        raise ValueError("8-bit pools need k_scale and v_scale; bf16 pools take none")
+    if q8:
+        shape = (k_cache.shape[0], k_cache.shape[2])
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale))[:1 if v_cache is None else 2]:
+            specs.append((t, _dtypes()[2], name, 2))
             if t.shape != shape:
                 raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
-
-
-def _need_pools(k_cache, v_cache):
-    _pool_dtype(k_cache)
-    _need(k_cache, k_cache.dtype, "k_cache", 4)
-    _need(v_cache, k_cache.dtype, "v_cache", 4)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-
-
-def _need_tables(block_tables, seq_lens):
-    import torch
-    _need(block_tables, torch.int32, "block_tables", 2)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    if block_tables.shape[0] != seq_lens.shape[0]:
-        raise ValueError("block_tables and seq_lens must have one row per sequence")
-
-
-def _need_weights(weights, batch, num_kv_heads):
-    import torch
-    _need(weights, torch.float32, "weights", 3)
-    if weights.shape[0] != batch or weights.shape[1] != num_kv_heads:
-        raise ValueError("weights must be [batch, num_kv_heads, tokens]")
+    return dt
 
 
 def _space(workspace):
@@ -717,30 +723,33 @@ def append_scaled(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_le
     query_start[b] + i at position seq_lens[b] - n_b + i (one token per
     sequence without query_start).  Rows already in a block are coded again
     when its scale grows."""
-    import torch
-    _need(k, torch.bfloat16, "k", 3)
-    _need(v, torch.bfloat16, "v", 3)
-    _need_pools(k_cache, v_cache)
-    dt = _pool_dtype(k_cache)
+    bf16, i32, _, _ = _dtypes()
+    specs = [(k, bf16, "k", 3), (v, bf16, "v", 3), (block_tables, i32, "block_tables", 2),
+             (seq_lens, i32, "seq_lens", 1)]
+    dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
+    if query_start is not None:
+        specs.append((query_start, i32, "query_start", 1))
+    _need_all(*specs)
     if dt == DTYPE_BF16:
         raise TypeError("append_scaled writes 8-bit pools (torch.int8 or torch.float8_e4m3fn)")
-    _need_scales(k_cache, k_scale, v_scale)
-    _need_tables(block_tables, seq_lens)
     nb, bs, hkv, d = k_cache.shape
     T, B = k.shape[0], seq_lens.shape[0]
     if k.shape != (T, hkv, d) or v.shape != k.shape:
         raise ValueError("k, v must be [tokens, num_kv_heads, head_dim]")
-    if query_start is not None:
-        _need(query_start, torch.int32, "query_start", 1)
-        if query_start.shape[0] != B + 1:
-            raise ValueError("query_start must have batch + 1 entries")
-    elif T != B:
-        raise ValueError("without query_start there is one token per sequence")
-    _here(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, query_start)
-    _check(load().pagedkv_append_scaled(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                        _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-                                        _ptr(seq_lens), _ptr(query_start), B, T, int(max_query_len),
-                                        nb, bs, hkv, d, dt, _stream(stream)))
+    mb = block_tables.shape
+    if mb[0] != B:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+    if query_start is None:
+        if T != B:
+            raise ValueError("without query_start there is one token per sequence")
+    elif query_start.shape[0] != B + 1:
+        raise ValueError("query_start must have batch + 1 entries")
+    st = load().pagedkv_append_scaled(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), _ptr(query_start), B, T,
+        int(max_query_len), nb, bs, hkv, d, dt, _stream(stream))
+    if st != KV_OK:
+        _check(st)
 
 
 def diff_workspace_bytes(batch, num_heads, head_dim, max_seq_len, block_size) -> int:
@@ -755,32 +764,32 @@ def paged_diff_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens
     bf16 [B, 2 H, d] (rows 2h, 2h + 1 of head h), pools of 2 Hkv heads (KV head
     j: pool heads 2j, 2j + 1), lam fp32 [H] and, for the row's RMS
     normalisation, norm_weight fp32 [2 d] (None: the plain difference)."""
-    import torch
-    _need(out, torch.bfloat16, "out", 3)
-    _need(q, torch.bfloat16, "q", 3)
-    _need_pools(k_cache, v_cache)
-    _need_scales(k_cache, k_scale, v_scale)
-    _need_tables(block_tables, seq_lens)
-    _need(lam, torch.float32, "lam", 1)
+    bf16, i32, f32, _ = _dtypes()
+    specs = [(out, bf16, "out", 3), (q, bf16, "q", 3), (block_tables, i32, "block_tables", 2),
+             (seq_lens, i32, "seq_lens", 1), (lam, f32, "lam", 1)]
+    dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
+    if norm_weight is not None:
+        specs.append((norm_weight, f32, "norm_weight", 1))
+    _need_all(*specs)
     nb, bs, pool_heads, d = k_cache.shape
     B, rows, dq = q.shape
     H = rows // 2
+    mb = block_tables.shape
     if rows % 2 or pool_heads % 2 or dq != d or out.shape != (B, H, 2 * d) or lam.shape[0] != H:
         raise ValueError("q must be [batch, 2 heads, head_dim], out [batch, heads, 2 head_dim], lam "
                          "[heads] and the pools hold 2 KV heads per differential one")
-    if seq_lens.shape[0] != B:
+    if seq_lens.shape[0] != B or mb[0] != B:
         raise ValueError("block_tables / seq_lens must have one row per sequence")
-    if norm_weight is not None:
-        _need(norm_weight, torch.float32, "norm_weight", 1)
-        if norm_weight.shape[0] != 2 * d:
-            raise ValueError("norm_weight must have 2 head_dim entries")
-    _here(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, lam, norm_weight, workspace)
+    if norm_weight is not None and norm_weight.shape[0] != 2 * d:
+        raise ValueError("norm_weight must have 2 head_dim entries")
     ws, ws_n = _space(workspace)
-    _check(load().paged_diff_attention_decode(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, H, pool_heads // 2, d, nb, bs,
-        int(max_seq_len), float(scale), _ptr(lam), _ptr(norm_weight), float(eps), _pool_dtype(k_cache),
-        ws, ws_n, _stream(stream)))
+    st = load().paged_diff_attention_decode(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+        _ptr(v_scale), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), B, H, pool_heads // 2, d, nb,
+        bs, int(max_seq_len), float(scale), lam.data_ptr(), _ptr(norm_weight), float(eps), dt, ws, ws_n,
+        _stream(stream))
+    if st != KV_OK:
+        _check(st)
     return out
 
 
@@ -794,24 +803,26 @@ def paged_attention_decode_weights(out, weights, q, k_cache, v_cache, block_tabl
     """paged_attention_decode that also adds each token's attention weight,
     summed over the query heads of a KV head, to ``weights`` (fp32 [B, Hkv,
     tokens]; the step's own token's entry is stored)."""
-    import torch
-    _need(out, torch.bfloat16, "out", 3)
-    _need(q, torch.bfloat16, "q", 3)
-    _need_pools(k_cache, v_cache)
-    _need_scales(k_cache, k_scale, v_scale)
-    _need_tables(block_tables, seq_lens)
+    bf16, i32, f32, _ = _dtypes()
+    specs = [(out, bf16, "out", 3), (weights, f32, "weights", 3), (q, bf16, "q", 3),
+             (block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1)]
+    dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
+    _need_all(*specs)
     nb, bs, hkv, d = k_cache.shape
     B, hq, dq = q.shape
-    if out.shape != q.shape or dq != d or seq_lens.shape[0] != B:
+    mb = block_tables.shape
+    if out.shape != q.shape or dq != d or seq_lens.shape[0] != B or mb[0] != B:
         raise ValueError("q, out, the pools and the tables disagree")
-    _need_weights(weights, B, hkv)
-    _here(out, weights, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace)
+    wb, wh, stride = weights.shape
+    if wb != B or wh != hkv:
+        raise ValueError("weights must be [batch, num_kv_heads, tokens]")
     ws, ws_n = _space(workspace)
-    _check(load().paged_attention_decode_weights(
-        _ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, hq,
-        hkv, d, nb, bs, int(max_seq_len), float(scale), _pool_dtype(k_cache), ws, ws_n,
-        _stream(stream)))
+    st = load().paged_attention_decode_weights(
+        out.data_ptr(), weights.data_ptr(), stride, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), B, hq, hkv, d,
+        nb, bs, int(max_seq_len), float(scale), dt, ws, ws_n, _stream(stream))
+    if st != KV_OK:
+        _check(st)
     return out
 
 
@@ -825,25 +836,28 @@ def attention_weights(weights, q, k_cache, block_tables, seq_lens, query_start, 
     bf16 [T, Hq, d], as for paged_attention_multi) give the cached tokens:
     added to ``weights`` (fp32 [B, Hkv, tokens]) for earlier tokens, stored for
     the queries' own positions (for all of them with accumulate False)."""
-    import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(k_cache, k_cache.dtype, "k_cache", 4)
-    _need_scales(k_cache, k_scale, None, with_v=False)
-    _need_tables(block_tables, seq_lens)
-    _need(query_start, torch.int32, "query_start", 1)
+    bf16, i32, f32, _ = _dtypes()
+    specs = [(weights, f32, "weights", 3), (q, bf16, "q", 3), (block_tables, i32, "block_tables", 2),
+             (seq_lens, i32, "seq_lens", 1), (query_start, i32, "query_start", 1)]
+    dt = _pools(k_cache, None, k_scale, None, specs)
+    _need_all(*specs)
     nb, bs, hkv, d = k_cache.shape
     T, hq, dq = q.shape
     B = seq_lens.shape[0]
-    if dq != d or query_start.shape[0] != B + 1:
-        raise ValueError("q, the pool and query_start disagree")
-    _need_weights(weights, B, hkv)
-    _here(weights, q, k_cache, k_scale, block_tables, seq_lens, query_start, workspace)
+    mb = block_tables.shape
+    if dq != d or query_start.shape[0] != B + 1 or mb[0] != B:
+        raise ValueError("q, the pool, the tables and query_start disagree")
+    wb, wh, stride = weights.shape
+    if wb != B or wh != hkv:
+        raise ValueError("weights must be [batch, num_kv_heads, tokens]")
     ws, ws_n = _space(workspace)
-    _check(load().pagedkv_attention_weights(
-        _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), _ptr(query_start), B, T, int(max_query_len), hq, hkv, d,
-        nb, bs, int(max_seq_len), float(scale), 1 if accumulate else 0, _pool_dtype(k_cache), ws, ws_n,
-        _stream(stream)))
+    st = load().pagedkv_attention_weights(
+        weights.data_ptr(), stride, q.data_ptr(), k_cache.data_ptr(), _ptr(k_scale),
+        block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), query_start.data_ptr(), B, T,
+        int(max_query_len), hq, hkv, d, nb, bs, int(max_seq_len), float(scale), 1 if accumulate else 0,
+        dt, ws, ws_n, _stream(stream))
+    if st != KV_OK:
+        _check(st)
     return weights
 
 
@@ -852,18 +866,20 @@ def select_tokens(keep_idx, keep_len, weights, seq_lens, max_seq_len, recent, st
     [B, Hkv, budget], ascending, -1 after the last) and their number into
     ``keep_len`` (int32 [B]): the last ``recent`` tokens and the heaviest of
     the others, all when the sequence fits the budget."""
-    import torch
-    _need(keep_idx, torch.int32, "keep_idx", 3)
-    _need(keep_len, torch.int32, "keep_len", 1)
-    _need(seq_lens, torch.int32, "seq_lens", 1)
+    _, i32, f32, _ = _dtypes()
+    _need_all((keep_idx, i32, "keep_idx", 3), (keep_len, i32, "keep_len", 1),
+              (weights, f32, "weights", 3), (seq_lens, i32, "seq_lens", 1))
     B, hkv, budget = keep_idx.shape
+    wb, wh, stride = weights.shape
     if keep_len.shape[0] != B or seq_lens.shape[0] != B:
         raise ValueError("keep_idx, keep_len and seq_lens disagree on the batch size")
-    _need_weights(weights, B, hkv)
-    _here(keep_idx, keep_len, weights, seq_lens)
-    _check(load().pagedkv_select_tokens(_ptr(keep_idx), _ptr(keep_len), _ptr(weights),
-                                        weights.shape[2], _ptr(seq_lens), B, hkv, int(max_seq_len),
-                                        budget, int(recent), _stream(stream)))
+    if wb != B or wh != hkv:
+        raise ValueError("weights must be [batch, num_kv_heads, tokens]")
+    st = load().pagedkv_select_tokens(keep_idx.data_ptr(), keep_len.data_ptr(), weights.data_ptr(),
+                                      stride, seq_lens.data_ptr(), B, hkv, int(max_seq_len), budget,
+                                      int(recent), _stream(stream))
+    if st != KV_OK:
+        _check(st)
     return keep_idx, keep_len
 
 
@@ -873,28 +889,34 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
     every (sequence, KV head) into rows 0 .. of the blocks of
     ``dst_block_tables`` (None: in place), K, V and ``weights`` alike; 8-bit
     blocks get scales of their own.  ``keep_len`` is the new length."""
-    import torch
-    _need_pools(k_cache, v_cache)
-    _need_scales(k_cache, k_scale, v_scale)
-    _need_tables(block_tables, seq_lens)
-    _need(keep_idx, torch.int32, "keep_idx", 3)
-    _need(keep_len, torch.int32, "keep_len", 1)
-    nb, bs, hkv, d = k_cache.shape
-    B = seq_lens.shape[0]
-    if keep_idx.shape[:2] != (B, hkv) or keep_len.shape[0] != B:
-        raise ValueError("keep_idx must be [batch, num_kv_heads, budget] and keep_len [batch]")
+    _, i32, f32, _ = _dtypes()
     dst = block_tables if dst_block_tables is None else dst_block_tables
-    _need(dst, torch.int32, "dst_block_tables", 2)
-    if dst.shape[0] != B:
-        raise ValueError("dst_block_tables must have one row per sequence")
+    specs = [(block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1),
+             (keep_idx, i32, "keep_idx", 3), (keep_len, i32, "keep_len", 1)]
+    dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
+    if dst is not block_tables:
+        specs.append((dst, i32, "dst_block_tables", 2))
     if weights is not None:
-        _need_weights(weights, B, hkv)
-    _here(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len, dst, weights, k_scale, v_scale)
-    _check(load().pagedkv_evict_tokens(
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-        block_tables.shape[1], _ptr(dst), dst.shape[1], _ptr(seq_lens), _ptr(keep_idx), _ptr(keep_len),
-        keep_idx.shape[2], _ptr(weights), 0 if weights is None else weights.shape[2], B, nb, bs, hkv, d,
-        _pool_dtype(k_cache), _stream(stream)))
+        specs.append((weights, f32, "weights", 3))
+    _need_all(*specs)
+    nb, bs, hkv, d = k_cache.shape
+    B, kh, budget = keep_idx.shape
+    mb, md = block_tables.shape, dst.shape
+    if kh != hkv or keep_len.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("keep_idx must be [batch, num_kv_heads, budget], keep_len and seq_lens [batch]")
+    if mb[0] != B or md[0] != B:
+        raise ValueError("the block tables must have one row per sequence")
+    stride = 0
+    if weights is not None:
+        wb, wh, stride = weights.shape
+        if wb != B or wh != hkv:
+            raise ValueError("weights must be [batch, num_kv_heads, tokens]")
+    st = load().pagedkv_evict_tokens(
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(),
+        mb[1], dst.data_ptr(), md[1], seq_lens.data_ptr(), keep_idx.data_ptr(), keep_len.data_ptr(),
+        budget, _ptr(weights), stride, B, nb, bs, hkv, d, dt, _stream(stream))
+    if st != KV_OK:
+        _check(st)
 
 
 def get_status(stream=None):

@@ -74,11 +74,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_scaled_kernel(const 
     return;
   }
   const int r0 = max(first - lb * BS, 0), r1 = min(L - lb * BS, BS);  // the new rows
-  const uint4* src = a.rows[kv];
-  float* scale = a.scale[kv] + (int64_t)p * Hkv + h;
+  const uint4* src = kv ? a.rows[1] : a.rows[0];
+  float* scale = (kv ? a.scale[1] : a.scale[0]) + (int64_t)p * Hkv + h;
   const int sub = lane / kLanes, piece = lane % kLanes;
   uint4 x[kSteps][2];
-  float amax = 0.0f;
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int r = u * kRows + sub;
@@ -90,34 +89,50 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_scaled_kernel(const 
     }
   }
   const float old = r0 > 0 ? *scale : 0.0f;
+  // The magnitudes of finite bf16 values order as their bits do, and every
+  // non-finite one is above them.
+  uint32_t most = 0u;
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int r = u * kRows + sub;
     if (r >= r0 && r < r1) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t w[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[i] << 16)),
-                                   finite_abs(__uint_as_float(w[i] & 0xffff0000u))));
-      }
+      for (int k = 0; k < 2; ++k)
+        most = max_u16x2(max_u16x2(max_u16x2(most, x[u][k].x & 0x7fff7fffu), x[u][k].y & 0x7fff7fffu),
+                         max_u16x2(x[u][k].z & 0x7fff7fffu, x[u][k].w & 0x7fff7fffu));
     }
   }
-  const float made = block_scale<kFp8>(warp_max(amax));
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+  float amax = __uint_as_float(bits << 16);
+  const bool finite = bits < 0x7f80u;
+  if (!finite) {
+    amax = 0.0f;
+    for (int u = 0; u < kSteps; ++u) {
+      const int r = u * kRows + sub;
+      if (r < r0 || r >= r1) continue;
+      const int64_t token = (int64_t)q0 + (lb * BS + r - first);
+      const __nv_bfloat16* at = reinterpret_cast<const __nv_bfloat16*>(src) + (token * Hkv + h) * D + 16 * piece;
+      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(__bfloat162float(at[i])));
+    }
+    amax = warp_max(amax);
+  }
+  const float made = block_scale<kFp8>(amax);
   const float s = fmaxf(old, made);                  // (a NaN old scale gives way)
-  uint4* pool = static_cast<uint4*>(a.cache[kv]);
+  uint4* pool = static_cast<uint4*>(kv ? a.cache[1] : a.cache[0]);
   const int64_t base = ((int64_t)p * BS * Hkv + h) * kLanes + piece;  // row r: + r * Hkv * kLanes
   if (s > old && r0 > 0) {
+    const Interval again = quotients(old, s);
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const int r = u * kRows + sub;
       if (r < r0) {
         uint4* at = pool + base + (int64_t)r * Hkv * kLanes;
-        *at = recode16<kFp8>(*at, old, s);
+        *at = recode16<kFp8>(*at, again, old, s);
       }
     }
   }
+  Interval q = quotients(s);
+  q.on &= finite;                                    // (an infinity saturates, NaN has its code)
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int r = u * kRows + sub;
@@ -125,11 +140,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_scaled_kernel(const 
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 q = x[u][i / 2];
-        const uint32_t w0 = i % 2 ? q.z : q.x, w1 = i % 2 ? q.w : q.y;
+        const uint4 y = x[u][i / 2];
+        const uint32_t w0 = i % 2 ? y.z : y.x, w1 = i % 2 ? y.w : y.y;
         const float v[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
                             __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)};
-        o[i] = code4<kFp8>(v, s);
+        o[i] = code4<kFp8>(v, q, s);
       }
       pool[base + (int64_t)r * Hkv * kLanes] = make_uint4(o[0], o[1], o[2], o[3]);
     }

@@ -537,10 +537,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Joins the partials of both maps of one head (one CTA per (sequence, head)):
-// its warps take the partials in turn, one warp writes the row.
+// even warps take the first map's partials in turn, odd ones the second's, and
+// warp 0 writes the row.
 template <int D>
 __global__ void __launch_bounds__(512) diff_merge_kernel(const DiffArgs da) {
-  extern __shared__ float merge_red[];                  // [warps][2][2 D + 1]
+  extern __shared__ float merge_red[];                  // [warps][2 D + 1]
   const DecodeArgs& a = da.d;
   const int b = blockIdx.x / da.num_heads, h = blockIdx.x % da.num_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x / 32;
@@ -550,61 +551,63 @@ __global__ void __launch_bounds__(512) diff_merge_kernel(const DiffArgs da) {
       (int64_t)L > (int64_t)a.max_blocks_per_seq * a.block_size)
     return;                                             // written whole, or zeroed
   const int np = (L + a.part_tokens - 1) / a.part_tokens;
-  const int64_t row = ((int64_t)b * da.num_heads + h) * 2;
-  constexpr int E = D / 16;                             // elements per lane: lane + 32 k
+  constexpr int E = D / 64;                             // float4 pieces per lane
+  const int64_t row = ((int64_t)b * da.num_heads + h) * 2 + (warp & 1);
+  const float* ml = a.ws_ml + row * a.slots * 2;
+  const float4* acc = reinterpret_cast<const float4*>(a.ws_acc + row * a.slots * 2 * D) + lane;
   bool bad = false;
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float* ml = a.ws_ml + (row + m) * a.slots * 2;
-    const float* acc = a.ws_acc + (row + m) * a.slots * 2 * D;
-    float M = -INFINITY;
-    for (int i = lane; i < np; i += 32) {
-      M = fmaxf(M, ml[2 * i]);
-      bad |= ml[2 * i + 1] < 0.0f;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float num[E], den = 0.0f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) num[k] = 0.0f;
-#pragma unroll 2
-    for (int i = warp; i < np; i += warps) {
-      const float w = exp2f(ml[2 * i] - M);
-      den = fmaf(w, ml[2 * i + 1], den);
-#pragma unroll
-      for (int k = 0; k < E; ++k) num[k] = fmaf(w, acc[(int64_t)i * 2 * D + lane + 32 * k], num[k]);
-    }
-    float* r = merge_red + (warp * 2 + m) * (2 * D + 1);
-#pragma unroll
-    for (int k = 0; k < E; ++k) r[lane + 32 * k] = num[k];
-    if (lane == 0) r[2 * D] = den;
+  float M = -INFINITY;
+  for (int i = lane; i < np; i += 32) {
+    M = fmaxf(M, ml[2 * i]);
+    bad |= ml[2 * i + 1] < 0.0f;
   }
-  bad = __any_sync(0xffffffffu, bad);
-  __syncthreads();
-  if (warp != 0) return;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)b * da.num_heads + h) * 2 * D;
-  float y[E], a2[E], d1 = 0.0f, d2 = 0.0f;
 #pragma unroll
-  for (int k = 0; k < E; ++k) y[k] = a2[k] = 0.0f;
-  for (int w = 0; w < warps; ++w) {
-    const float* r = merge_red + w * 2 * (2 * D + 1);
-    d1 += r[2 * D];
-    d2 += r[2 * (2 * D + 1) - 1];
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float4 num[E];
+  float den = 0.0f;
+#pragma unroll
+  for (int k = 0; k < E; ++k) num[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp >> 1; i < np; i += warps >> 1) {
+    const float w = exp2f(ml[2 * i] - M);
+    den = fmaf(w, ml[2 * i + 1], den);
 #pragma unroll
     for (int k = 0; k < E; ++k) {
-      y[k] += r[lane + 32 * k];
-      a2[k] += r[2 * D + 1 + lane + 32 * k];
+      const float4 x = acc[(int64_t)i * (D / 2) + 32 * k];
+      num[k].x = fmaf(w, x.x, num[k].x);
+      num[k].y = fmaf(w, x.y, num[k].y);
+      num[k].z = fmaf(w, x.z, num[k].z);
+      num[k].w = fmaf(w, x.w, num[k].w);
     }
   }
-  if (bad) {
+  float* r = merge_red + warp * (2 * D + 4);
 #pragma unroll
-    for (int k = 0; k < E; ++k) out[lane + 32 * k] = __float2bfloat16_rn(0.0f);
+  for (int k = 0; k < E; ++k) reinterpret_cast<float4*>(r)[lane + 32 * k] = num[k];
+  if (lane == 0) r[2 * D] = den;
+  if (__syncthreads_or(bad)) {
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x)
+      static_cast<__nv_bfloat16*>(a.out)[((int64_t)b * da.num_heads + h) * 2 * D + i] = __float2bfloat16_rn(0.0f);
     return;
+  }
+  if (warp != 0) return;
+  float y[D / 16], a2[D / 16], d1 = 0.0f, d2 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) y[k] = a2[k] = 0.0f;
+  for (int w = 0; w < warps; w += 2) {
+    const float* r1 = merge_red + w * (2 * D + 4);
+    const float* r2 = r1 + 2 * D + 4;
+    d1 += r1[2 * D];
+    d2 += r2[2 * D];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      y[k] += r1[lane + 32 * k];
+      a2[k] += r2[lane + 32 * k];
+    }
   }
   const float lam = da.lam[h];
 #pragma unroll
-  for (int k = 0; k < E; ++k) y[k] = y[k] / d1 - lam * (a2[k] / d2);
-  write_row<D>(da, out, y, lane);
+  for (int k = 0; k < D / 16; ++k) y[k] = y[k] / d1 - lam * (a2[k] / d2);
+  write_row<D>(da, static_cast<__nv_bfloat16*>(a.out) + ((int64_t)b * da.num_heads + h) * 2 * D, y, lane);
 }
 
 template <int D, int BS, bool kQ8, bool kFp8>
@@ -629,13 +632,13 @@ kv_status launch_diff_t(const DiffArgs& da, int dev, cudaStream_t s) {
   diff_decode_kernel<D, BS, kQ8, kFp8><<<grid, kThreads, G::kSmemBytes, s>>>(km, vm, da);
   if ((st = cuda_check(cudaGetLastError(), "diff_decode_kernel launch")) != KV_OK) return st;
   if (da.d.max_parts == 1) return KV_OK;
-  // about 8 partials per warp and map
-  int warps = (da.d.max_parts + 7) / 8;
+  // about 4 partials per warp, an even number of warps
+  int warps = 2 * ((da.d.max_parts + 3) / 4);
   warps = warps > 16 ? 16 : warps;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(da.d.batch * da.num_heads));
   cfg.blockDim = dim3((unsigned)(32 * warps));
-  cfg.dynamicSmemBytes = (size_t)warps * 2 * (2 * D + 1) * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)warps * (2 * D + 4) * sizeof(float);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -24,22 +24,23 @@ using namespace dev;
 // ---------------------------------------------------------------------------
 //
 // One cluster of C CTAs per (sequence, KV head).  With L tokens, the last
-// `recent` are kept; of the C = L - recent candidates, the k = budget - recent
-// of largest weight, ties to the lowest position:
-//   1. a radix select over the weights as 32-bit ordered integers, three
-//      digits (11, 11, 10 bits) from the top, finds the k-th largest value T
-//      and how many candidates equal to T are kept (r);
-//   2. a counting pass and a writing pass place every candidate above T and
-//      the first r equal to T in ascending order of position.
-// Each CTA holds a contiguous slice of the candidates in shared memory (what
-// does not fit is read again from global memory), so the weights are read
-// once; histograms and counts of the other CTAs are read through distributed
-// shared memory.
+// `recent` are kept; of the L - recent candidates, the k = budget - recent of
+// largest weight, ties to the lowest position.  A radix select over the
+// weights as 32-bit ordered integers, digits of 11, 11 and 10 bits from the
+// top, finds the k-th largest key T and how many candidates equal to T are
+// kept.  Each CTA holds a contiguous slice of the candidates in shared memory
+// (what does not fit is read again from global memory) and two bits per
+// candidate, in chunks of 32: "kept" (its leading digits are above T's) and
+// "open" (equal so far).  The first two digits go over all keys, after which
+// few are open, and the rest is done by one thread per chunk on its open bits
+// alone.  Histograms and counts of the other CTAs are read through distributed
+// shared memory; the chunks' counts give every kept position its place, in
+// ascending order.
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
+constexpr int kMostCtas = 8;                         // of a cluster
+constexpr int kBatch = 8;                            // loads in flight per thread
 
 struct SelectArgs {
   const float* weights;      // [B, Hkv, stride]
@@ -50,6 +51,7 @@ struct SelectArgs {
   int64_t stride;
   int num_kv_heads, budget, recent, max_len;
   int cap;                   // candidates of a slice kept in shared memory
+  int chunk_cap;             // 32-candidate chunks of the longest slice
 };
 
 // Ordered integer of a weight: larger weight, larger key; -0 equals +0, NaN
@@ -62,7 +64,9 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 // Exclusive prefix of v over the CTA's threads; `total` gets the sum.
+template <int kThreads>
 __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -72,7 +76,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  const int s = lane < kSelWarps ? warp_sums[lane] : 0;
+  const int s = lane < kWarps ? warp_sums[lane] : 0;
   int before = lane < warp ? s : 0;
   before = __reduce_add_sync(0xffffffffu, before);
   *total = __reduce_add_sync(0xffffffffu, s);
@@ -80,11 +84,13 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
   return before + x - v;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kBinsPer = kBins / kThreads;         // bins per thread, at most
   extern __shared__ uint32_t sel_smem[];
   uint32_t* hist = sel_smem;                         // [kPasses][kBins]
-  uint32_t* keys = sel_smem + kPasses * kBins;       // [cap]
-  __shared__ int warp_sums[kSelWarps], sh_bin, sh_need;
+  __shared__ int warp_sums[kWarps], sh_bin, sh_need;
   __shared__ int sh_counts[2];                       // this CTA's (above, equal) counts
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -92,10 +98,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   const int b = row / a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = a.keep_idx + (int64_t)row * a.budget;
+  for (int i = tid; i < kPasses * kBins; i += kThreads) hist[i] = 0u;
   const int L = a.seq_lens[b];
   const bool bad = L <= 0 || L > a.max_len;          // (cluster-uniform)
   if (bad || L <= a.budget) {
-    for (int i = rank * kSelThreads + tid; i < a.budget; i += C * kSelThreads)
+    for (int i = rank * kThreads + tid; i < a.budget; i += C * kThreads)
       out[i] = !bad && i < L ? i : -1;
     if (row % a.num_kv_heads == 0 && rank == 0 && tid == 0) {
       a.keep_len[b] = bad ? 0 : L;
@@ -105,97 +112,208 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   }
   if (row % a.num_kv_heads == 0 && rank == 0 && tid == 0) a.keep_len[b] = a.budget;
   const int cand = L - a.recent, k = a.budget - a.recent;
-  for (int i = rank * kSelThreads + tid; i < a.recent; i += C * kSelThreads) out[k + i] = cand + i;
+  for (int i = rank * kThreads + tid; i < a.recent; i += C * kThreads) out[k + i] = cand + i;
   if (k == 0) return;
 
   const int per = (cand + C - 1) / C;
   const int lo = min(rank * per, cand), n = min(cand - lo, per);   // this CTA's slice
   const float* w = a.weights + (int64_t)row * a.stride + lo;
+  const int chunks = (n + 31) / 32;
+  uint32_t* shared_sums = hist + kPasses * kBins;    // [kBins]
+  uint32_t* open = shared_sums + kBins;              // [chunks of a slice], then as many kept
+  uint32_t* kept = open + a.chunk_cap;
+  uint32_t* keys = kept + a.chunk_cap;               // [cap]
   auto key_at = [&](int i) { return i < a.cap ? keys[i] : order_key(w[i]); };
+  __syncthreads();                                   // the histograms are zero
 
-  for (int i = tid; i < kPasses * kBins; i += kSelThreads) hist[i] = 0u;
-  __syncthreads();
-  uint32_t prefix = 0u, mask = 0u;
-  int need = k;
+  // first digit of every key; a batch of loads is under way at a time
+  for (int i0 = tid; i0 < n; i0 += kThreads * kBatch) {
+    float x[kBatch];
 #pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const int bins = pass == 2 ? 1024 : 2048;
-    uint32_t* h = hist + pass * kBins;
-    if (pass == 0) {
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = order_key(w[i]);
+    for (int u = 0; u < kBatch; ++u)
+      if (i0 + u * kThreads < n) x[u] = w[i0 + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i < n) {
+        const uint32_t key = order_key(x[u]);
         if (i < a.cap) keys[i] = key;
-        atomicAdd(&h[key >> 21], 1u);
-      }
-    } else {
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = key_at(i);
-        if ((key & mask) == prefix) atomicAdd(&h[(key >> shift) & (bins - 1)], 1u);
+        atomicAdd(&hist[key >> 21], 1u);
       }
     }
-    cluster.sync();
-    // bins from the top: this thread's two, summed over the cluster
-    uint32_t c0 = 0u, c1 = 0u;
-    const int top = bins - 1 - 2 * tid;
-    if (top > 0)
-      for (int r = 0; r < C; ++r) {
-        const uint32_t* o = cluster.map_shared_rank(h, r);
-        c0 += o[top];
-        c1 += o[top - 1];
+  }
+  uint32_t prefix = 0u;
+  int need = k;
+  // The digit of T among `h`'s bins from the top, summed over the cluster:
+  // each CTA adds up its share of the bins and hands the sums to all (every
+  // CTA reading every peer's whole histogram took eight times the traffic).
+  auto digit = [&](const uint32_t* h, int bins) {
+    const uint32_t* sums = h;
+    if (C > 1) {
+      cluster.sync();
+      const int share = bins / C;
+      for (int i = rank * share + tid; i < (rank + 1) * share; i += kThreads) {
+        uint32_t v = 0u;
+#pragma unroll
+        for (int r = 0; r < kMostCtas; ++r)
+          if (r < C) v += cluster.map_shared_rank(h, r)[i];
+#pragma unroll
+        for (int r = 0; r < kMostCtas; ++r)
+          if (r < C) cluster.map_shared_rank(shared_sums, r)[i] = v;
       }
+      cluster.sync();
+      sums = shared_sums;
+    } else {
+      __syncthreads();
+    }
+    const int run = bins / kThreads;                 // bins per thread
+    const int top = bins - 1 - run * tid;
+    int c[kBinsPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) c[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i)
+      if (i < run) sum += c[i] = (int)sums[top - i];
     int total;
-    const int before = block_exclusive((int)(c0 + c1), warp_sums, &total);
-    if (before < need && need <= before + (int)(c0 + c1)) {
-      const bool first = need <= before + (int)c0;
-      sh_bin = first ? top : top - 1;
-      sh_need = need - before - (first ? 0 : (int)c0);
+    int before = block_exclusive<kThreads>(sum, warp_sums, &total);
+    if (before < need && need <= before + sum) {
+      int at = top;
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        if (before + c[i] >= need) break;
+        before += c[i];
+        --at;
+      }
+      sh_bin = at;
+      sh_need = need - before;
     }
     __syncthreads();
     need = sh_need;
-    prefix |= (uint32_t)sh_bin << shift;
-    mask |= (uint32_t)(bins - 1) << shift;
-    __syncthreads();                                 // sh_bin, sh_need may be written again
+    return (uint32_t)sh_bin;                         // (written again after further barriers only)
+  };
+  prefix = digit(hist, 2048) << 21;
+
+  // second digit of the open keys; the chunks' bits
+  uint32_t* h2 = hist + kBins;
+  for (int c0 = warp; c0 < chunks; c0 += kWarps * kBatch) {
+    uint32_t key[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = (c0 + u * kWarps) * 32 + lane;
+      key[u] = i < n ? key_at(i) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = c0 + u * kWarps;
+      if (c >= chunks) break;
+      const bool in = c * 32 + lane < n;
+      const bool eq = in && (key[u] >> 21) == (prefix >> 21);
+      const uint32_t bo = __ballot_sync(0xffffffffu, eq);
+      const uint32_t bk = __ballot_sync(0xffffffffu, in && (key[u] >> 21) > (prefix >> 21));
+      if (eq) atomicAdd(&h2[(key[u] >> 10) & 2047u], 1u);
+      if (lane == 0) {
+        open[c] = bo;
+        kept[c] = bk;
+      }
+    }
   }
-  // T = prefix; all candidates above it and the first `need` equal to it.
-  // Each warp takes a contiguous part of the slice.
-  const int seg = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int s0 = min(warp * seg, n), s1 = min(s0 + seg, n);
+  prefix |= digit(h2, 2048) << 10;
+
+  // From here on a thread owns a run of chunks.  An open key whose bits above
+  // `shift` are above T's is kept, one below is dropped.
+  const int mine = (chunks + kThreads - 1) / kThreads;
+  const int c_lo = min(tid * mine, chunks), c_hi = min(c_lo + mine, chunks);
+  auto settle = [&](int shift, auto still) {
+    for (int c = c_lo; c < c_hi; ++c) {
+      uint32_t o = open[c], k_bits = kept[c];
+      for (uint32_t left = o; left; left &= left - 1) {
+        const int bit = __ffs((int)left) - 1;
+        const uint32_t key = key_at(c * 32 + bit);
+        if ((key >> shift) == (prefix >> shift)) {
+          still(key);
+        } else {
+          o &= ~(1u << bit);
+          if ((key >> shift) > (prefix >> shift)) k_bits |= 1u << bit;
+        }
+      }
+      open[c] = o;
+      kept[c] = k_bits;
+    }
+  };
+  uint32_t* h3 = hist + 2 * kBins;
+  settle(10, [&](uint32_t key) { atomicAdd(&h3[key & 1023u], 1u); });
+  prefix |= digit(h3, 1024);                         // = T; `need` of the keys equal to it are kept
+  settle(0, [](uint32_t) {});
+
   int above = 0, equal = 0;
-  for (int i = s0 + lane; i < s1; i += 32) {
-    const uint32_t key = key_at(i);
-    above += key > prefix;
-    equal += key == prefix;
+  for (int c = c_lo; c < c_hi; ++c) {
+    above += __popc(kept[c]);
+    equal += __popc(open[c]);
   }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
   int total_above, total_equal;
-  int above_before = block_exclusive(lane == 0 ? above : 0, warp_sums, &total_above);
-  int equal_before = block_exclusive(lane == 0 ? equal : 0, warp_sums, &total_equal);
-  above_before = __shfl_sync(0xffffffffu, above_before, 0);
-  equal_before = __shfl_sync(0xffffffffu, equal_before, 0);
-  if (tid == 0) {
-    sh_counts[0] = total_above;
-    sh_counts[1] = total_equal;
+  int above_before = block_exclusive<kThreads>(above, warp_sums, &total_above);
+  int equal_before = block_exclusive<kThreads>(equal, warp_sums, &total_equal);
+  if (C > 1) {
+    if (tid == 0) {
+      sh_counts[0] = total_above;
+      sh_counts[1] = total_equal;
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      const int* o = cluster.map_shared_rank(sh_counts, r);
+      above_before += o[0];
+      equal_before += o[1];
+    }
   }
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) {
-    const int* o = cluster.map_shared_rank(sh_counts, r);
-    above_before += o[0];
-    equal_before += o[1];
+  for (int c = c_lo; c < c_hi; ++c) {
+    const uint32_t eq = open[c];
+    for (uint32_t left = eq | kept[c]; left; left &= left - 1) {
+      const int bit = __ffs((int)left) - 1;
+      if (eq >> bit & 1u) {
+        if (equal_before < need) out[above_before + equal_before] = lo + c * 32 + bit;
+        ++equal_before;
+      } else {
+        out[above_before + min(equal_before, need)] = lo + c * 32 + bit;
+        ++above_before;
+      }
+    }
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = s0; i0 < s1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < s1 ? key_at(i) : 0u;
-    const bool gt = i < s1 && key > prefix, eq = i < s1 && key == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    const int g = above_before + __popc(bg & below), e = equal_before + __popc(be & below);
-    if (gt || (eq && e < need)) out[g + min(e, need)] = lo + i;
-    above_before += __popc(bg);
-    equal_before += __popc(be);
+  if (C > 1) cluster.sync();                         // peers may still read this CTA's counts
+}
+
+// Shared memory of a CTA at most, and the longest rows whose chunk bits fit it.
+constexpr int kMostSmem = 200 * 1024;
+constexpr int kMostTokens = 1 << 21;
+
+template <int kThreads>
+kv_status launch_select(const SelectArgs& a, int64_t rows, int C, int dev, cudaStream_t s) {
+  static std::mutex mu;
+  static bool attr_set[64] = {};
+  kv_status st;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      st = cuda_check(cudaFuncSetAttribute(select_kernel<kThreads>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMostSmem),
+                      "cudaFuncSetAttribute(select_kernel)");
+      if (st != KV_OK) return st;
+      attr_set[dev] = true;
+    }
   }
-  cluster.sync();                                    // peers may still read this CTA's counts
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)((kPasses + 1) * kBins + 2 * a.chunk_cap + a.cap) * sizeof(uint32_t);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, select_kernel<kThreads>, a), "select_kernel launch");
 }
 
 // ---------------------------------------------------------------------------
@@ -252,8 +370,8 @@ __global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs
   }
   const int32_t* bt = a.block_tables + (int64_t)b * a.max_blocks;
   const int32_t* dt = a.dst_tables + (int64_t)b * a.dst_max_blocks;
-  uint4* cache = static_cast<uint4*>(a.cache[kv]);
-  float* scale = a.scale[kv];
+  uint4* cache = static_cast<uint4*>(kv ? a.cache[1] : a.cache[0]);
+  float* scale = kv ? a.scale[1] : a.scale[0];
   float* wrow = kv == 0 && a.weights ? a.weights + ((int64_t)b * Hkv + h) * a.weights_stride : nullptr;
   const int nblk = (m + BS - 1) / BS;
   for (int j0 = 0; j0 < nblk; j0 += kEvictWarps) {
@@ -305,7 +423,7 @@ __global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs
         for (int u = 0; u < kPer; ++u) {
           const int r = (u * 32 + lane) / kRow;
           const float sr = __shfl_sync(0xffffffffu, s, r);
-          if (r < rows) x[u] = recode16<kFp8>(x[u], sr, ns);
+          if (r < rows) x[u] = recode16<kFp8>(x[u], quotients(sr, ns), sr, ns);
         }
       }
     }
@@ -350,13 +468,15 @@ kv_status pagedkv_select_tokens(int32_t* keep_idx, int32_t* keep_len, const floa
   if (max_seq_len > weights_stride)
     return fail(KV_ERR_INVALID_ARG, "pagedkv_select_tokens: max_seq_len %d exceeds the weights' rows of %d",
                 max_seq_len, weights_stride);
+  if (max_seq_len > kMostTokens)
+    return fail(KV_ERR_INVALID_ARG, "pagedkv_select_tokens: max_seq_len is at most %d", kMostTokens);
   if (batch == 0) return KV_OK;
   if (!keep_idx || !keep_len || !weights || !seq_lens)
     return fail(KV_ERR_INVALID_ARG, "pagedkv_select_tokens: NULL pointer");
   const int64_t rows = (int64_t)batch * num_kv_heads;
   // CTAs per row: slices of about 4096 candidates, at most 8 CTAs
   int C = 1;
-  while (C < 8 && (int64_t)C * 4096 < max_seq_len) C *= 2;
+  while (C < kMostCtas && (int64_t)C * 4096 < max_seq_len) C *= 2;
   if (rows * C > 0x7fffffffLL)
     return fail(KV_ERR_INVALID_ARG, "pagedkv_select_tokens: too many rows");
   DeviceInfo di;
@@ -373,35 +493,13 @@ kv_status pagedkv_select_tokens(int32_t* keep_idx, int32_t* keep_len, const floa
   a.budget = budget;
   a.recent = recent;
   a.max_len = max_seq_len;
-  constexpr int kMostKeys = 40 * 1024;
   const int per = (max_seq_len + C - 1) / C;
-  a.cap = per < kMostKeys ? per : kMostKeys;
-  const size_t smem = (size_t)(kPasses * kBins + a.cap) * sizeof(uint32_t);
-  {
-    static std::mutex mu;
-    static bool attr_set[64] = {};
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr_set[di.device]) {
-      st = cuda_check(cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)((kPasses * kBins + kMostKeys) * sizeof(uint32_t))),
-                      "cudaFuncSetAttribute(select_kernel)");
-      if (st != KV_OK) return st;
-      attr_set[di.device] = true;
-    }
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, select_kernel, a), "select_kernel launch");
+  a.chunk_cap = (per + 31) / 32;
+  const int room = kMostSmem / (int)sizeof(uint32_t) - (kPasses + 1) * kBins - 2 * a.chunk_cap;
+  a.cap = per < room ? per : room;
+  cudaStream_t s = (cudaStream_t)stream;
+  return per <= 4096 ? launch_select<256>(a, rows, C, di.device, s)
+                     : launch_select<512>(a, rows, C, di.device, s);
 }
 
 kv_status pagedkv_evict_tokens(void* k_cache, void* v_cache, float* k_scale, float* v_scale,

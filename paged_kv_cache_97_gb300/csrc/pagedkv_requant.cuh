@@ -14,6 +14,8 @@ namespace dev {
 template <bool kFp8>
 constexpr float kCodeMax = kFp8 ? 448.0f : 127.0f;
 
+constexpr float kLargestFinite = 3.402823466e38f;
+
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
@@ -23,7 +25,7 @@ __device__ __forceinline__ float warp_max(float x) {
 // |x| when finite, else 0 (an infinity or NaN never sets a scale).
 __device__ __forceinline__ float finite_abs(float x) {
   const float m = fabsf(x);
-  return m <= 3.402823466e38f ? m : 0.0f;
+  return m <= kLargestFinite ? m : 0.0f;
 }
 
 // The scale of a block whose largest finite magnitude is amax (0: all zero).
@@ -32,7 +34,25 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __fdiv_rn(amax, kCodeMax<kFp8>);
 }
 
-// The four code values of a 32-bit word, lowest byte first.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The four code values of a 32-bit word, lowest byte first.  int8: each byte
+// is placed under the exponent of 2^23, c + 128 + 2^23, and 2^23 + 128 taken
+// off (exact; an integer conversion runs at an eighth of the add's rate).
 template <bool kFp8>
 __device__ __forceinline__ void code_values(uint32_t w, float (&v)[4]) {
   if constexpr (kFp8) {
@@ -44,46 +64,142 @@ __device__ __forceinline__ void code_values(uint32_t w, float (&v)[4]) {
     v[2] = b.x;
     v[3] = b.y;
   } else {
+    const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
+    for (int i = 0; i < 4; ++i)
+      v[i] = __uint_as_float(prmt(u, 0x4b000000u, 0x7440u + i)) - 8388736.0f;
   }
 }
 
-// Largest finite |c * s| of 16 codes.
+// Largest magnitude among 16 codes, as a code value (NaN codes passed over).
 template <bool kFp8>
-__device__ __forceinline__ float codes_amax(uint4 x, float s) {
+__device__ __forceinline__ float largest_code(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (kFp8) {
+    __half2 m = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = codes_to_f16x2<true>(w[i], 0x4140u), hi = codes_to_f16x2<true>(w[i], 0x4342u);
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&lo)));
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&hi)));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    // even and odd bytes as the upper bytes of 16-bit lanes
+    uint32_t most = 0u, least = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t odd = w[i] & 0xff00ff00u, even = (w[i] << 8) & 0xff00ff00u;
+      most = max_s16x2(most, max_s16x2(odd, even));
+      least = min_s16x2(least, min_s16x2(odd, even));
+    }
+    const int hi = max((int)(int16_t)(most & 0xffffu), (int)(int16_t)(most >> 16)) >> 8;
+    const int lo = min((int)(int16_t)(least & 0xffffu), (int)(int16_t)(least >> 16)) >> 8;
+    return (float)max(hi, -lo);
+  }
+}
+
+// Largest finite |c * s| of 16 codes, one by one (an overflowing or NaN scale).
+template <bool kFp8>
+__device__ __noinline__ float codes_amax_each(uint4 x, float s) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   float m = 0.0f;
-#pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[4];
     code_values<kFp8>(w[i], v);
-#pragma unroll
     for (int k = 0; k < 4; ++k) m = fmaxf(m, finite_abs(__fmul_rn(v[k], s)));
   }
   return m;
 }
 
-// The codes of four values under scale s, lowest byte first.
+// Largest finite |c * s| of 16 codes.  |c * s| in fp32 grows with |c|, so the
+// largest code decides unless its product is not finite.
 template <bool kFp8>
-__device__ __forceinline__ uint32_t code4(const float (&x)[4], float s) {
-  uint32_t o = 0u;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) o |= (uint32_t)code8<kFp8>(x[k], s) << (8 * k);
-  return o;
+__device__ __forceinline__ float codes_amax(uint4 x, float s) {
+  const float m = fabsf(__fmul_rn(largest_code<kFp8>(x), s));
+  return m <= kLargestFinite ? m : codes_amax_each<kFp8>(x, s);
 }
 
-// 16 codes under scale s as codes under scale ns.
+// Codes without a division per element.  The code of the fp32 quotient q =
+// x / s is wanted; q lies within a relative 2^-22 of x * r for the rounded
+// r = 1 / s (or, for x = c * t under an old scale t, of c * (t r)), so between
+// x * lo and x * hi with lo, hi = r (1 -+ 2^-21).  The code grows with the
+// value: where both ends have the same code it is q's, and only the words
+// where they differ (a border between two codes lies in between: about one
+// element in 2^16) are divided.  An IEEE division takes some 12 instructions
+// of the 22 per element these kernels had; they were bound by instruction
+// issue, at 21 % of the memory rate.  s == 0 reads as 1; factors outside
+// [2^-100, 2^100], whose products could lose bits, always divide.
+struct Interval {
+  float lo, hi;
+  bool on;
+};
+
+__device__ __forceinline__ bool plain_size(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+__device__ __forceinline__ Interval interval(float factor, bool on) {
+  return {factor * (1.0f - 0x1p-21f), factor * (1.0f + 0x1p-21f), on};
+}
+
+__device__ __forceinline__ float scale_or_one(float s) { return s == 0.0f ? 1.0f : s; }
+
+// Interval of x / s for finite x with |x / s| at most the largest code.
+__device__ __forceinline__ Interval quotients(float s) {
+  s = scale_or_one(s);
+  return interval(__frcp_rn(s), plain_size(s));
+}
+// Interval of (c * t) / s for codes c.
+__device__ __forceinline__ Interval quotients(float t, float s) {
+  s = scale_or_one(s);
+  return interval(t * __frcp_rn(s), plain_size(s) && plain_size(t));
+}
+
+// The codes of four values by division (out of line: rare, and its code,
+// repeated in every unrolled word, would not fit the instruction cache).
 template <bool kFp8>
-__device__ __forceinline__ uint4 recode16(uint4 x, float s, float ns) {
+__device__ __noinline__ uint32_t code4_divided(float x0, float x1, float x2, float x3, float s) {
+  return (uint32_t)code8<kFp8>(x0, s) | (uint32_t)code8<kFp8>(x1, s) << 8 |
+         (uint32_t)code8<kFp8>(x2, s) << 16 | (uint32_t)code8<kFp8>(x3, s) << 24;
+}
+
+// The codes of x[k] * f, lowest byte first (int8: |x[k] * f| < 128).
+template <bool kFp8>
+__device__ __forceinline__ uint32_t code4_times(const float (&x)[4], float f) {
+  if constexpr (kFp8) {
+    unsigned short lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * f), "f"(x[0] * f));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * f), "f"(x[2] * f));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  } else {
+    // x f + 1.5 2^23, rounded once, holds the nearest integer in its low bits
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = __float_as_uint(fmaf(x[k], f, 12582912.0f));
+    return prmt(prmt(t[0], t[1], 0x0040u), prmt(t[2], t[3], 0x0040u), 0x5410u);
+  }
+}
+
+// The codes of four finite values under scale s, with q = quotients(s).
+template <bool kFp8>
+__device__ __forceinline__ uint32_t code4(const float (&x)[4], const Interval& q, float s) {
+  const uint32_t o = code4_times<kFp8>(x, q.lo);
+  if (q.on && o == code4_times<kFp8>(x, q.hi)) return o;
+  return code4_divided<kFp8>(x[0], x[1], x[2], x[3], s);
+}
+
+// 16 codes under scale t as codes under scale s, with q = quotients(t, s).
+template <bool kFp8>
+__device__ __forceinline__ uint4 recode16(uint4 x, const Interval& q, float t, float s) {
   uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[4];
     code_values<kFp8>(w[i], v);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(v[k], s);
-    w[i] = code4<kFp8>(v, ns);
+    const uint32_t o = code4_times<kFp8>(v, q.lo);
+    w[i] = q.on && o == code4_times<kFp8>(v, q.hi)
+               ? o
+               : code4_divided<kFp8>(__fmul_rn(v[0], t), __fmul_rn(v[1], t), __fmul_rn(v[2], t),
+                                     __fmul_rn(v[3], t), s);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
