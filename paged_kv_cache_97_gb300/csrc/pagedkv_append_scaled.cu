@@ -22,7 +22,10 @@ namespace {
 
 using namespace dev;
 
-constexpr int kAppendWarps = 4;
+#ifndef PAGEDKV_APPEND_WARPS
+#define PAGEDKV_APPEND_WARPS 4
+#endif
+constexpr int kAppendWarps = PAGEDKV_APPEND_WARPS;
 
 struct AppendArgs {
   const uint4* rows[2];      // new K, V: bf16 [num_tokens, Hkv, D]
@@ -137,16 +140,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_scaled_kernel(const 
   for (int u = 0; u < kSteps; ++u) {
     const int r = u * kRows + sub;
     if (r >= r0 && r < r1) {
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 y = x[u][i / 2];
-        const uint32_t w0 = i % 2 ? y.z : y.x, w1 = i % 2 ? y.w : y.y;
-        const float v[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
-                            __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)};
-        o[i] = code4<kFp8>(v, q, s);
-      }
-      pool[base + (int64_t)r * Hkv * kLanes] = make_uint4(o[0], o[1], o[2], o[3]);
+      pool[base + (int64_t)r * Hkv * kLanes] = code16<kFp8>(x[u][0], x[u][1], q, s);
     }
   }
   if (lane == 0) *scale = s;

@@ -328,7 +328,10 @@ kv_status launch_select(const SelectArgs& a, int64_t rows, int C, int dev, cudaS
 // holding the whole block of one head in registers.  For 8-bit pools the warp
 // also finds the block's new scale from the rows it holds.
 
-constexpr int kEvictWarps = 8;
+#ifndef PAGEDKV_EVICT_WARPS
+#define PAGEDKV_EVICT_WARPS 8
+#endif
+constexpr int kEvictWarps = PAGEDKV_EVICT_WARPS;
 
 struct EvictArgs {
   void* cache[2];            // K, V

@@ -133,12 +133,13 @@ __device__ __forceinline__ float codes_amax(uint4 x, float s) {
 struct Interval {
   float lo, hi;
   bool on;
+  float s, r;                                        // the scale (0 as 1), its reciprocal
 };
 
 __device__ __forceinline__ bool plain_size(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
 
-__device__ __forceinline__ Interval interval(float factor, bool on) {
-  return {factor * (1.0f - 0x1p-21f), factor * (1.0f + 0x1p-21f), on};
+__device__ __forceinline__ Interval interval(float factor, bool on, float s, float r) {
+  return {factor * (1.0f - 0x1p-21f), factor * (1.0f + 0x1p-21f), on, s, r};
 }
 
 __device__ __forceinline__ float scale_or_one(float s) { return s == 0.0f ? 1.0f : s; }
@@ -146,20 +147,14 @@ __device__ __forceinline__ float scale_or_one(float s) { return s == 0.0f ? 1.0f
 // Interval of x / s for finite x with |x / s| at most the largest code.
 __device__ __forceinline__ Interval quotients(float s) {
   s = scale_or_one(s);
-  return interval(__frcp_rn(s), plain_size(s));
+  const float r = __frcp_rn(s);
+  return interval(r, plain_size(s), s, r);
 }
 // Interval of (c * t) / s for codes c.
 __device__ __forceinline__ Interval quotients(float t, float s) {
   s = scale_or_one(s);
-  return interval(t * __frcp_rn(s), plain_size(s) && plain_size(t));
-}
-
-// The codes of four values by division (out of line: rare, and its code,
-// repeated in every unrolled word, would not fit the instruction cache).
-template <bool kFp8>
-__device__ __noinline__ uint32_t code4_divided(float x0, float x1, float x2, float x3, float s) {
-  return (uint32_t)code8<kFp8>(x0, s) | (uint32_t)code8<kFp8>(x1, s) << 8 |
-         (uint32_t)code8<kFp8>(x2, s) << 16 | (uint32_t)code8<kFp8>(x3, s) << 24;
+  const float r = __frcp_rn(s);
+  return interval(t * r, plain_size(s) && plain_size(t), s, r);
 }
 
 // The codes of x[k] * f, lowest byte first (int8: |x[k] * f| < 128).
@@ -179,29 +174,87 @@ __device__ __forceinline__ uint32_t code4_times(const float (&x)[4], float f) {
   }
 }
 
-// The codes of four finite values under scale s, with q = quotients(s).
-template <bool kFp8>
-__device__ __forceinline__ uint32_t code4(const float (&x)[4], const Interval& q, float s) {
-  const uint32_t o = code4_times<kFp8>(x, q.lo);
-  if (q.on && o == code4_times<kFp8>(x, q.hi)) return o;
-  return code4_divided<kFp8>(x[0], x[1], x[2], x[3], s);
+// Four values of a source: the bf16 pairs of two words, or (kCodes) the codes
+// of one.
+template <bool kFp8, bool kCodes>
+__device__ __forceinline__ void four_values(const uint32_t* w, float (&v)[4]) {
+  if constexpr (kCodes) {
+    code_values<kFp8>(w[0], v);
+  } else {
+    v[0] = __uint_as_float(w[0] << 16);
+    v[1] = __uint_as_float(w[0] & 0xffff0000u);
+    v[2] = __uint_as_float(w[1] << 16);
+    v[3] = __uint_as_float(w[1] & 0xffff0000u);
+  }
 }
 
-// 16 codes under scale t as codes under scale s, with q = quotients(t, s).
+// 16 codes by division (out of line: rare, and its code, repeated in every
+// unrolled piece, would not fit the instruction cache).
+template <bool kFp8, bool kCodes>
+__device__ __noinline__ uint4 code16_divided(uint4 a, uint4 b, float t, float s) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    four_values<kFp8, kCodes>(w + (kCodes ? i : 2 * i), v);
+    o[i] = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[i] |= (uint32_t)code8<kFp8>(kCodes ? __fmul_rn(v[k], t) : v[k], s) << (8 * k);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 16 codes under scale t as codes under scale s, at both ends of q =
+// quotients(t, s), and by division when any differ: one branch per 16, so that
+// the conversions of all four words run together.
 template <bool kFp8>
 __device__ __forceinline__ uint4 recode16(uint4 x, const Interval& q, float t, float s) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4], off = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[4];
     code_values<kFp8>(w[i], v);
-    const uint32_t o = code4_times<kFp8>(v, q.lo);
-    w[i] = q.on && o == code4_times<kFp8>(v, q.hi)
-               ? o
-               : code4_divided<kFp8>(__fmul_rn(v[0], t), __fmul_rn(v[1], t), __fmul_rn(v[2], t),
-                                     __fmul_rn(v[3], t), s);
+    o[i] = code4_times<kFp8>(v, q.lo);
+    off |= o[i] ^ code4_times<kFp8>(v, q.hi);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  if (q.on && off == 0u) return make_uint4(o[0], o[1], o[2], o[3]);
+  return code16_divided<kFp8, true>(x, x, t, s);
+}
+
+// 16 finite bf16 values under scale s, with q = quotients(s).  int8 goes by
+// the interval as above.  For E4M3 a border is often met: both the values and
+// the block's largest (448 s) have 8 significant bits, so x / s falls next to
+// a midpoint of two codes in 0.5 % of N(0, 1) values and 43 % of warps had to
+// divide.  There the quotient itself is made, by two of Markstein's correction
+// steps (P. Markstein, IBM J. Res. Dev. 34, 1990) with r the correctly rounded
+// reciprocal: q0 = x r is within 2 units in the last place, the first step
+// brings it within one, from where the second rounds correctly.
+template <bool kFp8>
+__device__ __forceinline__ uint4 code16(uint4 a, uint4 b, const Interval& q, float s) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t o[4], off = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    four_values<kFp8, false>(w + 2 * i, v);
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float y = v[k] * q.r;
+        y = fmaf(fmaf(-y, q.s, v[k]), q.r, y);
+        v[k] = fmaf(fmaf(-y, q.s, v[k]), q.r, y);
+      }
+      o[i] = code4_times<true>(v, 1.0f);
+    } else {
+      o[i] = code4_times<false>(v, q.lo);
+      off |= o[i] ^ code4_times<false>(v, q.hi);
+    }
+  }
+  if (q.on && off == 0u) return make_uint4(o[0], o[1], o[2], o[3]);
+  return code16_divided<kFp8, false>(a, b, 1.0f, s);
 }
 
 }  // namespace dev
