@@ -22,10 +22,7 @@ namespace {
 
 using namespace dev;
 
-#ifndef PAGEDKV_APPEND_WARPS
-#define PAGEDKV_APPEND_WARPS 4
-#endif
-constexpr int kAppendWarps = PAGEDKV_APPEND_WARPS;
+constexpr int kAppendWarps = 4;
 
 struct AppendArgs {
   const uint4* rows[2];      // new K, V: bf16 [num_tokens, Hkv, D]

@@ -324,14 +324,19 @@ kv_status launch_select(const SelectArgs& a, int64_t rows, int C, int dev, cudaS
 // list ascends), so a CTA that packs destination blocks in ascending order
 // may work in place: the rows it stores lie before every row it still has to
 // load, and the loads of one round are all done before its stores.  One CTA
-// per (KV head, sequence, K or V); one warp per destination block and round,
-// holding the whole block of one head in registers.  For 8-bit pools the warp
-// also finds the block's new scale from the rows it holds.
+// (or, in small batches, a cluster) per (KV head, sequence, K or V); one warp
+// per destination block and round, holding the whole block of one head in
+// registers.  For 8-bit pools the warp also finds the block's new scale from
+// the rows it holds.  Where no destination block is its own source, nothing is
+// stored where anything is read and the warps run on without the barrier.
+//
+// 8-bit pools are bound by instruction issue (the codes), bf16 by HBM: 128
+// sequences of 1..8K tokens packed to 2K, E4M3, 321 us to fresh blocks and 277
+// in place (49 and 57 % of the copy rate; four CTAs per SM, with the registers
+// held to 64, against three: 359 and 361); 64 sequences of 512..4096 packed to
+// 1K, bf16 in place, 84 us (91 %).
 
-#ifndef PAGEDKV_EVICT_WARPS
-#define PAGEDKV_EVICT_WARPS 8
-#endif
-constexpr int kEvictWarps = PAGEDKV_EVICT_WARPS;
+constexpr int kEvictWarps = 8;
 
 struct EvictArgs {
   void* cache[2];            // K, V
@@ -348,17 +353,20 @@ struct EvictArgs {
 };
 
 template <int D, int BS, int kKind>
-__global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 : 1)
+    evict_kernel(const EvictArgs a) {
   constexpr bool kQ8 = kKind != KV_DTYPE_BF16, kFp8 = kKind == KV_DTYPE_FP8_E4M3;
   constexpr int kRow = D * (kQ8 ? 1 : 2) / 16;       // 16-byte pieces per row
   constexpr int kPer = BS * kRow / 32;               // pieces per lane
-  const int h = blockIdx.x, b = blockIdx.y, kv = blockIdx.z;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int h = blockIdx.x / C, b = blockIdx.y, kv = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = a.num_kv_heads;
   const int L = a.seq_lens[b], m = a.keep_len[b];
   if (m < 0 || m > L || m > a.budget || (int64_t)L > (int64_t)a.max_blocks * BS ||
       (m + BS - 1) / BS > a.dst_max_blocks || (a.weights && L > a.weights_stride)) {
-    if (threadIdx.x == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+    if (threadIdx.x == 0 && rank == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
     return;
   }
   const int32_t* idx = a.keep_idx + ((int64_t)b * Hkv + h) * a.budget;
@@ -368,17 +376,21 @@ __global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs
     bad |= t >= L || t <= (j > 0 ? idx[j - 1] : -1);
   }
   if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
+    if (threadIdx.x == 0 && rank == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
     return;
   }
   const int32_t* bt = a.block_tables + (int64_t)b * a.max_blocks;
   const int32_t* dt = a.dst_tables + (int64_t)b * a.dst_max_blocks;
+  const int nblk = (m + BS - 1) / BS;
+  // no block stays: nothing is stored where something is still to be read
+  bool stays = false;
+  for (int j = threadIdx.x; j < nblk; j += blockDim.x) stays |= dt[j] == bt[j];
+  const bool in_place = __syncthreads_or(stays);
   uint4* cache = static_cast<uint4*>(kv ? a.cache[1] : a.cache[0]);
   float* scale = kv ? a.scale[1] : a.scale[0];
   float* wrow = kv == 0 && a.weights ? a.weights + ((int64_t)b * Hkv + h) * a.weights_stride : nullptr;
-  const int nblk = (m + BS - 1) / BS;
-  for (int j0 = 0; j0 < nblk; j0 += kEvictWarps) {
-    const int j = j0 + warp;                         // this warp's destination block
+  for (int j0 = 0; j0 < nblk; j0 += C * kEvictWarps) {
+    const int j = j0 + rank * kEvictWarps + warp;    // this warp's destination block
     bool move = j < nblk;
     const int rows = move ? min(BS, m - j * BS) : 0;
     int64_t slot = 0;                                // lane r: row r's source slot
@@ -430,7 +442,10 @@ __global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs
         }
       }
     }
-    __syncthreads();                                 // the round's loads are done
+    if (in_place) {                                  // the round's loads are done
+      if (C > 1) cluster.sync();
+      else __syncthreads();
+    }
     if (move) {
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
@@ -443,14 +458,33 @@ __global__ void __launch_bounds__(kEvictWarps * 32) evict_kernel(const EvictArgs
   }
 }
 
+template <int D, int BS, int kKind>
+kv_status launch_evict_t(const EvictArgs& a, int batch, int C, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.num_kv_heads * C), (unsigned)batch, 2);
+  cfg.blockDim = dim3(kEvictWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cuda_check(cudaLaunchKernelEx(&cfg, evict_kernel<D, BS, kKind>, a), "evict_kernel launch");
+}
+
 template <int D, int BS>
-kv_status launch_evict(const EvictArgs& a, kv_dtype dtype, int batch, cudaStream_t s) {
-  const dim3 grid((unsigned)a.num_kv_heads, (unsigned)batch, 2);
-  const int threads = kEvictWarps * 32;
-  if (dtype == KV_DTYPE_INT8) evict_kernel<D, BS, KV_DTYPE_INT8><<<grid, threads, 0, s>>>(a);
-  else if (dtype == KV_DTYPE_FP8_E4M3) evict_kernel<D, BS, KV_DTYPE_FP8_E4M3><<<grid, threads, 0, s>>>(a);
-  else evict_kernel<D, BS, KV_DTYPE_BF16><<<grid, threads, 0, s>>>(a);
-  return cuda_check(cudaGetLastError(), "evict_kernel launch");
+kv_status launch_evict(const EvictArgs& a, kv_dtype dtype, int batch, int num_sms, cudaStream_t s) {
+  // CTAs of a (KV head, sequence, K or V): one, or a cluster while those alone
+  // leave SMs idle and there are further rounds to share
+  int C = 1;
+  while (C < kMostCtas && (int64_t)a.num_kv_heads * batch * 4 * C <= num_sms &&
+         (int64_t)C * kEvictWarps * BS < a.budget)
+    C *= 2;
+  if (dtype == KV_DTYPE_INT8) return launch_evict_t<D, BS, KV_DTYPE_INT8>(a, batch, C, s);
+  if (dtype == KV_DTYPE_FP8_E4M3) return launch_evict_t<D, BS, KV_DTYPE_FP8_E4M3>(a, batch, C, s);
+  return launch_evict_t<D, BS, KV_DTYPE_BF16>(a, batch, C, s);
 }
 
 }  // namespace
@@ -520,6 +554,7 @@ kv_status pagedkv_evict_tokens(void* k_cache, void* v_cache, float* k_scale, flo
   if (block_size != 16 && block_size != 32)
     return fail(KV_ERR_INVALID_ARG, "pagedkv_evict_tokens: block_size must be 16 or 32");
   if (batch > 65535) return fail(KV_ERR_INVALID_ARG, "pagedkv_evict_tokens: at most 65535 sequences");
+  if (num_kv_heads > 65535) return fail(KV_ERR_INVALID_ARG, "pagedkv_evict_tokens: at most 65535 KV heads");
   if (batch == 0) return KV_OK;
   if (!k_cache || !v_cache || !block_tables || !dst_block_tables || !seq_lens || !keep_idx || !keep_len)
     return fail(KV_ERR_INVALID_ARG, "pagedkv_evict_tokens: NULL pointer");
@@ -552,8 +587,10 @@ kv_status pagedkv_evict_tokens(void* k_cache, void* v_cache, float* k_scale, flo
   a.budget = budget;
   cudaStream_t s = (cudaStream_t)stream;
   if (head_dim == 128)
-    return block_size == 32 ? launch_evict<128, 32>(a, dtype, batch, s) : launch_evict<128, 16>(a, dtype, batch, s);
-  return block_size == 32 ? launch_evict<64, 32>(a, dtype, batch, s) : launch_evict<64, 16>(a, dtype, batch, s);
+    return block_size == 32 ? launch_evict<128, 32>(a, dtype, batch, di.num_sms, s)
+                            : launch_evict<128, 16>(a, dtype, batch, di.num_sms, s);
+  return block_size == 32 ? launch_evict<64, 32>(a, dtype, batch, di.num_sms, s)
+                          : launch_evict<64, 16>(a, dtype, batch, di.num_sms, s);
 }
 
 }  // extern "C"
