@@ -100,6 +100,12 @@ inline size_t ml_region_floats(size_t rows, int slots) {
 // a small cache.
 kv_status make_kv_maps(const DecodeArgs& a, CUtensorMap* k_map, CUtensorMap* v_map);
 
+// Tensor map over bf16 query rows [num_tokens, num_q_heads, head_dim]: box =
+// 64 elements of the `group` heads of one KV head of `tile_tokens` tokens
+// (128-byte swizzle; group * tile_tokens rows, token-major).
+kv_status make_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads,
+                         int head_dim, int group, int tile_tokens);
+
 // Launches the per-partition decode kernel (with the append fused in when
 // new_k is set).
 kv_status launch_decode(const DecodeArgs& a, cudaStream_t stream);

@@ -18,17 +18,13 @@
 #include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
 #include "pagedkv_requant.cuh"
+#include "pagedkv_tc.cuh"
+#include "pagedkv_weights.cuh"
 
 namespace pagedkv {
 namespace {
 
 using namespace dev;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // ---------------------------------------------------------------------------
 // One-token decode
@@ -116,33 +112,6 @@ constexpr int kNTiles = kRowTile / 8;
 constexpr int kWarps = 4;
 constexpr int kWarpKeys = 32;                          // keys per warp and step
 constexpr int kCtaKeys = kWarps * kWarpKeys;
-
-struct PromptArgs {
-  float* weights;            // [B, Hkv, stride]
-  const void* q;             // bf16 [T, Hq, D]
-  const void* k_cache;
-  const float* k_scale;
-  const int32_t* block_tables;
-  const int32_t* seq_lens;
-  const int32_t* query_start;
-  float* stats;              // [T, Hq, splits, 2] (m, l)
-  unsigned int* flags;
-  int64_t stride;
-  int batch, num_tokens, max_query_len, num_q_heads, num_kv_heads, num_blocks, max_blocks;
-  int max_seq_len, part_tokens, splits, accumulate;
-  float scale_log2;
-};
-
-// Row and key range of sequence b; false (and a flag once per head) when its
-// length or offsets are bad.  n == 0: no queries.
-__device__ __forceinline__ bool prompt_rows(const PromptArgs& a, int b, int bs, int* q0, int* n, int* L) {
-  *q0 = a.query_start[b];
-  *n = a.query_start[b + 1] - *q0;
-  *L = a.seq_lens[b];
-  return *q0 >= 0 && *n >= 0 && *q0 <= a.num_tokens - *n && *n <= a.max_query_len && *L > 0 &&
-         *n <= *L && *L <= a.max_seq_len && (int64_t)*L <= (int64_t)a.max_blocks * bs &&
-         (int64_t)*L <= a.stride;
-}
 
 template <int D>
 constexpr int kQStride = D * 2 + 64;                   // bytes; 16-byte pieces of 2 rows fill 32 banks
@@ -436,7 +405,7 @@ kv_status launch_prompt_t(const PromptArgs& a, int tiles, cudaStream_t s) {
 }
 
 template <int D, int BS>
-kv_status launch_prompt(const PromptArgs& a, kv_dtype dtype, int tiles, cudaStream_t s) {
+kv_status launch_prompt_mma(const PromptArgs& a, kv_dtype dtype, int tiles, cudaStream_t s) {
   if (dtype == KV_DTYPE_INT8) return launch_prompt_t<D, BS, KV_DTYPE_INT8>(a, tiles, s);
   if (dtype == KV_DTYPE_FP8_E4M3) return launch_prompt_t<D, BS, KV_DTYPE_FP8_E4M3>(a, tiles, s);
   return launch_prompt_t<D, BS, KV_DTYPE_BF16>(a, tiles, s);
@@ -602,7 +571,13 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
     return fail(KV_ERR_INVALID_ARG, "%s: 8-bit pools need k_scale; bf16 pools take NULL", who);
   const int64_t G = num_q_heads / num_kv_heads;
   const int longest = max_query_len < num_tokens ? max_query_len : num_tokens;
-  const int64_t tiles = (longest * G + kRowTile - 1) / kRowTile;
+  // Many rows per KV head on a bf16 pool: the tcgen05 kernels, whose row tile
+  // is 128 rows of whole tokens; else the mma.sync kernels above.  (Their
+  // score scale is positive.)
+  const bool tc = dtype == KV_DTYPE_BF16 && scale > 0.0f && G <= 128 && longest * G > kRowTile;
+  const int64_t tile_tokens = tc ? 128 / G : 0;
+  const int64_t tiles = tc ? (longest + tile_tokens - 1) / tile_tokens
+                           : (longest * G + kRowTile - 1) / kRowTile;
   if (longest * G > 0x7fffff00LL || tiles > 65535 || tiles * batch > 0x7fffffffLL ||
       (max_seq_len - 1) / kCtaKeys + 1 > 65535)
     return fail(KV_ERR_INVALID_ARG, "%s: too many query tokens or too long sequences", who);
@@ -639,12 +614,14 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
                 "%s: workspace must be 16-byte aligned and hold %zu bytes "
                 "(pagedkv_attention_weights_workspace_bytes gives a safe size)", who, need);
   a.stats = static_cast<float*>(workspace);
+  a.tile_tokens = (int)tile_tokens;
   cudaStream_t s = (cudaStream_t)stream;
+  if (tc) return launch_prompt_tc(a, head_dim, block_size, (int)tiles, s);
   if (head_dim == 128)
-    return block_size == 32 ? launch_prompt<128, 32>(a, dtype, (int)tiles, s)
-                            : launch_prompt<128, 16>(a, dtype, (int)tiles, s);
-  return block_size == 32 ? launch_prompt<64, 32>(a, dtype, (int)tiles, s)
-                          : launch_prompt<64, 16>(a, dtype, (int)tiles, s);
+    return block_size == 32 ? launch_prompt_mma<128, 32>(a, dtype, (int)tiles, s)
+                            : launch_prompt_mma<128, 16>(a, dtype, (int)tiles, s);
+  return block_size == 32 ? launch_prompt_mma<64, 32>(a, dtype, (int)tiles, s)
+                          : launch_prompt_mma<64, 16>(a, dtype, (int)tiles, s);
 }
 
 }  // extern "C"
