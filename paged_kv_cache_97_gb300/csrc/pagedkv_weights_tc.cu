@@ -11,17 +11,19 @@
 //   column sums      fixed: 128 keys,        streamed: the row tiles that see
 //                    them; a thread owns a key and adds 2^(s - m') over the
 //                    rows, m' = m + log2 l of each row from shared memory
-// so that neither a maximum nor a sum crosses threads.  Warps 0-3 hold one
-// fixed row per thread (a TMEM lane), warp 4 issues the MMAs (S[128 x 128] =
-// fixed . streamed^T into one of two TMEM buffers), warp 5 the TMA loads, and
-// in the column sums warps 6-9 join each row tile's statistics.  A query tile
-// is whole tokens, tile_tokens = 128 / G of them times the G heads, as one TMA
-// box; rows past the sequence's queries are masked.
+// so that neither a maximum nor a sum crosses threads.  Warps 0-7 hold one
+// fixed row per thread (a TMEM lane) and 64 of its 128 columns, warp 8 issues
+// the MMAs (S[128 x 128] = fixed . streamed^T into one of two TMEM buffers),
+// warp 9 the TMA loads, and in the column sums warp 10 fetches each row tile's
+// m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
+// heads, as one TMA box; rows past the sequence's queries are masked.
 //
-// The exponentials bound it: 128 x 128 of them take 1024 cycles of an SM's
-// special-function unit, the MMAs of a tile 256.  Two CTAs per SM (256 TMEM
-// columns and about 100 KB of shared memory each) so that one's start and end
-// overlap the other's work.
+// What bounds it is the issue of the epilogue's instructions: a 128 x 128 tile
+// has 16384 exponentials against 256 cycles of MMA, so each costs one packed
+// half of a multiply-add and of an add beside it (f32x2), and no maximum: a
+// row's reference is its first scores' and moves only when a sum grows past
+// 2^60.  Two CTAs per SM (256 TMEM columns and about 100 KB of shared memory
+// each), so that one's start and end overlap the other's work.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,9 +42,11 @@ using namespace dev;
 
 constexpr int kTile = 128;                             // rows of either operand
 constexpr int kStages = 2;                             // = TMEM buffers
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kStatWarp = 6;
+constexpr int kRowWarps = 8;                           // two per 32 rows, 64 columns each
+constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1, kStatWarp = kRowWarps + 2;
+constexpr int kStatsThreads = (kRowWarps + 2) * 32, kSumsThreads = (kRowWarps + 3) * 32;
 constexpr int kTmemCols = kStages * kTile;
-constexpr float kMoveLog2 = 8.0f;                      // move a row's reference past 2^8
+constexpr float kMoveSum = 0x1p60f;                    // a sum of 32 that moves a row's reference
 
 template <int D>
 struct PGeo {
@@ -62,63 +66,120 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Running statistics of a query row: 2^(s sl2 - ref) summed to l.  The
-// reference moves only when a score passes it by 2^8, so l <= 2^8 keys.
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float x) { return pack_f32x2(__float_as_uint(x), __float_as_uint(x)); }
+
+// 2^x of both halves.
+__device__ __forceinline__ uint64_t ex2_f32x2(uint64_t v) {
+  float lo, hi;
+  unpack_f32x2(v, lo, hi);
+  return pack_f32x2(__float_as_uint(ex2(lo)), __float_as_uint(ex2(hi)));
+}
+
+// Sum of the halves of two pairs.
+__device__ __forceinline__ float sum_f32x2(uint64_t a, uint64_t b) {
+  float lo, hi;
+  unpack_f32x2(add_f32x2(a, b), lo, hi);
+  return lo + hi;
+}
+
+// sum over 32 scores of 2^(s sl2 + off).
+__device__ __forceinline__ float exp_sum(const uint32_t (&raw)[32], float sl2, float off) {
+  const uint64_t f = both(sl2), o = both(off);
+  uint64_t s[2] = {0ull, 0ull};
+#pragma unroll
+  for (int j = 0; j < 32; j += 2)
+    s[(j >> 1) & 1] = add_f32x2(s[(j >> 1) & 1], ex2_f32x2(fma_f32x2(pack_f32x2(raw[j], raw[j + 1]), f, o)));
+  return sum_f32x2(s[0], s[1]);
+}
+
+// Running statistics of a query row: l = sum of 2^(s sl2 - ref).  Any
+// reference serves as long as nothing overflows (fp32 sums keep their relative
+// precision), so it is the largest of the row's first scores and moves only
+// when 32 scores sum to more than 2^60 against it.
 struct RowStats {
   float ref, l;
 };
 
+__device__ __forceinline__ float largest(const uint32_t (&raw)[32]) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(raw[j]));
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
 // 32 scores of the row (of keys up to `lim` of the 32 when kMask).
 template <bool kMask>
 __device__ __forceinline__ void add_scores(RowStats& st, uint32_t (&raw)[32], float sl2, int lim) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if constexpr (kMask) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (kMask && j > lim) raw[j] = 0xff800000u;        // -inf
-    mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(raw[j]));
+    for (int j = 0; j < 32; ++j)
+      if (j > lim) raw[j] = 0xff800000u;               // -inf
   }
-  const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-  if (m > st.ref + kMoveLog2) {
+  if (st.ref == -INFINITY) st.ref = largest(raw) * sl2;
+  float part = exp_sum(raw, sl2, st.ref == -INFINITY ? 0.0f : -st.ref);
+  if (part > kMoveSum) {
+    const float m = largest(raw) * sl2;
     st.l *= ex2(st.ref - m);
     st.ref = m;
+    part = exp_sum(raw, sl2, -m);
   }
-  const float off = st.ref == -INFINITY ? 0.0f : st.ref;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(raw[j]), sl2, -off));
-  st.l += (s[0] + s[1]) + (s[2] + s[3]);
+  st.l += part;
 }
 
-// sum over 32 rows of 2^(s sl2 - m') (rows at or past `key` when kMask).
+// sum over 32 rows of 2^(s sl2 - m'), neg_m = -m' (rows in [from, to) of the
+// 32 when kMask).
 template <bool kMask>
-__device__ __forceinline__ float column_part(const uint32_t (&raw)[32], float sl2, const float* m,
-                                             const int* pos, int key) {
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ float column_part(const uint32_t (&raw)[32], float sl2, const float* neg_m,
+                                             int from, int to) {
+  const uint64_t f = both(sl2);
+  uint64_t s[2] = {0ull, 0ull};
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
-    const float4 r = *reinterpret_cast<const float4*>(m + j);
-    const float e0 = ex2(fmaf(__uint_as_float(raw[j]), sl2, -r.x));
-    const float e1 = ex2(fmaf(__uint_as_float(raw[j + 1]), sl2, -r.y));
-    const float e2 = ex2(fmaf(__uint_as_float(raw[j + 2]), sl2, -r.z));
-    const float e3 = ex2(fmaf(__uint_as_float(raw[j + 3]), sl2, -r.w));
+    const uint4 m = *reinterpret_cast<const uint4*>(neg_m + j);
+    uint64_t e0 = ex2_f32x2(fma_f32x2(pack_f32x2(raw[j], raw[j + 1]), f, pack_f32x2(m.x, m.y)));
+    uint64_t e1 = ex2_f32x2(fma_f32x2(pack_f32x2(raw[j + 2], raw[j + 3]), f, pack_f32x2(m.z, m.w)));
     if constexpr (kMask) {
-      const int4 p = *reinterpret_cast<const int4*>(pos + j);
-      s[0] += p.x >= key ? e0 : 0.0f;
-      s[1] += p.y >= key ? e1 : 0.0f;
-      s[2] += p.z >= key ? e2 : 0.0f;
-      s[3] += p.w >= key ? e3 : 0.0f;
-    } else {
-      s[0] += e0;
-      s[1] += e1;
-      s[2] += e2;
-      s[3] += e3;
+      float a, b, c, d;
+      unpack_f32x2(e0, a, b);
+      unpack_f32x2(e1, c, d);
+      a = j >= from && j < to ? a : 0.0f;
+      b = j + 1 >= from && j + 1 < to ? b : 0.0f;
+      c = j + 2 >= from && j + 2 < to ? c : 0.0f;
+      d = j + 3 >= from && j + 3 < to ? d : 0.0f;
+      e0 = pack_f32x2(__float_as_uint(a), __float_as_uint(b));
+      e1 = pack_f32x2(__float_as_uint(c), __float_as_uint(d));
     }
+    s[0] = add_f32x2(s[0], e0);
+    s[1] = add_f32x2(s[1], e1);
   }
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  return sum_f32x2(s[0], s[1]);
+}
+
+// m + log2 l of a row.
+__device__ __forceinline__ float row_log_sum(float m, float l) {
+  return m == -INFINITY ? __uint_as_float(0x7fc00000u) : m + log2f(l);
 }
 
 template <int D, int BS, bool kStats>
-__global__ void __launch_bounds__(kStats ? 192 : 320, 2)
+__global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap q_map, const PromptArgs a) {
   using P = PGeo<D>;
@@ -127,8 +188,8 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
       stat_full[kStages], drain_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int sh_bad, sh_fail;
-  __shared__ __align__(16) float row_m[kStages][kTile];
-  __shared__ __align__(16) int row_pos[kStages][kTile];
+  __shared__ __align__(16) float row_m[kStages][kTile];  // -m' of the row tile's rows
+  __shared__ float half_part[kTile], half_ref[kTile];  // the upper columns' results
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x, b = blockIdx.y;
   const int G = a.num_q_heads / a.num_kv_heads, TT = a.tile_tokens;
@@ -150,12 +211,15 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
   const int kend = kStats ? min(first_pos + tn, k0 + a.part_tokens) : min(L, k0 + kTile);
   const int rt0 = kStats ? 0 : max(0, k0 - (L - n)) / TT;        // first row tile that sees a key
   const int nch = kStats ? max(0, (kend - k0 + kTile - 1) / kTile) : (n - 1) / TT + 1 - rt0;
-  // global row of row r of the tile that starts at token i
-  auto row_at = [&](int i, int r) { return (int64_t)(q0 + i + r / G) * a.num_q_heads + hk * G + r % G; };
+  // statistics of row 0 of the tile that starts at token i: [Hkv][T][G], so
+  // that a tile's rows lie together
+  auto stats_at = [&](int i) {
+    return a.stats + ((int64_t)hk * a.num_tokens + q0 + i) * G * a.splits * 2;
+  };
   const int my_rows = kStats ? tn * G : 0;
   if (kStats && nch == 0) {                            // no key of this split
     if (tid < my_rows) {
-      float* o = a.stats + (row_at(i0, tid) * a.splits + split) * 2;
+      float* o = stats_at(i0) + ((int64_t)tid * a.splits + split) * 2;
       o[0] = -INFINITY;
       o[1] = 0.0f;
     }
@@ -172,8 +236,8 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 1);
       mbar_init(smem_addr(&s_full[s]), 1);
-      mbar_init(smem_addr(&buf_free[s]), 4);
-      mbar_init(smem_addr(&stat_full[s]), 4);
+      mbar_init(smem_addr(&buf_free[s]), kRowWarps);
+      mbar_init(smem_addr(&stat_full[s]), 1);
     }
     mbar_init(smem_addr(&drain_bar), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -269,46 +333,42 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
       mbar_wait(smem_addr(&drain_bar), 0);
     }
     __syncwarp();
-  } else if (!kStats && warp >= kStatWarp) {
-    // ======================= column sums: the row tiles' statistics =========
-    const int r = tid - kStatWarp * 32;
+  } else if (!kStats && warp == kStatWarp) {
+    // ======================= column sums: -m' of the row tiles ==============
     bool bad = false, ok = true;
     for (int c = 0; c < nch; ++c) {
       const int s = c % kStages, i = (rt0 + c) * TT;
-      float m = 0.0f;
-      int pos = -1;
-      if (r < min(TT, n - i) * G) {
-        pos = L - n + i + r / G;
-        const float* ml = a.stats + row_at(i, r) * a.splits * 2;
-        const int ns = pos / a.part_tokens + 1;        // splits with keys of this row
-        float M = -INFINITY, den = 0.0f;
-        for (int k = 0; k < ns; ++k) M = fmaxf(M, ml[2 * k]);
-        for (int k = 0; k < ns; ++k) {
-          bad |= ml[2 * k + 1] < 0.0f;
-          den = fmaf(exp2f(ml[2 * k] - M), ml[2 * k + 1], den);
-        }
-        m = M + log2f(den);
+      const int rows = min(TT, n - i) * G;
+      const float* st_row = stats_at(i);
+      float m[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = u * 32 + lane;
+        m[u] = r < rows ? st_row[(int64_t)r * a.splits * 2] : 0.0f;
+        bad |= m[u] == -INFINITY;                      // a row without statistics
       }
       if (c >= kStages && !warp_wait(smem_addr(&buf_free[s]), ((c / kStages) - 1) & 1)) {
         ok = false;
         break;
       }
-      row_m[s][r] = m;
-      row_pos[s][r] = pos;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) row_m[s][u * 32 + lane] = -m[u];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&stat_full[s]));
     }
     if (bad) sh_bad = 1;
-    if (!ok) sh_fail = 1;
+    if (!ok && lane == 0) sh_fail = 1;
   } else {
-    // ======================= one fixed row per thread (warps 0-3) ===========
+    // ======================= one fixed row per thread, 64 columns ===========
     bool ok = true;
-    const int key = k0 + tid;                          // column sums
-    const int pos = kStats && tid < my_rows ? first_pos + tid / G : -1;
+    const int row = tid & (kTile - 1), half = warp >> 2;
+    const int key = k0 + row;                          // column sums
+    const int pos = kStats && row < my_rows ? first_pos + row / G : -1;
     // a warp whose rows are all padding only keeps the barriers' phases
-    const bool live = kStats ? warp * 32 < my_rows : k0 + warp * 32 < kend;
+    const int row_lo = (warp & 3) * 32;
+    const bool live = kStats ? row_lo < my_rows : k0 + row_lo < kend;
     const float sl2 = a.scale_log2;
-    const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tm + ((uint32_t)row_lo << 16) + 64 * half;
     for (int c = 0; c < nch; ++c) {
       const int s = c % kStages, ph = (c / kStages) & 1;
       if (!warp_wait(smem_addr(&s_full[s]), ph) ||
@@ -317,29 +377,32 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
         break;
       }
       tc_fence_after();
-      if (live) {
+      const int c0 = k0 + c * kTile;                   // row statistics: the chunk's first key
+      const int i = (rt0 + c) * TT;                    // column sums: the tile's first token
+      const int cols = kStats ? kTile : min(TT, n - i) * G;
+      if (live && 64 * half < cols) {
         uint32_t x[2][32];
-        const uint32_t at = lanes + s * kTile;
-        const int c0 = k0 + c * kTile;                 // row statistics: the chunk's first key
-        const int i = (rt0 + c) * TT;                  // column sums: the tile's first token
-        const int cols = kStats ? kTile : min(TT, n - i) * G;
-        const bool whole = kStats ? c0 + kTile - 1 <= first_pos
-                                  : cols == kTile && L - n + i >= k0 + kTile - 1;
-        tmem_ld32(at, x[0]);
+        tmem_ld32(lanes + s * kTile, x[0]);
+        tmem_ld32(lanes + s * kTile + 32, x[1]);
         tmem_wait_ld32(x[0]);
+        tmem_wait_ld32(x[1]);
+        if constexpr (kStats) {
+          const bool whole = c0 + 64 * half + 63 <= first_pos;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          __syncwarp();                                // (the TMEM loads are the whole warp's)
-          if (h < 3 && 32 * (h + 1) < cols) tmem_ld32(at + 32 * (h + 1), x[(h + 1) & 1]);
-          if constexpr (kStats) {
-            if (whole) add_scores<false>(st, x[h & 1], sl2, 0);
-            else add_scores<true>(st, x[h & 1], sl2, pos - c0 - 32 * h);
-          } else {
-            if (whole) acc += column_part<false>(x[h & 1], sl2, row_m[s] + 32 * h, row_pos[s] + 32 * h, key);
-            else if (32 * h < cols) acc += column_part<true>(x[h & 1], sl2, row_m[s] + 32 * h, row_pos[s] + 32 * h, key);
+          for (int h = 0; h < 2; ++h) {
+            if (whole) add_scores<false>(st, x[h], sl2, 0);
+            else add_scores<true>(st, x[h], sl2, pos - c0 - 64 * half - 32 * h);
           }
-          __syncwarp();
-          if (h < 3 && 32 * (h + 1) < cols) tmem_wait_ld32(x[(h + 1) & 1]);
+        } else {
+          const int pos0 = L - n + i;                  // of the tile's first token
+          const bool whole = cols == kTile && pos0 >= k0 + kTile - 1;
+          const int from = max(0, key - pos0) * G - 64 * half, to = cols - 64 * half;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float* m = row_m[s] + 64 * half + 32 * h;
+            acc += whole ? column_part<false>(x[h], sl2, m, 0, 32)
+                         : column_part<true>(x[h], sl2, m, from - 32 * h, to - 32 * h);
+          }
         }
       }
       tc_fence_before();
@@ -347,6 +410,10 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
       if (lane == 0) mbar_arrive(smem_addr(&buf_free[s]));
     }
     if (!ok && lane == 0) sh_fail = 1;
+    if (half == 1) {
+      half_part[row] = kStats ? st.l : acc;
+      half_ref[row] = st.ref;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -358,14 +425,38 @@ __global__ void __launch_bounds__(kStats ? 192 : 320, 2)
   if constexpr (kStats) {
     if (tid == 0 && sh_bad) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
     if (tid < my_rows) {
-      float* o = a.stats + (row_at(i0, tid) * a.splits + split) * 2;
-      o[0] = st.ref;
-      o[1] = failed || sh_bad ? -1.0f : st.l;          // l < 0: the weights stay as they are
+      const float r1 = half_ref[tid], M = fmaxf(st.ref, r1);
+      float l = 0.0f;
+      if (st.ref > -INFINITY || st.l != st.l) l = st.l * ex2(st.ref - M);
+      if (r1 > -INFINITY || half_part[tid] != half_part[tid]) l = fmaf(half_part[tid], ex2(r1 - M), l);
+      const bool lost = failed || sh_bad;
+      float* o = stats_at(i0) + ((int64_t)tid * a.splits + split) * 2;
+      // one split: m' at once (-inf: no statistics, the weights stay as they
+      // are; a row whose every score is -inf has NaN weights)
+      o[0] = a.splits > 1 ? M : (lost ? -INFINITY : row_log_sum(M, l));
+      o[1] = lost ? -1.0f : l;
     }
   } else if (!failed && !sh_bad && tid < kend - k0) {
+    acc += half_part[tid];
     float* w = a.weights + ((int64_t)b * a.num_kv_heads + hk) * a.stride + k0 + tid;
     *w = a.accumulate && k0 + tid < L - n ? *w + acc : acc;
   }
+}
+
+// Row statistics of several key splits: m' of a row into its first entry.
+__global__ void __launch_bounds__(256) join_stats_kernel(float* stats, int64_t rows, int splits) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (r >= rows) return;
+  float* ml = stats + r * splits * 2;
+  float M = -INFINITY, l = 0.0f;
+  bool lost = false;
+  for (int i = 0; i < splits; ++i) M = fmaxf(M, ml[2 * i]);
+  for (int i = 0; i < splits; ++i) {
+    const float m = ml[2 * i], x = ml[2 * i + 1];
+    lost |= x < 0.0f;
+    if (m > -INFINITY || x != x) l = fmaf(x, ex2(m - M), l);
+  }
+  ml[0] = lost ? -INFINITY : row_log_sum(M, l);
 }
 
 template <int D, int BS, bool kStats>
@@ -387,14 +478,21 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
     }
   }
   const dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
-  prompt_tc_kernel<D, BS, kStats><<<grid, kStats ? 192 : 320, PGeo<D>::kSmemBytes, s>>>(km, qm, a);
+  prompt_tc_kernel<D, BS, kStats><<<grid, kStats ? kStatsThreads : kSumsThreads, PGeo<D>::kSmemBytes, s>>>(km, qm, a);
   return cuda_check(cudaGetLastError(), "prompt_tc_kernel launch");
 }
 
 template <int D, int BS>
 kv_status launch_tc(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles, cudaStream_t s) {
-  const kv_status st = launch_tc_t<D, BS, true>(a, km, qm, (unsigned)(tiles * a.splits), s);
+  kv_status st = launch_tc_t<D, BS, true>(a, km, qm, (unsigned)(tiles * a.splits), s);
   if (st != KV_OK) return st;
+  if (a.splits > 1) {
+    const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
+    if ((rows + 255) / 256 > 0x7fffffffLL)
+      return fail(KV_ERR_INVALID_ARG, "pagedkv_attention_weights: too many query tokens");
+    join_stats_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.stats, rows, a.splits);
+    if ((st = cuda_check(cudaGetLastError(), "join_stats_kernel launch")) != KV_OK) return st;
+  }
   return launch_tc_t<D, BS, false>(a, km, qm, (unsigned)((a.max_seq_len - 1) / kTile + 1), s);
 }
 
