@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
     const bool append = a.new_k != nullptr && t1 == L;
     int issued = 0;
     bool ok = true;
+    uint64_t once = 0;
+    if constexpr (kScores) once = evict_first_policy();
     for (int it = 0; it < n_iter; ++it) {
       const int s = it % S;
       if (it >= S && !mbar_wait(smem_addr(&empty_bar[s]), ((it / S) - 1) & 1)) {
@@ -333,8 +335,14 @@ __global__ void __launch_bounds__(kThreads, (kQ8 || kMulti) ? PAGEDKV_Q8_MIN_BLO
           const uint32_t vdst = kdst + G::kTensorBytes;
 #pragma unroll
           for (int x = 0; x < G::kBoxes; ++x) {
-            tma_load_4d(kdst + x * G::kBoxBytes, &k_map, fb, x * G::kBoxElems, hk, 0, p);
-            tma_load_4d(vdst + x * G::kBoxBytes, &v_map, fb, x * G::kBoxElems, hk, 0, p);
+            if constexpr (kScores) {
+              // the scores written meanwhile are read again; K and V are not
+              tma_load_4d_hint(kdst + x * G::kBoxBytes, &k_map, fb, x * G::kBoxElems, hk, 0, p, once);
+              tma_load_4d_hint(vdst + x * G::kBoxBytes, &v_map, fb, x * G::kBoxElems, hk, 0, p, once);
+            } else {
+              tma_load_4d(kdst + x * G::kBoxBytes, &k_map, fb, x * G::kBoxElems, hk, 0, p);
+              tma_load_4d(vdst + x * G::kBoxBytes, &v_map, fb, x * G::kBoxElems, hk, 0, p);
+            }
           }
         }
       }

@@ -80,17 +80,31 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
   }
   __syncthreads();
   if (row_bad) return;                                 // a bad block: the weights stay
+  // four consecutive tokens per thread: every row's scores in one 16-byte load
+  // each, all under way before the first is used
   float* w = a.weights + ((int64_t)b * a.num_kv_heads + hk) * a.stride;
   const float* sc = a.scores + row0 * a.score_stride;
+  const int t = t0 + 4 * threadIdx.x;
+  if (t >= L) return;
+  float4 s[kMaxGroup];
 #pragma unroll
-  for (int u = 0; u < kStepTokens / kStepThreads; ++u) {
-    const int t = t0 + u * kStepThreads + threadIdx.x;
-    if (t >= L) break;
-    float sum = t < L - 1 ? w[t] : 0.0f;
-    for (int g = 0; g < GQ; ++g)
-      sum = fmaf(ex2(sc[g * a.score_stride + t] - row_m[g]), row_inv[g], sum);
-    w[t] = sum;
+  for (int g = 0; g < kMaxGroup; ++g)
+    if (g < GQ) s[g] = __ldcs(reinterpret_cast<const float4*>(sc + g * a.score_stride + t));
+  float sum[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[k] = t + k < L - 1 ? w[t + k] : 0.0f;
+#pragma unroll
+  for (int g = 0; g < kMaxGroup; ++g) {
+    if (g >= GQ) break;
+    const float m = row_m[g], inv = row_inv[g];
+    sum[0] = fmaf(ex2(s[g].x - m), inv, sum[0]);
+    sum[1] = fmaf(ex2(s[g].y - m), inv, sum[1]);
+    sum[2] = fmaf(ex2(s[g].z - m), inv, sum[2]);
+    sum[3] = fmaf(ex2(s[g].w - m), inv, sum[3]);
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t + k < L) w[t + k] = sum[k];
 }
 
 // ---------------------------------------------------------------------------
@@ -507,7 +521,7 @@ kv_status paged_attention_decode_weights(void* out, float* weights, int weights_
   const size_t rows = (size_t)batch * num_q_heads;
   a.ws_ml = static_cast<float*>(workspace);
   a.ws_acc = a.ws_ml + ml_region_floats(rows, a.slots);
-  a.ws_scores = a.ws_acc + (a.slots > 1 ? rows * a.slots * head_dim : 0);
+  a.ws_scores = a.ws_acc + (a.slots > 1 ? rows * a.slots * head_dim : 0);  // (16-byte aligned rows)
   a.score_stride = score_row(max_seq_len);
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = launch_decode(a, s)) != KV_OK || (st = launch_merge(a, s)) != KV_OK) return st;
