@@ -585,10 +585,10 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
     return fail(KV_ERR_INVALID_ARG, "%s: 8-bit pools need k_scale; bf16 pools take NULL", who);
   const int64_t G = num_q_heads / num_kv_heads;
   const int longest = max_query_len < num_tokens ? max_query_len : num_tokens;
-  // Many rows per KV head on a bf16 pool: the tcgen05 kernels, whose row tile
+  // Many rows per KV head: the tcgen05 kernels, whose row tile
   // is 128 rows of whole tokens; else the mma.sync kernels above.  (Their
   // score scale is positive.)
-  const bool tc = dtype == KV_DTYPE_BF16 && scale > 0.0f && G <= 128 && longest * G > kRowTile;
+  const bool tc = scale > 0.0f && G <= 128 && longest * G > kRowTile;
   const int64_t tile_tokens = tc ? 128 / G : 0;
   const int64_t tiles = tc ? (longest + tile_tokens - 1) / tile_tokens
                            : (longest * G + kRowTile - 1) / kRowTile;
@@ -630,7 +630,7 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
   a.stats = static_cast<float*>(workspace);
   a.tile_tokens = (int)tile_tokens;
   cudaStream_t s = (cudaStream_t)stream;
-  if (tc) return launch_prompt_tc(a, head_dim, block_size, (int)tiles, s);
+  if (tc) return launch_prompt_tc(a, head_dim, block_size, dtype, (int)tiles, s);
   if (head_dim == 128)
     return block_size == 32 ? launch_prompt_mma<128, 32>(a, dtype, (int)tiles, s)
                             : launch_prompt_mma<128, 16>(a, dtype, (int)tiles, s);

@@ -37,9 +37,9 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, int b, int bs, 
 
 
 // Row statistics and column sums on the tensor cores with TMEM accumulators;
-// `tiles` row tiles of a.tile_tokens tokens at most per sequence (bf16 pools,
-// positive scale).
-kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, int tiles,
-                           cudaStream_t stream);
+// `tiles` row tiles of a.tile_tokens tokens at most per sequence (positive
+// scale).
+kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, kv_dtype dtype,
+                           int tiles, cudaStream_t stream);
 
 }  // namespace pagedkv

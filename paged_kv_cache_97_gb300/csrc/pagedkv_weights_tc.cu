@@ -22,7 +22,11 @@
 // has 16384 exponentials against 256 cycles of MMA, so each costs one packed
 // half of a multiply-add and of an add beside it (f32x2), and no maximum: a
 // row's reference is its first scores' and moves only when a sum grows past
-// 2^60.  Two CTAs per SM (256 TMEM columns and about 100 KB of shared memory
+// 2^60.  8-bit pools: the row warps load the codes themselves, widen them to
+// bf16 (exact: 8 significant bits hold every int8 and E4M3 code) and write
+// them into the swizzled image, the streamed keys two chunks ahead, right
+// after the scores of the chunk that used the stage before; a block's K scale
+// multiplies its scores.  Two CTAs per SM (256 TMEM columns and about 100 KB of shared memory
 // each), so that one's start and end overlap the other's work.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -32,6 +36,7 @@
 
 #include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
+#include "pagedkv_requant.cuh"
 #include "pagedkv_tc.cuh"
 #include "pagedkv_weights.cuh"
 
@@ -98,6 +103,20 @@ __device__ __forceinline__ float sum_f32x2(uint64_t a, uint64_t b) {
   float lo, hi;
   unpack_f32x2(add_f32x2(a, b), lo, hi);
   return lo + hi;
+}
+
+// raw *= f (the first 16 by f0, the others by f1).
+__device__ __forceinline__ void scale_scores(uint32_t (&raw)[32], float f0, float f1) {
+  const uint64_t f[2] = {both(f0), both(f1)};
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    float lo, hi;
+    uint64_t v = pack_f32x2(raw[j], raw[j + 1]);
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(f[j >> 4]));
+    unpack_f32x2(v, lo, hi);
+    raw[j] = __float_as_uint(lo);
+    raw[j + 1] = __float_as_uint(hi);
+  }
 }
 
 // sum over 32 scores of 2^(s sl2 + off).
@@ -178,11 +197,66 @@ __device__ __forceinline__ float row_log_sum(float m, float l) {
   return m == -INFINITY ? __uint_as_float(0x7fc00000u) : m + log2f(l);
 }
 
-template <int D, int BS, bool kStats>
+// 8-bit pools: this thread's codes of the 128 keys from `from` (zeros from L
+// on), and the codes widened into a swizzled bf16 image.  256 threads; thread
+// piece u holds 16 codes of key (u * 256 + tid) / (D / 16).
+template <int D, int BS, int kKind>
+struct Codes {
+  static constexpr int kRowPieces = D / 16;
+  static constexpr int kPieces = kTile * kRowPieces / (kRowWarps * 32);
+  uint4 x[kPieces];
+
+  // False when a key's block is outside the pool.
+  __device__ __forceinline__ bool load(const PromptArgs& a, const int32_t* bt, int hk, int from, int L) {
+    bool ok = true;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = u * kRowWarps * 32 + (int)threadIdx.x, key = from + i / kRowPieces;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (key >= L) continue;
+      const int p = bt[key / BS];
+      if (p < 0 || p >= a.num_blocks) {
+        ok = false;
+        continue;
+      }
+      x[u] = static_cast<const uint4*>(a.k_cache)[(((int64_t)p * BS + key % BS) * a.num_kv_heads + hk) * kRowPieces +
+                                                  i % kRowPieces];
+    }
+    return ok;
+  }
+
+  __device__ __forceinline__ void store(unsigned char* img) const {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = u * kRowWarps * 32 + (int)threadIdx.x, r = i / kRowPieces;
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[4];
+        code_values<kKind == KV_DTYPE_FP8_E4M3>(w[k], v);
+        o[2 * k] = pack2<false>(v[0], v[1]);
+        o[2 * k + 1] = pack2<false>(v[2], v[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = 2 * (i % kRowPieces) + k;          // 8-element chunk of the row
+        *reinterpret_cast<uint4*>(img + (c / 8) * (kTile * 128) + sw128(r, c % 8)) =
+            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+};
+
+template <int D, int BS, int kKind, bool kStats>
 __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap q_map, const PromptArgs a) {
   using P = PGeo<D>;
+  constexpr bool kQ8 = kKind != KV_DTYPE_BF16;
+  constexpr bool kWidenStream = kQ8 && kStats, kWidenFixed = kQ8 && !kStats;
+  constexpr int kScaleSlots = 4;                       // chunks whose scales may be in use
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t fixed_full, full[kStages], empty[kStages], s_full[kStages], buf_free[kStages],
       stat_full[kStages], drain_bar;
@@ -190,6 +264,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   __shared__ int sh_bad, sh_fail;
   __shared__ __align__(16) float row_m[kStages][kTile];  // -m' of the row tile's rows
   __shared__ float half_part[kTile], half_ref[kTile];  // the upper columns' results
+  __shared__ float blk_ks[kWidenStream ? kScaleSlots : 1][kTile / BS];  // K scales of the chunks' blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x, b = blockIdx.y;
   const int G = a.num_q_heads / a.num_kv_heads, TT = a.tile_tokens;
@@ -227,13 +302,14 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   }
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - smem_addr(smem_raw));
   auto stage_img = [&](int s) { return base + (uint32_t)((1 + s) * P::kImage); };
   if (tid == 0) {
     sh_bad = 0;
     sh_fail = 0;
-    mbar_init(smem_addr(&fixed_full), 1);
+    mbar_init(smem_addr(&fixed_full), kWidenFixed ? kRowWarps : 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&full[s]), kWidenStream ? kRowWarps : 1);
       mbar_init(smem_addr(&empty[s]), 1);
       mbar_init(smem_addr(&s_full[s]), 1);
       mbar_init(smem_addr(&buf_free[s]), kRowWarps);
@@ -287,10 +363,10 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       __syncwarp();
     };
     if (kStats) load_q(base, &fixed_full, i0);
-    else load_k(base, &fixed_full, k0);
+    else if (!kQ8) load_k(base, &fixed_full, k0);
     int issued = 0;
     bool ok = true;
-    for (int c = 0; c < nch; ++c) {
+    for (int c = 0; c < (kWidenStream ? 0 : nch); ++c) {
       const int s = c % kStages;
       if (c >= kStages && !warp_wait(smem_addr(&empty[s]), ((c / kStages) - 1) & 1)) {
         ok = false;
@@ -301,7 +377,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       issued = c + 1;
     }
     // every load has landed before the CTA ends (bounded; normally it has)
-    if (!warp_wait(smem_addr(&fixed_full), 0)) ok = false;
+    if (!kWidenFixed && !warp_wait(smem_addr(&fixed_full), 0)) ok = false;
     for (int s = 0; s < kStages && s < issued; ++s) {
       const int last = s + kStages * ((issued - 1 - s) / kStages);
       if (!warp_wait(smem_addr(&full[s]), (last / kStages) & 1)) ok = false;
@@ -367,12 +443,45 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     // a warp whose rows are all padding only keeps the barriers' phases
     const int row_lo = (warp & 3) * 32;
     const bool live = kStats ? row_lo < my_rows : k0 + row_lo < kend;
-    const float sl2 = a.scale_log2;
+    float sl2 = a.scale_log2;
     const uint32_t lanes = tm + ((uint32_t)row_lo << 16) + 64 * half;
+    [[maybe_unused]] Codes<D, BS, kQ8 ? kKind : KV_DTYPE_INT8> codes;
+    // K scales of the blocks of the chunk whose codes this thread widens
+    auto put_scales = [&](int c) {
+      const int j = tid, from = k0 + c * kTile + j * BS;
+      if (j < kTile / BS) {
+        const int p = from < L ? bt[from / BS] : -1;
+        blk_ks[c & (kScaleSlots - 1)][j] =
+            p >= 0 && p < a.num_blocks ? a.k_scale[(int64_t)p * a.num_kv_heads + hk] : 0.0f;
+      }
+    };
+    if constexpr (kWidenFixed) {
+      if (!codes.load(a, bt, hk, k0, L)) sh_bad = 1;
+      codes.store(gbase);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&fixed_full));
+      if (key < kend) {
+        const int p = bt[key / BS];
+        if (p >= 0 && p < a.num_blocks) sl2 *= a.k_scale[(int64_t)p * a.num_kv_heads + hk];
+      }
+    }
+    if constexpr (kWidenStream) {
+      for (int c = 0; c < kStages && c < nch; ++c) {
+        if (!codes.load(a, bt, hk, k0 + c * kTile, L)) sh_bad = 1;
+        put_scales(c);
+        codes.store(gbase + (1 + c) * P::kImage);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&full[c]));
+      }
+    }
     for (int c = 0; c < nch; ++c) {
+      if constexpr (kWidenStream) {
+        if (c + kStages < nch && !codes.load(a, bt, hk, k0 + (c + kStages) * kTile, L)) sh_bad = 1;
+      }
       const int s = c % kStages, ph = (c / kStages) & 1;
       if (!warp_wait(smem_addr(&s_full[s]), ph) ||
-          (!kStats && !warp_wait(smem_addr(&stat_full[s]), ph))) {
+          (!kStats && !warp_wait(smem_addr(&stat_full[s]), ph)) ||
+          (kWidenStream && !warp_wait(smem_addr(&full[s]), ph))) {  // (the other warps' scales)
         ok = false;
         break;
       }
@@ -383,13 +492,23 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       if (live && 64 * half < cols) {
         uint32_t x[2][32];
         tmem_ld32(lanes + s * kTile, x[0]);
-        tmem_ld32(lanes + s * kTile + 32, x[1]);
+        if (!kWidenStream) tmem_ld32(lanes + s * kTile + 32, x[1]);
         tmem_wait_ld32(x[0]);
-        tmem_wait_ld32(x[1]);
+        if (!kWidenStream) tmem_wait_ld32(x[1]);
         if constexpr (kStats) {
           const bool whole = c0 + 64 * half + 63 <= first_pos;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            if constexpr (kWidenStream) {
+              if (h == 1) {
+                __syncwarp();
+                tmem_ld32(lanes + s * kTile + 32, x[1]);
+                tmem_wait_ld32(x[1]);
+              }
+              const float* ks = blk_ks[c & (kScaleSlots - 1)];
+              const int at = 64 * half + 32 * h;
+              scale_scores(x[h], ks[at / BS], ks[(at + 16) / BS]);
+            }
             if (whole) add_scores<false>(st, x[h], sl2, 0);
             else add_scores<true>(st, x[h], sl2, pos - c0 - 64 * half - 32 * h);
           }
@@ -408,6 +527,15 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&buf_free[s]));
+      if constexpr (kWidenStream) {
+        // the scores of chunk c are complete, so its stage is free
+        if (c + kStages < nch) {
+          put_scales(c + kStages);
+          codes.store(gbase + (1 + s) * P::kImage);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&full[s]));
+        }
+      }
     }
     if (!ok && lane == 0) sh_fail = 1;
     if (half == 1) {
@@ -459,7 +587,7 @@ __global__ void __launch_bounds__(256) join_stats_kernel(float* stats, int64_t r
   ml[0] = lost ? -INFINITY : row_log_sum(M, l);
 }
 
-template <int D, int BS, bool kStats>
+template <int D, int BS, int kKind, bool kStats>
 kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, unsigned z,
                       cudaStream_t s) {
   static std::mutex mu;
@@ -470,7 +598,7 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(prompt_tc_kernel<D, BS, kStats>,
+      st = cuda_check(cudaFuncSetAttribute(prompt_tc_kernel<D, BS, kKind, kStats>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, PGeo<D>::kSmemBytes),
                       "cudaFuncSetAttribute(prompt_tc_kernel)");
       if (st != KV_OK) return st;
@@ -478,13 +606,13 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
     }
   }
   const dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
-  prompt_tc_kernel<D, BS, kStats><<<grid, kStats ? kStatsThreads : kSumsThreads, PGeo<D>::kSmemBytes, s>>>(km, qm, a);
+  prompt_tc_kernel<D, BS, kKind, kStats><<<grid, kStats ? kStatsThreads : kSumsThreads, PGeo<D>::kSmemBytes, s>>>(km, qm, a);
   return cuda_check(cudaGetLastError(), "prompt_tc_kernel launch");
 }
 
-template <int D, int BS>
-kv_status launch_tc(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles, cudaStream_t s) {
-  kv_status st = launch_tc_t<D, BS, true>(a, km, qm, (unsigned)(tiles * a.splits), s);
+template <int D, int BS, int kKind>
+kv_status launch_tc_kind(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles, cudaStream_t s) {
+  kv_status st = launch_tc_t<D, BS, kKind, true>(a, km, qm, (unsigned)(tiles * a.splits), s);
   if (st != KV_OK) return st;
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
@@ -493,12 +621,21 @@ kv_status launch_tc(const PromptArgs& a, const CUtensorMap& km, const CUtensorMa
     join_stats_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.stats, rows, a.splits);
     if ((st = cuda_check(cudaGetLastError(), "join_stats_kernel launch")) != KV_OK) return st;
   }
-  return launch_tc_t<D, BS, false>(a, km, qm, (unsigned)((a.max_seq_len - 1) / kTile + 1), s);
+  return launch_tc_t<D, BS, kKind, false>(a, km, qm, (unsigned)((a.max_seq_len - 1) / kTile + 1), s);
+}
+
+template <int D, int BS>
+kv_status launch_tc(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, kv_dtype dtype, int tiles,
+                    cudaStream_t s) {
+  if (dtype == KV_DTYPE_INT8) return launch_tc_kind<D, BS, KV_DTYPE_INT8>(a, km, qm, tiles, s);
+  if (dtype == KV_DTYPE_FP8_E4M3) return launch_tc_kind<D, BS, KV_DTYPE_FP8_E4M3>(a, km, qm, tiles, s);
+  return launch_tc_kind<D, BS, KV_DTYPE_BF16>(a, km, qm, tiles, s);
 }
 
 }  // namespace
 
-kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, int tiles, cudaStream_t s) {
+kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, kv_dtype dtype, int tiles,
+                           cudaStream_t s) {
   DecodeArgs d = {};
   d.k_cache = a.k_cache;
   d.v_cache = a.k_cache;                               // (the V map is not used)
@@ -506,7 +643,7 @@ kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, in
   d.num_blocks = a.num_blocks;
   d.head_dim = head_dim;
   d.block_size = block_size;
-  d.dtype = KV_DTYPE_BF16;
+  d.dtype = dtype;
   alignas(64) CUtensorMap km, vm, qm;
   kv_status st = make_kv_maps(d, &km, &vm);
   if (st == KV_OK)
@@ -514,8 +651,10 @@ kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, in
                         a.tile_tokens);
   if (st != KV_OK) return st;
   if (head_dim == 128)
-    return block_size == 32 ? launch_tc<128, 32>(a, km, qm, tiles, s) : launch_tc<128, 16>(a, km, qm, tiles, s);
-  return block_size == 32 ? launch_tc<64, 32>(a, km, qm, tiles, s) : launch_tc<64, 16>(a, km, qm, tiles, s);
+    return block_size == 32 ? launch_tc<128, 32>(a, km, qm, dtype, tiles, s)
+                            : launch_tc<128, 16>(a, km, qm, dtype, tiles, s);
+  return block_size == 32 ? launch_tc<64, 32>(a, km, qm, dtype, tiles, s)
+                            : launch_tc<64, 16>(a, km, qm, dtype, tiles, s);
 }
 
 }  // namespace pagedkv

@@ -7,7 +7,7 @@ import math
 import torch
 
 CODE_MAX = {"int8": 127.0, "fp8": 448.0}
-DTYPES = {"bf16": torch.bfloat16, "int8": torch.int8, "fp8": torch.float8_e4m3fn}
+FLUSHED = 2.0 ** -126                   # a weight below this may be stored as 0
 
 
 def f64(x):
@@ -140,7 +140,7 @@ def decode_weights(pool, q, weights, scale):
             tol[b, h * G:(h + 1) * G] = 2.0 ** -8 * o.abs() + (2.0 ** -8 + rel) * 1.01 * (p @ V.abs())
             w[b, h, L - 1] = 0
             w[b, h, :L] += p.sum(dim=0)
-            wtol[b, h, :L] = (p * rel).sum(dim=0) + 2.0 ** -22 * w[b, h, :L].abs()
+            wtol[b, h, :L] = (p * rel).sum(dim=0) + 2.0 ** -22 * w[b, h, :L].abs() + G * FLUSHED
     return out, tol, w, wtol
 
 
@@ -163,8 +163,9 @@ def prompt_weights(pool, q, counts, weights, scale, accumulate=True):
                 off[:end] += (p * rel).sum(dim=0)
             w[b, h, (L - n if accumulate else 0):L] = 0
             w[b, h, :L] += acc
-            # sums of n G weights in fp32
-            wtol[b, h, :L] = off + (n * G * 2.0 ** -24 + 2.0 ** -22) * w[b, h, :L].abs()
+            # sums of n G weights in fp32, each flushed to 0 below fp32's
+            # smallest normal number, 2^-126
+            wtol[b, h, :L] = off + (n * G * 2.0 ** -24 + 2.0 ** -22) * w[b, h, :L].abs() + n * G * FLUSHED
         at += n
     return w, wtol
 

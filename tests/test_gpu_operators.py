@@ -230,6 +230,38 @@ def test_prompt_weights_long(pkv, dtype, L, counts, accumulate):
         assert same_bits(w[b, :, n:], weights[b, :, n:])
 
 
+@pytest.mark.parametrize("dtype,block,dim", POOLS)
+@pytest.mark.parametrize("group,n,L", [(3, 130, [130, 300]), (7, 40, [290, 41]), (1, 200, [456, 200]),
+                                       (4, 96, [700, 97]), (16, 9, [140, 10])])
+def test_prompt_weights_row_tiles(pkv, dtype, block, dim, group, n, L):
+    """Several 128-row tiles, heads that do not divide them, keys split over
+    CTAs, chunks that end inside a tile; a sequence of one query beside them."""
+    pool = ref.Pool(L + [50], 1, dim, block, dtype, seed=group)
+    counts = [n, n, 1]
+    q = pool.randn(sum(counts), group, dim, scale=2.0)
+    weights = torch.rand((3, 1, max(L) + 5), generator=pool.g) * group * n / 300
+    w = prompt_weights(pkv, pool, q, counts, weights, dim ** -0.5)
+    want, tol = ref.prompt_weights(pool, q, counts, weights, dim ** -0.5)
+    within(w, want, tol)
+    for b, m in enumerate(pool.L):
+        assert same_bits(w[b, :, m:], weights[b, :, m:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("scale", [0.125, 3.0, -0.125])
+def test_prompt_weights_steep_scores(pkv, dtype, scale):
+    """Scores whose exponentials pass fp32's range many times over against the
+    first keys' (the running reference has to move), and a negative scale."""
+    pool = ref.Pool([260], 1, 64, 16, dtype, seed=11)
+    q = pool.randn(100, 2, 64, scale=2.0)
+    for j in range(16):                                       # the first keys are small
+        ref.raw(pool.k)[pool.tables[0, 0].item(), j] = 0
+    weights = torch.zeros((1, 1, 260))
+    w = prompt_weights(pkv, pool, q, [100], weights, scale)
+    want, tol = ref.prompt_weights(pool, q, [100], weights, scale)
+    within(w, want, tol)
+
+
 def test_prompt_weights_of_one_token_are_the_decode_step(pkv):
     L = [300, 41]
     pool = ref.Pool(L, 2, 128, 32, "bf16", seed=9)
