@@ -744,8 +744,8 @@ kv_status pagedkv_select_tokens(int32_t *keep_idx, int32_t *keep_len,
  *   dst_block_tables  device int32 [batch, dst_max_blocks]: may be
  *                 block_tables (packing in place).  Entry j of a row is either
  *                 entry j of the source row or a block that no source row of
- *                 the call lists, and no block is the destination of two
- *                 sequences (kv_pool_prepare_evict makes such tables)
+ *                 the call lists, and no block is a destination twice
+ *                 (kv_pool_prepare_evict makes such tables)
  *   keep_idx, keep_len, budget  as pagedkv_select_tokens gives them: each list
  *                 strictly ascending within [0, seq_lens[b])
  *   weights       device fp32 [batch, num_kv_heads, weights_stride] or NULL

@@ -630,6 +630,15 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
   a.stats = static_cast<float*>(workspace);
   a.tile_tokens = (int)tile_tokens;
   cudaStream_t s = (cudaStream_t)stream;
+  // Few rows on a bf16 pool whose scores fit a cluster's TMEM: one pass over K
+  // (64 sequences of 512..4096 tokens, five queries each, 32/8 heads: two
+  // passes of the mma.sync kernels 189 us, one pass 103).
+  const int ctas = dtype == KV_DTYPE_BF16 && longest * G <= kFewRows
+                       ? few_rows_ctas(batch, num_kv_heads, max_seq_len, di.num_sms) : 0;
+  if (ctas > 0) {
+    a.tile_tokens = (int)(kFewRows / G);
+    return launch_prompt_few(a, head_dim, block_size, ctas, s);
+  }
   if (tc) return launch_prompt_tc(a, head_dim, block_size, dtype, (int)tiles, s);
   if (head_dim == 128)
     return block_size == 32 ? launch_prompt_mma<128, 32>(a, dtype, (int)tiles, s)

@@ -42,4 +42,13 @@ __device__ __forceinline__ bool prompt_rows(const PromptArgs& a, int b, int bs, 
 kv_status launch_prompt_tc(const PromptArgs& a, int head_dim, int block_size, kv_dtype dtype,
                            int tiles, cudaStream_t stream);
 
+// At most this many rows (query tokens x grouped heads) per KV head: one pass
+// over K with the scores kept in TMEM, on a cluster of `ctas` CTAs per
+// (sequence, KV head) (bf16 pools).  few_rows_ctas is 0 when sequences of
+// max_seq_len tokens do not fit the largest cluster.
+constexpr int kFewRows = 32;
+int few_rows_ctas(int batch, int num_kv_heads, int max_seq_len, int num_sms);
+kv_status launch_prompt_few(const PromptArgs& a, int head_dim, int block_size, int ctas,
+                            cudaStream_t stream);
+
 }  // namespace pagedkv
