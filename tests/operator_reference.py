@@ -7,6 +7,7 @@ import math
 import torch
 
 CODE_MAX = {"int8": 127.0, "fp8": 448.0}
+DTYPES = {"bf16": torch.bfloat16, "int8": torch.int8, "fp8": torch.float8_e4m3fn}
 FLUSHED = 2.0 ** -126                   # a weight below this may be stored as 0
 
 
