@@ -324,17 +324,20 @@ kv_status launch_select(const SelectArgs& a, int64_t rows, int C, int dev, cudaS
 // list ascends), so a CTA that packs destination blocks in ascending order
 // may work in place: the rows it stores lie before every row it still has to
 // load, and the loads of one round are all done before its stores.  One CTA
-// (or, in small batches, a cluster) per (KV head, sequence, K or V); one warp
-// per destination block and round, holding the whole block of one head in
-// registers.  For 8-bit pools the warp also finds the block's new scale from
-// the rows it holds.  Where no destination block is its own source, nothing is
+// (or, in small batches, a cluster) per (KV head, sequence) and one of K, V and
+// the weights; one warp per destination block and round, holding the whole
+// block of one head in registers.  For 8-bit pools the warp also finds the
+// block's new scale from the rows it holds.  Where no destination block is its own source, nothing is
 // stored where anything is read and the warps run on without the barrier.
 //
-// 8-bit pools are bound by instruction issue (the codes), bf16 by HBM: 128
-// sequences of 1..8K tokens packed to 2K, E4M3, 321 us to fresh blocks and 277
-// in place (49 and 57 % of the copy rate; four CTAs per SM, with the registers
-// held to 64, against three: 359 and 361); 64 sequences of 512..4096 packed to
-// 1K, bf16 in place, 84 us (91 %).
+// bf16 is bound by HBM, 8-bit pools by the arithmetic of the codes (about nine
+// issue slots per E4M3 code and eleven per int8 code, logic and permutes
+// counting double).  128 sequences of 1..8K tokens packed to 2K: E4M3 276 us to
+// fresh blocks, 284 in place (56 % of the copy rate), int8 372 and 302; four
+// CTAs per SM with the registers held to 64 against three: 276 and 305.  64
+// sequences of 512..4096 packed to 1K, bf16 in place: 85 us (90 %).  Tried and
+// dropped: the rows a round ahead by asynchronous copies (321 -> 349 us), the
+// lists and tables of several rounds staged in shared memory (352 -> 465).
 
 constexpr int kEvictWarps = 8;
 
@@ -352,8 +355,67 @@ struct EvictArgs {
   int max_blocks, dst_max_blocks, num_kv_heads, num_blocks, budget;
 };
 
+// One destination block's codes: rows [0, rows) of 16-byte pieces from the
+// byte offsets `from` (lane r: row r's) of `pool` to `to` + r * row_bytes,
+// coded again under the block's own scale, which is returned.  scale_r: lane
+// r's old scale.  `stored` is called between the loads and the stores.
+// kFull: rows == BS.
+template <int D, int BS, bool kFp8, bool kFull, class Barrier>
+__device__ __forceinline__ float recode_block(unsigned char* pool, int64_t from, int64_t to, int64_t row_bytes,
+                                              float scale_r, int rows, Barrier loaded) {
+  constexpr int kRow = D / 16;                       // 16-byte pieces per row
+  constexpr int kPer = BS * kRow / 32;               // pieces per lane
+  constexpr int kStep = 32 / kRow;                   // rows per step
+  const int lane = threadIdx.x & 31, sub = lane / kRow;
+  const unsigned char* src = pool + (lane % kRow) * 16;
+  uint4 x[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int64_t off = __shfl_sync(0xffffffffu, from, u * kStep + sub);
+    if (kFull || u * kStep + sub < rows) x[u] = *reinterpret_cast<const uint4*>(src + off);
+    else x[u] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // |c * s| in fp32 grows with |c|, so a piece's largest code decides unless
+  // its product is not finite
+  float amax = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const float s = __shfl_sync(0xffffffffu, scale_r, u * kStep + sub);
+    amax = fmaxf(amax, fabsf(__fmul_rn(largest_code<kFp8>(x[u]), s)));  // (passes over NaN)
+  }
+  if (__any_sync(0xffffffffu, amax > kLargestFinite)) {
+    amax = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      amax = fmaxf(amax, codes_amax_each<kFp8>(x[u], __shfl_sync(0xffffffffu, scale_r, u * kStep + sub)));
+  }
+  const float ns = block_scale<kFp8>(warp_max(amax));
+  // lane r: the interval of row r's quotients
+  const Interval q = quotients(scale_r, ns);
+  const bool on = __all_sync(0xffffffffu, q.on || lane >= rows);
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const float lo = __shfl_sync(0xffffffffu, q.lo, u * kStep + sub);
+    const float hi = __shfl_sync(0xffffffffu, q.hi, u * kStep + sub);
+    // (opaque here, or the values converted above would be kept for all pieces
+    // and spill)
+    asm volatile("" : "+r"(x[u].x), "+r"(x[u].y), "+r"(x[u].z), "+r"(x[u].w));
+    uint4 o, off;
+    const bool some = recode16_between<kFp8>(x[u], lo, hi, o, off);
+    if (__any_sync(0xffffffffu, some) || !on)
+      o = divide_words<kFp8>(x[u], o, off, __shfl_sync(0xffffffffu, scale_r, u * kStep + sub), ns, !on);
+    x[u] = o;
+  }
+  loaded();
+  unsigned char* dst = pool + to + sub * row_bytes + (lane % kRow) * 16;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    if (kFull || u * kStep + sub < rows) *reinterpret_cast<uint4*>(dst + u * kStep * row_bytes) = x[u];
+  return ns;
+}
+
 template <int D, int BS, int kKind>
-__global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 : 1)
+__global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 : 2)
     evict_kernel(const EvictArgs a) {
   constexpr bool kQ8 = kKind != KV_DTYPE_BF16, kFp8 = kKind == KV_DTYPE_FP8_E4M3;
   constexpr int kRow = D * (kQ8 ? 1 : 2) / 16;       // 16-byte pieces per row
@@ -379,6 +441,27 @@ __global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 :
     if (threadIdx.x == 0 && rank == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
     return;
   }
+  if (kv == 2) {
+    // the weights, always in place: entry keep_idx[j] to entry j
+    if (rank != 0) return;
+    constexpr int kBatchRows = 8;
+    float* w = a.weights + ((int64_t)b * Hkv + h) * a.weights_stride;
+    for (int j0 = 0; j0 < m; j0 += kBatchRows * kEvictWarps * 32) {
+      float x[kBatchRows];
+#pragma unroll
+      for (int u = 0; u < kBatchRows; ++u) {
+        const int j = j0 + u * kEvictWarps * 32 + (int)threadIdx.x;
+        if (j < m) x[u] = w[idx[j]];
+      }
+      __syncthreads();                               // the round's loads are done
+#pragma unroll
+      for (int u = 0; u < kBatchRows; ++u) {
+        const int j = j0 + u * kEvictWarps * 32 + (int)threadIdx.x;
+        if (j < m) w[j] = x[u];
+      }
+    }
+    return;
+  }
   const int32_t* bt = a.block_tables + (int64_t)b * a.max_blocks;
   const int32_t* dt = a.dst_tables + (int64_t)b * a.dst_max_blocks;
   const int nblk = (m + BS - 1) / BS;
@@ -386,74 +469,67 @@ __global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 :
   bool stays = false;
   for (int j = threadIdx.x; j < nblk; j += blockDim.x) stays |= dt[j] == bt[j];
   const bool in_place = __syncthreads_or(stays);
-  uint4* cache = static_cast<uint4*>(kv ? a.cache[1] : a.cache[0]);
+  unsigned char* pool = static_cast<unsigned char*>(kv ? a.cache[1] : a.cache[0]);
   float* scale = kv ? a.scale[1] : a.scale[0];
-  float* wrow = kv == 0 && a.weights ? a.weights + ((int64_t)b * Hkv + h) * a.weights_stride : nullptr;
+  const int64_t row_bytes = (int64_t)Hkv * kRow * 16;  // between rows of a block
+  auto loaded = [&]() {                              // the round's loads are done
+    if (in_place) {
+      if (C > 1) cluster.sync();
+      else __syncthreads();
+    }
+  };
   for (int j0 = 0; j0 < nblk; j0 += C * kEvictWarps) {
     const int j = j0 + rank * kEvictWarps + warp;    // this warp's destination block
     bool move = j < nblk;
     const int rows = move ? min(BS, m - j * BS) : 0;
-    int64_t slot = 0;                                // lane r: row r's source slot
+    int64_t from = 0, to = 0;                        // byte offsets; lane r: row r's source
     int dst = 0;
-    float s = 0.0f, wt = 0.0f;
+    float s = 0.0f;
     if (move) {
       dst = dt[j];
-      const int from = bt[j];
+      const int own = bt[j];
       const int t = lane < rows ? idx[j * BS + lane] : 0;
       const int sb = lane < rows ? bt[t / BS] : 0;
       const bool off = dst < 0 || dst >= a.num_blocks || sb < 0 || sb >= a.num_blocks;
-      const bool still = from == dst && (lane >= rows || t == j * BS + lane);
+      const bool still = own == dst && (lane >= rows || t == j * BS + lane);
       if (__any_sync(0xffffffffu, off)) {
         if (lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
         move = false;
       } else if (__all_sync(0xffffffffu, still)) {
         move = false;
       } else {
-        slot = (int64_t)sb * BS + t % BS;
+        from = (((int64_t)sb * BS + t % BS) * Hkv + h) * (kRow * 16);
+        to = ((int64_t)dst * BS * Hkv + h) * (kRow * 16);
         if (kQ8 && lane < rows) s = scale[(int64_t)sb * Hkv + h];
-        if (wrow && lane < rows) wt = wrow[t];
       }
     }
-    uint4 x[kPer];
-    if (move) {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int piece = u * 32 + lane, r = piece / kRow;
-        const int64_t sl = __shfl_sync(0xffffffffu, slot, r);
-        if (r < rows) x[u] = cache[(sl * Hkv + h) * kRow + piece % kRow];
-      }
-    }
-    float ns = 0.0f;
     if constexpr (kQ8) {
+      if (!move) {
+        loaded();
+      } else {
+        const float ns = rows == BS
+            ? recode_block<D, BS, kFp8, true>(pool, from, to, row_bytes, s, rows, loaded)
+            : recode_block<D, BS, kFp8, false>(pool, from, to, row_bytes, s, rows, loaded);
+        if (lane == 0) scale[(int64_t)dst * Hkv + h] = ns;
+      }
+    } else {
+      uint4 x[kPer];
+      constexpr int kStep = kRow < 32 ? 32 / kRow : 1;
+      const int sub = lane / kRow;
       if (move) {
-        float amax = 0.0f;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
-          const int r = (u * 32 + lane) / kRow;
-          const float sr = __shfl_sync(0xffffffffu, s, r);
-          if (r < rows) amax = fmaxf(amax, codes_amax<kFp8>(x[u], sr));
-        }
-        ns = block_scale<kFp8>(warp_max(amax));
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const int r = (u * 32 + lane) / kRow;
-          const float sr = __shfl_sync(0xffffffffu, s, r);
-          if (r < rows) x[u] = recode16<kFp8>(x[u], quotients(sr, ns), sr, ns);
+          const int64_t at = __shfl_sync(0xffffffffu, from, u * kStep + sub);
+          if (u * kStep + sub < rows) x[u] = *reinterpret_cast<const uint4*>(pool + at + (lane % kRow) * 16);
         }
       }
-    }
-    if (in_place) {                                  // the round's loads are done
-      if (C > 1) cluster.sync();
-      else __syncthreads();
-    }
-    if (move) {
+      loaded();
+      if (move) {
+        unsigned char* out = pool + to + sub * row_bytes + (lane % kRow) * 16;
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int piece = u * 32 + lane, r = piece / kRow;
-        if (r < rows) cache[(((int64_t)dst * BS + r) * Hkv + h) * kRow + piece % kRow] = x[u];
+        for (int u = 0; u < kPer; ++u)
+          if (u * kStep + sub < rows) *reinterpret_cast<uint4*>(out + u * kStep * row_bytes) = x[u];
       }
-      if (kQ8 && lane == 0) scale[(int64_t)dst * Hkv + h] = ns;
-      if (wrow && lane < rows) wrow[j * BS + lane] = wt;
     }
   }
 }
@@ -461,7 +537,7 @@ __global__ void __launch_bounds__(kEvictWarps * 32, kKind != KV_DTYPE_BF16 ? 4 :
 template <int D, int BS, int kKind>
 kv_status launch_evict_t(const EvictArgs& a, int batch, int C, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.num_kv_heads * C), (unsigned)batch, 2);
+  cfg.gridDim = dim3((unsigned)(a.num_kv_heads * C), (unsigned)batch, a.weights ? 3 : 2);
   cfg.blockDim = dim3(kEvictWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

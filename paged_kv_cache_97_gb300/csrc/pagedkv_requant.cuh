@@ -39,17 +39,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // The four code values of a 32-bit word, lowest byte first.  int8: each byte
 // is placed under the exponent of 2^23, c + 128 + 2^23, and 2^23 + 128 taken
 // off (exact; an integer conversion runs at an eighth of the add's rate).
@@ -74,29 +63,16 @@ __device__ __forceinline__ void code_values(uint32_t w, float (&v)[4]) {
 // Largest magnitude among 16 codes, as a code value (NaN codes passed over).
 template <bool kFp8>
 __device__ __forceinline__ float largest_code(uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  if constexpr (kFp8) {
-    __half2 m = __float2half2_rn(0.0f);
+  const uint32_t w[4] = {x.x ^ kCodeBias<kFp8>, x.y ^ kCodeBias<kFp8>, x.z ^ kCodeBias<kFp8>,
+                         x.w ^ kCodeBias<kFp8>};
+  __half2 m = __float2half2_rn(0.0f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = codes_to_f16x2<true>(w[i], 0x4140u), hi = codes_to_f16x2<true>(w[i], 0x4342u);
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&lo)));
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&hi)));
-    }
-    return fmaxf(__low2float(m), __high2float(m));
-  } else {
-    // even and odd bytes as the upper bytes of 16-bit lanes
-    uint32_t most = 0u, least = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t odd = w[i] & 0xff00ff00u, even = (w[i] << 8) & 0xff00ff00u;
-      most = max_s16x2(most, max_s16x2(odd, even));
-      least = min_s16x2(least, min_s16x2(odd, even));
-    }
-    const int hi = max((int)(int16_t)(most & 0xffffu), (int)(int16_t)(most >> 16)) >> 8;
-    const int lo = min((int)(int16_t)(least & 0xffffu), (int)(int16_t)(least >> 16)) >> 8;
-    return (float)max(hi, -lo);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = codes_to_f16x2<kFp8>(w[i], 0x4140u), hi = codes_to_f16x2<kFp8>(w[i], 0x4342u);
+    m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&lo)));
+    m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&hi)));
   }
+  return fmaxf(__low2float(m), __high2float(m));
 }
 
 // Largest finite |c * s| of 16 codes, one by one (an overflowing or NaN scale).
@@ -112,31 +88,22 @@ __device__ __noinline__ float codes_amax_each(uint4 x, float s) {
   return m;
 }
 
-// Largest finite |c * s| of 16 codes.  |c * s| in fp32 grows with |c|, so the
-// largest code decides unless its product is not finite.
-template <bool kFp8>
-__device__ __forceinline__ float codes_amax(uint4 x, float s) {
-  const float m = fabsf(__fmul_rn(largest_code<kFp8>(x), s));
-  return m <= kLargestFinite ? m : codes_amax_each<kFp8>(x, s);
-}
-
 // Codes without a division per element.  The code of the fp32 quotient q =
 // x / s is wanted; q lies within a relative 2^-22 of x * r for the rounded
 // r = 1 / s (or, for x = c * t under an old scale t, of c * (t r)), so between
 // x * lo and x * hi with lo, hi = r (1 -+ 2^-21).  The code grows with the
 // value: where both ends have the same code it is q's, and only the words
-// where they differ (a border between two codes lies in between: about one
-// element in 2^16) are divided.  An IEEE division takes some 12 instructions
-// of the 22 per element these kernels had; they were bound by instruction
-// issue, at 21 % of the memory rate.  s == 0 reads as 1; factors outside
-// [2^-100, 2^100], whose products could lose bits, always divide.
+// where they differ (a border between two codes lies in between) are divided.
+// An IEEE division per element bound these kernels at 21 % of the memory rate.
+// s == 0 reads as 1; factors outside [2^-80, 2^80], whose products or
+// remainders could lose bits, always divide.
 struct Interval {
   float lo, hi;
   bool on;
   float s, r;                                        // the scale (0 as 1), its reciprocal
 };
 
-__device__ __forceinline__ bool plain_size(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+__device__ __forceinline__ bool plain_size(float s) { return s >= 0x1p-80f && s <= 0x1p80f; }
 
 __device__ __forceinline__ Interval interval(float factor, bool on, float s, float r) {
   return {factor * (1.0f - 0x1p-21f), factor * (1.0f + 0x1p-21f), on, s, r};
@@ -174,54 +141,84 @@ __device__ __forceinline__ uint32_t code4_times(const float (&x)[4], float f) {
   }
 }
 
-// Four values of a source: the bf16 pairs of two words, or (kCodes) the codes
-// of one.
-template <bool kFp8, bool kCodes>
-__device__ __forceinline__ void four_values(const uint32_t* w, float (&v)[4]) {
-  if constexpr (kCodes) {
-    code_values<kFp8>(w[0], v);
-  } else {
-    v[0] = __uint_as_float(w[0] << 16);
-    v[1] = __uint_as_float(w[0] & 0xffff0000u);
-    v[2] = __uint_as_float(w[1] << 16);
-    v[3] = __uint_as_float(w[1] & 0xffff0000u);
-  }
+// The bf16 values of two words.
+__device__ __forceinline__ void bf16_values(uint32_t w0, uint32_t w1, float (&v)[4]) {
+  v[0] = __uint_as_float(w0 << 16);
+  v[1] = __uint_as_float(w0 & 0xffff0000u);
+  v[2] = __uint_as_float(w1 << 16);
+  v[3] = __uint_as_float(w1 & 0xffff0000u);
 }
 
-// 16 codes by division (out of line: rare, and its code, repeated in every
-// unrolled piece, would not fit the instruction cache).
-template <bool kFp8, bool kCodes>
-__device__ __noinline__ uint4 code16_divided(uint4 a, uint4 b, float t, float s) {
+// The codes of four values by division.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t code4_divided(const float (&x)[4], float s) {
+  uint32_t o = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o |= (uint32_t)code8<kFp8>(x[k], s) << (8 * k);
+  return o;
+}
+
+// 16 codes at both ends of an interval of factors: those of the lower end into
+// `o`, and where they differ from the upper end's into `off` (the codes
+// between are then not known).  One test per 16, so that the conversions of
+// all four words run together.
+template <bool kFp8>
+__device__ __forceinline__ bool recode16_between(uint4 x, float lo, float hi, uint4& o, uint4& off) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[4], d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    code_values<kFp8>(w[i], v);
+    c[i] = code4_times<kFp8>(v, lo);
+    d[i] = c[i] ^ code4_times<kFp8>(v, hi);
+  }
+  o = make_uint4(c[0], c[1], c[2], c[3]);
+  off = make_uint4(d[0], d[1], d[2], d[3]);
+  return (d[0] | d[1] | d[2] | d[3]) != 0u;
+}
+
+// `o` with the words marked in `off` (all of them with `every`) made by
+// division: the codes of (code * t) / s.  Out of line: rare, and its code,
+// repeated in every unrolled piece, would not fit the instruction cache.
+template <bool kFp8>
+__device__ __noinline__ uint4 divide_words(uint4 x, uint4 o, uint4 off, float t, float s, bool every) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w}, d[4] = {off.x, off.y, off.z, off.w};
+  uint32_t r[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!every && d[i] == 0u) continue;
+    float v[4];
+    code_values<kFp8>(w[i], v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __fmul_rn(v[k], t);
+    r[i] = code4_divided<kFp8>(v, s);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// 16 codes under scale t as codes under scale s, with q = quotients(t, s).
+// (A code -128, which this library never writes, may round to -128 again
+// where the definition clamps to -127: such pieces divide.)
+template <bool kFp8>
+__device__ __forceinline__ uint4 recode16(uint4 x, const Interval& q, float t, float s) {
+  const bool on = q.on && (kFp8 || largest_code<false>(x) <= 127.0f);
+  uint4 o, off;
+  return recode16_between<kFp8>(x, q.lo, q.hi, o, off) || !on ? divide_words<kFp8>(x, o, off, t, s, !on) : o;
+}
+
+// 16 bf16 values' codes under scale s by division.
+template <bool kFp8>
+__device__ __noinline__ uint4 code16_divided(uint4 a, uint4 b, float s) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[4];
-    four_values<kFp8, kCodes>(w + (kCodes ? i : 2 * i), v);
-    o[i] = 0u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o[i] |= (uint32_t)code8<kFp8>(kCodes ? __fmul_rn(v[k], t) : v[k], s) << (8 * k);
+    bf16_values(w[2 * i], w[2 * i + 1], v);
+    o[i] = code4_divided<kFp8>(v, s);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-// 16 codes under scale t as codes under scale s, at both ends of q =
-// quotients(t, s), and by division when any differ: one branch per 16, so that
-// the conversions of all four words run together.
-template <bool kFp8>
-__device__ __forceinline__ uint4 recode16(uint4 x, const Interval& q, float t, float s) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t o[4], off = 0u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float v[4];
-    code_values<kFp8>(w[i], v);
-    o[i] = code4_times<kFp8>(v, q.lo);
-    off |= o[i] ^ code4_times<kFp8>(v, q.hi);
-  }
-  if (q.on && off == 0u) return make_uint4(o[0], o[1], o[2], o[3]);
-  return code16_divided<kFp8, true>(x, x, t, s);
 }
 
 // 16 finite bf16 values under scale s, with q = quotients(s).  int8 goes by
@@ -239,7 +236,7 @@ __device__ __forceinline__ uint4 code16(uint4 a, uint4 b, const Interval& q, flo
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v[4];
-    four_values<kFp8, false>(w + 2 * i, v);
+    bf16_values(w[2 * i], w[2 * i + 1], v);
     if constexpr (kFp8) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -254,7 +251,7 @@ __device__ __forceinline__ uint4 code16(uint4 a, uint4 b, const Interval& q, flo
     }
   }
   if (q.on && off == 0u) return make_uint4(o[0], o[1], o[2], o[3]);
-  return code16_divided<kFp8, false>(a, b, 1.0f, s);
+  return code16_divided<kFp8>(a, b, s);
 }
 
 }  // namespace dev

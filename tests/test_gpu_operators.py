@@ -405,6 +405,23 @@ def test_evict(pkv, dtype, block, dim, budget, fresh):
     check_evict(got, ref.evict(pool, idx, num, dst, weights))
 
 
+@pytest.mark.parametrize("dtype,block,dim", [("bf16", 16, 64), ("int8", 16, 64), ("fp8", 32, 128)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_evict_many_rounds(pkv, dtype, block, dim, fresh):
+    """Many rounds per CTA and clusters of CTAs, with weights that always move
+    in place: lists whose sources lie far and near."""
+    L = [5000, 3001]
+    pool = ref.Pool(L, 1, dim, block, dtype, seed=3, extra=2 * (2500 // block + 1) if fresh else 3)
+    idx, num = random_keep(pool, 2500, 1, pool.g)
+    idx[0, 0] = torch.cat([torch.arange(1000), torch.arange(3500, 5000)])
+    n = 2500 // block + 1
+    dst = pool.free[:2 * n].view(2, n).contiguous() if fresh else pool.tables
+    weights = torch.rand((2, 1, 5000), generator=pool.g)
+    want = ref.evict(pool, idx, num, dst, weights)
+    for _ in range(5):
+        check_evict(evict(pkv, pool, idx, num, dst if fresh else None, weights), want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_evict_mixed_destinations(pkv, dtype):
     """Some destination blocks replaced, some in place; no weights."""
@@ -522,6 +539,39 @@ def test_append_special_values(pkv, dtype):
     k_new[-2] = 1e-40                                         # bf16 subnormals
     got = append(pkv, pool, k_new, v_new, counts)
     for a, b in zip(got, ref.append(pool, k_new, v_new, counts)):
+        assert same_bits(a, b)
+
+
+def test_append_recodes_minus_128(pkv):
+    """A pool whose int8 codes hold -128 (no call of the library writes it):
+    coded again, it clamps to -127."""
+    pool = ref.Pool([20, 18], 1, 64, 16, "int8", seed=1)
+    for b in (0, 1):
+        pool.k[pool.tables[b, 1].item()][:, :, ::3] = -128
+        pool.v[pool.tables[b, 1].item()] = 127
+    new = pool.randn(2, 1, 64)
+    top = pool.k_scale[pool.tables[:, 1].long(), 0] * 127
+    new[:, 0, 0] = (top * 1.005).to(torch.bfloat16)           # the scale grows by less than one code step
+    got = append(pkv, pool, new, new, [1, 1], decode=True)
+    for a, b in zip(got, ref.append(pool, new, new, [1, 1])):
+        assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["int8", "fp8"])
+@pytest.mark.parametrize("size", [1e-30, 1e-26, 1e-20, 1.0, 1e20, 1e26])
+def test_append_codes_next_to_borders(pkv, dtype, size):
+    """Values whose quotients by the scale fall on or next to the border of two
+    codes, at every magnitude of the scale."""
+    pool = ref.Pool([16 * 12], 2, 64, 16, dtype, seed=5)
+    n = 16 * 12
+    new = []
+    for _ in range(2):
+        # few significant bits, so that x * Q / amax is often a midpoint
+        x = torch.randint(-15, 16, (n, 2, 64), generator=pool.g).double()
+        x[::16, :, 0] = torch.randint(8, 16, (12, 2), generator=pool.g).double() * 2
+        new.append((x * size).to(torch.bfloat16))
+    got = append(pkv, pool, *new, [n])
+    for a, b in zip(got, ref.append(pool, *new, [n])):
         assert same_bits(a, b)
 
 
