@@ -113,11 +113,11 @@ __device__ __forceinline__ void scale_scores(uint32_t (&raw)[32], float f0, floa
 // sum over 32 scores of 2^(s sl2 + off).
 __device__ __forceinline__ float exp_sum(const uint32_t (&raw)[32], float sl2, float off) {
   const uint64_t f = both(sl2), o = both(off);
-  uint64_t s[2] = {0ull, 0ull};
+  uint64_t s[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
   for (int j = 0; j < 32; j += 2)
-    s[(j >> 1) & 1] = add_f32x2(s[(j >> 1) & 1], ex2_f32x2(fma_f32x2(pack_f32x2(raw[j], raw[j + 1]), f, o)));
-  return sum_f32x2(s[0], s[1]);
+    s[(j >> 1) & 3] = add_f32x2(s[(j >> 1) & 3], ex2_f32x2(fma_f32x2(pack_f32x2(raw[j], raw[j + 1]), f, o)));
+  return sum_f32x2(add_f32x2(s[0], s[1]), add_f32x2(s[2], s[3]));
 }
 
 // Running statistics of a query row: l = sum of 2^(s sl2 - ref).  Any
@@ -135,10 +135,9 @@ __device__ __forceinline__ float largest(const uint32_t (&raw)[32]) {
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
-// 32 scores of the row (of keys up to `lim` of the 32 when kMask).
-template <bool kMask>
-__device__ __forceinline__ void add_scores(RowStats& st, uint32_t (&raw)[32], float sl2, int lim) {
-  if constexpr (kMask) {
+// 32 scores of the row (of keys up to `lim` of the 32 unless `whole`).
+__device__ __forceinline__ void add_scores(RowStats& st, uint32_t (&raw)[32], float sl2, bool whole, int lim) {
+  if (!whole) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (j > lim) raw[j] = 0xff800000u;               // -inf
@@ -263,6 +262,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   const bool ok_seq = prompt_rows(a, b, BS, &q0, &n, &L);
   if (!ok_seq) {
     if (kStats && blockIdx.z == 0 && tid == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   // The unit.  Row statistics: row tile (the last ones, with most keys, first)
@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   const int i0 = unit * TT;                            // first query token of the fixed tile
   const int tn = min(TT, n - i0);                      // its tokens
   const int k0 = kStats ? split * a.part_tokens : unit * kTile;  // first key
-  if (kStats ? tn <= 0 : (n == 0 || k0 >= L)) return;
+  if (kStats ? tn <= 0 : (n == 0 || k0 >= L)) {
+    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int first_pos = L - n + i0;
   const int kend = kStats ? min(first_pos + tn, k0 + a.part_tokens) : min(L, k0 + kTile);
   const int rt0 = kStats ? 0 : max(0, k0 - (L - n)) / TT;        // first row tile that sees a key
@@ -317,6 +320,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kStats) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = tmem_base;
   const int32_t* bt = a.block_tables + (int64_t)b * a.max_blocks;
 
@@ -402,6 +406,9 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     __syncwarp();
   } else if (!kStats && warp == kStatWarp) {
     // ======================= column sums: -m' of the row tiles ==============
+    // The kernel may start beside the last CTAs of the one before it (a
+    // programmatic dependent); from here on that one has ended.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     bool bad = false, ok = true;
     for (int c = 0; c < nch; ++c) {
       const int s = c % kStages, i = (rt0 + c) * TT;
@@ -500,8 +507,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
               const int at = 64 * half + 32 * h;
               scale_scores(x[h], ks[at / BS], ks[(at + 16) / BS]);
             }
-            if (whole) add_scores<false>(st, x[h], sl2, 0);
-            else add_scores<true>(st, x[h], sl2, pos - c0 - 64 * half - 32 * h);
+            add_scores(st, x[h], sl2, whole, pos - c0 - 64 * half - 32 * h);
           }
         } else {
           const int pos0 = L - n + i;                  // of the tile's first token
@@ -596,9 +602,19 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
       attr_set[dev] = true;
     }
   }
-  const dim3 grid((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
-  prompt_tc_kernel<D, BS, kKind, kStats><<<grid, kStats ? kStatsThreads : kSumsThreads, PGeo<D>::kSmemBytes, s>>>(km, qm, a);
-  return cuda_check(cudaGetLastError(), "prompt_tc_kernel launch");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
+  cfg.blockDim = dim3(kStats ? kStatsThreads : kSumsThreads);
+  cfg.dynamicSmemBytes = PGeo<D>::kSmemBytes;
+  cfg.stream = s;
+  // the column sums start in the tail of the kernel before them
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kStats ? 0 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, prompt_tc_kernel<D, BS, kKind, kStats>, km, qm, a),
+                    "prompt_tc_kernel launch");
 }
 
 template <int D, int BS, int kKind>
