@@ -11,8 +11,9 @@
 //   column sums      fixed: 128 keys,        streamed: the row tiles that see
 //                    them; a thread owns a key and adds 2^(s - m') over the
 //                    rows, m' = m + log2 l of each row from shared memory
-// so that neither a maximum nor a sum crosses threads.  Warps 0-7 hold one
-// fixed row per thread (a TMEM lane) and 64 of its 128 columns, warp 8 issues
+// so that neither a maximum nor a sum crosses threads.  Warps 0-3 hold one
+// fixed row per thread (a TMEM lane) and take the even chunks, warps 4-7 the
+// odd ones (so a set, a stage and a TMEM buffer go together), warp 8 issues
 // the MMAs (S[128 x 128] = fixed . streamed^T into one of two TMEM buffers),
 // warp 9 the TMA loads, and in the column sums warp 10 fetches each row tile's
 // m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
@@ -47,7 +48,8 @@ using namespace dev;
 
 constexpr int kTile = 128;                             // rows of either operand
 constexpr int kStages = 2;                             // = TMEM buffers
-constexpr int kRowWarps = 8;                           // two per 32 rows, 64 columns each
+constexpr int kRowWarps = 8;                           // two sets of four, by the chunk's parity
+constexpr int kSetWarps = kRowWarps / 2, kSetThreads = kSetWarps * 32;
 constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1, kStatWarp = kRowWarps + 2;
 constexpr int kStatsThreads = (kRowWarps + 2) * 32, kSumsThreads = (kRowWarps + 3) * 32;
 constexpr int kTmemCols = kStages * kTile;
@@ -187,21 +189,26 @@ __device__ __forceinline__ float row_log_sum(float m, float l) {
   return m == -INFINITY ? __uint_as_float(0x7fc00000u) : m + log2f(l);
 }
 
-// 8-bit pools: this thread's codes of the 128 keys from `from` (zeros from L
-// on), and the codes widened into a swizzled bf16 image.  256 threads; thread
-// piece u holds 16 codes of key (u * 256 + tid) / (D / 16).
+// 8-bit pools: the codes of the 128 keys from `from` (zeros from L on), loaded
+// by one set of row warps and widened into a swizzled bf16 image; a piece is 16
+// codes of a key.
 template <int D, int BS, int kKind>
 struct Codes {
   static constexpr int kRowPieces = D / 16;
-  static constexpr int kPieces = kTile * kRowPieces / (kRowWarps * 32);
+  static constexpr int kParts = 2;                       // held one at a time
+  static constexpr int kPieces = kTile * kRowPieces / kSetThreads / kParts;
   uint4 x[kPieces];
 
+  __device__ __forceinline__ static int piece(int part, int u) {
+    return (part * kPieces + u) * kSetThreads + (int)(threadIdx.x % kSetThreads);
+  }
+
   // False when a key's block is outside the pool.
-  __device__ __forceinline__ bool load(const PromptArgs& a, const int32_t* bt, int hk, int from, int L) {
+  __device__ __forceinline__ bool load(const PromptArgs& a, const int32_t* bt, int hk, int from, int L, int part) {
     bool ok = true;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int i = u * kRowWarps * 32 + (int)threadIdx.x, key = from + i / kRowPieces;
+      const int i = piece(part, u), key = from + i / kRowPieces;
       x[u] = make_uint4(0u, 0u, 0u, 0u);
       if (key >= L) continue;
       const int p = bt[key / BS];
@@ -215,10 +222,10 @@ struct Codes {
     return ok;
   }
 
-  __device__ __forceinline__ void store(unsigned char* img) const {
+  __device__ __forceinline__ void store(unsigned char* img, int part) const {
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int i = u * kRowWarps * 32 + (int)threadIdx.x, r = i / kRowPieces;
+      const int i = piece(part, u), r = i / kRowPieces;
       const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
       uint32_t o[8];
 #pragma unroll
@@ -235,7 +242,16 @@ struct Codes {
             make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
+  }
+
+  // The other part, after the one that is held; then the image is complete.
+  __device__ __forceinline__ bool finish(const PromptArgs& a, const int32_t* bt, int hk, int from, int L,
+                                         unsigned char* img) {
+    store(img, 0);
+    const bool ok = load(a, bt, hk, from, L, 1);
+    store(img, 1);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return ok;
   }
 };
 
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int sh_bad, sh_fail;
   __shared__ __align__(16) float row_m[kStages][kTile];  // -m' of the row tile's rows
-  __shared__ float half_part[kTile], half_ref[kTile];  // the upper columns' results
+  __shared__ float half_part[kTile], half_ref[kTile];  // the odd chunks' results
   __shared__ float blk_ks[kWidenStream ? kScaleSlots : 1][kTile / BS];  // K scales of the chunks' blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x, b = blockIdx.y;
@@ -301,12 +317,12 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
   if (tid == 0) {
     sh_bad = 0;
     sh_fail = 0;
-    mbar_init(smem_addr(&fixed_full), kWidenFixed ? kRowWarps : 1);
+    mbar_init(smem_addr(&fixed_full), kWidenFixed ? kSetWarps : 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(&full[s]), kWidenStream ? kRowWarps : 1);
+      mbar_init(smem_addr(&full[s]), kWidenStream ? kSetWarps : 1);
       mbar_init(smem_addr(&empty[s]), 1);
       mbar_init(smem_addr(&s_full[s]), 1);
-      mbar_init(smem_addr(&buf_free[s]), kRowWarps);
+      mbar_init(smem_addr(&buf_free[s]), kSetWarps);
       mbar_init(smem_addr(&stat_full[s]), 1);
     }
     mbar_init(smem_addr(&drain_bar), 1);
@@ -433,20 +449,20 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     if (bad) sh_bad = 1;
     if (!ok && lane == 0) sh_fail = 1;
   } else {
-    // ======================= one fixed row per thread, 64 columns ===========
+    // ======================= one fixed row per thread =======================
     bool ok = true;
-    const int row = tid & (kTile - 1), half = warp >> 2;
+    const int row = tid & (kTile - 1), set = warp / kSetWarps;
     const int key = k0 + row;                          // column sums
     const int pos = kStats && row < my_rows ? first_pos + row / G : -1;
     // a warp whose rows are all padding only keeps the barriers' phases
-    const int row_lo = (warp & 3) * 32;
+    const int row_lo = (warp % kSetWarps) * 32;
     const bool live = kStats ? row_lo < my_rows : k0 + row_lo < kend;
     float sl2 = a.scale_log2;
-    const uint32_t lanes = tm + ((uint32_t)row_lo << 16) + 64 * half;
+    const uint32_t scores = tm + ((uint32_t)row_lo << 16) + set * kTile;
     [[maybe_unused]] Codes<D, BS, kQ8 ? kKind : KV_DTYPE_INT8> codes;
-    // K scales of the blocks of the chunk whose codes this thread widens
+    // K scales of the blocks of a chunk that this set widens
     auto put_scales = [&](int c) {
-      const int j = tid, from = k0 + c * kTile + j * BS;
+      const int j = row, from = k0 + c * kTile + j * BS;
       if (j < kTile / BS) {
         const int p = from < L ? bt[from / BS] : -1;
         blk_ks[c & (kScaleSlots - 1)][j] =
@@ -454,32 +470,39 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       }
     };
     if constexpr (kWidenFixed) {
-      if (!codes.load(a, bt, hk, k0, L)) sh_bad = 1;
-      codes.store(gbase);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&fixed_full));
+      if (set == 0) {
+        bool all = codes.load(a, bt, hk, k0, L, 0);
+        all &= codes.finish(a, bt, hk, k0, L, gbase);
+        if (!all) sh_bad = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&fixed_full));
+      }
       if (key < kend) {
         const int p = bt[key / BS];
         if (p >= 0 && p < a.num_blocks) sl2 *= a.k_scale[(int64_t)p * a.num_kv_heads + hk];
       }
     }
+    // chunk c of this set into its stage, once part 0 of its codes is held
+    auto put_chunk = [&](int c) {
+      put_scales(c);
+      if (!codes.finish(a, bt, hk, k0 + c * kTile, L, gbase + (1 + set) * P::kImage)) sh_bad = 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&full[set]));
+    };
     if constexpr (kWidenStream) {
-      for (int c = 0; c < kStages && c < nch; ++c) {
-        if (!codes.load(a, bt, hk, k0 + c * kTile, L)) sh_bad = 1;
-        put_scales(c);
-        codes.store(gbase + (1 + c) * P::kImage);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&full[c]));
+      if (set < nch) {
+        if (!codes.load(a, bt, hk, k0 + set * kTile, L, 0)) sh_bad = 1;
+        put_chunk(set);
       }
     }
-    for (int c = 0; c < nch; ++c) {
+    for (int c = set; c < nch; c += kStages) {
       if constexpr (kWidenStream) {
-        if (c + kStages < nch && !codes.load(a, bt, hk, k0 + (c + kStages) * kTile, L)) sh_bad = 1;
+        if (c + kStages < nch && !codes.load(a, bt, hk, k0 + (c + kStages) * kTile, L, 0)) sh_bad = 1;
       }
-      const int s = c % kStages, ph = (c / kStages) & 1;
-      if (!warp_wait(smem_addr(&s_full[s]), ph) ||
-          (!kStats && !warp_wait(smem_addr(&stat_full[s]), ph)) ||
-          (kWidenStream && !warp_wait(smem_addr(&full[s]), ph))) {  // (the other warps' scales)
+      const int ph = (c / kStages) & 1;
+      if (!warp_wait(smem_addr(&s_full[set]), ph) ||
+          (!kStats && !warp_wait(smem_addr(&stat_full[set]), ph)) ||
+          (kWidenStream && !warp_wait(smem_addr(&full[set]), ph))) {  // (the other warps' scales)
         ok = false;
         break;
       }
@@ -487,55 +510,51 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       const int c0 = k0 + c * kTile;                   // row statistics: the chunk's first key
       const int i = (rt0 + c) * TT;                    // column sums: the tile's first token
       const int cols = kStats ? kTile : min(TT, n - i) * G;
-      if (live && 64 * half < cols) {
-        uint32_t x[2][32];
-        tmem_ld32(lanes + s * kTile, x[0]);
-        if (!kWidenStream) tmem_ld32(lanes + s * kTile + 32, x[1]);
-        tmem_wait_ld32(x[0]);
-        if (!kWidenStream) tmem_wait_ld32(x[1]);
-        if constexpr (kStats) {
-          const bool whole = c0 + 64 * half + 63 <= first_pos;
+      if (live) {
+        const bool whole = kStats ? c0 + kTile - 1 <= first_pos
+                                  : cols == kTile && L - n + i >= k0 + kTile - 1;
+        const int from = max(0, key - (L - n + i)) * G;  // column sums: the rows [from, cols) see the key
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          if (32 * g >= cols) break;
+          uint32_t x[2][32];
+          __syncwarp();                                // (the TMEM loads are the whole warp's)
+          tmem_ld32(scores + 32 * g, x[0]);
+          if (!kWidenStream) tmem_ld32(scores + 32 * g + 32, x[1]);
+          tmem_wait_ld32(x[0]);
+          if (!kWidenStream) tmem_wait_ld32(x[1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if constexpr (kWidenStream) {
-              if (h == 1) {
-                __syncwarp();
-                tmem_ld32(lanes + s * kTile + 32, x[1]);
-                tmem_wait_ld32(x[1]);
+            const int at = 32 * (g + h);
+            if constexpr (kStats) {
+              if constexpr (kWidenStream) {
+                if (h == 1) {
+                  __syncwarp();
+                  tmem_ld32(scores + at, x[1]);
+                  tmem_wait_ld32(x[1]);
+                }
+                const float* ks = blk_ks[c & (kScaleSlots - 1)];
+                scale_scores(x[h], ks[at / BS], ks[(at + 16) / BS]);
               }
-              const float* ks = blk_ks[c & (kScaleSlots - 1)];
-              const int at = 64 * half + 32 * h;
-              scale_scores(x[h], ks[at / BS], ks[(at + 16) / BS]);
+              add_scores(st, x[h], sl2, whole, pos - c0 - at);
+            } else {
+              const float* m = row_m[set] + at;
+              acc += whole ? column_part<false>(x[h], sl2, m, 0, 32)
+                           : column_part<true>(x[h], sl2, m, from - at, cols - at);
             }
-            add_scores(st, x[h], sl2, whole, pos - c0 - 64 * half - 32 * h);
-          }
-        } else {
-          const int pos0 = L - n + i;                  // of the tile's first token
-          const bool whole = cols == kTile && pos0 >= k0 + kTile - 1;
-          const int from = max(0, key - pos0) * G - 64 * half, to = cols - 64 * half;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float* m = row_m[s] + 64 * half + 32 * h;
-            acc += whole ? column_part<false>(x[h], sl2, m, 0, 32)
-                         : column_part<true>(x[h], sl2, m, from - 32 * h, to - 32 * h);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&buf_free[s]));
+      if (lane == 0) mbar_arrive(smem_addr(&buf_free[set]));
       if constexpr (kWidenStream) {
         // the scores of chunk c are complete, so its stage is free
-        if (c + kStages < nch) {
-          put_scales(c + kStages);
-          codes.store(gbase + (1 + s) * P::kImage);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&full[s]));
-        }
+        if (c + kStages < nch) put_chunk(c + kStages);
       }
     }
     if (!ok && lane == 0) sh_fail = 1;
-    if (half == 1) {
+    if (set == 1) {
       half_part[row] = kStats ? st.l : acc;
       half_ref[row] = st.ref;
     }
