@@ -7,6 +7,7 @@
 #include <cooperative_groups.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
@@ -39,8 +40,10 @@ using namespace dev;
 
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
+template <int n>
+using Bins = std::integral_constant<int, n>;
 constexpr int kMostCtas = 8;                         // of a cluster
-constexpr int kBatch = 8;                            // loads in flight per thread
+constexpr int kBatch = 4;                            // loads in flight per thread
 
 struct SelectArgs {
   const float* weights;      // [B, Hkv, stride]
@@ -84,11 +87,16 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
   return before + x - v;
 }
 
+// Four CTAs of 256 threads per SM (64 registers): the barriers and histogram
+// adds of one wait while others run.  64 x 8 rows: of 4096 tokens 18.7 -> 14.6
+// us against two CTAs per SM, of 8192 43 -> 35.6, of 32768 172 -> 140; 64 x 8
+// rows of mixed 512..4096 tokens, which two per SM balance better, 12.3 ->
+// 13.5.  The 512-thread form (longer rows, fewer of them) gains nothing from a
+// third CTA (8 x 8 rows of 131072 tokens: 37.8 us with two, 40.0 with three).
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 2) select_kernel(const SelectArgs a) {
   constexpr int kWarps = kThreads / 32;
-  constexpr int kBinsPer = kBins / kThreads;         // bins per thread, at most
-  extern __shared__ uint32_t sel_smem[];
+  extern __shared__ __align__(16) uint32_t sel_smem[];
   uint32_t* hist = sel_smem;                         // [kPasses][kBins]
   __shared__ int warp_sums[kWarps], sh_bin, sh_need;
   __shared__ int sh_counts[2];                       // this CTA's (above, equal) counts
@@ -98,7 +106,8 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
   const int b = row / a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = a.keep_idx + (int64_t)row * a.budget;
-  for (int i = tid; i < kPasses * kBins; i += kThreads) hist[i] = 0u;
+  for (int i = tid; i < kPasses * kBins / 4; i += kThreads)
+    reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   const int L = a.seq_lens[b];
   const bool bad = L <= 0 || L > a.max_len;          // (cluster-uniform)
   if (bad || L <= a.budget) {
@@ -147,11 +156,12 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
   // The digit of T among `h`'s bins from the top, summed over the cluster:
   // each CTA adds up its share of the bins and hands the sums to all (every
   // CTA reading every peer's whole histogram took eight times the traffic).
-  auto digit = [&](const uint32_t* h, int bins) {
+  auto digit = [&](const uint32_t* h, auto bins) {
+    constexpr int kBinsOf = decltype(bins)::value;
     const uint32_t* sums = h;
     if (C > 1) {
       cluster.sync();
-      const int share = bins / C;
+      const int share = kBinsOf / C;
       for (int i = rank * share + tid; i < (rank + 1) * share; i += kThreads) {
         uint32_t v = 0u;
 #pragma unroll
@@ -166,20 +176,27 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
     } else {
       __syncthreads();
     }
-    const int run = bins / kThreads;                 // bins per thread
-    const int top = bins - 1 - run * tid;
-    int c[kBinsPer], sum = 0;
+    constexpr int run = kBinsOf / kThreads;          // bins per thread, loaded as vectors
+    const int top = kBinsOf - 1 - run * tid;
+    int c[run], sum = 0;                             // from the top down
+    if constexpr (run >= 4) {
 #pragma unroll
-    for (int i = 0; i < kBinsPer; ++i) c[i] = 0;
+      for (int i = 0; i < run; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sums + top - i - 3);
+        c[i] = (int)v.w, c[i + 1] = (int)v.z, c[i + 2] = (int)v.y, c[i + 3] = (int)v.x;
+      }
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(sums + top - 1);
+      c[0] = (int)v.y, c[1] = (int)v.x;
+    }
 #pragma unroll
-    for (int i = 0; i < kBinsPer; ++i)
-      if (i < run) sum += c[i] = (int)sums[top - i];
+    for (int i = 0; i < run; ++i) sum += c[i];
     int total;
     int before = block_exclusive<kThreads>(sum, warp_sums, &total);
     if (before < need && need <= before + sum) {
       int at = top;
 #pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) {
+      for (int i = 0; i < run; ++i) {
         if (before + c[i] >= need) break;
         before += c[i];
         --at;
@@ -191,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
     need = sh_need;
     return (uint32_t)sh_bin;                         // (written again after further barriers only)
   };
-  prefix = digit(hist, 2048) << 21;
+  prefix = digit(hist, Bins<kBins>()) << 21;
 
   // second digit of the open keys; the chunks' bits
   uint32_t* h2 = hist + kBins;
@@ -217,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
       }
     }
   }
-  prefix |= digit(h2, 2048) << 10;
+  prefix |= digit(h2, Bins<kBins>()) << 10;
 
   // From here on a thread owns a run of chunks.  An open key whose bits above
   // `shift` are above T's is kept, one below is dropped.
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a)
   };
   uint32_t* h3 = hist + 2 * kBins;
   settle(10, [&](uint32_t key) { atomicAdd(&h3[key & 1023u], 1u); });
-  prefix |= digit(h3, 1024);                         // = T; `need` of the keys equal to it are kept
+  prefix |= digit(h3, Bins<1024>());                         // = T; `need` of the keys equal to it are kept
   settle(0, [](uint32_t) {});
 
   int above = 0, equal = 0;
