@@ -702,9 +702,9 @@ size_t pagedkv_attention_weights_workspace_bytes(int num_tokens,
  * they are, and so do bad offsets, lengths and blocks (flagged as in
  * paged_attention_multi).  V is not read.  Any group of query heads per KV
  * head.  Other arguments as for paged_attention_multi; the workspace is
- * 16-byte aligned, pagedkv_attention_weights_workspace_bytes(...).  Two
- * launches, asynchronous on `stream`; no atomics, so equal inputs give equal
- * bits. */
+ * 16-byte aligned, pagedkv_attention_weights_workspace_bytes(...).  One to
+ * three launches, asynchronous on `stream`; no atomics, so equal inputs give
+ * equal bits. */
 kv_status pagedkv_attention_weights(
     float *weights, int weights_stride, const void *q, const void *k_cache,
     const float *k_scale, const int32_t *block_tables, int max_blocks_per_seq,
@@ -757,7 +757,8 @@ kv_status pagedkv_select_tokens(int32_t *keep_idx, int32_t *keep_len,
  * A list that does not ascend in range leaves that (sequence, head) as it was
  * and sets PAGEDKV_FLAG_BAD_INDEX; bad lengths skip the sequence
  * (PAGEDKV_FLAG_BAD_SEQ_LEN), a table entry outside the pool skips the
- * destination block (PAGEDKV_FLAG_BAD_BLOCK).  One launch, asynchronous on
+ * destination block (PAGEDKV_FLAG_BAD_BLOCK; the weights, which are no part of
+ * a block, move all the same).  One launch, asynchronous on
  * `stream`. */
 kv_status pagedkv_evict_tokens(void *k_cache, void *v_cache, float *k_scale,
                                float *v_scale, const int32_t *block_tables,

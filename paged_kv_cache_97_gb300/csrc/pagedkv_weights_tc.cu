@@ -19,16 +19,25 @@
 // m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
 // heads, as one TMA box; rows past the sequence's queries are masked.
 //
-// What bounds it is the issue of the epilogue's instructions: a 128 x 128 tile
-// has 16384 exponentials against 256 cycles of MMA, so each costs one packed
-// half of a multiply-add and of an add beside it (f32x2), and no maximum: a
-// row's reference is its first scores' and moves only when a sum grows past
-// 2^60.  8-bit pools: the row warps load the codes themselves, widen them to
-// bf16 (exact: 8 significant bits hold every int8 and E4M3 code) and write
-// them into the swizzled image, the streamed keys two chunks ahead, right
-// after the scores of the chunk that used the stage before; a block's K scale
-// multiplies its scores.  Two CTAs per SM (256 TMEM columns and about 100 KB of shared memory
-// each), so that one's start and end overlap the other's work.
+// What bounds it is the exponentials, 16 per clock and SM: a 128 x 128 tile has
+// 16384 of them, 1024 cycles against 256 of MMA, and one prompt of 16K tokens
+// (32/8 heads, bf16) takes about 1030 per tile and pass: 1857 us.  Beside each
+// stand one packed half of a multiply-add and of an add (f32x2) and no
+// maximum: a row's reference is its first scores' and moves only when a sum
+// grows past 2^60.  4 prompts of 1..4K tokens take 267 us, where the
+// exponentials alone would take about 229; the rest is the CTAs' start and end
+// and the masked halves of diagonal tiles.  Measured and not taken: the fixed
+// operand in TMEM and the streamed tiles shared by two CTAs through TMA
+// multicast (1857 -> 1870..1880 us, 267 -> 286..288): the feeding of the MMA is
+// not what it waits for.
+//
+// 8-bit pools: the row warps load the codes themselves, widen them to bf16
+// (exact: 8 significant bits hold every int8 and E4M3 code) and write them into
+// the swizzled image, the streamed keys two chunks ahead, right after the
+// scores of the chunk that used the stage before; a block's K scale multiplies
+// its scores (one prompt of 8K tokens, E4M3: 791 us).  Two CTAs per SM (256
+// TMEM columns and about 100 KB of shared memory each), so that one's start
+// and end overlap the other's work.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
