@@ -15,8 +15,7 @@
 // fixed row per thread (a TMEM lane) and take the even chunks, warps 4-7 the
 // odd ones (so a set, a stage and a TMEM buffer go together), warp 8 issues
 // the MMAs (S[128 x 128] = fixed . streamed^T into one of two TMEM buffers),
-// warp 9 the TMA loads, and in the column sums warp 10 fetches each row tile's
-// m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
+// warp 9 the TMA loads and, in the column sums, each row tile's m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
 // heads, as one TMA box; rows past the sequence's queries are masked.
 //
 // What bounds it is the exponentials, 16 per clock and SM: a 128 x 128 tile has
@@ -59,8 +58,9 @@ constexpr int kTile = 128;                             // rows of either operand
 constexpr int kStages = 2;                             // = TMEM buffers
 constexpr int kRowWarps = 8;                           // two sets of four, by the chunk's parity
 constexpr int kSetWarps = kRowWarps / 2, kSetThreads = kSetWarps * 32;
-constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1, kStatWarp = kRowWarps + 2;
-constexpr int kStatsThreads = (kRowWarps + 2) * 32, kSumsThreads = (kRowWarps + 3) * 32;
+constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1;
+constexpr int kThreads = (kRowWarps + 2) * 32;
+constexpr int kRowSlots = 8;                           // chunks whose rows' m' may be in use
 constexpr int kTmemCols = kStages * kTile;
 constexpr float kMoveSum = 0x1p60f;                    // a sum of 32 that moves a row's reference
 
@@ -108,7 +108,7 @@ __device__ __forceinline__ float sum_f32x2(uint64_t a, uint64_t b) {
 }
 
 // raw *= f (the first 16 by f0, the others by f1).
-__device__ __forceinline__ void scale_scores(uint32_t (&raw)[32], float f0, float f1) {
+__device__ __forceinline__ void scale_scores(uint32_t* raw, float f0, float f1) {
   const uint64_t f[2] = {both(f0), both(f1)};
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
@@ -122,7 +122,7 @@ __device__ __forceinline__ void scale_scores(uint32_t (&raw)[32], float f0, floa
 }
 
 // sum over 32 scores of 2^(s sl2 + off).
-__device__ __forceinline__ float exp_sum(const uint32_t (&raw)[32], float sl2, float off) {
+__device__ __forceinline__ float exp_sum(const uint32_t* raw, float sl2, float off) {
   const uint64_t f = both(sl2), o = both(off);
   uint64_t s[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -139,7 +139,7 @@ struct RowStats {
   float ref, l;
 };
 
-__device__ __forceinline__ float largest(const uint32_t (&raw)[32]) {
+__device__ __forceinline__ float largest(const uint32_t* raw) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(raw[j]));
@@ -147,7 +147,7 @@ __device__ __forceinline__ float largest(const uint32_t (&raw)[32]) {
 }
 
 // 32 scores of the row (of keys up to `lim` of the 32 unless `whole`).
-__device__ __forceinline__ void add_scores(RowStats& st, uint32_t (&raw)[32], float sl2, bool whole, int lim) {
+__device__ __forceinline__ void add_scores(RowStats& st, uint32_t* raw, float sl2, bool whole, int lim) {
   if (!whole) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -167,7 +167,7 @@ __device__ __forceinline__ void add_scores(RowStats& st, uint32_t (&raw)[32], fl
 // sum over 32 rows of 2^(s sl2 - m'), neg_m = -m' (rows in [from, to) of the
 // 32 when kMask).
 template <bool kMask>
-__device__ __forceinline__ float column_part(const uint32_t (&raw)[32], float sl2, const float* neg_m,
+__device__ __forceinline__ float column_part(const uint32_t* raw, float sl2, const float* neg_m,
                                              int from, int to) {
   const uint64_t f = both(sl2);
   uint64_t s[2] = {0ull, 0ull};
@@ -265,19 +265,20 @@ struct Codes {
 };
 
 template <int D, int BS, int kKind, bool kStats>
-__global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap q_map, const PromptArgs a) {
   using P = PGeo<D>;
   constexpr bool kQ8 = kKind != KV_DTYPE_BF16;
   constexpr bool kWidenStream = kQ8 && kStats, kWidenFixed = kQ8 && !kStats;
+  constexpr int kRead = kWidenStream ? 32 : 64;        // scores of a row in registers at a time
   constexpr int kScaleSlots = 4;                       // chunks whose scales may be in use
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t fixed_full, full[kStages], empty[kStages], s_full[kStages], buf_free[kStages],
-      stat_full[kStages], drain_bar;
+      stat_full[kRowSlots], drain_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int sh_bad, sh_fail;
-  __shared__ __align__(16) float row_m[kStages][kTile];  // -m' of the row tile's rows
+  __shared__ __align__(16) float row_m[kStats ? 1 : kRowSlots][kTile];  // -m' of the row tiles' rows
   __shared__ float half_part[kTile], half_ref[kTile];  // the odd chunks' results
   __shared__ float blk_ks[kWidenStream ? kScaleSlots : 1][kTile / BS];  // K scales of the chunks' blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -332,8 +333,8 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       mbar_init(smem_addr(&empty[s]), 1);
       mbar_init(smem_addr(&s_full[s]), 1);
       mbar_init(smem_addr(&buf_free[s]), kSetWarps);
-      mbar_init(smem_addr(&stat_full[s]), 1);
     }
+    for (int s = 0; s < kRowSlots; ++s) mbar_init(smem_addr(&stat_full[s]), 1);
     mbar_init(smem_addr(&drain_bar), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -384,8 +385,19 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
     };
     if (kStats) load_q(base, &fixed_full, i0);
     else if (!kQ8) load_k(base, &fixed_full, k0);
+    // column sums: m' of the rows of chunk c's row tile
+    [[maybe_unused]] float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto fetch = [&](int c) {
+      const int i = (rt0 + c) * TT, rows = min(TT, n - i) * G;
+      const float* st_row = stats_at(i);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = u * 32 + lane;
+        m[u] = r < rows ? st_row[(int64_t)r * a.splits * 2] : 0.0f;
+      }
+    };
     int issued = 0;
-    bool ok = true;
+    bool ok = true, bad = false;
     for (int c = 0; c < (kWidenStream ? 0 : nch); ++c) {
       const int s = c % kStages;
       if (c >= kStages && !warp_wait(smem_addr(&empty[s]), ((c / kStages) - 1) & 1)) {
@@ -395,7 +407,26 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       if (kStats) load_k(stage_img(s), &full[s], k0 + c * kTile);
       else load_q(stage_img(s), &full[s], (rt0 + c) * TT);
       issued = c + 1;
+      if constexpr (!kStats) {
+        if (c == 0) {
+          // The kernel may start beside the last CTAs of the one before it (a
+          // programmatic dependent); from here on that one has ended.
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          fetch(0);
+        }
+        // (the MMA of chunk c - 2 is done, so chunk c - 4's scores were read, and
+        // before them chunk c - 6 was finished: its slot and barrier phase are free)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          bad |= m[u] == -INFINITY;                    // a row without statistics
+          row_m[c % kRowSlots][u * 32 + lane] = -m[u];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&stat_full[c % kRowSlots]));
+        if (c + 1 < nch) fetch(c + 1);
+      }
     }
+    if (bad) sh_bad = 1;
     // every load has landed before the CTA ends (bounded; normally it has)
     if (!kWidenFixed && !warp_wait(smem_addr(&fixed_full), 0)) ok = false;
     for (int s = 0; s < kStages && s < issued; ++s) {
@@ -429,34 +460,6 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       mbar_wait(smem_addr(&drain_bar), 0);
     }
     __syncwarp();
-  } else if (!kStats && warp == kStatWarp) {
-    // ======================= column sums: -m' of the row tiles ==============
-    // The kernel may start beside the last CTAs of the one before it (a
-    // programmatic dependent); from here on that one has ended.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    bool bad = false, ok = true;
-    for (int c = 0; c < nch; ++c) {
-      const int s = c % kStages, i = (rt0 + c) * TT;
-      const int rows = min(TT, n - i) * G;
-      const float* st_row = stats_at(i);
-      float m[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = u * 32 + lane;
-        m[u] = r < rows ? st_row[(int64_t)r * a.splits * 2] : 0.0f;
-        bad |= m[u] == -INFINITY;                      // a row without statistics
-      }
-      if (c >= kStages && !warp_wait(smem_addr(&buf_free[s]), ((c / kStages) - 1) & 1)) {
-        ok = false;
-        break;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) row_m[s][u * 32 + lane] = -m[u];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&stat_full[s]));
-    }
-    if (bad) sh_bad = 1;
-    if (!ok && lane == 0) sh_fail = 1;
   } else {
     // ======================= one fixed row per thread =======================
     bool ok = true;
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       }
       const int ph = (c / kStages) & 1;
       if (!warp_wait(smem_addr(&s_full[set]), ph) ||
-          (!kStats && !warp_wait(smem_addr(&stat_full[set]), ph)) ||
+          (!kStats && !warp_wait(smem_addr(&stat_full[c % kRowSlots]), (c / kRowSlots) & 1)) ||
           (kWidenStream && !warp_wait(smem_addr(&full[set]), ph))) {  // (the other warps' scales)
         ok = false;
         break;
@@ -519,44 +522,40 @@ __global__ void __launch_bounds__(kStats ? kStatsThreads : kSumsThreads, 2)
       const int c0 = k0 + c * kTile;                   // row statistics: the chunk's first key
       const int i = (rt0 + c) * TT;                    // column sums: the tile's first token
       const int cols = kStats ? kTile : min(TT, n - i) * G;
+      auto free_buf = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&buf_free[set]));
+      };
       if (live) {
         const bool whole = kStats ? c0 + kTile - 1 <= first_pos
                                   : cols == kTile && L - n + i >= k0 + kTile - 1;
         const int from = max(0, key - (L - n + i)) * G;  // column sums: the rows [from, cols) see the key
 #pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          if (32 * g >= cols) break;
-          uint32_t x[2][32];
+        for (int at = 0; at < kTile; at += kRead) {
+          if (at >= cols) break;
+          uint32_t x[kRead];
           __syncwarp();                                // (the TMEM loads are the whole warp's)
-          tmem_ld32(scores + 32 * g, x[0]);
-          if (!kWidenStream) tmem_ld32(scores + 32 * g + 32, x[1]);
-          tmem_wait_ld32(x[0]);
-          if (!kWidenStream) tmem_wait_ld32(x[1]);
+          if constexpr (kRead == 64) tmem_read64(scores + at, x);
+          else tmem_read32(scores + at, x);
+          if (at + kRead >= cols) free_buf();          // the buffer's last scores are in registers
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int at = 32 * (g + h);
+          for (int h = 0; h < kRead; h += 32) {
             if constexpr (kStats) {
               if constexpr (kWidenStream) {
-                if (h == 1) {
-                  __syncwarp();
-                  tmem_ld32(scores + at, x[1]);
-                  tmem_wait_ld32(x[1]);
-                }
                 const float* ks = blk_ks[c & (kScaleSlots - 1)];
-                scale_scores(x[h], ks[at / BS], ks[(at + 16) / BS]);
+                scale_scores(x + h, ks[(at + h) / BS], ks[(at + h + 16) / BS]);
               }
-              add_scores(st, x[h], sl2, whole, pos - c0 - at);
+              add_scores(st, x + h, sl2, whole, pos - c0 - at - h);
             } else {
-              const float* m = row_m[set] + at;
-              acc += whole ? column_part<false>(x[h], sl2, m, 0, 32)
-                           : column_part<true>(x[h], sl2, m, from - at, cols - at);
+              const float* m = row_m[c % kRowSlots] + at + h;
+              acc += whole ? column_part<false>(x + h, sl2, m, 0, 32)
+                           : column_part<true>(x + h, sl2, m, from - at - h, cols - at - h);
             }
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&buf_free[set]));
+      if (!live) free_buf();
       if constexpr (kWidenStream) {
         // the scores of chunk c are complete, so its stage is free
         if (c + kStages < nch) put_chunk(c + kStages);
@@ -632,7 +631,7 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
-  cfg.blockDim = dim3(kStats ? kStatsThreads : kSumsThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = PGeo<D>::kSmemBytes;
   cfg.stream = s;
   // the column sums start in the tail of the kernel before them
