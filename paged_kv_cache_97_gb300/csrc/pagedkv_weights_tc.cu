@@ -355,10 +355,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == kLoadWarp) {
     // ======================= loads (TMA) ====================================
-    // Keys [from, from + 128) (up to L) into an image, one block per lane.
-    auto load_k = [&](uint32_t img, uint64_t* bar, int from) {
+    // Keys [from, from + 128) (up to L) into an image, one block per lane: its
+    // table entry, read ahead of the wait for the image, then the load.
+    auto entry = [&](int from) {
+      return lane < min(kTile / BS, (L - from + BS - 1) / BS) ? bt[from / BS + lane] : 0;
+    };
+    auto load_k = [&](uint32_t img, uint64_t* bar, int from, int p) {
       const int nb = min(kTile / BS, (L - from + BS - 1) / BS);
-      int p = lane < nb ? bt[from / BS + lane] : 0;
       if (p < 0 || p >= a.num_blocks) {
         sh_bad = 1;
         p = 0;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
     };
     if (kStats) load_q(base, &fixed_full, i0);
-    else if (!kQ8) load_k(base, &fixed_full, k0);
+    else if (!kQ8) load_k(base, &fixed_full, k0, entry(k0));
     // column sums: m' of the rows of chunk c's row tile
     [[maybe_unused]] float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     auto fetch = [&](int c) {
@@ -398,14 +401,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     int issued = 0;
     bool ok = true, bad = false;
+    [[maybe_unused]] int next = kStats && !kWidenStream ? entry(k0) : 0;
     for (int c = 0; c < (kWidenStream ? 0 : nch); ++c) {
       const int s = c % kStages;
       if (c >= kStages && !warp_wait(smem_addr(&empty[s]), ((c / kStages) - 1) & 1)) {
         ok = false;
         break;
       }
-      if (kStats) load_k(stage_img(s), &full[s], k0 + c * kTile);
-      else load_q(stage_img(s), &full[s], (rt0 + c) * TT);
+      if (kStats) {
+        load_k(stage_img(s), &full[s], k0 + c * kTile, next);
+        next = entry(k0 + (c + 1) * kTile);
+      }
+      if (!kStats) load_q(stage_img(s), &full[s], (rt0 + c) * TT);
       issued = c + 1;
       if constexpr (!kStats) {
         if (c == 0) {
