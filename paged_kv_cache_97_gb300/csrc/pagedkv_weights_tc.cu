@@ -3,40 +3,50 @@
 // of pagedkv_attention_weights over Q K^T (pagedkv_weights.cu) with the scores
 // in TMEM.
 //
-// The two passes are one kernel with the operands exchanged.  A CTA keeps one
-// tile of 128 rows of one operand in shared memory and streams tiles of 128
-// rows of the other through two stages:
+// The two passes are one kernel with the operands exchanged.  A unit of work
+// keeps one tile of 128 rows of one operand in shared memory and streams tiles
+// of 128 rows of the other (chunks) through two stages:
 //   row statistics   fixed: 128 query rows,  streamed: the keys they see;
 //                    a thread owns a query row and keeps its (m, l)
 //   column sums      fixed: 128 keys,        streamed: the row tiles that see
 //                    them; a thread owns a key and adds 2^(s - m') over the
 //                    rows, m' = m + log2 l of each row from shared memory
-// so that neither a maximum nor a sum crosses threads.  Warps 0-3 hold one
-// fixed row per thread (a TMEM lane) and take the even chunks, warps 4-7 the
-// odd ones (so a set, a stage and a TMEM buffer go together), warp 8 issues
-// the MMAs (S[128 x 128] = fixed . streamed^T into one of two TMEM buffers),
-// warp 9 the TMA loads and, in the column sums, each row tile's m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times the G
-// heads, as one TMA box; rows past the sequence's queries are masked.
+// so that neither a maximum nor a sum crosses threads but for the joining of
+// the sets.  Warps 0-3 hold one fixed row per thread (a TMEM lane) and take the
+// even chunks, warps 4-7 the odd ones (so a set, a stage and a TMEM buffer go
+// together), warp 8 issues the MMAs (S[128 x 128] = fixed . streamed^T into one
+// of two TMEM buffers), warp 9 the TMA loads and, in the column sums, each row
+// tile's m'.  A query tile is whole tokens, tile_tokens = 128 / G of them times
+// the G heads, as one TMA box; rows past the sequence's queries are masked.
+// Two CTAs per SM (256 TMEM columns and about 110 KB of shared memory each).
 //
-// What bounds it is the exponentials, 16 per clock and SM: a 128 x 128 tile has
-// 16384 of them, 1024 cycles against 256 of MMA, and one prompt of 16K tokens
-// (32/8 heads, bf16) takes about 1030 per tile and pass: 1857 us.  Beside each
-// stand one packed half of a multiply-add and of an add (f32x2) and no
-// maximum: a row's reference is its first scores' and moves only when a sum
-// grows past 2^60.  4 prompts of 1..4K tokens take 267 us, where the
-// exponentials alone would take about 229; the rest is the CTAs' start and end
-// and the masked halves of diagonal tiles.  Measured and not taken: the fixed
-// operand in TMEM and the streamed tiles shared by two CTAs through TMA
-// multicast (1857 -> 1870..1880 us, 267 -> 286..288): the feeding of the MMA is
-// not what it waits for.
+// A CTA goes on with units of the grid that have not been launched (cluster
+// launch control): it starts up once, its next unit's loads run beside the last
+// chunks of this one, and the balance stays the hardware's.  A CTA per unit
+// instead: 4 prompts of 1..4K tokens 251 us against 231, 64 sequences x 32
+// queries, whose column sums have one chunk a unit, 283 against 187; units
+// dealt out in advance: 273..294 and 165; claimed at a unit's start and not
+// near its end: 290.
+//
+// No unit of the SM is busy more than about 55 % of a long prompt (one of 16K
+// tokens, 32/8 heads, bf16: 1669 us, 900 cycles per 128 x 128 tile): its
+// 16384 exponentials take 512 cycles at 32 per clock, its MMAs 512 (both
+// operands come from shared memory), its instructions about as many issue
+// slots, and the row warps wait for their own chains.  So each score costs one
+// packed half of a multiply-add and of an add (f32x2), and no maximum: a row's
+// reference is its first scores' and moves only when a sum grows past 2^60; the
+// scores are read 64 columns at a time and their buffer is free before they are
+// used.  Measured and not taken: the fixed operand in TMEM, streamed tiles
+// shared by two CTAs through TMA multicast (neither changed a long prompt, 286
+// to 288 us for the short ones), one CTA per SM with four stages, four sets and
+// two MMA and load warps (270), an eighth to a half of the exponentials as
+// polynomials on the FMA pipe (3 to 42 % slower).
 //
 // 8-bit pools: the row warps load the codes themselves, widen them to bf16
 // (exact: 8 significant bits hold every int8 and E4M3 code) and write them into
 // the swizzled image, the streamed keys two chunks ahead, right after the
 // scores of the chunk that used the stage before; a block's K scale multiplies
-// its scores (one prompt of 8K tokens, E4M3: 791 us).  Two CTAs per SM (256
-// TMEM columns and about 100 KB of shared memory each), so that one's start
-// and end overlap the other's work.
+// its scores (one prompt of 8K tokens, E4M3: 780 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -55,12 +65,16 @@ namespace {
 using namespace dev;
 
 constexpr int kTile = 128;                             // rows of either operand
-constexpr int kStages = 2;                             // = TMEM buffers
-constexpr int kRowWarps = 8;                           // two sets of four, by the chunk's parity
-constexpr int kSetWarps = kRowWarps / 2, kSetThreads = kSetWarps * 32;
+constexpr int kSets = 2;                               // sets of four row warps
+constexpr int kStages = kSets;                         // = TMEM buffers; chunk g of a CTA: number g % 2 of each
+constexpr int kRowWarps = 4 * kSets, kSetThreads = 128;
 constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1;
 constexpr int kThreads = (kRowWarps + 2) * 32;
-constexpr int kRowSlots = 8;                           // chunks whose rows' m' may be in use
+constexpr int kNotes = 8;                              // chunks whose notes (rows' m', bad blocks) may be in use
+constexpr int kClaimChunks = 3;                        // chunks left to load when the next unit is claimed
+constexpr int kClaims = 4;                             // claims whose answers may be in use
+constexpr int kUnits = 8;                              // units whose verdicts may be in use
+constexpr int kParts = 4;                              // units whose sets' results may be in use
 constexpr int kTmemCols = kStages * kTile;
 constexpr float kMoveSum = 0x1p60f;                    // a sum of 32 that moves a row's reference
 
@@ -69,8 +83,19 @@ struct PGeo {
   static constexpr int kBands = D / 64;
   static constexpr int kImage = kTile * D * 2;         // bytes of 128 rows
   static constexpr int kUsed = (1 + kStages) * kImage + 1024;
-  // at least 100 KB, so that no more than two CTAs (512 TMEM columns) share an SM
-  static constexpr int kSmemBytes = kUsed > 100 * 1024 ? kUsed : 100 * 1024;
+  // at least 80 KB, so that no more than two CTAs (512 TMEM columns) share an SM
+  static constexpr int kSmemBytes = kUsed > 80 * 1024 ? kUsed : 80 * 1024;
+};
+
+// One unit of a CTA's work: a fixed tile and the chunks streamed past it.
+struct Unit {
+  int hk, b, q0, n, L;
+  int split;                 // row statistics: the key split
+  int i0, tn;                // row statistics: first query token of the fixed tile, its tokens
+  int k0, kend;              // keys: of the split, or of the fixed tile
+  int first_pos;             // row statistics: position of token i0
+  int rt0;                   // column sums: first row tile that sees a key
+  int nch;                   // chunks
 };
 
 __device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
@@ -267,75 +292,116 @@ struct Codes {
 template <int D, int BS, int kKind, bool kStats>
 __global__ void __launch_bounds__(kThreads, 2)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap q_map, const PromptArgs a) {
+                     const __grid_constant__ CUtensorMap q_map, const PromptArgs a, int tiles) {
   using P = PGeo<D>;
   constexpr bool kQ8 = kKind != KV_DTYPE_BF16;
   constexpr bool kWidenStream = kQ8 && kStats, kWidenFixed = kQ8 && !kStats;
   constexpr int kRead = kWidenStream ? 32 : 64;        // scores of a row in registers at a time
-  constexpr int kScaleSlots = 4;                       // chunks whose scales may be in use
+  constexpr int kScaleSlots = 2 * kSets;               // chunks whose scales may be in use
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t fixed_full, full[kStages], empty[kStages], s_full[kStages], buf_free[kStages],
-      stat_full[kRowSlots], drain_bar;
+  __shared__ uint64_t fixed_full, fixed_free, full[kStages], s_full[kStages], buf_free[kStages],
+      noted[kNotes], checked[kUnits], claim_full[kClaims], claim_free[kClaims], part_full[kParts], part_free[kParts], drain_bar, near_end;
+  __shared__ __align__(16) uint4 claim[kClaims];
   __shared__ uint32_t tmem_base;
-  __shared__ int sh_bad, sh_fail;
-  __shared__ __align__(16) float row_m[kStats ? 1 : kRowSlots][kTile];  // -m' of the row tiles' rows
-  __shared__ float half_part[kTile], half_ref[kTile];  // the odd chunks' results
+  __shared__ int sh_fail;
+  __shared__ __align__(16) float row_m[kStats ? 1 : kNotes][kTile];  // -m' of the row tiles' rows
+  __shared__ int unit_bad[kUnits];                     // a block or a row of the unit is bad
+  __shared__ float part_sum[kParts][kSets][kTile], part_ref[kStats ? kParts : 1][kSets][kTile];
+  __shared__ int part_bad[kParts][kRowWarps];
   __shared__ float blk_ks[kWidenStream ? kScaleSlots : 1][kTile / BS];  // K scales of the chunks' blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.x, b = blockIdx.y;
   const int G = a.num_q_heads / a.num_kv_heads, TT = a.tile_tokens;
-  int q0, n, L;
-  const bool ok_seq = prompt_rows(a, b, BS, &q0, &n, &L);
-  if (!ok_seq) {
-    if (kStats && blockIdx.z == 0 && tid == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
-    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  // The unit.  Row statistics: row tile (the last ones, with most keys, first)
-  // and key split; column sums: key tile.
-  const int split = kStats ? (int)(blockIdx.z % a.splits) : 0;
-  const int unit = kStats ? (int)((gridDim.z - 1 - blockIdx.z) / a.splits) : (int)blockIdx.z;
-  const int i0 = unit * TT;                            // first query token of the fixed tile
-  const int tn = min(TT, n - i0);                      // its tokens
-  const int k0 = kStats ? split * a.part_tokens : unit * kTile;  // first key
-  if (kStats ? tn <= 0 : (n == 0 || k0 >= L)) {
-    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  const int first_pos = L - n + i0;
-  const int kend = kStats ? min(first_pos + tn, k0 + a.part_tokens) : min(L, k0 + kTile);
-  const int rt0 = kStats ? 0 : max(0, k0 - (L - n)) / TT;        // first row tile that sees a key
-  const int nch = kStats ? max(0, (kend - k0 + kTile - 1) / kTile) : (n - 1) / TT + 1 - rt0;
-  // statistics of row 0 of the tile that starts at token i: [Hkv][T][G], so
-  // that a tile's rows lie together
-  auto stats_at = [&](int i) {
-    return a.stats + ((int64_t)hk * a.num_tokens + q0 + i) * G * a.splits * 2;
+  bool ok = true;
+
+  // Unit u is (KV head, sequence, tile), tiles slowest, those with most chunks
+  // first: the last row tiles of the row statistics, the first key tiles of the
+  // column sums.  There is a CTA for each in the grid; one that runs takes over
+  // CTAs that have not been launched yet (cluster launch control), so that it
+  // starts up once and loads the next unit beside the last chunks of this one.
+  const unsigned per_tile = (unsigned)(a.num_kv_heads * a.batch);
+  // The CTA's unit number k (> 0), claimed by the loading warp; false: no more.
+  auto claimed = [&](int k, unsigned& u) {
+    uint32_t yes, x;
+    asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%2];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+                 : "=r"(yes), "=r"(x) : "r"(smem_addr(&claim[(k - 1) % kClaims])) : "memory");
+    u = x;
+    return yes != 0;
   };
-  const int my_rows = kStats ? tn * G : 0;
-  if (kStats && nch == 0) {                            // no key of this split
-    if (tid < my_rows) {
-      float* o = stats_at(i0) + ((int64_t)tid * a.splits + split) * 2;
-      o[0] = -INFINITY;
-      o[1] = 0.0f;
+  auto next_unit = [&](int k, unsigned& u) {           // (a whole warp)
+    if (!warp_wait(smem_addr(&claim_full[(k - 1) % kClaims]), ((k - 1) / kClaims) & 1)) {
+      ok = false;
+      return false;
     }
-    return;
-  }
+    const bool yes = claimed(k, u);
+    __syncwarp();
+    if (warp < kRowWarps && lane == 0) mbar_arrive(smem_addr(&claim_free[(k - 1) % kClaims]));
+    return yes;
+  };
+  // False: nothing to stream past the tile (un.nch == 0).  A bad sequence is
+  // flagged by the loading warp.
+  auto locate = [&](unsigned u, Unit& un) {
+    un.nch = un.tn = 0;
+    if (u >= gridDim.x) return false;
+    const int z = (int)(u / per_tile), r = (int)(u % per_tile);
+    un.hk = r % a.num_kv_heads;
+    un.b = r / a.num_kv_heads;
+    if (!prompt_rows(a, un.b, BS, &un.q0, &un.n, &un.L)) {
+      if (kStats && z == 0 && warp == kLoadWarp && lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+      return false;
+    }
+    const int tile = kStats ? (tiles - 1 - z) / a.splits : z;
+    un.split = kStats ? (tiles - 1 - z) % a.splits : 0;
+    un.k0 = kStats ? un.split * a.part_tokens : tile * kTile;
+    if (kStats) {
+      if ((int64_t)tile * TT >= un.n) return false;
+      un.i0 = tile * TT;
+      un.tn = min(TT, un.n - un.i0);
+      un.first_pos = un.L - un.n + un.i0;
+      un.kend = min(un.first_pos + un.tn, un.k0 + a.part_tokens);
+      un.rt0 = 0;
+      un.nch = max(0, (un.kend - un.k0 + kTile - 1) / kTile);
+    } else {
+      if (un.n == 0 || un.k0 >= un.L) return false;
+      un.i0 = un.first_pos = 0;
+      un.kend = min(un.L, un.k0 + kTile);
+      un.rt0 = max(0, un.k0 - (un.L - un.n)) / TT;
+      un.nch = (un.n - 1) / TT + 1 - un.rt0;
+    }
+    return un.nch > 0;
+  };
+  // statistics of row 0 of the tile that starts at token i of the unit's
+  // sequence: [Hkv][T][G], so that a tile's rows lie together
+  auto stats_at = [&](const Unit& un, int i) {
+    return a.stats + ((int64_t)un.hk * a.num_tokens + un.q0 + i) * G * a.splits * 2;
+  };
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   unsigned char* gbase = smem_raw + (base - smem_addr(smem_raw));
   auto stage_img = [&](int s) { return base + (uint32_t)((1 + s) * P::kImage); };
   if (tid == 0) {
-    sh_bad = 0;
     sh_fail = 0;
-    mbar_init(smem_addr(&fixed_full), kWidenFixed ? kSetWarps : 1);
+    mbar_init(smem_addr(&fixed_full), kWidenFixed ? kSetThreads / 32 : 1);
+    mbar_init(smem_addr(&fixed_free), 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(&full[s]), kWidenStream ? kSetWarps : 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&full[s]), kWidenStream ? kSetThreads / 32 : 1);
       mbar_init(smem_addr(&s_full[s]), 1);
-      mbar_init(smem_addr(&buf_free[s]), kSetWarps);
+      mbar_init(smem_addr(&buf_free[s]), kSetThreads / 32);
     }
-    for (int s = 0; s < kRowSlots; ++s) mbar_init(smem_addr(&stat_full[s]), 1);
+    for (int s = 0; s < kNotes; ++s) mbar_init(smem_addr(&noted[s]), 1);
+    for (int s = 0; s < kUnits; ++s) mbar_init(smem_addr(&checked[s]), 1);
+    for (int s = 0; s < kClaims; ++s) {
+      mbar_init(smem_addr(&claim_full[s]), 1);
+      mbar_init(smem_addr(&claim_free[s]), kRowWarps + 1);
+    }
+    for (int s = 0; s < kParts; ++s) {
+      mbar_init(smem_addr(&part_full[s]), kRowWarps);
+      mbar_init(smem_addr(&part_free[s]), kSetThreads / 32);
+    }
     mbar_init(smem_addr(&drain_bar), 1);
+    mbar_init(smem_addr(&near_end), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -348,32 +414,33 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   if (kStats) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = tmem_base;
-  const int32_t* bt = a.block_tables + (int64_t)b * a.max_blocks;
 
-  RowStats st = {-INFINITY, 0.0f};
-  float acc = 0.0f;
-
+  // Every role walks the same units and counts the same chunks: g of them
+  // before the unit, us units with chunks before it.
+  Unit un = {};
+  int g = 0, us = 0;
+  unsigned u = blockIdx.x;
   if (warp == kLoadWarp) {
-    // ======================= loads (TMA) ====================================
+    // ======================= loads (TMA) and notes ==========================
+    const int32_t* bt = nullptr;
     // Keys [from, from + 128) (up to L) into an image, one block per lane: its
     // table entry, read ahead of the wait for the image, then the load.
     auto entry = [&](int from) {
-      return lane < min(kTile / BS, (L - from + BS - 1) / BS) ? bt[from / BS + lane] : 0;
+      return lane < min(kTile / BS, (un.L - from + BS - 1) / BS) ? bt[from / BS + lane] : 0;
     };
+    // False when a key's block is outside the pool.
     auto load_k = [&](uint32_t img, uint64_t* bar, int from, int p) {
-      const int nb = min(kTile / BS, (L - from + BS - 1) / BS);
-      if (p < 0 || p >= a.num_blocks) {
-        sh_bad = 1;
-        p = 0;
-      }
+      const int nb = min(kTile / BS, (un.L - from + BS - 1) / BS);
+      const bool in = p >= 0 && p < a.num_blocks;
       if (lane == 0) mbar_expect_tx(smem_addr(bar), (uint32_t)(nb * BS * D * 2));
       __syncwarp();
       if (lane < nb) {
 #pragma unroll
         for (int x = 0; x < P::kBands; ++x)
-          tma_load_4d(img + x * (kTile * 128) + lane * (BS * 128), &k_map, smem_addr(bar), x * 64, hk, 0, p);
+          tma_load_4d(img + x * (kTile * 128) + lane * (BS * 128), &k_map, smem_addr(bar), x * 64, un.hk, 0,
+                      in ? p : 0);
       }
-      __syncwarp();
+      return __all_sync(0xffffffffu, in);
     };
     // The row tile that starts at query token i (whole boxes; rows past the
     // tensor are zeros).
@@ -382,60 +449,120 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_expect_tx(smem_addr(bar), (uint32_t)(TT * G * D * 2));
 #pragma unroll
         for (int x = 0; x < P::kBands; ++x)
-          tma_load_3d(img + x * (kTile * 128), &q_map, smem_addr(bar), x * 64, hk * G, q0 + i);
+          tma_load_3d(img + x * (kTile * 128), &q_map, smem_addr(bar), x * 64, un.hk * G, un.q0 + i);
       }
       __syncwarp();
     };
-    if (kStats) load_q(base, &fixed_full, i0);
-    else if (!kQ8) load_k(base, &fixed_full, k0, entry(k0));
-    // column sums: m' of the rows of chunk c's row tile
-    [[maybe_unused]] float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto fetch = [&](int c) {
-      const int i = (rt0 + c) * TT, rows = min(TT, n - i) * G;
-      const float* st_row = stats_at(i);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = u * 32 + lane;
-        m[u] = r < rows ? st_row[(int64_t)r * a.splits * 2] : 0.0f;
+    bool first = true;
+    int fixed_issued = 0, issued = 0, last_claim = 0;
+    bool have = true;
+    for (int nth = 0; have; have = ok && next_unit(++nth, u)) {
+      // claim unit nth + 1
+      auto claim_next = [&] {
+        const int slot = nth % kClaims, turn = nth / kClaims;
+        if (turn > 0 && !warp_wait(smem_addr(&claim_free[slot]), (turn - 1) & 1)) return false;
+        if (lane == 0) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_expect_tx(smem_addr(&claim_full[slot]), 16);
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                       ::"r"(smem_addr(&claim[slot])), "r"(smem_addr(&claim_full[slot])) : "memory");
+        }
+        __syncwarp();
+        last_claim = nth + 1;
+        return true;
+      };
+      if (!locate(u, un)) {
+        ok = claim_next();
+        continue;
       }
-    };
-    int issued = 0;
-    bool ok = true, bad = false;
-    [[maybe_unused]] int next = kStats && !kWidenStream ? entry(k0) : 0;
-    for (int c = 0; c < (kWidenStream ? 0 : nch); ++c) {
-      const int s = c % kStages;
-      if (c >= kStages && !warp_wait(smem_addr(&empty[s]), ((c / kStages) - 1) & 1)) {
+      // Late, when few chunks remain: a unit claimed early would be out of reach
+      // of CTAs that finish sooner.
+      const int claim_at = max(0, un.nch - kClaimChunks);
+      bt = a.block_tables + (int64_t)un.b * a.max_blocks;
+      bool good = true;
+      int next = kStats && !kWidenStream ? entry(un.k0) : 0;
+      const int p = kStats || kWidenFixed ? 0 : entry(un.k0);
+      // the fixed tile, once the last unit's MMAs are done (behind the unit's
+      // first chunk, whose stage is free before)
+      auto load_fixed = [&] {
+        if (kWidenFixed) return true;
+        if (us >= 1 && !warp_wait(smem_addr(&fixed_free), (us - 1) & 1)) return false;
+        if (kStats) load_q(base, &fixed_full, un.i0);
+        else good = load_k(base, &fixed_full, un.k0, p);
+        fixed_issued = us + 1;
+        return true;
+      };
+      if (kWidenStream && (!load_fixed() || !warp_wait(smem_addr(&near_end), us & 1) || !claim_next())) {
         ok = false;
         break;
       }
-      if (kStats) {
-        load_k(stage_img(s), &full[s], k0 + c * kTile, next);
-        next = entry(k0 + (c + 1) * kTile);
-      }
-      if (!kStats) load_q(stage_img(s), &full[s], (rt0 + c) * TT);
-      issued = c + 1;
-      if constexpr (!kStats) {
-        if (c == 0) {
-          // The kernel may start beside the last CTAs of the one before it (a
-          // programmatic dependent); from here on that one has ended.
-          asm volatile("griddepcontrol.wait;" ::: "memory");
-          fetch(0);
-        }
-        // (the MMA of chunk c - 2 is done, so chunk c - 4's scores were read, and
-        // before them chunk c - 6 was finished: its slot and barrier phase are free)
+      // column sums: m' of the rows of chunk c's row tile
+      [[maybe_unused]] float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto fetch = [&](int c) {
+        const int i = (un.rt0 + c) * TT, rows = min(TT, un.n - i) * G;
+        const float* st_row = stats_at(un, i);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          bad |= m[u] == -INFINITY;                    // a row without statistics
-          row_m[c % kRowSlots][u * 32 + lane] = -m[u];
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * 32 + lane;
+          m[k] = r < rows ? st_row[(int64_t)r * a.splits * 2] : 0.0f;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&stat_full[c % kRowSlots]));
-        if (c + 1 < nch) fetch(c + 1);
+      };
+      for (int c = 0; c < (kWidenStream ? 0 : un.nch); ++c) {
+        const int gc = g + c, s = gc % kStages, note = gc % kNotes;
+        if (gc >= kStages && !warp_wait(smem_addr(&s_full[s]), ((gc / kStages) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        if (kStats) {
+          good &= load_k(stage_img(s), &full[s], un.k0 + c * kTile, next);
+          next = entry(un.k0 + (c + 1) * kTile);
+        } else {
+          load_q(stage_img(s), &full[s], (un.rt0 + c) * TT);
+        }
+        issued = gc + 1;
+        if ((c == 0 && !load_fixed()) || (c == claim_at && !claim_next())) {
+          ok = false;
+          break;
+        }
+        // (the MMA of chunk gc - 2 is done, so chunk gc - 4's scores were read,
+        // and before them chunk gc - 6 was finished: its note's slot and the
+        // slot's barrier phase are free)
+        if constexpr (!kStats) {
+          if (first) {
+            // The kernel may start beside the last CTAs of the one before it (a
+            // programmatic dependent); from here on that one has ended.
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            first = false;
+          }
+          if (c == 0) fetch(0);
+          bool lost = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            lost |= m[k] == -INFINITY;                 // a row without statistics
+            row_m[note][k * 32 + lane] = -m[k];
+          }
+          good &= !__any_sync(0xffffffffu, lost);
+        }
+        if constexpr (!kStats) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&noted[note]));
+          if (c + 1 < un.nch) fetch(c + 1);
+        }
       }
+      // (the chunk 6 before the last one is finished, so a unit that ended there
+      // was joined: eight slots do)
+      if (lane == 0) {
+        unit_bad[us % kUnits] = !good;
+        mbar_arrive(smem_addr(&checked[us % kUnits]));
+      }
+      __syncwarp();
+      g += un.nch;
+      ++us;
     }
-    if (bad) sh_bad = 1;
-    // every load has landed before the CTA ends (bounded; normally it has)
-    if (!kWidenFixed && !warp_wait(smem_addr(&fixed_full), 0)) ok = false;
+    if (!kStats && first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // every load and claim has landed before the CTA ends (bounded; normally it has)
+    if (last_claim > 0 && !warp_wait(smem_addr(&claim_full[(last_claim - 1) % kClaims]), ((last_claim - 1) / kClaims) & 1)) ok = false;
+    if (fixed_issued > 0 && !warp_wait(smem_addr(&fixed_full), (fixed_issued - 1) & 1)) ok = false;
     for (int s = 0; s < kStages && s < issued; ++s) {
       const int last = s + kStages * ((issued - 1 - s) / kStages);
       if (!warp_wait(smem_addr(&full[s]), (last / kStages) & 1)) ok = false;
@@ -445,21 +572,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ======================= tensor-core issue (one lane) ===================
     if (lane == 0) {
       const uint32_t idesc = mma_idesc<false>(kTile, kTile, 0);
-      bool ok = mbar_wait(smem_addr(&fixed_full), 0);
-      for (int c = 0; c < nch && ok; ++c) {
-        const int s = c % kStages, ph = (c / kStages) & 1;
-        ok = mbar_wait(smem_addr(&full[s]), ph) &&
-             (c < kStages || mbar_wait(smem_addr(&buf_free[s]), ph ^ 1));
-        if (!ok) break;
-        tc_fence_after();
+      bool have = true;
+      for (int nth = 0; have;) {
+        if (locate(u, un)) {
+          ok = mbar_wait(smem_addr(&fixed_full), us & 1);
+          for (int c = 0; c < un.nch && ok; ++c) {
+            const int gc = g + c, s = gc % kStages, ph = (gc / kStages) & 1;
+            ok = mbar_wait(smem_addr(&full[s]), ph) &&
+                 (gc < kStages || mbar_wait(smem_addr(&buf_free[s]), ph ^ 1));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * (kTile * 128) + (ks % 4) * 32;
-          mma_ss(tm + s * kTile, smem_desc(base + off, 16, 1024), smem_desc(stage_img(s) + off, 16, 1024),
-                 idesc, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * (kTile * 128) + (ks % 4) * 32;
+              mma_ss(tm + s * kTile, smem_desc(base + off, 16, 1024), smem_desc(stage_img(s) + off, 16, 1024),
+                     idesc, ks > 0);
+            }
+            mma_commit(smem_addr(&s_full[s]));
+          }
+          if (ok) mma_commit(smem_addr(&fixed_free));
+          g += un.nch;
+          ++us;
         }
-        mma_commit(smem_addr(&s_full[s]));
-        mma_commit(smem_addr(&empty[s]));
+        ++nth;
+        ok = ok && mbar_wait(smem_addr(&claim_full[(nth - 1) % kClaims]), ((nth - 1) / kClaims) & 1);
+        have = ok && claimed(nth, u);
+        if (ok) mbar_arrive(smem_addr(&claim_free[(nth - 1) % kClaims]));
       }
       if (!ok) sh_fail = 1;
       // the tensor core is done with shared memory and TMEM before they go
@@ -469,137 +607,183 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // ======================= one fixed row per thread =======================
-    bool ok = true;
-    const int row = tid & (kTile - 1), set = warp / kSetWarps;
-    const int key = k0 + row;                          // column sums
-    const int pos = kStats && row < my_rows ? first_pos + row / G : -1;
-    // a warp whose rows are all padding only keeps the barriers' phases
-    const int row_lo = (warp % kSetWarps) * 32;
-    const bool live = kStats ? row_lo < my_rows : k0 + row_lo < kend;
-    float sl2 = a.scale_log2;
+    const int row = tid % kSetThreads, set = warp / 4, row_lo = (warp % 4) * 32;
     const uint32_t scores = tm + ((uint32_t)row_lo << 16) + set * kTile;
     [[maybe_unused]] Codes<D, BS, kQ8 ? kKind : KV_DTYPE_INT8> codes;
-    // K scales of the blocks of a chunk that this set widens
-    auto put_scales = [&](int c) {
-      const int j = row, from = k0 + c * kTile + j * BS;
-      if (j < kTile / BS) {
-        const int p = from < L ? bt[from / BS] : -1;
-        blk_ks[c & (kScaleSlots - 1)][j] =
-            p >= 0 && p < a.num_blocks ? a.k_scale[(int64_t)p * a.num_kv_heads + hk] : 0.0f;
+    bool have = true;
+    for (int nth = 0; have; have = ok && next_unit(++nth, u)) {
+      const bool any = locate(u, un);
+      const int my_rows = un.tn * G;                   // row statistics: rows of the tile
+      if (!any) {
+        if (kStats && set == 0 && row < my_rows) {     // no key of this split
+          float* o = stats_at(un, un.i0) + ((int64_t)row * a.splits + un.split) * 2;
+          o[0] = -INFINITY;
+          o[1] = 0.0f;
+        }
+        continue;
       }
-    };
-    if constexpr (kWidenFixed) {
-      if (set == 0) {
-        bool all = codes.load(a, bt, hk, k0, L, 0);
-        all &= codes.finish(a, bt, hk, k0, L, gbase);
-        if (!all) sh_bad = 1;
+      const int32_t* bt = a.block_tables + (int64_t)un.b * a.max_blocks;
+      RowStats st = {-INFINITY, 0.0f};
+      float acc = 0.0f;
+      bool bad = false;
+      const int key = un.k0 + row;                     // column sums
+      const int pos = kStats && row < my_rows ? un.first_pos + row / G : -1;
+      // a warp whose rows are all padding only keeps the barriers' phases
+      const bool live = kStats ? row_lo < my_rows : un.k0 + row_lo < un.kend;
+      float sl2 = a.scale_log2;
+      if constexpr (kWidenFixed) {
+        if (set == us % kSets) {
+          bad = !codes.load(a, bt, un.hk, un.k0, un.L, 0);
+          if (us >= 1 && !warp_wait(smem_addr(&fixed_free), (us - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          bad |= !codes.finish(a, bt, un.hk, un.k0, un.L, gbase);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&fixed_full));
+        }
+        if (key < un.kend) {
+          const int p = bt[key / BS];
+          if (p >= 0 && p < a.num_blocks) sl2 *= a.k_scale[(int64_t)p * a.num_kv_heads + un.hk];
+        }
+      }
+      // chunk c of this set into its stage (the set has waited for the MMA of
+      // the chunk before), once part 0 of its codes is held, and the K scales
+      // of its blocks
+      auto put_chunk = [&](int c) {
+        const int from = un.k0 + c * kTile + row * BS;
+        if (row < kTile / BS) {
+          const int p = from < un.L ? bt[from / BS] : -1;
+          blk_ks[(g + c) % kScaleSlots][row] =
+              p >= 0 && p < a.num_blocks ? a.k_scale[(int64_t)p * a.num_kv_heads + un.hk] : 0.0f;
+        }
+        bad |= !codes.finish(a, bt, un.hk, un.k0 + c * kTile, un.L, gbase + (1 + set) * P::kImage);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&fixed_full));
-      }
-      if (key < kend) {
-        const int p = bt[key / BS];
-        if (p >= 0 && p < a.num_blocks) sl2 *= a.k_scale[(int64_t)p * a.num_kv_heads + hk];
-      }
-    }
-    // chunk c of this set into its stage, once part 0 of its codes is held
-    auto put_chunk = [&](int c) {
-      put_scales(c);
-      if (!codes.finish(a, bt, hk, k0 + c * kTile, L, gbase + (1 + set) * P::kImage)) sh_bad = 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&full[set]));
-    };
-    if constexpr (kWidenStream) {
-      if (set < nch) {
-        if (!codes.load(a, bt, hk, k0 + set * kTile, L, 0)) sh_bad = 1;
-        put_chunk(set);
-      }
-    }
-    for (int c = set; c < nch; c += kStages) {
+        if (lane == 0) mbar_arrive(smem_addr(&full[set]));
+      };
+      const int c_first = (set - g) & (kSets - 1);     // the set's first chunk of the unit
       if constexpr (kWidenStream) {
-        if (c + kStages < nch && !codes.load(a, bt, hk, k0 + (c + kStages) * kTile, L, 0)) sh_bad = 1;
+        if (c_first < un.nch) {
+          bad |= !codes.load(a, bt, un.hk, un.k0 + c_first * kTile, un.L, 0);
+          put_chunk(c_first);
+        }
       }
-      const int ph = (c / kStages) & 1;
-      if (!warp_wait(smem_addr(&s_full[set]), ph) ||
-          (!kStats && !warp_wait(smem_addr(&stat_full[c % kRowSlots]), (c / kRowSlots) & 1)) ||
-          (kWidenStream && !warp_wait(smem_addr(&full[set]), ph))) {  // (the other warps' scales)
+      for (int c = c_first; c < un.nch; c += kSets) {
+        const bool more = kWidenStream && c + kSets < un.nch;
+        if constexpr (kWidenStream) {
+          if (more) bad |= !codes.load(a, bt, un.hk, un.k0 + (c + kSets) * kTile, un.L, 0);
+        }
+        const int gc = g + c, ph = (gc / kStages) & 1, note = gc % kNotes;
+        if (!warp_wait(smem_addr(&s_full[set]), ph) ||
+            (kWidenStream && !warp_wait(smem_addr(&full[set]), ph)) ||  // (the other warps' scales)
+            (!kStats && !warp_wait(smem_addr(&noted[note]), (gc / kNotes) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int c0 = un.k0 + c * kTile;              // row statistics: the chunk's first key
+        const int i = (un.rt0 + c) * TT;               // column sums: the tile's first token
+        const int cols = kStats ? kTile : min(TT, un.n - i) * G;
+        auto free_buf = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&buf_free[set]));
+        };
+        if (live) {
+          const bool whole = kStats ? c0 + kTile - 1 <= un.first_pos
+                                    : cols == kTile && un.L - un.n + i >= un.k0 + kTile - 1;
+          const int from = max(0, key - (un.L - un.n + i)) * G;  // column sums: rows [from, cols) see the key
+#pragma unroll
+          for (int at = 0; at < kTile; at += kRead) {
+            if (at >= cols) break;
+            uint32_t x[kRead];
+            __syncwarp();                              // (the TMEM loads are the whole warp's)
+            if constexpr (kRead == 64) tmem_read64(scores + at, x);
+            else tmem_read32(scores + at, x);
+            if (at + kRead >= cols) free_buf();        // the buffer's last scores are in registers
+#pragma unroll
+            for (int h = 0; h < kRead; h += 32) {
+              if constexpr (kStats) {
+                if constexpr (kWidenStream) {
+                  const float* ks = blk_ks[gc % kScaleSlots];
+                  scale_scores(x + h, ks[(at + h) / BS], ks[(at + h + 16) / BS]);
+                }
+                add_scores(st, x + h, sl2, whole, pos - c0 - at - h);
+              } else {
+                const float* m = row_m[note] + at + h;
+                acc += whole ? column_part<false>(x + h, sl2, m, 0, 32)
+                             : column_part<true>(x + h, sl2, m, from - at - h, cols - at - h);
+              }
+            }
+          }
+        } else {
+          free_buf();
+        }
+        if constexpr (kWidenStream) {
+          if (more) put_chunk(c + kSets);
+          // (the loading warp claims the next unit)
+          if (c == max(0, un.nch - kClaimChunks) && warp % 4 == 0 && lane == 0) mbar_arrive(smem_addr(&near_end));
+        }
+      }
+      if (!ok) break;
+      // The sets' results of the unit; the set of its last chunk joins them.
+      const int slot = us % kParts, turn = us / kParts;
+      if (turn > 0 && !warp_wait(smem_addr(&part_free[slot]), (turn - 1) & 1)) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      const int c0 = k0 + c * kTile;                   // row statistics: the chunk's first key
-      const int i = (rt0 + c) * TT;                    // column sums: the tile's first token
-      const int cols = kStats ? kTile : min(TT, n - i) * G;
-      auto free_buf = [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&buf_free[set]));
-      };
-      if (live) {
-        const bool whole = kStats ? c0 + kTile - 1 <= first_pos
-                                  : cols == kTile && L - n + i >= k0 + kTile - 1;
-        const int from = max(0, key - (L - n + i)) * G;  // column sums: the rows [from, cols) see the key
-#pragma unroll
-        for (int at = 0; at < kTile; at += kRead) {
-          if (at >= cols) break;
-          uint32_t x[kRead];
-          __syncwarp();                                // (the TMEM loads are the whole warp's)
-          if constexpr (kRead == 64) tmem_read64(scores + at, x);
-          else tmem_read32(scores + at, x);
-          if (at + kRead >= cols) free_buf();          // the buffer's last scores are in registers
-#pragma unroll
-          for (int h = 0; h < kRead; h += 32) {
-            if constexpr (kStats) {
-              if constexpr (kWidenStream) {
-                const float* ks = blk_ks[c & (kScaleSlots - 1)];
-                scale_scores(x + h, ks[(at + h) / BS], ks[(at + h + 16) / BS]);
-              }
-              add_scores(st, x + h, sl2, whole, pos - c0 - at - h);
-            } else {
-              const float* m = row_m[c % kRowSlots] + at + h;
-              acc += whole ? column_part<false>(x + h, sl2, m, 0, 32)
-                           : column_part<true>(x + h, sl2, m, from - at - h, cols - at - h);
-            }
-          }
+      part_sum[slot][set][row] = kStats ? st.l : acc;
+      if constexpr (kStats) part_ref[slot][set][row] = st.ref;
+      const bool warp_bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) part_bad[slot][warp] = warp_bad;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&part_full[slot]));
+      if (set == (g + un.nch - 1) % kSets) {
+        if (!warp_wait(smem_addr(&part_full[slot]), turn & 1) ||
+            !warp_wait(smem_addr(&checked[us % kUnits]), (us / kUnits) & 1)) {
+          ok = false;
+          break;
         }
+        const bool lost = unit_bad[us % kUnits] != 0 ||
+                          __any_sync(0xffffffffu, lane < kRowWarps && part_bad[slot][lane % kRowWarps] != 0);
+        if constexpr (kStats) {
+          if (lost && row == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
+          if (row < my_rows) {
+            float M = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int t = 0; t < kSets; ++t) M = fmaxf(M, part_ref[slot][t][row]);
+#pragma unroll
+            for (int t = 0; t < kSets; ++t) {
+              const float r = part_ref[slot][t][row], p = part_sum[slot][t][row];
+              if (r > -INFINITY || p != p) l = fmaf(p, ex2(r - M), l);
+            }
+            float* o = stats_at(un, un.i0) + ((int64_t)row * a.splits + un.split) * 2;
+            // one split: m' at once (-inf: no statistics, the weights stay as
+            // they are; a row whose every score is -inf has NaN weights)
+            o[0] = a.splits > 1 ? M : (lost ? -INFINITY : row_log_sum(M, l));
+            o[1] = lost ? -1.0f : l;
+          }
+        } else if (!lost && key < un.kend) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int t = 0; t < kSets; ++t) sum += part_sum[slot][t][row];
+          float* w = a.weights + ((int64_t)un.b * a.num_kv_heads + un.hk) * a.stride + key;
+          *w = a.accumulate && key < un.L - un.n ? *w + sum : sum;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&part_free[slot]));
       }
-      if (!live) free_buf();
-      if constexpr (kWidenStream) {
-        // the scores of chunk c are complete, so its stage is free
-        if (c + kStages < nch) put_chunk(c + kStages);
-      }
+      g += un.nch;
+      ++us;
     }
     if (!ok && lane == 0) sh_fail = 1;
-    if (set == 1) {
-      half_part[row] = kStats ? st.l : acc;
-      half_ref[row] = st.ref;
-    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmemCols) : "memory");
-  const bool failed = sh_fail != 0;
-  if (tid == 0 && failed) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
-  if constexpr (kStats) {
-    if (tid == 0 && sh_bad) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
-    if (tid < my_rows) {
-      const float r1 = half_ref[tid], M = fmaxf(st.ref, r1);
-      float l = 0.0f;
-      if (st.ref > -INFINITY || st.l != st.l) l = st.l * ex2(st.ref - M);
-      if (r1 > -INFINITY || half_part[tid] != half_part[tid]) l = fmaf(half_part[tid], ex2(r1 - M), l);
-      const bool lost = failed || sh_bad;
-      float* o = stats_at(i0) + ((int64_t)tid * a.splits + split) * 2;
-      // one split: m' at once (-inf: no statistics, the weights stay as they
-      // are; a row whose every score is -inf has NaN weights)
-      o[0] = a.splits > 1 ? M : (lost ? -INFINITY : row_log_sum(M, l));
-      o[1] = lost ? -1.0f : l;
-    }
-  } else if (!failed && !sh_bad && tid < kend - k0) {
-    acc += half_part[tid];
-    float* w = a.weights + ((int64_t)b * a.num_kv_heads + hk) * a.stride + k0 + tid;
-    *w = a.accumulate && k0 + tid < L - n ? *w + acc : acc;
-  }
+  if (tid == 0 && sh_fail) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
 }
 
 // Row statistics of several key splits: m' of a row into its first entry.
@@ -619,13 +803,14 @@ __global__ void __launch_bounds__(256) join_stats_kernel(float* stats, int64_t r
 }
 
 template <int D, int BS, int kKind, bool kStats>
-kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, unsigned z,
+kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles,
                       cudaStream_t s) {
   static std::mutex mu;
   static bool attr_set[64] = {};
-  int dev = 0;
-  kv_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  DeviceInfo di;
+  kv_status st = device_info(&di);
   if (st != KV_OK) return st;
+  const int dev = di.device;
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
@@ -637,7 +822,9 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.num_kv_heads, (unsigned)a.batch, z);
+  const int64_t units = (int64_t)a.num_kv_heads * a.batch * tiles;
+  if (units > 0x7fff0000LL) return fail(KV_ERR_INVALID_ARG, "pagedkv_attention_weights: too many row or key tiles");
+  cfg.gridDim = dim3((unsigned)units);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = PGeo<D>::kSmemBytes;
   cfg.stream = s;
@@ -647,13 +834,13 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kStats ? 0 : 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, prompt_tc_kernel<D, BS, kKind, kStats>, km, qm, a),
+  return cuda_check(cudaLaunchKernelEx(&cfg, prompt_tc_kernel<D, BS, kKind, kStats>, km, qm, a, tiles),
                     "prompt_tc_kernel launch");
 }
 
 template <int D, int BS, int kKind>
 kv_status launch_tc_kind(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles, cudaStream_t s) {
-  kv_status st = launch_tc_t<D, BS, kKind, true>(a, km, qm, (unsigned)(tiles * a.splits), s);
+  kv_status st = launch_tc_t<D, BS, kKind, true>(a, km, qm, tiles * a.splits, s);
   if (st != KV_OK) return st;
   if (a.splits > 1) {
     const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
@@ -662,7 +849,7 @@ kv_status launch_tc_kind(const PromptArgs& a, const CUtensorMap& km, const CUten
     join_stats_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.stats, rows, a.splits);
     if ((st = cuda_check(cudaGetLastError(), "join_stats_kernel launch")) != KV_OK) return st;
   }
-  return launch_tc_t<D, BS, kKind, false>(a, km, qm, (unsigned)((a.max_seq_len - 1) / kTile + 1), s);
+  return launch_tc_t<D, BS, kKind, false>(a, km, qm, (a.max_seq_len - 1) / kTile + 1, s);
 }
 
 template <int D, int BS>
