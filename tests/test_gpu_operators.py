@@ -274,6 +274,68 @@ def test_prompt_weights_of_one_token_are_the_decode_step(pkv):
     within(b, want, tol)
 
 
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 128), ("int8", 64), ("fp8", 128)])
+def test_prompt_weights_many_units(pkv, dtype, dim):
+    """More units of work (row tiles, key tiles) than CTAs fit the GPU several
+    times over, ragged, some empty; bad sequences among them change nothing."""
+    B, hkv, G = 48, 8, 2
+    L = [(37 * b * b + 11 * b) % 690 + 1 for b in range(B)]
+    counts = [min(n, (b * 29) % 83) for b, n in enumerate(L)]
+    counts[5] = min(L[5], 82)
+    good, pool = (ref.Pool(L, hkv, dim, 16, dtype, seed=21) for _ in range(2))
+    q = pool.randn(sum(counts), hkv * G, dim, scale=2.0)
+    weights = torch.rand((B, hkv, 700), generator=pool.g)
+    block = next(b for b in range(20, B) if L[b] > 200 and counts[b] > 40)
+    pool.tables[block, 3] = pool.k.shape[0]                   # outside the pool
+    length = next(b for b in range(block + 1, B) if counts[b] > 40)
+    pool.seq_lens[length] = 16 * pool.tables.shape[1] + 1     # past the table
+    w = prompt_weights(pkv, pool, q, counts, weights, dim ** -0.5, max_len=700)
+    assert pkv.get_status()[1] == pkv.FLAG_BAD_SEQ_LEN | pkv.FLAG_BAD_BLOCK
+    want, tol = ref.prompt_weights(good, q, counts, weights, dim ** -0.5)
+    for b, n in enumerate(L):
+        if b in (block, length):
+            assert same_bits(w[b], weights[b])
+            continue
+        within(w[b, :, :n], want[b, :, :n], tol[b, :, :n])
+        assert same_bits(w[b, :, n:], weights[b, :, n:])
+
+
+def test_prompt_weights_on_two_streams_and_in_a_graph(pkv):
+    """Calls that overlap on two streams, each with a workspace of its own, and
+    replays of a captured call give the bits of a call alone."""
+    L, counts = [900, 640, 333], [200, 90, 100]
+    pools = [ref.Pool(L, 4, 64, 16, "bf16", seed=s) for s in (1, 2)]
+    args = []
+    for pool in pools:
+        k, v, sc, bt, sl = pool.on()
+        q = pool.randn(sum(counts), 8, 64, scale=2.0).cuda()
+        qs = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+        ws = workspace(pkv.attention_weights_workspace_bytes(q.shape[0], 8, 900))
+        args.append((q, k, bt, sl, qs, 900, max(counts), 0.125, ws))
+    alone = []
+    for a in args:
+        w = torch.zeros((3, 4, 900), device="cuda")
+        pkv.attention_weights(w, *a)
+        alone.append(w.cpu())
+    ws = [torch.zeros((3, 4, 900), device="cuda") for _ in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for i in range(6):
+        for st, w, a in zip(streams, ws, args):
+            pkv.attention_weights(w, *a, accumulate=False, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    for w, want in zip(ws, alone):
+        assert same_bits(w.cpu(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.attention_weights(ws[0], *args[0], accumulate=False, stream=torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        ws[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(ws[0].cpu(), alone[0])
+
+
 def test_prompt_weights_bad_sequences(pkv):
     L = [40, 20, 50, 64, 64]
     counts = [4, 21, 5, 6, 6]                                # 21 > 20
