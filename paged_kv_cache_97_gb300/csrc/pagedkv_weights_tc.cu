@@ -66,6 +66,7 @@ using namespace dev;
 
 constexpr int kTile = 128;                             // rows of either operand
 constexpr int kSets = 2;                               // sets of four row warps
+static_assert(kSets == 2, "the sets' results are joined symmetrically");
 constexpr int kStages = kSets;                         // = TMEM buffers; chunk g of a CTA: number g % 2 of each
 constexpr int kRowWarps = 4 * kSets, kSetThreads = 128;
 constexpr int kMmaWarp = kRowWarps, kLoadWarp = kRowWarps + 1;
@@ -749,14 +750,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if constexpr (kStats) {
           if (lost && row == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
           if (row < my_rows) {
-            float M = -INFINITY, l = 0.0f;
-#pragma unroll
-            for (int t = 0; t < kSets; ++t) M = fmaxf(M, part_ref[slot][t][row]);
-#pragma unroll
-            for (int t = 0; t < kSets; ++t) {
-              const float r = part_ref[slot][t][row], p = part_sum[slot][t][row];
-              if (r > -INFINITY || p != p) l = fmaf(p, ex2(r - M), l);
-            }
+            // (which set had the even chunks depends on the CTA's earlier units:
+            // the join is the same with the two exchanged)
+            const float r0 = part_ref[slot][0][row], r1 = part_ref[slot][1][row];
+            const float p0 = part_sum[slot][0][row], p1 = part_sum[slot][1][row];
+            const float M = fmaxf(r0, r1);
+            const float l = __fadd_rn(r0 > -INFINITY || p0 != p0 ? __fmul_rn(p0, ex2(r0 - M)) : 0.0f,
+                                      r1 > -INFINITY || p1 != p1 ? __fmul_rn(p1, ex2(r1 - M)) : 0.0f);
             float* o = stats_at(un, un.i0) + ((int64_t)row * a.splits + un.split) * 2;
             // one split: m' at once (-inf: no statistics, the weights stay as
             // they are; a row whose every score is -inf has NaN weights)
@@ -764,9 +764,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[1] = lost ? -1.0f : l;
           }
         } else if (!lost && key < un.kend) {
-          float sum = 0.0f;
-#pragma unroll
-          for (int t = 0; t < kSets; ++t) sum += part_sum[slot][t][row];
+          const float sum = part_sum[slot][0][row] + part_sum[slot][1][row];
           float* w = a.weights + ((int64_t)un.b * a.num_kv_heads + un.hk) * a.stride + key;
           *w = a.accumulate && key < un.L - un.n ? *w + sum : sum;
         }

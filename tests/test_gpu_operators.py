@@ -300,6 +300,31 @@ def test_prompt_weights_many_units(pkv, dtype, dim):
         assert same_bits(w[b, :, n:], weights[b, :, n:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+def test_prompt_weights_repeat_bit_for_bit(pkv, dtype):
+    """Which CTA takes which unit differs from call to call; the bits do not."""
+    L = [(131 * b * b + 17 * b) % 1500 + 300 for b in range(24)]
+    pool = ref.Pool([max(L)], 8, 64, 16, dtype, seed=3)       # one context that all sequences share
+    k, v, sc, bt, sl = pool.on()
+    bt = bt.expand(len(L), -1).contiguous()
+    sl = torch.tensor(L, dtype=torch.int32, device="cuda")
+    q = pool.randn(sum(L), 16, 64, scale=2.0).cuda()
+    qs = torch.tensor(np.concatenate([[0], np.cumsum(L)]), dtype=torch.int32, device="cuda")
+    ws = workspace(pkv.attention_weights_workspace_bytes(sum(L), 16, max(L)))
+    first = None
+    for _ in range(8):
+        w = torch.zeros((len(L), 8, max(L)), device="cuda")
+        pkv.attention_weights(w, q, k, bt, sl, qs, max(L), max(L), 0.125, ws, k_scale=sc["k_scale"])
+        if first is None:
+            first = w.cpu()
+        assert same_bits(w.cpu(), first)
+    # Every query row's weights add up to one: an exponential is off by 2^-22
+    # and by its argument's rounding (|s - m'| < 2^7: 2^-18 by the product and
+    # the sum), the sums of up to 2048 positive terms by 2^-13 at most.
+    total = first.double().sum(dim=(1, 2))
+    assert torch.allclose(total, torch.tensor(L).double() * 16, rtol=2.0 ** -12)
+
+
 def test_prompt_weights_on_two_streams_and_in_a_graph(pkv):
     """Calls that overlap on two streams, each with a workspace of its own, and
     replays of a captured call give the bits of a call alone."""
