@@ -655,13 +655,15 @@ def paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_l
 # Self-scaling append, differential attention, eviction
 # --------------------------------------------------------------------------
 
-_dt = None                  # torch's dtypes by the names used below, resolved once
+_dt = _device = None        # torch's dtypes by the names used below, its current-device query; resolved once
 
 
 def _dtypes():
-    global _dt
+    global _dt, _device
     if _dt is None:
         import torch
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _device = _device if torch.cuda.is_available() else lambda: 0
         _dt = (torch.bfloat16, torch.int32, torch.float32,
                {torch.bfloat16: DTYPE_BF16, torch.int8: DTYPE_INT8, torch.float8_e4m3fn: DTYPE_FP8_E4M3})
     return _dt
@@ -669,9 +671,8 @@ def _dtypes():
 
 def _need_all(*specs):
     """Every (tensor, dtype, name, dimensions) is a contiguous tensor of that
-    type on the current device (the kernels run there)."""
-    import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    type on the current device (the kernels run there), which is returned."""
+    dev = _device()
     for t, dtype, name, ndim in specs:
         try:
             if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
@@ -680,6 +681,12 @@ def _need_all(*specs):
             pass
         _need(t, dtype, name, ndim)
         raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+    return dev
+
+
+def _stream_on(stream, dev):
+    """_stream(stream) for the current device `dev`."""
+    return _raw_stream(dev) if stream is None and _raw_stream else _stream(stream)
 
 
 def _pools(k_cache, v_cache, k_scale, v_scale, specs):
@@ -707,16 +714,15 @@ def _pools(k_cache, v_cache, k_scale, v_scale, specs):
     return dt
 
 
-def _space(workspace):
-    """(pointer, bytes) of a workspace tensor or None."""
+def _space(workspace, dev):
+    """(pointer, bytes) of a workspace tensor on device `dev`, or of None."""
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    import torch
-    if workspace.get_device() != torch.cuda.current_device():
-        raise ValueError(f"workspace must be on the current device, got {workspace.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        raise ValueError(f"workspace must be on the current device (cuda:{dev}), got {workspace.device}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def append_scaled(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
@@ -732,7 +738,7 @@ def append_scaled(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_le
     dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
     if query_start is not None:
         specs.append((query_start, i32, "query_start", 1))
-    _need_all(*specs)
+    dev = _need_all(*specs)
     if dt == DTYPE_BF16:
         raise TypeError("append_scaled writes 8-bit pools (torch.int8 or torch.float8_e4m3fn)")
     nb, bs, hkv, d = k_cache.shape
@@ -750,7 +756,7 @@ def append_scaled(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, seq_le
     st = load().pagedkv_append_scaled(
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), _ptr(query_start), B, T,
-        int(max_query_len), nb, bs, hkv, d, dt, _stream(stream))
+        int(max_query_len), nb, bs, hkv, d, dt, _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
 
@@ -773,7 +779,7 @@ def paged_diff_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens
     dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
     if norm_weight is not None:
         specs.append((norm_weight, f32, "norm_weight", 1))
-    _need_all(*specs)
+    dev = _need_all(*specs)
     nb, bs, pool_heads, d = k_cache.shape
     B, rows, dq = q.shape
     H = rows // 2
@@ -785,12 +791,12 @@ def paged_diff_attention_decode(out, q, k_cache, v_cache, block_tables, seq_lens
         raise ValueError("block_tables / seq_lens must have one row per sequence")
     if norm_weight is not None and norm_weight.shape[0] != 2 * d:
         raise ValueError("norm_weight must have 2 head_dim entries")
-    ws, ws_n = _space(workspace)
+    ws, ws_n = _space(workspace, dev)
     st = load().paged_diff_attention_decode(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
         _ptr(v_scale), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), B, H, pool_heads // 2, d, nb,
         bs, int(max_seq_len), float(scale), lam.data_ptr(), _ptr(norm_weight), float(eps), dt, ws, ws_n,
-        _stream(stream))
+        _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
     return out
@@ -810,7 +816,7 @@ def paged_attention_decode_weights(out, weights, q, k_cache, v_cache, block_tabl
     specs = [(out, bf16, "out", 3), (weights, f32, "weights", 3), (q, bf16, "q", 3),
              (block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1)]
     dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
-    _need_all(*specs)
+    dev = _need_all(*specs)
     nb, bs, hkv, d = k_cache.shape
     B, hq, dq = q.shape
     mb = block_tables.shape
@@ -819,11 +825,11 @@ def paged_attention_decode_weights(out, weights, q, k_cache, v_cache, block_tabl
     wb, wh, stride = weights.shape
     if wb != B or wh != hkv:
         raise ValueError("weights must be [batch, num_kv_heads, tokens]")
-    ws, ws_n = _space(workspace)
+    ws, ws_n = _space(workspace, dev)
     st = load().paged_attention_decode_weights(
         out.data_ptr(), weights.data_ptr(), stride, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), B, hq, hkv, d,
-        nb, bs, int(max_seq_len), float(scale), dt, ws, ws_n, _stream(stream))
+        nb, bs, int(max_seq_len), float(scale), dt, ws, ws_n, _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
     return out
@@ -843,7 +849,7 @@ def attention_weights(weights, q, k_cache, block_tables, seq_lens, query_start, 
     specs = [(weights, f32, "weights", 3), (q, bf16, "q", 3), (block_tables, i32, "block_tables", 2),
              (seq_lens, i32, "seq_lens", 1), (query_start, i32, "query_start", 1)]
     dt = _pools(k_cache, None, k_scale, None, specs)
-    _need_all(*specs)
+    dev = _need_all(*specs)
     nb, bs, hkv, d = k_cache.shape
     T, hq, dq = q.shape
     B = seq_lens.shape[0]
@@ -853,12 +859,12 @@ def attention_weights(weights, q, k_cache, block_tables, seq_lens, query_start, 
     wb, wh, stride = weights.shape
     if wb != B or wh != hkv:
         raise ValueError("weights must be [batch, num_kv_heads, tokens]")
-    ws, ws_n = _space(workspace)
+    ws, ws_n = _space(workspace, dev)
     st = load().pagedkv_attention_weights(
         weights.data_ptr(), stride, q.data_ptr(), k_cache.data_ptr(), _ptr(k_scale),
         block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), query_start.data_ptr(), B, T,
         int(max_query_len), hq, hkv, d, nb, bs, int(max_seq_len), float(scale), 1 if accumulate else 0,
-        dt, ws, ws_n, _stream(stream))
+        dt, ws, ws_n, _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
     return weights
@@ -870,7 +876,7 @@ def select_tokens(keep_idx, keep_len, weights, seq_lens, max_seq_len, recent, st
     ``keep_len`` (int32 [B]): the last ``recent`` tokens and the heaviest of
     the others, all when the sequence fits the budget."""
     _, i32, f32, _ = _dtypes()
-    _need_all((keep_idx, i32, "keep_idx", 3), (keep_len, i32, "keep_len", 1),
+    dev = _need_all((keep_idx, i32, "keep_idx", 3), (keep_len, i32, "keep_len", 1),
               (weights, f32, "weights", 3), (seq_lens, i32, "seq_lens", 1))
     B, hkv, budget = keep_idx.shape
     wb, wh, stride = weights.shape
@@ -880,7 +886,7 @@ def select_tokens(keep_idx, keep_len, weights, seq_lens, max_seq_len, recent, st
         raise ValueError("weights must be [batch, num_kv_heads, tokens]")
     st = load().pagedkv_select_tokens(keep_idx.data_ptr(), keep_len.data_ptr(), weights.data_ptr(),
                                       stride, seq_lens.data_ptr(), B, hkv, int(max_seq_len), budget,
-                                      int(recent), _stream(stream))
+                                      int(recent), _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
     return keep_idx, keep_len
@@ -901,7 +907,7 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
         specs.append((dst, i32, "dst_block_tables", 2))
     if weights is not None:
         specs.append((weights, f32, "weights", 3))
-    _need_all(*specs)
+    dev = _need_all(*specs)
     nb, bs, hkv, d = k_cache.shape
     B, kh, budget = keep_idx.shape
     mb, md = block_tables.shape, dst.shape
@@ -917,7 +923,7 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
     st = load().pagedkv_evict_tokens(
         k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), block_tables.data_ptr(),
         mb[1], dst.data_ptr(), md[1], seq_lens.data_ptr(), keep_idx.data_ptr(), keep_len.data_ptr(),
-        budget, _ptr(weights), stride, B, nb, bs, hkv, d, dt, _stream(stream))
+        budget, _ptr(weights), stride, B, nb, bs, hkv, d, dt, _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
 
