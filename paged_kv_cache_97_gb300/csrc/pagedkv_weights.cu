@@ -125,11 +125,12 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
 // piece p holds elements 8p .. 8p + 7.  8-bit codes become bf16, exactly
 // (|c| <= 127 and E4M3's 4 significant bits fit bf16's 8).
 //
-// These kernels serve what the tcgen05 ones do not: up to 64 rows on 8-bit
-// pools or past a cluster's TMEM, 33 to 64 rows, scales that are not positive,
-// groups of more than 128 heads.  64 sequences of 512..4096 tokens, 32/8 heads:
-// five queries on an int8 pool 232 us; the two reads of K and the issue of the
-// loads' and exponentials' instructions share the bound.
+// These kernels serve what the tcgen05 ones do not: 33 to 64 rows, up to 64 rows
+// past a cluster's TMEM, scales that are not positive, groups of more than 128
+// heads.  The two reads of K and the issue of the loads' and exponentials'
+// instructions share the bound: 64 sequences of 512..4096 tokens x five
+// queries, 32/8 heads, 189 us on a bf16 pool and 232 on int8 (one pass with the
+// scores in TMEM: 103 and 139).
 
 constexpr int kRowTile = 64;                           // rows of Q per tile
 constexpr int kNTiles = kRowTile / 8;
@@ -640,14 +641,13 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
   a.stats = static_cast<float*>(workspace);
   a.tile_tokens = (int)tile_tokens;
   cudaStream_t s = (cudaStream_t)stream;
-  // Few rows on a bf16 pool whose scores fit a cluster's TMEM: one pass over K
-  // (64 sequences of 512..4096 tokens, five queries each, 32/8 heads: two
-  // passes of the mma.sync kernels 189 us, one pass 103).
-  const int ctas = dtype == KV_DTYPE_BF16 && longest * G <= kFewRows
-                       ? few_rows_ctas(batch, num_kv_heads, max_seq_len, di.num_sms) : 0;
+  // Few rows whose scores fit a cluster's TMEM: one pass over K (64 sequences of
+  // 512..4096 tokens, five queries each, 32/8 heads: two passes of the mma.sync
+  // kernels 189 us, one pass 103; int8 232 and 139).
+  const int ctas = longest * G <= kFewRows ? few_rows_ctas(batch, num_kv_heads, max_seq_len, di.num_sms) : 0;
   if (ctas > 0) {
     a.tile_tokens = (int)(kFewRows / G);
-    return launch_prompt_few(a, head_dim, block_size, ctas, s);
+    return launch_prompt_few(a, head_dim, block_size, dtype, ctas, s);
   }
   if (tc) return launch_prompt_tc(a, head_dim, block_size, dtype, (int)tiles, s);
   if (head_dim == 128)

@@ -87,11 +87,12 @@ __device__ __forceinline__ float transpose_reduce(float (&v)[32], Op op) {
   return v[0];
 }
 
-template <int D, int BS>
+template <int D, int BS, int kKind>
 __global__ void __launch_bounds__(kThreads, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap q_map, const PromptArgs a) {
   using F = FGeo<D>;
+  constexpr bool kQ8 = kKind != KV_DTYPE_BF16;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t q_full, full[kStages], empty[kStages], s_full[kChunks], drain_bar;
   __shared__ uint32_t tmem_base;
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ float part[kKeyWarps][kRows];             // the warps' maxima, then sums
   __shared__ float cta_max[kRows], cta_sum[kRows];     // read by the cluster
   __shared__ __align__(16) float neg_m[kRows];         // -m'
+  __shared__ float key_scale[kQ8 ? kChunks : 1][kTile];  // 8-bit: a key's score scale, its thread's own
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     sh_fail = 0;
     mbar_init(smem_addr(&q_full), 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&full[s]), kQ8 ? 4 : 1);
       mbar_init(smem_addr(&empty[s]), 1);
     }
     for (int c = 0; c < kChunks; ++c) mbar_init(smem_addr(&s_full[c]), 1);
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     int issued = 0;
     bool ok = true;
-    for (int c = 0; c < nch; ++c) {
+    for (int c = 0; c < (kQ8 ? 0 : nch); ++c) {
       const int s = c % kStages, from = k0 + c * kTile;
       const int nb = min(kTile / BS, (L - from + BS - 1) / BS);
       int p = lane < nb ? bt[from / BS + lane] : 0;
@@ -224,8 +226,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_wait_ld32(x);
     const int key = k0 + c * kTile + row;
     const int from = max(0, key - (L - n)) * G;
+    const float f = kQ8 ? key_scale[c][row] : sl2;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(x[j]) * sl2;
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(x[j]) * f;
     if (k0 + c * kTile + kTile > L - n + 1) {          // (CTA-uniform)
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -237,7 +240,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     float m[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) m[j] = -INFINITY;
+    // 8-bit pools: chunk c's codes into its stage, once part 0 of them is held
+    // and the MMA of the chunk before it there is done
+    [[maybe_unused]] Codes<D, BS, kQ8 ? kKind : KV_DTYPE_INT8> codes;
+    if constexpr (kQ8) {
+      if (first < nch && !codes.load(a, bt, hk, k0 + first * kTile, L, 0)) sh_bad = 1;
+    }
     for (int c = first; c < nch; c += kSets) {
+      if constexpr (kQ8) {
+        const int from = k0 + c * kTile, key = from + row;
+        float f = 0.0f;
+        if (key < L) {
+          const int p = bt[key / BS];
+          if (p >= 0 && p < a.num_blocks) f = sl2 * a.k_scale[(int64_t)p * a.num_kv_heads + hk];
+        }
+        key_scale[c][row] = f;
+        if (c >= kStages && !warp_wait(smem_addr(&s_full[c - kStages]), 0)) {
+          ok = false;
+          break;
+        }
+        if (!codes.finish(a, bt, hk, from, L, smem_raw + (stage_img(c % kStages) - smem_addr(smem_raw)))) sh_bad = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&full[c % kStages]));
+        if (c + kSets < nch && !codes.load(a, bt, hk, from + kSets * kTile, L, 0)) sh_bad = 1;
+      }
       if (!warp_wait(smem_addr(&s_full[c]), 0)) {
         ok = false;
         break;
@@ -341,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster.sync();                                      // peers may still read this CTA's statistics
 }
 
-template <int D, int BS>
-kv_status launch_few(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int C, cudaStream_t s) {
+template <int D, int BS, int kKind>
+kv_status launch_few_t(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int C, cudaStream_t s) {
   static std::mutex mu;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -351,7 +377,7 @@ kv_status launch_few(const PromptArgs& a, const CUtensorMap& km, const CUtensorM
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(few_rows_kernel<D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      st = cuda_check(cudaFuncSetAttribute(few_rows_kernel<D, BS, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            FGeo<D>::kSmemBytes),
                       "cudaFuncSetAttribute(few_rows_kernel)");
       if (st != KV_OK) return st;
@@ -370,7 +396,15 @@ kv_status launch_few(const PromptArgs& a, const CUtensorMap& km, const CUtensorM
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, few_rows_kernel<D, BS>, km, qm, a), "few_rows_kernel launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, few_rows_kernel<D, BS, kKind>, km, qm, a), "few_rows_kernel launch");
+}
+
+template <int D, int BS>
+kv_status launch_few(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, kv_dtype dtype, int C,
+                     cudaStream_t s) {
+  if (dtype == KV_DTYPE_INT8) return launch_few_t<D, BS, KV_DTYPE_INT8>(a, km, qm, C, s);
+  if (dtype == KV_DTYPE_FP8_E4M3) return launch_few_t<D, BS, KV_DTYPE_FP8_E4M3>(a, km, qm, C, s);
+  return launch_few_t<D, BS, KV_DTYPE_BF16>(a, km, qm, C, s);
 }
 
 }  // namespace
@@ -385,7 +419,8 @@ int few_rows_ctas(int batch, int num_kv_heads, int max_seq_len, int num_sms) {
   return C;
 }
 
-kv_status launch_prompt_few(const PromptArgs& a, int head_dim, int block_size, int ctas, cudaStream_t s) {
+kv_status launch_prompt_few(const PromptArgs& a, int head_dim, int block_size, kv_dtype dtype, int ctas,
+                            cudaStream_t s) {
   DecodeArgs d = {};
   d.k_cache = a.k_cache;
   d.v_cache = a.k_cache;                               // (the V map is not used)
@@ -393,7 +428,7 @@ kv_status launch_prompt_few(const PromptArgs& a, int head_dim, int block_size, i
   d.num_blocks = a.num_blocks;
   d.head_dim = head_dim;
   d.block_size = block_size;
-  d.dtype = KV_DTYPE_BF16;
+  d.dtype = dtype;
   alignas(64) CUtensorMap km, vm, qm;
   kv_status st = make_kv_maps(d, &km, &vm);
   if (st == KV_OK)
@@ -401,8 +436,8 @@ kv_status launch_prompt_few(const PromptArgs& a, int head_dim, int block_size, i
                         a.tile_tokens);
   if (st != KV_OK) return st;
   if (head_dim == 128)
-    return block_size == 32 ? launch_few<128, 32>(a, km, qm, ctas, s) : launch_few<128, 16>(a, km, qm, ctas, s);
-  return block_size == 32 ? launch_few<64, 32>(a, km, qm, ctas, s) : launch_few<64, 16>(a, km, qm, ctas, s);
+    return block_size == 32 ? launch_few<128, 32>(a, km, qm, dtype, ctas, s) : launch_few<128, 16>(a, km, qm, dtype, ctas, s);
+  return block_size == 32 ? launch_few<64, 32>(a, km, qm, dtype, ctas, s) : launch_few<64, 16>(a, km, qm, dtype, ctas, s);
 }
 
 }  // namespace pagedkv

@@ -224,72 +224,6 @@ __device__ __forceinline__ float row_log_sum(float m, float l) {
   return m == -INFINITY ? __uint_as_float(0x7fc00000u) : m + log2f(l);
 }
 
-// 8-bit pools: the codes of the 128 keys from `from` (zeros from L on), loaded
-// by one set of row warps and widened into a swizzled bf16 image; a piece is 16
-// codes of a key.
-template <int D, int BS, int kKind>
-struct Codes {
-  static constexpr int kRowPieces = D / 16;
-  static constexpr int kParts = 2;                       // held one at a time
-  static constexpr int kPieces = kTile * kRowPieces / kSetThreads / kParts;
-  uint4 x[kPieces];
-
-  __device__ __forceinline__ static int piece(int part, int u) {
-    return (part * kPieces + u) * kSetThreads + (int)(threadIdx.x % kSetThreads);
-  }
-
-  // False when a key's block is outside the pool.
-  __device__ __forceinline__ bool load(const PromptArgs& a, const int32_t* bt, int hk, int from, int L, int part) {
-    bool ok = true;
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int i = piece(part, u), key = from + i / kRowPieces;
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (key >= L) continue;
-      const int p = bt[key / BS];
-      if (p < 0 || p >= a.num_blocks) {
-        ok = false;
-        continue;
-      }
-      x[u] = static_cast<const uint4*>(a.k_cache)[(((int64_t)p * BS + key % BS) * a.num_kv_heads + hk) * kRowPieces +
-                                                  i % kRowPieces];
-    }
-    return ok;
-  }
-
-  __device__ __forceinline__ void store(unsigned char* img, int part) const {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int i = piece(part, u), r = i / kRowPieces;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[4];
-        code_values<kKind == KV_DTYPE_FP8_E4M3>(w[k], v);
-        o[2 * k] = pack2<false>(v[0], v[1]);
-        o[2 * k + 1] = pack2<false>(v[2], v[3]);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = 2 * (i % kRowPieces) + k;          // 8-element chunk of the row
-        *reinterpret_cast<uint4*>(img + (c / 8) * (kTile * 128) + sw128(r, c % 8)) =
-            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      }
-    }
-  }
-
-  // The other part, after the one that is held; then the image is complete.
-  __device__ __forceinline__ bool finish(const PromptArgs& a, const int32_t* bt, int hk, int from, int L,
-                                         unsigned char* img) {
-    store(img, 0);
-    const bool ok = load(a, bt, hk, from, L, 1);
-    store(img, 1);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    return ok;
-  }
-};
-
 template <int D, int BS, int kKind, bool kStats>
 __global__ void __launch_bounds__(kThreads, 2)
     prompt_tc_kernel(const __grid_constant__ CUtensorMap k_map,
