@@ -1,7 +1,6 @@
 // pagedkv_weights_few.cu -- the attention weights of a few query tokens per
 // sequence (speculative verification) in one pass over K: pagedkv_attention_
-// weights for at most 32 rows (query tokens times grouped heads) per KV head
-// on bf16 pools.
+// weights for at most 32 rows (query tokens times grouped heads) per KV head.
 //
 // With so few rows the keys' bytes bound it, and a second pass over K Q^T
 // would read them again.  Here the scores of a whole sequence stay in TMEM
@@ -26,6 +25,11 @@
 // mma.sync kernels: 189).  K is read at the copy rate while the first sweep
 // runs; the other two sweeps and the exchange read no memory, and only the
 // second CTA of an SM hides them.
+//
+// 8-bit pools: the key warps load the codes themselves, a chunk ahead, and widen
+// them to bf16 (exact) into the stage; a key's K scale multiplies its scores.
+// The same batch: int8 139 us, E4M3 135 (232 in two passes), bound by the
+// widening beside the sweeps.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
