@@ -69,9 +69,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-// 32 consecutive TMEM columns of this warp's 32 lanes, complete on return (one
-// instruction sequence: a separate wait that ties the registers costs a move
-// for each).
+// 32 consecutive TMEM columns of this warp's 32 lanes, complete on return.
 __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -87,9 +85,7 @@ __device__ __forceinline__ void tmem_read32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-// 64 consecutive TMEM columns of this warp's 32 lanes, complete on return (one
-// instruction sequence: a separate wait that ties the registers costs a move
-// for each).
+// 64 consecutive TMEM columns of this warp's 32 lanes, complete on return.
 __device__ __forceinline__ void tmem_read64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
@@ -150,20 +146,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// tcgen05.wait::ld tied to the registers of a load (nothing that reads them
-// moves above it), for loads in flight beside arithmetic on others.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
-               :
-               : "memory");
-  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
-}
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
                                             int c1, int c2) {

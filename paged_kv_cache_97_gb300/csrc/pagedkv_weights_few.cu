@@ -226,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto scores = [&](int c, float (&v)[32]) {
     uint32_t x[32];
     __syncwarp();
-    tmem_ld32(lanes + c * kRows, x);
-    tmem_wait_ld32(x);
+    tmem_read32(lanes + c * kRows, x);
     const int key = k0 + c * kTile + row;
     const int from = max(0, key - (L - n)) * G;
     const float f = kQ8 ? key_scale[c][row] : sl2;
