@@ -125,12 +125,13 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
 // piece p holds elements 8p .. 8p + 7.  8-bit codes become bf16, exactly
 // (|c| <= 127 and E4M3's 4 significant bits fit bf16's 8).
 //
-// These kernels serve what the tcgen05 ones do not: 33 to 64 rows, up to 64 rows
-// past a cluster's TMEM, scales that are not positive, groups of more than 128
-// heads.  The two reads of K and the issue of the loads' and exponentials'
-// instructions share the bound: 64 sequences of 512..4096 tokens x five
-// queries, 32/8 heads, 189 us on a bf16 pool and 232 on int8 (one pass with the
-// scores in TMEM: 103 and 139).
+// These kernels serve what the tcgen05 ones do not: up to 64 rows on 8-bit pools
+// and 15 on bf16 pools where the one-pass kernel does not hold them, scales that
+// are not positive, groups of more than 128 heads.  The two reads of K and the
+// issue of the loads' and exponentials' instructions share the bound: 64
+// sequences of 512..4096 tokens x five queries, 32/8 heads, 189 us on a bf16
+// pool and 196 on int8 (one pass with the scores in TMEM: 103 and 139), 64/8
+// heads on int8 232.
 
 constexpr int kRowTile = 64;                           // rows of Q per tile
 constexpr int kNTiles = kRowTile / 8;
@@ -596,10 +597,19 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
     return fail(KV_ERR_INVALID_ARG, "%s: 8-bit pools need k_scale; bf16 pools take NULL", who);
   const int64_t G = num_q_heads / num_kv_heads;
   const int longest = max_query_len < num_tokens ? max_query_len : num_tokens;
-  // Many rows per KV head: the tcgen05 kernels, whose row tile
-  // is 128 rows of whole tokens; else the mma.sync kernels above.  (Their
-  // score scale is positive.)
-  const bool tc = scale > 0.0f && G <= 128 && longest * G > kRowTile;
+  // Many rows per KV head: the tcgen05 kernels, whose row tile is 128 rows of
+  // whole tokens; else the mma.sync kernels above.  (Their score scale is
+  // positive.)  On bf16 pools they win from some 16 rows on (8 KV heads: 64 x
+  // 512..4096 tokens x 48 rows 246 -> 176 us, four of 16K x 16 rows 132 -> 103, one
+  // of 131072 x 20 rows 587 -> 209; 16 x 16K x 4 rows, two heads of 64: 43 -> 69).
+  // On 8-bit pools a unit's keys are widened for one tile of rows, which pays for
+  // more than 64 rows or in long sequences (one of 32K x 64 rows 248 -> 115, eight
+  // of 32K x 48 rows 619 -> 527; 64 x 512..4096 x 48 rows 252 -> 365, four of 16K x
+  // 16 rows 122 -> 160).
+  const int64_t most_rows = longest * G;
+  const bool tc = scale > 0.0f && G <= 128 &&
+                  (most_rows > kRowTile || (dtype == KV_DTYPE_BF16 && most_rows >= 16) ||
+                   (most_rows > 32 && max_seq_len >= 8192));
   const int64_t tile_tokens = tc ? 128 / G : 0;
   const int64_t tiles = tc ? (longest + tile_tokens - 1) / tile_tokens
                            : (longest * G + kRowTile - 1) / kRowTile;
@@ -643,7 +653,7 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
   cudaStream_t s = (cudaStream_t)stream;
   // Few rows whose scores fit a cluster's TMEM: one pass over K (64 sequences of
   // 512..4096 tokens, five queries each, 32/8 heads: two passes of the mma.sync
-  // kernels 189 us, one pass 103; int8 232 and 139).
+  // kernels 189 us, one pass 103; int8 196 and 139).
   const int ctas = longest * G <= kFewRows ? few_rows_ctas(batch, num_kv_heads, max_seq_len, di.num_sms) : 0;
   if (ctas > 0) {
     a.tile_tokens = (int)(kFewRows / G);

@@ -300,6 +300,22 @@ def test_prompt_weights_many_units(pkv, dtype, dim):
         assert same_bits(w[b, :, n:], weights[b, :, n:])
 
 
+@pytest.mark.parametrize("dtype,block,dim", POOLS)
+@pytest.mark.parametrize("n", [3, 4, 5, 10, 16])
+def test_prompt_weights_few_rows_long_bound(pkv, dtype, block, dim, n):
+    """12 to 64 rows where max_seq_len is past what a cluster's TMEM holds: the
+    two-pass kernels, most key splits empty."""
+    pool = ref.Pool([n + 3, 700, 260, 1], 2, dim, block, dtype, seed=n, width=9008 // block)
+    counts = [n, n, 1, 1]
+    q = pool.randn(sum(counts), 8, dim, scale=2.0)
+    weights = torch.rand((4, 2, 9000), generator=pool.g) * n / 30
+    w = prompt_weights(pkv, pool, q, counts, weights, dim ** -0.5, max_len=9000)
+    want, tol = ref.prompt_weights(pool, q, counts, weights, dim ** -0.5)
+    for b, m in enumerate(pool.L):
+        within(w[b, :, :m], want[b, :, :m], tol[b, :, :m])
+        assert same_bits(w[b, :, m:], weights[b, :, m:])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "int8"])
 def test_prompt_weights_repeat_bit_for_bit(pkv, dtype):
     """Which CTA takes which unit differs from call to call; the bits do not."""
