@@ -95,11 +95,13 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
   __shared__ int32_t blk_id[kMaxBlocks];
-  // K scales of the two maps, V scales of the two halves relative to the
-  // CTA's largest
+  // K scales of the two maps, V scales of the two value halves, each relative
+  // to the CTA's largest of that half: the halves are different output elements
+  // of pool heads with scales of their own, so under one maximum the half with
+  // the smaller scales would have its probabilities in fp16's subnormals
   __shared__ float blk_ks[kQ8 ? 2 * kMaxBlocks : 1], blk_vr[kQ8 ? 2 * kMaxBlocks : 1];
   __shared__ int cta_bad, cta_timeout;
-  __shared__ float v_max_scale;
+  __shared__ float v_max_scale[2];
 
   const int j = blockIdx.x / da.head_groups, hg = blockIdx.x % da.head_groups;
   const int part = a.reverse_parts ? (int)(gridDim.z - 1 - blockIdx.z) : (int)blockIdx.z;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) {
     cta_bad = 0;
     cta_timeout = 0;
-    v_max_scale = 0.0f;
+    v_max_scale[0] = v_max_scale[1] = 0.0f;
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_addr(&full_bar[s]), 1);
       mbar_init(smem_addr(&empty_bar[s]), kDiffConsumers);
@@ -179,17 +181,19 @@ __global__ void __launch_bounds__(kThreads)
           blk_ks[2 * i + m] = a.k_scale[(int64_t)p * P + 2 * j + m];
           const float vs = a.v_scale[(int64_t)p * P + 2 * j + m];
           blk_vr[2 * i + m] = vs;
-          atomicMax(reinterpret_cast<int*>(&v_max_scale), __float_as_int(fabsf(vs)));
+          atomicMax(reinterpret_cast<int*>(&v_max_scale[m]), __float_as_int(fabsf(vs)));
         }
       }
     }
   }
   __syncthreads();
   if constexpr (kQ8) {
-    // p enters the second product times (V scale / the CTA's largest), in
+    // p enters the second product times (V scale / the half's largest), in
     // fp16 range; the output is multiplied back by the largest
-    const float vmax = v_max_scale > 0.0f ? v_max_scale : 1.0f;
-    for (int i = threadIdx.x; i < 2 * nblk; i += kThreads) blk_vr[i] = blk_vr[i] / vmax;
+    for (int i = threadIdx.x; i < 2 * nblk; i += kThreads) {
+      const float vmax = v_max_scale[i & 1];
+      blk_vr[i] = blk_vr[i] / (vmax > 0.0f ? vmax : 1.0f);
+    }
     __syncthreads();
   }
   const bool bad = cta_bad != 0;
@@ -488,7 +492,10 @@ __global__ void __launch_bounds__(kThreads)
 
   if (failed && threadIdx.x == 0)
     atomicOr(a.flags, bad ? PAGEDKV_FLAG_BAD_BLOCK : PAGEDKV_FLAG_WAIT_TIMEOUT);
-  const float out_scale = kQ8 ? (v_max_scale > 0.0f ? v_max_scale : 1.0f) : 1.0f;
+  float out_scale[2] = {1.0f, 1.0f};
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (kQ8 && v_max_scale[x] > 0.0f) out_scale[x] = v_max_scale[x];
   // column c's joined element e, max and denominator over the warps
   auto joined = [&](int c, int e, float* M, float* den) {
     *M = -INFINITY;
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kThreads)
       num = fmaf(f, red_acc[(w * 8 + c) * 2 * D + e], num);
       *den = fmaf(f, red_l[w * 8 + c], *den);
     }
-    return num * out_scale;
+    return num * (e < D ? out_scale[0] : out_scale[1]);
   };
   if (direct) {
     for (int i = warp; i < nh; i += kThreads / 32) {

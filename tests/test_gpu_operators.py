@@ -799,3 +799,36 @@ def test_diff_bad_sequences(pkv):
     one.k, one.v, one.tables = pool.k, pool.v, good[0][None]
     want, tol = ref.diff_attention(one, q[:1], 0.125, lam, torch.ones(128), 1e-5)
     within(out[:1], want, tol)
+
+
+@pytest.mark.parametrize("dtype,block,dim,L", [("int8", 16, 128, [2049, 513, 7]), ("fp8", 32, 64, [1025, 40]),
+                                               ("int8", 32, 64, [300]), ("fp8", 16, 128, [90, 1])])
+@pytest.mark.parametrize("ratio", [2.0 ** -10, 1e-4, 1e-6, 2.0 ** -40, 1e6])
+@pytest.mark.parametrize("norm", [False, True])
+def test_diff_value_halves_of_different_scales(pkv, dtype, block, dim, L, ratio, norm):
+    """The two pool heads of a value have scales of their own, whatever their
+    ratio: each half keeps the precision of its own probabilities.  (The bound
+    of an element goes by its own half: p in fp16 is off by 2^-11 p, below
+    fp16's smallest normal number by 2^-25 of the largest, sum p = 1, which
+    over 2049 tokens is 2^-14 of the half's values; the bound counts 2^-8.)"""
+    pool = ref.Pool(L, 4, dim, block, dtype, seed=6)
+    pool.v_scale[:, 1::2] *= ratio
+    q = pool.randn(len(L), 12, dim, scale=2.0)
+    lam = 0.2 + 0.6 * torch.rand(6, generator=pool.g)
+    weight = 0.5 + torch.rand(2 * dim, generator=pool.g) if norm else None
+    out = diff(pkv, pool, q, dim ** -0.5, lam, weight)
+    want, tol = ref.diff_attention(pool, q, dim ** -0.5, lam, weight, 1e-5)
+    within(out, want, tol)
+
+
+def test_diff_value_half_of_zeros(pkv):
+    """A V head whose scales are all zero, and one whose values are all zero."""
+    for head in (0, 1):
+        pool = ref.Pool([300, 20], 2, 64, 16, "int8", seed=7)
+        pool.v_scale[:, head] = 0.0
+        ref.raw(pool.v)[pool.tables[1, :2].long(), :, 1 - head] = 0
+        q = pool.randn(2, 4, 64, scale=2.0)
+        lam = torch.tensor([0.3, 0.7])
+        out = diff(pkv, pool, q, 0.125, lam, None)
+        want, tol = ref.diff_attention(pool, q, 0.125, lam, None, 1e-5)
+        within(out, want, tol)
