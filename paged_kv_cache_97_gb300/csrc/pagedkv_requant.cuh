@@ -95,8 +95,10 @@ __device__ __noinline__ float codes_amax_each(uint4 x, float s) {
 // value: where both ends have the same code it is q's, and only the words
 // where they differ (a border between two codes lies in between) are divided.
 // An IEEE division per element bound these kernels at 21 % of the memory rate.
-// s == 0 reads as 1; factors outside [2^-80, 2^80], whose products or
-// remainders could lose bits, always divide.
+// s == 0 reads as 1; scales outside [2^-80, 2^80], whose products or
+// remainders could lose bits, always divide, and so do ratios of two scales
+// above 2^80: t r may be infinite, and 0 * infinity is no code.  (Any smaller
+// ratio will do: below 2^-19 every product has the code 0, as its quotient.)
 struct Interval {
   float lo, hi;
   bool on;
@@ -121,7 +123,8 @@ __device__ __forceinline__ Interval quotients(float s) {
 __device__ __forceinline__ Interval quotients(float t, float s) {
   s = scale_or_one(s);
   const float r = __frcp_rn(s);
-  return interval(t * r, plain_size(s) && plain_size(t), s, r);
+  const float f = t * r;
+  return interval(f, plain_size(s) && plain_size(t) && f <= 0x1p80f, s, r);
 }
 
 // The codes of x[k] * f, lowest byte first (int8: |x[k] * f| < 128).

@@ -555,6 +555,35 @@ def test_evict_zero_and_nan_values(pkv):
     assert got[2][pool.tables[0, 0].item(), 0] == 0
 
 
+@pytest.mark.parametrize("dtype", ["int8", "fp8"])
+@pytest.mark.parametrize("large,small", [(70, -70), (64, -64), (80, -40), (40, -80), (79, 1), (80, -80), (100, -30),
+                                         (30, -100), (8, -126)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_evict_scales_far_apart(pkv, dtype, large, small, fresh):
+    """A row of zeros under a scale 2^large packed beside rows under 2^small:
+    the zeros are codes of 0 under the new scale, whatever the two's ratio."""
+    pool = ref.Pool([64, 50], 2, 64, 16, dtype, seed=4, extra=8)
+    for b in (0, 1):
+        blocks = pool.tables[b].long()
+        for cache, scale in ((pool.k, pool.k_scale), (pool.v, pool.v_scale)):
+            scale[blocks] = 2.0 ** small
+            scale[blocks[2]] = 2.0 ** large
+            ref.raw(cache)[blocks[2]] = 0
+            if dtype == "fp8":
+                ref.raw(cache)[blocks[2], :, :, ::3] = 0x80           # -0
+    idx, num = random_keep(pool, 30, 2, pool.g)
+    for b in (0, 1):
+        idx[b, :, :8] = torch.arange(1, 9)
+        idx[b, :, 8:16] = torch.arange(33, 41)                  # the zeros, beside them
+        idx[b, :, 16:24] = torch.arange(41, 49)                 # zeros in the next block
+        idx[b, :, 24:30] = torch.tensor([49, 49, 49, 49, 49, 49]) if b else torch.arange(49, 55)
+    num[1] = 25                                                 # the second keeps one row after them
+    weights = torch.rand((2, 2, 64), generator=pool.g)
+    dst = pool.free[:4].view(2, 2).contiguous() if fresh else None
+    got = evict(pkv, pool, idx, num, dst, weights)
+    check_evict(got, ref.evict(pool, idx, num, pool.tables if dst is None else dst, weights))
+
+
 def test_evict_bad_lists(pkv):
     """A list that does not ascend in range leaves its head alone, a bad
     length its sequence, a bad block its destination block."""
