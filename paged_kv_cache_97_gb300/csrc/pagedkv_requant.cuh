@@ -231,7 +231,9 @@ __device__ __noinline__ uint4 code16_divided(uint4 a, uint4 b, float s) {
 // divide.  There the quotient itself is made, by two of Markstein's correction
 // steps (P. Markstein, IBM J. Res. Dev. 34, 1990) with r the correctly rounded
 // reciprocal: q0 = x r is within 2 units in the last place, the first step
-// brings it within one, from where the second rounds correctly.
+// brings it within one, from where the second rounds correctly.  The remainder
+// is taken as y s - x, which is +0 for either zero: y - (+0) r then keeps the
+// sign of a -0 (y + (+0) r, with the remainder x - y s, would lose it).
 template <bool kFp8>
 __device__ __forceinline__ uint4 code16(uint4 a, uint4 b, const Interval& q, float s) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -244,8 +246,8 @@ __device__ __forceinline__ uint4 code16(uint4 a, uint4 b, const Interval& q, flo
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float y = v[k] * q.r;
-        y = fmaf(fmaf(-y, q.s, v[k]), q.r, y);
-        v[k] = fmaf(fmaf(-y, q.s, v[k]), q.r, y);
+        y = fmaf(fmaf(y, q.s, -v[k]), -q.r, y);
+        v[k] = fmaf(fmaf(y, q.s, -v[k]), -q.r, y);
       }
       o[i] = code4_times<true>(v, 1.0f);
     } else {

@@ -674,6 +674,33 @@ def test_append_special_values(pkv, dtype):
         assert same_bits(a, b)
 
 
+@pytest.mark.parametrize("dtype,block,dim", EIGHT)
+def test_append_codes_are_those_of_reshape_and_cache(pkv, dtype, block, dim):
+    """Under the scales that the append has made, reshape_and_cache stores the
+    same codes, the sign of a zero among them: blocks of small and large values
+    with zeros of both signs, of zeros alone, and with infinities and NaN."""
+    L = [5 * block, 3, block + 1]
+    pool = ref.Pool(L, 2, dim, block, dtype, seed=12)
+    T = sum(L)
+    k_new, v_new = pool.randn(T, 2, dim), pool.randn(T, 2, dim, scale=1e-20)
+    for x in (k_new, v_new):
+        x[:, :, 1::3] = -0.0
+        x[:, :, 2::7] = 0.0
+        x[block:2 * block] = -0.0
+        x[2 * block, 0, 5], x[2 * block + 1, 0, 6], x[2 * block + 2, 0, 7] = float("inf"), -float("inf"), float("nan")
+        x[3 * block:4 * block] *= 1e-19                       # (of v: bf16's subnormals)
+    got = append(pkv, pool, k_new, v_new, L)
+    for a, b in zip(got, ref.append(pool, k_new, v_new, L)):
+        assert same_bits(a, b)
+    k, v, _, bt, _ = pool.on()
+    pos = torch.tensor([i for n in L for i in range(n)], dtype=torch.int32, device="cuda")
+    seq = torch.tensor([b for b, n in enumerate(L) for _ in range(n)], dtype=torch.int32, device="cuda")
+    slots = torch.empty(T, dtype=torch.int64, device="cuda")
+    pkv.token_slot_mapping(bt, pos, pool.num_blocks, block, slots, seq_idx=seq)
+    pkv.reshape_and_cache(k_new.cuda(), v_new.cuda(), k, v, slots, got[1], got[3])
+    assert same_bits(got[0], k.cpu()) and same_bits(got[2], v.cpu())
+
+
 def test_append_recodes_minus_128(pkv):
     """A pool whose int8 codes hold -128 (no call of the library writes it):
     coded again, it clamps to -127."""
