@@ -168,14 +168,17 @@ kv_status kv_pool_prepare_append(kv_pool *pool, int32_t *block_tables,
 /* Destination blocks of an eviction (pagedkv_evict_tokens) that leaves
  * keep_lens[b] of sequence b's seq_lens[b] tokens per KV head, packed into its
  * first ceil(keep_lens[b] / block_size) blocks (host arrays):
- *   - keep_lens[b] == seq_lens[b]: nothing moves, dst_tables[b] lists the same
- *     blocks;
+ *   - keep_lens[b] == seq_lens[b]: nothing moves, dst_tables[b] is the same
+ *     row;
  *   - otherwise each of those first blocks stays the sequence's own when it
  *     holds the only reference (its prefix-cache entry is dropped: the rows
  *     will be others), and is replaced by a block of the free list when it is
  *     shared (the other holders keep reading the old one; the sequence's
- *     reference on it is dropped), and the blocks after them lose the
- *     sequence's reference.
+ *     reference on it is dropped), and the tokens' blocks after them lose the
+ *     sequence's reference;
+ *   - what the row lists past its ceil(seq_lens[b] / block_size) blocks (blocks
+ *     reserved ahead, which stay the sequence's, or -1) follows the kept
+ *     blocks, neither checked nor released.
  * All new blocks are taken before any reference is dropped, so no destination
  * is a block that another sequence of the call is still read from.  The caller
  * uploads dst_tables, runs the eviction with block_tables as the source, and
@@ -183,8 +186,8 @@ kv_status kv_pool_prepare_append(kv_pool *pool, int32_t *block_tables,
  * freed blocks has to be ordered behind it (the same stream).
  *   block_tables  host int32 [batch, max_blocks_per_seq] (read only)
  *   seq_lens, keep_lens  host int32 [batch], 0 <= keep_lens[b] <= seq_lens[b]
- *   dst_tables    host int32 [batch, max_blocks_per_seq] (output; -1 past the
- *                 kept blocks; must not be block_tables)
+ *   dst_tables    host int32 [batch, max_blocks_per_seq] (output; -1 after the
+ *                 kept and the reserved blocks; must not be block_tables)
  * All or nothing: KV_ERR_OUT_OF_BLOCKS when the free list is too short for
  * the shared blocks, KV_ERR_INVALID_ARG for lengths out of range or a table
  * entry that is not allocated (or is listed more often than it is
@@ -742,9 +745,10 @@ kv_status pagedkv_select_tokens(int32_t *keep_idx, int32_t *keep_len,
  *   k_cache, v_cache, k_scale, v_scale  device pools as for copy_blocks (written)
  *   block_tables  device int32 [batch, max_blocks_per_seq], the source
  *   dst_block_tables  device int32 [batch, dst_max_blocks]: may be
- *                 block_tables (packing in place).  Entry j of a row is either
- *                 entry j of the source row or a block that no source row of
- *                 the call lists, and no block is a destination twice
+ *                 block_tables (packing in place).  Entry j of a row's first
+ *                 ceil(keep_len[b] / block_size) (the others are not read) is
+ *                 either entry j of the source row or a block that no source
+ *                 row of the call lists, and no block is a destination twice
  *                 (kv_pool_prepare_evict makes such tables)
  *   keep_idx, keep_len, budget  as pagedkv_select_tokens gives them: each list
  *                 strictly ascending within [0, seq_lens[b])

@@ -266,7 +266,8 @@ class KVPool:
     def prepare_evict(self, block_tables, seq_lens, keep_lens):
         """Destination tables (a host int32 array like block_tables) of an
         eviction that leaves keep_lens[b] of seq_lens[b] tokens: blocks the
-        sequence shares are replaced, those it no longer needs released.
+        sequence shares are replaced, those it no longer needs released, and
+        what a row lists past its tokens' blocks follows the kept ones.
         block_tables stays the source table of evict_tokens."""
         import numpy as np
         bt = block_tables

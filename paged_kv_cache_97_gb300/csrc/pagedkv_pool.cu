@@ -351,26 +351,28 @@ kv_status kv_pool_prepare_evict(kv_pool* p, const int32_t* block_tables, int max
   if (need > p->free_list.size())
     return fail(KV_ERR_OUT_OF_BLOCKS, "kv_pool_prepare_evict: %zu blocks needed, %zu free", need,
                 p->free_list.size());
-  // Pass 2: all destinations; pass 3: the references dropped (in table order).
+  auto blocks = [bs](int tokens) { return tokens / bs + (tokens % bs != 0); };
+  // Pass 2: all destinations, and behind them what the row lists past its
+  // tokens' blocks; pass 3: the references dropped (in table order).
   for (int b = 0; b < batch; ++b) {
-    const int L = seq_lens[b], m = keep_lens[b];
-    for (int j = 0; j < max_blocks_per_seq; ++j) {
-      int32_t& to = dst_tables[(int64_t)b * max_blocks_per_seq + j];
-      to = -1;
-      if ((int64_t)j * bs >= m) continue;
-      to = block_tables[(int64_t)b * max_blocks_per_seq + j];
-      if (m == L) continue;
-      if (p->refs[to] > 1) to = take_block(p);
-      else evict(p, to);                               // its rows become others
+    const int nsrc = blocks(seq_lens[b]), ndst = blocks(keep_lens[b]);
+    const int32_t* from = block_tables + (int64_t)b * max_blocks_per_seq;
+    int32_t* to = dst_tables + (int64_t)b * max_blocks_per_seq;
+    for (int j = 0; j < max_blocks_per_seq; ++j)
+      to[j] = j < ndst ? from[j] : j - ndst < max_blocks_per_seq - nsrc ? from[j - ndst + nsrc] : -1;
+    if (keep_lens[b] == seq_lens[b]) continue;
+    for (int j = 0; j < ndst; ++j) {
+      if (p->refs[to[j]] > 1) to[j] = take_block(p);
+      else evict(p, to[j]);                            // its rows become others
     }
   }
   for (int b = 0; b < batch; ++b) {
-    const int L = seq_lens[b], m = keep_lens[b];
-    if (m == L) continue;
-    for (int j = 0; (int64_t)j * bs < L; ++j) {
-      const int64_t at = (int64_t)b * max_blocks_per_seq + j;
-      if (dst_tables[at] != block_tables[at]) drop_ref(p, block_tables[at]);
-    }
+    if (keep_lens[b] == seq_lens[b]) continue;
+    const int nsrc = blocks(seq_lens[b]), ndst = blocks(keep_lens[b]);
+    const int32_t* from = block_tables + (int64_t)b * max_blocks_per_seq;
+    const int32_t* to = dst_tables + (int64_t)b * max_blocks_per_seq;
+    for (int j = 0; j < nsrc; ++j)
+      if (j >= ndst || to[j] != from[j]) drop_ref(p, from[j]);
   }
   return KV_OK;
 }

@@ -214,6 +214,33 @@ def test_prepare_evict_and_the_prefix_cache(pkv):
     assert pool.stats() == (0, 6) and pool.match_prefix(tokens) == a
 
 
+def test_prepare_evict_blocks_reserved_ahead(pkv):
+    """Blocks that a row lists beyond its tokens stay the sequence's: behind
+    the kept blocks, in their order, with their references."""
+    pool = pkv.KVPool(16, 16, 2, 64)
+    a, b, c, d = pool.alloc(4), pool.alloc(4), pool.alloc(3), pool.alloc(2)
+    bt = table([a, b, c, d], 4)
+    dst = pool.prepare_evict(bt, [40, 20, 48, 0], [16, 20, 1, 0])
+    assert dst.tolist() == [[a[0], a[3], -1, -1], b, [c[0], -1, -1, -1], d + [-1, -1]]
+    assert [pool.refcount(i) for i in a + b + c + d] == [1, 0, 0, 1] + [1] * 4 + [1, 0, 0] + [1, 1]
+    assert pool.stats() == (9, 7)
+    held = [int(x) for row in dst for x in row if x >= 0]
+    pool.free(held)                                            # every reference is in the tables
+    assert pool.stats() == (0, 16)
+    # a shared block is replaced, the reserved ones follow its replacement
+    pool = pkv.KVPool(8, 16, 2, 64)
+    a = pool.alloc(5)
+    pool.fork(a[:2])
+    dst = pool.prepare_evict(table([a], 6), [33], [17])
+    assert dst.tolist() == [[5, 6, a[3], a[4], -1, -1]]
+    assert [pool.refcount(i) for i in a] == [1, 1, 0, 1, 1]
+    # nothing kept: the reserved blocks come first
+    pool = pkv.KVPool(4, 16, 2, 64)
+    a = pool.alloc(3)
+    assert pool.prepare_evict(table([a], 3), [16], [0]).tolist() == [[a[1], a[2], -1]]
+    assert pool.stats() == (2, 2)
+
+
 def test_prepare_evict_arguments(pkv):
     pool = pkv.KVPool(4, 16, 2, 64)
     with pytest.raises(TypeError):
