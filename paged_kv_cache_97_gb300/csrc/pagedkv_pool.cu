@@ -18,6 +18,7 @@
 // the current decode token writes, so that write is the only trigger.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <unordered_map>
 #include <vector>
 
@@ -100,6 +101,8 @@ struct kv_pool {
   kv_dtype dtype;
   FreeQueue free_list;            // front = next to hand out
   std::vector<int32_t> refs;      // references per block; 0 = free
+  std::vector<int32_t> listed;    // per block, of kv_pool_prepare_evict (made with
+                                  // the pool: an exception there would end the process)
   int used = 0;                   // blocks with refs > 0
   std::vector<CachedBlock> cache;                    // per block
   std::unordered_map<uint64_t, int32_t> by_hash;     // registered blocks
@@ -200,6 +203,7 @@ kv_status kv_pool_create(int num_blocks, int block_size, int num_kv_heads, int h
   p->dtype = dtype;
   p->free_list.init(num_blocks);
   p->refs.assign(num_blocks, 0);
+  p->listed.assign(num_blocks, 0);
   p->cache.assign(num_blocks, CachedBlock());
   *out = p;
   return KV_OK;
@@ -331,7 +335,8 @@ kv_status kv_pool_prepare_evict(kv_pool* p, const int32_t* block_tables, int max
   // listing; count the shared blocks that need a replacement (by the counts at
   // the call's start: a block that two sequences of the call share is read for
   // both, so neither may pack into it).
-  std::vector<int32_t> listed(p->num_blocks, 0);
+  std::vector<int32_t>& listed = p->listed;
+  std::fill(listed.begin(), listed.end(), 0);
   size_t need = 0;
   for (int b = 0; b < batch; ++b) {
     const int L = seq_lens[b], m = keep_lens[b];

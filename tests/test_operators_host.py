@@ -241,6 +241,33 @@ def test_prepare_evict_blocks_reserved_ahead(pkv):
     assert pool.stats() == (2, 2)
 
 
+def test_prepare_evict_allocates_nothing(pkv):
+    """In a process that can get no more memory the call works (a C++ exception
+    would end it at the C entry)."""
+    import subprocess
+    import sys
+    code = """
+import resource, sys
+import numpy as np
+import paged_kv_cache_97_gb300 as pkv
+pool = pkv.KVPool(1 << 22, 16, 2, 64)
+ids = pool.alloc(4)
+pool.fork(ids[:1])
+bt = np.array([ids], np.int32)
+pool.prepare_evict(np.full((1, 4), -1, np.int32), [0], [0])
+with open("/proc/self/statm") as f:
+    now = int(f.read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (now + (4 << 20), resource.RLIM_INFINITY))
+dst = pool.prepare_evict(bt, [64], [20])
+assert dst.tolist() == [[4, ids[1], -1, -1]], dst
+print("done")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(pkv.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-500:]
+
+
 def test_prepare_evict_arguments(pkv):
     pool = pkv.KVPool(4, 16, 2, 64)
     with pytest.raises(TypeError):
