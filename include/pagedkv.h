@@ -706,8 +706,9 @@ size_t pagedkv_attention_weights_workspace_bytes(int num_tokens,
  * paged_attention_multi).  V is not read.  Any group of query heads per KV
  * head.  Other arguments as for paged_attention_multi; the workspace is
  * 16-byte aligned, pagedkv_attention_weights_workspace_bytes(...).  One to
- * three launches, asynchronous on `stream`; no atomics, so equal inputs give
- * equal bits. */
+ * four launches, asynchronous on `stream`; no atomics, so equal inputs give
+ * equal bits.  After PAGEDKV_FLAG_WAIT_TIMEOUT entries may be missing the
+ * call's weights (left as they were); none is wrong. */
 kv_status pagedkv_attention_weights(
     float *weights, int weights_stride, const void *q, const void *k_cache,
     const float *k_scale, const int32_t *block_tables, int max_blocks_per_seq,

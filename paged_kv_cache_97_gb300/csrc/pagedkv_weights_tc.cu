@@ -219,6 +219,20 @@ __device__ __forceinline__ float column_part(const uint32_t* raw, float sl2, con
   return sum_f32x2(s[0], s[1]);
 }
 
+// Statistics of a row that has none (yet): the weights of its sequence stay as
+// they are.
+constexpr float kNoMax = -INFINITY, kNoSum = -1.0f;
+
+// Marks every row as without statistics before the row statistics: a unit whose
+// CTA gives up (a bounded wait) stores none, and what the workspace held from
+// before, finite numbers of an earlier call as a rule, must not pass for its.
+__global__ void __launch_bounds__(256) mark_stats_kernel(float2* stats, int64_t n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  if (i + 1 < n) *reinterpret_cast<float4*>(stats + i) = make_float4(kNoMax, kNoSum, kNoMax, kNoSum);
+  else if (i < n) stats[i] = make_float2(kNoMax, kNoSum);
+}
+
 // m + log2 l of a row.
 __device__ __forceinline__ float row_log_sum(float m, float l) {
   return m == -INFINITY ? __uint_as_float(0x7fc00000u) : m + log2f(l);
@@ -494,7 +508,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       g += un.nch;
       ++us;
     }
-    if (!kStats && first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (row statistics: the marks are there before the column sums start, whether
+    // this CTA stored anything behind them or not)
+    if (kStats || first) asm volatile("griddepcontrol.wait;" ::: "memory");
     // every load and claim has landed before the CTA ends (bounded; normally it has)
     if (last_claim > 0 && !warp_wait(smem_addr(&claim_full[(last_claim - 1) % kClaims]), ((last_claim - 1) / kClaims) & 1)) ok = false;
     if (fixed_issued > 0 && !warp_wait(smem_addr(&fixed_full), (fixed_issued - 1) & 1)) ok = false;
@@ -551,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int my_rows = un.tn * G;                   // row statistics: rows of the tile
       if (!any) {
         if (kStats && set == 0 && row < my_rows) {     // no key of this split
+          asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are marked
           float* o = stats_at(un, un.i0) + ((int64_t)row * a.splits + un.split) * 2;
           o[0] = -INFINITY;
           o[1] = 0.0f;
@@ -684,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if constexpr (kStats) {
           if (lost && row == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
           if (row < my_rows) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows are marked
             // (which set had the even chunks depends on the CTA's earlier units:
             // the join is the same with the two exchanged)
             const float r0 = part_ref[slot][0][row], r1 = part_ref[slot][1][row];
@@ -694,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             float* o = stats_at(un, un.i0) + ((int64_t)row * a.splits + un.split) * 2;
             // one split: m' at once (-inf: no statistics, the weights stay as
             // they are; a row whose every score is -inf has NaN weights)
-            o[0] = a.splits > 1 ? M : (lost ? -INFINITY : row_log_sum(M, l));
-            o[1] = lost ? -1.0f : l;
+            o[0] = a.splits > 1 ? M : (lost ? kNoMax : row_log_sum(M, l));
+            o[1] = lost ? kNoSum : l;
           }
         } else if (!lost && key < un.kend) {
           const float sum = part_sum[slot][0][row] + part_sum[slot][1][row];
@@ -731,7 +749,7 @@ __global__ void __launch_bounds__(256) join_stats_kernel(float* stats, int64_t r
     lost |= x < 0.0f;
     if (m > -INFINITY || x != x) l = fmaf(x, ex2(m - M), l);
   }
-  ml[0] = lost ? -INFINITY : row_log_sum(M, l);
+  ml[0] = lost ? kNoMax : row_log_sum(M, l);
 }
 
 template <int D, int BS, int kKind, bool kStats>
@@ -760,24 +778,27 @@ kv_status launch_tc_t(const PromptArgs& a, const CUtensorMap& km, const CUtensor
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = PGeo<D>::kSmemBytes;
   cfg.stream = s;
-  // the column sums start in the tail of the kernel before them
+  // both start beside the end of the kernel before them
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kStats ? 0 : 1;
+  cfg.numAttrs = 1;
   return cuda_check(cudaLaunchKernelEx(&cfg, prompt_tc_kernel<D, BS, kKind, kStats>, km, qm, a, tiles),
                     "prompt_tc_kernel launch");
 }
 
 template <int D, int BS, int kKind>
 kv_status launch_tc_kind(const PromptArgs& a, const CUtensorMap& km, const CUtensorMap& qm, int tiles, cudaStream_t s) {
-  kv_status st = launch_tc_t<D, BS, kKind, true>(a, km, qm, tiles * a.splits, s);
+  const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
+  const int64_t marks = (rows * a.splits + 511) / 512;
+  if ((rows + 255) / 256 > 0x7fffffffLL || marks > 0x7fffffffLL)
+    return fail(KV_ERR_INVALID_ARG, "pagedkv_attention_weights: too many query tokens");
+  mark_stats_kernel<<<(unsigned)marks, 256, 0, s>>>(reinterpret_cast<float2*>(a.stats), rows * a.splits);
+  kv_status st = cuda_check(cudaGetLastError(), "mark_stats_kernel launch");
+  if (st == KV_OK) st = launch_tc_t<D, BS, kKind, true>(a, km, qm, tiles * a.splits, s);
   if (st != KV_OK) return st;
   if (a.splits > 1) {
-    const int64_t rows = (int64_t)a.num_tokens * a.num_q_heads;
-    if ((rows + 255) / 256 > 0x7fffffffLL)
-      return fail(KV_ERR_INVALID_ARG, "pagedkv_attention_weights: too many query tokens");
     join_stats_kernel<<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a.stats, rows, a.splits);
     if ((st = cuda_check(cudaGetLastError(), "join_stats_kernel launch")) != KV_OK) return st;
   }

@@ -377,6 +377,39 @@ def test_prompt_weights_on_two_streams_and_in_a_graph(pkv):
         assert same_bits(ws[0].cpu(), alone[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("L", [[250, 200, 240], [1000, 900, 1024]])
+def test_prompt_weights_rows_start_without_statistics(pkv, dtype, L):
+    """The rows of the workspace ([Hkv][tokens][group][key splits] pairs) that
+    no unit of work completes say so (maximum -inf, sum -1), whatever was there
+    before, so that the weights they would give are left out: here rows of a
+    sequence with a bad length and rows that no sequence has, over the finite
+    statistics of an earlier call."""
+    H, G, counts, T = 1, 4, [40, 50, 60], 170
+    pool = ref.Pool(L, H, 64, 16, dtype, seed=6)
+    k, v, sc, bt, sl = pool.on()
+    q = pool.randn(T, H * G, 64, scale=2.0)
+    n = pkv.attention_weights_workspace_bytes(T, H * G, max(L))
+    splits = n // (T * H * G * 8)
+    assert splits == (1 if max(L) <= 256 else 4)              # of 256 tokens: few units, all of them are used
+    ws = torch.full((n // 4,), 1.5, device="cuda")
+    qs = torch.tensor([0, 40, 90, 150], dtype=torch.int32, device="cuda")
+    sl[1] = 2000                                              # past the table
+    weights = torch.rand((3, H, max(L)), generator=pool.g)
+    w = weights.cuda()
+    pkv.attention_weights(w, q.cuda(), k, bt, sl, qs, max(L), 60, 0.125, ws, k_scale=sc["k_scale"])
+    assert pkv.get_status()[1] == pkv.FLAG_BAD_SEQ_LEN
+    want, tol = ref.prompt_weights(pool, q, counts, weights, 0.125)
+    for b in (0, 2):
+        within(w[b, :, :L[b]], want[b, :, :L[b]], tol[b, :, :L[b]])
+    assert same_bits(w[1], weights[1])
+    rows = ws.view(H, T, G, splits, 2).cpu()
+    none = torch.zeros(T, dtype=torch.bool)
+    none[40:90] = none[150:] = True
+    assert (rows[:, none, :, :, 0] == -float("inf")).all() and (rows[:, none, :, :, 1] == -1).all()
+    assert torch.isfinite(rows[:, ~none, :, 0, 0]).all() and (rows[:, ~none, :, 0, 1] > 0).all()
+
+
 def test_prompt_weights_bad_sequences(pkv):
     L = [40, 20, 50, 64, 64]
     counts = [4, 21, 5, 6, 6]                                # 21 > 20
