@@ -630,7 +630,11 @@ size_t pagedkv_diff_workspace_bytes(int batch, int num_heads, int head_dim,
  *   out[b, h] = y / sqrt(mean(y^2) + eps) * norm_weight,  or y without one.
  * A pool for it is one of 2 * num_kv_heads heads, filled, copied and freed by
  * the calls above.  A factor on the normalised row (1 - lambda_init) belongs
- * in norm_weight.
+ * in norm_weight.  Scores, softmax sums, both products' sums, the difference and
+ * the norm are fp32; the softmax weights enter the product with V to 2^-16 of
+ * their value on bf16 pools and 2^-11 on 8-bit pools (fp16, relative to the
+ * largest V scale of their value half among 256 to 2048 tokens), which counts
+ * |a_0| / |y| times where the difference cancels.
  *   out           device bf16 [batch, num_heads, 2 * head_dim] (output)
  *   q             device bf16 [batch, 2 * num_heads, head_dim]
  *   k_cache, v_cache  device pools [num_blocks, block_size, 2 * num_kv_heads,

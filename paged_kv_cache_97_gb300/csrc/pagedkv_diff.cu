@@ -15,13 +15,21 @@
 //   S^T[16 x 8] = K_1 . Q^T and K_2 . Q^T, of which the even columns of the
 //   first and the odd ones of the second are the scores,
 //   O^T[2 d x 8] += (V_1 | V_2)^T . P^T.
+// P enters the second product in 16 bits.  a_1 - lambda a_2 may cancel, and the
+// row is normalised after it, so an error of P counts times |a| / |y|.  On bf16
+// pools P is therefore the sum of two bf16 numbers (2^-16 of it is lost, not
+// bf16's 2^-8) and has two MMAs per V fragment: 109.7 -> 110.6 us on the batch
+// below, 192.9 -> 194.2 with 8 heads over 8.  On 8-bit pools it is one fp16
+// number (2^-11): a second one would cost 5 % there (82.6 -> 87.6 us on int8), for
+// values that 8 bits hold to 2^-8 or worse.
+//
 // The pipeline (a producer warp issuing TMA loads of whole blocks, consumer
 // warps with their own online softmax, partials joined by log-sum-exp) and the
 // treatment of 8-bit codes are those of the decode kernel.
 //
 // Bound by the bytes of K and V: 64 sequences of 512..4096 tokens, 16 heads
-// over 4 KV heads of 2 x 128 (bf16), 109 us, 5600 GB/s or 82 % of the copy rate;
-// paged_attention_decode takes 105 for the same bytes.  Half of the scores'
+// over 4 KV heads of 2 x 128 (bf16), 110.6 us, 5530 GB/s or 81 % of the copy
+// rate; paged_attention_decode takes 105 for the same bytes.  Half of the scores'
 // MMA columns are computed and not used (each K tile meets both maps'
 // queries), which the tensor cores have to spare.
 #include <cuda.h>
@@ -385,19 +393,29 @@ __global__ void __launch_bounds__(kThreads)
             mlo = (k0 < valid ? 0x0000ffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
             mhi = (k0 + 8 < valid ? 0x0000ffffu : 0u) | (k0 + 9 < valid ? 0xffff0000u : 0u);
           }
-          uint32_t pb0 = 0u, pb1 = 0u;
+          // P^T as the B operand: tokens 2t, 2t + 1 of column g, and those 8 up
+          auto turned = [&](uint32_t r) {
+            const uint32_t a = __shfl_sync(0xffffffffu, r, src_a), b = __shfl_sync(0xffffffffu, r, src_b);
+            return prmt(a, b, half_sel);
+          };
+          uint32_t ph[2] = {0u, 0u};
+          [[maybe_unused]] uint32_t pl[2] = {0u, 0u};     // bf16: what the rounding to ph left
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            // P^T as the B operand (8-bit: one per value half, with its scale)
+            // (8-bit: one per value half, with its scale)
             if (x == 0 || kQ8) {
               const float vr = kQ8 ? blk_vr[2 * jb + x] : 1.0f;
-              const uint32_t r0 = pack2<kF16>(p0 * vr, p1 * vr), r1 = pack2<kF16>(p2 * vr, p3 * vr);
-              const uint32_t x0 = __shfl_sync(0xffffffffu, r0, src_a);
-              const uint32_t x1 = __shfl_sync(0xffffffffu, r0, src_b);
-              const uint32_t y0 = __shfl_sync(0xffffffffu, r1, src_a);
-              const uint32_t y1 = __shfl_sync(0xffffffffu, r1, src_b);
-              pb0 = prmt(x0, x1, half_sel);
-              pb1 = prmt(y0, y1, half_sel);
+              const float q0 = p0 * vr, q1 = p1 * vr, q2 = p2 * vr, q3 = p3 * vr;
+              const uint32_t r0 = pack2<kF16>(q0, q1), r1 = pack2<kF16>(q2, q3);
+              ph[0] = turned(r0);
+              ph[1] = turned(r1);
+              if constexpr (!kQ8) {
+                auto left = [](uint32_t r, float lo, float hi) {
+                  return pack2<false>(lo - __uint_as_float(r << 16), hi - __uint_as_float(r & 0xffff0000u));
+                };
+                pl[0] = turned(left(r0, q0, q1));
+                pl[1] = turned(left(r1, q2, q3));
+              }
             }
             const uint32_t vx = vb + x * G::kTensorBytes;
             if constexpr (!kQ8) {
@@ -410,7 +428,8 @@ __global__ void __launch_bounds__(kThreads)
                 fa[1] &= mlo;
                 fa[2] &= mhi;
                 fa[3] &= mhi;
-                mma16816<false>(o[x][i], fa, pb0, pb1);
+                mma16816<false>(o[x][i], fa, ph[0], ph[1]);
+                mma16816<false>(o[x][i], fa, pl[0], pl[1]);
               }
             } else {
               constexpr int NB = D / 8;                 // bytes per lane per token
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(kThreads)
                   fa[2] &= mhi;
                   fa[3] &= mhi;
                 }
-                mma16816<true>(o[x][i], fa, pb0, pb1);
+                mma16816<true>(o[x][i], fa, ph[0], ph[1]);
               }
             }
           }

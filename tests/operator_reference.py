@@ -171,7 +171,9 @@ def prompt_weights(pool, q, counts, weights, scale, accumulate=True):
     return w, wtol
 
 
-def diff_attention(pool, q, scale, lam, norm_weight, eps):
+def diff_attention(pool, q, scale, lam, norm_weight, eps, p_off=2.0 ** -8):
+    """(out, bound of out); p_off bounds the relative error with which a
+    softmax weight enters the product with V."""
     B, rows, d = q.shape
     H, Hkv = rows // 2, pool.heads // 2
     G = H // Hkv
@@ -184,7 +186,7 @@ def diff_attention(pool, q, scale, lam, norm_weight, eps):
             for m in (0, 1):
                 p, rel = softmax_bound(q[b, 2 * h + m:2 * h + m + 1].double(), pool.rows("k", b, 2 * j + m), scale)
                 a.append((p @ V)[0])
-                e.append(((2.0 ** -8 + rel) * 1.01 * (p @ V.abs()))[0])
+                e.append(((p_off + rel) * 1.01 * (p @ V.abs()))[0])
             y = a[0] - lam[h].double() * a[1]
             off = e[0] + lam[h].double().abs() * e[1] + 2.0 ** -22 * (a[0].abs() + a[1].abs())
             if norm_weight is not None:

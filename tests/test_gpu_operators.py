@@ -921,3 +921,28 @@ def test_diff_value_half_of_zeros(pkv):
         out = diff(pkv, pool, q, 0.125, lam, None)
         want, tol = ref.diff_attention(pool, q, 0.125, lam, None, 1e-5)
         within(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype,block,dim,L", [("bf16", 16, 64, [1, 200]), ("bf16", 32, 128, [700, 33]),
+                                               ("bf16", 16, 128, [2500]), ("int8", 16, 128, [700, 33]),
+                                               ("fp8", 32, 64, [300])])
+@pytest.mark.parametrize("norm", [False, True])
+def test_diff_of_maps_that_cancel(pkv, dtype, block, dim, L, norm):
+    """Two maps that are nearly one, lambda near 1: the difference is a small
+    part of either, and the errors of P count so many times more.  P as two
+    bf16 numbers is off by 2^-16 (2^-8 of what the first left, itself 2^-8 of P);
+    as fp16 by 2^-11, and by 2^-25 of the sum below fp16's normal numbers, which
+    over 700 tokens is 2^-15; the fp32 sums over a warp's third of the tokens,
+    truncated, by 2^-23 a step of 16 and the rescaling, 2^-16 over 2500."""
+    pool = ref.Pool(L, 2, dim, block, dtype, seed=8)
+    q = pool.randn(len(L), 8, dim, scale=2.0)
+    ref.raw(pool.k)[:, :, 1] = ref.raw(pool.k)[:, :, 0]
+    if dtype != "bf16":
+        pool.k_scale[:, 1] = pool.k_scale[:, 0]
+    q[:, 1::2] = (q[:, ::2].float() * (1 + 0.1 * torch.randn(q[:, ::2].shape, generator=pool.g))).to(torch.bfloat16)
+    lam = torch.full((4,), 0.96875)
+    weight = 0.5 + torch.rand(2 * dim, generator=pool.g) if norm else None
+    out = diff(pkv, pool, q, dim ** -0.5, lam, weight)
+    p_off = 2.0 ** -16 + 2.0 ** -16 if dtype == "bf16" else 2.0 ** -11 + 2.0 ** -15 + 2.0 ** -16
+    want, tol = ref.diff_attention(pool, q, dim ** -0.5, lam, weight, 1e-5, p_off)
+    within(out, want, tol)
