@@ -113,11 +113,12 @@ def softmax_bound(q, K, scale):
     """Softmax rows of q K^T in 64 bits and a bound on the relative error of
     every weight computed from fp32 scores: a score of d products accumulated
     in fp32 (truncation allowed: a whole unit 2^-23 per addition) is off by at
-    most d 2^-23 sum |q k| scale, a weight by twice the largest of its row's
-    (its own score and the denominator's), plus a few units of exp2, the
-    division and the sums."""
+    most d 2^-23 sum |q k| |scale| (scaling by s makes s e of an error e, of size
+    |s| |e|: under a negative scale the bound is no negative number), a weight
+    by twice the largest of its row's (its own score and the denominator's),
+    plus a few units of exp2, the division and the sums."""
     S = q @ K.T * scale
-    off = q.shape[-1] * 2.0 ** -23 * (q.abs() @ K.abs().T * scale).amax(dim=-1, keepdim=True)
+    off = q.shape[-1] * 2.0 ** -23 * (q.abs() @ K.abs().T * abs(scale)).amax(dim=-1, keepdim=True)
     off = off + S.abs().amax(dim=-1, keepdim=True) * 2.0 ** -22     # the base-2 scaling
     return torch.softmax(S, dim=-1), torch.expm1(2 * off) + 2.0 ** -19
 

@@ -244,6 +244,63 @@ def test_graph_of_every_operator(pkv, dtype):
     assert pkv.get_status()[1] == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+def test_overlapping_calls(pkv, dtype):
+    """Every operator on two streams at once, each with a state of its own, in
+    small batches (clusters of CTAs side by side): the bits of the calls alone."""
+    H, d, bs, G, L = 2, 64, 16, 2, [2000, 700]
+
+    def state(seed):
+        pool = ref.Pool(L, H, d, bs, dtype, seed=seed)
+        k, v, sc, bt, sl = pool.on()
+        i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+        bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        return dict(k=k, v=v, sc=sc, bt=bt, sl=sl, q=pool.randn(2, H * G, d, scale=2.0).cuda(),
+                    few=pool.randn(7, H * G, d, scale=2.0).cuda(), many=pool.randn(300, H * G, d, scale=2.0).cuda(),
+                    fs=torch.tensor([0, 4, 7], dtype=torch.int32, device="cuda"),
+                    ms=torch.tensor([0, 180, 300], dtype=torch.int32, device="cuda"),
+                    new=[pool.randn(2, H, d, scale=2.0).cuda() for _ in range(2)],
+                    lam=torch.full((1,), 0.4, device="cuda"), qd=pool.randn(2, 2, d, scale=2.0).cuda(),
+                    w=torch.rand((2, H, 2000), generator=pool.g).cuda(), idx=i32(2, H, 600), num=i32(2),
+                    out=bf(2, H * G, d), od=bf(2, 1, 2 * d),
+                    ws=[workspace(n) for n in (pkv.weights_workspace_bytes(2, H * G, d, 2000, bs),
+                                               pkv.attention_weights_workspace_bytes(300, H * G, 2000),
+                                               pkv.diff_workspace_bytes(2, 1, d, 2000, bs))])
+
+    def run(s, stream):
+        k, v, bt, sl, sc, w = (s[n] for n in ("k", "v", "bt", "sl", "sc", "w"))
+        if dtype != "bf16":
+            pkv.append_scaled(*s["new"], k, v, sc["k_scale"], sc["v_scale"], bt, sl, stream=stream)
+        for q, qs, n in ((s["few"], s["fs"], 4), (s["many"], s["ms"], 180)):
+            pkv.attention_weights(w, q, k, bt, sl, qs, 2000, n, 0.125, s["ws"][1], k_scale=sc["k_scale"], stream=stream)
+        pkv.paged_attention_decode_weights(s["out"], w, s["q"], k, v, bt, sl, 2000, 0.125, s["ws"][0], stream=stream, **sc)
+        pkv.paged_diff_attention_decode(s["od"], s["qd"], k, v, bt, sl, 2000, 0.125, s["lam"], None,
+                                        workspace=s["ws"][2], stream=stream, **sc)
+        pkv.select_tokens(s["idx"], s["num"], w, sl, 2000, 100, stream=stream)
+        pkv.evict_tokens(k, v, bt, sl, s["idx"], s["num"], weights=w, stream=stream, **sc)
+
+    def results(s):
+        torch.cuda.synchronize()
+        return [s[n].cpu() for n in ("k", "v", "w", "idx", "num", "out", "od")] + \
+            [x.cpu() for x in s["sc"].values() if x is not None]
+
+    alone = []
+    for seed in (1, 2):
+        s = state(seed)
+        run(s, torch.cuda.current_stream().cuda_stream)
+        alone.append(results(s))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        both = [state(seed) for seed in (1, 2)]
+        torch.cuda.synchronize()
+        for s, stream in zip(both, streams):
+            run(s, stream.cuda_stream)
+        for s, want in zip(both, alone):
+            for a, b in zip(results(s), want):
+                assert same_bits(a, b)
+    assert pkv.get_status()[1] == 0
+
+
 def test_argument_checks(pkv):
     """Shapes, types and layouts that do not fit are refused before a launch."""
     pool = ref.Pool([40, 20], 2, 64, 16, "int8", seed=1, extra=4)

@@ -262,6 +262,53 @@ def test_prompt_weights_steep_scores(pkv, dtype, scale):
     within(w, want, tol)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("scale", [0.125, 3.0, -0.125, 0.0])
+@pytest.mark.parametrize("n,group", [(5, 2), (16, 2), (3, 1), (1, 32)])
+@pytest.mark.parametrize("accumulate", [True, False])
+def test_prompt_weights_steep_scores_of_few_rows(pkv, dtype, scale, n, group, accumulate):
+    """The one-pass kernel (at most 32 rows) under steep scores, negative ones
+    and none, added to earlier weights and stored over anything."""
+    L = [260, 1100, n]
+    pool = ref.Pool(L, 1, 64, 16, dtype, seed=11)
+    q = pool.randn(3 * n, group, 64, scale=2.0)
+    for b in (0, 1):
+        for j in range(16):                                   # the first keys are small
+            ref.raw(pool.k)[pool.tables[b, 0].item(), j] = 0
+    weights = torch.rand((3, 1, 1100), generator=pool.g) if accumulate else torch.full((3, 1, 1100), float("nan"))
+    w = prompt_weights(pkv, pool, q, [n] * 3, weights, scale, accumulate)
+    want, tol = ref.prompt_weights(pool, q, [n] * 3, torch.nan_to_num(weights), scale, accumulate)
+    for b, m in enumerate(L):
+        within(w[b, :, :m], want[b, :, :m], tol[b, :, :m])
+        assert same_bits(w[b, :, m:], weights[b, :, m:])
+
+
+@pytest.mark.parametrize("dtype,block,dim", POOLS)
+@pytest.mark.parametrize("group,counts", [(11, [2, 1, 0]), (24, [1, 1, 1]), (31, [1, 0, 1]), (130, [3, 1, 2]),
+                                          (128, [2, 1, 1])])
+def test_prompt_weights_large_groups(pkv, dtype, block, dim, group, counts):
+    """Groups that leave rows of a tile unused, and ones past a row tile."""
+    pool = ref.Pool([200, 70, 33], 1, dim, block, dtype, seed=group)
+    q = pool.randn(sum(counts), group, dim, scale=2.0)
+    weights = torch.rand((3, 1, 211), generator=pool.g) * group / 50
+    w = prompt_weights(pkv, pool, q, counts, weights, dim ** -0.5)
+    want, tol = ref.prompt_weights(pool, q, counts, weights, dim ** -0.5)
+    within(w, want, tol)
+    for b, m in enumerate(pool.L):
+        assert same_bits(w[b, :, m:], weights[b, :, m:])
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 2), ("bf16", 5), ("bf16", 40), ("fp8", 5), ("int8", 12)])
+def test_prompt_weights_of_a_long_context(pkv, dtype, n):
+    """The last queries of contexts past what a cluster's TMEM holds."""
+    pool = ref.Pool([20001, 8193, 50], 1, 64, 32, dtype, seed=n)
+    q = pool.randn(3 * n, 4, 64, scale=2.0)
+    weights = torch.rand((3, 1, 20100), generator=pool.g) / 1000
+    w = prompt_weights(pkv, pool, q, [n] * 3, weights, 0.125)
+    want, tol = ref.prompt_weights(pool, q, [n] * 3, weights, 0.125)
+    within(w, want, tol)
+
+
 def test_prompt_weights_of_one_token_are_the_decode_step(pkv):
     L = [300, 41]
     pool = ref.Pool(L, 2, 128, 32, "bf16", seed=9)
@@ -480,6 +527,17 @@ def test_select_long(pkv, L, budget, recent):
     assert torch.equal(idx, want)
 
 
+def test_select_longest_rows(pkv):
+    """The longest rows that the call takes."""
+    L = [1 << 21, 5, (1 << 21) - 77]
+    g = torch.Generator().manual_seed(2)
+    w = torch.randn((3, 1, 1 << 21), generator=g)
+    w[0, 0, ::3] = 0.5
+    idx, num = select(pkv, w, L, 5000, 17)
+    want, wnum = ref.select(w, L, 5000, 17)
+    assert torch.equal(num, wnum) and torch.equal(idx, want)
+
+
 def test_select_bad_lengths(pkv):
     w = torch.rand((4, 2, 64))
     idx, num = select(pkv, w, [0, 64, -3, 65], 8, 2)
@@ -556,6 +614,18 @@ def test_evict_many_rounds(pkv, dtype, block, dim, fresh):
     want = ref.evict(pool, idx, num, dst, weights)
     for _ in range(5):
         check_evict(evict(pkv, pool, idx, num, dst if fresh else None, weights), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+def test_evict_nothing_kept_and_padding(pkv, dtype):
+    """Sequences that keep nothing, or are padding of length 0, beside one that
+    is packed."""
+    pool = ref.Pool([50, 0, 70], 2, 64, 16, dtype, seed=9)
+    idx, num = random_keep(pool, 20, 2, pool.g)
+    num[0] = 0
+    weights = torch.rand((3, 2, 80), generator=pool.g)
+    got = evict(pkv, pool, idx, num, None, weights)
+    check_evict(got, ref.evict(pool, idx, num, pool.tables, weights))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
@@ -798,6 +868,47 @@ def test_append_then_attend(pkv):
             assert ((val - x).abs() <= step[:, :, None] * 0.5 * 8).all()
             assert ((val - x).abs().mean() <= step.mean() * 0.5)
     assert pkv.get_status()[1] == 0
+
+
+@pytest.mark.parametrize("dtype,block", [("int8", 16), ("fp8", 32)])
+def test_appended_pool_is_attended(pkv, dtype, block):
+    """Prompts and decode steps through the append, then the plain decode, the
+    decode with weights, the weights of several queries and the differential
+    attention over what it stored, against 64 bits of the stored codes."""
+    d, H, G = 64, 2, 2
+    L = [20, 33, 100]
+    pool = ref.Pool([n + 6 for n in L], H, d, block, dtype, seed=5)
+    k, v, sc, bt, sl = pool.on()
+    for x in sc.values():
+        x.fill_(float("nan"))                                 # the append makes every scale
+    sl.copy_(torch.tensor(L))
+    qs = torch.tensor(np.concatenate([[0], np.cumsum(L)]), dtype=torch.int32, device="cuda")
+    T = sum(L)
+    pkv.append_scaled(pool.randn(T, H, d).cuda(), pool.randn(T, H, d).cuda(), k, v, sc["k_scale"], sc["v_scale"],
+                      bt, sl, qs, max(L))
+    for i in range(6):
+        sl += 1
+        size = 0.5 + i
+        pkv.append_scaled(pool.randn(3, H, d, scale=size).cuda(), pool.randn(3, H, d, scale=size).cuda(), k, v,
+                          sc["k_scale"], sc["v_scale"], bt, sl)
+    pool.k, pool.v, pool.k_scale, pool.v_scale = k.cpu(), v.cpu(), sc["k_scale"].cpu(), sc["v_scale"].cpu()
+    assert sl.tolist() == pool.L
+    top, scale = max(pool.L), d ** -0.5
+    q = pool.randn(3, H * G, d)
+    weights = torch.rand((3, H, top), generator=pool.g)
+    want, tol, ww, wtol = ref.decode_weights(pool, q, weights, scale)
+    out, w = decode_weights(pkv, pool, q, weights, scale)
+    within(out, want, tol)
+    within(w, ww, wtol)
+    plain = torch.full_like(out, float("nan"))
+    pkv.paged_attention_decode(plain, q.cuda(), k, v, bt, sl, top, scale,
+                               workspace(pkv.workspace_bytes(3, H * G, d, top, block)), **sc)
+    within(plain, want, tol)
+    counts = [4, 1, 7]
+    q = pool.randn(12, H * G, d)
+    within(prompt_weights(pkv, pool, q, counts, weights, scale), *ref.prompt_weights(pool, q, counts, weights, scale))
+    q, lam = pool.randn(3, 4, d), torch.tensor([0.3, 0.8])
+    within(diff(pkv, pool, q, scale, lam, None), *ref.diff_attention(pool, q, scale, lam, None, 1e-5))
 
 
 def test_append_bad_sequences(pkv):
