@@ -708,7 +708,9 @@ size_t pagedkv_attention_weights_workspace_bytes(int num_tokens,
  * weights of these queries alone).  n_b == 0 leaves the sequence's entries as
  * they are, and so do bad offsets, lengths and blocks (flagged as in
  * paged_attention_multi).  V is not read.  Any group of query heads per KV
- * head.  Other arguments as for paged_attention_multi; the workspace is
+ * head.  Other arguments as for paged_attention_multi (a max_seq_len far above
+ * the lengths costs time: at most 32 rows of query tokens x grouped heads under
+ * one of 8192 or less take one pass over K); the workspace is
  * 16-byte aligned, pagedkv_attention_weights_workspace_bytes(...).  One to
  * four launches, asynchronous on `stream`; no atomics, so equal inputs give
  * equal bits.  After PAGEDKV_FLAG_WAIT_TIMEOUT entries may be missing the

@@ -11,10 +11,10 @@
 // grows, the rows already in the block are coded again under the new one.
 // Warps never share a block, so there are no atomics and no second pass.
 //
-// Bytes bound it up to the arithmetic of the codes: eight prompts of 1..8K
-// tokens (8 heads of 128, E4M3) take 50 us, 4700 GB/s or 69 % of the copy rate
-// (84 us with a division per element); 128 single tokens 10.6 us, the call
-// itself.
+// The arithmetic of the codes and the loads' latency bound it together (issue
+// slots 59 %, DRAM 51 % in use): eight prompts of 1..8K tokens (8 heads of 128)
+// take 52 us on E4M3, 4470 GB/s or 66 % of the copy rate (84 us with a division
+// per element), and 67 us on int8; 128 single tokens 10.6 us, the call itself.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

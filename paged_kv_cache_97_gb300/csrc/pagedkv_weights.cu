@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
 // are not positive, groups of more than 128 heads.  The two reads of K and the
 // issue of the loads' and exponentials' instructions share the bound: 64
 // sequences of 512..4096 tokens x five queries, 32/8 heads, 189 us on a bf16
-// pool and 196 on int8 (one pass with the scores in TMEM: 103 and 139), 64/8
+// pool and 196 on int8 (one pass with the scores in TMEM: 103 and 140), 64/8
 // heads on int8 232.
 
 constexpr int kRowTile = 64;                           // rows of Q per tile
@@ -653,7 +653,7 @@ kv_status pagedkv_attention_weights(float* weights, int weights_stride, const vo
   cudaStream_t s = (cudaStream_t)stream;
   // Few rows whose scores fit a cluster's TMEM: one pass over K (64 sequences of
   // 512..4096 tokens, five queries each, 32/8 heads: two passes of the mma.sync
-  // kernels 189 us, one pass 103; int8 196 and 139).
+  // kernels 189 us, one pass 103; int8 196 and 140).
   const int ctas = longest * G <= kFewRows ? few_rows_ctas(batch, num_kv_heads, max_seq_len, di.num_sms) : 0;
   if (ctas > 0) {
     a.tile_tokens = (int)(kFewRows / G);

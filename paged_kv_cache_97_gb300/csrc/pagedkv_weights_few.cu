@@ -28,7 +28,7 @@
 //
 // 8-bit pools: the key warps load the codes themselves, a chunk ahead, and widen
 // them to bf16 (exact) into the stage; a key's K scale multiplies its scores.
-// The same batch: int8 139 us, E4M3 135 (196 and 189 in two passes), bound by
+// The same batch: int8 140 us, E4M3 136 (196 and 189 in two passes), bound by
 // the widening beside the sweeps.
 #include <cooperative_groups.h>
 #include <cuda.h>

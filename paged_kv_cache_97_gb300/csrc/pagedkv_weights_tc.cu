@@ -29,10 +29,12 @@
 // near its end: 290.
 //
 // No unit of the SM is busy more than about 55 % of a long prompt (one of 16K
-// tokens, 32/8 heads, bf16: 1669 us, 900 cycles per 128 x 128 tile): its
-// 16384 exponentials take 512 cycles at 32 per clock, its MMAs 512 (both
-// operands come from shared memory), its instructions about as many issue
-// slots, and the row warps wait for their own chains.  So each score costs one
+// tokens, 32/8 heads, bf16: 1678 us, 900 cycles per 128 x 128 tile): its
+// 16384 exponentials take 512 cycles at 32 per clock, its MMAs 512, its
+// instructions about as many issue slots.  The rest is the chain of a chunk: its
+// load into one of two stages, its MMA and the hand-over, which two CTAs per SM
+// hide in part (with the row warps idle the row statistics of 8K tokens take 198
+// of 227 us).  So each score costs one
 // packed half of a multiply-add and of an add (f32x2), and no maximum: a row's
 // reference is its first scores' and moves only when a sum grows past 2^60; the
 // scores are read 64 columns at a time and their buffer is free before they are
@@ -46,7 +48,11 @@
 // (exact: 8 significant bits hold every int8 and E4M3 code) and write them into
 // the swizzled image, the streamed keys two chunks ahead, right after the
 // scores of the chunk that used the stage before; a block's K scale multiplies
-// its scores (one prompt of 8K tokens, E4M3: 780 us).
+// its scores (one prompt of 8K tokens: E4M3 787 us, int8 827, bf16 477).
+//
+// Before the first pass every row is marked as without statistics, so that what
+// a unit leaves out when a wait gives up is left out of the weights too (2 us:
+// 4 prompts 230 -> 232).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
