@@ -1057,3 +1057,23 @@ def test_diff_of_maps_that_cancel(pkv, dtype, block, dim, L, norm):
     p_off = 2.0 ** -16 + 2.0 ** -16 if dtype == "bf16" else 2.0 ** -11 + 2.0 ** -15 + 2.0 ** -16
     want, tol = ref.diff_attention(pool, q, dim ** -0.5, lam, weight, 1e-5, p_off)
     within(out, want, tol)
+
+
+@pytest.mark.parametrize("dim,L", [(64, 40), (128, 700)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_diff_values_that_are_not_finite(pkv, dim, L, value):
+    """One such value makes its element not finite (NaN, the difference of two
+    infinities, under a lambda that is not negative) and no other; with a norm
+    it reaches its row, and no other row."""
+    pool = ref.Pool([L, 50], 4, dim, 16, "bf16", seed=3)
+    q = pool.randn(2, 8, dim, scale=2.0)
+    lam = torch.tensor([0.4, -0.4, 0.0, 0.9])
+    want, tol = ref.diff_attention(pool, q, dim ** -0.5, lam, None, 1e-5)
+    at = L // 2
+    pool.v[pool.tables[0, at // 16].item(), at % 16, 1, 5] = value   # element dim + 5 of KV head 0's heads
+    out = diff(pkv, pool, q, dim ** -0.5, lam, None).cpu()
+    assert torch.isnan(out[0, 0, dim + 5]) and not torch.isfinite(out[0, 1, dim + 5])
+    out[0, :2, dim + 5] = want[0, :2, dim + 5]
+    within(out, want, tol)
+    out = diff(pkv, pool, q, dim ** -0.5, lam, torch.ones(2 * dim)).cpu()
+    assert torch.isnan(out[0, 0]).all() and torch.isfinite(out[0, 2:].float()).all() and torch.isfinite(out[1].float()).all()
