@@ -94,9 +94,11 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
 #pragma unroll
   for (int g = 0; g < kMaxGroup; ++g)
     if (g < GQ) s[g] = __ldcs(reinterpret_cast<const float4*>(sc + g * a.score_stride + t));
-  float sum[4];
+  float old[4], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sum[k] = t + k < L - 1 ? w[t + k] : 0.0f;
+  for (int k = 0; k < 4; ++k) old[k] = t + k < L - 1 ? w[t + k] : 0.0f;
+  // (the rows' sum first: added one by one to an entry that has grown, weights
+  // below half its last place would all be lost)
 #pragma unroll
   for (int g = 0; g < kMaxGroup; ++g) {
     if (g >= GQ) break;
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(kStepThreads) step_weights_kernel(const StepAr
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (t + k < L) w[t + k] = sum[k];
+    if (t + k < L) w[t + k] = old[k] + sum[k];
 }
 
 // ---------------------------------------------------------------------------

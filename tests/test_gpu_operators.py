@@ -113,6 +113,30 @@ def test_decode_weights_output_is_the_decode_attention(pkv):
     assert (total - 4).abs().max() <= 4 * 2.0 ** -17       # 700 weights, each with a relative error of 2^-18
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "int8", "fp8"])
+def test_decode_weights_add_up_small_ones(pkv, dtype):
+    """Weights of 2^-24.1 from each of eight heads, on entries of 1: none alone
+    changes the entry, their sum 2^-21.1 does.  (One rounding of the sum, 2^-24
+    of the entry, is within the bound's 2^-22.)"""
+    pool = ref.Pool([600, 40], 1, 64, 16, dtype, seed=1)
+    ref.raw(pool.k)[:] = 0
+    one = {"bf16": 0x3F80, "int8": 1, "fp8": 0x38}[dtype]
+    for b in (0, 1):
+        k = pool.k.view(torch.int16) if dtype == "bf16" else ref.raw(pool.k)
+        k[pool.tables[b, 0].item(), 3, 0, 0] = one
+    if dtype != "bf16":
+        pool.k_scale[:] = 1.0
+    q = torch.zeros((2, 8, 64), dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    weights = torch.ones((2, 1, 600))
+    scale = 24.1 * 0.6931471805599453
+    out, w = decode_weights(pkv, pool, q, weights, scale)
+    want, tol, ww, wtol = ref.decode_weights(pool, q, weights, scale)
+    assert abs(ww[0, 0, 100].item() - 1 - 2.0 ** -21.1) < 2.0 ** -24
+    within(w[0], ww[0], wtol[0])
+    within(w[1, :, :40], ww[1, :, :40], wtol[1, :, :40])
+
+
 def test_decode_weights_shared_blocks(pkv):
     """Sequences that share physical blocks keep weights of their own."""
     pool = ref.Pool([64, 64, 64], 2, 64, 16, "bf16", seed=3)
