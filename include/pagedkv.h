@@ -632,9 +632,10 @@ size_t pagedkv_diff_workspace_bytes(int batch, int num_heads, int head_dim,
  * the calls above.  A factor on the normalised row (1 - lambda_init) belongs
  * in norm_weight.  Scores, softmax sums, both products' sums, the difference and
  * the norm are fp32; the softmax weights enter the product with V to 2^-16 of
- * their value on bf16 pools and 2^-11 on 8-bit pools (fp16, relative to the
- * largest V scale of their value half among 256 to 2048 tokens), which counts
- * |a_0| / |y| times where the difference cancels.  An infinity or NaN among
+ * their value on bf16 pools, and as fp16 on 8-bit pools (2^-11 of their value,
+ * at best 2^-25 of the largest weight times V scale of their value half among
+ * 256 to 2048 tokens), which counts |a_0| / |y| times where the difference
+ * cancels.  An infinity or NaN among
  * the values of the sequence's tokens leaves its element NaN (or, under a
  * negative lambda, infinite) and with a norm the row's others NaN or 0; rows
  * of a block past the sequence's last token may hold anything.
