@@ -787,6 +787,185 @@ kv_status pagedkv_evict_tokens(void *k_cache, void *v_cache, float *k_scale,
                                void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Rotated append, 4-bit pools, verification of drafts                      */
+/* ------------------------------------------------------------------------ */
+
+/* One step's new rows in one launch: queries and keys rotated by their
+ * positions, keys and values stored in the pool (what comes before
+ * paged_attention_decode or paged_attention_multi in a model with rotary
+ * positions).  Sequence b's n_b = query_start[b + 1] - query_start[b] new tokens
+ * are its last n_b ones (seq_lens counts them), rows query_start[b] .. of q, k
+ * and v; token i of them has the cache position seq_lens[b] - n_b + i.
+ * Frequency j < rotary_dim / 2 of a head turns the pair (x1, x2) of elements
+ * (j, j + rotary_dim / 2), or with interleaved != 0 (2 j, 2 j + 1), into
+ *   x1 c - x2 s,  x2 c + x1 s
+ * with c = cos_sin[p][j], s = cos_sin[p][rotary_dim / 2 + j] and p the token's
+ * position on j's axis; elements from rotary_dim on are kept.  fp32, every
+ * product and sum rounded once, then rounded to bf16: a key is stored from that
+ * bf16 row exactly as reshape_and_cache stores it (8-bit pools: under the block's
+ * scale as it is).
+ *   q_out, q      device bf16, num_q_heads rows of head_dim per token; q_out may
+ *                 be q (with the same stride).  Both NULL (num_q_heads is then
+ *                 ignored): keys and values alone.
+ *   k, v          device bf16, num_kv_heads rows per token
+ *   *_stride      elements from one token's rows to the next's: a multiple of 8,
+ *                 at least the heads' size (q, k and v may lie in one projection)
+ *   cos_sin       device fp32 [max_position, rotary_dim]; NULL: nothing is
+ *                 rotated (rotary_dim, positions and the axes are then ignored)
+ *   rotary_dim    a multiple of 16, at most head_dim
+ *   positions     device int32 [num_axes, num_tokens], or NULL with one axis: the
+ *                 cache position
+ *   num_axes      1 to 4 (time, height and width of images and video, say)
+ *   axis_sections host int32 [num_axes]: axis x has the next axis_sections[x] of
+ *                 the rotary_dim / 2 frequencies; NULL with one axis
+ *   block_tables, max_blocks_per_seq, seq_lens, batch  as for pagedkv_multi_step
+ *   query_start   device int32 [batch + 1], or NULL: one token per sequence
+ *                 (num_tokens == batch); n_b == 0 is allowed
+ *   max_query_len host bound on every n_b
+ * All rows 16-byte aligned.  Two tokens of a call must not share a slot.  A token
+ * with bad offsets or length (PAGEDKV_FLAG_BAD_SEQ_LEN) or a position outside
+ * [0, max_position) (PAGEDKV_FLAG_BAD_INDEX) stores nothing and gets zeros in
+ * q_out; a table entry outside the pool (PAGEDKV_FLAG_BAD_BLOCK) stores nothing,
+ * q_out is written.  Rows that belong to no sequence are left as they are.
+ * Asynchronous on `stream`. */
+kv_status pagedkv_append_rotary(
+    void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+    void *k_cache, void *v_cache, const float *k_scale, const float *v_scale,
+    const float *cos_sin, int max_position, int rotary_dim, int interleaved,
+    const int32_t *positions, int num_axes, const int32_t *axis_sections,
+    const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *seq_lens, const int32_t *query_start, int batch,
+    int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+    int head_dim, int num_blocks, int block_size, kv_dtype dtype, void *stream);
+
+/* 4-bit pools.  One device tensor holds K and V: kv_cache [num_blocks,
+ * num_kv_heads, record], 16-byte aligned, record = pagedkv_q4_record_bytes =
+ * block_size * head_dim * 9 / 8 bytes (4.5 bits per value):
+ *   K's codes  [block_size][head_dim / 2],  V's codes  likewise,
+ *   K's pairs  [block_size][head_dim / 64] of (scale, min) bf16,  V's  likewise.
+ * A code c in 0..15 stands for min + scale * c with its row's pair of its 64
+ * elements.  Element e of a row is nibble e % 8 (a byte's low one first) of the
+ * 32-bit little-endian word (e % 64 / 8) * (head_dim / 64) + e / 64 of its codes.
+ * head_dim 64 or 128, block_size 16 or 32.  Tables, lengths, the block pool's
+ * bookkeeping (kv_pool_*, whose dtype then only sets kv_pool_block_bytes) and
+ * errors are those of the other pools. */
+size_t pagedkv_q4_record_bytes(int block_size, int head_dim);
+
+/* pagedkv_append_rotary into a 4-bit pool (cos_sin NULL: a plain append).  Per
+ * 64 elements of a bf16 row, in fp32:
+ *   min   = the least element
+ *   scale = (largest - min) * fp32(1 / 15), up to the next bf16 number, 2^-126 at
+ *           least
+ *   code  = round_half_even((x - min) * (1 / scale)), held in 0..15;
+ * NaN counts as 0, magnitudes above 2^126 (infinities too) as 2^126, -0 as 0.  A
+ * stored value is off by at most half a scale of its 64 elements. */
+kv_status pagedkv_append_rotary_q4(
+    void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+    void *kv_cache, const float *cos_sin, int max_position, int rotary_dim,
+    int interleaved, const int32_t *positions, int num_axes,
+    const int32_t *axis_sections, const int32_t *block_tables,
+    int max_blocks_per_seq, const int32_t *seq_lens,
+    const int32_t *query_start, int batch, int num_tokens, int max_query_len,
+    int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    int block_size, void *stream);
+
+/* The last n_b tokens' rows of a 4-bit pool as values, bf16(min + scale * code):
+ * k_out and v_out device bf16 [num_tokens, num_kv_heads, head_dim], 16-byte
+ * aligned; query_start, seq_lens and the tables as for pagedkv_append_rotary
+ * (n_b = seq_lens[b] reads a whole sequence).  Rows of a bad sequence or block are
+ * zero and flagged; rows that belong to no sequence are left as they are. */
+kv_status pagedkv_read_q4(void *k_out, void *v_out, const void *kv_cache,
+                          const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *seq_lens, const int32_t *query_start,
+                          int batch, int num_tokens, int max_query_len,
+                          int num_kv_heads, int head_dim, int num_blocks,
+                          int block_size, void *stream);
+
+/* pagedkv_copy_blocks for a 4-bit pool. */
+kv_status pagedkv_copy_blocks_q4(void *kv_cache, const int32_t *block_pairs,
+                                 int num_pairs, int num_blocks, int block_size,
+                                 int num_kv_heads, int head_dim, void *stream);
+
+/* Workspace bytes the two calls below may need, whatever the batch and the
+ * lengths (max_query_len 1 for paged_attention_decode_q4). */
+size_t pagedkv_q4_workspace_bytes(int max_query_len, int num_q_heads,
+                                  int num_kv_heads, int head_dim);
+
+/* paged_attention_decode and paged_attention_multi over a 4-bit pool; arguments,
+ * errors and the treatment of bad lengths, offsets and blocks as there (the rows
+ * of a sequence with n_b > max_query_len are all zeroed).  The codes enter both
+ * products exactly, q exactly down to 2^-27 of the largest |q| of the grouped
+ * heads; a weight times V's scale is one fp16 number (2^-11 of its value, at best
+ * 2^-30 of the largest weight * max(scale, |min| / 16) of the row, where one
+ * below 2^-100 counts as 2^-100); scores, weights' sums and both products' sums are fp32.
+ * Rows of a block past the sequence's last token may hold anything.  One or two
+ * launches, asynchronous on `stream`; no atomics, so equal inputs give equal
+ * bits. */
+kv_status paged_attention_decode_q4(
+    void *out, const void *q, const void *kv_cache,
+    const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *seq_lens, int batch, int num_q_heads, int num_kv_heads,
+    int head_dim, int num_blocks, int block_size, int max_seq_len, float scale,
+    void *workspace, size_t workspace_bytes, void *stream);
+kv_status paged_attention_multi_q4(
+    void *out, const void *q, const void *kv_cache,
+    const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *seq_lens, const int32_t *query_start, int batch,
+    int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads,
+    int head_dim, int num_blocks, int block_size, int max_seq_len, float scale,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Element type of probabilities. */
+typedef enum {
+    PAGEDKV_PROB_F32 = 0,
+    PAGEDKV_PROB_BF16 = 1,
+    PAGEDKV_PROB_F16 = 2
+} pagedkv_prob_dtype;
+
+/* The end of a speculative step (“让 Agent 跑得快”, §六 投机解码): which drafted
+ * tokens the target keeps, the token that follows them, and the lengths the
+ * cache goes on with.  Sequence b's rows query_start[b] .. are the step's n_b
+ * query tokens (those of paged_attention_multi): its last known token, then
+ * n_b - 1 drafts.  With r = query_start[b], x_i = tokens[r + i + 1], p_i = row
+ * r + i of target_probs (the target's distribution after query token i) and q_i =
+ * row r - b + i of draft_probs (the one x_i was drawn from; without draft_probs 1
+ * at x_i), draft i is kept while
+ *   uniform[r + i] * q_i(x_i) < p_i(x_i).
+ * With a the drafts kept before the first refusal, the next token z is drawn by
+ * u = uniform[r + n_b - 1] from the weights
+ *   max(p_a - q_a, 0) after a refusal (p_a itself where nothing is left),  p_a else:
+ * the lowest z whose inclusive sum exceeds u times the sum of all.
+ *   out_tokens[r ..]  x_0 .. x_{a-1}, z, then -1
+ *   num_accepted[b]   a
+ *   new_lens[b]       seq_lens[b] - n_b + 1 + a: the cached tokens that stay (z's
+ *                     own K and V are appended by the next step)
+ *   out_tokens, tokens  device int32 [num_tokens], different buffers
+ *   target_probs  device [num_tokens, vocab], draft_probs [num_tokens - batch,
+ *                 vocab] or NULL, of `dtype`; uniform device fp32 [num_tokens]
+ *   query_start   device int32 [batch + 1]; n_b == 0 (without draft_probs) gives
+ *                 num_accepted 0 and the length as it is
+ *   seq_lens, new_lens  device int32 [batch], both or neither; may be one buffer
+ *   max_query_len host bound on every n_b;  vocab less than 2^19
+ * A weight counts as 0 where it is NaN or negative and as 1 above 1, a draft
+ * compared with NaN is refused; the difference p - q is one fp32 number, and the
+ * weights, held to 2^-45 each, are added without further rounding, so the drawn token does not depend on how the
+ * row was split.  u counts as 0 if NaN or negative, as the last number below 1
+ * from 1 on; a row without weight gives vocab - 1.  A draft outside [0, vocab) is
+ * refused (the next token is then drawn from p_a) and sets
+ * PAGEDKV_FLAG_BAD_INDEX; offsets or lengths that do not fit give num_accepted 0,
+ * the length as it is and -1 in the sequence's rows, and set
+ * PAGEDKV_FLAG_BAD_SEQ_LEN.  Rows that belong to no sequence are left as they
+ * are.  One launch, asynchronous on `stream`. */
+kv_status pagedkv_verify_drafts(
+    int32_t *out_tokens, int32_t *num_accepted, const int32_t *tokens,
+    const void *target_probs, const void *draft_probs, const float *uniform,
+    const int32_t *query_start, const int32_t *seq_lens, int32_t *new_lens,
+    int batch, int num_tokens, int max_query_len, int vocab,
+    pagedkv_prob_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */
 

@@ -25,9 +25,11 @@ KV_OK, KV_ERR_INVALID_ARG, KV_ERR_OUT_OF_BLOCKS, KV_ERR_CUDA, KV_ERR_DEVICE_INDE
 DTYPE_BF16, DTYPE_INT8, DTYPE_FP8_E4M3 = 0, 1, 2
 FLAG_BAD_SLOT, FLAG_BAD_BLOCK, FLAG_BAD_SEQ_LEN, FLAG_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 FLAG_BAD_INDEX = 0x10
+PROB_F32, PROB_BF16, PROB_F16 = range(3)
 
 # Every symbol include/pagedkv.h declares, with its ctypes signature.
 _P, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_L = ctypes.c_int64
 SIGNATURES = {
     "kv_pool_create": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_P)]),
     "kv_pool_destroy": (None, [_P]),
@@ -83,6 +85,18 @@ SIGNATURES = {
     "pagedkv_select_tokens": (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P]),
     "pagedkv_evict_tokens": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I,
                                   _I, _I, _I, _I, _P]),
+    "pagedkv_append_rotary": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I,
+                                   _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pagedkv_append_rotary_q4": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I,
+                                      _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pagedkv_q4_record_bytes": (_SZ, [_I, _I]),
+    "pagedkv_read_q4": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "pagedkv_copy_blocks_q4": (_I, [_P, _P, _I, _I, _I, _I, _I, _P]),
+    "pagedkv_q4_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "paged_attention_decode_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P]),
+    "paged_attention_multi_q4": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                      _SZ, _P]),
+    "pagedkv_verify_drafts": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
 }
 
 _lib = None
@@ -927,6 +941,276 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
         budget, _ptr(weights), stride, B, nb, bs, hkv, d, dt, _stream_on(stream, dev))
     if st != KV_OK:
         _check(st)
+
+
+# --------------------------------------------------------------------------
+# Rotated append, 4-bit pools, verification of drafts
+# --------------------------------------------------------------------------
+
+def _rows(t, name, dev, heads=None, d=None):
+    """The token stride of bf16 rows [tokens, heads, head_dim] on device `dev`
+    (the rows of a token are contiguous, its neighbours any stride away)."""
+    bf16 = _dtypes()[0]
+    try:
+        good = t.dtype is bf16 and t.get_device() == dev and t.dim() == 3
+    except AttributeError:
+        good = False
+    if not good:
+        _need(t, bf16, name, 3)
+        raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+    T, h, dim = t.shape
+    st, sh, sd = t.stride()
+    if heads is not None and (h != heads or dim != d):
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    if T and ((sd != 1 and dim > 1) or (sh != dim and h > 1)):
+        raise ValueError(f"{name}: the rows of a token must be contiguous")
+    return st if T > 1 else h * dim
+
+
+def _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens, positions, sections, rotary_dim,
+                 query_start, specs):
+    """The checks of append_rotary and append_rotary_q4 and the arguments they
+    share: (rows and strides), (rotation), (tables), T, query heads, device."""
+    _, i32, f32, _ = _dtypes()
+    specs += [(block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1)]
+    if cos_sin is not None:
+        specs.append((cos_sin, f32, "cos_sin", 2))
+    if positions is not None:
+        specs.append((positions, i32, "positions", 2))
+    if query_start is not None:
+        specs.append((query_start, i32, "query_start", 1))
+    dev = _need_all(*specs)
+    T, B = k.shape[0], seq_lens.shape[0]
+    rows = [None, 0, None, 0, k.data_ptr(), _rows(k, "k", dev, hkv, d), v.data_ptr(), _rows(v, "v", dev, hkv, d)]
+    if v.shape[0] != T:
+        raise ValueError("k and v disagree on the number of tokens")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out belong together")
+    hq = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        rows[:4] = [q_out.data_ptr(), _rows(q_out, "q_out", dev, hq, d), q.data_ptr(), _rows(q, "q", dev, hq, d)]
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q, q_out and k disagree on the number of tokens")
+    mb = block_tables.shape
+    if mb[0] != B:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+    if query_start is None:
+        if T != B:
+            raise ValueError("without query_start there is one token per sequence")
+    elif query_start.shape[0] != B + 1:
+        raise ValueError("query_start must have batch + 1 entries")
+    axes, sec, limit, width = 1, None, 0, 0
+    if cos_sin is not None:
+        limit, width = cos_sin.shape
+        if rotary_dim is not None and rotary_dim != width:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        if positions is not None:
+            axes = positions.shape[0]
+            if positions.shape[1] != T:
+                raise ValueError("positions must be [axes, tokens]")
+        if sections is not None:
+            if len(sections) != axes:
+                raise ValueError("one section per axis of positions is needed")
+            sec = (ctypes.c_int32 * len(sections))(*sections)
+    how = (_ptr(cos_sin), limit, width)
+    where = (_ptr(positions) if cos_sin is not None else None, axes, sec)
+    tables = (block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), _ptr(query_start), B, T)
+    return rows, how, where, tables, hq, dev
+
+
+def append_rotary(q_out, q, k, v, k_cache, v_cache, cos_sin, block_tables, seq_lens, positions=None, sections=None,
+                  interleaved=False, query_start=None, max_query_len=1, rotary_dim=None, k_scale=None, v_scale=None,
+                  stream=None):
+    """A step's queries and keys rotated by their positions, its keys and values
+    appended, in one launch: q bf16 [T, Hq, d] into q_out (or in place, or both
+    None), k and v bf16 [T, Hkv, d] into the pools (row query_start[b] + i at
+    position seq_lens[b] - n_b + i; one token per sequence without query_start).
+    Rows may lie in one projection (any token stride).  cos_sin fp32
+    [max_position, rotary_dim]: cosines, then sines (None: no rotation);
+    positions int32 [axes, T] with ``sections`` frequencies per axis, or None:
+    the cache positions.  ``interleaved``: pairs (2j, 2j + 1)."""
+    specs = []
+    dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
+    nb, bs, hkv, d = k_cache.shape
+    rows, how, where, tables, hq, dev = _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens,
+                                                     positions, sections, rotary_dim, query_start, specs)
+    st = load().pagedkv_append_rotary(*rows, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                                      *how, 1 if interleaved else 0, *where, *tables, int(max_query_len), hq, hkv, d,
+                                      nb, bs, dt, _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return q_out
+
+
+def q4_record_bytes(block_size, head_dim) -> int:
+    """Bytes of one (block, KV head) of a 4-bit pool, which is uint8
+    [num_blocks, num_kv_heads, record bytes] (0: unsupported sizes)."""
+    return load().pagedkv_q4_record_bytes(block_size, head_dim)
+
+
+def _pool_q4(kv_cache, block_size, specs):
+    """(num_blocks, num_kv_heads, head_dim) of a 4-bit pool; its check goes to specs."""
+    import torch
+    specs.append((kv_cache, torch.uint8, "kv_cache", 3))
+    if getattr(kv_cache, "dtype", None) is not torch.uint8 or kv_cache.dim() != 3:
+        _need(kv_cache, torch.uint8, "kv_cache", 3)
+        raise ValueError("kv_cache must be [num_blocks, num_kv_heads, record bytes]")
+    nb, hkv, rec = kv_cache.shape
+    d = rec * 8 // (9 * block_size) if block_size in (16, 32) else 0
+    if d not in (64, 128) or block_size * d * 9 // 8 != rec:
+        raise ValueError("kv_cache's last dimension must be q4_record_bytes(block_size, head_dim) (block_size 16 or "
+                         "32, head_dim 64 or 128)")
+    return nb, hkv, d
+
+
+def append_rotary_q4(q_out, q, k, v, kv_cache, cos_sin, block_tables, seq_lens, block_size, positions=None,
+                     sections=None, interleaved=False, query_start=None, max_query_len=1, rotary_dim=None,
+                     stream=None):
+    """append_rotary into a 4-bit pool (uint8 [num_blocks, Hkv,
+    q4_record_bytes]): every 64 values of a row as codes 0..15 under a (scale,
+    min) pair of their own."""
+    specs = []
+    nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
+    rows, how, where, tables, hq, dev = _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens,
+                                                     positions, sections, rotary_dim, query_start, specs)
+    st = load().pagedkv_append_rotary_q4(*rows, kv_cache.data_ptr(), *how, 1 if interleaved else 0, *where, *tables,
+                                         int(max_query_len), hq, hkv, d, nb, int(block_size), _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return q_out
+
+
+def read_q4(k_out, v_out, kv_cache, block_tables, seq_lens, block_size, query_start=None, max_query_len=1,
+            stream=None):
+    """The last n_b tokens of every sequence as values: k_out, v_out bf16 [T, Hkv,
+    d], row query_start[b] + i the token at position seq_lens[b] - n_b + i (one
+    token per sequence without query_start)."""
+    bf16, i32, _, _ = _dtypes()
+    specs = [(k_out, bf16, "k_out", 3), (v_out, bf16, "v_out", 3), (block_tables, i32, "block_tables", 2),
+             (seq_lens, i32, "seq_lens", 1)]
+    nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
+    if query_start is not None:
+        specs.append((query_start, i32, "query_start", 1))
+    dev = _need_all(*specs)
+    T, B = k_out.shape[0], seq_lens.shape[0]
+    mb = block_tables.shape
+    if k_out.shape != (T, hkv, d) or v_out.shape != k_out.shape or mb[0] != B:
+        raise ValueError("k_out, v_out must be [tokens, num_kv_heads, head_dim], the tables one row per sequence")
+    if query_start is None:
+        if T != B:
+            raise ValueError("without query_start there is one token per sequence")
+    elif query_start.shape[0] != B + 1:
+        raise ValueError("query_start must have batch + 1 entries")
+    st = load().pagedkv_read_q4(k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), mb[1],
+                                seq_lens.data_ptr(), _ptr(query_start), B, T, int(max_query_len), hkv, d, nb,
+                                int(block_size), _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return k_out, v_out
+
+
+def copy_blocks_q4(kv_cache, block_pairs, block_size, stream=None):
+    """copy_blocks for a 4-bit pool."""
+    specs = [(block_pairs, _dtypes()[1], "block_pairs", 2)]
+    nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
+    dev = _need_all(*specs)
+    if block_pairs.shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    _check(load().pagedkv_copy_blocks_q4(kv_cache.data_ptr(), block_pairs.data_ptr(), block_pairs.shape[0], nb,
+                                         int(block_size), hkv, d, _stream_on(stream, dev)))
+
+
+def q4_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_query_len=1) -> int:
+    return load().pagedkv_q4_workspace_bytes(max_query_len, num_q_heads, num_kv_heads, head_dim)
+
+
+def _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size, workspace, query_start):
+    bf16, i32, _, _ = _dtypes()
+    specs = [(out, bf16, "out", 3), (q, bf16, "q", 3), (block_tables, i32, "block_tables", 2),
+             (seq_lens, i32, "seq_lens", 1)]
+    nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
+    if query_start is not None:
+        specs.append((query_start, i32, "query_start", 1))
+    dev = _need_all(*specs)
+    T, hq, dq = q.shape
+    B = seq_lens.shape[0]
+    mb = block_tables.shape
+    if out.shape != q.shape or dq != d or mb[0] != B:
+        raise ValueError("q, out, the pool and the tables disagree")
+    if (T != B) if query_start is None else (query_start.shape[0] != B + 1):
+        raise ValueError("one query token per sequence, or query_start of batch + 1 entries")
+    ws, ws_n = _space(workspace, dev)
+    return (out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), mb[1],
+            seq_lens.data_ptr()), B, T, (hq, hkv, d, nb, int(block_size)), ws, ws_n, dev
+
+
+def paged_attention_decode_q4(out, q, kv_cache, block_tables, seq_lens, block_size, max_seq_len, scale,
+                              workspace=None, stream=None):
+    """paged_attention_decode over a 4-bit pool."""
+    first, B, _, sizes, ws, ws_n, dev = _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size,
+                                                      workspace, None)
+    st = load().paged_attention_decode_q4(*first, B, *sizes, int(max_seq_len), float(scale), ws, ws_n,
+                                          _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return out
+
+
+def paged_attention_multi_q4(out, q, kv_cache, block_tables, seq_lens, query_start, block_size, max_seq_len,
+                             max_query_len, scale, workspace=None, stream=None):
+    """paged_attention_multi over a 4-bit pool."""
+    if query_start is None:
+        raise TypeError("query_start must be a torch.Tensor")
+    first, B, T, sizes, ws, ws_n, dev = _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size,
+                                                      workspace, query_start)
+    st = load().paged_attention_multi_q4(*first, query_start.data_ptr(), B, T, int(max_query_len), *sizes,
+                                         int(max_seq_len), float(scale), ws, ws_n, _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return out
+
+
+def verify_drafts(out_tokens, num_accepted, tokens, target_probs, draft_probs, uniform, query_start, max_query_len=None,
+                  seq_lens=None, new_lens=None, stream=None):
+    """The drafts the target keeps and the token that follows them (int32
+    out_tokens [T]: kept drafts, the next token, -1), their number (int32
+    num_accepted [B]) and the cached lengths to go on with (new_lens, from
+    seq_lens).  tokens int32 [T]: each sequence's last known token, then its
+    drafts; target_probs [T, V], draft_probs [T - B, V] (None: drafts without
+    probabilities) of one of fp32, bf16, fp16; uniform fp32 [T] in [0, 1)."""
+    import torch
+    _, i32, f32, _ = _dtypes()
+    kinds = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}
+    kind = kinds.get(getattr(target_probs, "dtype", None))
+    if kind is None:
+        raise TypeError("target_probs must be a torch.float32, torch.bfloat16 or torch.float16 tensor")
+    specs = [(out_tokens, i32, "out_tokens", 1), (num_accepted, i32, "num_accepted", 1), (tokens, i32, "tokens", 1),
+             (target_probs, target_probs.dtype, "target_probs", 2), (uniform, f32, "uniform", 1),
+             (query_start, i32, "query_start", 1)]
+    if draft_probs is not None:
+        specs.append((draft_probs, target_probs.dtype, "draft_probs", 2))
+    if (seq_lens is None) != (new_lens is None):
+        raise ValueError("seq_lens and new_lens belong together")
+    if seq_lens is not None:
+        specs += [(seq_lens, i32, "seq_lens", 1), (new_lens, i32, "new_lens", 1)]
+    dev = _need_all(*specs)
+    T, V = target_probs.shape
+    B = num_accepted.shape[0]
+    if tokens.shape[0] != T or out_tokens.shape[0] != T or uniform.shape[0] != T or query_start.shape[0] != B + 1:
+        raise ValueError("tokens, out_tokens, uniform, target_probs and query_start disagree")
+    if draft_probs is not None and draft_probs.shape != (T - B, V):
+        raise ValueError("draft_probs must be [tokens - batch, vocab]")
+    if seq_lens is not None and (seq_lens.shape[0] != B or new_lens.shape[0] != B):
+        raise ValueError("seq_lens and new_lens must have one entry per sequence")
+    st = load().pagedkv_verify_drafts(out_tokens.data_ptr(), num_accepted.data_ptr(), tokens.data_ptr(),
+                                      target_probs.data_ptr(), _ptr(draft_probs), uniform.data_ptr(),
+                                      query_start.data_ptr(), _ptr(seq_lens), _ptr(new_lens), B, T,
+                                      int(T if max_query_len is None else max_query_len) or 1, V, kind,
+                                      _stream_on(stream, dev))
+    if st != KV_OK:
+        _check(st)
+    return out_tokens, num_accepted
 
 
 def get_status(stream=None):

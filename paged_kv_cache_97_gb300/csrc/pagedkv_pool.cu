@@ -514,4 +514,26 @@ kv_status pagedkv_copy_blocks(void* k_cache, void* v_cache, float* k_scale, floa
   return cuda_check(cudaGetLastError(), "copy_blocks_kernel launch");
 }
 
+kv_status pagedkv_copy_blocks_q4(void* kv_cache, const int32_t* block_pairs, int num_pairs, int num_blocks,
+                                 int block_size, int num_kv_heads, int head_dim, void* stream) {
+  if (num_pairs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) ||
+      (block_size != 16 && block_size != 32))
+    return fail(KV_ERR_INVALID_ARG, "pagedkv_copy_blocks_q4: bad sizes");
+  if (num_pairs == 0) return KV_OK;
+  if (!kv_cache || !block_pairs || !aligned16(kv_cache))
+    return fail(KV_ERR_INVALID_ARG, "pagedkv_copy_blocks_q4: the pool must be non-NULL and 16-byte aligned");
+  if (num_pairs > 65535) return fail(KV_ERR_INVALID_ARG, "pagedkv_copy_blocks_q4: at most 65535 pairs");
+  DeviceInfo di;
+  kv_status st = device_info(&di);
+  if (st != KV_OK) return st;
+  const int64_t block_bytes = (int64_t)num_kv_heads * (block_size * head_dim * 9 / 8);
+  if (block_bytes > (1ll << 30)) return fail(KV_ERR_INVALID_ARG, "pagedkv_copy_blocks_q4: block too large");
+  // one tensor holds K and V: the kernel's first half alone
+  const dim3 grid((unsigned)((block_bytes + kChunk - 1) / kChunk), (unsigned)num_pairs, 1);
+  copy_blocks_kernel<<<grid, kCopyThreads, 0, (cudaStream_t)stream>>>(
+      static_cast<uint4*>(kv_cache), nullptr, nullptr, nullptr, block_pairs, num_blocks, (int)block_bytes,
+      num_kv_heads, di.flags);
+  return cuda_check(cudaGetLastError(), "copy_blocks_kernel launch");
+}
+
 }  // extern "C"

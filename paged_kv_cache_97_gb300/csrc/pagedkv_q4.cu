@@ -1,0 +1,997 @@
+// pagedkv_q4.cu -- attention over the 4-bit pool, for one query token per
+// sequence or several causal ones.
+//
+//   out[j, h] = softmax_t(scale * q[j, h] . K_t) . V_t,
+//   K_t[e] = kmin + kscale * c, V_t[e] = vmin + vscale * c  per 64 values.
+//
+// The codes go to the tensor cores as they are.  c masked out of a word,
+// (w & 0x000F000F) or (w & 0x00F000F0), is an fp16 pair c * 2^-24 or c * 2^-20
+// (subnormals, exact), so a word of eight codes is four registers after five
+// instructions; scale and min enter outside of the product:
+//   q . K_t = sum over the row's groups of kscale * (q . c) + kmin * sum(q),
+//   sum_t p_t V_t = (sum_t (p_t vscale_t) c_t) + (sum_t p_t vmin_t).
+// q is fp16, scaled by a power of two (and by 1/16 where its code is a high
+// nibble); kscale and kmin multiply in fp32; p * vscale is rounded once, to
+// fp16; p * vmin is summed in fp32.  A column's reference is the largest of
+// score + exponent of max(vscale, |vmin| / 16) so far, less five, not of the
+// score alone: p * vscale then has fp16's whole range below 2^11 whatever the
+// scales are.  It moves only when a tile passes it by more than ten octaves.
+//
+// Tile products (mma.sync m16n8k16, fp32 sums) with tokens, then dims, on M and
+// the columns (query token x grouped head) on N: the unpacked codes are used for
+// all kNT * 8 columns of the CTA, eight for one query token per sequence, up to
+// 32 for several.  S's layout becomes P's operand by one 8x8 transposition
+// (movmatrix) per 8 tokens and group.
+//
+// A warp runs on its own: it copies the records of every fourth block of the
+// CTA's range into its own ring of stages (one bulk copy each) and works on them
+// in turn; the four warps meet where a sequence ends.  The CTAs of a KV head cut
+// the whole batch's blocks into equal ranges (each finds its own from the
+// lengths), so the last wave is as full as the first whatever the lengths are; a
+// sequence cut by a range leaves partials, at most two per CTA, which the merge
+// kernel joins.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "pagedkv_common.cuh"
+#include "pagedkv_device.cuh"
+#include "pagedkv_q4.cuh"
+
+namespace pagedkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kWarps = 4;
+constexpr int kThreads4 = kWarps * 32;
+// Ranges are not cut below this many tokens: a warp then has two blocks of 16,
+// and the partials of a range cost less than its blocks.
+constexpr int kMinRangeTokens = 128;
+// Lengths up to this many tokens take one CTA per sequence, with no merge behind it.
+constexpr int kWholeTokens = 512;
+constexpr float kNoRef = -1e30f;      // the reference of a column without a key
+
+struct Q4Args {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const unsigned char* kv;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start;  // [batch + 1], or null: one query token per sequence
+  float* ws_acc;               // [Hkv, ctas, 2, columns, D]
+  float* ws_ml;                // [Hkv, ctas, 2, columns, 2]: (reference, sum)
+  int4* ws_meta;               // [Hkv, ctas]: {CTAs that follow, first token row, tokens, -}
+  unsigned int* flags;
+  int max_blocks, batch, num_tokens, max_query_len, num_q_heads, num_kv_heads;
+  int num_blocks, max_seq_len;
+  int group;                   // query heads per KV head
+  int tile_tokens;             // query tokens per column tile
+  int ctas;                    // ranges per KV head (or, whole: column tiles at most)
+  int whole;                   // one CTA per column tile of a sequence
+  float scale_log2;
+};
+
+// What the kernel needs of a sequence; nct == 0: nothing to do (or not valid).
+struct Seq {
+  int q0, n, L, nblk, nct;
+  bool bad;
+};
+
+template <int BS, bool kMulti>
+__device__ __forceinline__ Seq seq_of(const Q4Args& a, int b) {
+  Seq s;
+  s.L = __ldg(a.seq_lens + b);
+  s.q0 = b;
+  s.n = 1;
+  bool rows = true;
+  if constexpr (kMulti) {
+    s.q0 = __ldg(a.query_start + b);
+    const int q1 = __ldg(a.query_start + b + 1);
+    rows = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.num_tokens;
+    s.n = rows ? q1 - s.q0 : 0;                    // rows that may be written
+  }
+  const bool len = s.L > 0 && s.L <= a.max_seq_len && (s.L - 1) / BS < a.max_blocks &&
+                   s.n <= s.L && s.n <= a.max_query_len;
+  s.bad = !rows || (!len && (!kMulti || s.n > 0));
+  const bool use = !s.bad && s.n > 0;
+  s.nblk = use ? (s.L + BS - 1) / BS : 0;
+  s.nct = use ? (kMulti ? (s.n + a.tile_tokens - 1) / a.tile_tokens : 1) : 0;
+  return s;
+}
+
+// A walk over the pieces of [0, len) block positions of one CTA: unit (b, ct)
+// (a sequence's column tile) begins at position `us` (negative where the CTA's
+// range begins inside it).
+template <int BS, bool kMulti>
+struct Walk {
+  Seq s;
+  int b, ct, us, len;
+  int j0, j1;                                      // blocks of this piece: [j0, j1)
+
+  __device__ __forceinline__ int visible(const Q4Args& a) const {
+    if constexpr (!kMulti) return s.nblk;
+    const int last = min(s.n, (ct + 1) * a.tile_tokens);
+    return (s.L - s.n + last + BS - 1) / BS;       // blocks its last query sees
+  }
+  __device__ __forceinline__ bool done() const { return us >= len; }
+  __device__ __forceinline__ void piece(const Q4Args& a) {
+    j0 = max(0, -us);
+    j1 = min(visible(a), len - us);
+  }
+  __device__ __forceinline__ void start(const Q4Args& a, int b_, int ct_, int us_, int len_) {
+    b = b_;
+    ct = ct_;
+    us = us_;
+    len = len_;
+    s = seq_of<BS, kMulti>(a, b);
+    piece(a);
+  }
+  __device__ __forceinline__ void next(const Q4Args& a) {
+    us += s.nblk;
+    if (us >= len) return;
+    if (++ct >= s.nct) {
+      ct = 0;
+      // (us < len: a further valid sequence exists)
+      do {
+        s = seq_of<BS, kMulti>(a, ++b);
+      } while (s.nct == 0 && b + 1 < a.batch);
+    }
+    piece(a);
+  }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// 8x8 16-bit matrix over the warp (row = lane / 4, columns 2 (lane % 4), +1), transposed.
+__device__ __forceinline__ uint32_t transposed8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// kGroups consecutive words.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+  if constexpr (N == 4) {
+    const uint4 v = lds128(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = lds64(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = lds32(addr);
+  }
+}
+
+// The exponent of a row's largest V scale or |min| / 16, from its (scale, min) pairs.
+template <int N>
+__device__ __forceinline__ float value_exponent(const uint32_t (&pairs)[N]) {
+  uint32_t x = pairs[0] & 0x7fff7fffu;
+  if constexpr (N == 2) x = __vmaxu2(x, pairs[1] & 0x7fff7fffu);
+  const int s = (int)(x >> 7 & 0xffu), m = (int)(x >> 23);
+  return (float)(max(max(s, m - 4), 27) - 127);
+}
+
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes * 2^-24, * 2^-20
+
+template <int D, int BS, int NT>
+struct Cfg4 {
+  using G = Geo4<D, BS>;
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
+  static constexpr bool kQShared = NT > 2;               // q's fragments in shared memory
+  static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
+  static constexpr int kDump = NT * (D / 4 + 4);          // registers a lane hands over
+  static constexpr int kRedBytes = 2 * kDump * 32 * 4;
+  static constexpr int kBudget = (NT == 1 ? 55 : 111) * 1024 - kRedBytes - kQBytes;
+  static constexpr int kStages0 = kBudget / (kWarps * G::kRecord);
+  static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
+  static constexpr int kSmem = kWarps * kStages * G::kRecord + kRedBytes + kQBytes;
+  static_assert(kStages >= 2, "a ring has two stages at least");
+};
+
+template <int D, int BS, int NT, bool kMulti>
+__global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_kernel(const Q4Args a) {
+  using C = Cfg4<D, BS, NT>;
+  using G = Geo4<D, BS>;
+  constexpr int S = C::kStages, NG = G::kGroups;
+  constexpr int kKSteps = D / 16, kMTiles = D / 16;
+  extern __shared__ __align__(128) unsigned char smem4[];
+  __shared__ uint64_t bars[kWarps][8];
+  __shared__ long long scan[kWarps];
+  __shared__ int start_b, start_ct, start_us, range_len;
+  __shared__ int range_per;
+
+  const int hk = blockIdx.x, c = a.whole ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int GQ = a.group, Hq = a.num_q_heads;
+
+  if (threadIdx.x < kWarps * S)
+    mbar_init(smem_addr(&bars[threadIdx.x / S][threadIdx.x % S]), 1);
+  if (threadIdx.x == 0) start_b = -1;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+
+  // ---- this CTA's range of the head's block positions ----------------------
+  if (a.whole && !kMulti) {
+    // one CTA per sequence
+    if (threadIdx.x == 0) {
+      const Seq s = seq_of<BS, kMulti>(a, c);
+      if (s.bad) {
+        atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+        for (int e = 0; e < GQ * D / 8; ++e)
+          reinterpret_cast<uint4*>(a.out + ((int64_t)c * Hq + (int64_t)hk * GQ) * D)[e] = make_uint4(0, 0, 0, 0);
+      } else {
+        start_b = c;
+        start_ct = start_us = 0;
+        range_len = s.nblk;
+      }
+    }
+  } else {
+    // Every thread sums a run of sequences; the sums' prefix says where the
+    // range begins.  Positions are blocks (whole: column tiles).
+    const int run = (a.batch + kThreads4 - 1) / kThreads4;
+    const int b0 = threadIdx.x * run, b1 = min(a.batch, b0 + run);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of<BS, kMulti>(a, b);
+      sum += a.whole ? s.nct : (long long)s.nct * s.nblk;
+      if (s.bad && b % a.ctas == c) {
+        if (hk == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+        for (int i = 0; i < s.n; ++i) {
+          uint4* o = reinterpret_cast<uint4*>(a.out + ((int64_t)(s.q0 + i) * Hq + (int64_t)hk * GQ) * D);
+          for (int e = 0; e < GQ * D / 8; ++e) o[e] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    long long at = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, at, off);
+      if (lane >= off) at += x;
+    }
+    if (lane == 31) scan[warp] = at;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += scan[w];
+      total += scan[w];
+    }
+    at -= sum;                                      // sequences before this thread's
+    constexpr int kMinRange = kMinRangeTokens / BS;
+    const long long even = (total + a.ctas - 1) / a.ctas;
+    const long long per = a.whole ? 1 : (even > kMinRange ? even : kMinRange);
+    const long long u0 = (long long)c * per;
+    if (u0 >= at && u0 < at + sum) {
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of<BS, kMulti>(a, b);
+        const long long w = a.whole ? s.nct : (long long)s.nct * s.nblk;
+        if (u0 < at + w) {
+          const long long in = u0 - at;
+          start_b = b;
+          if (a.whole) {
+            start_ct = (int)in;
+            start_us = 0;
+            range_len = s.nblk;
+          } else {
+            start_ct = (int)(in / s.nblk);
+            start_us = -(int)(in % s.nblk);
+            range_len = (int)(u0 + per < total ? per : total - u0);
+            range_per = (int)per;
+          }
+          break;
+        }
+        at += w;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t cell = (int64_t)hk * a.ctas + c;
+  if (start_b < 0) {                                // nothing for this CTA
+    if (!a.whole && threadIdx.x == 0) a.ws_meta[cell] = make_int4(0, 0, 0, 0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return;
+  }
+
+  const uint32_t ring = smem_addr(smem4) + warp * S * G::kRecord;
+  float* red = reinterpret_cast<float*>(smem4 + kWarps * S * G::kRecord);
+  const uint32_t qsm = smem_addr(smem4) + kWarps * S * G::kRecord + C::kRedBytes;
+
+  // ---- the warp's ring: every fourth block of each piece -------------------
+  Walk<BS, kMulti> f, w;
+  f.start(a, start_b, start_ct, start_us, range_len);
+  w = f;
+  int fj = f.j0 + warp, fid = 0, fcount = 0, ccount = 0;
+  uint32_t bad_stages = 0;
+  bool dead = false;
+  auto settle = [&]() {                             // to the next block the warp will copy
+    while (!f.done() && fj >= f.j1) {
+      f.next(a);
+      fj = f.j0 + warp;
+    }
+    if (!f.done()) fid = __ldg(a.block_tables + (int64_t)f.b * a.max_blocks + fj);
+  };
+  settle();
+  auto fetch = [&]() {
+    if (f.done() || dead) return;
+    const int s = fcount % S;
+    const bool ok = fid >= 0 && fid < a.num_blocks;
+    bad_stages = (bad_stages & ~(1u << s)) | (ok ? 0u : 1u << s);
+    if (lane == 0) {
+      if (!ok) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
+      const uint32_t bar = smem_addr(&bars[warp][s]);
+      mbar_expect_tx(bar, G::kRecord);
+      bulk_load(ring + s * G::kRecord,
+                a.kv + ((int64_t)(ok ? fid : 0) * a.num_kv_heads + hk) * G::kRecord, G::kRecord, bar);
+    }
+    ++fcount;
+    fj += kWarps;
+    settle();
+  };
+  for (int s = 0; s < S; ++s) fetch();
+
+  // rows of a 16-token tile: MMA row r holds token tau(r) (and 8 + tau), so
+  // that both products read shared memory with few conflicts
+  const int tau = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;
+  const int va = t, vb = 4 + (t ^ 1);               // tau(2t), tau(2t + 1)
+
+  bool merged = false;                              // this CTA's meta entry is written
+  for (; !w.done(); w.next(a)) {
+    if (w.j0 >= w.j1) continue;                     // no query of the tile sees these blocks
+    // ---- queries: columns 8 nt + c are (token ct * tile + col / G, head col % G)
+    const int tok0 = w.ct * a.tile_tokens;
+    const int ntok = kMulti ? min(a.tile_tokens, w.s.n - tok0) : 1;
+    const int nta = (ntok * GQ + 7) / 8;            // column tiles in use
+    uint32_t qf[C::kQShared ? 1 : kKSteps][C::kQShared ? 1 : NT][2];
+    float qs[NT][NG][2];                            // sums of q, in score units
+    int cpos[kMulti ? NT : 1][2];
+    float kfac;
+    {
+      // B fragments: column g, words 2t and 2t + 1 of every group
+      float amax = 0.0f;
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+        int e = 0;
+        if (pass == 1) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+          if (amax > 0.0f) e = 14 - (int)((__float_as_uint(amax) >> 23) - 126);   // amax * 2^e in [2^13, 2^14)
+          e = min(max(e, -110), 110);
+          kfac = a.scale_log2 * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23);
+          if constexpr (C::kQShared) __syncthreads();   // the last unit's fragments are no longer read
+        }
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int col = 8 * nt + g;
+          const int i = col / GQ;
+          const bool used = i < ntok && col < a.tile_tokens * GQ;
+          const uint4* row = reinterpret_cast<const uint4*>(
+              a.q + ((int64_t)(w.s.q0 + tok0 + (used ? i : 0)) * Hq + (int64_t)hk * GQ + (used ? col % GQ : 0)) * D);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int ci = 0; ci < 2; ++ci) {
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (used) x = __ldg(row + gr * 8 + 2 * t + ci);
+              const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(xw[k] << 16);
+                v[2 * k + 1] = __uint_as_float(xw[k] & 0xffff0000u);
+              }
+              if (pass == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  if (fabsf(v[k]) <= 3.4e38f) amax = fmaxf(amax, fabsf(v[k]));
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += v[k];
+                const float down = up * 0.0625f;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t x0 = pack2<true>(v[2 * hh] * up, v[2 * hh + 4] * up);
+                  const uint32_t x1 = pack2<true>(v[2 * hh + 1] * down, v[2 * hh + 5] * down);
+                  const int ks = (gr * 2 + ci) * 2 + hh;
+                  if constexpr (C::kQShared) {
+                    if (warp == nt % kWarps)
+                      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qsm + ((ks * NT + nt) * 32 + lane) * 8),
+                                   "r"(x0), "r"(x1)
+                                   : "memory");
+                  } else {
+                    qf[ks][nt][0] = x0;
+                    qf[ks][nt][1] = x1;
+                  }
+                }
+              }
+            }
+            if (pass == 1) {
+              sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+              sum += __shfl_xor_sync(0xffffffffu, sum, 2);          // column g's sum, in lanes 4g ..
+              sum *= a.scale_log2;
+              qs[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+              qs[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            }
+          }
+          if constexpr (kMulti) {
+            const int p0 = (8 * nt + 2 * t) / GQ, p1 = (8 * nt + 2 * t + 1) / GQ;
+            cpos[nt][0] = w.s.L - w.s.n + tok0 + min(p0, ntok - 1);
+            cpos[nt][1] = w.s.L - w.s.n + tok0 + min(p1, ntok - 1);
+          }
+        }
+      }
+      if constexpr (C::kQShared) __syncthreads();
+    }
+    const int all_see = kMulti ? w.s.L - w.s.n + tok0 + 1 : w.s.L;   // tokens every column sees
+
+    float o[NT][kMTiles][4];
+    float ref[NT][2], l[NT][2], pm[NT][NG][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kMTiles; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+      ref[nt][0] = ref[nt][1] = kNoRef;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) pm[nt][gr][0] = pm[nt][gr][1] = 0.0f;
+    }
+    bool bad = dead;
+
+    for (int j = w.j0 + warp; j < w.j1; j += kWarps) {
+      if (dead && ccount >= fcount) break;
+      const int s = ccount % S;
+      const uint32_t bar = smem_addr(&bars[warp][s]);
+      if (!mbar_wait(bar, (ccount / S) & 1) && !mbar_wait(bar, (ccount / S) & 1)) {
+        if (lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
+        dead = true;
+      }
+      bad |= dead || ((bad_stages >> s) & 1u);
+      ++ccount;
+      const uint32_t rec = ring + s * G::kRecord;
+      const int valid = w.s.L - j * BS;             // (may exceed BS)
+      const bool inner = (j + 1) * BS <= all_see;   // every row written and seen by every column
+      if (!bad) {
+#pragma unroll 1
+        for (int tile = 0; tile < BS / 16; ++tile) {
+          if (tile * 16 >= valid) break;
+          const int lo = tile * 16 + tau, hi = lo + 8;
+          // ---- scores of 16 tokens --------------------------------------
+          float sc[NT][4];
+          {
+            uint32_t kw[2][2 * NG], kp[2][NG];
+            lds_words(kw[0], rec + lo * G::kRowBytes + t * (D / 8));
+            lds_words(kw[1], rec + hi * G::kRowBytes + t * (D / 8));
+            lds_words(kp[0], rec + G::kParAt + lo * G::kParBytes);
+            lds_words(kp[1], rec + G::kParAt + hi * G::kParBytes);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              float acc[NT][4];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+#pragma unroll
+              for (int ci = 0; ci < 2; ++ci) {
+                uint32_t x = kw[0][ci * NG + gr], y = kw[1][ci * NG + gr];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                  const uint32_t fa[4] = {x & kLow, y & kLow, x & kHigh, y & kHigh};
+                  const int ks = (gr * 2 + ci) * 2 + hh;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if (NT > 1 && nt >= nta) break;
+                    if constexpr (C::kQShared) {
+                      const uint2 b = lds64(qsm + ((ks * NT + nt) * 32 + lane) * 8);
+                      mma16816<true>(acc[nt], fa, b.x, b.y);
+                    } else {
+                      mma16816<true>(acc[nt], fa, qf[ks][nt][0], qf[ks][nt][1]);
+                    }
+                  }
+                  x >>= 8;
+                  y >>= 8;
+                }
+              }
+              const float s0 = __uint_as_float(kp[0][gr] << 16) * kfac, s1 = __uint_as_float(kp[1][gr] << 16) * kfac;
+              const float m0 = __uint_as_float(kp[0][gr] & 0xffff0000u), m1 = __uint_as_float(kp[1][gr] & 0xffff0000u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float* qq = qs[nt][gr];
+                sc[nt][0] = fmaf(s0, acc[nt][0], gr ? fmaf(m0, qq[0], sc[nt][0]) : m0 * qq[0]);
+                sc[nt][1] = fmaf(s0, acc[nt][1], gr ? fmaf(m0, qq[1], sc[nt][1]) : m0 * qq[1]);
+                sc[nt][2] = fmaf(s1, acc[nt][2], gr ? fmaf(m1, qq[0], sc[nt][2]) : m1 * qq[0]);
+                sc[nt][3] = fmaf(s1, acc[nt][3], gr ? fmaf(m1, qq[1], sc[nt][3]) : m1 * qq[1]);
+              }
+            }
+          }
+          // ---- V's scales and minima of the same two tokens ---------------
+          uint32_t vp[2][NG];
+          lds_words(vp[0], rec + G::kParAt + G::kParams + lo * G::kParBytes);
+          lds_words(vp[1], rec + G::kParAt + G::kParams + hi * G::kParBytes);
+          if (!inner) {
+            const int at = j * BS;
+            if (lo >= valid)
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) vp[0][gr] = 0;       // a row never written may hold NaN
+            if (hi >= valid)
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) vp[1][gr] = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int c0 = kMulti ? cpos[nt][0] : 0x7fffffff, c1 = kMulti ? cpos[nt][1] : 0x7fffffff;
+              if (lo >= valid || at + lo > c0) sc[nt][0] = -INFINITY;
+              if (lo >= valid || at + lo > c1) sc[nt][1] = -INFINITY;
+              if (hi >= valid || at + hi > c0) sc[nt][2] = -INFINITY;
+              if (hi >= valid || at + hi > c1) sc[nt][3] = -INFINITY;
+            }
+          }
+          // exponents of the two tokens' V: of the largest scale or |min| / 16
+          // (rows of equal values have the least scale, and p * vmin has to stay
+          // within fp32 too), -100 at least
+          const float e0 = value_exponent(vp[0]), e1 = value_exponent(vp[1]);
+          // ---- references ---------------------------------------------------
+          bool move = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            move |= fmaxf(sc[nt][0] + e0, sc[nt][2] + e1) - ref[nt][0] > 10.0f;
+            move |= fmaxf(sc[nt][1] + e0, sc[nt][3] + e1) - ref[nt][1] > 10.0f;
+          }
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float mx = fmaxf(sc[nt][k] + e0, sc[nt][k + 2] + e1);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float to = fmaxf(ref[nt][k], mx - 5.0f);
+                const float al = ex2(ref[nt][k] - to);
+                ref[nt][k] = to;
+                l[nt][k] *= al;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) pm[nt][gr][k] *= al;
+#pragma unroll
+                for (int i = 0; i < kMTiles; ++i) {
+                  o[nt][i][k] *= al;
+                  o[nt][i][k + 2] *= al;
+                }
+              }
+            }
+          }
+          // ---- weights: fp32 sums, p * vscale as the fp16 operand -------------
+          uint32_t pb[NT][NG][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && nt >= nta) break;
+            const float p0 = ex2(sc[nt][0] - ref[nt][0]), p1 = ex2(sc[nt][1] - ref[nt][1]);
+            const float p2 = ex2(sc[nt][2] - ref[nt][0]), p3 = ex2(sc[nt][3] - ref[nt][1]);
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              const float s0 = __uint_as_float(vp[0][gr] << 16), s1 = __uint_as_float(vp[1][gr] << 16);
+              const float m0 = __uint_as_float(vp[0][gr] & 0xffff0000u);
+              const float m1 = __uint_as_float(vp[1][gr] & 0xffff0000u);
+              pb[nt][gr][0] = transposed8(pack2<true>(p0 * s0, p1 * s0));
+              pb[nt][gr][1] = transposed8(pack2<true>(p2 * s1, p3 * s1));
+              pm[nt][gr][0] = fmaf(p0, m0, fmaf(p2, m1, pm[nt][gr][0]));
+              pm[nt][gr][1] = fmaf(p1, m0, fmaf(p3, m1, pm[nt][gr][1]));
+            }
+          }
+          // ---- O^T += V^T . P^T: lane g has word g of every group -------------
+          uint32_t vw[4][NG];
+          {
+            const uint32_t vrow = rec + G::kCodes + tile * 16 * G::kRowBytes + g * (NG * 4);
+            lds_words(vw[0], vrow + va * G::kRowBytes);
+            lds_words(vw[1], vrow + vb * G::kRowBytes);
+            lds_words(vw[2], vrow + (va + 8) * G::kRowBytes);
+            lds_words(vw[3], vrow + (vb + 8) * G::kRowBytes);
+          }
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t x = prmt(vw[0][gr], vw[1][gr], half ? 0x7632u : 0x5410u);   // tokens 2t, 2t + 1
+              uint32_t y = prmt(vw[2][gr], vw[3][gr], half ? 0x7632u : 0x5410u);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const uint32_t fa[4] = {x & kLow, x & kHigh, y & kLow, y & kHigh};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (NT > 1 && nt >= nta) break;
+                  mma16816<true>(o[nt][gr * 4 + half * 2 + hh], fa, pb[nt][gr][0], pb[nt][gr][1]);
+                }
+                x >>= 8;
+                y >>= 8;
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      fetch();
+    }
+
+    // ---- the four warps' (reference, sum, O), joined in warp 0 -----------------
+    // O[nt][gr * 4 + k]: elements gr * 64 + 8 g + 2 k (c0, c1: * 2^24) and + 1 (c2, c3: * 2^20)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) pm[nt][gr][k] += __shfl_xor_sync(0xffffffffu, pm[nt][gr][k], off);
+        }
+        if (bad) l[nt][k] = -1.0f;
+#pragma unroll
+        for (int i = 0; i < kMTiles; ++i) {
+          o[nt][i][k] = fmaf(o[nt][i][k], 16777216.0f, pm[nt][i / 4][k]);
+          o[nt][i][k + 2] = fmaf(o[nt][i][k + 2], 1048576.0f, pm[nt][i / 4][k]);
+        }
+      }
+    }
+    auto give = [&](int slot) {
+      float* r = red + slot * C::kDump * 32 + lane;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* x = r + nt * (D / 4 + 4) * 32;
+#pragma unroll
+        for (int i = 0; i < kMTiles; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[(i * 4 + k) * 32] = o[nt][i][k];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          x[(D / 4 + k) * 32] = ref[nt][k];
+          x[(D / 4 + 2 + k) * 32] = l[nt][k];
+        }
+      }
+    };
+    auto take = [&](int slot) {
+      const float* r = red + slot * C::kDump * 32 + lane;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float* x = r + nt * (D / 4 + 4) * 32;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float ro = x[(D / 4 + k) * 32], lo = x[(D / 4 + 2 + k) * 32];
+          const float to = fmaxf(ref[nt][k], ro), am = ex2(ref[nt][k] - to), ao = ex2(ro - to);
+          ref[nt][k] = to;
+          l[nt][k] = l[nt][k] < 0.0f || lo < 0.0f ? -1.0f : l[nt][k] * am + lo * ao;
+#pragma unroll
+          for (int i = 0; i < kMTiles; ++i) {
+            o[nt][i][k] = o[nt][i][k] * am + x[(i * 4 + k) * 32] * ao;
+            o[nt][i][k + 2] = o[nt][i][k + 2] * am + x[(i * 4 + k + 2) * 32] * ao;
+          }
+        }
+      }
+    };
+    __syncthreads();                                // the last piece's sums have been read
+    if (warp >= 2) give(warp - 2);
+    __syncthreads();
+    if (warp < 2) take(warp);
+    if (warp == 1) give(1);
+    __syncthreads();
+    if (warp == 0) {
+      take(1);
+      const bool starts = w.j0 == 0;
+      // CTAs that hold the rest of the unit's visible blocks
+      const int follow = a.whole ? 0 : (c * (long long)range_per + w.us + w.visible(a) - 1) / range_per - c;
+      const bool direct = starts && follow == 0;
+      if (!direct && starts) {
+        merged = true;
+        if (lane == 0) a.ws_meta[cell] = make_int4(follow, w.s.q0 + tok0, ntok, 0);
+      }
+      const int64_t part = cell * 2 + (starts ? 1 : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int col = 8 * nt + 2 * t + k;
+          const int i = col / GQ;
+          if (i >= ntok || col >= a.tile_tokens * GQ) continue;
+          if (direct) {
+            const float r = l[nt][k] < 0.0f ? 0.0f : 1.0f / l[nt][k];
+            __nv_bfloat16* out = a.out + ((int64_t)(w.s.q0 + tok0 + i) * Hq + (int64_t)hk * GQ + col % GQ) * D;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              uint32_t x[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const float u = o[nt][gr * 4 + m][k] * r, v = o[nt][gr * 4 + m][k + 2] * r;
+                x[m] = l[nt][k] < 0.0f ? 0u : pack2<false>(u, v);
+              }
+              *reinterpret_cast<uint4*>(out + gr * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else {
+            float* acc = a.ws_acc + (part * C::kCols + col) * D;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+              float4* to = reinterpret_cast<float4*>(acc + gr * 64 + 8 * g);
+              to[0] = make_float4(o[nt][gr * 4][k], o[nt][gr * 4][k + 2], o[nt][gr * 4 + 1][k], o[nt][gr * 4 + 1][k + 2]);
+              to[1] = make_float4(o[nt][gr * 4 + 2][k], o[nt][gr * 4 + 2][k + 2], o[nt][gr * 4 + 3][k],
+                                  o[nt][gr * 4 + 3][k + 2]);
+            }
+            if (g == 0) {
+              float* ml = a.ws_ml + (part * C::kCols + col) * 2;
+              ml[0] = ref[nt][k];
+              ml[1] = l[nt][k];
+            }
+          }
+        }
+      }
+    }
+  }
+  if (!a.whole && threadIdx.x == 0 && !merged) a.ws_meta[cell] = make_int4(0, 0, 0, 0);
+  // copies still in flight (after a wait that gave up) land before the CTA ends
+  for (; ccount < fcount; ++ccount) mbar_wait(smem_addr(&bars[warp][ccount % S]), (ccount / S) & 1);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Joins the partials of the unit that CTA c of a KV head began and later CTAs
+// ended: out = sum_i 2^(r_i - R) acc_i / sum_i 2^(r_i - R) l_i.  One CTA per
+// (range, KV head, column); its warps take the partials in turn.
+template <int D>
+__global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols) {
+  constexpr int E = D / 32;
+  __shared__ float part[4][32][E + 1];
+  const int c = blockIdx.x, hk = blockIdx.y, col = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t cell = (int64_t)hk * a.ctas + c;
+  const int4 meta = a.ws_meta[cell];
+  const int i = col / a.group;
+  if (meta.x == 0 || i >= meta.z || col >= a.tile_tokens * a.group) return;
+  const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
+  const int64_t p0 = (cell * 2 + 1) * cols + col;
+  auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
+  float R = kNoRef;
+  bool bad = false;
+  for (int k = lane; k < count; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
+    R = fmaxf(R, ml.x);
+    bad |= ml.y < 0.0f;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
+  bad = __any_sync(0xffffffffu, bad);
+  float num[E], den = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) num[e] = 0.0f;
+#pragma unroll 4
+  for (int k = warp; k < count; k += 4) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
+    const float f = ex2(ml.x - R);
+    den = fmaf(f, ml.y, den);
+    const float* acc = a.ws_acc + at(k) * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(acc);
+      num[0] = fmaf(f, x.x, num[0]);
+      num[1] = fmaf(f, x.y, num[1]);
+      num[2] = fmaf(f, x.z, num[2]);
+      num[3] = fmaf(f, x.w, num[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(acc);
+      num[0] = fmaf(f, x.x, num[0]);
+      num[1] = fmaf(f, x.y, num[1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
+  part[warp][lane][E] = den;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int k = 1; k < 4; ++k) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
+    den += part[k][lane][E];
+  }
+  const float r = bad ? 0.0f : 1.0f / den;
+  uint32_t x[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
+  __nv_bfloat16* out =
+      a.out + ((int64_t)(meta.y + i) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
+  else *reinterpret_cast<uint32_t*>(out) = x[0];
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+template <int D, int BS, int NT, bool kMulti>
+kv_status launch_q4(const Q4Args& a, cudaStream_t s) {
+  using C = Cfg4<D, BS, NT>;
+  static std::mutex mu;
+  static bool set[64] = {};
+  int dev = 0;
+  kv_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != KV_OK) return st;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && !set[dev]) {
+      st = cuda_check(cudaFuncSetAttribute(q4_kernel<D, BS, NT, kMulti>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem),
+                      "cudaFuncSetAttribute(q4_kernel)");
+      if (st != KV_OK) return st;
+      set[dev] = true;
+    }
+  }
+  q4_kernel<D, BS, NT, kMulti>
+      <<<dim3((unsigned)a.num_kv_heads, (unsigned)a.ctas), kThreads4, C::kSmem, s>>>(a);
+  if ((st = cuda_check(cudaGetLastError(), "q4_kernel launch")) != KV_OK || a.whole) return st;
+  cudaLaunchConfig_t cfg = {};
+  const int used = (kMulti ? min(a.max_query_len, a.tile_tokens) : 1) * a.group;
+  cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)a.num_kv_heads, (unsigned)used);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_merge_kernel<D>, a, C::kCols), "q4_merge_kernel launch");
+}
+
+template <int D, int BS>
+kv_status launch_q4_nt(const Q4Args& a, int nt, cudaStream_t s) {
+  if (a.query_start == nullptr) return launch_q4<D, BS, 1, false>(a, s);
+  if (nt == 1) return launch_q4<D, BS, 1, true>(a, s);
+  if (nt == 2) return launch_q4<D, BS, 2, true>(a, s);
+  if (nt == 3) return launch_q4<D, BS, 3, true>(a, s);
+  return launch_q4<D, BS, 4, true>(a, s);
+}
+
+// Column tiles of 8 that hold a sequence's queries, four at most.
+int column_tiles(int max_query_len, int group) {
+  const long long cols = (long long)max_query_len * group;
+  return cols >= 32 ? 4 : (int)((cols + 7) / 8);
+}
+
+// CTAs of all KV heads together that one wave holds, at most, in a split call:
+// `sms` SMs with 4 CTAs (8 columns) or 2 (more).
+int split_ctas(int sms, int nt, int num_kv_heads) {
+  const int all = sms * (nt == 1 ? 4 : 2);
+  return all / num_kv_heads > 0 ? all / num_kv_heads : 1;
+}
+
+size_t q4_workspace(int ctas, int num_kv_heads, int nt, int head_dim) {
+  const size_t cells = (size_t)ctas * num_kv_heads;
+  return cells * (16 + 2 * 8 * (size_t)nt * (head_dim + 2) * sizeof(float));
+}
+
+constexpr int kMostSms = 160;                       // what the size query sizes for
+
+kv_status q4_common(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+                    int max_blocks, const int32_t* seq_lens, const int32_t* query_start, int batch,
+                    int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                    int num_blocks, int block_size, int max_seq_len, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream, bool multi, const char* who) {
+  if (batch < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
+      max_blocks <= 0 || num_blocks <= 0 || max_seq_len <= 0 || max_query_len <= 0)
+    return fail(KV_ERR_INVALID_ARG, "%s: bad sizes", who);
+  const int G = num_q_heads / num_kv_heads;
+  if (G > kMaxGroup) return fail(KV_ERR_INVALID_ARG, "%s: at most 8 query heads per KV head (got %d)", who, G);
+  if (head_dim != 64 && head_dim != 128) return fail(KV_ERR_INVALID_ARG, "%s: head_dim must be 64 or 128", who);
+  if (block_size != 16 && block_size != 32) return fail(KV_ERR_INVALID_ARG, "%s: block_size must be 16 or 32", who);
+  if (batch == 0 || num_tokens == 0) return KV_OK;
+  if (!out || !q || !kv_cache || !block_tables || !seq_lens || (multi && !query_start))
+    return fail(KV_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache))
+    return fail(KV_ERR_INVALID_ARG, "%s: out, q and the pool must be 16-byte aligned", who);
+  DeviceInfo di;
+  kv_status st = device_info(&di);
+  if (st != KV_OK) return st;
+  Q4Args a = {};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const unsigned char*>(kv_cache);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start = multi ? query_start : nullptr;
+  a.flags = di.flags;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.num_tokens = num_tokens;
+  a.max_query_len = multi ? max_query_len : 1;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.num_blocks = num_blocks;
+  a.max_seq_len = max_seq_len;
+  a.group = G;
+  a.scale_log2 = scale * kLog2e;
+  const int nt = multi ? column_tiles(max_query_len, G) : 1;
+  a.tile_tokens = multi ? 8 * nt / G : 1;
+  // Column tiles of the whole batch, at most.  Short sequences, and calls with
+  // long queries whose tiles alone fill the GPU twice, take a CTA for each tile.
+  const int sms = di.num_sms < kMostSms ? di.num_sms : kMostSms;
+  const bool long_queries = multi && max_query_len > a.tile_tokens;
+  const int64_t tiles = long_queries ? (int64_t)num_tokens / a.tile_tokens + batch : batch;
+  const int split = split_ctas(sms, nt, num_kv_heads);
+  a.whole = (max_seq_len <= kWholeTokens || (long_queries && tiles >= 2 * (int64_t)split)) && tiles <= 65535;
+  a.ctas = a.whole ? (int)tiles : split;
+  if (!a.whole) {
+    const size_t need = q4_workspace(a.ctas, num_kv_heads, nt, head_dim);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+      return fail(KV_ERR_INVALID_ARG,
+                  "%s: workspace must be 16-byte aligned and hold %zu bytes "
+                  "(pagedkv_q4_workspace_bytes gives a safe size)", who, need);
+    const size_t cells = (size_t)a.ctas * num_kv_heads;
+    a.ws_meta = static_cast<int4*>(workspace);
+    a.ws_acc = reinterpret_cast<float*>(a.ws_meta + cells);
+    a.ws_ml = a.ws_acc + cells * 2 * 8 * nt * head_dim;
+  }
+  cudaStream_t s = (cudaStream_t)stream;
+  if (head_dim == 128)
+    return block_size == 32 ? launch_q4_nt<128, 32>(a, nt, s) : launch_q4_nt<128, 16>(a, nt, s);
+  return block_size == 32 ? launch_q4_nt<64, 32>(a, nt, s) : launch_q4_nt<64, 16>(a, nt, s);
+}
+
+}  // namespace
+}  // namespace pagedkv
+
+using namespace pagedkv;
+
+extern "C" {
+
+size_t pagedkv_q4_record_bytes(int block_size, int head_dim) {
+  if ((block_size != 16 && block_size != 32) || (head_dim != 64 && head_dim != 128)) return 0;
+  return (size_t)block_size * head_dim * 9 / 8;
+}
+
+size_t pagedkv_q4_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (max_query_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0)
+    return 0;
+  const int nt = column_tiles(max_query_len, num_q_heads / num_kv_heads);
+  return q4_workspace(split_ctas(kMostSms, nt, num_kv_heads), num_kv_heads, nt, head_dim);
+}
+
+kv_status paged_attention_decode_q4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* seq_lens, int batch, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                    int max_seq_len, float scale, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  return q4_common(out, q, kv_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, batch, batch, 1,
+                   num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_seq_len, scale, workspace,
+                   workspace_bytes, stream, false, "paged_attention_decode_q4");
+}
+
+kv_status paged_attention_multi_q4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start,
+                                   int batch, int num_tokens, int max_query_len, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int num_blocks, int block_size,
+                                   int max_seq_len, float scale, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return q4_common(out, q, kv_cache, block_tables, max_blocks_per_seq, seq_lens, query_start, batch, num_tokens,
+                   max_query_len, num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_seq_len, scale,
+                   workspace, workspace_bytes, stream, true, "paged_attention_multi_q4");
+}
+
+}  // extern "C"

@@ -1,0 +1,38 @@
+// pagedkv_q4.cuh -- the 4-bit pool's records, shared by the kernels that write
+// and read them.  Internal only.
+//
+// One record per (physical block, KV head): the codes of K, the codes of V,
+// then the (scale, min) bf16 pairs of K and of V, one pair per 64 values of a
+// row; a code c in 0..15 stands for min + scale * c.  Everything an attention
+// CTA needs of a block is one contiguous, 16-byte aligned piece of
+// BS * D * 9 / 8 bytes (2304 for 16 tokens of 128), which one bulk copy moves.
+//
+// Element e of a row is nibble e % 8 of 32-bit word (e % 64 / 8) * (D / 64) +
+// e / 64 of its codes: the words of equal place in every 64-group are
+// neighbours, so that a lane reads its share of all groups with one load.
+#pragma once
+
+#include "pagedkv_device.cuh"
+
+namespace pagedkv {
+
+template <int D, int BS>
+struct Geo4 {
+  static constexpr int kGroups = D / 64;
+  static constexpr int kRowBytes = D / 2;                 // codes of a row
+  static constexpr int kParBytes = kGroups * 4;           // (scale, min) pairs of a row
+  static constexpr int kCodes = BS * kRowBytes;           // one tensor's codes
+  static constexpr int kParams = BS * kParBytes;
+  static constexpr int kParAt = 2 * kCodes;               // K's pairs; V's follow
+  static constexpr int kRecord = 2 * (kCodes + kParams);
+};
+
+// Byte of a record where row `row` of tensor x (0 K, 1 V) has its codes / pairs.
+__device__ __forceinline__ int q4_codes_at(int x, int row, int bs, int d) {
+  return (x * bs + row) * (d / 2);
+}
+__device__ __forceinline__ int q4_pairs_at(int x, int row, int bs, int d) {
+  return bs * d + (x * bs + row) * (d / 16);
+}
+
+}  // namespace pagedkv

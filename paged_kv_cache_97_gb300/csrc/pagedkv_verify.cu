@@ -1,0 +1,354 @@
+// pagedkv_verify.cu -- verification of drafted tokens against the target's
+// probabilities, from given random numbers (“让 Agent 跑得快：LLM 推理服务”, §六 投机
+// 解码: the target scores the drafts in one parallel pass and keeps a prefix).
+//
+// Draft x at position i is kept while u_i q_i(x) < p_i(x).  At the first refusal
+// the token is drawn from max(p_i - q_i, 0), after all drafts from p_i: the
+// lowest z whose inclusive sum of weights exceeds u * (the sum of all).  So that
+// every split of the row gives the same token, the weights are added as whole
+// numbers of 2^-44 (64 bits): w + 1 in fp32 has round(w 2^23) in its last bits,
+// and what that leaves off, added to 1.5 * 2^-21, the next 21; two integer adds
+// per weight and no conversion.
+//
+// A cluster of up to 8 CTAs takes a sequence: every CTA finds the row from the
+// drafts by itself, each sums its part of the row, the parts' sums go to all
+// CTAs through distributed shared memory, and the one warp whose part holds the
+// drawn place reads that part again (L2).  Bound by the one row (two with q) that
+// has to be read per sequence, and in small batches by the chain of loads:
+// offsets, drafts, their probabilities, the row, the part again.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pagedkv_common.cuh"
+#include "pagedkv_device.cuh"
+
+namespace pagedkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;
+
+struct VerifyArgs {
+  int32_t* out_tokens;         // [T]
+  int32_t* accepted;           // [batch]
+  int32_t* new_lens;           // [batch], or null
+  const int32_t* seq_lens;
+  const int32_t* tokens;       // [T]
+  const void* target;          // [T, V]
+  const void* draft;           // [T - batch, V], or null: q is 1 at the draft
+  const float* uniform;        // [T]
+  const int32_t* query_start;  // [batch + 1]
+  unsigned int* flags;
+  int batch, num_tokens, max_query_len, vocab, cluster;
+};
+
+template <typename T>
+__device__ __forceinline__ float prob(const T* p) {
+  if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const float*>(p));
+  else return static_cast<float>(*p);
+}
+
+// N consecutive probabilities (kVec: one aligned 16-byte load).
+template <typename T, int N, bool kVec>
+__device__ __forceinline__ void probs(const T* p, int have, float (&v)[N]) {
+  if constexpr (kVec) {
+    if (have >= N) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          v[i] = __uint_as_float(w[i]);
+        } else {
+          const unsigned short h = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
+          T t;
+          memcpy(&t, &h, 2);
+          v[i] = static_cast<float>(t);
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = i < have ? prob(p + i) : 0.0f;
+}
+
+// What the token is drawn by: p; max(p - q, 0); or p without the draft's own.
+enum { kPlain = 0, kLess = 1, kWithout = 2 };
+
+struct Row {
+  int how, without;
+};
+
+// Weights of elements i .. i + N - 1 of a row (0 past `end`), in [0, 1]; NaN counts as 0.
+template <typename T, int N, bool kVec>
+__device__ __forceinline__ void weights_of(const T* p, const T* q, const Row& r, int i, int end, float (&w)[N]) {
+  probs<T, N, kVec>(p + i, end - i, w);
+  if (r.how == kLess) {
+    float x[N];
+    probs<T, N, kVec>(q + i, end - i, x);
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = __fsub_rn(w[k], x[k]);
+  } else if (r.how == kWithout) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (i + k == r.without) w[k] = 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) w[k] = fminf(fmaxf(w[k], 0.0f), 1.0f);
+}
+
+constexpr uint32_t kHiZero = 0x3f800000u;           // 1
+constexpr uint32_t kLoZero = 0x35400000u;           // 1.5 * 2^-21
+
+// Adds w's 2^-23 units and its further 2^-44 units (each with its zero's bits).
+__device__ __forceinline__ void add_units(float w, uint32_t& hi, uint32_t& lo) {
+  const float a = __fadd_rn(w, 1.0f);
+  const float e = __fsub_rn(w, __fsub_rn(a, 1.0f));
+  hi += __float_as_uint(a);
+  lo += __float_as_uint(__fadd_rn(e, __uint_as_float(kLoZero)));
+}
+// The sum of n <= 511 weights in 2^-44 units.
+__device__ __forceinline__ long long units(uint32_t hi, uint32_t lo, int n) {
+  return ((long long)(hi - (uint32_t)n * kHiZero) << 21) + (int32_t)(lo - (uint32_t)n * kLoZero);
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyArgs a) {
+  constexpr int N = 16 / sizeof(T);
+  __shared__ int first_refused, drawn_bad;
+  __shared__ long long warp_sum[kVerifyWarps], cta_sum[2][kMaxCluster];
+  const int b = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0;
+  const int64_t d0 = (int64_t)q0 - b;               // the sequence's first row of draft
+  const bool lens = a.seq_lens != nullptr;
+  const int L = lens ? __ldg(a.seq_lens + b) : 0;
+  // (uniform over the cluster)
+  const bool rows = q0 >= 0 && n >= 0 && q0 <= a.num_tokens - n;
+  if (!rows || n > a.max_query_len || (lens && n > L) ||
+      (a.draft != nullptr && (n == 0 || d0 < 0 || d0 + n - 1 > a.num_tokens - a.batch))) {
+    if (rank == 0) {
+      if (threadIdx.x == 0) {
+        atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+        a.accepted[b] = 0;
+        if (lens) a.new_lens[b] = L;
+      }
+      if (rows)
+        for (int i = threadIdx.x; i < n; i += kVerifyThreads) a.out_tokens[q0 + i] = -1;
+    }
+    return;
+  }
+  if (n == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
+      a.accepted[b] = 0;
+      if (lens) a.new_lens[b] = L;
+    }
+    return;
+  }
+  const int V = a.vocab;
+  const T* target = static_cast<const T*>(a.target);
+  const T* draft = static_cast<const T*>(a.draft);
+
+  // ---- drafts kept -----------------------------------------------------------
+  if (threadIdx.x == 0) {
+    first_refused = n - 1;
+    drawn_bad = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n - 1; i += kVerifyThreads) {
+    const int x = __ldg(a.tokens + q0 + i + 1);
+    bool keep = false;
+    if (x < 0 || x >= V) {
+      if (rank == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
+    } else {
+      const float p = prob(target + (int64_t)(q0 + i) * V + x);
+      const float q = draft ? prob(draft + (d0 + i) * V + x) : 1.0f;
+      // (products of two fp32 numbers are exact in fp64)
+      keep = (double)__ldg(a.uniform + q0 + i) * (double)q < (double)p;
+    }
+    if (!keep) atomicMin(&first_refused, i);
+  }
+  __syncthreads();
+  const int kept = first_refused;
+  Row r = {kPlain, -1};
+  if (kept < n - 1) {
+    r.without = __ldg(a.tokens + q0 + kept + 1);
+    const bool in = r.without >= 0 && r.without < V;
+    r.how = !in ? kPlain : draft ? kLess : kWithout;   // a draft outside the vocabulary: from p
+  }
+  const T* p = target + (int64_t)(q0 + kept) * V;
+  const T* q = r.how == kLess ? draft + (d0 + kept) * V : p;
+  float u = __ldg(a.uniform + q0 + n - 1);
+  u = u >= 0.0f ? fminf(u, 0.99999994f) : 0.0f;
+
+  if (rank == 0) {
+    for (int i = threadIdx.x; i < n; i += kVerifyThreads)
+      if (i != kept) a.out_tokens[q0 + i] = i < kept ? __ldg(a.tokens + q0 + i + 1) : -1;
+    if (threadIdx.x == 0) a.accepted[b] = kept;
+  }
+
+  // ---- this warp's part of the row: [w0, w1) ----------------------------------
+  constexpr int kStep = 32 * N;
+  const int all_warps = a.cluster * kVerifyWarps;
+  const int per = ((V + all_warps - 1) / all_warps + kStep - 1) / kStep * kStep;
+  const int64_t at = (int64_t)(rank * kVerifyWarps + warp) * per;
+  const int w0 = (int)(at < V ? at : V), w1 = (int)(at + per < V ? at + per : V);
+  for (int pass = 0;; ++pass) {
+    long long sum = 0;
+    for (int i0 = w0; i0 < w1; i0 += 8 * kStep) {   // at most 64 weights a lane before they are joined
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float w[N];
+        weights_of<T, N, kVec>(p, q, r, min(i0 + k * kStep + lane * N, w1), w1, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) add_units(w[e], hi, lo);
+      }
+      sum += units(hi, lo, 8 * N);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) warp_sum[warp] = sum;
+    __syncthreads();
+    long long mine = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < kVerifyWarps; ++k) {
+      if (k < warp) before += warp_sum[k];
+      mine += warp_sum[k];
+    }
+    long long total = mine;
+    if (a.cluster > 1) {
+      if (threadIdx.x < a.cluster) {
+        uint32_t to;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(to)
+                     : "r"(smem_addr(&cta_sum[pass][rank])), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
+      }
+      cluster_barrier();
+      total = 0;
+      for (int k = 0; k < a.cluster; ++k) {
+        if (k < rank) before += cta_sum[pass][k];
+        total += cta_sum[pass][k];
+      }
+    }
+    // (after the barrier: new_lens may be seq_lens, which every CTA has read by now)
+    if (rank == 0 && threadIdx.x == 0 && lens) a.new_lens[b] = L - n + 1 + kept;
+    if (total == 0 && r.how != kPlain) {            // nothing is left of p: drawn from p itself
+      r.how = kPlain;
+      __syncthreads();
+      continue;
+    }
+    const double goal = (double)u * (double)total;
+    if (total == 0) {
+      if (rank == 0 && threadIdx.x == 0) a.out_tokens[q0 + kept] = V - 1;
+      return;
+    }
+    // ---- the place is this warp's if its sums pass the goal first --------------
+    if (!((double)before <= goal && (double)(before + sum) > goal)) return;
+    for (int i0 = w0; i0 < w1; i0 += kStep) {
+      float w[N];
+      const int i = min(i0 + lane * N, w1);
+      weights_of<T, N, kVec>(p, q, r, i, w1, w);
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) add_units(w[e], hi, lo);
+      const long long own = units(hi, lo, N);
+      long long incl = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, (double)(before + incl) > goal);
+      if (past != 0) {
+        if (lane == __ffs(past) - 1) {
+          long long s = before + incl - own;
+          int z = i;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            uint32_t h1 = 0, l1 = 0;
+            add_units(w[e], h1, l1);
+            s += units(h1, l1, 1);
+            if ((double)s <= goal) ++z;
+          }
+          a.out_tokens[q0 + kept] = z;
+        }
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return;
+  }
+}
+
+template <typename T>
+kv_status launch_verify(const VerifyArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.batch * a.cluster));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool vec = (int64_t)a.vocab * sizeof(T) % 16 == 0 && aligned16(a.target) && aligned16(a.draft);
+  return cuda_check(vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, a)
+                        : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, a),
+                    "verify_kernel launch");
+}
+
+}  // namespace
+}  // namespace pagedkv
+
+using namespace pagedkv;
+
+extern "C" kv_status pagedkv_verify_drafts(int32_t* out_tokens, int32_t* num_accepted, const int32_t* tokens,
+                                           const void* target_probs, const void* draft_probs, const float* uniform,
+                                           const int32_t* query_start, const int32_t* seq_lens, int32_t* new_lens,
+                                           int batch, int num_tokens, int max_query_len, int vocab,
+                                           pagedkv_prob_dtype dtype, void* stream) {
+  const char* who = "pagedkv_verify_drafts";
+  if (batch < 0 || num_tokens < 0 || max_query_len <= 0 || vocab <= 0 || vocab >= (1 << 19) ||
+      (dtype != PAGEDKV_PROB_F32 && dtype != PAGEDKV_PROB_BF16 && dtype != PAGEDKV_PROB_F16))
+    return fail(KV_ERR_INVALID_ARG, "%s: bad sizes or dtype (vocab 1 to 2^19 - 1)", who);
+  if (batch > (1 << 24)) return fail(KV_ERR_INVALID_ARG, "%s: too many sequences", who);
+  if (batch == 0) return KV_OK;
+  if (!num_accepted || !query_start ||
+      (num_tokens > 0 && (!out_tokens || !tokens || !target_probs || !uniform)))
+    return fail(KV_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if ((seq_lens == nullptr) != (new_lens == nullptr))
+    return fail(KV_ERR_INVALID_ARG, "%s: give both seq_lens and new_lens, or neither", who);
+  if (draft_probs && num_tokens < batch)
+    return fail(KV_ERR_INVALID_ARG, "%s: with draft_probs every sequence has a token at least", who);
+  const uintptr_t unit = dtype == PAGEDKV_PROB_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(target_probs) & unit) || (reinterpret_cast<uintptr_t>(draft_probs) & unit))
+    return fail(KV_ERR_INVALID_ARG, "%s: the probabilities must be aligned to their type", who);
+  if (out_tokens == tokens && num_tokens > 0)
+    return fail(KV_ERR_INVALID_ARG, "%s: out_tokens must not be tokens", who);
+  DeviceInfo di;
+  kv_status st = device_info(&di);
+  if (st != KV_OK) return st;
+  VerifyArgs a = {out_tokens, num_accepted, new_lens, seq_lens, tokens, target_probs, draft_probs, uniform,
+                  query_start, di.flags, batch, num_tokens, max_query_len, vocab, 1};
+  // as many CTAs a sequence as the GPU holds at once (two of 512 threads per SM
+  // are enough to keep the loads coming), while a warp has 256 weights
+  while (a.cluster < kMaxCluster && 2LL * a.cluster * batch <= 4LL * di.num_sms &&
+         vocab >= a.cluster * kVerifyWarps * 256)
+    a.cluster *= 2;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == PAGEDKV_PROB_F32) return launch_verify<float>(a, s);
+  if (dtype == PAGEDKV_PROB_BF16) return launch_verify<__nv_bfloat16>(a, s);
+  return launch_verify<__half>(a, s);
+}
