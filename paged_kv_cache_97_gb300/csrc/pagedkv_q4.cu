@@ -23,8 +23,8 @@
 // 32 for several.  S's layout becomes P's operand by one 8x8 transposition
 // (movmatrix) per 8 tokens and group.
 //
-// A warp runs on its own: it copies the records of every fourth block of the
-// CTA's range into its own ring of stages (one bulk copy each) and works on them
+// A warp runs on its own: it copies the records of every fourth 32 tokens of
+// the CTA's range into its own ring of stages (one bulk copy per block) and works on them
 // in turn; the four warps meet where a sequence ends.  The CTAs of a KV head cut
 // the whole batch's blocks into equal ranges (each finds its own from the
 // lengths), so the last wave is as full as the first whatever the lengths are; a
@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
@@ -159,8 +160,17 @@ __device__ __forceinline__ uint32_t transposed8(uint32_t x) {
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// mma16816<true> on an accumulator of zeros.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -198,19 +208,26 @@ __device__ __forceinline__ float value_exponent(const uint32_t (&pairs)[N]) {
 
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes * 2^-24, * 2^-20
 
+#ifndef PAGEDKV_Q4_CTAS
+#define PAGEDKV_Q4_CTAS 3
+#endif
+// A stage holds a step's blocks: 32 tokens, two MMA tiles.
 template <int D, int BS, int NT>
 struct Cfg4 {
   using G = Geo4<D, BS>;
   static constexpr int kCols = 8 * NT;
-  static constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
+  static constexpr int kCtasPerSm = NT == 1 ? PAGEDKV_Q4_CTAS : 2;
+  static constexpr int kBlocks = 32 / BS;                 // blocks of a step
+  static constexpr int kStage = kBlocks * G::kRecord;
+  static constexpr int kTiles = NT <= 2 ? 2 : 1;          // tiles worked on together
   static constexpr bool kQShared = NT > 2;               // q's fragments in shared memory
   static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
   static constexpr int kDump = NT * (D / 4 + 4);          // registers a lane hands over
   static constexpr int kRedBytes = 2 * kDump * 32 * 4;
-  static constexpr int kBudget = (NT == 1 ? 55 : 111) * 1024 - kRedBytes - kQBytes;
-  static constexpr int kStages0 = kBudget / (kWarps * G::kRecord);
+  static constexpr int kBudget = (224 / kCtasPerSm - 1) * 1024 - kRedBytes - kQBytes;
+  static constexpr int kStages0 = kBudget / (kWarps * kStage);
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-  static constexpr int kSmem = kWarps * kStages * G::kRecord + kRedBytes + kQBytes;
+  static constexpr int kSmem = kWarps * kStages * kStage + kRedBytes + kQBytes;
   static_assert(kStages >= 2, "a ring has two stages at least");
 };
 
@@ -319,39 +336,50 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     return;
   }
 
-  const uint32_t ring = smem_addr(smem4) + warp * S * G::kRecord;
-  float* red = reinterpret_cast<float*>(smem4 + kWarps * S * G::kRecord);
-  const uint32_t qsm = smem_addr(smem4) + kWarps * S * G::kRecord + C::kRedBytes;
+  const uint32_t ring = smem_addr(smem4) + warp * S * C::kStage;
+  float* red = reinterpret_cast<float*>(smem4 + kWarps * S * C::kStage);
+  const uint32_t qsm = smem_addr(smem4) + kWarps * S * C::kStage + C::kRedBytes;
 
-  // ---- the warp's ring: every fourth block of each piece -------------------
+  // ---- the warp's ring: every fourth step of each piece ---------------------
+  constexpr int PB = C::kBlocks;
   Walk<BS, kMulti> f, w;
   f.start(a, start_b, start_ct, start_us, range_len);
   w = f;
-  int fj = f.j0 + warp, fid = 0, fcount = 0, ccount = 0;
-  uint32_t bad_stages = 0;
+  int fj = f.j0 + warp * PB, fid[PB];               // next blocks to copy
+  int fs = 0, cs = 0, ahead = 0;                    // stages: next to fill, to use; filled
+  uint32_t phase = 0, bad_stages = 0;
   bool dead = false;
-  auto settle = [&]() {                             // to the next block the warp will copy
+  auto settle = [&]() {                             // to the next step the warp will copy
     while (!f.done() && fj >= f.j1) {
       f.next(a);
-      fj = f.j0 + warp;
+      fj = f.j0 + warp * PB;
     }
-    if (!f.done()) fid = __ldg(a.block_tables + (int64_t)f.b * a.max_blocks + fj);
+    if (f.done()) return;
+    const int32_t* row = a.block_tables + (int64_t)f.b * a.max_blocks + fj;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) fid[i] = i == 0 || fj + i < f.j1 ? __ldg(row + i) : 0;
   };
   settle();
   auto fetch = [&]() {
     if (f.done() || dead) return;
-    const int s = fcount % S;
-    const bool ok = fid >= 0 && fid < a.num_blocks;
-    bad_stages = (bad_stages & ~(1u << s)) | (ok ? 0u : 1u << s);
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) ok = ok && (unsigned)fid[i] < (unsigned)a.num_blocks;
+    bad_stages = (bad_stages & ~(1u << fs)) | (ok ? 0u : 1u << fs);
     if (lane == 0) {
       if (!ok) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
-      const uint32_t bar = smem_addr(&bars[warp][s]);
-      mbar_expect_tx(bar, G::kRecord);
-      bulk_load(ring + s * G::kRecord,
-                a.kv + ((int64_t)(ok ? fid : 0) * a.num_kv_heads + hk) * G::kRecord, G::kRecord, bar);
+      const uint32_t bar = smem_addr(&bars[warp][fs]), dst = ring + fs * C::kStage;
+      const int have = min(PB, f.j1 - fj);
+      mbar_expect_tx(bar, have * G::kRecord);
+#pragma unroll
+      for (int i = 0; i < PB; ++i)
+        if (i < have)
+          bulk_load(dst + i * G::kRecord, a.kv + ((int64_t)(ok ? fid[i] : 0) * a.num_kv_heads + hk) * G::kRecord,
+                    G::kRecord, bar);
     }
-    ++fcount;
-    fj += kWarps;
+    fs = fs + 1 == S ? 0 : fs + 1;
+    ++ahead;
+    fj += kWarps * PB;
     settle();
   };
   for (int s = 0; s < S; ++s) fetch();
@@ -465,176 +493,214 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     }
     bool bad = dead;
 
-    for (int j = w.j0 + warp; j < w.j1; j += kWarps) {
-      if (dead && ccount >= fcount) break;
-      const int s = ccount % S;
-      const uint32_t bar = smem_addr(&bars[warp][s]);
-      if (!mbar_wait(bar, (ccount / S) & 1) && !mbar_wait(bar, (ccount / S) & 1)) {
-        if (lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
-        dead = true;
-      }
-      bad |= dead || ((bad_stages >> s) & 1u);
-      ++ccount;
-      const uint32_t rec = ring + s * G::kRecord;
-      const int valid = w.s.L - j * BS;             // (may exceed BS)
-      const bool inner = (j + 1) * BS <= all_see;   // every row written and seen by every column
-      if (!bad) {
+    // kA of the kNT column tiles in use: a sequence with few queries in a call
+    // with long ones pays for one
+    auto steps = [&](auto tiles_in_use) {
+      constexpr int A = decltype(tiles_in_use)::value;
+      constexpr int T = C::kTiles;
+      for (int j = w.j0 + warp * PB; j < w.j1; j += kWarps * PB) {
+        if (ahead == 0) break;                      // (after a wait that gave up)
+        const uint32_t bar = smem_addr(&bars[warp][cs]);
+        if (!mbar_wait(bar, (phase >> cs) & 1u) && !mbar_wait(bar, (phase >> cs) & 1u)) {
+          if (lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
+          dead = true;
+        }
+        bad |= dead || ((bad_stages >> cs) & 1u);
+        const uint32_t stage = ring + cs * C::kStage;
+        phase ^= 1u << cs;
+        cs = cs + 1 == S ? 0 : cs + 1;
+        --ahead;
+        const int first = j * BS;                   // the step's first token
+        const int have = min((j + PB <= w.j1 ? PB : 1) * BS, w.s.L - first);
+        const bool inner = first + 32 <= all_see && have == 32;   // every row written and seen by every column
+        if (!bad) {
 #pragma unroll 1
-        for (int tile = 0; tile < BS / 16; ++tile) {
-          if (tile * 16 >= valid) break;
-          const int lo = tile * 16 + tau, hi = lo + 8;
-          // ---- scores of 16 tokens --------------------------------------
-          float sc[NT][4];
-          {
-            uint32_t kw[2][2 * NG], kp[2][NG];
-            lds_words(kw[0], rec + lo * G::kRowBytes + t * (D / 8));
-            lds_words(kw[1], rec + hi * G::kRowBytes + t * (D / 8));
-            lds_words(kp[0], rec + G::kParAt + lo * G::kParBytes);
-            lds_words(kp[1], rec + G::kParAt + hi * G::kParBytes);
+          for (int base = 0; base < 32; base += 16 * T) {
+            if (base >= have) break;
+            // this lane's rows of tile x: its block's record, rows lo and lo + 8 of it
+            uint32_t rec[T];
+            int row0[T];
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              float acc[NT][4];
+            for (int x = 0; x < T; ++x) {
+              const int at = base + 16 * x;
+              rec[x] = stage + (BS == 16 ? at / 16 * G::kRecord : 0);
+              row0[x] = BS == 16 ? 0 : at;
+            }
+            // ---- scores ------------------------------------------------------
+            float sc[T][A][4];
+            {
+              uint32_t kw[T][2][2 * NG], kp[T][2][NG];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+              for (int x = 0; x < T; ++x) {
+                const int lo = row0[x] + tau;
+                lds_words(kw[x][0], rec[x] + lo * G::kRowBytes + t * (D / 8));
+                lds_words(kw[x][1], rec[x] + (lo + 8) * G::kRowBytes + t * (D / 8));
+                lds_words(kp[x][0], rec[x] + G::kParAt + lo * G::kParBytes);
+                lds_words(kp[x][1], rec[x] + G::kParAt + (lo + 8) * G::kParBytes);
+              }
 #pragma unroll
-              for (int ci = 0; ci < 2; ++ci) {
-                uint32_t x = kw[0][ci * NG + gr], y = kw[1][ci * NG + gr];
+              for (int gr = 0; gr < NG; ++gr) {
+                float acc[T][A][4];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  const uint32_t fa[4] = {x & kLow, y & kLow, x & kHigh, y & kHigh};
-                  const int ks = (gr * 2 + ci) * 2 + hh;
+                for (int ks = 0; ks < 4; ++ks) {    // word ci = ks / 2 of the lane's two, half ks % 2
+                  uint2 b[A];
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    if (NT > 1 && nt >= nta) break;
-                    if constexpr (C::kQShared) {
-                      const uint2 b = lds64(qsm + ((ks * NT + nt) * 32 + lane) * 8);
-                      mma16816<true>(acc[nt], fa, b.x, b.y);
-                    } else {
-                      mma16816<true>(acc[nt], fa, qf[ks][nt][0], qf[ks][nt][1]);
+                  for (int nt = 0; nt < A; ++nt) {
+                    if constexpr (C::kQShared) b[nt] = lds64(qsm + (((gr * 4 + ks) * NT + nt) * 32 + lane) * 8);
+                    else b[nt] = make_uint2(qf[gr * 4 + ks][nt][0], qf[gr * 4 + ks][nt][1]);
+                  }
+#pragma unroll
+                  for (int x = 0; x < T; ++x) {
+                    const uint32_t u = kw[x][0][ks / 2 * NG + gr] >> (ks % 2 * 8);
+                    const uint32_t v = kw[x][1][ks / 2 * NG + gr] >> (ks % 2 * 8);
+                    const uint32_t fa[4] = {u & kLow, v & kLow, u & kHigh, v & kHigh};
+#pragma unroll
+                    for (int nt = 0; nt < A; ++nt) {
+                      if (ks == 0) mma16816_first(acc[x][nt], fa, b[nt].x, b[nt].y);
+                      else mma16816<true>(acc[x][nt], fa, b[nt].x, b[nt].y);
                     }
                   }
-                  x >>= 8;
-                  y >>= 8;
+                }
+#pragma unroll
+                for (int x = 0; x < T; ++x) {
+                  const uint32_t k0 = kp[x][0][gr], k1 = kp[x][1][gr];
+                  const float s0 = __uint_as_float(k0 << 16) * kfac, s1 = __uint_as_float(k1 << 16) * kfac;
+                  const float m0 = __uint_as_float(k0 & 0xffff0000u), m1 = __uint_as_float(k1 & 0xffff0000u);
+#pragma unroll
+                  for (int nt = 0; nt < A; ++nt) {
+                    const float* qq = qs[nt][gr];
+                    float* y = sc[x][nt];
+                    y[0] = fmaf(s0, acc[x][nt][0], gr ? fmaf(m0, qq[0], y[0]) : m0 * qq[0]);
+                    y[1] = fmaf(s0, acc[x][nt][1], gr ? fmaf(m0, qq[1], y[1]) : m0 * qq[1]);
+                    y[2] = fmaf(s1, acc[x][nt][2], gr ? fmaf(m1, qq[0], y[2]) : m1 * qq[0]);
+                    y[3] = fmaf(s1, acc[x][nt][3], gr ? fmaf(m1, qq[1], y[3]) : m1 * qq[1]);
+                  }
                 }
               }
-              const float s0 = __uint_as_float(kp[0][gr] << 16) * kfac, s1 = __uint_as_float(kp[1][gr] << 16) * kfac;
-              const float m0 = __uint_as_float(kp[0][gr] & 0xffff0000u), m1 = __uint_as_float(kp[1][gr] & 0xffff0000u);
+            }
+            // ---- V's scales and minima of the same tokens ----------------------
+            uint32_t vp[T][2][NG];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const float* qq = qs[nt][gr];
-                sc[nt][0] = fmaf(s0, acc[nt][0], gr ? fmaf(m0, qq[0], sc[nt][0]) : m0 * qq[0]);
-                sc[nt][1] = fmaf(s0, acc[nt][1], gr ? fmaf(m0, qq[1], sc[nt][1]) : m0 * qq[1]);
-                sc[nt][2] = fmaf(s1, acc[nt][2], gr ? fmaf(m1, qq[0], sc[nt][2]) : m1 * qq[0]);
-                sc[nt][3] = fmaf(s1, acc[nt][3], gr ? fmaf(m1, qq[1], sc[nt][3]) : m1 * qq[1]);
+            for (int x = 0; x < T; ++x) {
+              const uint32_t at = rec[x] + G::kParAt + G::kParams + (row0[x] + tau) * G::kParBytes;
+              lds_words(vp[x][0], at);
+              lds_words(vp[x][1], at + 8 * G::kParBytes);
+            }
+            if (!inner) {
+#pragma unroll
+              for (int x = 0; x < T; ++x) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int tok = base + 16 * x + tau + 8 * r;
+                  const bool out = tok >= have;
+#pragma unroll
+                  for (int gr = 0; gr < NG; ++gr)
+                    if (out) vp[x][r][gr] = 0;          // a row never written may hold NaN
+#pragma unroll
+                  for (int nt = 0; nt < A; ++nt) {
+                    if (out || (kMulti && first + tok > cpos[nt][0])) sc[x][nt][2 * r] = -INFINITY;
+                    if (out || (kMulti && first + tok > cpos[nt][1])) sc[x][nt][2 * r + 1] = -INFINITY;
+                  }
+                }
               }
             }
-          }
-          // ---- V's scales and minima of the same two tokens ---------------
-          uint32_t vp[2][NG];
-          lds_words(vp[0], rec + G::kParAt + G::kParams + lo * G::kParBytes);
-          lds_words(vp[1], rec + G::kParAt + G::kParams + hi * G::kParBytes);
-          if (!inner) {
-            const int at = j * BS;
-            if (lo >= valid)
+            // exponents of the tokens' V: of the largest scale or |min| / 16 (rows
+            // of equal values have the least scale, and p * vmin has to stay within
+            // fp32 too), -100 at least
+            float e[T][2];
 #pragma unroll
-              for (int gr = 0; gr < NG; ++gr) vp[0][gr] = 0;       // a row never written may hold NaN
-            if (hi >= valid)
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) vp[1][gr] = 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int c0 = kMulti ? cpos[nt][0] : 0x7fffffff, c1 = kMulti ? cpos[nt][1] : 0x7fffffff;
-              if (lo >= valid || at + lo > c0) sc[nt][0] = -INFINITY;
-              if (lo >= valid || at + lo > c1) sc[nt][1] = -INFINITY;
-              if (hi >= valid || at + hi > c0) sc[nt][2] = -INFINITY;
-              if (hi >= valid || at + hi > c1) sc[nt][3] = -INFINITY;
+            for (int x = 0; x < T; ++x) {
+              e[x][0] = value_exponent(vp[x][0]);
+              e[x][1] = value_exponent(vp[x][1]);
             }
-          }
-          // exponents of the two tokens' V: of the largest scale or |min| / 16
-          // (rows of equal values have the least scale, and p * vmin has to stay
-          // within fp32 too), -100 at least
-          const float e0 = value_exponent(vp[0]), e1 = value_exponent(vp[1]);
-          // ---- references ---------------------------------------------------
-          bool move = false;
+            // ---- references ------------------------------------------------------
+            float most[A][2];
+            bool move = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            move |= fmaxf(sc[nt][0] + e0, sc[nt][2] + e1) - ref[nt][0] > 10.0f;
-            move |= fmaxf(sc[nt][1] + e0, sc[nt][3] + e1) - ref[nt][1] > 10.0f;
-          }
-          if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                float mx = fmaxf(sc[nt][k] + e0, sc[nt][k + 2] + e1);
+                float y = fmaxf(sc[0][nt][k] + e[0][0], sc[0][nt][k + 2] + e[0][1]);
+                if constexpr (T == 2) y = fmaxf(y, fmaxf(sc[T - 1][nt][k] + e[T - 1][0], sc[T - 1][nt][k + 2] + e[T - 1][1]));
+                most[nt][k] = y;
+                move |= y - ref[nt][k] > 10.0f;
+              }
+            }
+            if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float to = fmaxf(ref[nt][k], mx - 5.0f);
-                const float al = ex2(ref[nt][k] - to);
-                ref[nt][k] = to;
-                l[nt][k] *= al;
+              for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr) pm[nt][gr][k] *= al;
+                for (int k = 0; k < 2; ++k) {
+                  float mx = most[nt][k];
 #pragma unroll
-                for (int i = 0; i < kMTiles; ++i) {
-                  o[nt][i][k] *= al;
-                  o[nt][i][k + 2] *= al;
+                  for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                  const float to = fmaxf(ref[nt][k], mx - 5.0f);
+                  const float al = ex2(ref[nt][k] - to);
+                  ref[nt][k] = to;
+                  l[nt][k] *= al;
+#pragma unroll
+                  for (int gr = 0; gr < NG; ++gr) pm[nt][gr][k] *= al;
+#pragma unroll
+                  for (int i = 0; i < kMTiles; ++i) {
+                    o[nt][i][k] *= al;
+                    o[nt][i][k + 2] *= al;
+                  }
                 }
               }
             }
-          }
-          // ---- weights: fp32 sums, p * vscale as the fp16 operand -------------
-          uint32_t pb[NT][NG][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && nt >= nta) break;
-            const float p0 = ex2(sc[nt][0] - ref[nt][0]), p1 = ex2(sc[nt][1] - ref[nt][1]);
-            const float p2 = ex2(sc[nt][2] - ref[nt][0]), p3 = ex2(sc[nt][3] - ref[nt][1]);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
+            for (int x = 0; x < T; ++x) {
+              // ---- V's codes: lane g has word g of every group --------------------
+              uint32_t vw[4][NG];
+              const uint32_t vrow = rec[x] + G::kCodes + row0[x] * G::kRowBytes + g * (NG * 4);
+              lds_words(vw[0], vrow + va * G::kRowBytes);
+              lds_words(vw[1], vrow + vb * G::kRowBytes);
+              lds_words(vw[2], vrow + (va + 8) * G::kRowBytes);
+              lds_words(vw[3], vrow + (vb + 8) * G::kRowBytes);
+              // ---- weights: fp32 sums, p * vscale as the fp16 operand ---------------
+              uint32_t pb[A][NG][2];
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              const float s0 = __uint_as_float(vp[0][gr] << 16), s1 = __uint_as_float(vp[1][gr] << 16);
-              const float m0 = __uint_as_float(vp[0][gr] & 0xffff0000u);
-              const float m1 = __uint_as_float(vp[1][gr] & 0xffff0000u);
-              pb[nt][gr][0] = transposed8(pack2<true>(p0 * s0, p1 * s0));
-              pb[nt][gr][1] = transposed8(pack2<true>(p2 * s1, p3 * s1));
-              pm[nt][gr][0] = fmaf(p0, m0, fmaf(p2, m1, pm[nt][gr][0]));
-              pm[nt][gr][1] = fmaf(p1, m0, fmaf(p3, m1, pm[nt][gr][1]));
-            }
-          }
-          // ---- O^T += V^T . P^T: lane g has word g of every group -------------
-          uint32_t vw[4][NG];
-          {
-            const uint32_t vrow = rec + G::kCodes + tile * 16 * G::kRowBytes + g * (NG * 4);
-            lds_words(vw[0], vrow + va * G::kRowBytes);
-            lds_words(vw[1], vrow + vb * G::kRowBytes);
-            lds_words(vw[2], vrow + (va + 8) * G::kRowBytes);
-            lds_words(vw[3], vrow + (vb + 8) * G::kRowBytes);
-          }
+              for (int nt = 0; nt < A; ++nt) {
+                const float p0 = ex2(sc[x][nt][0] - ref[nt][0]), p1 = ex2(sc[x][nt][1] - ref[nt][1]);
+                const float p2 = ex2(sc[x][nt][2] - ref[nt][0]), p3 = ex2(sc[x][nt][3] - ref[nt][1]);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t x = prmt(vw[0][gr], vw[1][gr], half ? 0x7632u : 0x5410u);   // tokens 2t, 2t + 1
-              uint32_t y = prmt(vw[2][gr], vw[3][gr], half ? 0x7632u : 0x5410u);
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t fa[4] = {x & kLow, x & kHigh, y & kLow, y & kHigh};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if (NT > 1 && nt >= nta) break;
-                  mma16816<true>(o[nt][gr * 4 + half * 2 + hh], fa, pb[nt][gr][0], pb[nt][gr][1]);
+                for (int gr = 0; gr < NG; ++gr) {
+                  const uint32_t v0 = vp[x][0][gr], v1 = vp[x][1][gr];
+                  const float s0 = __uint_as_float(v0 << 16), s1 = __uint_as_float(v1 << 16);
+                  const float m0 = __uint_as_float(v0 & 0xffff0000u), m1 = __uint_as_float(v1 & 0xffff0000u);
+                  pb[nt][gr][0] = transposed8(pack2<true>(p0 * s0, p1 * s0));
+                  pb[nt][gr][1] = transposed8(pack2<true>(p2 * s1, p3 * s1));
+                  pm[nt][gr][0] = fmaf(p0, m0, fmaf(p2, m1, pm[nt][gr][0]));
+                  pm[nt][gr][1] = fmaf(p1, m0, fmaf(p3, m1, pm[nt][gr][1]));
                 }
-                x >>= 8;
-                y >>= 8;
+              }
+              // ---- O^T += V^T . P^T ---------------------------------------------------
+#pragma unroll
+              for (int gr = 0; gr < NG; ++gr) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  // tokens 2t, 2t + 1 and 2t + 8, 2t + 9; nibbles 2k and 2k + 1
+                  const uint32_t u = prmt(vw[0][gr], vw[1][gr], k >= 2 ? 0x7632u : 0x5410u) >> (k % 2 * 8);
+                  const uint32_t v = prmt(vw[2][gr], vw[3][gr], k >= 2 ? 0x7632u : 0x5410u) >> (k % 2 * 8);
+                  const uint32_t fa[4] = {u & kLow, u & kHigh, v & kLow, v & kHigh};
+#pragma unroll
+                  for (int nt = 0; nt < A; ++nt) mma16816<true>(o[nt][gr * 4 + k], fa, pb[nt][gr][0], pb[nt][gr][1]);
+                }
               }
             }
           }
         }
+        __syncwarp();
+        fetch();
       }
-      __syncwarp();
-      fetch();
+    };
+    if constexpr (NT > 1) {
+      if (nta == 1) steps(std::integral_constant<int, 1>{});
+      else steps(std::integral_constant<int, NT>{});
+    } else {
+      steps(std::integral_constant<int, 1>{});
     }
 
     // ---- the four warps' (reference, sum, O), joined in warp 0 -----------------
@@ -750,7 +816,10 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
   }
   if (!a.whole && threadIdx.x == 0 && !merged) a.ws_meta[cell] = make_int4(0, 0, 0, 0);
   // copies still in flight (after a wait that gave up) land before the CTA ends
-  for (; ccount < fcount; ++ccount) mbar_wait(smem_addr(&bars[warp][ccount % S]), (ccount / S) & 1);
+  for (; ahead > 0; --ahead) {
+    mbar_wait(smem_addr(&bars[warp][cs]), (phase >> cs) & 1u);
+    cs = cs + 1 == S ? 0 : cs + 1;
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -875,10 +944,9 @@ int column_tiles(int max_query_len, int group) {
   return cols >= 32 ? 4 : (int)((cols + 7) / 8);
 }
 
-// CTAs of all KV heads together that one wave holds, at most, in a split call:
-// `sms` SMs with 4 CTAs (8 columns) or 2 (more).
+// CTAs per KV head of a split call: one wave of them over all heads.
 int split_ctas(int sms, int nt, int num_kv_heads) {
-  const int all = sms * (nt == 1 ? 4 : 2);
+  const int all = sms * (nt == 1 ? PAGEDKV_Q4_CTAS : 2);
   return all / num_kv_heads > 0 ? all / num_kv_heads : 1;
 }
 
