@@ -893,6 +893,17 @@ kv_status pagedkv_copy_blocks_q4(void *kv_cache, const int32_t *block_pairs,
 size_t pagedkv_q4_workspace_bytes(int max_query_len, int num_q_heads,
                                   int num_kv_heads, int head_dim);
 
+/* The same and what long queries take beside it: paged_attention_multi_q4 widens
+ * the rows of every sequence whose query tokens x grouped heads are at least 128
+ * into fp16 operands in the workspace (4 * num_kv_heads * head_dim bytes per token
+ * of max_seq_len and such sequence) and serves it on the tensor cores.  With a
+ * smaller workspace, pagedkv_q4_workspace_bytes at least, it does so for as many
+ * sequences as fit and takes longer for the others (prompts about four times). */
+size_t pagedkv_q4_long_workspace_bytes(int batch, int num_tokens,
+                                       int max_query_len, int max_seq_len,
+                                       int num_q_heads, int num_kv_heads,
+                                       int head_dim);
+
 /* paged_attention_decode and paged_attention_multi over a 4-bit pool; arguments,
  * errors and the treatment of bad lengths, offsets and blocks as there (the rows
  * of a sequence with n_b > max_query_len are all zeroed).  The codes enter both

@@ -93,6 +93,7 @@ SIGNATURES = {
     "pagedkv_read_q4": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
     "pagedkv_copy_blocks_q4": (_I, [_P, _P, _I, _I, _I, _I, _I, _P]),
     "pagedkv_q4_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "pagedkv_q4_long_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "paged_attention_decode_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P]),
     "paged_attention_multi_q4": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                       _SZ, _P]),
@@ -1123,6 +1124,14 @@ def copy_blocks_q4(kv_cache, block_pairs, block_size, stream=None):
 
 def q4_workspace_bytes(num_q_heads, num_kv_heads, head_dim, max_query_len=1) -> int:
     return load().pagedkv_q4_workspace_bytes(max_query_len, num_q_heads, num_kv_heads, head_dim)
+
+
+def q4_long_workspace_bytes(batch, num_tokens, max_query_len, max_seq_len, num_q_heads, num_kv_heads,
+                            head_dim) -> int:
+    """q4_workspace_bytes, and what lets paged_attention_multi_q4 serve every
+    sequence with long queries on the tensor cores."""
+    return load().pagedkv_q4_long_workspace_bytes(batch, num_tokens, max_query_len, max_seq_len, num_q_heads,
+                                                  num_kv_heads, head_dim)
 
 
 def _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size, workspace, query_start):

@@ -15,7 +15,7 @@
 // fp16; p * vmin is summed in fp32.  A column's reference is the largest of
 // score + exponent of max(vscale, |vmin| / 16) so far, less five, not of the
 // score alone: p * vscale then has fp16's whole range below 2^11 whatever the
-// scales are.  It moves only when a tile passes it by more than ten octaves.
+// scales are.  It moves only when a product passes 2^11 (or a weight 2^32).
 //
 // Tile products (mma.sync m16n8k16, fp32 sums) with tokens, then dims, on M and
 // the columns (query token x grouped head) on N: the unpacked codes are used for
@@ -66,6 +66,7 @@ struct Q4Args {
   float* ws_ml;                // [Hkv, ctas, 2, columns, 2]: (reference, sum)
   int4* ws_meta;               // [Hkv, ctas]: {CTAs that follow, first token row, tokens, -}
   unsigned int* flags;
+  const int* slot_of;          // [batch]: >= 0 where the long queries' kernel has the sequence; or null
   int max_blocks, batch, num_tokens, max_query_len, num_q_heads, num_kv_heads;
   int num_blocks, max_seq_len;
   int group;                   // query heads per KV head
@@ -97,7 +98,9 @@ __device__ __forceinline__ Seq seq_of(const Q4Args& a, int b) {
   const bool len = s.L > 0 && s.L <= a.max_seq_len && (s.L - 1) / BS < a.max_blocks &&
                    s.n <= s.L && s.n <= a.max_query_len;
   s.bad = !rows || (!len && (!kMulti || s.n > 0));
-  const bool use = !s.bad && s.n > 0;
+  bool use = !s.bad && s.n > 0;
+  if constexpr (kMulti)
+    if (a.slot_of != nullptr && use) use = __ldg(a.slot_of + b) < 0;
   s.nblk = use ? (s.L + BS - 1) / BS : 0;
   s.nct = use ? (kMulti ? (s.n + a.tile_tokens - 1) / a.tile_tokens : 1) : 0;
   return s;
@@ -206,6 +209,9 @@ __device__ __forceinline__ float value_exponent(const uint32_t (&pairs)[N]) {
   return (float)(max(max(s, m - 4), 27) - 127);
 }
 
+__device__ __forceinline__ float pair_scale(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float pair_min(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes * 2^-24, * 2^-20
 
 #ifndef PAGEDKV_Q4_CTAS
@@ -220,14 +226,15 @@ struct Cfg4 {
   static constexpr int kBlocks = 32 / BS;                 // blocks of a step
   static constexpr int kStage = kBlocks * G::kRecord;
   static constexpr int kTiles = NT <= 2 ? 2 : 1;          // tiles worked on together
-  static constexpr bool kQShared = NT > 2;               // q's fragments in shared memory
-  static constexpr int kQBytes = kQShared ? (D / 16) * NT * 32 * 8 : 0;
-  static constexpr int kDump = NT * (D / 4 + 4);          // registers a lane hands over
-  static constexpr int kRedBytes = 2 * kDump * 32 * 4;
-  static constexpr int kBudget = (224 / kCtasPerSm - 1) * 1024 - kRedBytes - kQBytes;
+  static constexpr bool kQShared = NT > 2;               // q's fragments stay in shared memory
+  static constexpr int kQBytes = (D / 16) * NT * 32 * 8;
+  // what the warps hand over at the end of a sequence: O, then (reference, sum)
+  static constexpr int kRow = NT == 4 ? D : D + 4;        // floats of a column
+  static constexpr int kDumpBytes = kWarps * kCols * (kRow + 2) * 4;
+  static constexpr int kBudget = (225 / kCtasPerSm - 1) * 1024 - kDumpBytes - kQBytes - 1024;
   static constexpr int kStages0 = kBudget / (kWarps * kStage);
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-  static constexpr int kSmem = kWarps * kStages * kStage + kRedBytes + kQBytes;
+  static constexpr int kSmem = kWarps * kStages * kStage + kDumpBytes + kQBytes;
   static_assert(kStages >= 2, "a ring has two stages at least");
 };
 
@@ -242,12 +249,17 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
   __shared__ long long scan[kWarps];
   __shared__ int start_b, start_ct, start_us, range_len;
   __shared__ int range_per;
+  __shared__ unsigned int q_top;                    // bits of the largest finite |q| of a piece
+  __shared__ float q_sum[C::kCols][NG];
 
   const int hk = blockIdx.x, c = a.whole ? (int)(gridDim.y - 1 - blockIdx.y) : (int)blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int GQ = a.group, Hq = a.num_q_heads;
 
+  // (launched as a programmatic dependent: what is before may still run until here)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < kWarps * S)
     mbar_init(smem_addr(&bars[threadIdx.x / S][threadIdx.x % S]), 1);
   if (threadIdx.x == 0) start_b = -1;
@@ -302,7 +314,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     }
     at -= sum;                                      // sequences before this thread's
     constexpr int kMinRange = kMinRangeTokens / BS;
-    const long long even = (total + a.ctas - 1) / a.ctas;
+    const long long even = total < 0x7fffffff - a.ctas ? ((int)total + a.ctas - 1) / a.ctas
+                                                       : (total + a.ctas - 1) / a.ctas;
     const long long per = a.whole ? 1 : (even > kMinRange ? even : kMinRange);
     const long long u0 = (long long)c * per;
     if (u0 >= at && u0 < at + sum) {
@@ -317,8 +330,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
             start_us = 0;
             range_len = s.nblk;
           } else {
-            start_ct = (int)(in / s.nblk);
-            start_us = -(int)(in % s.nblk);
+            start_ct = kMulti ? (int)(in / s.nblk) : 0;
+            start_us = -(int)(in - (long long)start_ct * s.nblk);
             range_len = (int)(u0 + per < total ? per : total - u0);
             range_per = (int)per;
           }
@@ -332,13 +345,13 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
   const int64_t cell = (int64_t)hk * a.ctas + c;
   if (start_b < 0) {                                // nothing for this CTA
     if (!a.whole && threadIdx.x == 0) a.ws_meta[cell] = make_int4(0, 0, 0, 0);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     return;
   }
 
   const uint32_t ring = smem_addr(smem4) + warp * S * C::kStage;
-  float* red = reinterpret_cast<float*>(smem4 + kWarps * S * C::kStage);
-  const uint32_t qsm = smem_addr(smem4) + kWarps * S * C::kStage + C::kRedBytes;
+  float* dump = reinterpret_cast<float*>(smem4 + kWarps * S * C::kStage);   // [warp][column][kRow]
+  float* dump_ml = dump + kWarps * C::kCols * C::kRow;                      // [warp][column][2]
+  const uint32_t qsm = smem_addr(smem4) + kWarps * S * C::kStage + C::kDumpBytes;
 
   // ---- the warp's ring: every fourth step of each piece ---------------------
   constexpr int PB = C::kBlocks;
@@ -382,6 +395,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     fj += kWarps * PB;
     settle();
   };
+#pragma unroll 1
   for (int s = 0; s < S; ++s) fetch();
 
   // rows of a 16-token tile: MMA row r holds token tau(r) (and 8 + tau), so
@@ -396,87 +410,97 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     const int tok0 = w.ct * a.tile_tokens;
     const int ntok = kMulti ? min(a.tile_tokens, w.s.n - tok0) : 1;
     const int nta = (ntok * GQ + 7) / 8;            // column tiles in use
-    uint32_t qf[C::kQShared ? 1 : kKSteps][C::kQShared ? 1 : NT][2];
-    float qs[NT][NG][2];                            // sums of q, in score units
-    int cpos[kMulti ? NT : 1][2];
     float kfac;
     {
-      // B fragments: column g, words 2t and 2t + 1 of every group
-      float amax = 0.0f;
+      // A thread takes words (8 elements) word, of columns first, first + step, ..
+      constexpr int kWords = D / 8, kStep = kThreads4 / kWords, kEach = (C::kCols + kStep - 1) / kStep;
+      const int word = threadIdx.x % kWords, col0 = threadIdx.x / kWords;
+      uint4 x[kEach];
+      uint32_t top = 0;
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
-        int e = 0;
-        if (pass == 1) {
+      for (int i = 0; i < kEach; ++i) {
+        const int col = col0 + i * kStep, tok = col / GQ;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (tok < ntok && col < a.tile_tokens * GQ)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(
+                           a.q + ((int64_t)(w.s.q0 + tok0 + tok) * Hq + (int64_t)hk * GQ + col % GQ) * D) + word);
+        // the largest finite magnitude, both halves of a word at once
+        const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-          if (amax > 0.0f) e = 14 - (int)((__float_as_uint(amax) >> 23) - 126);   // amax * 2^e in [2^13, 2^14)
-          e = min(max(e, -110), 110);
-          kfac = a.scale_log2 * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23);
-          if constexpr (C::kQShared) __syncthreads();   // the last unit's fragments are no longer read
-        }
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int col = 8 * nt + g;
-          const int i = col / GQ;
-          const bool used = i < ntok && col < a.tile_tokens * GQ;
-          const uint4* row = reinterpret_cast<const uint4*>(
-              a.q + ((int64_t)(w.s.q0 + tok0 + (used ? i : 0)) * Hq + (int64_t)hk * GQ + (used ? col % GQ : 0)) * D);
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int ci = 0; ci < 2; ++ci) {
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (used) x = __ldg(row + gr * 8 + 2 * t + ci);
-              const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-              float v[8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(xw[k] << 16);
-                v[2 * k + 1] = __uint_as_float(xw[k] & 0xffff0000u);
-              }
-              if (pass == 0) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  if (fabsf(v[k]) <= 3.4e38f) amax = fmaxf(amax, fabsf(v[k]));
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum += v[k];
-                const float down = up * 0.0625f;
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                  const uint32_t x0 = pack2<true>(v[2 * hh] * up, v[2 * hh + 4] * up);
-                  const uint32_t x1 = pack2<true>(v[2 * hh + 1] * down, v[2 * hh + 5] * down);
-                  const int ks = (gr * 2 + ci) * 2 + hh;
-                  if constexpr (C::kQShared) {
-                    if (warp == nt % kWarps)
-                      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qsm + ((ks * NT + nt) * 32 + lane) * 8),
-                                   "r"(x0), "r"(x1)
-                                   : "memory");
-                  } else {
-                    qf[ks][nt][0] = x0;
-                    qf[ks][nt][1] = x1;
-                  }
-                }
-              }
-            }
-            if (pass == 1) {
-              sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-              sum += __shfl_xor_sync(0xffffffffu, sum, 2);          // column g's sum, in lanes 4g ..
-              sum *= a.scale_log2;
-              qs[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-              qs[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-            }
-          }
-          if constexpr (kMulti) {
-            const int p0 = (8 * nt + 2 * t) / GQ, p1 = (8 * nt + 2 * t + 1) / GQ;
-            cpos[nt][0] = w.s.L - w.s.n + tok0 + min(p0, ntok - 1);
-            cpos[nt][1] = w.s.L - w.s.n + tok0 + min(p1, ntok - 1);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = xw[k] & 0x7fffu, hi = xw[k] >> 16 & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
         }
       }
-      if constexpr (C::kQShared) __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (threadIdx.x == 0) q_top = 0;
+      __syncthreads();                              // the last piece's fragments and sums are no longer read
+      if (lane == 0) atomicMax(&q_top, top);
+      __syncthreads();
+      top = q_top;
+      // largest * 2^e in [2^13, 2^14): exact in fp16 from 2^-27 of it on
+      int e = top > 0 ? 140 - (int)(top >> 7) : 0;
+      e = min(max(e, -110), 110);
+      // (a negative scale turns q's sign, a zero one takes q as 0: kfac is positive,
+      // so that a masked score of -infinity stays one)
+      float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      kfac = fmaxf(fabsf(a.scale_log2) * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+      if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
+      const float down = up * 0.0625f;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int col = col0 + i * kStep;
+        if (C::kCols % kStep != 0 && col >= C::kCols) break;        // (whole groups of 8 lanes)
+        const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float v[8], sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = __uint_as_float(xw[k] << 16);
+          v[2 * k + 1] = __uint_as_float(xw[k] & 0xffff0000u);
+          sum += v[2 * k] + v[2 * k + 1];
+        }
+        // B fragment of k-step ks: lane (g = column % 8, t) holds elements 2 hh, 2 hh
+        // + 4 and (times 1/16, its codes are high nibbles) 2 hh + 1, 2 hh + 5 of word
+        // 2 t + ci of the group
+        const int gr = word / 8, tt = word % 8 / 2, ci = word % 2;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int ks = (gr * 2 + ci) * 2 + hh;
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
+                           qsm + ((ks * NT + col / 8) * 32 + col % 8 * 4 + tt) * 8),
+                       "r"(pack2<true>(v[2 * hh] * up, v[2 * hh + 4] * up)),
+                       "r"(pack2<true>(v[2 * hh + 1] * down, v[2 * hh + 5] * down))
+                       : "memory");
+        }
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(__activemask(), sum, off);
+        if (word % 8 == 0) q_sum[col][gr] = sum * (up * 5.9604644775390625e-8f);   // * 2^(e - 24)
+      }
+      __syncthreads();
+    }
+    uint32_t qf[C::kQShared ? 1 : kKSteps][C::kQShared ? 1 : NT][2];
+    if constexpr (!C::kQShared) {
+#pragma unroll
+      for (int ks = 0; ks < kKSteps; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 b = lds64(qsm + ((ks * NT + nt) * 32 + lane) * 8);
+          qf[ks][nt][0] = b.x;
+          qf[ks][nt][1] = b.y;
+        }
+    }
+    // sums of q over a group, in units of the products with codes
+    float qs[NT][NG][2];
+    int cpos[kMulti ? NT : 1][2];                   // last token a column sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int col = 8 * nt + 2 * t + k;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) qs[nt][gr][k] = q_sum[col][gr];
+        if constexpr (kMulti) cpos[nt][k] = w.s.L - w.s.n + tok0 + min(col / GQ, ntok - 1);
+      }
     }
     const int all_see = kMulti ? w.s.L - w.s.n + tok0 + 1 : w.s.L;   // tokens every column sees
 
@@ -564,8 +588,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
 #pragma unroll
                 for (int x = 0; x < T; ++x) {
                   const uint32_t k0 = kp[x][0][gr], k1 = kp[x][1][gr];
-                  const float s0 = __uint_as_float(k0 << 16) * kfac, s1 = __uint_as_float(k1 << 16) * kfac;
-                  const float m0 = __uint_as_float(k0 & 0xffff0000u), m1 = __uint_as_float(k1 & 0xffff0000u);
+                  const float s0 = pair_scale(k0), s1 = pair_scale(k1);
+                  const float m0 = pair_min(k0), m1 = pair_min(k1);
 #pragma unroll
                   for (int nt = 0; nt < A; ++nt) {
                     const float* qq = qs[nt][gr];
@@ -604,34 +628,50 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
                 }
               }
             }
-            // exponents of the tokens' V: of the largest scale or |min| / 16 (rows
-            // of equal values have the least scale, and p * vmin has to stay within
-            // fp32 too), -100 at least
-            float e[T][2];
+            // ---- weights against the columns' references -------------------------
+            // p, and p * vscale as it enters the product; where one of them passes
+            // its bound (in the first tile, and rarely after it) the references move
+            // to the largest score + exponent of max(vscale, |vmin| / 16), less five
+            // (rows of equal values have the least scale, and p * vmin has to stay
+            // within fp32 too; exponents are -100 at least), and p is taken again.
+            float p[T][A][4], ps[T][A][NG][4];
+            auto weigh = [&]() {
+              float top = 0.0f, top_s = 0.0f;
 #pragma unroll
-            for (int x = 0; x < T; ++x) {
-              e[x][0] = value_exponent(vp[x][0]);
-              e[x][1] = value_exponent(vp[x][1]);
-            }
-            // ---- references ------------------------------------------------------
-            float most[A][2];
-            bool move = false;
+              for (int x = 0; x < T; ++x) {
 #pragma unroll
-            for (int nt = 0; nt < A; ++nt) {
+                for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float y = fmaxf(sc[0][nt][k] + e[0][0], sc[0][nt][k + 2] + e[0][1]);
-                if constexpr (T == 2) y = fmaxf(y, fmaxf(sc[T - 1][nt][k] + e[T - 1][0], sc[T - 1][nt][k + 2] + e[T - 1][1]));
-                most[nt][k] = y;
-                move |= y - ref[nt][k] > 10.0f;
+                  for (int k = 0; k < 4; ++k) p[x][nt][k] = ex2(fmaf(sc[x][nt][k], kfac, -ref[nt][k & 1]));
+                  top = fmaxf(fmaxf(top, p[x][nt][0]), p[x][nt][1]);
+                  top = fmaxf(fmaxf(top, p[x][nt][2]), p[x][nt][3]);
+#pragma unroll
+                  for (int gr = 0; gr < NG; ++gr) {
+                    const float s0 = pair_scale(vp[x][0][gr]), s1 = pair_scale(vp[x][1][gr]);
+                    float* y = ps[x][nt][gr];
+                    y[0] = p[x][nt][0] * s0;
+                    y[1] = p[x][nt][1] * s0;
+                    y[2] = p[x][nt][2] * s1;
+                    y[3] = p[x][nt][3] * s1;
+                    top_s = fmaxf(fmaxf(top_s, y[0]), y[1]);
+                    top_s = fmaxf(fmaxf(top_s, y[2]), y[3]);
+                  }
+                }
               }
-            }
-            if (__any_sync(0xffffffffu, move)) {
+              return top > 4294967296.0f || top_s > 2048.0f;
+            };
+            if (__any_sync(0xffffffffu, weigh())) {
+              
 #pragma unroll
               for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                  float mx = most[nt][k];
+                  float mx = -INFINITY;
+#pragma unroll
+                  for (int x = 0; x < T; ++x)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                      mx = fmaxf(mx, fmaf(sc[x][nt][k + 2 * r], kfac, value_exponent(vp[x][r])));
 #pragma unroll
                   for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                   const float to = fmaxf(ref[nt][k], mx - 5.0f);
@@ -647,6 +687,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
                   }
                 }
               }
+              weigh();
             }
 #pragma unroll
             for (int x = 0; x < T; ++x) {
@@ -657,23 +698,20 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
               lds_words(vw[1], vrow + vb * G::kRowBytes);
               lds_words(vw[2], vrow + (va + 8) * G::kRowBytes);
               lds_words(vw[3], vrow + (vb + 8) * G::kRowBytes);
-              // ---- weights: fp32 sums, p * vscale as the fp16 operand ---------------
               uint32_t pb[A][NG][2];
 #pragma unroll
               for (int nt = 0; nt < A; ++nt) {
-                const float p0 = ex2(sc[x][nt][0] - ref[nt][0]), p1 = ex2(sc[x][nt][1] - ref[nt][1]);
-                const float p2 = ex2(sc[x][nt][2] - ref[nt][0]), p3 = ex2(sc[x][nt][3] - ref[nt][1]);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
+                const float* y = p[x][nt];
+                l[nt][0] += y[0] + y[2];
+                l[nt][1] += y[1] + y[3];
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                  const uint32_t v0 = vp[x][0][gr], v1 = vp[x][1][gr];
-                  const float s0 = __uint_as_float(v0 << 16), s1 = __uint_as_float(v1 << 16);
-                  const float m0 = __uint_as_float(v0 & 0xffff0000u), m1 = __uint_as_float(v1 & 0xffff0000u);
-                  pb[nt][gr][0] = transposed8(pack2<true>(p0 * s0, p1 * s0));
-                  pb[nt][gr][1] = transposed8(pack2<true>(p2 * s1, p3 * s1));
-                  pm[nt][gr][0] = fmaf(p0, m0, fmaf(p2, m1, pm[nt][gr][0]));
-                  pm[nt][gr][1] = fmaf(p1, m0, fmaf(p3, m1, pm[nt][gr][1]));
+                  const float m0 = pair_min(vp[x][0][gr]), m1 = pair_min(vp[x][1][gr]);
+                  const float* z = ps[x][nt][gr];
+                  pb[nt][gr][0] = transposed8(pack2<true>(z[0], z[1]));
+                  pb[nt][gr][1] = transposed8(pack2<true>(z[2], z[3]));
+                  pm[nt][gr][0] = fmaf(y[0], m0, fmaf(y[2], m1, pm[nt][gr][0]));
+                  pm[nt][gr][1] = fmaf(y[1], m0, fmaf(y[3], m1, pm[nt][gr][1]));
                 }
               }
               // ---- O^T += V^T . P^T ---------------------------------------------------
@@ -682,8 +720,9 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   // tokens 2t, 2t + 1 and 2t + 8, 2t + 9; nibbles 2k and 2k + 1
-                  const uint32_t u = prmt(vw[0][gr], vw[1][gr], k >= 2 ? 0x7632u : 0x5410u) >> (k % 2 * 8);
-                  const uint32_t v = prmt(vw[2][gr], vw[3][gr], k >= 2 ? 0x7632u : 0x5410u) >> (k % 2 * 8);
+                  uint32_t u = prmt(vw[0][gr], vw[1][gr], k >= 2 ? 0x7632u : 0x5410u);
+                  uint32_t v = prmt(vw[2][gr], vw[3][gr], k >= 2 ? 0x7632u : 0x5410u);
+                  if (k % 2) u >>= 8, v >>= 8;
                   const uint32_t fa[4] = {u & kLow, u & kHigh, v & kLow, v & kHigh};
 #pragma unroll
                   for (int nt = 0; nt < A; ++nt) mma16816<true>(o[nt][gr * 4 + k], fa, pb[nt][gr][0], pb[nt][gr][1]);
@@ -703,7 +742,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
       steps(std::integral_constant<int, 1>{});
     }
 
-    // ---- the four warps' (reference, sum, O), joined in warp 0 -----------------
+    // ---- the four warps' (reference, sum, O), joined ---------------------------
     // O[nt][gr * 4 + k]: elements gr * 64 + 8 g + 2 k (c0, c1: * 2^24) and + 1 (c2, c3: * 2^20)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -723,94 +762,68 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
         }
       }
     }
-    auto give = [&](int slot) {
-      float* r = red + slot * C::kDump * 32 + lane;
+    // columns in use; the warps' shares are added by all threads, four elements each
+    const int used = ntok * GQ;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float* x = r + nt * (D / 4 + 4) * 32;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < kMTiles; ++i)
+      for (int k = 0; k < 2; ++k) {
+        const int col = 8 * nt + 2 * t + k;
+        if (col >= used) continue;
+        float* to = dump + (warp * C::kCols + col) * C::kRow;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[(i * 4 + k) * 32] = o[nt][i][k];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          x[(D / 4 + k) * 32] = ref[nt][k];
-          x[(D / 4 + 2 + k) * 32] = l[nt][k];
+        for (int gr = 0; gr < NG; ++gr) {
+          const int i = gr * 4;
+          float4* y = reinterpret_cast<float4*>(to + gr * 64 + 8 * g);
+          y[0] = make_float4(o[nt][i][k], o[nt][i][k + 2], o[nt][i + 1][k], o[nt][i + 1][k + 2]);
+          y[1] = make_float4(o[nt][i + 2][k], o[nt][i + 2][k + 2], o[nt][i + 3][k], o[nt][i + 3][k + 2]);
+        }
+        if (g == 0) {
+          dump_ml[(warp * C::kCols + col) * 2] = ref[nt][k];
+          dump_ml[(warp * C::kCols + col) * 2 + 1] = l[nt][k];
         }
       }
-    };
-    auto take = [&](int slot) {
-      const float* r = red + slot * C::kDump * 32 + lane;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float* x = r + nt * (D / 4 + 4) * 32;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float ro = x[(D / 4 + k) * 32], lo = x[(D / 4 + 2 + k) * 32];
-          const float to = fmaxf(ref[nt][k], ro), am = ex2(ref[nt][k] - to), ao = ex2(ro - to);
-          ref[nt][k] = to;
-          l[nt][k] = l[nt][k] < 0.0f || lo < 0.0f ? -1.0f : l[nt][k] * am + lo * ao;
-#pragma unroll
-          for (int i = 0; i < kMTiles; ++i) {
-            o[nt][i][k] = o[nt][i][k] * am + x[(i * 4 + k) * 32] * ao;
-            o[nt][i][k + 2] = o[nt][i][k + 2] * am + x[(i * 4 + k + 2) * 32] * ao;
-          }
-        }
-      }
-    };
-    __syncthreads();                                // the last piece's sums have been read
-    if (warp >= 2) give(warp - 2);
+    }
     __syncthreads();
-    if (warp < 2) take(warp);
-    if (warp == 1) give(1);
-    __syncthreads();
-    if (warp == 0) {
-      take(1);
-      const bool starts = w.j0 == 0;
-      // CTAs that hold the rest of the unit's visible blocks
-      const int follow = a.whole ? 0 : (c * (long long)range_per + w.us + w.visible(a) - 1) / range_per - c;
-      const bool direct = starts && follow == 0;
-      if (!direct && starts) {
-        merged = true;
-        if (lane == 0) a.ws_meta[cell] = make_int4(follow, w.s.q0 + tok0, ntok, 0);
+    const bool starts = w.j0 == 0;
+    // CTAs that hold the rest of the unit's visible blocks
+    const int follow = !starts || a.whole ? 0 : (w.us + w.visible(a) - 1) / range_per;
+    const bool direct = starts && follow == 0;
+    if (!direct && starts) {
+      merged = true;
+      if (threadIdx.x == 0) a.ws_meta[cell] = make_int4(follow, w.s.q0 + tok0, ntok, 0);
+    }
+    const int64_t part = cell * 2 + (starts ? 1 : 0);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < used * (D / 4); i += kThreads4) {
+      const int col = i / (D / 4), e = i % (D / 4) * 4;
+      float R = kNoRef, den = 0.0f;
+      bool any_bad = false;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) R = fmaxf(R, dump_ml[(v * C::kCols + col) * 2]);
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float2 ml = *reinterpret_cast<const float2*>(dump_ml + (v * C::kCols + col) * 2);
+        const float4 y = *reinterpret_cast<const float4*>(dump + (v * C::kCols + col) * C::kRow + e);
+        const float f = ex2(ml.x - R);
+        any_bad |= ml.y < 0.0f;
+        den = fmaf(f, ml.y, den);
+        sum.x = fmaf(f, y.x, sum.x);
+        sum.y = fmaf(f, y.y, sum.y);
+        sum.z = fmaf(f, y.z, sum.z);
+        sum.w = fmaf(f, y.w, sum.w);
       }
-      const int64_t part = cell * 2 + (starts ? 1 : 0);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = 8 * nt + 2 * t + k;
-          const int i = col / GQ;
-          if (i >= ntok || col >= a.tile_tokens * GQ) continue;
-          if (direct) {
-            const float r = l[nt][k] < 0.0f ? 0.0f : 1.0f / l[nt][k];
-            __nv_bfloat16* out = a.out + ((int64_t)(w.s.q0 + tok0 + i) * Hq + (int64_t)hk * GQ + col % GQ) * D;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              uint32_t x[4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const float u = o[nt][gr * 4 + m][k] * r, v = o[nt][gr * 4 + m][k + 2] * r;
-                x[m] = l[nt][k] < 0.0f ? 0u : pack2<false>(u, v);
-              }
-              *reinterpret_cast<uint4*>(out + gr * 64 + 8 * g) = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          } else {
-            float* acc = a.ws_acc + (part * C::kCols + col) * D;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              float4* to = reinterpret_cast<float4*>(acc + gr * 64 + 8 * g);
-              to[0] = make_float4(o[nt][gr * 4][k], o[nt][gr * 4][k + 2], o[nt][gr * 4 + 1][k], o[nt][gr * 4 + 1][k + 2]);
-              to[1] = make_float4(o[nt][gr * 4 + 2][k], o[nt][gr * 4 + 2][k + 2], o[nt][gr * 4 + 3][k],
-                                  o[nt][gr * 4 + 3][k + 2]);
-            }
-            if (g == 0) {
-              float* ml = a.ws_ml + (part * C::kCols + col) * 2;
-              ml[0] = ref[nt][k];
-              ml[1] = l[nt][k];
-            }
-          }
-        }
+      if (direct) {
+        const float r = 1.0f / den;
+        uint2 y = make_uint2(0u, 0u);
+        if (!any_bad) y = make_uint2(pack2<false>(sum.x * r, sum.y * r), pack2<false>(sum.z * r, sum.w * r));
+        *reinterpret_cast<uint2*>(
+            a.out + ((int64_t)(w.s.q0 + tok0 + col / GQ) * Hq + (int64_t)hk * GQ + col % GQ) * D + e) = y;
+      } else {
+        *reinterpret_cast<float4*>(a.ws_acc + (part * C::kCols + col) * D + e) = sum;
+        if (e == 0)
+          *reinterpret_cast<float2*>(a.ws_ml + (part * C::kCols + col) * 2) = make_float2(R, any_bad ? -1.0f : den);
       }
     }
   }
@@ -820,23 +833,23 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     mbar_wait(smem_addr(&bars[warp][cs]), (phase >> cs) & 1u);
     cs = cs + 1 == S ? 0 : cs + 1;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the partials of the unit that CTA c of a KV head began and later CTAs
 // ended: out = sum_i 2^(r_i - R) acc_i / sum_i 2^(r_i - R) l_i.  One CTA per
-// (range, KV head, column); its warps take the partials in turn.
+// (range, KV head, column or four of them); its warps take the partials in turn.
 template <int D>
 __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols) {
   constexpr int E = D / 32;
   __shared__ float part[4][32][E + 1];
-  const int c = blockIdx.x, hk = blockIdx.y, col = blockIdx.z;
+  const int c = blockIdx.x, hk = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t cell = (int64_t)hk * a.ctas + c;
   const int4 meta = a.ws_meta[cell];
+  if (meta.x == 0) return;
+  for (int col = blockIdx.z; col < meta.z * a.group; col += gridDim.z) {
   const int i = col / a.group;
-  if (meta.x == 0 || i >= meta.z || col >= a.tile_tokens * a.group) return;
   const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
   const int64_t p0 = (cell * 2 + 1) * cols + col;
   auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
@@ -875,7 +888,7 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
   for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
   part[warp][lane][E] = den;
   __syncthreads();
-  if (warp != 0) return;
+  if (warp == 0) {
   for (int k = 1; k < 4; ++k) {
 #pragma unroll
     for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
@@ -889,6 +902,9 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
       a.out + ((int64_t)(meta.y + i) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
   if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
   else *reinterpret_cast<uint32_t*>(out) = x[0];
+  }
+  __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -913,19 +929,24 @@ kv_status launch_q4(const Q4Args& a, cudaStream_t s) {
       set[dev] = true;
     }
   }
-  q4_kernel<D, BS, NT, kMulti>
-      <<<dim3((unsigned)a.num_kv_heads, (unsigned)a.ctas), kThreads4, C::kSmem, s>>>(a);
-  if ((st = cuda_check(cudaGetLastError(), "q4_kernel launch")) != KV_OK || a.whole) return st;
+  // Both launches are programmatic dependents of what is before them (each waits
+  // for it on the device before its first access), so that their launches overlap it.
   cudaLaunchConfig_t cfg = {};
-  const int used = (kMulti ? min(a.max_query_len, a.tile_tokens) : 1) * a.group;
-  cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)a.num_kv_heads, (unsigned)used);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)a.num_kv_heads, (unsigned)a.ctas);
+  cfg.blockDim = dim3(kThreads4);
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  st = cuda_check(cudaLaunchKernelEx(&cfg, q4_kernel<D, BS, NT, kMulti>, a), "q4_kernel launch");
+  if (st != KV_OK || a.whole) return st;
+  const int used = (kMulti ? min(a.max_query_len, a.tile_tokens) : 1) * a.group;
+  cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)a.num_kv_heads, (unsigned)(used > 8 ? (used + 3) / 4 : used));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_merge_kernel<D>, a, C::kCols), "q4_merge_kernel launch");
 }
 
@@ -953,6 +974,14 @@ int split_ctas(int sms, int nt, int num_kv_heads) {
 size_t q4_workspace(int ctas, int num_kv_heads, int nt, int head_dim) {
   const size_t cells = (size_t)ctas * num_kv_heads;
   return cells * (16 + 2 * 8 * (size_t)nt * (head_dim + 2) * sizeof(float));
+}
+
+// Sequences that may have long queries.
+int long_slots(int batch, int num_tokens, int max_query_len, int group) {
+  const int least = (kLongRows + group - 1) / group;
+  if (max_query_len < least) return 0;
+  const int most = num_tokens / least < batch ? num_tokens / least : batch;
+  return most < 65535 ? most : 65535;
 }
 
 constexpr int kMostSms = 160;                       // what the size query sizes for
@@ -1004,6 +1033,16 @@ kv_status q4_common(void* out, const void* q, const void* kv_cache, const int32_
   const int64_t tiles = long_queries ? (int64_t)num_tokens / a.tile_tokens + batch : batch;
   const int split = split_ctas(sms, nt, num_kv_heads);
   a.whole = (max_seq_len <= kWholeTokens || (long_queries && tiles >= 2 * (int64_t)split)) && tiles <= 65535;
+  // Long queries, as many sequences as the workspace has room for beside the partials
+  const size_t few = (q4_workspace(split, num_kv_heads, nt, head_dim) + 127) & ~(size_t)127;
+  const int slots = multi ? long_slots(batch, num_tokens, max_query_len, G) : 0;
+  const size_t slot = q4_slot_bytes(num_kv_heads, head_dim, max_seq_len), plan = q4_plan_bytes(batch, slots);
+  int fit = 0;
+  if (slots > 0 && workspace && aligned16(workspace) && workspace_bytes > few + 128 + plan) {
+    const size_t room = (workspace_bytes - few - 128 - plan) / slot;
+    fit = room < (size_t)slots ? (int)room : slots;
+  }
+  if (fit == slots && fit > 0) a.whole = 0;         // what is left has few rows
   a.ctas = a.whole ? (int)tiles : split;
   if (!a.whole) {
     const size_t need = q4_workspace(a.ctas, num_kv_heads, nt, head_dim);
@@ -1017,6 +1056,34 @@ kv_status q4_common(void* out, const void* q, const void* kv_cache, const int32_
     a.ws_ml = a.ws_acc + cells * 2 * 8 * nt * head_dim;
   }
   cudaStream_t s = (cudaStream_t)stream;
+  if (fit > 0) {
+    unsigned char* w = static_cast<unsigned char*>(workspace) + few;
+    w += (0 - reinterpret_cast<uintptr_t>(w)) & 127;
+    Q4LongArgs g = {};
+    g.out = a.out;
+    g.q = a.q;
+    g.kv = a.kv;
+    g.block_tables = block_tables;
+    g.seq_lens = seq_lens;
+    g.query_start = query_start;
+    g.flags = di.flags;
+    g.slots = fit;
+    g.max_blocks = max_blocks;
+    g.batch = batch;
+    g.num_tokens = num_tokens;
+    g.max_query_len = max_query_len;
+    g.num_kv_heads = num_kv_heads;
+    g.group = G;
+    g.head_dim = head_dim;
+    g.num_blocks = num_blocks;
+    g.block_size = block_size;
+    g.max_seq_len = max_seq_len;
+    g.scale_log2 = a.scale_log2;
+    // slot_of at the end of what the slots and lists take
+    g.slot_of = reinterpret_cast<int*>(w + fit * slot) + 2 * fit + 2;
+    a.slot_of = g.slot_of;
+    if ((st = launch_q4_long(g, w, di.num_sms, s)) != KV_OK) return st;
+  }
   if (head_dim == 128)
     return block_size == 32 ? launch_q4_nt<128, 32>(a, nt, s) : launch_q4_nt<128, 16>(a, nt, s);
   return block_size == 32 ? launch_q4_nt<64, 32>(a, nt, s) : launch_q4_nt<64, 16>(a, nt, s);
@@ -1032,6 +1099,15 @@ extern "C" {
 size_t pagedkv_q4_record_bytes(int block_size, int head_dim) {
   if ((block_size != 16 && block_size != 32) || (head_dim != 64 && head_dim != 128)) return 0;
   return (size_t)block_size * head_dim * 9 / 8;
+}
+
+size_t pagedkv_q4_long_workspace_bytes(int batch, int num_tokens, int max_query_len, int max_seq_len, int num_q_heads,
+                                       int num_kv_heads, int head_dim) {
+  const size_t few = pagedkv_q4_workspace_bytes(max_query_len, num_q_heads, num_kv_heads, head_dim);
+  if (few == 0 || batch <= 0 || num_tokens <= 0 || max_seq_len <= 0) return few;
+  const int slots = long_slots(batch, num_tokens, max_query_len, num_q_heads / num_kv_heads);
+  if (slots == 0) return few;
+  return few + 512 + slots * q4_slot_bytes(num_kv_heads, head_dim, max_seq_len) + q4_plan_bytes(batch, slots);
 }
 
 size_t pagedkv_q4_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim) {

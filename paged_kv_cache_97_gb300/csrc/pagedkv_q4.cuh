@@ -12,6 +12,7 @@
 // neighbours, so that a lane reads its share of all groups with one load.
 #pragma once
 
+#include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
 
 namespace pagedkv {
@@ -34,5 +35,39 @@ __device__ __forceinline__ int q4_codes_at(int x, int row, int bs, int d) {
 __device__ __forceinline__ int q4_pairs_at(int x, int row, int bs, int d) {
   return bs * d + (x * bs + row) * (d / 16);
 }
+
+// ---------------------------------------------------------------------------
+// Long queries (pagedkv_q4_tc.cu): sequences whose query tokens x grouped heads
+// fill a 128-row tile at least, as many of them as there are slots for.
+// ---------------------------------------------------------------------------
+
+constexpr int kLongRows = 128;
+
+struct Q4LongArgs {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const unsigned char* kv;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start;
+  unsigned int* flags;
+  int* slot_of;                // [batch]: a sequence's slot, or -1 (written by the plan)
+  // set by launch_q4_long
+  unsigned char* images;       // [slots, Hkv, chunks, 2, 128 rows] fp16 operand images of K and V
+  int2* exps;                  // [slots, Hkv, chunks]: their powers of two
+  int* list;                   // [slots]: the listed sequences
+  int* bad;                    // [slots]: a block outside the pool
+  int* counters;               // [2]: sequences listed, units taken
+  int slots, chunks;
+  int max_blocks, batch, num_tokens, max_query_len, num_kv_heads, group, head_dim, num_blocks, block_size, max_seq_len;
+  float scale_log2;
+};
+
+// Bytes of a slot, and of the plan with `batch` slot_of entries before it.
+size_t q4_slot_bytes(int num_kv_heads, int head_dim, int max_seq_len);
+size_t q4_plan_bytes(int batch, int slots);
+// Plan, images and attention of the long sequences; `memory` (128-byte aligned)
+// holds slots * q4_slot_bytes and the lists.
+kv_status launch_q4_long(Q4LongArgs a, void* memory, int sms, cudaStream_t s);
 
 }  // namespace pagedkv

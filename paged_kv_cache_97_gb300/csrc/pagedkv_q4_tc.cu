@@ -1,0 +1,692 @@
+// pagedkv_q4_tc.cu -- attention of long queries (prompts, chunks of them) over
+// the 4-bit pool on tcgen05 with TMEM accumulators.
+//
+// 256 rows (query token x grouped head) of a sequence share every key, so the
+// codes are widened once per call instead of once per row tile: a first kernel
+// writes, for every sequence with long queries and KV head, the rows of each 128
+// keys as two fp16 operand images (K and V, 128-byte-swizzled bands of 64
+// elements, exactly as the tensor core reads them), each under one power of two
+// that puts its largest magnitude in [2^12, 2^13).  A value is then within 2^-11
+// of itself, or 2^-37 of the largest of its 128 rows.  The attention kernel loads
+// an image with one bulk copy; K's power multiplies the scores, V's goes into the
+// softmax's reference: with s a score in base 2 and E the chunk's power,
+//   p = 2^(s + E - m),  O += p V / 2^E,  l += p / 2^E,  out = O / l,
+// m at most the row's largest s + E less five, so that p as an fp16 number is
+// within 2^-11 of itself, or 2^-30 of the row's largest.
+//
+// Images cost 4 d bytes per token and KV head written once and read by every
+// 256 rows: 1 % of the arithmetic's time for a prompt.  The attention kernel is
+// bound by the exponentials (32 K a chunk at 16 per cycle and SM) and the MMAs
+// alike.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "pagedkv_common.cuh"
+#include "pagedkv_device.cuh"
+#include "pagedkv_q4.cuh"
+#include "pagedkv_tc.cuh"
+
+namespace pagedkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kRows = 128;                // query rows per tile (the MMA's M)
+constexpr int kTiles = 2;                 // row tiles per CTA, computed in ping-pong
+constexpr int kChunk = 128;               // keys per chunk
+constexpr int kKStages = 2, kVStages = 3; // V is released later than K
+constexpr int kSoftmaxWarps = 4 * kTiles; // one row per thread
+constexpr int kMmaWarp = kSoftmaxWarps, kKWarp = kMmaWarp + 1, kVWarp = kMmaWarp + 2;
+constexpr int kThreadsTc = (kSoftmaxWarps + 3) * 32;
+constexpr int kTmemCols = 512;            // the whole TMEM: one CTA per SM
+constexpr float kSlack = 8.0f;            // octaves a row may pass its reference by
+constexpr float kHead = 5.0f;             // octaves above 1 a reference leaves p
+
+template <int D>
+struct Img {
+  static constexpr int kBytes = kChunk * D * 2;          // K (or V) of a chunk; Q of a tile
+  static constexpr int kUsed = (kTiles + kKStages + kVStages) * kBytes + 1024;
+  // at least 120 KB, so that two CTAs never share an SM (each takes the whole TMEM)
+  static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+  __host__ __device__ static constexpr uint32_t ocol(int g) { return (uint32_t)(g * D); }
+  __host__ __device__ static constexpr uint32_t scol(int g) { return (uint32_t)(2 * D + 128 * g); }
+};
+
+// ---------------------------------------------------------------------------
+// Plan: the sequences with long queries, as many as have images
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ bool long_sequence(const Q4LongArgs& a, int b) {
+  const int q0 = a.query_start[b], q1 = a.query_start[b + 1], n = q1 - q0, L = a.seq_lens[b];
+  return q0 >= 0 && n > 0 && q1 <= a.num_tokens && L > 0 && L <= a.max_seq_len &&
+         (L - 1) / a.block_size < a.max_blocks && n <= L && n <= a.max_query_len &&
+         (int64_t)n * a.group >= kLongRows;
+}
+
+__global__ void __launch_bounds__(256) q4_plan_kernel(const Q4LongArgs a) {
+  __shared__ int sums[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = (a.batch + 255) / 256;
+  const int b0 = threadIdx.x * run, b1 = min(a.batch, b0 + run);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += long_sequence(a, b);
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int rank = incl - mine, total = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) rank += sums[w];
+    total += sums[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    int slot = -1;
+    if (long_sequence(a, b)) {
+      if (rank < a.slots) {
+        slot = rank;
+        a.list[rank] = b;
+        a.bad[rank] = 0;
+      }
+      ++rank;
+    }
+    a.slot_of[b] = slot;
+  }
+  if (threadIdx.x == 0) {
+    a.counters[0] = min(total, a.slots);
+    a.counters[1] = 0;                              // units taken
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Images
+// ---------------------------------------------------------------------------
+
+template <int D, int BS>
+__global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
+  using G = Geo4<D, BS>;
+  constexpr int NG = G::kGroups;
+  __shared__ unsigned int top[2];
+  __shared__ int32_t blk[kChunk / 16];
+  __shared__ int any_bad;
+  const int c = blockIdx.x, hk = blockIdx.y, slot = blockIdx.z;
+  if (slot >= a.counters[0]) return;
+  const int b = a.list[slot], L = a.seq_lens[b];
+  const int t0 = c * kChunk, rows = min(kChunk, L - t0);
+  if (rows <= 0) return;
+  if (threadIdx.x < 2) top[threadIdx.x] = 0;
+  if (threadIdx.x == 0) any_bad = 0;
+  __syncthreads();
+  if (threadIdx.x < kChunk / BS && (int)threadIdx.x * BS < rows) {
+    const int id = a.block_tables[(int64_t)b * a.max_blocks + t0 / BS + threadIdx.x];
+    const bool ok = id >= 0 && id < a.num_blocks;
+    if (!ok) any_bad = 1;
+    blk[threadIdx.x] = ok ? id : 0;
+  }
+  __syncthreads();
+  if (any_bad) {
+    if (threadIdx.x == 0) {
+      a.bad[slot] = 1;
+      atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
+    }
+    return;
+  }
+  const int x = threadIdx.x >> 7;                   // 0: K, 1: V
+  auto record = [&](int r) { return a.kv + ((int64_t)blk[r / BS] * a.num_kv_heads + hk) * G::kRecord; };
+  // the largest magnitude of the rows: a group's values lie between min and min + 15 scale
+  {
+    const int r = threadIdx.x & 127;
+    float m = 0.0f;
+    if (r < rows) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(record(r) + q4_pairs_at(x, r % BS, BS, D));
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        const float s = __uint_as_float(p[gr] << 16), lo = __uint_as_float(p[gr] & 0xffff0000u);
+        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(fmaf(15.0f, s, lo))));
+      }
+    }
+    const unsigned int u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if ((threadIdx.x & 31) == 0) atomicMax(&top[x], u);
+  }
+  __syncthreads();
+  // value * 2^-e is at most [2^12, 2^13); -80 keeps the sums of p / 2^E within fp32
+  const int e = min(max((int)(top[x] >> 23) - 127 - 12, -80), 100);
+  const int64_t cell = ((int64_t)slot * a.num_kv_heads + hk) * a.chunks + c;
+  if ((threadIdx.x & 127) == 0) reinterpret_cast<int*>(a.exps + cell)[x] = e;
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  unsigned char* img = a.images + (cell * 2 + x) * Img<D>::kBytes;
+  const int w4 = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 2
+  for (int r = w4 * 8 + g; r < kChunk; r += 32) {
+    const bool live = r < rows;
+    uint32_t w[2 * NG], pair[NG];
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) pair[i] = 0;
+    if (live) {
+      const unsigned char* rec = record(r);
+      const unsigned char* from = rec + q4_codes_at(x, r % BS, BS, D) + t * (D / 8);
+      if constexpr (NG == 2) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(from));
+        w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
+      } else {
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(from));
+        w[0] = y.x, w[1] = y.y;
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+        pair[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + q4_pairs_at(x, r % BS, BS, D)) + i);
+    }
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      const float s = __uint_as_float(pair[gr] << 16) * f, lo = __uint_as_float(pair[gr] & 0xffff0000u) * f;
+#pragma unroll
+      for (int ci = 0; ci < 2; ++ci) {
+        const uint32_t y = w[ci * NG + gr];
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // c as fp32: the low bits of 2^23 + c
+          const float c0 = __uint_as_float(0x4B000000u | (y >> (8 * k) & 15u)) - 8388608.0f;
+          const float c1 = __uint_as_float(0x4B000000u | (y >> (8 * k + 4) & 15u)) - 8388608.0f;
+          o[k] = pack2<true>(fmaf(s, c0, lo), fmaf(s, c1, lo));
+        }
+        *reinterpret_cast<uint4*>(img + gr * (kChunk * 128) + sw128(r, 2 * t + ci)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+
+template <bool kMask>
+__device__ __forceinline__ float half_max(const uint32_t (&raw)[64], int first, int lim) {
+  float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 64; ++j) {
+    float v = __uint_as_float(raw[j]);
+    if (kMask && first + j > lim) v = -INFINITY;
+    mr[j & 3] = fmaxf(mr[j & 3], v);
+  }
+  return fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3]));
+}
+
+// p = 2^(raw * k + add) (0 past `lim`) as fp16 pairs; their fp32 sum.
+template <bool kMask>
+__device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&pw)[32], int first, int lim, float k,
+                                          float add) {
+  float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float p0 = ex2(fmaf(__uint_as_float(raw[2 * j]), k, add));
+    float p1 = ex2(fmaf(__uint_as_float(raw[2 * j + 1]), k, add));
+    if (kMask) {
+      p0 = first + 2 * j <= lim ? p0 : 0.0f;
+      p1 = first + 2 * j + 1 <= lim ? p1 : 0.0f;
+    }
+    ls[(2 * j) & 3] += p0;
+    ls[(2 * j + 1) & 3] += p1;
+    pw[j] = pack2<true>(p0, p1);
+  }
+  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+}
+
+__device__ __forceinline__ void bulk_image(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  mbar_expect_tx(bar, bytes);
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a) {
+  using I = Img<D>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  __shared__ uint64_t s_full[kTiles], p_full[kTiles], o_done[kTiles], drain_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ int scan[32];
+  __shared__ int sh_unit, sh_slot, sh_pr, sh_fail;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hkv = a.num_kv_heads, GQ = a.group, Hq = Hkv * GQ;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - smem_addr(smem_raw));
+  auto q_img = [&](int g) { return base + (uint32_t)(g * I::kBytes); };
+  auto k_img = [&](int s) { return base + (uint32_t)((kTiles + s) * I::kBytes); };
+  auto v_img = [&](int s) { return base + (uint32_t)((kTiles + kKStages + s) * I::kBytes); };
+  auto pairs_of = [&](int slot) {
+    const int b = a.list[slot];
+    return ((a.query_start[b + 1] - a.query_start[b]) * GQ + kTiles * kRows - 1) / (kTiles * kRows);
+  };
+  // units: (pair of row tiles, KV head); pairs per listed sequence, summed by warp 0
+  const int count = a.counters[0];
+  const int per = (count + 31) / 32;
+  int mine = 0;
+  if (warp == 0) {
+    for (int i = 0; i < per; ++i)
+      if (lane * per + i < count) mine += pairs_of(lane * per + i);
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    scan[lane] = incl;
+  }
+  __syncthreads();
+  const int pairs = scan[31];
+  const long long units = (long long)pairs * Hkv;
+  bool tm_held = false;
+  uint32_t tm = 0;
+
+  for (;;) {
+    __syncthreads();                                // the last unit's readers are done
+    // Units are taken as CTAs become free; the last pairs of the last sequence
+    // (which see the most keys) first.
+    if (tid == 0) {
+      sh_unit = atomicAdd(&a.counters[1], 1);
+      sh_fail = 0;
+    }
+    __syncthreads();
+    const int u = sh_unit;
+    if (u >= units) break;
+    const int hk = u % Hkv, x = pairs - 1 - u / Hkv;
+    if (warp == 0 && x >= scan[lane] - mine && x < scan[lane]) {
+      int acc = scan[lane] - mine;
+      for (int i = 0; i < per; ++i) {
+        const int slot = lane * per + i;
+        if (slot >= count) break;
+        const int pl = pairs_of(slot);
+        if (x < acc + pl) {
+          sh_slot = slot;
+          sh_pr = x - acc;
+          break;
+        }
+        acc += pl;
+      }
+    }
+    __syncthreads();
+    const int slot = sh_slot, pr = sh_pr, b = a.list[slot];
+    const int q0 = a.query_start[b], n = a.query_start[b + 1] - q0, L = a.seq_lens[b];
+    const bool bad = a.bad[slot] != 0;
+    const int rows_b = n * GQ, row0 = pr * (kTiles * kRows);
+    const bool live1 = row0 + kRows < rows_b;       // tile 1 holds rows
+    const int last_row = min(row0 + kTiles * kRows, rows_b) - 1;
+    const int t_end = L - n + last_row / GQ + 1;    // keys the last row sees
+    const int nch = bad ? 0 : (t_end + kChunk - 1) / kChunk;
+    const int64_t cell = ((int64_t)slot * Hkv + hk) * a.chunks;
+    const int tile = warp >> 2, ri = tid & (kRows - 1);
+    const int r = row0 + tile * kRows + ri;         // (warps 0-7) this thread's row
+    const bool row_valid = warp < kSoftmaxWarps && r < rows_b;
+    const int pos = row_valid ? L - n + r / GQ : -1;
+    const int64_t qrow = row_valid ? (int64_t)(q0 + r / GQ) * Hq + (int64_t)hk * GQ + r % GQ : 0;
+    // Q row as fp16 under a power of two (largest in [2^13, 2^14)) into its tile's
+    // swizzled bands.  A negative scale turns its sign, a zero one takes it as 0.
+    float sl2 = 0.0f;
+    if (warp < kSoftmaxWarps) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * D);
+      uint4 qv[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) qv[c] = row_valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = w4[i] & 0x7fffu, hi = w4[i] >> 16 & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+      }
+      const int e = min(max(top > 0 ? 140 - (int)(top >> 7) : 0, -110), 110);
+      float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+      if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
+      unsigned char* qdst = gbase + (q_img(tile) - base);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t w4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+        uint32_t o4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o4[i] = pack2<true>(__uint_as_float(w4[i] << 16) * up, __uint_as_float(w4[i] & 0xffff0000u) * up);
+        *reinterpret_cast<uint4*>(qdst + (c / 8) * (kRows * 128) + sw128(ri, c % 8)) =
+            make_uint4(o4[0], o4[1], o4[2], o4[3]);
+      }
+    }
+    if (tid == 0) {
+      for (int s = 0; s < kKStages; ++s) {
+        mbar_init(smem_addr(&k_full[s]), 1);
+        mbar_init(smem_addr(&k_empty[s]), 1);
+      }
+      for (int s = 0; s < kVStages; ++s) {
+        mbar_init(smem_addr(&v_full[s]), 1);
+        mbar_init(smem_addr(&v_empty[s]), 1);
+      }
+      for (int g = 0; g < kTiles; ++g) {
+        mbar_init(smem_addr(&s_full[g]), 1);
+        mbar_init(smem_addr(&p_full[g]), kRows);
+        mbar_init(smem_addr(&o_done[g]), 1);
+      }
+      mbar_init(smem_addr(&drain_bar), 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const bool alloc_now = nch > 0 && !tm_held;
+    if (alloc_now && warp == 0) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                   ::"r"(smem_addr(&tmem_base)), "r"(kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // Q images -> tensor core
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (alloc_now) {
+      tm_held = true;
+      tm = tmem_base;
+    }
+    float m_ref = -INFINITY, l = 0.0f;
+
+    if (nch > 0) {
+      if (warp == kMmaWarp) {
+        // One lane issues.  Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage
+        // free], S_1(c+1), [K stage free]: one tile's softmax runs beside the other
+        // tile's products.  (S_g(c+1) overwrites the columns that P . V_g(c) reads;
+        // the MMAs of one issuing thread run in order.)
+        if (lane == 0) {
+          bool ok = true;
+          const uint32_t id_s = mma_idesc<true>(kRows, kChunk, 0), id_o = mma_idesc<true>(kRows, D, 1);
+          auto issue_s = [&](int g, int c) {
+            const uint32_t kb = k_img(c % kKStages);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              mma_ss(tm + I::scol(g), smem_desc(q_img(g) + (ks / 4) * (kRows * 128) + (ks % 4) * 32, 16, 1024),
+                     smem_desc(kb + (ks / 4) * (kChunk * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
+            mma_commit(smem_addr(&s_full[g]));
+          };
+          auto issue_pv = [&](int g, int c, int nsub) {
+            const uint32_t vb = v_img(c % kVStages);
+            for (int kk = 0; kk < nsub; ++kk)
+              mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, smem_desc(vb + kk * (16 * 128), kChunk * 128, 1024),
+                     id_o, (c > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(smem_addr(&o_done[g]));
+          };
+          if (mbar_wait(smem_addr(&k_full[0]), 0)) {
+            tc_fence_after();
+            issue_s(0, 0);
+            if (live1) issue_s(1, 0);
+            mma_commit(smem_addr(&k_empty[0]));
+          } else {
+            ok = false;
+          }
+          for (int c = 0; c < nch && ok; ++c) {
+            const int vs = c % kVStages, ks1 = (c + 1) % kKStages;
+            if (!mbar_wait(smem_addr(&v_full[vs]), (c / kVStages) & 1)) { ok = false; break; }
+            const int nsub = (min(t_end - c * kChunk, kChunk) + 15) / 16;
+            const bool next = c + 1 < nch;
+            if (!mbar_wait(smem_addr(&p_full[0]), c & 1)) { ok = false; break; }
+            if (next && !mbar_wait(smem_addr(&k_full[ks1]), ((c + 1) / kKStages) & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(0, c, nsub);
+            if (next) issue_s(0, c + 1);
+            if (live1) {
+              if (!mbar_wait(smem_addr(&p_full[1]), c & 1)) { ok = false; break; }
+              tc_fence_after();
+              issue_pv(1, c, nsub);
+            }
+            mma_commit(smem_addr(&v_empty[vs]));
+            if (next) {
+              if (live1) issue_s(1, c + 1);
+              mma_commit(smem_addr(&k_empty[ks1]));
+            }
+          }
+          if (!ok) sh_fail = 1;
+        }
+        __syncwarp();
+      } else if (warp == kKWarp || warp == kVWarp) {
+        // one lane per operand: chunk c into stage c % stages once the MMAs are done with it
+        if (lane == 0) {
+          const bool is_k = warp == kKWarp;
+          const int nst = is_k ? kKStages : kVStages;
+          uint64_t* full = is_k ? k_full : v_full;
+          uint64_t* empty = is_k ? k_empty : v_empty;
+          const unsigned char* src = a.images + (cell * 2 + (is_k ? 0 : 1)) * (int64_t)I::kBytes;
+          int issued = 0;
+          bool ok = true;
+          for (int c = 0; c < nch; ++c) {
+            const int st = c % nst;
+            if (c >= nst && !mbar_wait(smem_addr(&empty[st]), (c / nst - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            bulk_image(is_k ? k_img(st) : v_img(st), src + (int64_t)c * 2 * I::kBytes, I::kBytes, smem_addr(&full[st]));
+            issued = c + 1;
+          }
+          if (!ok) sh_fail = 1;
+          // every copy has landed before the CTA moves on (normally already so)
+          for (int st = 0; st < nst && st < issued; ++st)
+            mbar_wait(smem_addr(&full[st]), ((issued - 1 - st) / nst) & 1);
+        }
+        __syncwarp();
+      } else if (tile == 0 || live1) {
+        // One row per thread.  A chunk row's 128 scores in two halves, each read from
+        // TMEM once: its largest is tested against the reference, then P is written
+        // over the columns the half has read.  When a half passes the reference by
+        // more than kSlack octaves the reference moves by whole octaves, so that the
+        // rescaling of O (once P . V of the chunk before is done) and of a first half
+        // already written is exact.
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_tmem = tm + lane_base + I::scol(tile), o_tmem = tm + lane_base + I::ocol(tile);
+        bool ok = true;
+        const bool warp_live = __any_sync(0xffffffffu, row_valid);
+        int2 ex = __ldg(a.exps + cell);
+        for (int c = 0; c < nch; ++c) {
+          const int2 now = ex;
+          if (c + 1 < nch) ex = __ldg(a.exps + cell + c + 1);
+          if (__shfl_sync(0xffffffffu, sh_fail, 0)) { ok = false; break; }
+          if (!warp_wait(smem_addr(&s_full[tile]), c & 1)) { ok = false; break; }
+          tc_fence_after();
+          if (!warp_live) {                         // padding rows: keep the barriers' phases
+            tc_fence_before();
+            mbar_arrive(smem_addr(&p_full[tile]));
+            continue;
+          }
+          const float kf = sl2 * __uint_as_float((uint32_t)(127 + now.x) << 23), ev = (float)now.y;
+          const int cstart = c * kChunk, lim = pos;
+          const bool masked = __any_sync(0xffffffffu, cstart + kChunk - 1 > lim);
+          float lsum = 0.0f;
+#pragma unroll
+          for (int ps = 0; ps < 2; ++ps) {
+            uint32_t raw[64];
+            tmem_read64(s_tmem + 64 * ps, raw);
+            const int first = cstart + 64 * ps;
+            const float mx_raw = masked ? half_max<true>(raw, first, lim) : half_max<false>(raw, first, lim);
+            const float mx = mx_raw == -INFINITY ? -INFINITY : fmaf(mx_raw, kf, ev - kHead);
+            const bool need = m_ref == -INFINITY ? mx > -INFINITY : mx > m_ref + kSlack;
+            if (__any_sync(0xffffffffu, need)) {
+              const float k = (need && m_ref != -INFINITY) ? ceilf(mx - m_ref) : 0.0f;
+              const float m_new = !need ? m_ref : (m_ref == -INFINITY ? mx : m_ref + k);
+              const float alpha = need ? (m_ref == -INFINITY ? 0.0f : ldexpf(1.0f, -(int)k)) : 1.0f;
+              if (c > 0) {
+                if (!warp_wait(smem_addr(&o_done[tile]), (c - 1) & 1)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                  uint32_t ov[16];
+                  tmem_ld16(o_tmem + c0, ov);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+                  tmem_st16(o_tmem + c0, ov);
+                }
+              }
+              if (ps > 0) {
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c0 = 0; c0 < 32; c0 += 16) {
+                  uint32_t pv[16];
+                  tmem_ld16(s_tmem + c0, pv);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&pv[j]));
+                    pv[j] = pack2<true>(y.x * alpha, y.y * alpha);
+                  }
+                  tmem_st16(s_tmem + c0, pv);
+                }
+                lsum *= alpha;
+              }
+              tmem_wait_st();
+              l *= alpha;
+              m_ref = m_new;
+            }
+            const float add = m_ref == -INFINITY ? 0.0f : ev - m_ref;
+            uint32_t pw[32];
+            lsum += masked ? half_exp<true>(raw, pw, first, lim, kf, add) : half_exp<false>(raw, pw, first, lim, kf, add);
+            tmem_st32(s_tmem + 32 * ps, pw);
+          }
+          if (!ok) break;
+          tmem_wait_st();
+          l = fmaf(lsum, __uint_as_float((uint32_t)(127 - now.y) << 23), l);
+          tc_fence_before();
+          mbar_arrive(smem_addr(&p_full[tile]));
+        }
+        if (ok && !warp_wait(smem_addr(&o_done[tile]), (nch - 1) & 1)) ok = false;
+        if (!ok) sh_fail = 1;
+        tc_fence_after();
+      }
+    }
+    __syncthreads();
+    if (nch > 0 && warp == kMmaWarp && lane == 0) {
+      // all tensor-core work of this CTA completes before TMEM is read or freed
+      tc_fence_after();
+      mma_commit(smem_addr(&drain_bar));
+      if (!mbar_wait(smem_addr(&drain_bar), 0)) sh_fail = 1;
+    }
+    __syncthreads();
+    const bool have = nch > 0 && sh_fail == 0;
+    if (sh_fail && tid == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
+    if (warp < kSoftmaxWarps && (tile == 0 || live1)) {
+      tc_fence_after();
+      const uint32_t o_tmem = tm + ((uint32_t)(32 * (warp & 3)) << 16) + I::ocol(tile);
+      const float inv = have && row_valid ? 1.0f / l : 0.0f;
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t ov[32];
+        if (have) {
+          tmem_read32(o_tmem + c0, ov);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) ov[j] = 0u;
+        }
+        if (!row_valid) continue;
+        __nv_bfloat16* out = a.out + qrow * D + c0;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack2<false>(__uint_as_float(ov[j + 2 * i]) * inv, __uint_as_float(ov[j + 2 * i + 1]) * inv);
+          *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // every copy, MMA and arrival of this unit is done: the barriers start over
+    if (tid == 0) {
+      for (int s = 0; s < kKStages; ++s) {
+        mbar_inval(smem_addr(&k_full[s]));
+        mbar_inval(smem_addr(&k_empty[s]));
+      }
+      for (int s = 0; s < kVStages; ++s) {
+        mbar_inval(smem_addr(&v_full[s]));
+        mbar_inval(smem_addr(&v_empty[s]));
+      }
+      for (int g = 0; g < kTiles; ++g) {
+        mbar_inval(smem_addr(&s_full[g]));
+        mbar_inval(smem_addr(&p_full[g]));
+        mbar_inval(smem_addr(&o_done[g]));
+      }
+      mbar_inval(smem_addr(&drain_bar));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tm_held && warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmemCols) : "memory");
+}
+
+template <int D>
+kv_status launch_tc(const Q4LongArgs& a, int ctas, cudaStream_t s) {
+  static std::mutex mu;
+  static bool set[64] = {};
+  int dev = 0;
+  kv_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != KV_OK) return st;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && !set[dev]) {
+      st = cuda_check(cudaFuncSetAttribute(q4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Img<D>::kSmem),
+                      "cudaFuncSetAttribute(q4_tc_kernel)");
+      if (st != KV_OK) return st;
+      set[dev] = true;
+    }
+  }
+  q4_tc_kernel<D><<<(unsigned)ctas, kThreadsTc, Img<D>::kSmem, s>>>(a);
+  return cuda_check(cudaGetLastError(), "q4_tc_kernel launch");
+}
+
+}  // namespace
+
+size_t q4_slot_bytes(int num_kv_heads, int head_dim, int max_seq_len) {
+  const size_t chunks = ((size_t)max_seq_len + kChunk - 1) / kChunk;
+  return (size_t)num_kv_heads * chunks * (2 * kChunk * (size_t)head_dim * 2 + sizeof(int2));
+}
+
+size_t q4_plan_bytes(int batch, int slots) {
+  return (((size_t)batch + 2 * (size_t)slots + 2) * 4 + 127) & ~(size_t)127;
+}
+
+kv_status launch_q4_long(Q4LongArgs a, void* memory, int sms, cudaStream_t s) {
+  // [images][exponents][slot of each sequence][list][bad][counters]; images 128-byte aligned
+  a.chunks = (a.max_seq_len + kChunk - 1) / kChunk;
+  const size_t cells = (size_t)a.slots * a.num_kv_heads * a.chunks;
+  a.images = static_cast<unsigned char*>(memory);
+  a.exps = reinterpret_cast<int2*>(a.images + cells * 2 * kChunk * a.head_dim * 2);
+  a.list = reinterpret_cast<int*>(a.exps + cells);
+  a.bad = a.list + a.slots;
+  a.counters = a.bad + a.slots;
+  q4_plan_kernel<<<1, 256, 0, s>>>(a);
+  kv_status st = cuda_check(cudaGetLastError(), "q4_plan_kernel launch");
+  if (st != KV_OK) return st;
+  const dim3 grid((unsigned)a.chunks, (unsigned)a.num_kv_heads, (unsigned)a.slots);
+  if (a.head_dim == 128) {
+    if (a.block_size == 32) q4_widen_kernel<128, 32><<<grid, 256, 0, s>>>(a);
+    else q4_widen_kernel<128, 16><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (a.block_size == 32) q4_widen_kernel<64, 32><<<grid, 256, 0, s>>>(a);
+    else q4_widen_kernel<64, 16><<<grid, 256, 0, s>>>(a);
+  }
+  if ((st = cuda_check(cudaGetLastError(), "q4_widen_kernel launch")) != KV_OK) return st;
+  const long long units = ((long long)a.num_tokens * a.group / (kTiles * kRows) + a.slots) * a.num_kv_heads;
+  const int ctas = (int)(units < sms ? units : sms);
+  return a.head_dim == 128 ? launch_tc<128>(a, ctas, s) : launch_tc<64>(a, ctas, s);
+}
+
+}  // namespace pagedkv

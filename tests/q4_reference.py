@@ -157,7 +157,7 @@ def rows_of(rec, block, d, L):
     return out
 
 
-def attention(rows, q, scale, positions):
+def attention(rows, q, scale, positions, wide=False):
     """Attention of query rows q [n, Hq, d] (bf16) at `positions` [n] over one
     sequence's rows, and how far a kernel may be off.
 
@@ -170,7 +170,12 @@ def attention(rows, q, scale, positions):
     exponential, 2^-22, likewise; the fp32 sums over tokens, 2^-14 of
     sum w (scale code + |min|) for up to 2^14 steps of 2^-24 each and their ten
     joins; half a step of the smallest fp16 (2^-30 of the largest product, times
-    15 for its code) per token."""
+    15 for its code) per token.
+
+    ``wide``: keys and values enter the products as fp16 numbers (2^-11 of their
+    value, at best 2^-37 of the largest of their 128 rows, which the other terms
+    cover), the weight alone as one: 2^-11 of S_abs in the scores, of sum w |V|
+    twice in the sum, and the floor counts the weight times the largest |V|."""
     (kc, ks, km), (vc, vs, vm) = rows
     H, L, d = kc.shape
     n, hq, _ = q.shape
@@ -186,10 +191,13 @@ def attention(rows, q, scale, positions):
     mag = torch.einsum("nhgt,htd->nhgd", w, vs * vc + vm.abs())
     part = torch.einsum("nhgt,htd->nhgd", w, vs * vc)
     # a weight's relative error times what it carries, and the sum's own
-    shift = 2.0 ** -17 * Sabs + 2.0 ** -21
+    shift = (2.0 ** -17 + (2.0 ** -11 if wide else 0)) * Sabs + 2.0 ** -21
     moved = torch.einsum("nhgt,htd->nhgd", w * shift, vs * vc + vm.abs()) + mag * (w * shift).sum(-1, keepdim=True)
     floor = 2.0 ** -30 * 15 * L * (w[..., None] * vs.amax(-1)[None, :, None, :, None]).amax(dim=3)
     tol = 2.0 ** -8 * out.abs() + 2.0 ** -11 * part + moved + 2.0 ** -14 * mag + floor
+    if wide:
+        largest = (vm.abs() + 15 * vs).amax(-1)
+        tol = tol + 2.0 ** -10 * mag + 2.0 ** -30 * L * (w * largest[None, :, None]).amax(-1)[..., None]
     return out.reshape(n, hq, d), tol.reshape(n, hq, d)
 
 

@@ -281,22 +281,31 @@ def decode(pkv, pool, q, scale, max_len=None, dev=None):
     return pkv.paged_attention_decode_q4(out, q.cuda(), kv, bt, sl, pool.block, max_len or max(max(pool.L), 1), scale, ws)
 
 
-def multi(pkv, pool, q, n, scale, max_len=None, max_n=None, dev=None):
+def multi(pkv, pool, q, n, scale, max_len=None, max_n=None, dev=None, room=None):
+    """room: sequences whose long queries find room in the workspace (None: none, -1: all)."""
     kv, bt, sl = dev or pool.on()
     hq, most = q.shape[1], max_n or max(max(n), 1)
     out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
-    ws = poison(pkv.q4_workspace_bytes(hq, pool.heads, pool.dim, most))
+    size = pkv.q4_workspace_bytes(hq, pool.heads, pool.dim, most)
+    if room is not None:
+        longest = max_len or max(max(pool.L), 1)
+        size = pkv.q4_long_workspace_bytes(len(n), q.shape[0], most, longest, hq, pool.heads, pool.dim)
+        if room > 0:
+            slot = (longest + 127) // 128 * pool.heads * (512 * pool.dim + 8)
+            size = pkv.q4_workspace_bytes(hq, pool.heads, pool.dim, most) + room * slot + 4 * (3 * len(n) + 2) + 1024
+    ws = poison(size)
     return pkv.paged_attention_multi_q4(out, q.cuda(), kv, bt, sl, starts(n).cuda(), pool.block,
                                         max_len or max(max(pool.L), 1), most, scale, ws)
 
 
-def check(out, pool, q, n, scale):
+def check(out, pool, q, n, scale, wide=False):
     at = 0
     for b, m in enumerate(n):
         if m == 0:
             continue
         L = pool.L[b]
-        want, tol = ref.attention(pool.rows(b, L), q[at:at + m], scale, torch.arange(L - m, L))
+        want, tol = ref.attention(pool.rows(b, L), q[at:at + m], scale, torch.arange(L - m, L),
+                                  wide and m * q.shape[1] // pool.heads >= 128)
         within(out[at:at + m], want, tol)
         at += m
 
@@ -353,6 +362,54 @@ def test_multi_long(pkv, dim, heads, group, L, n):
     pool = ref.Pool4(L, heads, dim, 16, seed=8)
     q = pool.randn(sum(n), heads * group, dim, scale=2.0)
     check(multi(pkv, pool, q, n, dim ** -0.5), pool, q, n, dim ** -0.5)
+
+
+@pytest.mark.parametrize("block,dim", SHAPES)
+@pytest.mark.parametrize("heads,group,L,n", [
+    (1, 1, [128], [128]), (2, 4, [300, 40, 257, 33, 128], [40, 1, 0, 33, 32]), (1, 8, [500, 16], [33, 16]),
+    (2, 3, [600, 90, 700, 45], [600, 3, 50, 44]), (3, 5, [1200], [1200]), (1, 2, [70, 64, 1000], [63, 64, 129]),
+    (8, 4, [900, 700], [900, 5])])
+@pytest.mark.parametrize("room", [-1, 1])
+def test_multi_tensor_cores(pkv, block, dim, heads, group, L, n, room):
+    """Long queries through widened operands, beside short ones, at the border of
+    128 rows, with chunks, tiles and pairs of tiles that end anywhere, and with room
+    for one sequence only."""
+    pool = ref.Pool4(L, heads, dim, block, seed=len(L) + group)
+    q = pool.randn(sum(n), heads * group, dim, scale=2.0)
+    check(multi(pkv, pool, q, n, dim ** -0.5, room=room), pool, q, n, dim ** -0.5, wide=True)
+
+
+@pytest.mark.parametrize("scale,vspread,kspread", [(-0.2, 1.0, 1.0), (0.0, 1.0, 1.0), (3.0, 1.0, 1.0),
+                                                   (0.1, 1e-20, 1e10), (0.1, 1e20, 1e-10)])
+def test_multi_tensor_cores_scales(pkv, scale, vspread, kspread):
+    pool = ref.Pool4([700, 300], 2, 128, 16, seed=19, vscale=lambda s, g: vspread, kscale=lambda s, g: kspread)
+    q = (pool.randn(350, 8, 128).float() / kspread).to(torch.bfloat16)
+    check(multi(pkv, pool, q, [150, 200], scale, room=-1), pool, q, [150, 200], scale, wide=True)
+
+
+def test_multi_tensor_cores_rising_scores(pkv):
+    """Scores and V's magnitudes that rise along the sequence move the references
+    in every chunk."""
+    def rising(shape, g):
+        return torch.exp2(torch.arange(shape[0]).view(-1, 1, 1, 1) / 4.0).expand(shape)
+    pool = ref.Pool4([1000], 1, 64, 16, seed=20, vscale=rising, kscale=lambda s, g: rising(s, g) ** 0.25)
+    q = pool.randn(200, 4, 64)
+    check(multi(pkv, pool, q, [200], 1.0, room=-1), pool, q, [200], 1.0, wide=True)
+
+
+def test_multi_tensor_cores_faults(pkv):
+    """Bad blocks, lengths and offsets among long queries; repeats give the same bits."""
+    L, n = [400, 300, 500, 260], [100, 150, 200, 64]
+    pool = ref.Pool4(L, 2, 64, 16, seed=21)
+    q = pool.randn(sum(n), 8, 64)
+    kv, bt, sl = pool.on()
+    first = multi(pkv, pool, q, n, 0.125, dev=(kv, bt, sl), room=-1)
+    assert same_bits(first, multi(pkv, pool, q, n, 0.125, dev=(kv, bt, sl), room=-1).cpu())
+    bt[0, 3], sl[2] = pool.num_blocks, 501
+    out = multi(pkv, pool, q, n, 0.125, dev=(kv, bt, sl), room=-1)
+    assert flags_of(pkv) == pkv.FLAG_BAD_BLOCK | pkv.FLAG_BAD_SEQ_LEN
+    assert (out[:100] == 0).all() and (out[250:450] == 0).all()
+    assert same_bits(out[100:250], first[100:250].cpu()) and same_bits(out[450:], first[450:].cpu())
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
