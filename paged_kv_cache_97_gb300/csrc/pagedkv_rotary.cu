@@ -9,12 +9,11 @@
 // stored from that bf16 row by the pool's own rule, so the codes are those that
 // a rotation followed by an append would give.
 //
-// A warp works on one token: its position, its slot and (R <= D) its part of the
-// table's row are found once and serve all the rows (heads of q, k and v) it
-// takes.  D / 16 lanes hold a row, each two runs of 8 elements that are each
-// other's pairs, 16 bytes a load; a lane loads kRows rows before it works on
-// the first.  Few tokens take one row per lane group (more warps, shorter
-// chains), many take four.
+// A CTA works on one token (or a slice of its rows): its sequence, position, block
+// and table row are found once and serve all rows (heads of q, k and v).  D / 16
+// lanes hold a row, each two runs of 8 elements that are each other's pairs, 16
+// bytes a load; a lane loads its up to four rows before it works on the first.
+// Few tokens take one row per lane group (more CTAs, shorter chains).
 //
 // HBM bound: a prompt token of 32 + 8 + 8 heads of 128 moves 24 KB, against the
 // 512 bytes of its table row, which L2 holds.
@@ -24,13 +23,15 @@
 #include "pagedkv_common.cuh"
 #include "pagedkv_device.cuh"
 #include "pagedkv_q4.cuh"
+#include "pagedkv_requant.cuh"
 
 namespace pagedkv {
 namespace {
 
 using namespace dev;
 
-constexpr int kRotaryWarps = 4;
+constexpr int kRotaryThreads = 128;
+constexpr int kRotaryWarps = kRotaryThreads / 32;
 constexpr int kMaxAxes = 4;
 constexpr int kKindQ4 = 3;                          // beside the kv_dtype values
 
@@ -49,7 +50,7 @@ struct RotaryArgs {
   int max_position, rotary_dim, interleaved, axes;
   int section_end[kMaxAxes];   // frequencies below it belong to this axis or an earlier one
   int max_blocks, batch, num_tokens, max_query_len, num_q_heads, num_kv_heads, num_blocks;
-  int slices;                  // warps per token
+  int slices;                  // CTAs per token
 };
 
 // The sequence of token t: the last b with query_start[b] <= t (32 samples a
@@ -68,28 +69,94 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ query_sta
   return lo;
 }
 
-// Eight bf16 of a row as fp32, and back (rounded to nearest).
-__device__ __forceinline__ void widen8(const uint4& x, float (&v)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
+// Eight fp32 as bf16 (rounded to nearest).
 __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
   return make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
                     pack2<false>(v[6], v[7]));
 }
 
+// Largest magnitude of 16 bf16 values, as bits (NaN above infinity above the finite).
+__device__ __forceinline__ uint32_t magnitude_bits(const uint4& a, const uint4& b) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t m = max_u16x2(max_u16x2(a.x & kAbs, a.y & kAbs), max_u16x2(a.z & kAbs, a.w & kAbs));
+  m = max_u16x2(m, max_u16x2(max_u16x2(b.x & kAbs, b.y & kAbs), max_u16x2(b.z & kAbs, b.w & kAbs)));
+  return max(m & 0xffffu, m >> 16);
+}
+
+// The codes of 16 bf16 values under scale s, which the data did not set: the
+// quotients may pass the largest code.  As code16 for values up to 2^40 (E4M3:
+// the two corrections and a saturating conversion; int8: both ends of the
+// interval held in -127 .. 127), by division above.
 template <bool kFp8>
-__device__ __forceinline__ uint2 codes8(const uint4& x, float s) {
-  float v[8];
-  widen8(x, v);
-  uint32_t o[2] = {0u, 0u};
+__device__ __forceinline__ uint4 codes16(const uint4& a, const uint4& b, const Interval& q, float s) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t o[4], off = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i / 4] |= (uint32_t)code8<kFp8>(v[i], s) << (8 * (i % 4));
-  return make_uint2(o[0], o[1]);
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    bf16_values(w[2 * i], w[2 * i + 1], v);
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float y = v[k] * q.r;
+        y = fmaf(fmaf(y, q.s, -v[k]), -q.r, y);
+        v[k] = fmaf(fmaf(y, q.s, -v[k]), -q.r, y);
+      }
+      o[i] = code4_times<true>(v, 1.0f);
+    } else {
+      float u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        u[k] = fminf(fmaxf(v[k] * q.lo, -127.0f), 127.0f);
+        v[k] = fminf(fmaxf(v[k] * q.hi, -127.0f), 127.0f);
+      }
+      o[i] = code4_times<false>(u, 1.0f);
+      off |= o[i] ^ code4_times<false>(v, 1.0f);
+    }
+  }
+  if (q.on && off == 0u && magnitude_bits(a, b) <= 0x5380u) return make_uint4(o[0], o[1], o[2], o[3]);   // 2^40
+  return code16_divided<kFp8>(a, b, s);
+}
+
+// Two fp32 numbers in one register pair.  A packed sum of packed products becomes
+// a multiply-add in spite of its .rn, so what has to be rounded twice takes its
+// products packed and its sums one by one.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// The bf16 pair of a word as fp32.
+__device__ __forceinline__ F2 widen2(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+// The pairs (p, q) turned: p c - q s and q c + p s, as words of bf16.
+__device__ __forceinline__ void turn2(F2 p, F2 q, F2 c, F2 s, uint32_t& pw, uint32_t& qw) {
+  float a0, a1, b0, b1;
+  split(mul2(p, c), a0, a1);
+  split(mul2(q, s), b0, b1);
+  pw = pack2<false>(__fsub_rn(a0, b0), __fsub_rn(a1, b1));
+  split(mul2(q, c), a0, a1);
+  split(mul2(p, s), b0, b1);
+  qw = pack2<false>(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // A row's two runs of 8 (elements 8 ca .. and 8 cb ..) as 4-bit codes under one
@@ -99,79 +166,90 @@ __device__ __forceinline__ uint2 codes8(const uint4& x, float s) {
 // NaN counts as 0, magnitudes above 2^126 as 2^126.  Every lane of the warp
 // calls; lanes without `store` write nothing.
 template <int D>
-__device__ __forceinline__ void store_q4(bool store, unsigned char* rec, int x, int row, int bs, const uint4& ra,
-                                         const uint4& rb, int ca, int cb, int sub) {
+__device__ __forceinline__ void store_q4(bool store, unsigned char* rec, int x, int row, int bs, uint4 ra, uint4 rb,
+                                         int ca, int cb, int sub) {
   constexpr int kGroups = D / 64, kLanes = D / 16;
-  constexpr float kMost = 8.507059173023462e37f;   // 2^126
-  float v[2][8];
-  widen8(ra, v[0]);
-  widen8(rb, v[1]);
-  const int at[2] = {ca, cb};
-  float lo[kGroups], hi[kGroups];
+  if (__any_sync(0xffffffffu, magnitude_bits(ra, rb) > 0x7e80u)) {       // NaN or above 2^126 (rare)
+    uint32_t* w[2] = {&ra.x, &rb.x};
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    lo[g] = INFINITY;
-    hi[g] = -INFINITY;
-  }
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    float l = INFINITY, h = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y = v[p][i];
-      y = y != y ? 0.0f : fminf(fmaxf(y, -kMost), kMost);
-      y = __fadd_rn(y, 0.0f);                       // -0 is 0
-      v[p][i] = y;
-      l = fminf(l, y);
-      h = fmaxf(h, y);
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-      if (at[p] / 8 == g) {
-        lo[g] = fminf(lo[g], l);
-        hi[g] = fmaxf(hi[g], h);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t lo = w[p][i] & 0xffffu, hi = w[p][i] >> 16;
+        lo = (lo & 0x7fffu) > 0x7f80u ? 0u : (lo & 0x7fffu) > 0x7e80u ? (lo & 0x8000u) | 0x7e80u : lo;
+        hi = (hi & 0x7fffu) > 0x7f80u ? 0u : (hi & 0x7fffu) > 0x7e80u ? (hi & 0x8000u) | 0x7e80u : hi;
+        w[p][i] = lo | hi << 16;
       }
   }
-  float inv[kGroups];
+  // (min, min of the negated) of a run as a bf16 pair: one instruction and one
+  // shuffle take both ends of two values
+  auto ends = [](const uint4& r) {
+    constexpr uint32_t kSign = 0x80008000u;
+    const uint32_t lo = min_bf16x2(min_bf16x2(r.x, r.y), min_bf16x2(r.z, r.w));
+    const uint32_t hi = min_bf16x2(min_bf16x2(r.x ^ kSign, r.y ^ kSign), min_bf16x2(r.z ^ kSign, r.w ^ kSign));
+    return min_bf16x2(prmt(lo, hi, 0x5410u), prmt(lo, hi, 0x7632u));
+  };
+  const uint32_t ea = ends(ra), eb = ends(rb);
+  float low[kGroups], inv[kGroups];
   uint32_t pair[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
+    constexpr uint32_t kNone = 0x7f807f80u;         // infinities
+    uint32_t e = min_bf16x2(ca / 8 == g ? ea : kNone, cb / 8 == g ? eb : kNone);
 #pragma unroll
-    for (int off = 1; off < kLanes; off <<= 1) {
-      lo[g] = fminf(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], off));
-      hi[g] = fmaxf(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], off));
-    }
-    const float step = __fmul_rn(__fsub_rn(hi[g], lo[g]), 0.06666667014360428f);   // fp32 1 / 15
+    for (int off = 1; off < kLanes; off <<= 1) e = min_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, off));
+    low[g] = __fadd_rn(__uint_as_float(e << 16), 0.0f);                  // -0 is 0
+    const float high = -__uint_as_float(e & 0xffff0000u);
+    const float step = __fmul_rn(__fsub_rn(high, low[g]), 0.06666667014360428f);   // fp32 1 / 15
     const uint32_t up = (__float_as_uint(step) + 0xffffu) & 0xffff0000u;
     const float s = fmaxf(__uint_as_float(up), 1.1754943508222875e-38f);
-    inv[g] = __fdiv_rn(1.0f, s);
-    pair[g] = (__float_as_uint(s) >> 16) | (__float_as_uint(lo[g]) & 0xffff0000u);   // both bf16 already
+    inv[g] = __frcp_rn(s);
+    pair[g] = (__float_as_uint(s) >> 16) | (__float_as_uint(low[g]) & 0xffff0000u);   // both bf16 already
   }
+  const uint4 r[2] = {ra, rb};
+  const int at[2] = {ca, cb};
+  uint32_t word[2] = {0u, 0u};
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     const int g = at[p] / 8;
-    const float low = kGroups > 1 && g ? lo[kGroups - 1] : lo[0], f = kGroups > 1 && g ? inv[kGroups - 1] : inv[0];
-    uint32_t word = 0;
+    const float lo = kGroups > 1 && g ? low[kGroups - 1] : low[0], f = kGroups > 1 && g ? inv[kGroups - 1] : inv[0];
+    const uint32_t w[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
+    // y = (x - min) / scale is in [0, 15] but for a last place: added to 2^23 its
+    // nearest integer (ties to even) stands in the low bits, and the words of eight,
+    // times 16^i, add up to the codes and a constant
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = __float2int_rn(__fmul_rn(__fsub_rn(v[p][i], low), f));
-      word |= (uint32_t)min(max(c, 0), 15) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+      const F2 y = mul2(add2(widen2(w[i]), f2(-lo, -lo)), f2(f, f));
+      float c0, c1;
+      split(y, c0, c1);
+      word[p] += (__float_as_uint(__fadd_rn(c0, 8388608.0f)) << (8 * i)) +
+                 (__float_as_uint(__fadd_rn(c1, 8388608.0f)) << (8 * i + 4));
     }
-    if (store) *reinterpret_cast<uint32_t*>(rec + q4_codes_at(x, row, bs, D) + ((at[p] & 7) * kGroups + g) * 4) = word;
+    // 0x4B000000 * (1 + 16 + .. + 16^7) mod 2^32
+    word[p] -= 0x4B000000u * 0x11111111u;
+  }
+  if (store) {
+    unsigned char* to = rec + q4_codes_at(x, row, bs, D);
+    if (kGroups == 2 && ca + 8 == cb) {             // the same word of both groups: neighbours
+      *reinterpret_cast<uint2*>(to + ca * 8) = make_uint2(word[0], word[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(to + ((ca & 7) * kGroups + ca / 8) * 4) = word[0];
+      *reinterpret_cast<uint32_t*>(to + ((cb & 7) * kGroups + cb / 8) * 4) = word[1];
+    }
   }
   if (store && sub < kGroups)
-    *reinterpret_cast<uint32_t*>(rec + q4_pairs_at(x, row, bs, D) + sub * 4) = sub ? pair[kGroups - 1] : pair[0];
+    *reinterpret_cast<uint32_t*>(rec + q4_pairs_at(x, row, bs, D) + sub * 4) =
+        kGroups > 1 && sub ? pair[kGroups - 1] : pair[0];
 }
 
 template <int D, int kKind, int kRows>
-__global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const RotaryArgs a, int bs) {
-  constexpr int kLanes = D / 16, kPerWarp = 32 / kLanes;
+__global__ void __launch_bounds__(kRotaryThreads, 6) append_rotary_kernel(const RotaryArgs a, int bs) {
+  constexpr int kLanes = D / 16, kStep = kRotaryThreads / kLanes;        // rows taken side by side
+  __shared__ __align__(16) float table[128];        // the token's cosines, then its sines
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kRotaryWarps + (threadIdx.x >> 5);
-  const int64_t tok = unit / a.slices;
-  if (tok >= a.num_tokens) return;                  // (warp-uniform, as all below)
-  const int t = (int)tok, slice = (int)(unit % a.slices);
-  const int sub = lane % kLanes, row0 = (slice * kPerWarp + lane / kLanes) * kRows;
+  const int64_t tok = blockIdx.x / a.slices;
+  const int t = (int)tok, slice = blockIdx.x % a.slices;
+  const int sub = lane % kLanes, row0 = slice * kStep * kRows + threadIdx.x / kLanes;
   const int Hq = a.q_out ? a.num_q_heads : 0, Hkv = a.num_kv_heads;
   const int rows = Hq + 2 * Hkv;
   const int R = a.cos_sin ? a.rotary_dim : 0, half = R / 2;
@@ -194,7 +272,7 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const 
   uint4 xa[kRows], xb[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i;
+    const int r = row0 + i * kStep;
     xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
     if (r >= rows) continue;
     const __nv_bfloat16* p = r < Hq          ? a.q + tok * a.q_stride + (int64_t)r * D
@@ -204,7 +282,7 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const 
     xb[i] = reinterpret_cast<const uint4*>(p)[cb];
   }
 
-  // ---- the token's sequence, position and block --------------------------------
+  // ---- the token's sequence, position and block (uniform over the CTA) -----------
   int b = t, n = 1, q0 = t;
   if (a.query_start) {
     b = sequence_of(a.query_start, a.batch, t, lane);
@@ -215,7 +293,7 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const 
   }
   const int L = __ldg(a.seq_lens + b);
   bool use = true, kv_ok = true;
-  const bool teller = slice == 0 && lane == 0;
+  const bool teller = slice == 0 && threadIdx.x == 0;
   if (L <= 0 || q0 < 0 || q0 > a.num_tokens - n || n > L || n > a.max_query_len || (L - 1) / bs >= a.max_blocks) {
     if (teller) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
     use = false;
@@ -231,86 +309,62 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const 
   }
   const int in = pos % bs;
 
-  // ---- this lane's eight frequencies ----------------------------------------
-  float co[8], si[8];
-  if (R > 0 && use) {
-    int where[kMaxAxes];
+  // ---- the token's table row, each frequency from its own axis's position ---------
+  if (R > 0) {
+    bool lost = false;
+    if (use && (int)threadIdx.x < R) {
+      const int j = threadIdx.x < half ? threadIdx.x : threadIdx.x - half;
+      int x = 0;                                    // the first axis whose section ends behind j
 #pragma unroll
-    for (int x = 0; x < kMaxAxes; ++x) {
-      where[x] = 0;
-      if (x < a.axes) {
-        where[x] = a.positions ? __ldg(a.positions + (int64_t)x * a.num_tokens + t) : pos;
-        if (where[x] < 0 || where[x] >= a.max_position) {
-          if (teller) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
-          use = false;
-        }
-      }
+      for (int k = 0; k < kMaxAxes - 1; ++k) x += k < a.axes - 1 && j >= a.section_end[k];
+      const int at = a.positions ? __ldg(a.positions + (int64_t)x * a.num_tokens + t) : pos;
+      lost = at < 0 || at >= a.max_position;
+      if (!lost) table[threadIdx.x] = __ldg(a.cos_sin + (int64_t)at * R + threadIdx.x);
     }
-    if (use && turn) {
-      const int j0 = 8 * sub;
-      // the axis of frequency j: the first whose section ends behind it
-      auto axis_of = [&](int j) {
-        int x = 0;
+    if (__syncthreads_or(lost)) {
+      if (teller) atomicOr(a.flags, PAGEDKV_FLAG_BAD_INDEX);
+      use = false;
+    }
+  }
+  float co[8], si[8];
+  if (turn) {
 #pragma unroll
-        for (int k = 0; k < kMaxAxes - 1; ++k) x += k < a.axes - 1 && j >= a.section_end[k];
-        return x;
-      };
-      auto at = [&](int x) {
-        int w = where[0];
-#pragma unroll
-        for (int k = 1; k < kMaxAxes; ++k) w = x == k ? where[k] : w;
-        return a.cos_sin + (int64_t)w * R;
-      };
-      const int xf = axis_of(j0), xl = axis_of(j0 + 7);
-      if (xf == xl) {
-        const float* p = at(xf) + j0;
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(p)), c1 = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(p + half));
-        const float4 s1 = __ldg(reinterpret_cast<const float4*>(p + half) + 1);
-        co[0] = c0.x, co[1] = c0.y, co[2] = c0.z, co[3] = c0.w, co[4] = c1.x, co[5] = c1.y, co[6] = c1.z, co[7] = c1.w;
-        si[0] = s0.x, si[1] = s0.y, si[2] = s0.z, si[3] = s0.w, si[4] = s1.x, si[5] = s1.y, si[6] = s1.z, si[7] = s1.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float* p = at(axis_of(j0 + i)) + j0 + i;
-          co[i] = __ldg(p);
-          si[i] = __ldg(p + half);
-        }
-      }
+    for (int k = 0; k < 8; k += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(table + 8 * sub + k);
+      const float4 z = *reinterpret_cast<const float4*>(table + half + 8 * sub + k);
+      co[k] = y.x, co[k + 1] = y.y, co[k + 2] = y.z, co[k + 3] = y.w;
+      si[k] = z.x, si[k + 1] = z.y, si[k + 2] = z.z, si[k + 3] = z.w;
     }
   }
 
   // ---- rows ---------------------------------------------------------------------
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i;
+    const int r = row0 + i * kStep;
     const bool real = r < rows;
     const bool is_q = r < Hq, is_v = r >= Hq + Hkv;
     if (real && !is_v && use && turn) {
-      float u[8], w[8];
-      widen8(xa[i], u);
-      widen8(xb[i], w);
+      uint32_t u[4] = {xa[i].x, xa[i].y, xa[i].z, xa[i].w}, w[4] = {xb[i].x, xb[i].y, xb[i].z, xb[i].w};
       if (a.interleaved) {
         // pairs are neighbours: frequency k < 4 in the first run, the others in the second
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float p = u[2 * k], q = u[2 * k + 1];
-          u[2 * k] = __fsub_rn(__fmul_rn(p, co[k]), __fmul_rn(q, si[k]));
-          u[2 * k + 1] = __fadd_rn(__fmul_rn(q, co[k]), __fmul_rn(p, si[k]));
-          const float y = w[2 * k], z = w[2 * k + 1];
-          w[2 * k] = __fsub_rn(__fmul_rn(y, co[k + 4]), __fmul_rn(z, si[k + 4]));
-          w[2 * k + 1] = __fadd_rn(__fmul_rn(z, co[k + 4]), __fmul_rn(y, si[k + 4]));
+          const F2 c = f2(co[k], co[k + 4]), s = f2(si[k], si[k + 4]);
+          const F2 p = f2(__uint_as_float(u[k] << 16), __uint_as_float(w[k] << 16));
+          const F2 q = f2(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(w[k] & 0xffff0000u));
+          uint32_t pw, qw;                          // (first run's, second run's)
+          turn2(p, q, c, s, pw, qw);
+          u[k] = prmt(pw, qw, 0x5410u);
+          w[k] = prmt(pw, qw, 0x7632u);
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float p = u[k], q = w[k];
-          u[k] = __fsub_rn(__fmul_rn(p, co[k]), __fmul_rn(q, si[k]));
-          w[k] = __fadd_rn(__fmul_rn(q, co[k]), __fmul_rn(p, si[k]));
-        }
+        for (int k = 0; k < 4; ++k)
+          turn2(widen2(u[k]), widen2(w[k]), f2(co[2 * k], co[2 * k + 1]), f2(si[2 * k], si[2 * k + 1]),
+                u[k], w[k]);
       }
-      xa[i] = narrow8(u);
-      xb[i] = narrow8(w);
+      xa[i] = make_uint4(u[0], u[1], u[2], u[3]);
+      xb[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (real && is_q) {
       uint4* o = reinterpret_cast<uint4*>(a.q_out + tok * a.q_out_stride + (int64_t)r * D);
@@ -337,8 +391,9 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) append_rotary_kernel(const 
         constexpr bool kFp8 = kKind == KV_DTYPE_FP8_E4M3;
         const float s = __ldg((is_v ? a.v_scale : a.k_scale) + (int64_t)blk * Hkv + h);
         uint2* o = reinterpret_cast<uint2*>(static_cast<unsigned char*>(cache) + dst);
-        o[ca] = codes8<kFp8>(xa[i], s);
-        o[cb] = codes8<kFp8>(xb[i], s);
+        const uint4 y = codes16<kFp8>(xa[i], xb[i], quotients(s), s);
+        o[ca] = make_uint2(y.x, y.y);
+        o[cb] = make_uint2(y.z, y.w);
       }
     }
   }
@@ -402,7 +457,8 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) read_q4_kernel(const ReadAr
       const float s = __uint_as_float(p << 16), m = __uint_as_float(p & 0xffff0000u);
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = fmaf(s, (float)((w >> (4 * k)) & 15u), m);   // s * c is exact
+      for (int k = 0; k < 8; ++k)                   // c: the low bits of 2^23 + c; s * c is exact
+        v[k] = fmaf(s, __uint_as_float(0x4B000000u | (w >> (4 * k) & 15u)) - 8388608.0f, m);
       o = narrow8(v);
     }
     (x ? a.v_out : a.k_out)[tok * H * kWords + hw] = o;
@@ -416,20 +472,25 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) read_q4_kernel(const ReadAr
 template <int D, int kKind, int kRows>
 kv_status launch_rotary(RotaryArgs& a, int bs, cudaStream_t s) {
   const int rows = (a.q_out ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
-  constexpr int kStep = 32 / (D / 16) * kRows;
+  constexpr int kStep = kRotaryThreads / (D / 16) * kRows;
   a.slices = (rows + kStep - 1) / kStep;
-  const int64_t grid = ((int64_t)a.num_tokens * a.slices + kRotaryWarps - 1) / kRotaryWarps;
+  const int64_t grid = (int64_t)a.num_tokens * a.slices;
   if (grid > 0x7fffffffLL) return fail(KV_ERR_INVALID_ARG, "pagedkv_append_rotary: too many tokens");
-  append_rotary_kernel<D, kKind, kRows><<<(unsigned)grid, kRotaryWarps * 32, 0, s>>>(a, bs);
+  append_rotary_kernel<D, kKind, kRows><<<(unsigned)grid, kRotaryThreads, 0, s>>>(a, bs);
   return cuda_check(cudaGetLastError(), "append_rotary_kernel launch");
 }
 
 template <int D, int kKind>
 kv_status launch_rotary_rows(RotaryArgs& a, int bs, int sms, cudaStream_t s) {
-  // four rows a lane group once that leaves eight warps per SM
+  // up to four rows a lane group once that leaves two CTAs per SM
+  constexpr int kStep = kRotaryThreads / (D / 16);
   const int rows = (a.q_out ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
-  const int64_t warps = (int64_t)a.num_tokens * rows / (4 * 32 / (D / 16));
-  return warps >= 8LL * sms ? launch_rotary<D, kKind, 4>(a, bs, s) : launch_rotary<D, kKind, 1>(a, bs, s);
+  const int64_t most = (int64_t)a.num_tokens * ((rows + 4 * kStep - 1) / (4 * kStep));
+  if (most < 2LL * sms) return launch_rotary<D, kKind, 1>(a, bs, s);
+  // the fewest rows a group that take a token in as few CTAs
+  const int per = (rows + kStep - 1) / kStep;
+  if (per <= 2) return launch_rotary<D, kKind, 2>(a, bs, s);
+  return per == 3 ? launch_rotary<D, kKind, 3>(a, bs, s) : launch_rotary<D, kKind, 4>(a, bs, s);
 }
 
 template <int D>

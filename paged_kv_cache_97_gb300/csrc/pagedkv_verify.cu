@@ -13,7 +13,7 @@
 // A cluster of up to 8 CTAs takes a sequence: every CTA finds the row from the
 // drafts by itself, each sums its part of the row, the parts' sums go to all
 // CTAs through distributed shared memory, and the one warp whose part holds the
-// drawn place reads that part again (L2).  Bound by the one row (two with q) that
+// drawn place walks over it (a part longer than one round is read again, from L2).  Bound by the one row (two with q) that
 // has to be read per sequence, and in small batches by the chain of loads:
 // offsets, drafts, their probabilities, the row, the part again.
 #include <cuda_bf16.h>
@@ -28,7 +28,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
@@ -51,29 +51,29 @@ __device__ __forceinline__ float prob(const T* p) {
   else return static_cast<float>(*p);
 }
 
-// N consecutive probabilities (kVec: one aligned 16-byte load).
+// N consecutive probabilities (kVec: one aligned 16-byte load, all or none of
+// them there; else one).  `have` false: zeros.
 template <typename T, int N, bool kVec>
-__device__ __forceinline__ void probs(const T* p, int have, float (&v)[N]) {
+__device__ __forceinline__ void probs(const T* p, bool have, float (&v)[N]) {
   if constexpr (kVec) {
-    if (have >= N) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (have) x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          v[i] = __uint_as_float(w[i]);
-        } else {
-          const unsigned short h = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
-          T t;
-          memcpy(&t, &h, 2);
-          v[i] = static_cast<float>(t);
-        }
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        const unsigned short h = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
+        T t;
+        memcpy(&t, &h, 2);
+        v[i] = static_cast<float>(t);
       }
-      return;
     }
+  } else {
+    static_assert(N == 1, "one element a load");
+    v[0] = have ? prob(p) : 0.0f;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = i < have ? prob(p + i) : 0.0f;
 }
 
 // What the token is drawn by: p; max(p - q, 0); or p without the draft's own.
@@ -83,22 +83,39 @@ struct Row {
   int how, without;
 };
 
-// Weights of elements i .. i + N - 1 of a row (0 past `end`), in [0, 1]; NaN counts as 0.
-template <typename T, int N, bool kVec>
-__device__ __forceinline__ void weights_of(const T* p, const T* q, const Row& r, int i, int end, float (&w)[N]) {
-  probs<T, N, kVec>(p + i, end - i, w);
+// Weights of U runs of N elements, a run every `step`, from element i on (0 from
+// `end` on), in [0, 1]; NaN counts as 0.  All loads are issued before the first is
+// used.
+template <typename T, int N, int U, bool kVec>
+__device__ __forceinline__ void weights_of(const T* p, const T* q, const Row& r, int i, int step, int end,
+                                           float (&w)[U][N]) {
   if (r.how == kLess) {
-    float x[N];
-    probs<T, N, kVec>(q + i, end - i, x);
+    float x[U][N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) w[k] = __fsub_rn(w[k], x[k]);
-  } else if (r.how == kWithout) {
+    for (int u = 0; u < U; ++u) {
+      const bool have = i + u * step < end;
+      probs<T, N, kVec>(p + i + u * step, have, w[u]);
+      probs<T, N, kVec>(q + i + u * step, have, x[u]);
+    }
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (i + k == r.without) w[k] = 0.0f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[u][k] = __fsub_rn(w[u][k], x[u][k]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) probs<T, N, kVec>(p + i + u * step, i + u * step < end, w[u]);
+    if (r.how == kWithout) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (i + u * step + k == r.without) w[u][k] = 0.0f;
+    }
   }
 #pragma unroll
-  for (int k = 0; k < N; ++k) w[k] = fminf(fmaxf(w[k], 0.0f), 1.0f);
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[u][k] = fminf(fmaxf(w[u][k], 0.0f), 1.0f);
 }
 
 constexpr uint32_t kHiZero = 0x3f800000u;           // 1
@@ -122,9 +139,10 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyArgs a) {
-  constexpr int N = 16 / sizeof(T);
-  __shared__ int first_refused, drawn_bad;
+__global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_kernel(const VerifyArgs a) {
+  constexpr int N = kVec ? 16 / (int)sizeof(T) : 1;
+  constexpr int U = kVec ? 32 / N : 8;              // runs taken together
+  __shared__ int first_refused, refused_token;
   __shared__ long long warp_sum[kVerifyWarps], cta_sum[2][kMaxCluster];
   const int b = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -161,9 +179,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
   // ---- drafts kept -----------------------------------------------------------
   if (threadIdx.x == 0) {
     first_refused = n - 1;
-    drawn_bad = 0;
+    refused_token = -1;
   }
+  float u = __ldg(a.uniform + q0 + n - 1);
   __syncthreads();
+  int last = -1, last_x = -1;                       // this thread's latest refusal
   for (int i = threadIdx.x; i < n - 1; i += kVerifyThreads) {
     const int x = __ldg(a.tokens + q0 + i + 1);
     bool keep = false;
@@ -175,19 +195,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
       // (products of two fp32 numbers are exact in fp64)
       keep = (double)__ldg(a.uniform + q0 + i) * (double)q < (double)p;
     }
-    if (!keep) atomicMin(&first_refused, i);
+    if (!keep) {
+      atomicMin(&first_refused, i);
+      last = i;
+      last_x = x;
+      break;                                        // (a thread's later drafts come after this one)
+    }
   }
   __syncthreads();
   const int kept = first_refused;
+  if (last == kept) refused_token = last_x;
+  __syncthreads();
   Row r = {kPlain, -1};
   if (kept < n - 1) {
-    r.without = __ldg(a.tokens + q0 + kept + 1);
+    r.without = refused_token;
     const bool in = r.without >= 0 && r.without < V;
     r.how = !in ? kPlain : draft ? kLess : kWithout;   // a draft outside the vocabulary: from p
   }
   const T* p = target + (int64_t)(q0 + kept) * V;
   const T* q = r.how == kLess ? draft + (d0 + kept) * V : p;
-  float u = __ldg(a.uniform + q0 + n - 1);
   u = u >= 0.0f ? fminf(u, 0.99999994f) : 0.0f;
 
   if (rank == 0) {
@@ -204,16 +230,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
   const int w0 = (int)(at < V ? at : V), w1 = (int)(at + per < V ? at + per : V);
   for (int pass = 0;; ++pass) {
     long long sum = 0;
-    for (int i0 = w0; i0 < w1; i0 += 8 * kStep) {   // at most 64 weights a lane before they are joined
+    float w[U][N];                                  // the weights taken last
+#pragma unroll 1
+    for (int i0 = w0; i0 < w1; i0 += U * kStep) {
+      weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
       uint32_t hi = 0, lo = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float w[N];
-        weights_of<T, N, kVec>(p, q, r, min(i0 + k * kStep + lane * N, w1), w1, w);
+      for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int e = 0; e < N; ++e) add_units(w[e], hi, lo);
-      }
-      sum += units(hi, lo, 8 * N);
+        for (int e = 0; e < N; ++e) add_units(w[k][e], hi, lo);
+      sum += units(hi, lo, U * N);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -255,37 +281,40 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     }
     // ---- the place is this warp's if its sums pass the goal first --------------
     if (!((double)before <= goal && (double)(before + sum) > goal)) return;
-    for (int i0 = w0; i0 < w1; i0 += kStep) {
-      float w[N];
-      const int i = min(i0 + lane * N, w1);
-      weights_of<T, N, kVec>(p, q, r, i, w1, w);
-      uint32_t hi = 0, lo = 0;
+#pragma unroll 1
+    for (int i0 = w0; i0 < w1; i0 += U * kStep) {
+      // (a part of one round still has its weights)
+      if (w1 - w0 > U * kStep) weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
 #pragma unroll
-      for (int e = 0; e < N; ++e) add_units(w[e], hi, lo);
-      const long long own = units(hi, lo, N);
-      long long incl = own;
+      for (int k = 0; k < U; ++k) {
+        uint32_t hi = 0, lo = 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += x;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, (double)(before + incl) > goal);
-      if (past != 0) {
-        if (lane == __ffs(past) - 1) {
-          long long s = before + incl - own;
-          int z = i;
+        for (int e = 0; e < N; ++e) add_units(w[k][e], hi, lo);
+        const long long own = units(hi, lo, N);
+        long long incl = own;
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            uint32_t h1 = 0, l1 = 0;
-            add_units(w[e], h1, l1);
-            s += units(h1, l1, 1);
-            if ((double)s <= goal) ++z;
-          }
-          a.out_tokens[q0 + kept] = z;
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += x;
         }
-        return;
+        const unsigned past = __ballot_sync(0xffffffffu, (double)(before + incl) > goal);
+        if (past != 0) {
+          if (lane == __ffs(past) - 1) {
+            long long s = before + incl - own;
+            int z = i0 + k * kStep + lane * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              uint32_t h1 = 0, l1 = 0;
+              add_units(w[k][e], h1, l1);
+              s += units(h1, l1, 1);
+              if ((double)s <= goal) ++z;
+            }
+            a.out_tokens[q0 + kept] = z;
+          }
+          return;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
       }
-      before += __shfl_sync(0xffffffffu, incl, 31);
     }
     return;
   }

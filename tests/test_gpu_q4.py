@@ -179,6 +179,26 @@ def test_append_rotary_many_rows(pkv):
     assert same_bits(kv2, kv)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "q4"])
+def test_append_rotary_rounds_every_step(pkv, inter, kind):
+    """Enough elements that a product and a sum rounded as one would show (they
+    differ in one bf16 element of some 10^4)."""
+    s = Step([900], [900], 8, 8, 128, 16, 128, 1, max_pos=1000, seed=31)
+    where, how = s.how(inter)
+    q_out = torch.empty((900, 8, 128), dtype=torch.bfloat16, device="cuda")
+    k = s.rotated(s.k, inter)
+    if kind == "q4":
+        kv = torch.full((s.num_blocks, 8, ref.record_bytes(16, 128)), 0xFF, dtype=torch.uint8, device="cuda")
+        pkv.append_rotary_q4(q_out, s.dq, s.dk, s.dv, kv, *where, 16, **how)
+        assert same_bits(kv, expected_q4(s, k, s.v))
+    else:
+        kc, vc = (torch.zeros((s.num_blocks, 16, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        pkv.append_rotary(q_out, s.dq, s.dk, s.dv, kc, vc, *where, **how)
+        assert same_bits(kc[s.blk.cuda(), s.row.cuda()], k) and same_bits(vc[s.blk.cuda(), s.row.cuda()], s.v)
+    assert same_bits(q_out, s.rotated(s.q, inter))
+
+
 def test_append_one_token_without_offsets(pkv):
     L = [1, 16, 33, 64]
     s = Step(L, [1] * 4, 4, 2, 64, 16, 64, seed=9)
