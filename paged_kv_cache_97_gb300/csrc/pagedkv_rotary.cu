@@ -243,7 +243,7 @@ __device__ __forceinline__ void store_q4(bool store, unsigned char* rec, int x, 
 }
 
 template <int D, int kKind, int kRows>
-__global__ void __launch_bounds__(kRotaryThreads, 6) append_rotary_kernel(const RotaryArgs a, int bs) {
+__global__ void __launch_bounds__(kRotaryThreads, kRows <= 3 ? 8 : 6) append_rotary_kernel(const RotaryArgs a, int bs) {
   constexpr int kLanes = D / 16, kStep = kRotaryThreads / kLanes;        // rows taken side by side
   __shared__ __align__(16) float table[128];        // the token's cosines, then its sines
   const int lane = threadIdx.x & 31;
@@ -442,26 +442,32 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) read_q4_kernel(const ReadAr
       blk = -1;
     }
   }
-  const int H = a.num_kv_heads, in = pos % bs;
-  const int64_t base = (int64_t)blk * H;
-#pragma unroll 4
-  for (int i = lane; i < 2 * H * kWords; i += 32) {
-    const int x = i >= H * kWords;                  // 0: K, 1: V
-    const int hw = i - x * H * kWords, h = hw / kWords, e = hw % kWords;   // elements 8 e .. 8 e + 7
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (blk >= 0) {
-      const unsigned char* rec = a.kv + (base + h) * (bs * D * 9 / 8);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + q4_codes_at(x, in, bs, D) +
-                                                            ((e & 7) * kGroups + e / 8) * 4);
-      const uint32_t p = *reinterpret_cast<const uint32_t*>(rec + q4_pairs_at(x, in, bs, D) + (e / 8) * 4);
-      const float s = __uint_as_float(p << 16), m = __uint_as_float(p & 0xffff0000u);
-      float v[8];
+  // lane: word `e` of heads h0, h0 + 32 / kWords, .. ; elements 8 e .. 8 e + 7
+  constexpr int kSide = 32 / kWords;
+  const int H = a.num_kv_heads, in = pos % bs, rec_bytes = bs * D * 9 / 8;
+  const int e = lane % kWords, h0 = lane / kWords;
+  const unsigned char* block = a.kv + (int64_t)(blk >= 0 ? blk : 0) * H * rec_bytes;
+  uint4* out[2] = {a.k_out + tok * H * kWords, a.v_out + tok * H * kWords};
 #pragma unroll
-      for (int k = 0; k < 8; ++k)                   // c: the low bits of 2^23 + c; s * c is exact
-        v[k] = fmaf(s, __uint_as_float(0x4B000000u | (w >> (4 * k) & 15u)) - 8388608.0f, m);
-      o = narrow8(v);
+  for (int x = 0; x < 2; ++x) {
+    const int word_at = q4_codes_at(x, in, bs, D) + ((e & 7) * kGroups + e / 8) * 4;
+    const int pair_at = q4_pairs_at(x, in, bs, D) + (e / 8) * 4;
+#pragma unroll 8
+    for (int h = h0; h < H; h += kSide) {
+      const unsigned char* rec = block + (int64_t)h * rec_bytes;
+      uint4 o = make_uint4(0, 0, 0, 0);
+      if (blk >= 0) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + word_at));
+        const uint32_t p = __ldg(reinterpret_cast<const uint32_t*>(rec + pair_at));
+        const float s = __uint_as_float(p << 16), m = __uint_as_float(p & 0xffff0000u);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)                 // c: the low bits of 2^23 + c; s * c is exact
+          v[k] = fmaf(s, __uint_as_float(0x4B000000u | (w >> (4 * k) & 15u)) - 8388608.0f, m);
+        o = narrow8(v);
+      }
+      out[x][h * kWords + e] = o;
     }
-    (x ? a.v_out : a.k_out)[tok * H * kWords + hw] = o;
   }
 }
 
