@@ -976,6 +976,20 @@ kv_status pagedkv_verify_drafts(
     int batch, int num_tokens, int max_query_len, int vocab,
     pagedkv_prob_dtype dtype, void *stream);
 
+/* A call above with its arguments as an array of int64_t in the order of its
+ * declaration (pointers and integers as they are, a float as its 32 bits), for
+ * bindings that pay for every argument they convert.  Returns what the call
+ * returns; KV_ERR_INVALID_ARG for another `which` or number of arguments. */
+typedef enum {
+    PAGEDKV_CALL_APPEND_ROTARY = 0,
+    PAGEDKV_CALL_APPEND_ROTARY_Q4 = 1,
+    PAGEDKV_CALL_READ_Q4 = 2,
+    PAGEDKV_CALL_ATTENTION_DECODE_Q4 = 3,
+    PAGEDKV_CALL_ATTENTION_MULTI_Q4 = 4,
+    PAGEDKV_CALL_VERIFY_DRAFTS = 5
+} pagedkv_call_id;
+kv_status pagedkv_call(int which, const int64_t *args, int num_args);
+
 /* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */

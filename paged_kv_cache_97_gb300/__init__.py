@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -97,6 +98,7 @@ SIGNATURES = {
     "paged_attention_decode_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P]),
     "paged_attention_multi_q4": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                       _SZ, _P]),
+    "pagedkv_call": (_I, [_I, ctypes.c_char_p, _I]),
     "pagedkv_verify_drafts": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
 }
 
@@ -948,32 +950,55 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
 # Rotated append, 4-bit pools, verification of drafts
 # --------------------------------------------------------------------------
 
-def _rows(t, name, dev, heads=None, d=None):
-    """The token stride of bf16 rows [tokens, heads, head_dim] on device `dev`
-    (the rows of a token are contiguous, its neighbours any stride away)."""
-    bf16 = _dtypes()[0]
+# The calls below pass their arguments as one packed array (pagedkv_call): ctypes
+# converts them one by one otherwise, which for 33 arguments takes longer than the
+# launch.
+_ROTARY, _ROTARY_Q4, _READ_Q4, _DECODE_Q4, _MULTI_Q4, _VERIFY = range(6)
+_PACKS = [struct.Struct(f"{n}q").pack for n in (33, 29, 15, 17, 20, 15)]
+_COUNTS = (33, 29, 15, 17, 20, 15)
+_float_bits = struct.Struct("f").pack, struct.Struct("I").unpack
+
+
+def _call(which, *args):
+    st = (_lib or load()).pagedkv_call(which, _PACKS[which](*args), _COUNTS[which])
+    if st != KV_OK:
+        _check(st)
+
+
+def _bits(x):
+    """A float argument's 32 bits."""
+    return _float_bits[1](_float_bits[0](x))[0]
+
+
+def _at(t):
+    """A tensor's address, 0 for None."""
+    return 0 if t is None else t.data_ptr()
+
+
+def _rows(t, name, dev, heads, d):
+    """(tokens, token stride) of bf16 rows [tokens, heads, d] on device `dev` (the
+    rows of a token are contiguous, its neighbours any stride away)."""
     try:
-        good = t.dtype is bf16 and t.get_device() == dev and t.dim() == 3
+        good = t.dtype is _dt[0] and t.get_device() == dev and t.dim() == 3
     except AttributeError:
         good = False
     if not good:
-        _need(t, bf16, name, 3)
+        _need(t, _dt[0], name, 3)
         raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
     T, h, dim = t.shape
-    st, sh, sd = t.stride()
-    if heads is not None and (h != heads or dim != d):
+    if h != heads or dim != d:
         raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    if T and ((sd != 1 and dim > 1) or (sh != dim and h > 1)):
+    st, sh, sd = t.stride()
+    if T and (sd != 1 or (sh != dim and h > 1)):
         raise ValueError(f"{name}: the rows of a token must be contiguous")
-    return st if T > 1 else h * dim
+    return T, st if T > 1 else h * dim
 
 
-def _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens, positions, sections, rotary_dim,
-                 query_start, specs):
-    """The checks of append_rotary and append_rotary_q4 and the arguments they
-    share: (rows and strides), (rotation), (tables), T, query heads, device."""
-    _, i32, f32, _ = _dtypes()
-    specs += [(block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1)]
+def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, seq_lens, positions, sections,
+            rotary_dim, interleaved, query_start, max_query_len, specs, stream):
+    """append_rotary and append_rotary_q4: the checks they share, and the call."""
+    _, i32, f32, _ = _dt
+    specs += ((block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1))
     if cos_sin is not None:
         specs.append((cos_sin, f32, "cos_sin", 2))
     if positions is not None:
@@ -981,43 +1006,46 @@ def _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens, positi
     if query_start is not None:
         specs.append((query_start, i32, "query_start", 1))
     dev = _need_all(*specs)
-    T, B = k.shape[0], seq_lens.shape[0]
-    rows = [None, 0, None, 0, k.data_ptr(), _rows(k, "k", dev, hkv, d), v.data_ptr(), _rows(v, "v", dev, hkv, d)]
-    if v.shape[0] != T:
+    T, k_stride = _rows(k, "k", dev, hkv, d)
+    Tv, v_stride = _rows(v, "v", dev, hkv, d)
+    B, mb = block_tables.shape
+    if Tv != T:
         raise ValueError("k and v disagree on the number of tokens")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out belong together")
-    hq = 0
+    hq = q_stride = out_stride = 0
     if q is not None:
         hq = q.shape[1] if q.dim() == 3 else 0
-        rows[:4] = [q_out.data_ptr(), _rows(q_out, "q_out", dev, hq, d), q.data_ptr(), _rows(q, "q", dev, hq, d)]
-        if q.shape[0] != T or q_out.shape[0] != T:
+        Tq, q_stride = _rows(q, "q", dev, hq, d)
+        To, out_stride = _rows(q_out, "q_out", dev, hq, d)
+        if Tq != T or To != T:
             raise ValueError("q, q_out and k disagree on the number of tokens")
-    mb = block_tables.shape
-    if mb[0] != B:
+    if len(seq_lens) != B:
         raise ValueError("block_tables and seq_lens must have one row per sequence")
     if query_start is None:
         if T != B:
             raise ValueError("without query_start there is one token per sequence")
-    elif query_start.shape[0] != B + 1:
+    elif len(query_start) != B + 1:
         raise ValueError("query_start must have batch + 1 entries")
-    axes, sec, limit, width = 1, None, 0, 0
+    axes, sec, limit, width, where = 1, None, 0, 0, 0
     if cos_sin is not None:
         limit, width = cos_sin.shape
         if rotary_dim is not None and rotary_dim != width:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
         if positions is not None:
-            axes = positions.shape[0]
-            if positions.shape[1] != T:
+            axes, given = positions.shape
+            where = positions.data_ptr()
+            if given != T:
                 raise ValueError("positions must be [axes, tokens]")
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError("one section per axis of positions is needed")
-            sec = (ctypes.c_int32 * len(sections))(*sections)
-    how = (_ptr(cos_sin), limit, width)
-    where = (_ptr(positions) if cos_sin is not None else None, axes, sec)
-    tables = (block_tables.data_ptr(), mb[1], seq_lens.data_ptr(), _ptr(query_start), B, T)
-    return rows, how, where, tables, hq, dev
+            sec = (ctypes.c_int32 * axes)(*sections)
+    _call(which, _at(q_out), out_stride, _at(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, *pool,
+          _at(cos_sin), limit, width, 1 if interleaved else 0, where, axes, 0 if sec is None else ctypes.addressof(sec),
+          block_tables.data_ptr(), mb, seq_lens.data_ptr(), _at(query_start), B, T, int(max_query_len), hq, hkv, d,
+          *sizes, _stream_on(stream, dev) or 0)
+    return q_out
 
 
 def append_rotary(q_out, q, k, v, k_cache, v_cache, cos_sin, block_tables, seq_lens, positions=None, sections=None,
@@ -1031,17 +1059,13 @@ def append_rotary(q_out, q, k, v, k_cache, v_cache, cos_sin, block_tables, seq_l
     [max_position, rotary_dim]: cosines, then sines (None: no rotation);
     positions int32 [axes, T] with ``sections`` frequencies per axis, or None:
     the cache positions.  ``interleaved``: pairs (2j, 2j + 1)."""
+    _dtypes()
     specs = []
     dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
     nb, bs, hkv, d = k_cache.shape
-    rows, how, where, tables, hq, dev = _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens,
-                                                     positions, sections, rotary_dim, query_start, specs)
-    st = load().pagedkv_append_rotary(*rows, k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-                                      *how, 1 if interleaved else 0, *where, *tables, int(max_query_len), hq, hkv, d,
-                                      nb, bs, dt, _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
-    return q_out
+    return _rotary(_ROTARY, q_out, q, k, v, (k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale)),
+                   (nb, bs, dt), hkv, d, cos_sin, block_tables, seq_lens, positions, sections, rotary_dim,
+                   interleaved, query_start, max_query_len, specs, stream)
 
 
 def q4_record_bytes(block_size, head_dim) -> int:
@@ -1050,19 +1074,27 @@ def q4_record_bytes(block_size, head_dim) -> int:
     return load().pagedkv_q4_record_bytes(block_size, head_dim)
 
 
+_u8 = None                  # torch.uint8, resolved once
+
+
 def _pool_q4(kv_cache, block_size, specs):
     """(num_blocks, num_kv_heads, head_dim) of a 4-bit pool; its check goes to specs."""
-    import torch
-    specs.append((kv_cache, torch.uint8, "kv_cache", 3))
-    if getattr(kv_cache, "dtype", None) is not torch.uint8 or kv_cache.dim() != 3:
-        _need(kv_cache, torch.uint8, "kv_cache", 3)
+    global _u8
+    if _u8 is None:
+        import torch
+        _u8 = torch.uint8
+    specs.append((kv_cache, _u8, "kv_cache", 3))
+    if getattr(kv_cache, "dtype", None) is not _u8 or kv_cache.dim() != 3:
+        _need(kv_cache, _u8, "kv_cache", 3)
         raise ValueError("kv_cache must be [num_blocks, num_kv_heads, record bytes]")
     nb, hkv, rec = kv_cache.shape
-    d = rec * 8 // (9 * block_size) if block_size in (16, 32) else 0
-    if d not in (64, 128) or block_size * d * 9 // 8 != rec:
-        raise ValueError("kv_cache's last dimension must be q4_record_bytes(block_size, head_dim) (block_size 16 or "
-                         "32, head_dim 64 or 128)")
-    return nb, hkv, d
+    if block_size == 16 or block_size == 32:
+        if rec == 72 * block_size:
+            return nb, hkv, 64
+        if rec == 144 * block_size:
+            return nb, hkv, 128
+    raise ValueError("kv_cache's last dimension must be q4_record_bytes(block_size, head_dim) (block_size 16 or "
+                     "32, head_dim 64 or 128)")
 
 
 def append_rotary_q4(q_out, q, k, v, kv_cache, cos_sin, block_tables, seq_lens, block_size, positions=None,
@@ -1071,15 +1103,12 @@ def append_rotary_q4(q_out, q, k, v, kv_cache, cos_sin, block_tables, seq_lens, 
     """append_rotary into a 4-bit pool (uint8 [num_blocks, Hkv,
     q4_record_bytes]): every 64 values of a row as codes 0..15 under a (scale,
     min) pair of their own."""
+    _dtypes()
     specs = []
     nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
-    rows, how, where, tables, hq, dev = _rotary_args(q_out, q, k, v, hkv, d, cos_sin, block_tables, seq_lens,
-                                                     positions, sections, rotary_dim, query_start, specs)
-    st = load().pagedkv_append_rotary_q4(*rows, kv_cache.data_ptr(), *how, 1 if interleaved else 0, *where, *tables,
-                                         int(max_query_len), hq, hkv, d, nb, int(block_size), _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
-    return q_out
+    return _rotary(_ROTARY_Q4, q_out, q, k, v, (kv_cache.data_ptr(),), (nb, int(block_size)), hkv, d, cos_sin,
+                   block_tables, seq_lens, positions, sections, rotary_dim, interleaved, query_start, max_query_len,
+                   specs, stream)
 
 
 def read_q4(k_out, v_out, kv_cache, block_tables, seq_lens, block_size, query_start=None, max_query_len=1,
@@ -1094,7 +1123,7 @@ def read_q4(k_out, v_out, kv_cache, block_tables, seq_lens, block_size, query_st
     if query_start is not None:
         specs.append((query_start, i32, "query_start", 1))
     dev = _need_all(*specs)
-    T, B = k_out.shape[0], seq_lens.shape[0]
+    T, B = len(k_out), len(seq_lens)
     mb = block_tables.shape
     if k_out.shape != (T, hkv, d) or v_out.shape != k_out.shape or mb[0] != B:
         raise ValueError("k_out, v_out must be [tokens, num_kv_heads, head_dim], the tables one row per sequence")
@@ -1103,11 +1132,9 @@ def read_q4(k_out, v_out, kv_cache, block_tables, seq_lens, block_size, query_st
             raise ValueError("without query_start there is one token per sequence")
     elif query_start.shape[0] != B + 1:
         raise ValueError("query_start must have batch + 1 entries")
-    st = load().pagedkv_read_q4(k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), mb[1],
-                                seq_lens.data_ptr(), _ptr(query_start), B, T, int(max_query_len), hkv, d, nb,
-                                int(block_size), _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
+    _call(_READ_Q4, k_out.data_ptr(), v_out.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), mb[1],
+          seq_lens.data_ptr(), _at(query_start), B, T, int(max_query_len), hkv, d, nb, int(block_size),
+          _stream_on(stream, dev) or 0)
     return k_out, v_out
 
 
@@ -1151,7 +1178,7 @@ def _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size, workspac
         raise ValueError("one query token per sequence, or query_start of batch + 1 entries")
     ws, ws_n = _space(workspace, dev)
     return (out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), mb[1],
-            seq_lens.data_ptr()), B, T, (hq, hkv, d, nb, int(block_size)), ws, ws_n, dev
+            seq_lens.data_ptr()), B, T, (hq, hkv, d, nb, int(block_size)), ws or 0, ws_n, dev
 
 
 def paged_attention_decode_q4(out, q, kv_cache, block_tables, seq_lens, block_size, max_seq_len, scale,
@@ -1159,10 +1186,7 @@ def paged_attention_decode_q4(out, q, kv_cache, block_tables, seq_lens, block_si
     """paged_attention_decode over a 4-bit pool."""
     first, B, _, sizes, ws, ws_n, dev = _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size,
                                                       workspace, None)
-    st = load().paged_attention_decode_q4(*first, B, *sizes, int(max_seq_len), float(scale), ws, ws_n,
-                                          _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
+    _call(_DECODE_Q4, *first, B, *sizes, int(max_seq_len), _bits(scale), ws, ws_n, _stream_on(stream, dev) or 0)
     return out
 
 
@@ -1173,11 +1197,12 @@ def paged_attention_multi_q4(out, q, kv_cache, block_tables, seq_lens, query_sta
         raise TypeError("query_start must be a torch.Tensor")
     first, B, T, sizes, ws, ws_n, dev = _attention_q4(out, q, kv_cache, block_tables, seq_lens, block_size,
                                                       workspace, query_start)
-    st = load().paged_attention_multi_q4(*first, query_start.data_ptr(), B, T, int(max_query_len), *sizes,
-                                         int(max_seq_len), float(scale), ws, ws_n, _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
+    _call(_MULTI_Q4, *first, query_start.data_ptr(), B, T, int(max_query_len), *sizes, int(max_seq_len), _bits(scale),
+          ws, ws_n, _stream_on(stream, dev) or 0)
     return out
+
+
+_prob_kinds = None          # probabilities' types, resolved once
 
 
 def verify_drafts(out_tokens, num_accepted, tokens, target_probs, draft_probs, uniform, query_start, max_query_len=None,
@@ -1188,10 +1213,12 @@ def verify_drafts(out_tokens, num_accepted, tokens, target_probs, draft_probs, u
     seq_lens).  tokens int32 [T]: each sequence's last known token, then its
     drafts; target_probs [T, V], draft_probs [T - B, V] (None: drafts without
     probabilities) of one of fp32, bf16, fp16; uniform fp32 [T] in [0, 1)."""
-    import torch
+    global _prob_kinds
     _, i32, f32, _ = _dtypes()
-    kinds = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}
-    kind = kinds.get(getattr(target_probs, "dtype", None))
+    if _prob_kinds is None:
+        import torch
+        _prob_kinds = {torch.float32: PROB_F32, torch.bfloat16: PROB_BF16, torch.float16: PROB_F16}
+    kind = _prob_kinds.get(getattr(target_probs, "dtype", None))
     if kind is None:
         raise TypeError("target_probs must be a torch.float32, torch.bfloat16 or torch.float16 tensor")
     specs = [(out_tokens, i32, "out_tokens", 1), (num_accepted, i32, "num_accepted", 1), (tokens, i32, "tokens", 1),
@@ -1212,13 +1239,9 @@ def verify_drafts(out_tokens, num_accepted, tokens, target_probs, draft_probs, u
         raise ValueError("draft_probs must be [tokens - batch, vocab]")
     if seq_lens is not None and (seq_lens.shape[0] != B or new_lens.shape[0] != B):
         raise ValueError("seq_lens and new_lens must have one entry per sequence")
-    st = load().pagedkv_verify_drafts(out_tokens.data_ptr(), num_accepted.data_ptr(), tokens.data_ptr(),
-                                      target_probs.data_ptr(), _ptr(draft_probs), uniform.data_ptr(),
-                                      query_start.data_ptr(), _ptr(seq_lens), _ptr(new_lens), B, T,
-                                      int(T if max_query_len is None else max_query_len) or 1, V, kind,
-                                      _stream_on(stream, dev))
-    if st != KV_OK:
-        _check(st)
+    _call(_VERIFY, out_tokens.data_ptr(), num_accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
+          _at(draft_probs), uniform.data_ptr(), query_start.data_ptr(), _at(seq_lens), _at(new_lens), B, T,
+          int(T if max_query_len is None else max_query_len) or 1, V, kind, _stream_on(stream, dev) or 0)
     return out_tokens, num_accepted
 
 

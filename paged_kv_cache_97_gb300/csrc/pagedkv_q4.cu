@@ -260,34 +260,35 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
   // (launched as a programmatic dependent: what is before may still run until here)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x < kWarps * S)
-    mbar_init(smem_addr(&bars[threadIdx.x / S][threadIdx.x % S]), 1);
-  if (threadIdx.x == 0) start_b = -1;
+  if (lane < S) mbar_init(smem_addr(&bars[warp][lane]), 1);     // (a warp uses its own only)
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  __syncthreads();
+  __syncwarp();
 
   // ---- this CTA's range of the head's block positions ----------------------
-  if (a.whole && !kMulti) {
-    // one CTA per sequence
-    if (threadIdx.x == 0) {
-      const Seq s = seq_of<BS, kMulti>(a, c);
-      if (s.bad) {
-        atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
-        for (int e = 0; e < GQ * D / 8; ++e)
-          reinterpret_cast<uint4*>(a.out + ((int64_t)c * Hq + (int64_t)hk * GQ) * D)[e] = make_uint4(0, 0, 0, 0);
-      } else {
-        start_b = c;
-        start_ct = start_us = 0;
-        range_len = s.nblk;
-      }
+  const bool one = !kMulti && a.whole;              // one CTA per sequence
+  int b0 = c, ct0 = 0, us0 = 0, len0 = 0, fid = 0;
+  if (one) {
+    // the first blocks' ids and the queries are asked for beside the length
+    const int j = warp * C::kBlocks + lane;
+    if (lane < C::kBlocks && j < a.max_blocks) fid = __ldg(a.block_tables + (int64_t)c * a.max_blocks + j);
+    const __nv_bfloat16* row = a.q + ((int64_t)c * Hq + (int64_t)hk * GQ) * D;
+    if ((int)threadIdx.x * 64 < GQ * D) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + threadIdx.x * 64));
+    const Seq s = seq_of<BS, kMulti>(a, c);
+    if (s.bad) {
+      if (threadIdx.x == 0) atomicOr(a.flags, PAGEDKV_FLAG_BAD_SEQ_LEN);
+      uint4* o = reinterpret_cast<uint4*>(a.out + ((int64_t)c * Hq + (int64_t)hk * GQ) * D);
+      for (int e = threadIdx.x; e < GQ * D / 8; e += kThreads4) o[e] = make_uint4(0, 0, 0, 0);
+      return;
     }
+    len0 = s.nblk;
   } else {
     // Every thread sums a run of sequences; the sums' prefix says where the
     // range begins.  Positions are blocks (whole: column tiles).
+    if (threadIdx.x == 0) start_b = -1;
     const int run = (a.batch + kThreads4 - 1) / kThreads4;
-    const int b0 = threadIdx.x * run, b1 = min(a.batch, b0 + run);
+    const int r0 = threadIdx.x * run, r1 = min(a.batch, r0 + run);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
+    for (int b = r0; b < r1; ++b) {
       const Seq s = seq_of<BS, kMulti>(a, b);
       sum += a.whole ? s.nct : (long long)s.nct * s.nblk;
       if (s.bad && b % a.ctas == c) {
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
     const long long per = a.whole ? 1 : (even > kMinRange ? even : kMinRange);
     const long long u0 = (long long)c * per;
     if (u0 >= at && u0 < at + sum) {
-      for (int b = b0; b < b1; ++b) {
+      for (int b = r0; b < r1; ++b) {
         const Seq s = seq_of<BS, kMulti>(a, b);
         const long long w = a.whole ? s.nct : (long long)s.nct * s.nblk;
         if (u0 < at + w) {
@@ -340,14 +341,17 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
         at += w;
       }
     }
+    __syncthreads();
+    if (start_b < 0) {                              // nothing for this CTA
+      if (!a.whole && threadIdx.x == 0) a.ws_meta[(int64_t)hk * a.ctas + c] = make_int4(0, 0, 0, 0);
+      return;
+    }
+    b0 = start_b;
+    ct0 = start_ct;
+    us0 = start_us;
+    len0 = range_len;
   }
-  __syncthreads();
   const int64_t cell = (int64_t)hk * a.ctas + c;
-  if (start_b < 0) {                                // nothing for this CTA
-    if (!a.whole && threadIdx.x == 0) a.ws_meta[cell] = make_int4(0, 0, 0, 0);
-    return;
-  }
-
   const uint32_t ring = smem_addr(smem4) + warp * S * C::kStage;
   float* dump = reinterpret_cast<float*>(smem4 + kWarps * S * C::kStage);   // [warp][column][kRow]
   float* dump_ml = dump + kWarps * C::kCols * C::kRow;                      // [warp][column][2]
@@ -356,44 +360,39 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
   // ---- the warp's ring: every fourth step of each piece ---------------------
   constexpr int PB = C::kBlocks;
   Walk<BS, kMulti> f, w;
-  f.start(a, start_b, start_ct, start_us, range_len);
+  f.start(a, b0, ct0, us0, len0);
   w = f;
-  int fj = f.j0 + warp * PB, fid[PB];               // next blocks to copy
+  int fj = f.j0 + warp * PB;                        // next blocks to copy; lane i < PB has the i-th's id
   int fs = 0, cs = 0, ahead = 0;                    // stages: next to fill, to use; filled
   uint32_t phase = 0, bad_stages = 0;
   bool dead = false;
-  auto settle = [&]() {                             // to the next step the warp will copy
+  auto settle = [&](bool known) {                   // to the next step the warp will copy
     while (!f.done() && fj >= f.j1) {
       f.next(a);
       fj = f.j0 + warp * PB;
     }
-    if (f.done()) return;
-    const int32_t* row = a.block_tables + (int64_t)f.b * a.max_blocks + fj;
-#pragma unroll
-    for (int i = 0; i < PB; ++i) fid[i] = i == 0 || fj + i < f.j1 ? __ldg(row + i) : 0;
+    if (!known && !f.done() && lane < min(PB, f.j1 - fj))
+      fid = __ldg(a.block_tables + (int64_t)f.b * a.max_blocks + fj + lane);
   };
-  settle();
+  settle(one);
   auto fetch = [&]() {
     if (f.done() || dead) return;
-    bool ok = true;
-#pragma unroll
-    for (int i = 0; i < PB; ++i) ok = ok && (unsigned)fid[i] < (unsigned)a.num_blocks;
+    const int have = min(PB, f.j1 - fj);
+    const bool ok = __all_sync(0xffffffffu, lane >= have || (unsigned)fid < (unsigned)a.num_blocks);
     bad_stages = (bad_stages & ~(1u << fs)) | (ok ? 0u : 1u << fs);
-    if (lane == 0) {
-      if (!ok) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
-      const uint32_t bar = smem_addr(&bars[warp][fs]), dst = ring + fs * C::kStage;
-      const int have = min(PB, f.j1 - fj);
-      mbar_expect_tx(bar, have * G::kRecord);
-#pragma unroll
-      for (int i = 0; i < PB; ++i)
-        if (i < have)
-          bulk_load(dst + i * G::kRecord, a.kv + ((int64_t)(ok ? fid[i] : 0) * a.num_kv_heads + hk) * G::kRecord,
-                    G::kRecord, bar);
+    if (lane < have) {
+      const uint32_t bar = smem_addr(&bars[warp][fs]);
+      if (lane == 0) {
+        if (!ok) atomicOr(a.flags, PAGEDKV_FLAG_BAD_BLOCK);
+        mbar_expect_tx(bar, have * G::kRecord);
+      }
+      bulk_load(ring + fs * C::kStage + lane * G::kRecord,
+                a.kv + ((int64_t)(ok ? fid : 0) * a.num_kv_heads + hk) * G::kRecord, G::kRecord, bar);
     }
     fs = fs + 1 == S ? 0 : fs + 1;
     ++ahead;
     fj += kWarps * PB;
-    settle();
+    settle(false);
   };
 #pragma unroll 1
   for (int s = 0; s < S; ++s) fetch();

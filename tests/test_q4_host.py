@@ -101,6 +101,28 @@ def test_empty_batch_is_a_no_op(pkv, name, base):
     assert pkv.load().pagedkv_copy_blocks_q4(*dict(COPY, num_pairs=0).values()) == pkv.KV_OK
 
 
+def test_packed_calls(pkv):
+    """pagedkv_call passes on what the calls themselves get, and counts arguments."""
+    import struct
+    lib = pkv.load()
+    for which, (name, base) in enumerate([("pagedkv_append_rotary", ROTARY), ("pagedkv_append_rotary_q4", ROTARY_Q4),
+                                          ("pagedkv_read_q4", READ), ("paged_attention_decode_q4", DECODE),
+                                          ("paged_attention_multi_q4", MULTI), ("pagedkv_verify_drafts", VERIFY)]):
+        assert pkv._COUNTS[which] == len(base)
+
+        def packed(**change):
+            xs = [getattr(x, "value", x) or 0 for x in dict(base, **change).values()]
+            return struct.pack(f"{len(xs)}q", *[struct.unpack("I", struct.pack("f", x))[0] if isinstance(x, float) else x
+                                                for x in xs])
+        empty = dict(batch=0, **({"num_tokens": 0} if "num_tokens" in base else {}))
+        assert lib.pagedkv_call(which, packed(**empty), len(base)) == pkv.KV_OK
+        assert lib.pagedkv_call(which, packed(batch=-1), len(base)) == pkv.KV_ERR_INVALID_ARG
+        assert name in lib.pagedkv_last_error().decode()
+        assert lib.pagedkv_call(which, packed(), len(base) - 1) == pkv.KV_ERR_INVALID_ARG
+    assert lib.pagedkv_call(6, packed(), 15) == pkv.KV_ERR_INVALID_ARG
+    assert lib.pagedkv_call(0, None, 33) == pkv.KV_ERR_INVALID_ARG
+
+
 def test_sizes(pkv):
     for bs in (16, 32):
         for d in (64, 128):
