@@ -975,29 +975,23 @@ def _at(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _rows(t, name, dev, heads, d):
-    """(tokens, token stride) of bf16 rows [tokens, heads, d] on device `dev` (the
-    rows of a token are contiguous, its neighbours any stride away)."""
-    try:
-        good = t.dtype is _dt[0] and t.get_device() == dev and t.dim() == 3
-    except AttributeError:
-        good = False
-    if not good:
-        _need(t, _dt[0], name, 3)
+def _bad_rows(t, name, dev, shape):
+    """Raises for a tensor that is no rows of `shape` (None: any number of heads)."""
+    _need_rows = _dt[0]
+    if getattr(t, "dtype", None) is not _need_rows or t.dim() != 3 or not t.is_cuda:
+        _need(t, _need_rows, name, 3)
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
-    T, h, dim = t.shape
-    if h != heads or dim != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    st, sh, sd = t.stride()
-    if T and (sd != 1 or (sh != dim and h > 1)):
-        raise ValueError(f"{name}: the rows of a token must be contiguous")
-    return T, st if T > 1 else h * dim
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: the rows of a token must be contiguous")
 
 
 def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, seq_lens, positions, sections,
             rotary_dim, interleaved, query_start, max_query_len, specs, stream):
-    """append_rotary and append_rotary_q4: the checks they share, and the call."""
-    _, i32, f32, _ = _dt
+    """append_rotary and append_rotary_q4: the checks they share, and the call.
+    (Written flat: a step of few tokens takes no longer on the GPU than here.)"""
+    bf16, i32, f32, _ = _dt
     specs += ((block_tables, i32, "block_tables", 2), (seq_lens, i32, "seq_lens", 1))
     if cos_sin is not None:
         specs.append((cos_sin, f32, "cos_sin", 2))
@@ -1006,45 +1000,59 @@ def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, s
     if query_start is not None:
         specs.append((query_start, i32, "query_start", 1))
     dev = _need_all(*specs)
-    T, k_stride = _rows(k, "k", dev, hkv, d)
-    Tv, v_stride = _rows(v, "v", dev, hkv, d)
-    B, mb = block_tables.shape
-    if Tv != T:
-        raise ValueError("k and v disagree on the number of tokens")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out belong together")
-    hq = q_stride = out_stride = 0
+    T, hq = k.size(0), 0
+    kv_shape = (T, hkv, d)
+    # rows [T, heads, d]: a token's are contiguous, its neighbours any stride away
+    args = []
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        Tq, q_stride = _rows(q, "q", dev, hq, d)
-        To, out_stride = _rows(q_out, "q_out", dev, hq, d)
-        if Tq != T or To != T:
-            raise ValueError("q, q_out and k disagree on the number of tokens")
-    if len(seq_lens) != B:
+        hq = q.size(1)
+        q_shape = (T, hq, d)
+        given = (q_out, q_shape, "q_out"), (q, q_shape, "q"), (k, kv_shape, "k"), (v, kv_shape, "v")
+    else:
+        args = [0, 0, 0, 0]
+        given = (k, kv_shape, "k"), (v, kv_shape, "v")
+    for t, shape, name in given:
+        if t.dtype is not bf16 or t.get_device() != dev or t.shape != shape:
+            _bad_rows(t, name, dev, shape)
+        st, sh, sd = t.stride()
+        if (sh != d and shape[1] > 1 or sd != 1) and T:
+            _bad_rows(t, name, dev, shape)
+        args += (t.data_ptr(), st if T > 1 else shape[1] * d)
+    B, mb = block_tables.shape
+    if seq_lens.size(0) != B:
         raise ValueError("block_tables and seq_lens must have one row per sequence")
+    starts = 0
     if query_start is None:
         if T != B:
             raise ValueError("without query_start there is one token per sequence")
-    elif len(query_start) != B + 1:
-        raise ValueError("query_start must have batch + 1 entries")
-    axes, sec, limit, width, where = 1, None, 0, 0, 0
+    else:
+        starts = query_start.data_ptr()
+        if query_start.size(0) != B + 1:
+            raise ValueError("query_start must have batch + 1 entries")
+    table, axes, sec, limit, width, where = 0, 1, 0, 0, 0, 0
     if cos_sin is not None:
         limit, width = cos_sin.shape
+        table = cos_sin.data_ptr()
         if rotary_dim is not None and rotary_dim != width:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
         if positions is not None:
-            axes, given = positions.shape
+            axes, tokens = positions.shape
             where = positions.data_ptr()
-            if given != T:
+            if tokens != T:
                 raise ValueError("positions must be [axes, tokens]")
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError("one section per axis of positions is needed")
-            sec = (ctypes.c_int32 * axes)(*sections)
-    _call(which, _at(q_out), out_stride, _at(q), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, *pool,
-          _at(cos_sin), limit, width, 1 if interleaved else 0, where, axes, 0 if sec is None else ctypes.addressof(sec),
-          block_tables.data_ptr(), mb, seq_lens.data_ptr(), _at(query_start), B, T, int(max_query_len), hq, hkv, d,
-          *sizes, _stream_on(stream, dev) or 0)
+            sections = (ctypes.c_int32 * axes)(*sections)
+            sec = ctypes.addressof(sections)
+    st = _lib.pagedkv_call(which, _PACKS[which](
+        *args, *pool, table, limit, width, 1 if interleaved else 0, where, axes, sec, block_tables.data_ptr(), mb,
+        seq_lens.data_ptr(), starts, B, T, int(max_query_len), hq, hkv, d, *sizes, _stream_on(stream, dev) or 0),
+        _COUNTS[which])
+    if st != KV_OK:
+        _check(st)
     return q_out
 
 
@@ -1059,7 +1067,8 @@ def append_rotary(q_out, q, k, v, k_cache, v_cache, cos_sin, block_tables, seq_l
     [max_position, rotary_dim]: cosines, then sines (None: no rotation);
     positions int32 [axes, T] with ``sections`` frequencies per axis, or None:
     the cache positions.  ``interleaved``: pairs (2j, 2j + 1)."""
-    _dtypes()
+    if _lib is None or _dt is None:
+        load(), _dtypes()
     specs = []
     dt = _pools(k_cache, v_cache, k_scale, v_scale, specs)
     nb, bs, hkv, d = k_cache.shape
@@ -1103,7 +1112,8 @@ def append_rotary_q4(q_out, q, k, v, kv_cache, cos_sin, block_tables, seq_lens, 
     """append_rotary into a 4-bit pool (uint8 [num_blocks, Hkv,
     q4_record_bytes]): every 64 values of a row as codes 0..15 under a (scale,
     min) pair of their own."""
-    _dtypes()
+    if _lib is None or _dt is None:
+        load(), _dtypes()
     specs = []
     nb, hkv, d = _pool_q4(kv_cache, block_size, specs)
     return _rotary(_ROTARY_Q4, q_out, q, k, v, (kv_cache.data_ptr(),), (nb, int(block_size)), hkv, d, cos_sin,
