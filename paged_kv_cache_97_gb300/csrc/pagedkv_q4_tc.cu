@@ -208,14 +208,36 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
 // Attention
 // ---------------------------------------------------------------------------
 
+// Two fp32 numbers as one operand of the packed multiply-add and add.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Largest of 64 scores (those past `lim` left out when kMask).
 template <bool kMask>
 __device__ __forceinline__ float half_max(const uint32_t (&raw)[64], int first, int lim) {
   float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    float v = __uint_as_float(raw[j]);
+  for (int j = 0; j < 64; j += 2) {
+    float v = __uint_as_float(raw[j]), w = __uint_as_float(raw[j + 1]);
     if (kMask && first + j > lim) v = -INFINITY;
-    mr[j & 3] = fmaxf(mr[j & 3], v);
+    if (kMask && first + j + 1 > lim) w = -INFINITY;
+    mr[j / 2 & 3] = fmaxf(fmaxf(mr[j / 2 & 3], v), w);
   }
   return fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3]));
 }
@@ -224,20 +246,25 @@ __device__ __forceinline__ float half_max(const uint32_t (&raw)[64], int first, 
 template <bool kMask>
 __device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&pw)[32], int first, int lim, float k,
                                           float add) {
-  float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint64_t kk = pack_f32x2(k, k), aa = pack_f32x2(add, add);
+  uint64_t ls[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    float p0 = ex2(fmaf(__uint_as_float(raw[2 * j]), k, add));
-    float p1 = ex2(fmaf(__uint_as_float(raw[2 * j + 1]), k, add));
+    float p0, p1;
+    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), kk, aa), p0, p1);
+    p0 = ex2(p0);
+    p1 = ex2(p1);
     if (kMask) {
       p0 = first + 2 * j <= lim ? p0 : 0.0f;
       p1 = first + 2 * j + 1 <= lim ? p1 : 0.0f;
     }
-    ls[(2 * j) & 3] += p0;
-    ls[(2 * j + 1) & 3] += p1;
+    ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(p0, p1));
     pw[j] = pack2<true>(p0, p1);
   }
-  return (ls[0] + ls[1]) + (ls[2] + ls[3]);
+  float l0, l1, l2, l3;
+  unpack_f32x2(ls[0], l0, l1);
+  unpack_f32x2(ls[1], l2, l3);
+  return (l0 + l1) + (l2 + l3);
 }
 
 __device__ __forceinline__ void bulk_image(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
