@@ -633,7 +633,9 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
             // to the largest score + exponent of max(vscale, |vmin| / 16), less five
             // (rows of equal values have the least scale, and p * vmin has to stay
             // within fp32 too; exponents are -100 at least), and p is taken again.
-            float p[T][A][4], ps[T][A][NG][4];
+            // (The products are made again where they are packed: held meanwhile for 32
+            // columns they would not fit the registers.)
+            float p[T][A][4];
             auto weigh = [&]() {
               float top = 0.0f, top_s = 0.0f;
 #pragma unroll
@@ -647,13 +649,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
 #pragma unroll
                   for (int gr = 0; gr < NG; ++gr) {
                     const float s0 = pair_scale(vp[x][0][gr]), s1 = pair_scale(vp[x][1][gr]);
-                    float* y = ps[x][nt][gr];
-                    y[0] = p[x][nt][0] * s0;
-                    y[1] = p[x][nt][1] * s0;
-                    y[2] = p[x][nt][2] * s1;
-                    y[3] = p[x][nt][3] * s1;
-                    top_s = fmaxf(fmaxf(top_s, y[0]), y[1]);
-                    top_s = fmaxf(fmaxf(top_s, y[2]), y[3]);
+                    top_s = fmaxf(fmaxf(top_s, p[x][nt][0] * s0), p[x][nt][1] * s0);
+                    top_s = fmaxf(fmaxf(top_s, p[x][nt][2] * s1), p[x][nt][3] * s1);
                   }
                 }
               }
@@ -706,9 +703,9 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
                   const float m0 = pair_min(vp[x][0][gr]), m1 = pair_min(vp[x][1][gr]);
-                  const float* z = ps[x][nt][gr];
-                  pb[nt][gr][0] = transposed8(pack2<true>(z[0], z[1]));
-                  pb[nt][gr][1] = transposed8(pack2<true>(z[2], z[3]));
+                  const float s0 = pair_scale(vp[x][0][gr]), s1 = pair_scale(vp[x][1][gr]);
+                  pb[nt][gr][0] = transposed8(pack2<true>(y[0] * s0, y[1] * s0));
+                  pb[nt][gr][1] = transposed8(pack2<true>(y[2] * s1, y[3] * s1));
                   pm[nt][gr][0] = fmaf(y[0], m0, fmaf(y[2], m1, pm[nt][gr][0]));
                   pm[nt][gr][1] = fmaf(y[1], m0, fmaf(y[3], m1, pm[nt][gr][1]));
                 }

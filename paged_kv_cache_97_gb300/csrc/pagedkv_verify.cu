@@ -13,7 +13,8 @@
 // A cluster of up to 8 CTAs takes a sequence: every CTA finds the row from the
 // drafts by itself, each sums its part of the row, the parts' sums go to all
 // CTAs through distributed shared memory, and the one warp whose part holds the
-// drawn place walks over it (a part longer than one round is read again, from L2).  Bound by the one row (two with q) that
+// drawn place finds it by the sums of its rounds and steps (a round that is not its
+// last is read again, from L2).  Bound by the one row (two with q) that
 // has to be read per sequence, and in small batches by the chain of loads:
 // offsets, drafts, their probabilities, the row, the part again.
 #include <cuda_bf16.h>
@@ -30,6 +31,7 @@ using namespace dev;
 
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kRounds = 64;                         // rounds of a warp whose sums are kept
 
 struct VerifyArgs {
   int32_t* out_tokens;         // [T]
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
   constexpr int N = kVec ? 16 / (int)sizeof(T) : 1;
   constexpr int U = kVec ? 32 / N : 8;              // runs taken together
   __shared__ int first_refused, refused_token;
-  __shared__ long long warp_sum[kVerifyWarps], cta_sum[2][kMaxCluster];
+  __shared__ long long warp_sum[kVerifyWarps], cta_sum[2][kMaxCluster], round_sum[kVerifyWarps][kRounds];
   const int b = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q0 = __ldg(a.query_start + b), n = __ldg(a.query_start + b + 1) - q0;
@@ -232,17 +234,19 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
     long long sum = 0;
     float w[U][N];                                  // the weights taken last
 #pragma unroll 1
-    for (int i0 = w0; i0 < w1; i0 += U * kStep) {
+    for (int i0 = w0, round = 0; i0 < w1; i0 += U * kStep, ++round) {
       weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
       uint32_t hi = 0, lo = 0;
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int e = 0; e < N; ++e) add_units(w[k][e], hi, lo);
-      sum += units(hi, lo, U * N);
-    }
+      long long part = units(hi, lo, U * N);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      if (lane == 0 && round < kRounds) round_sum[warp][round] = part;
+      sum += part;
+    }
     if (lane == 0) warp_sum[warp] = sum;
     __syncthreads();
     long long mine = 0, before = 0;
@@ -281,40 +285,70 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
     }
     // ---- the place is this warp's if its sums pass the goal first --------------
     if (!((double)before <= goal && (double)(before + sum) > goal)) return;
+    // Its round by the rounds' sums, its step by the steps' (redux of the 2^-23 units
+    // and of the further ones, which stay within 32 bits), its place by a scan.
 #pragma unroll 1
-    for (int i0 = w0; i0 < w1; i0 += U * kStep) {
-      // (a part of one round still has its weights)
-      if (w1 - w0 > U * kStep) weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
+    for (int i0 = w0, round = 0; i0 < w1; i0 += U * kStep, ++round) {
+      if (round < kRounds) {
+        const long long part = round_sum[warp][round];
+        if (!((double)(before + part) > goal)) {
+          before += part;
+          continue;
+        }
+      }
+      // (the last round's weights are still held)
+      if (i0 + U * kStep < w1) weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
+      uint32_t hi[U];
+      int32_t lo[U];
+      long long step[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        uint32_t hi = 0, lo = 0;
+        uint32_t h = 0, l = 0;
 #pragma unroll
-        for (int e = 0; e < N; ++e) add_units(w[k][e], hi, lo);
-        const long long own = units(hi, lo, N);
-        long long incl = own;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const long long x = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += x;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, (double)(before + incl) > goal);
-        if (past != 0) {
-          if (lane == __ffs(past) - 1) {
-            long long s = before + incl - own;
-            int z = i0 + k * kStep + lane * N;
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              uint32_t h1 = 0, l1 = 0;
-              add_units(w[k][e], h1, l1);
-              s += units(h1, l1, 1);
-              if ((double)s <= goal) ++z;
-            }
-            a.out_tokens[q0 + kept] = z;
-          }
-          return;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        for (int e = 0; e < N; ++e) add_units(w[k][e], h, l);
+        hi[k] = h - (uint32_t)N * kHiZero;
+        lo[k] = (int32_t)(l - (uint32_t)N * kLoZero);
+        step[k] = ((long long)__reduce_add_sync(0xffffffffu, hi[k]) << 21) + __reduce_add_sync(0xffffffffu, lo[k]);
       }
+      // the step, its units and weights picked by selects
+      int at_step = -1;
+      uint32_t h0 = 0;
+      int32_t l0 = 0;
+      float v[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool here = at_step < 0 && (double)(before + step[k]) > goal;
+        if (at_step < 0 && !here) before += step[k];
+        at_step = here ? k : at_step;
+        h0 = here ? hi[k] : h0;
+        l0 = here ? lo[k] : l0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = here ? w[k][e] : v[e];
+      }
+      if (at_step < 0) continue;
+      const long long own = ((long long)h0 << 21) + l0;
+      long long incl = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, (double)(before + incl) > goal);
+      if (lane == __ffs(past) - 1) {
+        long long sofar = before + incl - own;
+        int z = i0 + at_step * kStep + lane * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          uint32_t h1 = 0, l1 = 0;
+          add_units(v[e], h1, l1);
+          sofar += units(h1, l1, 1);
+          if ((double)sofar <= goal) ++z;
+        }
+        a.out_tokens[q0 + kept] = z;
+      }
+      return;
     }
     return;
   }
