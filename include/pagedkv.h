@@ -906,14 +906,20 @@ size_t pagedkv_q4_long_workspace_bytes(int batch, int num_tokens,
 
 /* paged_attention_decode and paged_attention_multi over a 4-bit pool; arguments,
  * errors and the treatment of bad lengths, offsets and blocks as there (the rows
- * of a sequence with n_b > max_query_len are all zeroed).  The codes enter both
- * products exactly, q exactly down to 2^-27 of the largest |q| of the grouped
- * heads; a weight times V's scale is one fp16 number (2^-11 of its value, at best
- * 2^-30 of the largest weight * max(scale, |min| / 16) of the row, where one
- * below 2^-100 counts as 2^-100); scores, weights' sums and both products' sums are fp32.
- * Rows of a block past the sequence's last token may hold anything.  One or two
- * launches, asynchronous on `stream`; no atomics, so equal inputs give equal
- * bits. */
+ * of a sequence with n_b > max_query_len are all zeroed), num_kv_heads at most
+ * 65535 besides.  Scores, weights' sums and both products' sums are fp32.  Rows of a
+ * block past the sequence's last token may hold anything.  Asynchronous on `stream`;
+ * no sum's order depends on timing, so equal inputs give equal bits.
+ *
+ * Few query tokens (query tokens x grouped heads < 128, or no room in the
+ * workspace), one or two launches: the codes enter both products exactly, q exactly
+ * down to 2^-27 of the largest |q| of the grouped heads; a weight times V's scale is
+ * one fp16 number (2^-11 of its value, at best 2^-30 of the row's largest weight *
+ * max(scale, |min| / 16), where one below 2^-100 counts as 2^-100; with one of 2^e,
+ * e > 100, weights below 2^(e - 131) of the largest count as none).
+ * Long ones, three launches more: keys and values are fp16 numbers (2^-11 of their
+ * value, at best 2^-37 of the largest of their 128 rows), and so are weights (2^-11,
+ * at best 2^-30 of the row's largest weight * largest value of the 128 rows). */
 kv_status paged_attention_decode_q4(
     void *out, const void *q, const void *kv_cache,
     const int32_t *block_tables, int max_blocks_per_seq,

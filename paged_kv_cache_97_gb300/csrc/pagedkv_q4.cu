@@ -167,6 +167,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// x * 2^d: a reference may move by more octaves than one factor holds, where V's
+// scales lie far apart, and a sum of weights that is then small still counts.
+__device__ __forceinline__ float times_ex2(float x, float d) {
+  const float h = ex2(0.5f * d);
+  return x * h * h;
+}
+
 // mma16816<true> on an accumulator of zeros.
 __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -657,7 +664,6 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
               return top > 4294967296.0f || top_s > 2048.0f;
             };
             if (__any_sync(0xffffffffu, weigh())) {
-              
 #pragma unroll
               for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
@@ -672,8 +678,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
                   for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                   const float to = fmaxf(ref[nt][k], mx - 5.0f);
                   const float al = ex2(ref[nt][k] - to);
+                  l[nt][k] = times_ex2(l[nt][k], ref[nt][k] - to);
                   ref[nt][k] = to;
-                  l[nt][k] *= al;
 #pragma unroll
                   for (int gr = 0; gr < NG; ++gr) pm[nt][gr][k] *= al;
 #pragma unroll
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
         const float4 y = *reinterpret_cast<const float4*>(dump + (v * C::kCols + col) * C::kRow + e);
         const float f = ex2(ml.x - R);
         any_bad |= ml.y < 0.0f;
-        den = fmaf(f, ml.y, den);
+        den += times_ex2(ml.y, ml.x - R);
         sum.x = fmaf(f, y.x, sum.x);
         sum.y = fmaf(f, y.y, sum.y);
         sum.z = fmaf(f, y.z, sum.z);
@@ -845,61 +851,61 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
   const int4 meta = a.ws_meta[cell];
   if (meta.x == 0) return;
   for (int col = blockIdx.z; col < meta.z * a.group; col += gridDim.z) {
-  const int i = col / a.group;
-  const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
-  const int64_t p0 = (cell * 2 + 1) * cols + col;
-  auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
-  float R = kNoRef;
-  bool bad = false;
-  for (int k = lane; k < count; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
-    R = fmaxf(R, ml.x);
-    bad |= ml.y < 0.0f;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
-  bad = __any_sync(0xffffffffu, bad);
-  float num[E], den = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) num[e] = 0.0f;
-#pragma unroll 4
-  for (int k = warp; k < count; k += 4) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
-    const float f = ex2(ml.x - R);
-    den = fmaf(f, ml.y, den);
-    const float* acc = a.ws_acc + at(k) * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(acc);
-      num[0] = fmaf(f, x.x, num[0]);
-      num[1] = fmaf(f, x.y, num[1]);
-      num[2] = fmaf(f, x.z, num[2]);
-      num[3] = fmaf(f, x.w, num[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(acc);
-      num[0] = fmaf(f, x.x, num[0]);
-      num[1] = fmaf(f, x.y, num[1]);
+    const int i = col / a.group;
+    const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
+    const int64_t p0 = (cell * 2 + 1) * cols + col;
+    auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
+    float R = kNoRef;
+    bool bad = false;
+    for (int k = lane; k < count; k += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
+      R = fmaxf(R, ml.x);
+      bad |= ml.y < 0.0f;
     }
-  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
-  part[warp][lane][E] = den;
-  __syncthreads();
-  if (warp == 0) {
-  for (int k = 1; k < 4; ++k) {
+    for (int off = 16; off > 0; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
+    bad = __any_sync(0xffffffffu, bad);
+    float num[E], den = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
-    den += part[k][lane][E];
-  }
-  const float r = bad ? 0.0f : 1.0f / den;
-  uint32_t x[E / 2];
+    for (int e = 0; e < E; ++e) num[e] = 0.0f;
+#pragma unroll 4
+    for (int k = warp; k < count; k += 4) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
+      const float f = ex2(ml.x - R);
+      den += times_ex2(ml.y, ml.x - R);
+      const float* acc = a.ws_acc + at(k) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(acc);
+        num[0] = fmaf(f, x.x, num[0]);
+        num[1] = fmaf(f, x.y, num[1]);
+        num[2] = fmaf(f, x.z, num[2]);
+        num[3] = fmaf(f, x.w, num[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(acc);
+        num[0] = fmaf(f, x.x, num[0]);
+        num[1] = fmaf(f, x.y, num[1]);
+      }
+    }
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
-  __nv_bfloat16* out =
-      a.out + ((int64_t)(meta.y + i) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
-  else *reinterpret_cast<uint32_t*>(out) = x[0];
-  }
-  __syncthreads();
+    for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
+    part[warp][lane][E] = den;
+    __syncthreads();
+    if (warp == 0) {
+      for (int k = 1; k < 4; ++k) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
+        den += part[k][lane][E];
+      }
+      const float r = bad ? 0.0f : 1.0f / den;
+      uint32_t x[E / 2];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
+      __nv_bfloat16* out =
+          a.out + ((int64_t)(meta.y + i) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
+      if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
+      else *reinterpret_cast<uint32_t*>(out) = x[0];
+    }
+    __syncthreads();
   }
 }
 
@@ -992,6 +998,7 @@ kv_status q4_common(void* out, const void* q, const void* kv_cache, const int32_
     return fail(KV_ERR_INVALID_ARG, "%s: bad sizes", who);
   const int G = num_q_heads / num_kv_heads;
   if (G > kMaxGroup) return fail(KV_ERR_INVALID_ARG, "%s: at most 8 query heads per KV head (got %d)", who, G);
+  if (num_kv_heads > 65535) return fail(KV_ERR_INVALID_ARG, "%s: at most 65535 KV heads (got %d)", who, num_kv_heads);
   if (head_dim != 64 && head_dim != 128) return fail(KV_ERR_INVALID_ARG, "%s: head_dim must be 64 or 128", who);
   if (block_size != 16 && block_size != 32) return fail(KV_ERR_INVALID_ARG, "%s: block_size must be 16 or 32", who);
   if (batch == 0 || num_tokens == 0) return KV_OK;
@@ -1041,6 +1048,9 @@ kv_status q4_common(void* out, const void* q, const void* kv_cache, const int32_
   if (fit == slots && fit > 0) a.whole = 0;         // what is left has few rows
   a.ctas = a.whole ? (int)tiles : split;
   if (!a.whole) {
+    // (a CTA counts the blocks of its range in 32 bits)
+    if (tiles * ((max_seq_len + (int64_t)block_size - 1) / block_size) / split >= (int64_t)1 << 30)
+      return fail(KV_ERR_INVALID_ARG, "%s: more than 2^30 blocks of %d tokens per range", who, block_size);
     const size_t need = q4_workspace(a.ctas, num_kv_heads, nt, head_dim);
     if (!workspace || workspace_bytes < need || !aligned16(workspace))
       return fail(KV_ERR_INVALID_ARG,

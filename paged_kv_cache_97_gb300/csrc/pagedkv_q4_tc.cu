@@ -44,6 +44,7 @@ constexpr int kThreadsTc = (kSoftmaxWarps + 3) * 32;
 constexpr int kTmemCols = 512;            // the whole TMEM: one CTA per SM
 constexpr float kSlack = 8.0f;            // octaves a row may pass its reference by
 constexpr float kHead = 5.0f;             // octaves above 1 a reference leaves p
+constexpr float kFar = 100.0f;            // octaves below its reference where a weight is summed by itself
 
 template <int D>
 struct Img {
@@ -155,8 +156,9 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
     if ((threadIdx.x & 31) == 0) atomicMax(&top[x], u);
   }
   __syncthreads();
-  // value * 2^-e is at most [2^12, 2^13); -80 keeps the sums of p / 2^E within fp32
-  const int e = min(max((int)(top[x] >> 23) - 127 - 12, -80), 100);
+  // value * 2^-e is at most [2^12, 2^13) (|value| < 2^128); -80 keeps the sums of
+  // p / 2^E within fp32
+  const int e = min(max((int)(top[x] >> 23) - 127 - 12, -80), 115);
   const int64_t cell = ((int64_t)slot * a.num_kv_heads + hk) * a.chunks + c;
   if ((threadIdx.x & 127) == 0) reinterpret_cast<int*>(a.exps + cell)[x] = e;
   const float f = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -541,6 +543,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
             const float mx_raw = masked ? half_max<true>(raw, first, lim) : half_max<false>(raw, first, lim);
             const float mx = mx_raw == -INFINITY ? -INFINITY : fmaf(mx_raw, kf, ev - kHead);
             const bool need = m_ref == -INFINITY ? mx > -INFINITY : mx > m_ref + kSlack;
+            // V's magnitudes may lie further apart than fp32's exponents: p of rows of
+            // small values is then nothing while its weight 2^(s - m) still counts.
+            const bool far = mx > -INFINITY && mx < m_ref - kFar;
+            if (__any_sync(0xffffffffu, far)) {
+              const float by = m_ref == -INFINITY ? 0.0f : m_ref;
+              float sum = 0.0f;
+#pragma unroll 1
+              for (int c0 = 0; c0 < 64; c0 += 16) {
+                uint32_t sv[16];
+                tmem_ld16(s_tmem + 64 * ps + c0, sv);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  sum += first + c0 + j <= lim ? ex2(fmaf(__uint_as_float(sv[j]), kf, -by)) : 0.0f;
+              }
+              if (far) l += sum;
+            }
             if (__any_sync(0xffffffffu, need)) {
               const float k = (need && m_ref != -INFINITY) ? ceilf(mx - m_ref) : 0.0f;
               const float m_new = !need ? m_ref : (m_ref == -INFINITY ? mx : m_ref + k);
@@ -578,12 +597,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
                 lsum *= alpha;
               }
               tmem_wait_st();
-              l *= alpha;
+              if (need) l = m_ref == -INFINITY ? 0.0f : ldexpf(l, -(int)k);
               m_ref = m_new;
             }
             const float add = m_ref == -INFINITY ? 0.0f : ev - m_ref;
             uint32_t pw[32];
-            lsum += masked ? half_exp<true>(raw, pw, first, lim, kf, add) : half_exp<false>(raw, pw, first, lim, kf, add);
+            const float part =
+                masked ? half_exp<true>(raw, pw, first, lim, kf, add) : half_exp<false>(raw, pw, first, lim, kf, add);
+            if (!far) lsum += part;
             tmem_st32(s_tmem + 32 * ps, pw);
           }
           if (!ok) break;

@@ -173,9 +173,12 @@ def attention(rows, q, scale, positions, wide=False):
     15 for its code) per token.
 
     ``wide``: keys and values enter the products as fp16 numbers (2^-11 of their
-    value, at best 2^-37 of the largest of their 128 rows, which the other terms
-    cover), the weight alone as one: 2^-11 of S_abs in the scores, of sum w |V|
-    twice in the sum, and the floor counts the weight times the largest |V|."""
+    value), the weight alone as one: 2^-11 of S_abs in the scores, of sum w |V|
+    twice in the sum.  A weight is p = w 2^E M, E the exponent that brings the 128 rows'
+    largest |V|, top, into [2^12, 2^13) (-80 at least, as if top were 2^-67), and
+    the row's largest p is 2^5 at least: half a step of the smallest fp16, 2^-25, is
+    2^-30 of it.  Times |V| / 2^E < 2^13, and with 2^E <= top / 2^12, a token is off by at
+    most 2^-29 max(w top).  Half a step of a value, 2^-25 2^E <= 2^-37 top, is less."""
     (kc, ks, km), (vc, vs, vm) = rows
     H, L, d = kc.shape
     n, hq, _ = q.shape
@@ -196,8 +199,9 @@ def attention(rows, q, scale, positions, wide=False):
     floor = 2.0 ** -30 * 15 * L * (w[..., None] * vs.amax(-1)[None, :, None, :, None]).amax(dim=3)
     tol = 2.0 ** -8 * out.abs() + 2.0 ** -11 * part + moved + 2.0 ** -14 * mag + floor
     if wide:
-        largest = (vm.abs() + 15 * vs).amax(-1)
-        tol = tol + 2.0 ** -10 * mag + 2.0 ** -30 * L * (w * largest[None, :, None]).amax(-1)[..., None]
+        top = (vm.abs() + 15 * vs).amax(-1)
+        top = torch.cat([x.amax(1, keepdim=True).expand_as(x) for x in top.split(128, dim=1)], 1).clamp(min=2.0 ** -67)
+        tol = tol + 2.0 ** -10 * mag + 2.0 ** -29 * L * (w * top[None, :, None]).amax(-1)[..., None]
     return out.reshape(n, hq, d), tol.reshape(n, hq, d)
 
 

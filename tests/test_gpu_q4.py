@@ -457,6 +457,34 @@ def test_mixed_v_scales(pkv):
     check(decode(pkv, pool, q, 0.1), pool, q, [1, 1], 0.1)
 
 
+@pytest.mark.parametrize("block,dim", SHAPES)
+@pytest.mark.parametrize("n,room", [(1, None), (6, None), (150, None), (150, -1)])
+@pytest.mark.parametrize("L", [300, 900])
+@pytest.mark.parametrize("small_first", [True, False])
+def test_values_far_apart(pkv, block, dim, n, room, L, small_first):
+    """Tokens with nearly all of the weight and values of 2^-100 beside tokens of
+    nearly no weight and values of 2^100: the weights' sum is the first ones' although
+    the products' reference is the second ones'."""
+    def split(small, large):
+        def factor(shape, g):
+            at = torch.arange(shape[0])[:, None, None, None] * block + torch.arange(block)[:, None]
+            return torch.where((at < L // 2) == small_first, small, large).expand(shape)
+        return factor
+    # positive keys: the first kind's scores are 8 to 25, the others' within 0.03
+    pool = ref.Pool4([L], 2, dim, block, seed=31, low=0.0, kscale=split(1.0, 1e-3), vscale=split(2.0 ** -100, 2.0 ** 100))
+    q = torch.ones(n, 8, dim, dtype=torch.bfloat16)
+    scale = 6.4 / dim
+    got = decode(pkv, pool, q, scale) if n == 1 else multi(pkv, pool, q, [n], scale, room=room)
+    check(got, pool, q, [n], scale, wide=True)    # (the smaller workspace has room for one as well)
+
+
+def test_multi_tensor_cores_largest_values(pkv):
+    """Values up to nearly the format's 2^126."""
+    pool = ref.Pool4([300], 1, 64, 16, seed=32, vscale=lambda shape, g: 2.0 ** 123)
+    q = pool.randn(50, 4, 64)
+    check(multi(pkv, pool, q, [50], 0.125, room=-1), pool, q, [50], 0.125, wide=True)
+
+
 def test_rows_of_equal_values(pkv):
     """Zero rows and constant rows have the least scale there is."""
     x = torch.zeros((600, 2, 64), dtype=torch.bfloat16)
@@ -524,6 +552,14 @@ def test_faults_are_flagged(pkv):
         assert (out[9:] == 7).all()                 # offsets past the rows: left as they are
         want, tol = ref.attention(pool.rows(3, 200), q[6:9], 0.125, torch.arange(197, 200))
         within(out[6:9], want, tol)
+
+
+def test_ranges_are_counted_in_32_bits(pkv):
+    """A call whose ranges might pass 2^30 blocks is refused (and nothing is launched)."""
+    p = torch.zeros(16, dtype=torch.uint8, device="cuda").data_ptr()
+    st = pkv.load().paged_attention_multi_q4(p, p, p, p, 1 << 26, p, p, 2, 1 << 22, 40, 65535, 65535, 64, 64, 16, 1 << 30,
+                                             0.1, None, 0, None)
+    assert st == pkv.KV_ERR_INVALID_ARG and "2^30" in pkv.load().pagedkv_last_error().decode()
 
 
 def test_blocks_past_4_gib(pkv):

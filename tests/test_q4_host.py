@@ -70,10 +70,12 @@ REFUSED = (
         dict(num_blocks=0), dict(block_size=8), dict(num_kv_heads=0), dict(head_dim=96)]] +
     [("paged_attention_decode_q4", DECODE, c) for c in [g for g in GEOMETRY if not {"num_tokens", "max_query_len"} & set(g)] + [
         dict(out=None), dict(q=None), dict(kv_cache=None), dict(out=ODD), dict(q=ODD), dict(kv_cache=ODD),
-        dict(num_q_heads=7), dict(num_q_heads=18), dict(max_seq_len=0)]] +
+        dict(num_q_heads=7), dict(num_q_heads=18), dict(max_seq_len=0),
+        dict(num_q_heads=65536, num_kv_heads=65536)]] +
     [("paged_attention_multi_q4", MULTI, c) for c in GEOMETRY + [
         dict(out=None), dict(q=None), dict(kv_cache=None), dict(out=ODD), dict(q=ODD), dict(kv_cache=ODD),
-        dict(num_q_heads=7), dict(num_q_heads=18), dict(max_seq_len=0), dict(query_start=None)]] +
+        dict(num_q_heads=7), dict(num_q_heads=18), dict(max_seq_len=0), dict(query_start=None),
+        dict(num_q_heads=65536, num_kv_heads=65536)]] +
     [("pagedkv_verify_drafts", VERIFY, c) for c in [
         dict(batch=-1), dict(num_tokens=-1), dict(max_query_len=0), dict(vocab=0), dict(vocab=1 << 19), dict(dtype=3),
         dict(dtype=-1), dict(out_tokens=None), dict(num_accepted=None), dict(tokens=None), dict(target=None),
