@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   __shared__ int scan[32];
   __shared__ int sh_unit, sh_slot, sh_pr, sh_fail;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int Hkv = a.num_kv_heads, GQ = a.group, Hq = Hkv * GQ;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   unsigned char* gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -423,65 +423,66 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     tc_fence_after();
     if (alloc_now) {
       tm_held = true;
-      tm = tmem_base;
+      tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     }
     float m_ref = -INFINITY, l = 0.0f;
 
     if (nch > 0) {
       if (warp == kMmaWarp) {
-        // One lane issues.  Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage
-        // free], S_1(c+1), [K stage free]: one tile's softmax runs beside the other
-        // tile's products.  (S_g(c+1) overwrites the columns that P . V_g(c) reads;
-        // the MMAs of one issuing thread run in order.)
-        if (lane == 0) {
-          bool ok = true;
-          const uint32_t id_s = mma_idesc<true>(kRows, kChunk, 0), id_o = mma_idesc<true>(kRows, D, 1);
-          auto issue_s = [&](int g, int c) {
-            const uint32_t kb = k_img(c % kKStages);
+        // Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage free], S_1(c+1), [K
+        // stage free]: one tile's softmax runs beside the other tile's products.
+        // (S_g(c+1) overwrites the columns that P . V_g(c) reads; the MMAs of one
+        // issuing thread run in order.)
+        bool ok = true;
+        const uint32_t id_s = mma_idesc<true>(kRows, kChunk, 0), id_o = mma_idesc<true>(kRows, D, 1);
+        auto issue_s = [&](int g, int c) {
+          const uint64_t qd = smem_desc(q_img(g), 16, 1024), kd = smem_desc(k_img(c % kKStages), 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              mma_ss(tm + I::scol(g), smem_desc(q_img(g) + (ks / 4) * (kRows * 128) + (ks % 4) * 32, 16, 1024),
-                     smem_desc(kb + (ks / 4) * (kChunk * 128) + (ks % 4) * 32, 16, 1024), id_s, ks > 0);
-            mma_commit(smem_addr(&s_full[g]));
-          };
-          auto issue_pv = [&](int g, int c, int nsub) {
-            const uint32_t vb = v_img(c % kVStages);
-            for (int kk = 0; kk < nsub; ++kk)
-              mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, smem_desc(vb + kk * (16 * 128), kChunk * 128, 1024),
-                     id_o, (c > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(smem_addr(&o_done[g]));
-          };
-          if (mbar_wait(smem_addr(&k_full[0]), 0)) {
-            tc_fence_after();
-            issue_s(0, 0);
-            if (live1) issue_s(1, 0);
-            mma_commit(smem_addr(&k_empty[0]));
-          } else {
-            ok = false;
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const int at = ((ks / 4) * (kRows * 128) + (ks % 4) * 32) / 16;
+            warp_mma_ss(tm + I::scol(g), qd + at, kd + at, id_s, ks > 0);
           }
-          for (int c = 0; c < nch && ok; ++c) {
-            const int vs = c % kVStages, ks1 = (c + 1) % kKStages;
-            if (!mbar_wait(smem_addr(&v_full[vs]), (c / kVStages) & 1)) { ok = false; break; }
-            const int nsub = (min(t_end - c * kChunk, kChunk) + 15) / 16;
-            const bool next = c + 1 < nch;
-            if (!mbar_wait(smem_addr(&p_full[0]), c & 1)) { ok = false; break; }
-            if (next && !mbar_wait(smem_addr(&k_full[ks1]), ((c + 1) / kKStages) & 1)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(0, c, nsub);
-            if (next) issue_s(0, c + 1);
-            if (live1) {
-              if (!mbar_wait(smem_addr(&p_full[1]), c & 1)) { ok = false; break; }
-              tc_fence_after();
-              issue_pv(1, c, nsub);
-            }
-            mma_commit(smem_addr(&v_empty[vs]));
-            if (next) {
-              if (live1) issue_s(1, c + 1);
-              mma_commit(smem_addr(&k_empty[ks1]));
-            }
-          }
-          if (!ok) sh_fail = 1;
+          warp_mma_commit(smem_addr(&s_full[g]));
+        };
+        auto issue_pv = [&](int g, int c, int nsub) {
+          const uint64_t vd = smem_desc(v_img(c % kVStages), kChunk * 128, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 16; ++kk)
+            if (kk < nsub)
+              warp_mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, vd + kk * (16 * 128 / 16), id_o,
+                          (c > 0 || kk > 0) ? 1u : 0u);
+          warp_mma_commit(smem_addr(&o_done[g]));
+        };
+        if (warp_wait(smem_addr(&k_full[0]), 0)) {
+          tc_fence_after();
+          issue_s(0, 0);
+          if (live1) issue_s(1, 0);
+          warp_mma_commit(smem_addr(&k_empty[0]));
+        } else {
+          ok = false;
         }
+        for (int c = 0; c < nch && ok; ++c) {
+          const int vs = c % kVStages, ks1 = (c + 1) % kKStages;
+          if (!warp_wait(smem_addr(&v_full[vs]), (c / kVStages) & 1)) { ok = false; break; }
+          const int nsub = (min(t_end - c * kChunk, kChunk) + 15) / 16;
+          const bool next = c + 1 < nch;
+          if (!warp_wait(smem_addr(&p_full[0]), c & 1)) { ok = false; break; }
+          if (next && !warp_wait(smem_addr(&k_full[ks1]), ((c + 1) / kKStages) & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(0, c, nsub);
+          if (next) issue_s(0, c + 1);
+          if (live1) {
+            if (!warp_wait(smem_addr(&p_full[1]), c & 1)) { ok = false; break; }
+            tc_fence_after();
+            issue_pv(1, c, nsub);
+          }
+          warp_mma_commit(smem_addr(&v_empty[vs]));
+          if (next) {
+            if (live1) issue_s(1, c + 1);
+            warp_mma_commit(smem_addr(&k_empty[ks1]));
+          }
+        }
+        if (!ok) sh_fail = 1;
         __syncwarp();
       } else if (warp == kKWarp || warp == kVWarp) {
         // one lane per operand: chunk c into stage c % stages once the MMAs are done with it
@@ -619,11 +620,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       }
     }
     __syncthreads();
-    if (nch > 0 && warp == kMmaWarp && lane == 0) {
+    if (nch > 0 && warp == kMmaWarp) {
       // all tensor-core work of this CTA completes before TMEM is read or freed
       tc_fence_after();
-      mma_commit(smem_addr(&drain_bar));
-      if (!mbar_wait(smem_addr(&drain_bar), 0)) sh_fail = 1;
+      warp_mma_commit(smem_addr(&drain_bar));
+      if (!warp_wait(smem_addr(&drain_bar), 0)) sh_fail = 1;
     }
     __syncthreads();
     const bool have = nch > 0 && sh_fail == 0;
