@@ -40,7 +40,8 @@ constexpr int kChunk = 128;               // keys per chunk
 constexpr int kKStages = 2, kVStages = 3; // V is released later than K
 constexpr int kSoftmaxWarps = 4 * kTiles; // one row per thread
 constexpr int kMmaWarp = kSoftmaxWarps, kKWarp = kMmaWarp + 1, kVWarp = kMmaWarp + 2;
-constexpr int kThreadsTc = (kSoftmaxWarps + 3) * 32;
+constexpr int kUnitWarp = kMmaWarp + 3;
+constexpr int kThreadsTc = (kUnitWarp + 1) * 32;
 constexpr int kTmemCols = 512;            // the whole TMEM: one CTA per SM
 constexpr float kSlack = 8.0f;            // octaves a row may pass its reference by
 constexpr float kHead = 5.0f;             // octaves above 1 a reference leaves p
@@ -277,15 +278,33 @@ __device__ __forceinline__ void bulk_image(uint32_t dst, const void* src, uint32
       : "memory");
 }
 
+// A unit of work: 256 rows of a sequence and KV head.
+struct Unit {
+  int chunks;                  // of keys; 0: a bad sequence, its rows are zeroed; -1: no more units
+  int keys;                    // that the last row sees
+  int row0, rows;              // first row; rows of the sequence
+  int q0, before;              // first query token's row of q; keys before the first query's own
+  int head, cell;              // KV head; slot * heads + head
+
+  __device__ __forceinline__ bool live(int tile) const { return row0 + tile * kRows < rows; }
+};
+
+// Roles: warps 0-7 softmax (four per row tile), then one each for the MMAs, K's
+// and V's images, and the units.  Every role walks the same units at its own pace:
+// K and V of the next unit are loaded, and its first scores made, beside the end
+// of the last.  Waits are bounded; a role whose wait gives up sets sh_fail and
+// leaves, the others' waits then give up as well, and the units in hand stay
+// unwritten (flagged).
 template <int D>
 __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a) {
   using I = Img<D>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  __shared__ uint64_t s_full[kTiles], p_full[kTiles], o_done[kTiles], drain_bar;
+  __shared__ uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], o_done[kTiles], o_free[kTiles];
+  __shared__ uint64_t unit_full, unit_empty, drain_bar;
   __shared__ uint32_t tmem_base;
-  __shared__ int scan[32];
-  __shared__ int sh_unit, sh_slot, sh_pr, sh_fail;
+  __shared__ Unit sh_unit;
+  __shared__ int sh_fail;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int Hkv = a.num_kv_heads, GQ = a.group, Hq = Hkv * GQ;
@@ -294,15 +313,66 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   auto q_img = [&](int g) { return base + (uint32_t)(g * I::kBytes); };
   auto k_img = [&](int s) { return base + (uint32_t)((kTiles + s) * I::kBytes); };
   auto v_img = [&](int s) { return base + (uint32_t)((kTiles + kKStages + s) * I::kBytes); };
-  auto pairs_of = [&](int slot) {
-    const int b = a.list[slot];
-    return ((a.query_start[b + 1] - a.query_start[b]) * GQ + kTiles * kRows - 1) / (kTiles * kRows);
-  };
-  // units: (pair of row tiles, KV head); pairs per listed sequence, summed by warp 0
+
   const int count = a.counters[0];
-  const int per = (count + 31) / 32;
-  int mine = 0;
+  if (count == 0) return;
+  if (tid == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(smem_addr(&k_full[s]), 1);
+      mbar_init(smem_addr(&k_empty[s]), 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(smem_addr(&v_full[s]), 1);
+      mbar_init(smem_addr(&v_empty[s]), 1);
+    }
+    for (int g = 0; g < kTiles; ++g) {
+      mbar_init(smem_addr(&q_full[g]), kRows);
+      mbar_init(smem_addr(&s_full[g]), 1);
+      mbar_init(smem_addr(&p_full[g]), kRows);
+      mbar_init(smem_addr(&o_done[g]), 1);
+      mbar_init(smem_addr(&o_free[g]), kRows);
+    }
+    mbar_init(smem_addr(&unit_full), 1);
+    mbar_init(smem_addr(&unit_empty), kUnitWarp);   // the other roles' warps
+    mbar_init(smem_addr(&drain_bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    sh_fail = 0;
+  }
   if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(&tmem_base)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+
+  bool ok = true;
+  int taken = 0;                                    // units read
+  // The next unit (whole warp); chunks == -1 also after a wait that gave up.
+  auto next_unit = [&]() {
+    Unit u;
+    u.chunks = -1;
+    ok = warp_wait(smem_addr(&unit_full), taken & 1);
+    if (ok) {
+      u = sh_unit;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&unit_empty));
+      ++taken;
+    }
+    return u;
+  };
+
+  if (warp == kUnitWarp) {
+    // Units are taken as CTAs become free, one ahead of the roles; the last pairs
+    // of the last sequence (which see the most keys) first.
+    auto pairs_of = [&](int slot) {
+      const int b = a.list[slot];
+      return ((a.query_start[b + 1] - a.query_start[b]) * GQ + kTiles * kRows - 1) / (kTiles * kRows);
+    };
+    const int per = (count + 31) / 32;
+    int mine = 0;
     for (int i = 0; i < per; ++i)
       if (lane * per + i < count) mine += pairs_of(lane * per + i);
     int incl = mine;
@@ -311,221 +381,263 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       const int v = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += v;
     }
-    scan[lane] = incl;
-  }
-  __syncthreads();
-  const int pairs = scan[31];
-  const long long units = (long long)pairs * Hkv;
-  bool tm_held = false;
-  uint32_t tm = 0;
-
-  for (;;) {
-    __syncthreads();                                // the last unit's readers are done
-    // Units are taken as CTAs become free; the last pairs of the last sequence
-    // (which see the most keys) first.
-    if (tid == 0) {
-      sh_unit = atomicAdd(&a.counters[1], 1);
-      sh_fail = 0;
+    const int pairs = __shfl_sync(0xffffffffu, incl, 31);
+    const long long units = (long long)pairs * Hkv;
+    for (;; ++taken) {
+      int u = 0;
+      if (lane == 0) u = atomicAdd(&a.counters[1], 1);
+      u = __shfl_sync(0xffffffffu, u, 0);
+      Unit x = {};
+      x.chunks = -1;
+      if (u < units) {
+        const int at = pairs - 1 - u / Hkv;
+        int slot = 0, pr = 0;
+        const bool here = at >= incl - mine && at < incl;
+        if (here) {
+          int acc = incl - mine;
+          for (slot = lane * per;; ++slot) {
+            const int pl = pairs_of(slot);
+            if (at < acc + pl) break;
+            acc += pl;
+          }
+          pr = at - acc;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        slot = __shfl_sync(0xffffffffu, slot, src);
+        pr = __shfl_sync(0xffffffffu, pr, src);
+        const int b = a.list[slot], n = a.query_start[b + 1] - a.query_start[b];
+        x.head = u % Hkv;
+        x.cell = slot * Hkv + x.head;
+        x.q0 = a.query_start[b];
+        x.before = a.seq_lens[b] - n;
+        x.rows = n * GQ;
+        x.row0 = pr * (kTiles * kRows);
+        const int last = min(x.row0 + kTiles * kRows, x.rows) - 1;
+        x.keys = x.before + last / GQ + 1;          // keys the last row sees
+        x.chunks = a.bad[slot] != 0 ? 0 : (x.keys + kChunk - 1) / kChunk;
+        // its queries into L2
+        for (int t = x.row0 / GQ + lane; t <= last / GQ; t += 32) {
+          const __nv_bfloat16* row = a.q + ((int64_t)(x.q0 + t) * Hq + (int64_t)x.head * GQ) * D;
+          for (int e = 0; e < GQ * D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + e));
+        }
+      }
+      if (taken > 0 && !warp_wait(smem_addr(&unit_empty), (taken - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        sh_unit = x;
+        mbar_arrive(smem_addr(&unit_full));
+      }
+      __syncwarp();
+      if (x.chunks < 0) break;
     }
-    __syncthreads();
-    const int u = sh_unit;
-    if (u >= units) break;
-    const int hk = u % Hkv, x = pairs - 1 - u / Hkv;
-    if (warp == 0 && x >= scan[lane] - mine && x < scan[lane]) {
-      int acc = scan[lane] - mine;
-      for (int i = 0; i < per; ++i) {
-        const int slot = lane * per + i;
-        if (slot >= count) break;
-        const int pl = pairs_of(slot);
-        if (x < acc + pl) {
-          sh_slot = slot;
-          sh_pr = x - acc;
+  } else if (warp == kMmaWarp) {
+    // Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage free], S_1(c+1), [K
+    // stage free]: one tile's softmax runs beside the other tile's products.
+    // (S_g(c+1) overwrites the columns that P . V_g(c) reads; the MMAs of one
+    // issuing thread run in order.)  Where a unit ends, both tiles' P . V come
+    // before the next unit's scores, which wait for its queries.
+    const uint32_t id_s = mma_idesc<true>(kRows, kChunk, 0), id_o = mma_idesc<true>(kRows, D, 1);
+    int kc = 0, vc = 0;                             // chunks of K and V used
+    int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;         // units and chunks of each tile
+    auto issue_s = [&](int g) {
+      const uint64_t qd = smem_desc(q_img(g), 16, 1024), kd = smem_desc(k_img(kc % kKStages), 16, 1024);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int at = ((ks / 4) * (kRows * 128) + (ks % 4) * 32) / 16;
+        warp_mma_ss(tm + I::scol(g), qd + at, kd + at, id_s, ks > 0);
+      }
+      warp_mma_commit(smem_addr(&s_full[g]));
+    };
+    auto issue_pv = [&](int g, bool first, int nsub) {
+      const uint64_t vd = smem_desc(v_img(vc % kVStages), kChunk * 128, 1024);
+#pragma unroll
+      for (int kk = 0; kk < kChunk / 16; ++kk)
+        if (kk < nsub)
+          warp_mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, vd + kk * (16 * 128 / 16), id_o,
+                      (!first || kk > 0) ? 1u : 0u);
+      warp_mma_commit(smem_addr(&o_done[g]));
+    };
+    auto wait_k = [&]() { return warp_wait(smem_addr(&k_full[kc % kKStages]), (kc / kKStages) & 1); };
+    // the first scores of a unit
+    auto begin = [&](const Unit& u) {
+      if (!wait_k() || !warp_wait(smem_addr(&q_full[0]), nq0 & 1)) return false;
+      ++nq0;
+      tc_fence_after();
+      issue_s(0);
+      if (u.live(1)) {
+        if (!warp_wait(smem_addr(&q_full[1]), nq1 & 1)) return false;
+        ++nq1;
+        tc_fence_after();
+        issue_s(1);
+      }
+      warp_mma_commit(smem_addr(&k_empty[kc % kKStages]));
+      ++kc;
+      return true;
+    };
+    auto next_of = [&]() {
+      Unit u = next_unit();
+      while (u.chunks == 0) u = next_unit();
+      return u;
+    };
+    Unit u = next_of();
+    if (u.chunks > 0) ok = begin(u);
+    while (ok && u.chunks > 0) {
+      const bool live1 = u.live(1);
+      for (int c = 0; c < u.chunks; ++c) {
+        const int nsub = (min(u.keys - c * kChunk, kChunk) + 15) / 16;
+        const bool more = c + 1 < u.chunks;
+        ok = warp_wait(smem_addr(&v_full[vc % kVStages]), (vc / kVStages) & 1) &&
+             warp_wait(smem_addr(&p_full[0]), np0 & 1) && (!more || wait_k());
+        // (the last unit's O is read)
+        if (ok && c == 0 && nq0 > 1) ok = warp_wait(smem_addr(&o_free[0]), nq0 & 1);
+        if (!ok) break;
+        ++np0;
+        tc_fence_after();
+        issue_pv(0, c == 0, nsub);
+        if (more) issue_s(0);
+        if (live1) {
+          ok = warp_wait(smem_addr(&p_full[1]), np1 & 1);
+          if (ok && c == 0 && nq1 > 1) ok = warp_wait(smem_addr(&o_free[1]), nq1 & 1);
+          if (!ok) break;
+          ++np1;
+          tc_fence_after();
+          issue_pv(1, c == 0, nsub);
+        }
+        warp_mma_commit(smem_addr(&v_empty[vc % kVStages]));
+        ++vc;
+        if (more) {
+          if (live1) issue_s(1);
+          warp_mma_commit(smem_addr(&k_empty[kc % kKStages]));
+          ++kc;
+        }
+      }
+      if (!ok) break;
+      u = next_of();
+      if (ok && u.chunks > 0) ok = begin(u);
+    }
+    // all tensor-core work of this CTA completes before TMEM is freed
+    tc_fence_after();
+    warp_mma_commit(smem_addr(&drain_bar));
+    if (!warp_wait(smem_addr(&drain_bar), 0)) ok = false;
+  } else if (warp == kKWarp || warp == kVWarp) {
+    // one lane copies: chunk i into stage i % stages once the MMAs are done with it
+    const bool is_k = warp == kKWarp;
+    const int nst = is_k ? kKStages : kVStages;
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    int i = 0;
+    for (Unit u = next_unit(); ok && u.chunks >= 0; u = next_unit()) {
+      const unsigned char* src = a.images + ((int64_t)u.cell * a.chunks * 2 + (is_k ? 0 : 1)) * I::kBytes;
+      for (int c = 0; c < u.chunks; ++c, ++i) {
+        const int st = i % nst;
+        if (i >= nst && !warp_wait(smem_addr(&empty[st]), (i / nst - 1) & 1)) {
+          ok = false;
           break;
         }
-        acc += pl;
+        if (lane == 0)
+          bulk_image(is_k ? k_img(st) : v_img(st), src + (int64_t)c * 2 * I::kBytes, I::kBytes, smem_addr(&full[st]));
       }
+      if (!ok) break;
     }
-    __syncthreads();
-    const int slot = sh_slot, pr = sh_pr, b = a.list[slot];
-    const int q0 = a.query_start[b], n = a.query_start[b + 1] - q0, L = a.seq_lens[b];
-    const bool bad = a.bad[slot] != 0;
-    const int rows_b = n * GQ, row0 = pr * (kTiles * kRows);
-    const bool live1 = row0 + kRows < rows_b;       // tile 1 holds rows
-    const int last_row = min(row0 + kTiles * kRows, rows_b) - 1;
-    const int t_end = L - n + last_row / GQ + 1;    // keys the last row sees
-    const int nch = bad ? 0 : (t_end + kChunk - 1) / kChunk;
-    const int64_t cell = ((int64_t)slot * Hkv + hk) * a.chunks;
-    const int tile = warp >> 2, ri = tid & (kRows - 1);
-    const int r = row0 + tile * kRows + ri;         // (warps 0-7) this thread's row
-    const bool row_valid = warp < kSoftmaxWarps && r < rows_b;
-    const int pos = row_valid ? L - n + r / GQ : -1;
-    const int64_t qrow = row_valid ? (int64_t)(q0 + r / GQ) * Hq + (int64_t)hk * GQ + r % GQ : 0;
-    // Q row as fp16 under a power of two (largest in [2^13, 2^14)) into its tile's
-    // swizzled bands.  A negative scale turns its sign, a zero one takes it as 0.
-    float sl2 = 0.0f;
-    if (warp < kSoftmaxWarps) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * D);
-      uint4 qv[D / 8];
+    // every copy has landed before the CTA ends (normally already so)
+    for (int st = 0; st < nst && st < i; ++st) warp_wait(smem_addr(&full[st]), ((i - 1 - st) / nst) & 1);
+  } else {
+    const int tile = warp >> 2, wrow = (warp & 3) * 32, ri = wrow + lane;   // this thread's row of the tile
+    const uint32_t lane_base = (uint32_t)wrow << 16;
+    const uint32_t s_tmem = tm + lane_base + I::scol(tile), o_tmem = tm + lane_base + I::ocol(tile);
+    // The warp's 32 rows of q as fp16, each under a power of two (largest in [2^13,
+    // 2^14)), into the tile's swizzled bands; returns what this thread's own row
+    // multiplies the scores by.  A negative scale turns q's sign, a zero one takes it as 0.
+    auto load_q = [&](const Unit& u) {
+      constexpr int kLanes = D / 8, kEach = 32 / kLanes, kTurns = 32 / kEach;   // lanes of a row, rows of a load
+      const int part = lane % kLanes, sub = lane / kLanes;
+      const int r0 = u.row0 + tile * kRows + wrow + sub;
+      uint4 qv[kTurns];
+      {
+        int tok = r0 / GQ, h = r0 - tok * GQ;
+        const int dtok = kEach / GQ, dh = kEach - dtok * GQ;
+        const __nv_bfloat16* from = a.q + (int64_t)u.head * GQ * D + part * 8;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) qv[c] = row_valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t top = 0;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = w4[i] & 0x7fffu, hi = w4[i] >> 16 & 0x7fffu;
-          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        for (int i = 0; i < kTurns; ++i) {
+          qv[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r0 + i * kEach < u.rows)
+            qv[i] = __ldg(reinterpret_cast<const uint4*>(from + ((int64_t)(u.q0 + tok) * Hq + h) * D));
+          h += dh;
+          tok += dtok;
+          if (h >= GQ) {
+            h -= GQ;
+            ++tok;
+          }
         }
       }
-      const int e = min(max(top > 0 ? 140 - (int)(top >> 7) : 0, -110), 110);
-      float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      sl2 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
-      if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
-      unsigned char* qdst = gbase + (q_img(tile) - base);
+      // (the rows' steps side by side: a chain of shuffles per row would wait on itself)
+      uint32_t top[kTurns];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t w4[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+      for (int i = 0; i < kTurns; ++i) {
+        const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        top[i] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = w4[k] & 0x7fffu, hi = w4[k] >> 16 & 0x7fffu;
+          top[i] = max(top[i], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+      }
+#pragma unroll
+      for (int off = 1; off < kLanes; off <<= 1) {
+        uint32_t x[kTurns];
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) x[i] = __shfl_xor_sync(0xffffffffu, top[i], off);
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) top[i] = max(top[i], x[i]);
+      }
+      uint32_t own = 0;                             // the largest of this thread's own row
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const uint32_t theirs = __shfl_sync(0xffffffffu, top[i], lane % kEach * kLanes);
+        if (lane / kEach == i) own = theirs;
+      }
+      auto exponent = [](uint32_t x) { return min(max(x > 0 ? 140 - (int)(x >> 7) : 0, -110), 110); };
+      unsigned char* to = gbase + (q_img(tile) - base) + (part / 8) * (kRows * 128);
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        float up = __uint_as_float((uint32_t)(127 + exponent(top[i])) << 23);
+        if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
         uint32_t o4[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o4[i] = pack2<true>(__uint_as_float(w4[i] << 16) * up, __uint_as_float(w4[i] & 0xffff0000u) * up);
-        *reinterpret_cast<uint4*>(qdst + (c / 8) * (kRows * 128) + sw128(ri, c % 8)) =
-            make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        for (int k = 0; k < 4; ++k)
+          o4[k] = pack2<true>(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xffff0000u) * up);
+        *reinterpret_cast<uint4*>(to + sw128(wrow + i * kEach + sub, part % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
       }
-    }
-    if (tid == 0) {
-      for (int s = 0; s < kKStages; ++s) {
-        mbar_init(smem_addr(&k_full[s]), 1);
-        mbar_init(smem_addr(&k_empty[s]), 1);
-      }
-      for (int s = 0; s < kVStages; ++s) {
-        mbar_init(smem_addr(&v_full[s]), 1);
-        mbar_init(smem_addr(&v_empty[s]), 1);
-      }
-      for (int g = 0; g < kTiles; ++g) {
-        mbar_init(smem_addr(&s_full[g]), 1);
-        mbar_init(smem_addr(&p_full[g]), kRows);
-        mbar_init(smem_addr(&o_done[g]), 1);
-      }
-      mbar_init(smem_addr(&drain_bar), 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    const bool alloc_now = nch > 0 && !tm_held;
-    if (alloc_now && warp == 0) {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                   ::"r"(smem_addr(&tmem_base)), "r"(kTmemCols) : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // Q images -> tensor core
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (alloc_now) {
-      tm_held = true;
-      tm = __shfl_sync(0xffffffffu, tmem_base, 0);
-    }
-    float m_ref = -INFINITY, l = 0.0f;
-
-    if (nch > 0) {
-      if (warp == kMmaWarp) {
-        // Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage free], S_1(c+1), [K
-        // stage free]: one tile's softmax runs beside the other tile's products.
-        // (S_g(c+1) overwrites the columns that P . V_g(c) reads; the MMAs of one
-        // issuing thread run in order.)
-        bool ok = true;
-        const uint32_t id_s = mma_idesc<true>(kRows, kChunk, 0), id_o = mma_idesc<true>(kRows, D, 1);
-        auto issue_s = [&](int g, int c) {
-          const uint64_t qd = smem_desc(q_img(g), 16, 1024), kd = smem_desc(k_img(c % kKStages), 16, 1024);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const int at = ((ks / 4) * (kRows * 128) + (ks % 4) * 32) / 16;
-            warp_mma_ss(tm + I::scol(g), qd + at, kd + at, id_s, ks > 0);
-          }
-          warp_mma_commit(smem_addr(&s_full[g]));
-        };
-        auto issue_pv = [&](int g, int c, int nsub) {
-          const uint64_t vd = smem_desc(v_img(c % kVStages), kChunk * 128, 1024);
-#pragma unroll
-          for (int kk = 0; kk < kChunk / 16; ++kk)
-            if (kk < nsub)
-              warp_mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, vd + kk * (16 * 128 / 16), id_o,
-                          (c > 0 || kk > 0) ? 1u : 0u);
-          warp_mma_commit(smem_addr(&o_done[g]));
-        };
-        if (warp_wait(smem_addr(&k_full[0]), 0)) {
-          tc_fence_after();
-          issue_s(0, 0);
-          if (live1) issue_s(1, 0);
-          warp_mma_commit(smem_addr(&k_empty[0]));
-        } else {
-          ok = false;
-        }
-        for (int c = 0; c < nch && ok; ++c) {
-          const int vs = c % kVStages, ks1 = (c + 1) % kKStages;
-          if (!warp_wait(smem_addr(&v_full[vs]), (c / kVStages) & 1)) { ok = false; break; }
-          const int nsub = (min(t_end - c * kChunk, kChunk) + 15) / 16;
-          const bool next = c + 1 < nch;
-          if (!warp_wait(smem_addr(&p_full[0]), c & 1)) { ok = false; break; }
-          if (next && !warp_wait(smem_addr(&k_full[ks1]), ((c + 1) / kKStages) & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(0, c, nsub);
-          if (next) issue_s(0, c + 1);
-          if (live1) {
-            if (!warp_wait(smem_addr(&p_full[1]), c & 1)) { ok = false; break; }
-            tc_fence_after();
-            issue_pv(1, c, nsub);
-          }
-          warp_mma_commit(smem_addr(&v_empty[vs]));
-          if (next) {
-            if (live1) issue_s(1, c + 1);
-            warp_mma_commit(smem_addr(&k_empty[ks1]));
-          }
-        }
-        if (!ok) sh_fail = 1;
-        __syncwarp();
-      } else if (warp == kKWarp || warp == kVWarp) {
-        // one lane per operand: chunk c into stage c % stages once the MMAs are done with it
-        if (lane == 0) {
-          const bool is_k = warp == kKWarp;
-          const int nst = is_k ? kKStages : kVStages;
-          uint64_t* full = is_k ? k_full : v_full;
-          uint64_t* empty = is_k ? k_empty : v_empty;
-          const unsigned char* src = a.images + (cell * 2 + (is_k ? 0 : 1)) * (int64_t)I::kBytes;
-          int issued = 0;
-          bool ok = true;
-          for (int c = 0; c < nch; ++c) {
-            const int st = c % nst;
-            if (c >= nst && !mbar_wait(smem_addr(&empty[st]), (c / nst - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            bulk_image(is_k ? k_img(st) : v_img(st), src + (int64_t)c * 2 * I::kBytes, I::kBytes, smem_addr(&full[st]));
-            issued = c + 1;
-          }
-          if (!ok) sh_fail = 1;
-          // every copy has landed before the CTA moves on (normally already so)
-          for (int st = 0; st < nst && st < issued; ++st)
-            mbar_wait(smem_addr(&full[st]), ((issued - 1 - st) / nst) & 1);
-        }
-        __syncwarp();
-      } else if (tile == 0 || live1) {
-        // One row per thread.  A chunk row's 128 scores in two halves, each read from
-        // TMEM once: its largest is tested against the reference, then P is written
-        // over the columns the half has read.  When a half passes the reference by
-        // more than kSlack octaves the reference moves by whole octaves, so that the
-        // rescaling of O (once P . V of the chunk before is done) and of a first half
-        // already written is exact.
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_tmem = tm + lane_base + I::scol(tile), o_tmem = tm + lane_base + I::ocol(tile);
-        bool ok = true;
-        const bool warp_live = __any_sync(0xffffffffu, row_valid);
-        int2 ex = __ldg(a.exps + cell);
-        for (int c = 0; c < nch; ++c) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the images -> tensor core
+      mbar_arrive(smem_addr(&q_full[tile]));
+      return fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - exponent(own)) << 23), 1e-37f);
+    };
+    Unit u = next_unit();
+    float sl2 = 0.0f;
+    if (u.chunks > 0 && u.live(tile)) sl2 = load_q(u);
+    int j = 0;                                      // chunks of this tile
+    while (ok && u.chunks >= 0) {
+      const int r = u.row0 + tile * kRows + ri;
+      const bool valid = r < u.rows, mine = u.chunks > 0 && u.live(tile);
+      const int lim = valid ? u.before + r / GQ : -1;
+      // One row per thread.  A chunk row's 128 scores in two halves, each read from
+      // TMEM once: its largest is tested against the reference, then P is written
+      // over the columns the half has read.  When a half passes the reference by
+      // more than kSlack octaves the reference moves by whole octaves, so that the
+      // rescaling of O (once P . V of the chunk before is done) and of a first half
+      // already written is exact.
+      float m_ref = -INFINITY, l = 0.0f;
+      if (mine) {
+        const bool warp_live = __any_sync(0xffffffffu, valid);
+        const int2* exps = a.exps + (int64_t)u.cell * a.chunks;
+        int2 ex = __ldg(exps);
+        for (int c = 0; c < u.chunks; ++c, ++j) {
           const int2 now = ex;
-          if (c + 1 < nch) ex = __ldg(a.exps + cell + c + 1);
-          if (__shfl_sync(0xffffffffu, sh_fail, 0)) { ok = false; break; }
-          if (!warp_wait(smem_addr(&s_full[tile]), c & 1)) { ok = false; break; }
+          if (c + 1 < u.chunks) ex = __ldg(exps + c + 1);
+          if (!warp_wait(smem_addr(&s_full[tile]), j & 1)) { ok = false; break; }
           tc_fence_after();
           if (!warp_live) {                         // padding rows: keep the barriers' phases
             tc_fence_before();
@@ -533,7 +645,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
             continue;
           }
           const float kf = sl2 * __uint_as_float((uint32_t)(127 + now.x) << 23), ev = (float)now.y;
-          const int cstart = c * kChunk, lim = pos;
+          const int cstart = c * kChunk;
           const bool masked = __any_sync(0xffffffffu, cstart + kChunk - 1 > lim);
           float lsum = 0.0f;
 #pragma unroll
@@ -566,7 +678,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
               const float m_new = !need ? m_ref : (m_ref == -INFINITY ? mx : m_ref + k);
               const float alpha = need ? (m_ref == -INFINITY ? 0.0f : ldexpf(1.0f, -(int)k)) : 1.0f;
               if (c > 0) {
-                if (!warp_wait(smem_addr(&o_done[tile]), (c - 1) & 1)) {
+                if (!warp_wait(smem_addr(&o_done[tile]), (j - 1) & 1)) {
                   ok = false;
                   break;
                 }
@@ -614,70 +726,71 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
           tc_fence_before();
           mbar_arrive(smem_addr(&p_full[tile]));
         }
-        if (ok && !warp_wait(smem_addr(&o_done[tile]), (nch - 1) & 1)) ok = false;
-        if (!ok) sh_fail = 1;
-        tc_fence_after();
+        if (!ok) break;
       }
-    }
-    __syncthreads();
-    if (nch > 0 && warp == kMmaWarp) {
-      // all tensor-core work of this CTA completes before TMEM is read or freed
+      // the next unit's queries (this one's scores are all made), then this one's rows
+      const Unit nu = next_unit();
+      if (nu.chunks > 0 && nu.live(tile)) sl2 = load_q(nu);
+      if (mine && !warp_wait(smem_addr(&o_done[tile]), (j - 1) & 1)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
-      warp_mma_commit(smem_addr(&drain_bar));
-      if (!warp_wait(smem_addr(&drain_bar), 0)) sh_fail = 1;
-    }
-    __syncthreads();
-    const bool have = nch > 0 && sh_fail == 0;
-    if (sh_fail && tid == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
-    if (warp < kSoftmaxWarps && (tile == 0 || live1)) {
-      tc_fence_after();
-      const uint32_t o_tmem = tm + ((uint32_t)(32 * (warp & 3)) << 16) + I::ocol(tile);
-      const float inv = have && row_valid ? 1.0f / l : 0.0f;
+      if (u.live(tile)) {
+        // 32 columns of a row are four 16-byte pieces; four lanes exchange theirs, so
+        // that each store writes 64 bytes of eight rows instead of 16 bytes of 32.
+        const float inv = mine && valid ? 1.0f / l : 0.0f;
+        const int first = r - (lane & 3);
+        int64_t at[4];
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t ov[32];
-        if (have) {
-          tmem_read32(o_tmem + c0, ov);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) ov[j] = 0u;
+        for (int x = 0; x < 4; ++x) {
+          const int tok = (first + x) / GQ;
+          at[x] = first + x < u.rows
+                      ? ((int64_t)(u.q0 + tok) * Hq + (int64_t)u.head * GQ + (first + x - tok * GQ)) * D + (lane & 3) * 8
+                      : -1;
         }
-        if (!row_valid) continue;
-        __nv_bfloat16* out = a.out + qrow * D + c0;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t w[4];
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32], w[4][4];
+          if (mine) {
+            tmem_read32(o_tmem + c0, ov);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack2<false>(__uint_as_float(ov[j + 2 * i]) * inv, __uint_as_float(ov[j + 2 * i + 1]) * inv);
-          *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int x = 0; x < 32; ++x) ov[x] = 0u;
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            w[x / 4][x % 4] = pack2<false>(__uint_as_float(ov[2 * x]) * inv, __uint_as_float(ov[2 * x + 1]) * inv);
+#pragma unroll
+          for (int bit = 1; bit <= 2; bit <<= 1) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (x & bit) continue;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & bit ? w[x][y] : w[x | bit][y], bit);
+                if (lane & bit) w[x][y] = got;
+                else w[x | bit][y] = got;
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (at[x] >= 0)
+              *reinterpret_cast<uint4*>(a.out + at[x] + c0) = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
         }
       }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    // every copy, MMA and arrival of this unit is done: the barriers start over
-    if (tid == 0) {
-      for (int s = 0; s < kKStages; ++s) {
-        mbar_inval(smem_addr(&k_full[s]));
-        mbar_inval(smem_addr(&k_empty[s]));
-      }
-      for (int s = 0; s < kVStages; ++s) {
-        mbar_inval(smem_addr(&v_full[s]));
-        mbar_inval(smem_addr(&v_empty[s]));
-      }
-      for (int g = 0; g < kTiles; ++g) {
-        mbar_inval(smem_addr(&s_full[g]));
-        mbar_inval(smem_addr(&p_full[g]));
-        mbar_inval(smem_addr(&o_done[g]));
-      }
-      mbar_inval(smem_addr(&drain_bar));
+      tc_fence_before();
+      if (mine) mbar_arrive(smem_addr(&o_free[tile]));
+      u = nu;
     }
   }
+  if (!ok) sh_fail = 1;
   tc_fence_before();
   __syncthreads();
-  if (tm_held && warp == 0)
+  tc_fence_after();
+  if (sh_fail && tid == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
+  if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmemCols) : "memory");
 }
 
