@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   using I = Img<D>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  __shared__ uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], o_done[kTiles], o_free[kTiles];
+  __shared__ uint64_t q_full[kTiles], s_full[kTiles], p_half[kTiles], p_full[kTiles], o_half[kTiles], o_done[kTiles];
+  __shared__ uint64_t o_free[kTiles];
   __shared__ uint64_t unit_full, unit_empty, drain_bar;
   __shared__ uint32_t tmem_base;
   __shared__ Unit sh_unit;
@@ -328,7 +329,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     for (int g = 0; g < kTiles; ++g) {
       mbar_init(smem_addr(&q_full[g]), kRows);
       mbar_init(smem_addr(&s_full[g]), 1);
+      mbar_init(smem_addr(&p_half[g]), kRows);
       mbar_init(smem_addr(&p_full[g]), kRows);
+      mbar_init(smem_addr(&o_half[g]), 1);
       mbar_init(smem_addr(&o_done[g]), 1);
       mbar_init(smem_addr(&o_free[g]), kRows);
     }
@@ -450,14 +453,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       }
       warp_mma_commit(smem_addr(&s_full[g]));
     };
-    auto issue_pv = [&](int g, bool first, int nsub) {
+    // P . V of a chunk, 64 keys as soon as P of them is written, then the others.
+    auto issue_pv = [&](int g, bool first, int nsub, int np) {
       const uint64_t vd = smem_desc(v_img(vc % kVStages), kChunk * 128, 1024);
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 16; ++kk)
-        if (kk < nsub)
-          warp_mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, vd + kk * (16 * 128 / 16), id_o,
-                      (!first || kk > 0) ? 1u : 0u);
-      warp_mma_commit(smem_addr(&o_done[g]));
+      for (int half = 0; half < 2; ++half) {
+        if (!warp_wait(smem_addr(half ? &p_full[g] : &p_half[g]), np & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+          if (kk < nsub)
+            warp_mma_ts(tm + I::ocol(g), tm + I::scol(g) + kk * 8, vd + kk * (16 * 128 / 16), id_o,
+                        (!first || kk > 0) ? 1u : 0u);
+        warp_mma_commit(smem_addr(half ? &o_done[g] : &o_half[g]));
+      }
+      return true;
     };
     auto wait_k = [&]() { return warp_wait(smem_addr(&k_full[kc % kKStages]), (kc / kKStages) & 1); };
     // the first scores of a unit
@@ -488,22 +498,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       for (int c = 0; c < u.chunks; ++c) {
         const int nsub = (min(u.keys - c * kChunk, kChunk) + 15) / 16;
         const bool more = c + 1 < u.chunks;
-        ok = warp_wait(smem_addr(&v_full[vc % kVStages]), (vc / kVStages) & 1) &&
-             warp_wait(smem_addr(&p_full[0]), np0 & 1) && (!more || wait_k());
+        ok = warp_wait(smem_addr(&v_full[vc % kVStages]), (vc / kVStages) & 1) && (!more || wait_k());
         // (the last unit's O is read)
         if (ok && c == 0 && nq0 > 1) ok = warp_wait(smem_addr(&o_free[0]), nq0 & 1);
-        if (!ok) break;
-        ++np0;
-        tc_fence_after();
-        issue_pv(0, c == 0, nsub);
+        if (!ok || !issue_pv(0, c == 0, nsub, np0++)) { ok = false; break; }
         if (more) issue_s(0);
         if (live1) {
-          ok = warp_wait(smem_addr(&p_full[1]), np1 & 1);
-          if (ok && c == 0 && nq1 > 1) ok = warp_wait(smem_addr(&o_free[1]), nq1 & 1);
-          if (!ok) break;
-          ++np1;
-          tc_fence_after();
-          issue_pv(1, c == 0, nsub);
+          if (c == 0 && nq1 > 1) ok = warp_wait(smem_addr(&o_free[1]), nq1 & 1);
+          if (!ok || !issue_pv(1, c == 0, nsub, np1++)) { ok = false; break; }
         }
         warp_mma_commit(smem_addr(&v_empty[vc % kVStages]));
         ++vc;
@@ -556,19 +558,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       const int r0 = u.row0 + tile * kRows + wrow + sub;
       uint4 qv[kTurns];
       {
-        int tok = r0 / GQ, h = r0 - tok * GQ;
-        const int dtok = kEach / GQ, dh = kEach - dtok * GQ;
-        const __nv_bfloat16* from = a.q + (int64_t)u.head * GQ * D + part * 8;
+        const int tok = r0 / GQ, dtok = kEach / GQ, dh = kEach - dtok * GQ;
+        int h = r0 - tok * GQ;
+        const __nv_bfloat16* from = a.q + ((int64_t)(u.q0 + tok) * Hq + (int64_t)u.head * GQ + h) * D + part * 8;
+        const int step = (dtok * Hq + dh) * D, wrap = (Hq - GQ) * D;
 #pragma unroll
         for (int i = 0; i < kTurns; ++i) {
           qv[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r0 + i * kEach < u.rows)
-            qv[i] = __ldg(reinterpret_cast<const uint4*>(from + ((int64_t)(u.q0 + tok) * Hq + h) * D));
+          if (r0 + i * kEach < u.rows) qv[i] = __ldg(reinterpret_cast<const uint4*>(from));
           h += dh;
-          tok += dtok;
+          from += step;
           if (h >= GQ) {
             h -= GQ;
-            ++tok;
+            from += wrap;
           }
         }
       }
@@ -576,13 +578,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       uint32_t top[kTurns];
 #pragma unroll
       for (int i = 0; i < kTurns; ++i) {
-        const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-        top[i] = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t lo = w4[k] & 0x7fffu, hi = w4[k] >> 16 & 0x7fffu;
-          top[i] = max(top[i], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-        }
+        const uint32_t m = __vmaxu2(__vmaxu2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
+                                    __vmaxu2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu));
+        top[i] = max(m & 0xffffu, m >> 16);         // (255: an infinity or NaN, and so is the row)
       }
 #pragma unroll
       for (int off = 1; off < kLanes; off <<= 1) {
@@ -627,8 +625,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       // TMEM once: its largest is tested against the reference, then P is written
       // over the columns the half has read.  When a half passes the reference by
       // more than kSlack octaves the reference moves by whole octaves, so that the
-      // rescaling of O (once P . V of the chunk before is done) and of a first half
-      // already written is exact.
+      // rescaling of O (once the P . V before is done) is exact.
       float m_ref = -INFINITY, l = 0.0f;
       if (mine) {
         const bool warp_live = __any_sync(0xffffffffu, valid);
@@ -641,6 +638,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
           tc_fence_after();
           if (!warp_live) {                         // padding rows: keep the barriers' phases
             tc_fence_before();
+            mbar_arrive(smem_addr(&p_half[tile]));
             mbar_arrive(smem_addr(&p_full[tile]));
             continue;
           }
@@ -677,8 +675,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
               const float k = (need && m_ref != -INFINITY) ? ceilf(mx - m_ref) : 0.0f;
               const float m_new = !need ? m_ref : (m_ref == -INFINITY ? mx : m_ref + k);
               const float alpha = need ? (m_ref == -INFINITY ? 0.0f : ldexpf(1.0f, -(int)k)) : 1.0f;
-              if (c > 0) {
-                if (!warp_wait(smem_addr(&o_done[tile]), (j - 1) & 1)) {
+              // O so far: of the chunks before, or (second half) of the first half too
+              if (c > 0 || ps > 0) {
+                if (!(ps > 0 ? warp_wait(smem_addr(&o_half[tile]), j & 1)
+                             : warp_wait(smem_addr(&o_done[tile]), (j - 1) & 1))) {
                   ok = false;
                   break;
                 }
@@ -692,24 +692,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
                   for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
                   tmem_st16(o_tmem + c0, ov);
                 }
-              }
-              if (ps > 0) {
                 tmem_wait_st();
-#pragma unroll 1
-                for (int c0 = 0; c0 < 32; c0 += 16) {
-                  uint32_t pv[16];
-                  tmem_ld16(s_tmem + c0, pv);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&pv[j]));
-                    pv[j] = pack2<true>(y.x * alpha, y.y * alpha);
-                  }
-                  tmem_st16(s_tmem + c0, pv);
-                }
-                lsum *= alpha;
               }
-              tmem_wait_st();
+              lsum *= alpha;
               if (need) l = m_ref == -INFINITY ? 0.0f : ldexpf(l, -(int)k);
               m_ref = m_new;
             }
@@ -719,6 +704,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
                 masked ? half_exp<true>(raw, pw, first, lim, kf, add) : half_exp<false>(raw, pw, first, lim, kf, add);
             if (!far) lsum += part;
             tmem_st32(s_tmem + 32 * ps, pw);
+            if (ps == 0) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(smem_addr(&p_half[tile]));
+            }
           }
           if (!ok) break;
           tmem_wait_st();
