@@ -71,6 +71,9 @@ __device__ __forceinline__ bool long_sequence(const Q4LongArgs& a, int b) {
 __global__ void __launch_bounds__(256) q4_plan_kernel(const Q4LongArgs a) {
   __shared__ int sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (each launch is a programmatic dependent of the one before and waits for it here)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int run = (a.batch + 255) / 256;
   const int b0 = threadIdx.x * run, b1 = min(a.batch, b0 + run);
   int mine = 0;
@@ -118,12 +121,14 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
   __shared__ int32_t blk[kChunk / 16];
   __shared__ int any_bad;
   const int c = blockIdx.x, hk = blockIdx.y, slot = blockIdx.z;
+  if (threadIdx.x < 2) top[threadIdx.x] = 0;
+  if (threadIdx.x == 0) any_bad = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (slot >= a.counters[0]) return;
   const int b = a.list[slot], L = a.seq_lens[b];
   const int t0 = c * kChunk, rows = min(kChunk, L - t0);
   if (rows <= 0) return;
-  if (threadIdx.x < 2) top[threadIdx.x] = 0;
-  if (threadIdx.x == 0) any_bad = 0;
   __syncthreads();
   if (threadIdx.x < kChunk / BS && (int)threadIdx.x * BS < rows) {
     const int id = a.block_tables[(int64_t)b * a.max_blocks + t0 / BS + threadIdx.x];
@@ -139,23 +144,46 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
     }
     return;
   }
+  // Four lanes have a row (16 codes of every group each), a thread four rows, all
+  // asked for at once: the chain of loads before them is most of this kernel's time.
+  constexpr int kTurns = kChunk / 32;
   const int x = threadIdx.x >> 7;                   // 0: K, 1: V
-  auto record = [&](int r) { return a.kv + ((int64_t)blk[r / BS] * a.num_kv_heads + hk) * G::kRecord; };
-  // the largest magnitude of the rows: a group's values lie between min and min + 15 scale
-  {
-    const int r = threadIdx.x & 127;
-    float m = 0.0f;
-    if (r < rows) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(record(r) + q4_pairs_at(x, r % BS, BS, D));
+  const int w4 = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint32_t w[kTurns][2 * NG], pair[kTurns][NG];
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        const float s = __uint_as_float(p[gr] << 16), lo = __uint_as_float(p[gr] & 0xffff0000u);
-        m = fmaxf(m, fmaxf(fabsf(lo), fabsf(fmaf(15.0f, s, lo))));
+  for (int i = 0; i < kTurns; ++i) {
+    const int r = i * 32 + w4 * 8 + g;
+#pragma unroll
+    for (int k = 0; k < 2 * NG; ++k) w[i][k] = 0;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) pair[i][k] = 0;
+    if (r < rows) {
+      const unsigned char* rec = a.kv + ((int64_t)blk[r / BS] * a.num_kv_heads + hk) * G::kRecord;
+      const unsigned char* from = rec + q4_codes_at(x, r % BS, BS, D) + t * (D / 8);
+      if constexpr (NG == 2) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(from));
+        w[i][0] = y.x, w[i][1] = y.y, w[i][2] = y.z, w[i][3] = y.w;
+      } else {
+        const uint2 y = __ldg(reinterpret_cast<const uint2*>(from));
+        w[i][0] = y.x, w[i][1] = y.y;
       }
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+        pair[i][k] = __ldg(reinterpret_cast<const uint32_t*>(rec + q4_pairs_at(x, r % BS, BS, D)) + k);
     }
-    const unsigned int u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if ((threadIdx.x & 31) == 0) atomicMax(&top[x], u);
   }
+  // the largest magnitude of the rows: a group's values lie between min and min + 15 scale
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const float s = __uint_as_float(pair[i][k] << 16), lo = __uint_as_float(pair[i][k] & 0xffff0000u);
+      m = fmaxf(m, fmaxf(fabsf(lo), fabsf(fmaf(15.0f, s, lo))));
+    }
+  }
+  const unsigned int u = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  if (lane == 0) atomicMax(&top[x], u);
   __syncthreads();
   // value * 2^-e is at most [2^12, 2^13) (|value| < 2^128); -80 keeps the sums of
   // p / 2^E within fp32
@@ -164,35 +192,15 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
   if ((threadIdx.x & 127) == 0) reinterpret_cast<int*>(a.exps + cell)[x] = e;
   const float f = __uint_as_float((uint32_t)(127 - e) << 23);
   unsigned char* img = a.images + (cell * 2 + x) * Img<D>::kBytes;
-  const int w4 = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll 2
-  for (int r = w4 * 8 + g; r < kChunk; r += 32) {
-    const bool live = r < rows;
-    uint32_t w[2 * NG], pair[NG];
 #pragma unroll
-    for (int i = 0; i < 2 * NG; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) pair[i] = 0;
-    if (live) {
-      const unsigned char* rec = record(r);
-      const unsigned char* from = rec + q4_codes_at(x, r % BS, BS, D) + t * (D / 8);
-      if constexpr (NG == 2) {
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(from));
-        w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
-      } else {
-        const uint2 y = __ldg(reinterpret_cast<const uint2*>(from));
-        w[0] = y.x, w[1] = y.y;
-      }
-#pragma unroll
-      for (int i = 0; i < NG; ++i)
-        pair[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + q4_pairs_at(x, r % BS, BS, D)) + i);
-    }
+  for (int i = 0; i < kTurns; ++i) {
+    const int r = i * 32 + w4 * 8 + g;
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      const float s = __uint_as_float(pair[gr] << 16) * f, lo = __uint_as_float(pair[gr] & 0xffff0000u) * f;
+      const float s = __uint_as_float(pair[i][gr] << 16) * f, lo = __uint_as_float(pair[i][gr] & 0xffff0000u) * f;
 #pragma unroll
       for (int ci = 0; ci < 2; ++ci) {
-        const uint32_t y = w[ci * NG + gr];
+        const uint32_t y = w[i][ci * NG + gr];
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -315,8 +323,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   auto k_img = [&](int s) { return base + (uint32_t)((kTiles + s) * I::kBytes); };
   auto v_img = [&](int s) { return base + (uint32_t)((kTiles + kKStages + s) * I::kBytes); };
 
-  const int count = a.counters[0];
-  if (count == 0) return;
   if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(smem_addr(&k_full[s]), 1);
@@ -350,6 +356,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+  // (a programmatic dependent: plan and images may still be in the making until here)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int count = a.counters[0];
 
   bool ok = true;
   int taken = 0;                                    // units read
@@ -368,24 +377,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
   };
 
   if (warp == kUnitWarp) {
-    // Units are taken as CTAs become free, one ahead of the roles; the last pairs
-    // of the last sequence (which see the most keys) first.
-    auto pairs_of = [&](int slot) {
-      const int b = a.list[slot];
-      return ((a.query_start[b + 1] - a.query_start[b]) * GQ + kTiles * kRows - 1) / (kTiles * kRows);
+    // Units are taken as CTAs become free, one ahead of the roles, those with the
+    // most chunks first: what a CTA holds when the last is taken is short.  Which one
+    // the i-th is follows from how many have k chunks at least, for any k.
+    // pairs of row tiles of a slot whose last row sees k chunks at least
+    auto pairs_from = [&](int slot, int k) {
+      const int b = a.list[slot], n = a.query_start[b + 1] - a.query_start[b], rows = n * GQ;
+      const int64_t row = ((int64_t)(k - 1) * kChunk - (a.seq_lens[b] - n)) * GQ;   // the first that does
+      const int all = (rows + kTiles * kRows - 1) / (kTiles * kRows);
+      if (row >= rows) return 0;
+      return all - (row > 0 ? (int)(row / (kTiles * kRows)) : 0);
     };
-    const int per = (count + 31) / 32;
-    int mine = 0;
-    for (int i = 0; i < per; ++i)
-      if (lane * per + i < count) mine += pairs_of(lane * per + i);
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    const int pairs = __shfl_sync(0xffffffffu, incl, 31);
+    auto units_from = [&](int k) {
+      int mine = 0;
+      for (int i = lane; i < count; i += 32) mine += pairs_from(i, k);
+      return __reduce_add_sync(0xffffffffu, mine);
+    };
+    const int pairs = units_from(1);
     const long long units = (long long)pairs * Hkv;
+    int most = 1;
+    for (int i = lane; i < count; i += 32) most = max(most, (a.seq_lens[a.list[i]] + kChunk - 1) / kChunk);
+    most = __reduce_max_sync(0xffffffffu, most);
     for (;; ++taken) {
       int u = 0;
       if (lane == 0) u = atomicAdd(&a.counters[1], 1);
@@ -393,21 +405,43 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       Unit x = {};
       x.chunks = -1;
       if (u < units) {
-        const int at = pairs - 1 - u / Hkv;
-        int slot = 0, pr = 0;
-        const bool here = at >= incl - mine && at < incl;
-        if (here) {
-          int acc = incl - mine;
-          for (slot = lane * per;; ++slot) {
-            const int pl = pairs_of(slot);
-            if (at < acc + pl) break;
-            acc += pl;
-          }
-          pr = at - acc;
+        const int at = u / Hkv;
+        // the largest k with more than `at` pairs: not above the last unit's, and near it
+        int lo = most, hi = most;
+        for (int step = 1; lo > 1 && units_from(lo) <= at; step *= 2) {
+          hi = lo - 1;
+          lo = max(1, hi - step);
         }
-        const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-        slot = __shfl_sync(0xffffffffu, slot, src);
-        pr = __shfl_sync(0xffffffffu, pr, src);
+        while (lo < hi) {
+          const int k = (lo + hi + 1) / 2;
+          if (units_from(k) > at) lo = k;
+          else hi = k - 1;
+        }
+        most = lo;                                  // (the next unit has no more)
+        const int more = units_from(lo + 1);
+        // the (at - more)-th pair of exactly `lo` chunks, by slot
+        int slot = 0, pr = 0, left = at - more;
+        bool found = false;
+        for (int s0 = 0; s0 < count && !found; s0 += 32) {
+          const int i = s0 + lane, from = i < count ? pairs_from(i, lo) : 0, mine = from - (i < count ? pairs_from(i, lo + 1) : 0);
+          int incl = mine;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+          }
+          const unsigned here = __ballot_sync(0xffffffffu, left < incl);
+          if (here != 0) {
+            const int src = __ffs(here) - 1;
+            slot = s0 + src;
+            // a slot's pairs of `lo` chunks are consecutive, the first has `from` pairs from it on
+            const int all = i < count ? pairs_from(i, 1) : 0;
+            pr = __shfl_sync(0xffffffffu, all - from + (left - (incl - mine)), src);
+            found = true;
+          } else {
+            left -= __shfl_sync(0xffffffffu, incl, 31);
+          }
+        }
         const int b = a.list[slot], n = a.query_start[b + 1] - a.query_start[b];
         x.head = u % Hkv;
         x.cell = slot * Hkv + x.head;
@@ -418,11 +452,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
         const int last = min(x.row0 + kTiles * kRows, x.rows) - 1;
         x.keys = x.before + last / GQ + 1;          // keys the last row sees
         x.chunks = a.bad[slot] != 0 ? 0 : (x.keys + kChunk - 1) / kChunk;
-        // its queries into L2
-        for (int t = x.row0 / GQ + lane; t <= last / GQ; t += 32) {
-          const __nv_bfloat16* row = a.q + ((int64_t)(x.q0 + t) * Hq + (int64_t)x.head * GQ) * D;
-          for (int e = 0; e < GQ * D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + e));
-        }
       }
       if (taken > 0 && !warp_wait(smem_addr(&unit_empty), (taken - 1) & 1)) {
         ok = false;
@@ -434,6 +463,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       }
       __syncwarp();
       if (x.chunks < 0) break;
+      // its queries into L2
+      const int last = min(x.row0 + kTiles * kRows, x.rows) - 1;
+      for (int t = x.row0 / GQ + lane; t <= last / GQ; t += 32) {
+        const __nv_bfloat16* row = a.q + ((int64_t)(x.q0 + t) * Hq + (int64_t)x.head * GQ) * D;
+        for (int e = 0; e < GQ * D; e += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + e));
+      }
     }
   } else if (warp == kMmaWarp) {
     // Per chunk c: P . V_0(c), S_0(c+1), P . V_1(c), [V stage free], S_1(c+1), [K
@@ -784,6 +819,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(kTmemCols) : "memory");
 }
 
+// A launch as programmatic dependent of the one before it.
+kv_status launch_after(void (*kernel)(Q4LongArgs), dim3 grid, int threads, int smem, cudaStream_t s,
+                       const Q4LongArgs& a, const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, a), what);
+}
+
 template <int D>
 kv_status launch_tc(const Q4LongArgs& a, int ctas, cudaStream_t s) {
   static std::mutex mu;
@@ -800,8 +851,7 @@ kv_status launch_tc(const Q4LongArgs& a, int ctas, cudaStream_t s) {
       set[dev] = true;
     }
   }
-  q4_tc_kernel<D><<<(unsigned)ctas, kThreadsTc, Img<D>::kSmem, s>>>(a);
-  return cuda_check(cudaGetLastError(), "q4_tc_kernel launch");
+  return launch_after(q4_tc_kernel<D>, dim3((unsigned)ctas), kThreadsTc, Img<D>::kSmem, s, a, "q4_tc_kernel launch");
 }
 
 }  // namespace
@@ -824,21 +874,16 @@ kv_status launch_q4_long(Q4LongArgs a, void* memory, int sms, cudaStream_t s) {
   a.list = reinterpret_cast<int*>(a.exps + cells);
   a.bad = a.list + a.slots;
   a.counters = a.bad + a.slots;
-  q4_plan_kernel<<<1, 256, 0, s>>>(a);
-  kv_status st = cuda_check(cudaGetLastError(), "q4_plan_kernel launch");
+  kv_status st = launch_after(q4_plan_kernel, dim3(1), 256, 0, s, a, "q4_plan_kernel launch");
   if (st != KV_OK) return st;
+  const bool wide = a.head_dim == 128, big = a.block_size == 32;
+  void (*widen)(Q4LongArgs) = wide ? (big ? q4_widen_kernel<128, 32> : q4_widen_kernel<128, 16>)
+                                   : (big ? q4_widen_kernel<64, 32> : q4_widen_kernel<64, 16>);
   const dim3 grid((unsigned)a.chunks, (unsigned)a.num_kv_heads, (unsigned)a.slots);
-  if (a.head_dim == 128) {
-    if (a.block_size == 32) q4_widen_kernel<128, 32><<<grid, 256, 0, s>>>(a);
-    else q4_widen_kernel<128, 16><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (a.block_size == 32) q4_widen_kernel<64, 32><<<grid, 256, 0, s>>>(a);
-    else q4_widen_kernel<64, 16><<<grid, 256, 0, s>>>(a);
-  }
-  if ((st = cuda_check(cudaGetLastError(), "q4_widen_kernel launch")) != KV_OK) return st;
+  if ((st = launch_after(widen, grid, 256, 0, s, a, "q4_widen_kernel launch")) != KV_OK) return st;
   const long long units = ((long long)a.num_tokens * a.group / (kTiles * kRows) + a.slots) * a.num_kv_heads;
   const int ctas = (int)(units < sms ? units : sms);
-  return a.head_dim == 128 ? launch_tc<128>(a, ctas, s) : launch_tc<64>(a, ctas, s);
+  return wide ? launch_tc<128>(a, ctas, s) : launch_tc<64>(a, ctas, s);
 }
 
 }  // namespace pagedkv
