@@ -239,24 +239,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Largest of 64 scores (those past `lim` left out when kMask).
-template <bool kMask>
-__device__ __forceinline__ float half_max(const uint32_t (&raw)[64], int first, int lim) {
+// Largest of 64 scores.
+__device__ __forceinline__ float half_max(const uint32_t (&raw)[64]) {
   float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int j = 0; j < 64; j += 2) {
-    float v = __uint_as_float(raw[j]), w = __uint_as_float(raw[j + 1]);
-    if (kMask && first + j > lim) v = -INFINITY;
-    if (kMask && first + j + 1 > lim) w = -INFINITY;
-    mr[j / 2 & 3] = fmaxf(fmaxf(mr[j / 2 & 3], v), w);
-  }
+  for (int j = 0; j < 64; j += 2)
+    mr[j / 2 & 3] = fmaxf(fmaxf(mr[j / 2 & 3], __uint_as_float(raw[j])), __uint_as_float(raw[j + 1]));
   return fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3]));
 }
 
-// p = 2^(raw * k + add) (0 past `lim`) as fp16 pairs; their fp32 sum.
-template <bool kMask>
-__device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&pw)[32], int first, int lim, float k,
-                                          float add) {
+// p = 2^(raw * k + add) as fp16 pairs; their fp32 sum.
+__device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&pw)[32], float k, float add) {
   const uint64_t kk = pack_f32x2(k, k), aa = pack_f32x2(add, add);
   uint64_t ls[2] = {0, 0};
 #pragma unroll
@@ -265,10 +258,6 @@ __device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&
     unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])), kk, aa), p0, p1);
     p0 = ex2(p0);
     p1 = ex2(p1);
-    if (kMask) {
-      p0 = first + 2 * j <= lim ? p0 : 0.0f;
-      p1 = first + 2 * j + 1 <= lim ? p1 : 0.0f;
-    }
     ls[j & 1] = add_f32x2(ls[j & 1], pack_f32x2(p0, p1));
     pw[j] = pack2<true>(p0, p1);
   }
@@ -584,73 +573,71 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     const int tile = warp >> 2, wrow = (warp & 3) * 32, ri = wrow + lane;   // this thread's row of the tile
     const uint32_t lane_base = (uint32_t)wrow << 16;
     const uint32_t s_tmem = tm + lane_base + I::scol(tile), o_tmem = tm + lane_base + I::ocol(tile);
-    // The warp's 32 rows of q as fp16, each under a power of two (largest in [2^13,
-    // 2^14)), into the tile's swizzled bands; returns what this thread's own row
-    // multiplies the scores by.  A negative scale turns q's sign, a zero one takes it as 0.
-    auto load_q = [&](const Unit& u) {
-      constexpr int kLanes = D / 8, kEach = 32 / kLanes, kTurns = 32 / kEach;   // lanes of a row, rows of a load
-      const int part = lane % kLanes, sub = lane / kLanes;
-      const int r0 = u.row0 + tile * kRows + wrow + sub;
-      uint4 qv[kTurns];
-      {
-        const int tok = r0 / GQ, dtok = kEach / GQ, dh = kEach - dtok * GQ;
-        int h = r0 - tok * GQ;
-        const __nv_bfloat16* from = a.q + ((int64_t)(u.q0 + tok) * Hq + (int64_t)u.head * GQ + h) * D + part * 8;
-        const int step = (dtok * Hq + dh) * D, wrap = (Hq - GQ) * D;
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-          qv[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r0 + i * kEach < u.rows) qv[i] = __ldg(reinterpret_cast<const uint4*>(from));
-          h += dh;
-          from += step;
-          if (h >= GQ) {
-            h -= GQ;
-            from += wrap;
-          }
+    constexpr int kLanes = D / 8, kEach = 32 / kLanes, kTurns = 32 / kEach;   // lanes of a row, rows of a turn
+    const int part = lane % kLanes, sub = lane / kLanes;
+    const uint32_t q_band = q_img(tile) + (part / 8) * (kRows * 128);
+    // Asks for the warp's 32 rows of q, into their places of the tile's swizzled bands.
+    auto fetch_q = [&](const Unit& u) {
+      int r = u.row0 + tile * kRows + wrow + sub;
+      const int tok = r / GQ, dtok = kEach / GQ, dh = kEach - dtok * GQ;
+      int h = r - tok * GQ;
+      const __nv_bfloat16* from = a.q + ((int64_t)(u.q0 + tok) * Hq + (int64_t)u.head * GQ + h) * D + part * 8;
+      const int step = (dtok * Hq + dh) * D, wrap = (Hq - GQ) * D;
+#pragma unroll 4
+      for (int i = 0; i < kTurns; ++i) {
+        const bool in = r < u.rows;                 // (rows behind the last are zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         q_band + sw128(wrow + i * kEach + sub, part % 8)),
+                     "l"(in ? from : a.q), "r"(in ? 16 : 0)
+                     : "memory");
+        r += kEach;
+        h += dh;
+        from += step;
+        if (h >= GQ) {
+          h -= GQ;
+          from += wrap;
         }
       }
-      // (the rows' steps side by side: a chain of shuffles per row would wait on itself)
-      uint32_t top[kTurns];
-#pragma unroll
+    };
+    // Turns them to fp16 in place (each lane what it asked for), each row under a power
+    // of two (largest in [2^13, 2^14)); returns what this thread's own row multiplies
+    // the scores by.  A negative scale turns q's sign, a zero one takes it as 0.
+    auto turn_q = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      float own = 0.0f;
+#pragma unroll 4
       for (int i = 0; i < kTurns; ++i) {
-        const uint32_t m = __vmaxu2(__vmaxu2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
-                                    __vmaxu2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu));
-        top[i] = max(m & 0xffffu, m >> 16);         // (255: an infinity or NaN, and so is the row)
-      }
+        const uint32_t at = q_band + sw128(wrow + i * kEach + sub, part % 8);
+        const uint4 x = lds128(at);
+        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                    __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+        uint32_t top = max(m & 0xffffu, m >> 16);   // (255: an infinity or NaN, and so is the row)
 #pragma unroll
-      for (int off = 1; off < kLanes; off <<= 1) {
-        uint32_t x[kTurns];
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) x[i] = __shfl_xor_sync(0xffffffffu, top[i], off);
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) top[i] = max(top[i], x[i]);
-      }
-      uint32_t own = 0;                             // the largest of this thread's own row
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const uint32_t theirs = __shfl_sync(0xffffffffu, top[i], lane % kEach * kLanes);
+        for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const int e = min(max(top > 0 ? 140 - (int)(top >> 7) : 0, -110), 110);
+        float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        const float theirs =
+            __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23), lane % kEach * kLanes);
         if (lane / kEach == i) own = theirs;
-      }
-      auto exponent = [](uint32_t x) { return min(max(x > 0 ? 140 - (int)(x >> 7) : 0, -110), 110); };
-      unsigned char* to = gbase + (q_img(tile) - base) + (part / 8) * (kRows * 128);
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const uint32_t w4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-        float up = __uint_as_float((uint32_t)(127 + exponent(top[i])) << 23);
         if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
         uint32_t o4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o4[k] = pack2<true>(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xffff0000u) * up);
-        *reinterpret_cast<uint4*>(to + sw128(wrow + i * kEach + sub, part % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]), "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
+                     : "memory");
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the images -> tensor core
       mbar_arrive(smem_addr(&q_full[tile]));
-      return fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - exponent(own)) << 23), 1e-37f);
+      return fmaxf(fabsf(a.scale_log2) * own, 1e-37f);
     };
     Unit u = next_unit();
     float sl2 = 0.0f;
-    if (u.chunks > 0 && u.live(tile)) sl2 = load_q(u);
+    if (u.chunks > 0 && u.live(tile)) {
+      fetch_q(u);
+      sl2 = turn_q();
+    }
     int j = 0;                                      // chunks of this tile
     while (ok && u.chunks >= 0) {
       const int r = u.row0 + tile * kRows + ri;
@@ -662,6 +649,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
       // more than kSlack octaves the reference moves by whole octaves, so that the
       // rescaling of O (once the P . V before is done) is exact.
       float m_ref = -INFINITY, l = 0.0f;
+      Unit nu = {};
       if (mine) {
         const bool warp_live = __any_sync(0xffffffffu, valid);
         const int2* exps = a.exps + (int64_t)u.cell * a.chunks;
@@ -671,6 +659,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
           if (c + 1 < u.chunks) ex = __ldg(exps + c + 1);
           if (!warp_wait(smem_addr(&s_full[tile]), j & 1)) { ok = false; break; }
           tc_fence_after();
+          if (c + 1 == u.chunks) {                  // every score of this unit is made: the next one's queries
+            nu = next_unit();
+            if (!ok) break;
+            if (nu.chunks > 0 && nu.live(tile)) fetch_q(nu);
+          }
           if (!warp_live) {                         // padding rows: keep the barriers' phases
             tc_fence_before();
             mbar_arrive(smem_addr(&p_half[tile]));
@@ -681,12 +674,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
           const int cstart = c * kChunk;
           const bool masked = __any_sync(0xffffffffu, cstart + kChunk - 1 > lim);
           float lsum = 0.0f;
-#pragma unroll
+          // (rolled, and masks applied beforehand: code that runs once a unit comes from
+          // far away, 2500 cycles for a masked form of its own)
+#pragma unroll 1
           for (int ps = 0; ps < 2; ++ps) {
             uint32_t raw[64];
             tmem_read64(s_tmem + 64 * ps, raw);
             const int first = cstart + 64 * ps;
-            const float mx_raw = masked ? half_max<true>(raw, first, lim) : half_max<false>(raw, first, lim);
+            if (masked) {
+#pragma unroll
+              for (int x = 0; x < 64; ++x)
+                if (x > lim - first) raw[x] = 0xff800000u;
+            }
+            const float mx_raw = half_max(raw);
             const float mx = mx_raw == -INFINITY ? -INFINITY : fmaf(mx_raw, kf, ev - kHead);
             const bool need = m_ref == -INFINITY ? mx > -INFINITY : mx > m_ref + kSlack;
             // V's magnitudes may lie further apart than fp32's exponents: p of rows of
@@ -735,8 +735,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
             }
             const float add = m_ref == -INFINITY ? 0.0f : ev - m_ref;
             uint32_t pw[32];
-            const float part =
-                masked ? half_exp<true>(raw, pw, first, lim, kf, add) : half_exp<false>(raw, pw, first, lim, kf, add);
+            const float part = half_exp(raw, pw, kf, add);
             if (!far) lsum += part;
             tmem_st32(s_tmem + 32 * ps, pw);
             if (ps == 0) {
@@ -753,9 +752,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
         }
         if (!ok) break;
       }
-      // the next unit's queries (this one's scores are all made), then this one's rows
-      const Unit nu = next_unit();
-      if (nu.chunks > 0 && nu.live(tile)) sl2 = load_q(nu);
+      if (!mine) {
+        nu = next_unit();
+        if (nu.chunks > 0 && nu.live(tile)) fetch_q(nu);
+      }
+      if (nu.chunks > 0 && nu.live(tile)) sl2 = turn_q();
       if (mine && !warp_wait(smem_addr(&o_done[tile]), (j - 1) & 1)) {
         ok = false;
         break;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
                       ? ((int64_t)(u.q0 + tok) * Hq + (int64_t)u.head * GQ + (first + x - tok * GQ)) * D + (lane & 3) * 8
                       : -1;
         }
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t ov[32], w[4][4];
           if (mine) {
