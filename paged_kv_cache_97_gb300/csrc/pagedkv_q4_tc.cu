@@ -605,28 +605,50 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     auto turn_q = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
       float own = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < kTurns; ++i) {
-        const uint32_t at = q_band + sw128(wrow + i * kEach + sub, part % 8);
-        const uint4 x = lds128(at);
-        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-        const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                    __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-        uint32_t top = max(m & 0xffffu, m >> 16);   // (255: an infinity or NaN, and so is the row)
+      // (four turns side by side: one alone is a chain of shuffles)
+#pragma unroll 1
+      for (int i0 = 0; i0 < kTurns; i0 += 4) {
+        uint4 x[4];
+        uint32_t top[4];
 #pragma unroll
-        for (int off = 1; off < kLanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const int e = min(max(top > 0 ? 140 - (int)(top >> 7) : 0, -110), 110);
-        float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        const float theirs =
-            __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(127 - e) << 23), lane % kEach * kLanes);
-        if (lane / kEach == i) own = theirs;
-        if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
-        uint32_t o4[4];
+        for (int i = 0; i < 4; ++i) x[i] = lds128(q_band + sw128(wrow + (i0 + i) * kEach + sub, part % 8));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o4[k] = pack2<true>(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xffff0000u) * up);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o4[0]), "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
-                     : "memory");
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                      __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+          top[i] = max(m & 0xffffu, m >> 16);       // (255: an infinity or NaN, and so is the row)
+        }
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = __shfl_xor_sync(0xffffffffu, top[i], off);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max(top[i], y[i]);
+        }
+        float up[4], theirs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = min(max(top[i] > 0 ? 140 - (int)(top[i] >> 7) : 0, -110), 110);
+          up[i] = __uint_as_float((uint32_t)(127 + e) << 23);
+          theirs[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (a.scale_log2 <= 0.0f) up[i] = a.scale_log2 < 0.0f ? -up[i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) theirs[i] = __shfl_sync(0xffffffffu, theirs[i], lane % kEach * kLanes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (lane / kEach == i0 + i) own = theirs[i];
+          const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t o4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o4[k] = pack2<true>(__uint_as_float(w4[k] << 16) * up[i], __uint_as_float(w4[k] & 0xffff0000u) * up[i]);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           q_band + sw128(wrow + (i0 + i) * kEach + sub, part % 8)),
+                       "r"(o4[0]), "r"(o4[1]), "r"(o4[2]), "r"(o4[3])
+                       : "memory");
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the images -> tensor core
       mbar_arrive(smem_addr(&q_full[tile]));
