@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
     }
     return;
   }
-  // Four lanes have a row (16 codes of every group each), a thread four rows, all
-  // asked for at once: the chain of loads before them is most of this kernel's time.
+  // Four lanes have a row (words t and t + 4 of every group each, so that they write
+  // 64 bytes of the image together), a thread four rows, all asked for at once.
   constexpr int kTurns = kChunk / 32;
   const int x = threadIdx.x >> 7;                   // 0: K, 1: V
   const int w4 = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -159,13 +159,15 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
     for (int k = 0; k < NG; ++k) pair[i][k] = 0;
     if (r < rows) {
       const unsigned char* rec = a.kv + ((int64_t)blk[r / BS] * a.num_kv_heads + hk) * G::kRecord;
-      const unsigned char* from = rec + q4_codes_at(x, r % BS, BS, D) + t * (D / 8);
-      if constexpr (NG == 2) {
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(from));
-        w[i][0] = y.x, w[i][1] = y.y, w[i][2] = y.z, w[i][3] = y.w;
-      } else {
-        const uint2 y = __ldg(reinterpret_cast<const uint2*>(from));
-        w[i][0] = y.x, w[i][1] = y.y;
+      const unsigned char* from = rec + q4_codes_at(x, r % BS, BS, D) + t * (4 * NG);
+#pragma unroll
+      for (int ci = 0; ci < 2; ++ci) {
+        if constexpr (NG == 2) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(from + ci * 32));
+          w[i][2 * ci] = y.x, w[i][2 * ci + 1] = y.y;
+        } else {
+          w[i][ci] = __ldg(reinterpret_cast<const uint32_t*>(from + ci * 16));
+        }
       }
 #pragma unroll
       for (int k = 0; k < NG; ++k)
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) q4_widen_kernel(const Q4LongArgs a) {
           const float c1 = __uint_as_float(0x4B000000u | (y >> (8 * k + 4) & 15u)) - 8388608.0f;
           o[k] = pack2<true>(fmaf(s, c0, lo), fmaf(s, c1, lo));
         }
-        *reinterpret_cast<uint4*>(img + gr * (kChunk * 128) + sw128(r, 2 * t + ci)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(img + gr * (kChunk * 128) + sw128(r, t + 4 * ci)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
