@@ -53,6 +53,7 @@ constexpr int kThreads4 = kWarps * 32;
 constexpr int kMinRangeTokens = 128;
 // Lengths up to this many tokens take one CTA per sequence, with no merge behind it.
 constexpr int kWholeTokens = 512;
+constexpr int kAloneParts = 8;        // partials that one warp joins by itself
 constexpr float kNoRef = -1e30f;      // the reference of a column without a key
 
 struct Q4Args {
@@ -647,18 +648,21 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
               float top = 0.0f, top_s = 0.0f;
 #pragma unroll
               for (int x = 0; x < T; ++x) {
+                float row[2] = {0.0f, 0.0f};       // a token's largest p; times its largest scale
 #pragma unroll
                 for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
                   for (int k = 0; k < 4; ++k) p[x][nt][k] = ex2(fmaf(sc[x][nt][k], kfac, -ref[nt][k & 1]));
-                  top = fmaxf(fmaxf(top, p[x][nt][0]), p[x][nt][1]);
-                  top = fmaxf(fmaxf(top, p[x][nt][2]), p[x][nt][3]);
+                  row[0] = fmaxf(fmaxf(row[0], p[x][nt][0]), p[x][nt][1]);
+                  row[1] = fmaxf(fmaxf(row[1], p[x][nt][2]), p[x][nt][3]);
+                }
+                top = fmaxf(fmaxf(top, row[0]), row[1]);
 #pragma unroll
-                  for (int gr = 0; gr < NG; ++gr) {
-                    const float s0 = pair_scale(vp[x][0][gr]), s1 = pair_scale(vp[x][1][gr]);
-                    top_s = fmaxf(fmaxf(top_s, p[x][nt][0] * s0), p[x][nt][1] * s0);
-                    top_s = fmaxf(fmaxf(top_s, p[x][nt][2] * s1), p[x][nt][3] * s1);
-                  }
+                for (int r = 0; r < 2; ++r) {
+                  float most = pair_scale(vp[x][r][0]);
+#pragma unroll
+                  for (int gr = 1; gr < NG; ++gr) most = fmaxf(most, pair_scale(vp[x][r][gr]));
+                  top_s = fmaxf(top_s, row[r] * most);
                 }
               }
               return top > 4294967296.0f || top_s > 2048.0f;
@@ -839,7 +843,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
 
 // Joins the partials of the unit that CTA c of a KV head began and later CTAs
 // ended: out = sum_i 2^(r_i - R) acc_i / sum_i 2^(r_i - R) l_i.  One CTA per
-// (range, KV head, column or four of them); its warps take the partials in turn.
+// (range, KV head, column or four of them); its warps take a column each where the
+// partials are few, else a column's partials in turn.
 template <int D>
 __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols) {
   constexpr int E = D / 32;
@@ -850,9 +855,19 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
   const int64_t cell = (int64_t)hk * a.ctas + c;
   const int4 meta = a.ws_meta[cell];
   if (meta.x == 0) return;
-  for (int col = blockIdx.z; col < meta.z * a.group; col += gridDim.z) {
-    const int i = col / a.group;
-    const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
+  const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
+  auto write = [&](int col, const float (&num)[E], float den, bool bad) {
+    const float r = bad ? 0.0f : 1.0f / den;
+    uint32_t x[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
+    __nv_bfloat16* out =
+        a.out + ((int64_t)(meta.y + col / a.group) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
+    else *reinterpret_cast<uint32_t*>(out) = x[0];
+  };
+  // the partials first, first + step, .. of a column: (num, den) against the largest reference
+  auto join = [&](int col, int first, int step, float (&num)[E], float& den) {
     const int64_t p0 = (cell * 2 + 1) * cols + col;
     auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
     float R = kNoRef;
@@ -864,12 +879,11 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
-    bad = __any_sync(0xffffffffu, bad);
-    float num[E], den = 0.0f;
+    den = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) num[e] = 0.0f;
 #pragma unroll 4
-    for (int k = warp; k < count; k += 4) {
+    for (int k = first; k < count; k += step) {
       const float2 ml = *reinterpret_cast<const float2*>(a.ws_ml + at(k) * 2);
       const float f = ex2(ml.x - R);
       den += times_ex2(ml.y, ml.x - R);
@@ -886,6 +900,18 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
         num[1] = fmaf(f, x.y, num[1]);
       }
     }
+    return __any_sync(0xffffffffu, bad) != 0;
+  };
+  float num[E], den;
+  if (count <= kAloneParts) {                       // few partials: a warp has a column to itself
+    const int col = blockIdx.z + warp * gridDim.z;
+    if (col >= meta.z * a.group) return;
+    const bool bad = join(col, 0, 1, num, den);
+    write(col, num, den, bad);
+    return;
+  }
+  for (int col = blockIdx.z; col < meta.z * a.group; col += gridDim.z) {
+    const bool bad = join(col, warp, 4, num, den);
 #pragma unroll
     for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
     part[warp][lane][E] = den;
@@ -896,14 +922,7 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
         for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
         den += part[k][lane][E];
       }
-      const float r = bad ? 0.0f : 1.0f / den;
-      uint32_t x[E / 2];
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
-      __nv_bfloat16* out =
-          a.out + ((int64_t)(meta.y + i) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
-      if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
-      else *reinterpret_cast<uint32_t*>(out) = x[0];
+      write(col, num, den, bad);
     }
     __syncthreads();
   }
