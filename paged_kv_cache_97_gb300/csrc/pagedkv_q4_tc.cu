@@ -14,10 +14,26 @@
 // m at most the row's largest s + E less five, so that p as an fp16 number is
 // within 2^-11 of itself, or 2^-30 of the row's largest.
 //
-// Images cost 4 d bytes per token and KV head written once and read by every
-// 256 rows: 1 % of the arithmetic's time for a prompt.  The attention kernel is
-// bound by the exponentials (32 K a chunk at 16 per cycle and SM) and the MMAs
-// alike.
+// Images cost 4 d bytes per token and KV head written once and read by every 256
+// rows.
+//
+// What bounds it: the two row tiles of a CTA take turns on the tensor pipe, and a
+// tile's chunk is a chain: its scores and P . V (1024 cycles of MMA), the softmax of a
+// row per thread (1600) and the hand-overs (350), in all 2650 cycles for two tiles'
+// 2048 of MMA, so the pipe is busy 3 / 4 of the time inside a unit.  Around it a
+// unit ends with 3000 cycles for its rows and 3000 for the next one's queries.
+// Measured (GB300, 32 / 8 heads of 128): one prompt of 8192 tokens 406 us, 1355
+// TFLOP/s; four of 1.5 to 3.5 K 209 us, 1034 TFLOP/s (plan 3, images 14, attention
+// 180, and 5 for the kernels of short queries that find nothing); 512 tokens over 8192
+// 133 us (64 units for 152 SMs).
+// What made it fast, the prompt of 8192 (the four): MMAs issued by a whole warp, one
+// elected lane (operands in uniform registers; a divergent lane needs 100 cycles
+// per step of K 16 for the pipe's 64) 549 -> 487 us (316 -> 290); roles that walk the
+// units at their own pace 471 (278); P . V that begins with the first half of P
+// 446 (270); units by length, launches that overlap 454 (260); one form of the
+// softmax, rolled, masks beforehand: code that runs once a unit is fetched from far
+// away, 416 (221); queries turned four rows side by side 412 (215); the images
+// written 64 bytes at a time 406 (209).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
