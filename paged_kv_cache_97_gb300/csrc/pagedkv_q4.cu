@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
       for (int j = w.j0 + warp * PB; j < w.j1; j += kWarps * PB) {
         if (ahead == 0) break;                      // (after a wait that gave up)
         const uint32_t bar = smem_addr(&bars[warp][cs]);
-        if (!mbar_wait(bar, (phase >> cs) & 1u) && !mbar_wait(bar, (phase >> cs) & 1u)) {
+        // (the lanes agree on the outcome: what follows is the whole warp's)
+        if (__any_sync(0xffffffffu, !mbar_wait(bar, (phase >> cs) & 1u))) {
           if (lane == 0) atomicOr(a.flags, PAGEDKV_FLAG_WAIT_TIMEOUT);
           dead = true;
         }
@@ -869,18 +870,10 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
   const int4 meta = a.ws_meta[cell];
   if (meta.x == 0) return;
   const int count = meta.x + 1;                     // partial 0: this CTA's second, k: CTA c + k's first
-  auto write = [&](int col, const float (&num)[E], float den, bool bad) {
-    const float r = bad ? 0.0f : 1.0f / den;
-    uint32_t x[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
-    __nv_bfloat16* out =
-        a.out + ((int64_t)(meta.y + col / a.group) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
-    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
-    else *reinterpret_cast<uint32_t*>(out) = x[0];
-  };
-  // the partials first, first + step, .. of a column: (num, den) against the largest reference
-  auto join = [&](int col, int first, int step, float (&num)[E], float& den) {
+  const bool alone = count <= kAloneParts;          // few partials: a warp has a column to itself
+  const int first = alone ? 0 : warp, step = alone ? 1 : 4;
+  for (int col = blockIdx.z + (alone ? warp * gridDim.z : 0); col < meta.z * a.group;
+       col += alone ? 4 * gridDim.z : gridDim.z) {
     const int64_t p0 = (cell * 2 + 1) * cols + col;
     auto at = [&](int k) { return k == 0 ? p0 : (cell + k) * 2 * cols + col; };
     float R = kNoRef;
@@ -892,7 +885,8 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, off));
-    den = 0.0f;
+    bad = __any_sync(0xffffffffu, bad);
+    float num[E], den = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) num[e] = 0.0f;
 #pragma unroll 4
@@ -913,31 +907,27 @@ __global__ void __launch_bounds__(128) q4_merge_kernel(const Q4Args a, int cols)
         num[1] = fmaf(f, x.y, num[1]);
       }
     }
-    return __any_sync(0xffffffffu, bad) != 0;
-  };
-  float num[E], den;
-  if (count <= kAloneParts) {                       // few partials: a warp has a column to itself
-    const int col = blockIdx.z + warp * gridDim.z;
-    if (col >= meta.z * a.group) return;
-    const bool bad = join(col, 0, 1, num, den);
-    write(col, num, den, bad);
-    return;
-  }
-  for (int col = blockIdx.z; col < meta.z * a.group; col += gridDim.z) {
-    const bool bad = join(col, warp, 4, num, den);
+    if (!alone) {
+      __syncthreads();                              // (the last column's shares are read)
 #pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
-    part[warp][lane][E] = den;
-    __syncthreads();
-    if (warp == 0) {
+      for (int e = 0; e < E; ++e) part[warp][lane][e] = num[e];
+      part[warp][lane][E] = den;
+      __syncthreads();
+      if (warp != 0) continue;
       for (int k = 1; k < 4; ++k) {
 #pragma unroll
         for (int e = 0; e < E; ++e) num[e] += part[k][lane][e];
         den += part[k][lane][E];
       }
-      write(col, num, den, bad);
     }
-    __syncthreads();
+    const float r = bad ? 0.0f : 1.0f / den;
+    uint32_t x[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) x[e] = bad ? 0u : pack2<false>(num[2 * e] * r, num[2 * e + 1] * r);
+    __nv_bfloat16* out =
+        a.out + ((int64_t)(meta.y + col / a.group) * a.num_q_heads + (int64_t)hk * a.group + col % a.group) * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(x[0], x[1]);
+    else *reinterpret_cast<uint32_t*>(out) = x[0];
   }
 }
 
@@ -978,7 +968,10 @@ kv_status launch_q4(const Q4Args& a, cudaStream_t s) {
   st = cuda_check(cudaLaunchKernelEx(&cfg, q4_kernel<D, BS, NT, kMulti>, a), "q4_kernel launch");
   if (st != KV_OK || a.whole) return st;
   const int used = (kMulti ? min(a.max_query_len, a.tile_tokens) : 1) * a.group;
-  cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)a.num_kv_heads, (unsigned)(used > 8 ? (used + 3) / 4 : used));
+  // Four columns per CTA where a sequence has few ranges on average (a warp joins
+  // each) or columns are many; one where the partials are many and the cells few.
+  const bool several = used > 8 || a.ctas <= kAloneParts / 2 * a.batch;
+  cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)a.num_kv_heads, (unsigned)(several ? (used + 3) / 4 : used));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_merge_kernel<D>, a, C::kCols), "q4_merge_kernel launch");

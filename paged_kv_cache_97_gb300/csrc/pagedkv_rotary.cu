@@ -454,25 +454,39 @@ __global__ void __launch_bounds__(kRotaryWarps * 32) read_q4_kernel(const ReadAr
   const int e = lane % kWords, h0 = lane / kWords;
   const unsigned char* block = a.kv + (int64_t)(blk >= 0 ? blk : 0) * H * rec_bytes;
   uint4* out[2] = {a.k_out + tok * H * kWords, a.v_out + tok * H * kWords};
+  int word_at[2], pair_at[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int word_at = q4_codes_at(x, in, bs, D) + ((e & 7) * kGroups + e / 8) * 4;
-    const int pair_at = q4_pairs_at(x, in, bs, D) + (e / 8) * 4;
-#pragma unroll 8
-    for (int h = h0; h < H; h += kSide) {
+    word_at[x] = q4_codes_at(x, in, bs, D) + ((e & 7) * kGroups + e / 8) * 4;
+    pair_at[x] = q4_pairs_at(x, in, bs, D) + (e / 8) * 4;
+  }
+  constexpr int kBatch = 4;                         // heads whose K and V words are asked for together
+  for (int h1 = h0; h1 < H; h1 += kBatch * kSide) {
+    uint32_t w[kBatch][2], p[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h1 + i * kSide;
       const unsigned char* rec = block + (int64_t)h * rec_bytes;
-      uint4 o = make_uint4(0, 0, 0, 0);
-      if (blk >= 0) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + word_at));
-        const uint32_t p = __ldg(reinterpret_cast<const uint32_t*>(rec + pair_at));
-        const float s = __uint_as_float(p << 16), m = __uint_as_float(p & 0xffff0000u);
+      const bool live = blk >= 0 && h < H;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        w[i][x] = live ? __ldg(reinterpret_cast<const uint32_t*>(rec + word_at[x])) : 0u;
+        p[i][x] = live ? __ldg(reinterpret_cast<const uint32_t*>(rec + pair_at[x])) : 0u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h1 + i * kSide;
+      if (h >= H) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float s = __uint_as_float(p[i][x] << 16), m = __uint_as_float(p[i][x] & 0xffff0000u);
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)                 // c: the low bits of 2^23 + c; s * c is exact
-          v[k] = fmaf(s, __uint_as_float(0x4B000000u | (w >> (4 * k) & 15u)) - 8388608.0f, m);
-        o = narrow8(v);
+          v[k] = fmaf(s, __uint_as_float(0x4B000000u | (w[i][x] >> (4 * k) & 15u)) - 8388608.0f, m);
+        out[x][h * kWords + e] = narrow8(v);
       }
-      out[x][h * kWords + e] = o;
     }
   }
 }
