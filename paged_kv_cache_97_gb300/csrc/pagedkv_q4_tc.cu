@@ -852,6 +852,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
     }
   }
   if (!ok) sh_fail = 1;
+  asm volatile("cp.async.wait_all;" ::: "memory");   // (after a wait that gave up)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -399,6 +399,28 @@ def test_multi_tensor_cores(pkv, block, dim, heads, group, L, n, room):
     check(multi(pkv, pool, q, n, dim ** -0.5, room=room), pool, q, n, dim ** -0.5, wide=True)
 
 
+@pytest.mark.parametrize("group,dim", [(8, 64), (4, 128), (3, 64)])
+def test_multi_tensor_cores_many_sequences(pkv, group, dim):
+    """More long sequences than a warp has lanes, of equal and unequal chunks, one of
+    them bad, short ones between them, and rows that belong to none at the end."""
+    g = torch.Generator().manual_seed(group)
+    L = (torch.randint(64, 420, (90,), generator=g)).tolist()
+    n = [min(x, int(m)) for x, m in zip(L, torch.randint(1, 120, (90,), generator=g).tolist())]
+    n[40], n[41], n[89] = 0, 1, min(L[89], 64)
+    pool = ref.Pool4(L, 2, dim, 16, seed=33)
+    q = pool.randn(sum(n), 2 * group, dim, scale=2.0)
+    kv, bt, sl = pool.on()
+    bt[7, 0] = -5
+    out = multi(pkv, pool, q, n, dim ** -0.5, dev=(kv, bt, sl), room=-1)
+    assert flags_of(pkv) == pkv.FLAG_BAD_BLOCK
+    at = sum(n[:7])
+    assert (out[at:at + n[7]] == 0).all()
+    bt[7, 0] = pool.tables[7, 0]
+    again = multi(pkv, pool, q, n, dim ** -0.5, dev=(kv, bt, sl), room=-1)
+    assert same_bits(again[:at], out[:at].cpu()) and same_bits(again[at + n[7]:], out[at + n[7]:].cpu())
+    check(again, pool, q, n, dim ** -0.5, wide=True)
+
+
 @pytest.mark.parametrize("scale,vspread,kspread", [(-0.2, 1.0, 1.0), (0.0, 1.0, 1.0), (3.0, 1.0, 1.0),
                                                    (0.1, 1e-20, 1e10), (0.1, 1e20, 1e-10)])
 def test_multi_tensor_cores_scales(pkv, scale, vspread, kspread):
