@@ -32,13 +32,13 @@
 // kernel joins.
 //
 // Measured (GB300, 32 / 8 heads of 128, one query token): 8 sequences of up to
-// 131072 tokens 143 us, 4.9 TB/s of the pool (floor 104 at 6.8); 128 of up to
-// 8192, 64 query heads, 138 us (98); 64 of up to 4096 51 us (25).  With a pool that
+// 131072 tokens 142 us, 4.9 TB/s of the pool (floor 104 at 6.8); 128 of up to
+// 8192, 64 query heads, 135 us (98); 64 of up to 4096 47 us (25).  With a pool that
 // L2 holds, the first still takes 138 us, and memory alone 115: what bounds it is the
 // arithmetic of the codes (ALU pipe 55 % busy, legacy tensor pipe 23 %, issue
 // slots 53 %), with the memory close behind.  Three CTAs on an SM for eight
 // columns: two took 151 us for 137 with the pool in L2, four (and fewer registers) 146.  Five query tokens (20
-// columns, two CTAs on an SM): 64 of up to 4096 92 us, eight warps that wait on
+// columns, two CTAs on an SM): 64 of up to 4096 90 us, eight warps that wait on
 // their own chains (issue 43 %, each warp issues every fourth cycle).
 // Not better: q as two e4m3 numbers in an 8-bit product (175 us for 143: the fp8
 // form of mma.sync takes five times the f16 form's cycles), codes shifted by

@@ -19,7 +19,7 @@
 // 512 bytes of its table row, which L2 holds.  Measured (GB300), eight prompts of 1 to
 // 8 K tokens: bf16 147 us, 93 % of the copy rate; E4M3 161 us (78 %); 4-bit with
 // three position axes 187 us (64 %), the codes' arithmetic beside the loads, and
-// reading them back 48 us (29 at the copy rate).  Eight CTAs per SM (64 registers)
+// reading them back 38 us (29 at the copy rate).  Eight CTAs per SM (64 registers)
 // hide the chain sequence -> length -> block -> store: six took 170 us for bf16.  The
 // table row is read once per CTA into shared memory; each thread's own loads of it for
 // two axes spilled (387 us for 304 at that time).  128 single tokens 6 us.
