@@ -710,7 +710,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
             mbar_arrive(smem_addr(&p_full[tile]));
             continue;
           }
-          const float kf = sl2 * __uint_as_float((uint32_t)(127 + now.x) << 23), ev = (float)now.y;
+          // (positive in any case: a masked score of -infinity stays one)
+          const float kf = fmaxf(sl2 * __uint_as_float((uint32_t)(127 + now.x) << 23), 1e-37f), ev = (float)now.y;
           const int cstart = c * kChunk;
           const bool masked = __any_sync(0xffffffffu, cstart + kChunk - 1 > lim);
           float lsum = 0.0f;

@@ -429,6 +429,15 @@ def test_multi_tensor_cores_scales(pkv, scale, vspread, kspread):
     check(multi(pkv, pool, q, [150, 200], scale, room=-1), pool, q, [150, 200], scale, wide=True)
 
 
+@pytest.mark.parametrize("scale,qsize", [(0.0, 1.0), (0.1, 2.0 ** -100), (-1e-30, 1e-20)])
+@pytest.mark.parametrize("kspread", [0.0, 1e-25])
+def test_multi_tensor_cores_scores_of_nothing(pkv, scale, qsize, kspread):
+    """A factor of the scores below fp32's range: a masked score is still none."""
+    pool = ref.Pool4([200, 300], 2, 64, 16, seed=34, kscale=lambda s, g: kspread)
+    q = (pool.randn(190, 8, 64).float() * qsize).to(torch.bfloat16)
+    check(multi(pkv, pool, q, [150, 40], scale, room=-1), pool, q, [150, 40], scale, wide=True)
+
+
 def test_multi_tensor_cores_rising_scores(pkv):
     """Scores and V's magnitudes that rise along the sequence move the references
     in every chunk."""
