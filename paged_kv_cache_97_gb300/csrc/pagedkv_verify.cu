@@ -17,8 +17,8 @@
 // last is read again, from L2).  Bound by the one row (two with q) that
 // has to be read per sequence, and in small batches by the chain of loads:
 // offsets, drafts, their probabilities, the row, the part again.  Measured (GB300,
-// 128256 tokens): 64 sequences of 5 drafts, fp32 p and q, 22 us (9.7 at the copy
-// rate), 256 of bf16 31 us (19), 8 of fp32 11 us, one of 4 drafts 8 us.  Other
+// 128256 tokens): 64 sequences of 5 drafts, fp32 p and q, 21 us (9.7 at the copy
+// rate), 256 of bf16 31 us (19), 8 of fp32 11 us; one of 4 drafts over 32000, 8 us.  Other
 // counts of threads and sizes of clusters took up to 28.7 us where these took 24.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
