@@ -138,8 +138,10 @@ __device__ __forceinline__ long long units(uint32_t hi, uint32_t lo, int n) {
   return ((long long)(hi - (uint32_t)n * kHiZero) << 21) + (int32_t)(lo - (uint32_t)n * kLoZero);
 }
 
-__device__ __forceinline__ void cluster_barrier() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -177,6 +179,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
     }
     return;
   }
+  // This CTA runs; its peers' sums may come from here on.  (What left above left with
+  // its whole cluster.)
+  if (a.cluster > 1) cluster_arrive();
   const int V = a.vocab;
   const T* target = static_cast<const T*>(a.target);
   const T* draft = static_cast<const T*>(a.draft);
@@ -260,6 +265,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
     }
     long long total = mine;
     if (a.cluster > 1) {
+      // (a peer's shared memory is there only once the peer has begun)
+      if (pass == 0) cluster_wait();
       if (threadIdx.x < a.cluster) {
         uint32_t to;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -267,7 +274,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
                      : "r"(smem_addr(&cta_sum[pass][rank])), "r"(threadIdx.x));
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
       }
-      cluster_barrier();
+      cluster_arrive();
+      cluster_wait();
       total = 0;
       for (int k = 0; k < a.cluster; ++k) {
         if (k < rank) before += cta_sum[pass][k];
