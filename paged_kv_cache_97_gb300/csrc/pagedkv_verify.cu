@@ -307,8 +307,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
           continue;
         }
       }
-      // (the last round's weights are still held)
-      if (i0 + U * kStep < w1) weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
+      // (the last round's weights are still held, but for rounds without a sum of their
+      // own that were looked through since)
+      if (round >= kRounds || i0 + U * kStep < w1)
+        weights_of<T, N, U, kVec>(p, q, r, i0 + lane * N, kStep, w1, w);
       uint32_t hi[U];
       int32_t lo[U];
       long long step[U];
