@@ -15,7 +15,8 @@
 // fp16; p * vmin is summed in fp32.  A column's reference is the largest of
 // score + exponent of max(vscale, |vmin| / 16) so far, less five, not of the
 // score alone: p * vscale then has fp16's whole range below 2^11 whatever the
-// scales are.  It moves only when a product passes 2^11 (or a weight 2^32).
+// scales are, and p * vmin stays below 2^15.  It moves only when p times that maximum
+// passes 2^11 (or a weight 2^32).
 //
 // Tile products (mma.sync m16n8k16, fp32 sums) with tokens, then dims, on M and
 // the columns (query token x grouped head) on N: the unpacked codes are used for
@@ -650,11 +651,12 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
               }
             }
             // ---- weights against the columns' references -------------------------
-            // p, and p * vscale as it enters the product; where one of them passes
-            // its bound (in the first tile, and rarely after it) the references move
-            // to the largest score + exponent of max(vscale, |vmin| / 16), less five
-            // (rows of equal values have the least scale, and p * vmin has to stay
-            // within fp32 too; exponents are -100 at least), and p is taken again.
+            // p, and p * max(vscale, |vmin| / 16), with p * vscale as it enters the
+            // product (rows of equal values have the least scale, and p * vmin has to
+            // stay within fp32 too); where one of them passes its bound (in the first
+            // tile, and rarely after it) the references move to the largest score +
+            // exponent of that maximum, less five (exponents are -100 at least), and p
+            // is taken again.
             // (The products are made again where they are packed: held meanwhile for 32
             // columns they would not fit the registers.)
             float p[T][A][4];
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
               float top = 0.0f, top_s = 0.0f;
 #pragma unroll
               for (int x = 0; x < T; ++x) {
-                float row[2] = {0.0f, 0.0f};       // a token's largest p; times its largest scale
+                float row[2] = {0.0f, 0.0f};       // a token's largest p; times its largest scale or |min| / 16
 #pragma unroll
                 for (int nt = 0; nt < A; ++nt) {
 #pragma unroll
@@ -673,9 +675,13 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
                 top = fmaxf(fmaxf(top, row[0]), row[1]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  float most = pair_scale(vp[x][r][0]);
+                  // (a pair's word as a number is its min, off by less than 2^-7 of it)
+                  float most = fabsf(__uint_as_float(vp[x][r][0]));
 #pragma unroll
-                  for (int gr = 1; gr < NG; ++gr) most = fmaxf(most, pair_scale(vp[x][r][gr]));
+                  for (int gr = 1; gr < NG; ++gr) most = fmaxf(most, fabsf(__uint_as_float(vp[x][r][gr])));
+                  most *= 0.0625f;
+#pragma unroll
+                  for (int gr = 0; gr < NG; ++gr) most = fmaxf(most, pair_scale(vp[x][r][gr]));
                   top_s = fmaxf(top_s, row[r] * most);
                 }
               }

@@ -80,3 +80,47 @@ def test_verify_more_rounds_than_sums(pkv, dtype, B, V, shift):
     assert (got < V).all()
     assert ((want[:, 0] <= got) & (got <= want[:, 1])).all()
     assert (acc == 0).all()
+
+
+# --------------------------------------------------------------------------
+# Attention over the 4-bit pool
+# --------------------------------------------------------------------------
+
+def appended(pkv, k, v, block):
+    """A 4-bit pool that holds rows k, v [L, H, d] of one sequence: (pool, tables, lengths, reference rows)."""
+    L, H, d = k.shape
+    nb = (L + block - 1) // block
+    kv = torch.full((nb, H, ref.record_bytes(block, d)), 0xFF, dtype=torch.uint8, device="cuda")
+    bt = torch.arange(nb, dtype=torch.int32, device="cuda")[None].contiguous()
+    sl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    pkv.append_rotary_q4(None, None, k.cuda(), v.cuda(), kv, None, bt, sl, block,
+                         query_start=torch.tensor([0, L], dtype=torch.int32, device="cuda"), max_query_len=L)
+    return kv, bt, sl, ref.rows_of(kv.cpu(), block, d, L)
+
+
+@pytest.mark.parametrize("block,dim", [(16, 64), (32, 128)])
+@pytest.mark.parametrize("n,room", [(1, 0), (3, 0), (40, 0), (40, 1)])
+@pytest.mark.parametrize("size", [2.0 ** 97, -2.0 ** 110, 2.0 ** 122, -2.0 ** 125])
+@pytest.mark.parametrize("rest", [0.0, 1.0])
+def test_constant_rows_of_large_values(pkv, block, dim, n, room, size, rest):
+    """V's rows of one value each (the least scale, the value as minimum) that come
+    after ordinary ones: a weight times the minimum stays within fp32."""
+    L, H, G = 500, 2, 4                             # (four steps a warp)
+    g = torch.Generator().manual_seed(n)
+    k, v = (torch.randn((L, H, dim), generator=g).to(torch.bfloat16) for _ in "kv")
+    v = (v.float() * rest).to(torch.bfloat16)
+    v[250:] = size
+    v[260:350] = 0.0
+    q = torch.randn((n, H * G, dim), generator=g).to(torch.bfloat16)
+    kv, bt, sl, rows = appended(pkv, k, v, block)
+    want, tol = ref.attention(rows, q, dim ** -0.5, torch.arange(L - n, L), wide=room > 0)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    if n == 1:
+        pkv.paged_attention_decode_q4(out, q.cuda(), kv, bt, sl, block, L, dim ** -0.5,
+                                      poison(pkv.q4_workspace_bytes(H * G, H, dim)))
+    else:
+        size = (pkv.q4_long_workspace_bytes(1, n, n, L, H * G, H, dim) if room else
+                pkv.q4_workspace_bytes(H * G, H, dim, n))
+        pkv.paged_attention_multi_q4(out, q.cuda(), kv, bt, sl, starts([n]).cuda(), block, L, n, dim ** -0.5,
+                                     poison(size))
+    within(out, want, tol)
