@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
       if (lane == 0) atomicMax(&q_top, top);
       __syncthreads();
       top = q_top;
-      // largest * 2^e in [2^13, 2^14): exact in fp16 from 2^-27 of it on
-      int e = top > 0 ? 140 - (int)(top >> 7) : 0;
+      // largest * 2^e in [2^14, 2^15): q / 16 is exact in fp16 from 2^-27 of it on (the
+      // last of bf16's 8 bits is then 2^-24 at least)
+      int e = top > 0 ? 141 - (int)(top >> 7) : 0;
       e = min(max(e, -110), 110);
       // (a negative scale turns q's sign, a zero one takes q as 0: kfac is positive,
       // so that a masked score of -infinity stays one)

@@ -124,3 +124,27 @@ def test_constant_rows_of_large_values(pkv, block, dim, n, room, size, rest):
         pkv.paged_attention_multi_q4(out, q.cuda(), kv, bt, sl, starts([n]).cuda(), block, L, n, dim ** -0.5,
                                      poison(size))
     within(out, want, tol)
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_queries_exact_down_to_their_bound(pkv, n):
+    """Elements of q of 2^-27 of the largest (which is the least of its octave) that
+    meet keys of 2^27 enter exactly, high nibbles as well: tokens whose keys lie in the
+    odd elements and ones whose keys lie in the even ones have nearly equal scores, and
+    the odd elements' last bit is 2^-7 of theirs."""
+    L, d = n + 5, 128
+    k = torch.zeros((L, 1, d))
+    k[::2, :, 65::2], k[1::2, :, 64::2] = 3 * 2.0 ** 27, 3 * 2.0 ** 27
+    v = torch.randn((L, 1, d), generator=torch.Generator().manual_seed(50))
+    kv, bt, sl, rows = appended(pkv, k.to(torch.bfloat16), v.to(torch.bfloat16), 16)
+    q = torch.zeros((n, 4, d), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    q[..., 64:] = 2.0 ** -27 * (1 + 2.0 ** -7)
+    want, tol = ref.attention(rows, q, 1.0, torch.arange(L - n, L))
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws = poison(pkv.q4_workspace_bytes(4, 1, d, n))
+    if n == 1:
+        pkv.paged_attention_decode_q4(out, q.cuda(), kv, bt, sl, 16, L, 1.0, ws)
+    else:
+        pkv.paged_attention_multi_q4(out, q.cuda(), kv, bt, sl, starts([n]).cuda(), 16, L, n, 1.0, ws)
+    within(out, want, tol)
