@@ -914,10 +914,11 @@ size_t pagedkv_q4_long_workspace_bytes(int batch, int num_tokens,
  * Few query tokens (query tokens x grouped heads < 128, or no room in the
  * workspace), one or two launches: the codes enter both products exactly, q exactly
  * down to 2^-27 of the largest |q| of the up to 32 rows (query token x grouped head)
- * that are worked on together; a weight times V's scale is one fp16 number (2^-11 of
- * its value, at best 2^-30 of the row's largest weight * max(scale, |min| / 16),
- * where one below 2^-100 counts as 2^-100; with one of 2^e, e > 100, weights below
- * 2^(e - 131) of the largest count as none).
+ * that are worked on together (|scale| * that largest counts as 2^-130 at least and
+ * 2^117 at most); a weight times V's scale is one fp16 number (2^-11 of its value, at
+ * best 2^-30 of the row's largest weight * max(scale, |min| / 16), where one below
+ * 2^-100 counts as 2^-100; with one of 2^e, e > 100, weights below 2^(e - 131) of the
+ * largest count as none).
  * Long ones, three launches more: keys and values are fp16 numbers (2^-11 of their
  * value, at best 2^-37 of the largest of their 128 rows), and so are weights (2^-11,
  * at best 2^-30 of the row's largest weight * largest value of the 128 rows). */

@@ -462,11 +462,13 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
       // largest * 2^e in [2^14, 2^15): q / 16 is exact in fp16 from 2^-27 of it on (the
       // last of bf16's 8 bits is then 2^-24 at least)
       int e = top > 0 ? 141 - (int)(top >> 7) : 0;
-      e = min(max(e, -110), 110);
+      e = min(e, 126);                              // (-113 at least)
       // (a negative scale turns q's sign, a zero one takes q as 0: kfac is positive,
       // so that a masked score of -infinity stays one)
       float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      kfac = fmaxf(fabsf(a.scale_log2) * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+      // (finite too: no score of 0 becomes NaN)
+      kfac = fabsf(a.scale_log2) * 16777216.0f * __uint_as_float((uint32_t)(127 - e) << 23);
+      kfac = fminf(fmaxf(kfac, 1e-37f), 3e38f);
       if (a.scale_log2 <= 0.0f) up = a.scale_log2 < 0.0f ? -up : 0.0f;
       const float down = up * 0.0625f;
 #pragma unroll
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
         for (int k = 0; k < 4; ++k) {
           v[2 * k] = __uint_as_float(xw[k] << 16);
           v[2 * k + 1] = __uint_as_float(xw[k] & 0xffff0000u);
-          sum += v[2 * k] + v[2 * k + 1];
+          sum += v[2 * k] * up + v[2 * k + 1] * up;      // (unscaled it may pass fp32)
         }
         // B fragment of k-step ks: lane (g = column % 8, t) holds elements 2 hh, 2 hh
         // + 4 and (times 1/16, its codes are high nibbles) 2 hh + 1, 2 hh + 5 of word
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kThreads4, Cfg4<D, BS, NT>::kCtasPerSm) q4_ker
         }
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(__activemask(), sum, off);
-        if (word % 8 == 0) q_sum[col][gr] = sum * (up * 5.9604644775390625e-8f);   // * 2^(e - 24)
+        if (word % 8 == 0) q_sum[col][gr] = sum * 5.9604644775390625e-8f;   // * 2^-24
       }
       __syncthreads();
     }

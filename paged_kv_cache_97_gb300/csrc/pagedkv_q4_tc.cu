@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) q4_tc_kernel(const Q4LongArgs a
         float up[4], theirs[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int e = min(max(top[i] > 0 ? 140 - (int)(top[i] >> 7) : 0, -110), 110);
+          const int e = min(top[i] > 0 ? 140 - (int)(top[i] >> 7) : 0, 110);   // (-115 at least)
           up[i] = __uint_as_float((uint32_t)(127 + e) << 23);
           theirs[i] = __uint_as_float((uint32_t)(127 - e) << 23);
           if (a.scale_log2 <= 0.0f) up[i] = a.scale_log2 < 0.0f ? -up[i] : 0.0f;

@@ -148,3 +148,16 @@ def test_queries_exact_down_to_their_bound(pkv, n):
     else:
         pkv.paged_attention_multi_q4(out, q.cuda(), kv, bt, sl, starts([n]).cuda(), 16, L, n, 1.0, ws)
     within(out, want, tol)
+
+
+@pytest.mark.parametrize("n,room", [(1, None), (3, None), (40, -1)])
+@pytest.mark.parametrize("size", [2.0 ** -122, 2.0 ** -100, 2.0 ** 118, 2.0 ** 125, 1.5 * 2.0 ** 127])
+def test_queries_of_any_magnitude(pkv, n, room, size):
+    """Queries down to the smallest and up to the largest bf16 numbers, with keys and a
+    factor to match."""
+    pool = ref.Pool4([300], 2, 64, 16, seed=51, kscale=lambda s, g: 2.0 ** (-60 if size > 1 else 60))
+    q = (pool.randn(n, 8, 64).float().clamp(-1.9, 1.9) * (size / 4)).to(torch.bfloat16)
+    q[..., 0] = size
+    scale = 2.0 ** (60 if size > 1 else -60) / size
+    got = decode(pkv, pool, q, scale) if n == 1 else multi(pkv, pool, q, [n], scale, room=room)
+    check(got, pool, q, [n], scale, wide=True)
