@@ -987,6 +987,16 @@ def _bad_rows(t, name, dev, shape):
     raise ValueError(f"{name}: the rows of a token must be contiguous")
 
 
+def _extent(t, name, axis):
+    """The size of bf16 rows t along `axis`; raises for what is none."""
+    try:
+        if t.dtype is _dt[0] and t.dim() == 3:
+            return t.size(axis)
+    except (AttributeError, TypeError):
+        pass
+    _need(t, _dt[0], name, 3)
+
+
 def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, seq_lens, positions, sections,
             rotary_dim, interleaved, query_start, max_query_len, specs, stream):
     """append_rotary and append_rotary_q4: the checks they share, and the call.
@@ -1002,19 +1012,18 @@ def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, s
     dev = _need_all(*specs)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out belong together")
-    T, hq = k.size(0), 0
+    hq, T = 0 if q is None else _extent(q, "q", 1), _extent(k, "k", 0)
     kv_shape = (T, hkv, d)
     # rows [T, heads, d]: a token's are contiguous, its neighbours any stride away
     args = []
     if q is not None:
-        hq = q.size(1)
         q_shape = (T, hq, d)
         given = (q_out, q_shape, "q_out"), (q, q_shape, "q"), (k, kv_shape, "k"), (v, kv_shape, "v")
     else:
         args = [0, 0, 0, 0]
         given = (k, kv_shape, "k"), (v, kv_shape, "v")
     for t, shape, name in given:
-        if t.dtype is not bf16 or t.get_device() != dev or t.shape != shape:
+        if getattr(t, "dtype", None) is not bf16 or t.get_device() != dev or t.shape != shape:
             _bad_rows(t, name, dev, shape)
         st, sh, sd = t.stride()
         if (sh != d and shape[1] > 1 or sd != 1) and T:

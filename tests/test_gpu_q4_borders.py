@@ -161,3 +161,26 @@ def test_queries_of_any_magnitude(pkv, n, room, size):
     scale = 2.0 ** (60 if size > 1 else -60) / size
     got = decode(pkv, pool, q, scale) if n == 1 else multi(pkv, pool, q, [n], scale, room=room)
     check(got, pool, q, [n], scale, wide=True)
+
+
+# --------------------------------------------------------------------------
+# Appends
+# --------------------------------------------------------------------------
+
+def test_append_refuses_other_things(pkv):
+    """What is no tensor, or has too few dimensions, is named, as everywhere."""
+    bt, sl = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((2, 2), (2,)))
+    kv = torch.zeros((4, 2, ref.record_bytes(16, 64)), dtype=torch.uint8, device="cuda")
+    pool = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    rows = q[:, :2].contiguous()
+    for name, at in (("q_out", 0), ("q", 1), ("k", 2), ("v", 3)):
+        for bad, error in ((None, (TypeError, ValueError)), (3, TypeError), ("x", TypeError),
+                           (torch.zeros(128, dtype=torch.bfloat16, device="cuda"), ValueError),
+                           (torch.zeros((2, 2, 64), device="cuda"), TypeError), (rows.cpu(), ValueError)):
+            args = [q.clone(), q, rows, rows]
+            args[at] = bad
+            with pytest.raises(error, match=name):
+                pkv.append_rotary(*args, pool, pool.clone(), None, bt, sl)
+            with pytest.raises(error, match=name):
+                pkv.append_rotary_q4(*args, kv, None, bt, sl, 16)
