@@ -1258,8 +1258,11 @@ def verify_drafts(out_tokens, num_accepted, tokens, target_probs, draft_probs, u
         raise ValueError("draft_probs must be [tokens - batch, vocab]")
     if seq_lens is not None and (seq_lens.shape[0] != B or new_lens.shape[0] != B):
         raise ValueError("seq_lens and new_lens must have one entry per sequence")
+    # (rows of no element have no address: an address of its own says that drafts have
+    # probabilities, of which nothing is then read)
+    drafts = 0 if draft_probs is None else draft_probs.data_ptr() or target_probs.data_ptr()
     _call(_VERIFY, out_tokens.data_ptr(), num_accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
-          _at(draft_probs), uniform.data_ptr(), query_start.data_ptr(), _at(seq_lens), _at(new_lens), B, T,
+          drafts, uniform.data_ptr(), query_start.data_ptr(), _at(seq_lens), _at(new_lens), B, T,
           int(T if max_query_len is None else max_query_len) or 1, V, kind, _stream_on(stream, dev) or 0)
     return out_tokens, num_accepted
 

@@ -184,3 +184,21 @@ def test_append_refuses_other_things(pkv):
                 pkv.append_rotary(*args, pool, pool.clone(), None, bt, sl)
             with pytest.raises(error, match=name):
                 pkv.append_rotary_q4(*args, kv, None, bt, sl, 16)
+
+
+# --------------------------------------------------------------------------
+# Graphs and streams
+# --------------------------------------------------------------------------
+
+def test_verify_draft_probabilities_of_no_draft(pkv):
+    """draft_probs of no row (every sequence has its last token alone): a sequence
+    that has a draft all the same, or no token, is a bad one."""
+    p = torch.full((2, 64), 1 / 64, device="cuda")
+    tokens = torch.tensor([5, 6], dtype=torch.int32, device="cuda")
+    none, u = p[:0], torch.tensor([0.5, 0.25], device="cuda")
+    out, acc = (torch.full((2,), 77, dtype=torch.int32, device="cuda") for _ in "oa")
+    pkv.verify_drafts(out, acc, tokens, p, none, u, starts([1, 1]).cuda())
+    assert out.tolist() == [32, 16] and acc.tolist() == [0, 0]
+    pkv.verify_drafts(out, acc, tokens, p, none, u, starts([2, 0]).cuda())
+    assert flags_of(pkv) == pkv.FLAG_BAD_SEQ_LEN
+    assert out.tolist() == [-1, -1] and acc.tolist() == [0, 0]
