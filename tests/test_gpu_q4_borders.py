@@ -167,6 +167,38 @@ def test_queries_of_any_magnitude(pkv, n, room, size):
 # Appends
 # --------------------------------------------------------------------------
 
+@pytest.mark.parametrize("kind", ["int8", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_append_rotary_8_bit_borders(pkv, kind, dim):
+    """Values and scales at the borders of the 8-bit codes: what reshape_and_cache
+    stores, bit for bit."""
+    g = torch.Generator().manual_seed(60)
+    special = [0.0, -0.0, math.nan, -math.nan, math.inf, -math.inf, 3.3e38, -3.3e38, 1e-40, -1e-40, 448.0, 464.0, 465.0,
+               127.0, 127.5, -128.0, 2.0 ** 40, -2.0 ** 40, 2.0 ** 41, 2.0 ** -9, 2.0 ** -10, 0.5, 1.5, 2.5, 17.0, -33.0]
+    scales = [0.0, 1.0, 1e-45, 1e-38, 2.0 ** -81, 2.0 ** -80, 2.0 ** -40, 1 / 40, 3.0, 2.0 ** 40, 2.0 ** 80, 2.0 ** 81,
+              3e38, math.inf, math.nan, -1.0, -0.0]
+    H, n = 2, 3 * len(scales)
+    x = torch.randn((2, n * 16, H, dim), generator=g)
+    x *= torch.exp2(torch.randint(-45, 46, x.shape[:-1] + (1,), generator=g).float())
+    x[:, ::4] = torch.tensor(special)[torch.randint(0, len(special), x[:, ::4].shape, generator=g)]
+    s = torch.tensor(scales).repeat(3)[:, None].expand(n, H).contiguous()
+    x[:, 1::4] = torch.randn(x[:, 1::4].shape, generator=g) * 40 * s.nan_to_num(1.0, 1.0).abs().clamp(1e-38, 1e36).repeat_interleave(16, 0)[None, 1::4, :, None]
+    k, v = x.to(torch.bfloat16)
+    dt = torch.int8 if kind == "int8" else torch.float8_e4m3fn
+    caches = [torch.zeros((n, 16, H, dim), dtype=dt, device="cuda") for _ in range(4)]
+    ks, vs = s.cuda(), s.flip(0).contiguous().cuda()
+    bt = torch.arange(n, dtype=torch.int32, device="cuda").view(3, -1).contiguous()
+    sl = torch.full((3,), n * 16 // 3, dtype=torch.int32, device="cuda")
+    pkv.append_rotary(None, None, k.contiguous().cuda(), v.contiguous().cuda(), caches[0], caches[1], None, bt, sl,
+                      query_start=starts([n * 16 // 3] * 3).cuda(), max_query_len=n * 16 // 3, k_scale=ks, v_scale=vs)
+    slots = torch.arange(n * 16, device="cuda")
+    pkv.reshape_and_cache(k.contiguous().cuda(), v.contiguous().cuda(), caches[2], caches[3], slots, ks, vs)
+    for i in range(2):
+        a, b = (c.cpu().view(torch.uint8) for c in (caches[i], caches[i + 2]))
+        off = (a != b).nonzero()
+        assert len(off) == 0, f"{len(off)} codes differ, first at {off[0].tolist()}"
+
+
 def test_append_refuses_other_things(pkv):
     """What is no tensor, or has too few dimensions, is named, as everywhere."""
     bt, sl = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((2, 2), (2,)))
@@ -189,6 +221,86 @@ def test_append_refuses_other_things(pkv):
 # --------------------------------------------------------------------------
 # Graphs and streams
 # --------------------------------------------------------------------------
+
+def test_long_queries_on_streams_and_in_graphs(pkv):
+    """Plan, images, prompts and short queries: on two streams at once (a workspace
+    each), and two captured calls that share one workspace, replayed in turn."""
+    L, n = [700, 40, 900, 300], [600, 1, 200, 33]
+    pool = ref.Pool4(L, 2, 128, 16, seed=70)
+    dev = kv, bt, sl = pool.on()
+    q = pool.randn(sum(n), 8, 128)
+    first = multi(pkv, pool, q, n, 0.1, dev=dev, room=-1)
+    check(first, pool, q, n, 0.1, wide=True)
+    other_n = [1, 40, 128, 300]
+    second = multi(pkv, pool, q[:sum(other_n)], other_n, 0.1, dev=dev, room=-1)
+    qd, size = q.cuda(), pkv.q4_long_workspace_bytes(4, sum(n), 600, 900, 8, 2, 128)
+
+    def call(out, m, ws):
+        T = sum(m)
+        pkv.paged_attention_multi_q4(out[:T], qd[:T], kv, bt, sl, qs[tuple(m)], 16, 900, 600, 0.1, ws)
+    qs = {tuple(m): starts(m).cuda() for m in (n, other_n)}
+    outs, wss = [torch.empty_like(qd) for _ in range(2)], [poison(size) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for out, ws, st in zip(outs, wss, streams):
+            with torch.cuda.stream(st):
+                call(out, n, ws)
+    torch.cuda.synchronize()
+    assert all(same_bits(o, first) for o in outs)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, out, m in zip(graphs, outs, (n, other_n)):
+        with torch.cuda.graph(g):
+            call(out, m, wss[0])
+    for _ in range(4):
+        for g, out, m, want in zip(graphs, outs, (n, other_n), (first, second)):
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert same_bits(out[:sum(m)], want)
+
+
+def test_a_captured_step(pkv):
+    """Append, attention, read back and verification captured as one step, replayed on
+    new inputs in the same buffers; the eager calls give the same bits."""
+    B, n, hq, hkv, d, bs, V = 5, 4, 8, 2, 128, 16, 32000
+    T = B * n
+    kv = torch.zeros((40, hkv, ref.record_bytes(bs, d)), dtype=torch.uint8, device="cuda")
+    bt = torch.randperm(40, generator=torch.Generator().manual_seed(1))[:B * 8].view(B, 8).to(torch.int32).cuda()
+    cs, qs = ref.table(200, d).cuda(), starts([n] * B).cuda()
+    sl = torch.tensor([4, 17, 64, 100, 128], dtype=torch.int32, device="cuda")
+    x = torch.zeros((T, hq + 2 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    tokens, p, r, u, _ = [y.cuda() for y in verify_case([n] * B, V, torch.bfloat16, 80)]
+    ws = poison(pkv.q4_workspace_bytes(hq, hkv, d, n))
+
+    def step(kv, new):
+        q, out = (torch.empty((T, hq, d), dtype=torch.bfloat16, device="cuda") for _ in "qo")
+        rows = [torch.empty((T, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        got, acc = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (T, B))
+        pkv.append_rotary_q4(q, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], kv, cs, bt, sl, bs, query_start=qs,
+                             max_query_len=n)
+        pkv.paged_attention_multi_q4(out, q, kv, bt, sl, qs, bs, 128, n, d ** -0.5, ws)
+        pkv.read_q4(*rows, kv, bt, sl, bs, query_start=qs, max_query_len=n)
+        pkv.verify_drafts(got, acc, tokens, p, r, u, qs, max_query_len=n, seq_lens=sl, new_lens=new)
+        return q, out, *rows, got, acc, new
+    step(kv, torch.empty_like(sl))                  # (first use outside of a capture)
+    kept = kv.clone()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    new = torch.empty_like(sl)
+    with torch.cuda.graph(g):
+        captured = step(kv, new)
+    for seed in range(4):
+        gen = torch.Generator().manual_seed(seed)
+        x.copy_(torch.randn(x.shape, generator=gen))
+        u.copy_(torch.rand(T, generator=gen))
+        eager = [y.clone() for y in step(kept, torch.empty_like(sl))]
+        for y in captured:
+            y.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert same_bits(kv, kept) and all(same_bits(a, b) for a, b in zip(captured, eager))
+
 
 def test_verify_draft_probabilities_of_no_draft(pkv):
     """draft_probs of no row (every sequence has its last token alone): a sequence
