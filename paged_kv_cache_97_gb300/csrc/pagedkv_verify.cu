@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 1024 / kVerifyThreads) verify_
     }
     return;
   }
-  // This CTA runs; its peers' sums may come from here on.  (What left above left with
-  // its whole cluster.)
-  if (a.cluster > 1) cluster_arrive();
+  // This CTA runs: its peers may store into it.  (Relaxed: they find nothing of it.
+  // What left above left with its whole cluster.)
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int V = a.vocab;
   const T* target = static_cast<const T*>(a.target);
   const T* draft = static_cast<const T*>(a.draft);
