@@ -822,7 +822,8 @@ kv_status pagedkv_evict_tokens(void *k_cache, void *v_cache, float *k_scale,
  *   query_start   device int32 [batch + 1], or NULL: one token per sequence
  *                 (num_tokens == batch); n_b == 0 is allowed
  *   max_query_len host bound on every n_b
- * All rows 16-byte aligned.  Two tokens of a call must not share a slot.  A token
+ * All rows 16-byte aligned, at most 2^24 heads.  Two tokens of a call must not share
+ * a slot.  A token
  * with bad offsets or length (PAGEDKV_FLAG_BAD_SEQ_LEN) or a position outside
  * [0, max_position) (PAGEDKV_FLAG_BAD_INDEX) stores nothing and gets zeros in
  * q_out; a table entry outside the pool (PAGEDKV_FLAG_BAD_BLOCK) stores nothing,

@@ -542,6 +542,8 @@ kv_status rotary_common(void* q_out, int64_t q_out_stride, const void* q, int64_
   if (batch < 0 || num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks <= 0 ||
       max_query_len <= 0)
     return fail(KV_ERR_INVALID_ARG, "%s: bad sizes", who);
+  if ((q && num_q_heads > (1 << 24)) || num_kv_heads > (1 << 24))
+    return fail(KV_ERR_INVALID_ARG, "%s: at most 2^24 heads", who);
   if (head_dim != 64 && head_dim != 128) return fail(KV_ERR_INVALID_ARG, "%s: head_dim must be 64 or 128", who);
   if (block_size != 16 && block_size != 32) return fail(KV_ERR_INVALID_ARG, "%s: block_size must be 16 or 32", who);
   if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && num_q_heads == 0))
