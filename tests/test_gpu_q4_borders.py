@@ -314,3 +314,11 @@ def test_verify_draft_probabilities_of_no_draft(pkv):
     pkv.verify_drafts(out, acc, tokens, p, none, u, starts([2, 0]).cuda())
     assert flags_of(pkv) == pkv.FLAG_BAD_SEQ_LEN
     assert out.tolist() == [-1, -1] and acc.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dim,heads,group,L,n", [(128, 1, 4, [9000, 300], [200, 64]), (64, 1, 2, [5000], [1500]),
+                                                 (128, 2, 8, [4097, 33, 2500], [16, 1, 130])])
+def test_long_queries_over_long_contexts(pkv, dim, heads, group, L, n):
+    pool = ref.Pool4(L, heads, dim, 16, seed=71)
+    q = pool.randn(sum(n), heads * group, dim, scale=2.0)
+    check(multi(pkv, pool, q, n, dim ** -0.5, room=-1), pool, q, n, dim ** -0.5, wide=True)
