@@ -954,8 +954,8 @@ def evict_tokens(k_cache, v_cache, block_tables, seq_lens, keep_idx, keep_len,
 # converts them one by one otherwise, which for 33 arguments takes longer than the
 # launch.
 _ROTARY, _ROTARY_Q4, _READ_Q4, _DECODE_Q4, _MULTI_Q4, _VERIFY = range(6)
-_PACKS = [struct.Struct(f"{n}q").pack for n in (33, 29, 15, 17, 20, 15)]
 _COUNTS = (33, 29, 15, 17, 20, 15)
+_PACKS = [struct.Struct(f"{n}q").pack for n in _COUNTS]
 _float_bits = struct.Struct("f").pack, struct.Struct("I").unpack
 
 

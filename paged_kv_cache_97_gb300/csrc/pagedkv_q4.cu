@@ -162,13 +162,6 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // 8x8 16-bit matrix over the warp (row = lane / 4, columns 2 (lane % 4), +1), transposed.
 __device__ __forceinline__ uint32_t transposed8(uint32_t x) {
   uint32_t r;
@@ -236,15 +229,15 @@ __device__ __forceinline__ float pair_min(uint32_t pair) { return __uint_as_floa
 
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes * 2^-24, * 2^-20
 
-#ifndef PAGEDKV_Q4_CTAS
-#define PAGEDKV_Q4_CTAS 3
-#endif
+// CTAs of q4_kernel on an SM with `nt` column tiles.
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+
 // A stage holds a step's blocks: 32 tokens, two MMA tiles.
 template <int D, int BS, int NT>
 struct Cfg4 {
   using G = Geo4<D, BS>;
   static constexpr int kCols = 8 * NT;
-  static constexpr int kCtasPerSm = NT == 1 ? PAGEDKV_Q4_CTAS : 2;
+  static constexpr int kCtasPerSm = ctas_per_sm(NT);
   static constexpr int kBlocks = 32 / BS;                 // blocks of a step
   static constexpr int kStage = kBlocks * G::kRecord;
   static constexpr int kTiles = NT <= 2 ? 2 : 1;          // tiles worked on together
@@ -1003,7 +996,7 @@ int column_tiles(int max_query_len, int group) {
 
 // CTAs per KV head of a split call: one wave of them over all heads.
 int split_ctas(int sms, int nt, int num_kv_heads) {
-  const int all = sms * (nt == 1 ? PAGEDKV_Q4_CTAS : 2);
+  const int all = sms * ctas_per_sm(nt);
   return all / num_kv_heads > 0 ? all / num_kv_heads : 1;
 }
 

@@ -36,6 +36,14 @@ __device__ __forceinline__ int q4_pairs_at(int x, int row, int bs, int d) {
   return bs * d + (x * bs + row) * (d / 16);
 }
 
+// `bytes` consecutive bytes into shared memory, counted on a barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Long queries (pagedkv_q4_tc.cu): sequences whose query tokens x grouped heads
 // fill a 128-row tile at least, as many of them as there are slots for.

@@ -287,10 +287,7 @@ __device__ __forceinline__ float half_exp(const uint32_t (&raw)[64], uint32_t (&
 
 __device__ __forceinline__ void bulk_image(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   mbar_expect_tx(bar, bytes);
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+  bulk_load(dst, src, bytes, bar);
 }
 
 // A unit of work: 256 rows of a sequence and KV head.
