@@ -975,26 +975,22 @@ def _at(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _bad_rows(t, name, dev, shape):
-    """Raises for a tensor that is no rows of `shape` (None: any number of heads)."""
-    _need_rows = _dt[0]
-    if getattr(t, "dtype", None) is not _need_rows or t.dim() != 3 or not t.is_cuda:
-        _need(t, _need_rows, name, 3)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    raise ValueError(f"{name}: the rows of a token must be contiguous")
-
-
-def _extent(t, name, axis):
-    """The size of bf16 rows t along `axis`; raises for what is none."""
-    try:
-        if t.dtype is _dt[0] and t.dim() == 3:
-            return t.size(axis)
-    except (AttributeError, TypeError):
-        pass
-    _need(t, _dt[0], name, 3)
+def _bad_rows(rows, dev):
+    """Raises for the first (tensor, shape, name) that is no rows of its shape: for
+    what is no bf16 tensor of three dimensions before a shape (the shapes follow
+    from q and k)."""
+    for t, _, name in rows:
+        if getattr(t, "dtype", None) is not _dt[0] or t.dim() != 3 or not t.is_cuda:
+            _need(t, _dt[0], name, 3)
+    for t, shape, name in rows:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    for t, (_, heads, d), name in rows:
+        _, sh, sd = t.stride()
+        if (sh != d and heads > 1) or sd != 1:
+            raise ValueError(f"{name}: the rows of a token must be contiguous")
 
 
 def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, seq_lens, positions, sections,
@@ -1012,7 +1008,11 @@ def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, s
     dev = _need_all(*specs)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out belong together")
-    hq, T = 0 if q is None else _extent(q, "q", 1), _extent(k, "k", 0)
+    try:
+        hq, T = 0 if q is None else q.size(1), k.size(0)
+    except (AttributeError, TypeError, IndexError):
+        _bad_rows([(t, None, name) for t, name in ((q, "q"), (k, "k")) if t is not None or name == "k"], dev)
+        raise
     kv_shape = (T, hkv, d)
     # rows [T, heads, d]: a token's are contiguous, its neighbours any stride away
     args = []
@@ -1024,10 +1024,10 @@ def _rotary(which, q_out, q, k, v, pool, sizes, hkv, d, cos_sin, block_tables, s
         given = (k, kv_shape, "k"), (v, kv_shape, "v")
     for t, shape, name in given:
         if getattr(t, "dtype", None) is not bf16 or t.get_device() != dev or t.shape != shape:
-            _bad_rows(t, name, dev, shape)
+            _bad_rows(given, dev)
         st, sh, sd = t.stride()
         if (sh != d and shape[1] > 1 or sd != 1) and T:
-            _bad_rows(t, name, dev, shape)
+            _bad_rows(given, dev)
         args += (t.data_ptr(), st if T > 1 else shape[1] * d)
     B, mb = block_tables.shape
     if seq_lens.size(0) != B:
