@@ -849,8 +849,9 @@ kv_status pagedkv_append_rotary(
  * elements.  Element e of a row is nibble e % 8 (a byte's low one first) of the
  * 32-bit little-endian word (e % 64 / 8) * (head_dim / 64) + e / 64 of its codes.
  * head_dim 64 or 128, block_size 16 or 32.  Tables, lengths, the block pool's
- * bookkeeping (kv_pool_*, whose dtype then only sets kv_pool_block_bytes) and
- * errors are those of the other pools. */
+ * bookkeeping (kv_pool_*) and errors are those of the other pools.  kv_pool_create
+ * has no dtype for this format: kv_pool_block_bytes answers for the one it was given,
+ * while a block here takes num_kv_heads * pagedkv_q4_record_bytes bytes. */
 size_t pagedkv_q4_record_bytes(int block_size, int head_dim);
 
 /* pagedkv_append_rotary into a 4-bit pool (cos_sin NULL: a plain append).  Per
@@ -859,8 +860,9 @@ size_t pagedkv_q4_record_bytes(int block_size, int head_dim);
  *   scale = (largest - min) * fp32(1 / 15), up to the next bf16 number, 2^-126 at
  *           least
  *   code  = round_half_even((x - min) * (1 / scale)), held in 0..15;
- * NaN counts as 0, magnitudes above 2^126 (infinities too) as 2^126, -0 as 0.  A
- * stored value is off by at most half a scale of its 64 elements. */
+ * NaN counts as 0, magnitudes above 2^126 (infinities too) as 2^126, -0 as 0.  Any
+ * other value is off by at most 1/2 + 2^-16 of its 64 elements' scale (the quotient's
+ * own roundings can move it past a middle). */
 kv_status pagedkv_append_rotary_q4(
     void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
     const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -899,7 +901,10 @@ size_t pagedkv_q4_workspace_bytes(int max_query_len, int num_q_heads,
  * into fp16 operands in the workspace (4 * num_kv_heads * head_dim bytes per token
  * of max_seq_len and such sequence) and serves it on the tensor cores.  With a
  * smaller workspace, pagedkv_q4_workspace_bytes at least, it does so for as many
- * sequences as fit and takes longer for the others (prompts about four times). */
+ * sequences as fit, in the order of the batch, and serves the others as it serves few
+ * query tokens.  Prompts then take six to seven times as long, 512 tokens of 4 grouped
+ * heads over 8192 2.5 times; one sequence of up to 512 rows over a long context is the
+ * faster for it. */
 size_t pagedkv_q4_long_workspace_bytes(int batch, int num_tokens,
                                        int max_query_len, int max_seq_len,
                                        int num_q_heads, int num_kv_heads,
@@ -967,7 +972,7 @@ typedef enum {
  *   query_start   device int32 [batch + 1]; n_b == 0 (without draft_probs) gives
  *                 num_accepted 0 and the length as it is
  *   seq_lens, new_lens  device int32 [batch], both or neither; may be one buffer
- *   max_query_len host bound on every n_b;  vocab less than 2^19
+ *   max_query_len host bound on every n_b;  vocab less than 2^19, batch at most 2^24
  * A weight counts as 0 where it is NaN or negative and as 1 above 1, a draft
  * compared with NaN is refused; the difference p - q is one fp32 number, and the
  * weights, held to 2^-45 each, are added without further rounding, so the drawn token does not depend on how the

@@ -34,7 +34,7 @@
 //
 // Measured (GB300, 32 / 8 heads of 128, one query token): 8 sequences of up to
 // 131072 tokens 142 us, 4.9 TB/s of the pool (floor 104 at 6.8); 128 of up to
-// 8192, 64 query heads, 135 us (98); 64 of up to 4096 47 us (25).  With a pool that
+// 8192, 64 query heads, 134 us (98); 64 of up to 4096 48 us (25).  With a pool that
 // L2 holds, the first still takes 138 us, and memory alone 115: what bounds it is the
 // arithmetic of the codes (ALU pipe 55 % busy, legacy tensor pipe 23 %, issue
 // slots 53 %), with the memory close behind.  Three CTAs on an SM for eight

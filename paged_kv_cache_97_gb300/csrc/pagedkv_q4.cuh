@@ -47,6 +47,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // ---------------------------------------------------------------------------
 // Long queries (pagedkv_q4_tc.cu): sequences whose query tokens x grouped heads
 // fill a 128-row tile at least, as many of them as there are slots for.
+//
+// Both ways measured (GB300, 8 KV heads of 128, us; rows of a sequence: as few
+// queries / through images), by sequences and their lengths:
+//                         128 rows    256 rows    512 rows
+//   64 of 512..4096        464 / 258   878 / 280  1690 / 378
+//   16 of 512..4096        159 /  96   253 / 107   459 / 137
+//    4 of 1024..4096        53 /  68    85 /  77   141 /  79
+//    1 of 8192              52 / 111    68 / 129   104 / 131
+//    1 of 32768            110 / 364   183 / 425   333 / 427
+// Images pay from the first whole tile on where there are sequences enough to give
+// every SM a pair of tiles; the few sequences that do not have a chunk's keys worked
+// off by one CTA per pair, and would be the faster as few queries up to 512 rows.
+// The rule looks at the rows alone: how many sequences are long is known on the
+// device only, and a caller who knows better gives the smaller workspace.
 // ---------------------------------------------------------------------------
 
 constexpr int kLongRows = 128;

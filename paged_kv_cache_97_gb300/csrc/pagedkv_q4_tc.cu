@@ -22,8 +22,8 @@
 // row per thread (1600) and the hand-overs (350), in all 2650 cycles for two tiles'
 // 2048 of MMA, so the pipe is busy 3 / 4 of the time inside a unit.  Around it a
 // unit ends with 3000 cycles for its rows and 3000 for the next one's queries.
-// Measured (GB300, 32 / 8 heads of 128): one prompt of 8192 tokens 406 us, 1355
-// TFLOP/s; four of 1.5 to 3.5 K 209 us, 1034 TFLOP/s (plan 3, images 14, attention
+// Measured (GB300, 32 / 8 heads of 128): one prompt of 8192 tokens 405 us, 1358
+// TFLOP/s; four of 1.5 to 3.5 K 208 us, 1034 TFLOP/s (plan 3, images 14, attention
 // 180, and 5 for the kernels of short queries that find nothing); 512 tokens over 8192
 // 133 us (64 units for 152 SMs).
 // What made it fast, the prompt of 8192 (the four): MMAs issued by a whole warp, one

@@ -12,13 +12,15 @@
 //
 // A cluster of up to 8 CTAs takes a sequence: every CTA finds the row from the
 // drafts by itself, each sums its part of the row, the parts' sums go to all
-// CTAs through distributed shared memory, and the one warp whose part holds the
+// CTAs through distributed shared memory (once a barrier begun at the start has shown
+// that all of them run), and the one warp whose part holds the
 // drawn place finds it by the sums of its rounds and steps (a round that is not its
-// last is read again, from L2).  Bound by the one row (two with q) that
+// last is read again, from L2; so is every one past the 64 whose sums are kept).  Bound by the one row (two with q) that
 // has to be read per sequence, and in small batches by the chain of loads:
 // offsets, drafts, their probabilities, the row, the part again.  Measured (GB300,
 // 128256 tokens): 64 sequences of 5 drafts, fp32 p and q, 21 us (9.7 at the copy
-// rate), 256 of bf16 31 us (19), 8 of fp32 11 us; one of 4 drafts over 32000, 8 us.  Other
+// rate), 256 of bf16 32 us (19), 8 of fp32 10 us; one of 4 drafts over 32000, 8.5 us; drafts
+// without probabilities, 64 of 5 16.5 us (4.8), 256 of bf16 31 us (9.7).  Other
 // counts of threads and sizes of clusters took up to 28.7 us where these took 24.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -418,7 +420,7 @@ extern "C" kv_status pagedkv_verify_drafts(int32_t* out_tokens, int32_t* num_acc
   if (st != KV_OK) return st;
   VerifyArgs a = {out_tokens, num_accepted, new_lens, seq_lens, tokens, target_probs, draft_probs, uniform,
                   query_start, di.flags, batch, num_tokens, max_query_len, vocab, 1};
-  // as many CTAs a sequence as the GPU holds at once (two of 512 threads per SM
+  // as many CTAs a sequence as the GPU holds at once (four of 256 threads per SM
   // are enough to keep the loads coming), while a warp has 256 weights
   while (a.cluster < kMaxCluster && 2LL * a.cluster * batch <= 4LL * di.num_sms &&
          vocab >= a.cluster * kVerifyWarps * 256)
